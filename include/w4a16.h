@@ -96,6 +96,11 @@ extern "C" {
                                            once to bf16 (8 significant bits), products sum in
                                            fp32 and C is rounded once to bf16               */
 
+#define W4A16_FLAG_ROPE_ADJACENT (1u << 17) /* w4a16_rope_append: a pair is values 2i and 2i + 1 of the
+                                           rotated part, not i and rot_dim / 2 + i          */
+#define W4A16_FLAG_MOE_RENORM (1u << 18) /* w4a16_moe_layer: the chosen experts' probabilities are
+                                           divided by their sum                             */
+
 /* Detail codes of stage-1/2 statuses. */
 #define W4A16_ARG_NULL 1        /* a required pointer is NULL                                  */
 #define W4A16_ARG_ALIGN 2       /* a pointer or leading dimension breaks its alignment rule    */
@@ -118,6 +123,10 @@ extern "C" {
 #define W4A16_DEV_SCHEDULE 8    /* a CSR entry was outside its range                           */
 #define W4A16_DEV_ZERO 16       /* w4a16_zero_points_check: a zero point is not an integer in
                                    [0, 15]                                                   */
+#define W4A16_DEV_POSITION 32   /* w4a16_rope_append: a position outside [0, max_pos)          */
+#define W4A16_DEV_SLOT 64       /* w4a16_rope_append: a slot past the cache                    */
+#define W4A16_DEV_LENGTH 128    /* w4a16_paged_attention: a length outside [0, max_pages x page] */
+#define W4A16_DEV_PAGE 256      /* w4a16_paged_attention: a page number outside [0, n_pages)   */
 
 /* ------------------------------------------------------------------------------------------
  * Packed tile layout (this library's own; the pages only say the kernel layout is a
@@ -385,6 +394,124 @@ int w4a16_gemm_moe_blocks(const void *a, int lda, const int32_t *b_packed_stack,
 int w4a16_csr_from_token_routes(int n_expert, int n_tokens, int experts_per_token,
                                 const int32_t *selected, int32_t *ex_ids, int32_t *ex_off,
                                 int32_t *ex_pairs, int32_t *pair_tok);
+
+/* ------------------------------------------------------------------------------------------
+ * The rest of a decode step around the W4A16 products: rotary positions with the write into a
+ * paged key-value cache, the attention of one new token over that cache, and a whole expert
+ * layer for a few tokens.  The pages have no kernels for these; they are this library's own.
+ *
+ * Paged cache: keys and values live in two arrays of the same layout.  Position i of a sequence
+ * is token i % page_size of page block_table[i / page_size]; head c of it starts at element
+ *     page * kv_page_stride + token * kv_token_stride + c * kv_head_stride
+ * and is head_dim contiguous 16-bit values (fp16, or bf16 with W4A16_FLAG_BF16).  Any order of
+ * tokens and heads inside a page, and any page size, can be expressed.  Offsets are 64-bit.
+ * ---------------------------------------------------------------------------------------- */
+
+/* Rotary positions with one to four axes (a text position; or time, height and width of images
+ * and video) on q and k, and k and v written into the cache, in one launch.
+ * Pair i < rot_dim / 2 of a head belongs to axis a when it lies in a's section (sections[0] pairs
+ * of axis 0 first, then sections[1] of axis 1, ...).  With p = positions[a * ld_pos + t],
+ * c = cos_sin[p * rot_dim + i] and s = cos_sin[p * rot_dim + rot_dim / 2 + i]:
+ *     (x1, x2) -> (x1 c - x2 s, x2 c + x1 s)
+ * on values i and rot_dim / 2 + i of the head (2i and 2i + 1 with W4A16_FLAG_ROPE_ADJACENT); values
+ * rot_dim .. head_dim - 1 are copied.  Computed in fp32 and rounded once.
+ *   q, k, v      device 16-bit; token t's heads start at element t * ldq (ldk, ldv), head h
+ *                head_dim values further on; so the three parts of one fused projection's output
+ *                can be passed as they lie
+ *   q_out        device 16-bit [n_tokens][ldqo]; may be q itself (with ldqo == ldq), else must not
+ *                overlap an input
+ *   k_cache, v_cache  the paged cache; only the rows that slots name are written
+ *   cos_sin      device fp32 [max_pos][rot_dim]: rot_dim / 2 cosines, then as many sines
+ *   positions    device int32 [n_axes][ld_pos], ld_pos >= n_tokens
+ *   slots        device int64 [n_tokens]: page * page_size + token in the page; negative: the
+ *                token's k and v are not written (padding).  Two tokens must not share a slot
+ *   status       device int32 or NULL: W4A16_DEV_POSITION is OR-ed in when a position is outside
+ *                [0, max_pos) (values that need it are not written), W4A16_DEV_SLOT when a slot is
+ *                past the cache (that token's k and v are not written)
+ *   sections     host int32 [n_axes], non-negative, with sum rot_dim / 2;  n_axes 1..4
+ *   n_heads, n_kv_heads  either may be 0 (its pointers are then not looked at)
+ *   rot_dim      even, 2 .. head_dim
+ *   flags        W4A16_FLAG_BF16, W4A16_FLAG_ROPE_ADJACENT
+ * 16-bit buffers need 2-byte alignment only; with head_dim and rot_dim multiples of 16, strides
+ * multiples of 8 and 16-byte aligned buffers the copies are 16 bytes wide. */
+int w4a16_rope_append(const void *q, int ldq, const void *k, int ldk, const void *v, int ldv,
+                      void *q_out, int ldqo, void *k_cache, void *v_cache, long long kv_page_stride,
+                      long long kv_token_stride, long long kv_head_stride, const float *cos_sin,
+                      int max_pos, const int32_t *positions, int ld_pos, const long long *slots,
+                      int32_t *status, int n_tokens, int n_heads, int n_kv_heads, int head_dim,
+                      int rot_dim, const int32_t *sections, int n_axes, int page_size, int n_pages,
+                      unsigned flags, cudaStream_t stream);
+
+/* Workspace bytes of w4a16_paged_attention (num_sms <= 0: the current device; 0 for sizes that it
+ * rejects).  Zero-filled once after allocation, as w4a16_gemm's; calls that run concurrently need
+ * separate workspaces. */
+size_t w4a16_paged_attention_workspace_size(int batch, int n_heads, int n_kv_heads, int head_dim,
+                                            int num_sms);
+
+/* Attention of one new token per sequence over the paged cache, the work split over the cache's
+ * length and joined, in one launch.  For sequence b and query head h, with the KV head
+ * c = h / (n_heads / n_kv_heads), over positions i in [max(0, len - window), len) (window 0: all):
+ *     out[b][h] = sum_i p_i v_i,   p = softmax(scale q . k_i),   lse[b][h] = log sum_i e^(scale q . k_i)
+ * The new token's own key and value are part of the cache (w4a16_rope_append writes them first).
+ * A sequence of length 0 gets zeros and lse = -inf.  Rows of the cache past a length are never
+ * read, whatever they hold.  Softmax and sums are fp32; p enters the value product as a 16-bit
+ * value plus a 16-bit remainder, so a live value that is infinite gives NaN.
+ *   q            device 16-bit [batch][ldq], head h at h * head_dim;  ldq % 8 == 0
+ *   out          device 16-bit [batch][ldo];  ldo % 8 == 0;  lse  device fp32 [batch][n_heads] or NULL
+ *   block_table  device int32 [batch][ld_table], ld_table >= max_pages; entries past a sequence's
+ *                last page (and before a window's first) are not read
+ *   seq_lens     device int32 [batch], read on the device: no host copy of the lengths is needed
+ *   strides      multiples of 8 elements;  q, k_cache, v_cache, out 16-byte aligned
+ *   batch        0 (a no-op) .. 4096;  head_dim 64, 128 or 256;  n_heads a multiple of n_kv_heads
+ *   page_size, n_pages, max_pages  positive; max_pages x page_size bounds every length
+ *   flags        W4A16_FLAG_BF16
+ * A length outside [0, max_pages x page_size] is clamped and reported as W4A16_DEV_LENGTH; a page
+ * number outside [0, n_pages) makes its positions masked and is reported as W4A16_DEV_PAGE.
+ * Repeated calls with the same sizes and lengths are bit-identical. */
+int w4a16_paged_attention(const void *q, int ldq, const void *k_cache, const void *v_cache,
+                          long long kv_page_stride, long long kv_token_stride,
+                          long long kv_head_stride, void *out, int ldo, float *lse,
+                          const int32_t *block_table, int ld_table, const int32_t *seq_lens,
+                          void *workspace, size_t workspace_bytes, int batch, int n_heads,
+                          int n_kv_heads, int head_dim, int page_size, int n_pages, int max_pages,
+                          int window, float scale, unsigned flags, cudaStream_t stream);
+
+/* Workspace bytes of w4a16_moe_layer (0 for sizes that it rejects).  Zero-filled once after
+ * allocation; calls that run concurrently need separate workspaces. */
+size_t w4a16_moe_layer_workspace_size(int n_tokens, int hidden, int inter, int n_experts, int top_k);
+
+/* A whole expert layer with 4-bit weights for a few tokens: router product, softmax, top-k, the
+ * chosen experts' gated products and down products, the weighted sum and the residual.  For token t:
+ *     l_e = router[e] . x_t;   P = softmax(l);   the top_k experts of largest l, best first (the
+ *     lowest index where scores are equal);   w_j = P[e_j], divided by the sum of the chosen ones
+ *     with W4A16_FLAG_MOE_RENORM;
+ *     y_t = residual_t + sum_j w_j down_{e_j}( act(gate_{e_j} x_t) * (up_{e_j} x_t) )
+ * with act silu (W4A16_FLAG_SWIGLU) or gelu_tanh (W4A16_FLAG_GEGLU).  All sums are fp32, (q - z) s and
+ * the inner activations are not rounded to 16 bits, y is rounded once.  Routing runs on the device:
+ * no host synchronisation, and the call can be captured in a graph.  For more tokens than
+ * 64 use the grouped entry points.
+ *   x              device 16-bit [n_tokens][ldx];  residual 16-bit [n_tokens][ldr] or NULL
+ *   router         device 16-bit [n_experts][hidden]
+ *   gate_up        device int32, expert e's [hidden][2 inter] tiles at word e * hidden * 2 inter / 8:
+ *                  columns interleaved by w4_gate_up_interleave, then w4_repack
+ *   down           device int32, expert e's [inter][hidden] tiles (w4_repack)
+ *   *_scales, *_zeros  device 16-bit [n_experts][G][N] (gate_up's columns interleaved too); zeros for
+ *                  W4A16_TYPE_U4 only, with W4A16_FLAG_HAS_ZP, as for w4a16_gemm
+ *   y              device 16-bit [n_tokens][ldy]; may be residual or x itself (same leading dimension)
+ *   topk_ids, topk_weights  device int32 / fp32 [n_tokens][top_k] or NULL: the routing, written
+ *   n_tokens       0 (a no-op) .. 64;  hidden % 256 == 0;  inter % 128 == 0
+ *   n_experts      1 .. 512;  top_k 1 .. 16, at most n_experts
+ *   group_size     -1, or a positive multiple of 64 that divides hidden and inter
+ *   flags          exactly one of W4A16_FLAG_SWIGLU / _GEGLU; W4A16_FLAG_BF16, _HAS_ZP, _MOE_RENORM,
+ *                  _IS_K_FULL
+ * 16-byte aligned buffers, leading dimensions multiples of 8.  A NaN score counts as the lowest when
+ * experts are chosen; the token's output is then NaN.  Repeated calls are bit-identical. */
+int w4a16_moe_layer(const void *x, int ldx, const void *router, const int32_t *gate_up,
+                    const void *gate_up_scales, const void *gate_up_zeros, const int32_t *down,
+                    const void *down_scales, const void *down_zeros, const void *residual, int ldr,
+                    void *y, int ldy, int32_t *topk_ids, float *topk_weights, void *workspace,
+                    size_t workspace_bytes, int n_tokens, int hidden, int inter, int n_experts,
+                    int top_k, int group_size, int weight_type, unsigned flags, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------------------------
  * Checkpoint loading helpers (off the GEMM's path).

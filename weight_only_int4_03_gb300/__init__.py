@@ -31,12 +31,18 @@ W4A16_FLAG_STATIC_WEIGHTS = 1 << 12
 W4A16_FLAG_SWIGLU = 1 << 14
 W4A16_FLAG_GEGLU = 1 << 15
 W4A16_FLAG_BF16 = 1 << 16
+W4A16_FLAG_ROPE_ADJACENT = 1 << 17
+W4A16_FLAG_MOE_RENORM = 1 << 18
 
 W4A16_DEV_TIMEOUT = 1
 W4A16_DEV_PERM = 2
 W4A16_DEV_GIDX = 4
 W4A16_DEV_SCHEDULE = 8
 W4A16_DEV_ZERO = 16
+W4A16_DEV_POSITION = 32
+W4A16_DEV_SLOT = 64
+W4A16_DEV_LENGTH = 128
+W4A16_DEV_PAGE = 256
 
 W4A16_MAX_SEGMENTS = 1024
 W4A16_MOE_MAX_BLOCKS = 4096
@@ -54,6 +60,7 @@ _I = ctypes.c_int
 _U = ctypes.c_uint
 _SZ = ctypes.c_size_t
 _LL = ctypes.c_longlong
+_F = ctypes.c_float
 
 _SIGNATURES = {
     "w4a16_abi_version": (_I, []),
@@ -80,6 +87,14 @@ _SIGNATURES = {
     "w4a16_moe_blocks_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _U, _I]),
     "w4a16_gemm_moe_blocks": (_I, [_P, _I, _P, _P, _I, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I,
                                    _I, _I, _I, _I, _I, _I, _U, _P, _SZ, _P]),
+    "w4a16_rope_append": (_I, [_P, _I, _P, _I, _P, _I, _P, _I, _P, _P, _LL, _LL, _LL, _P, _I, _P, _I,
+                               _P, _P, _I, _I, _I, _I, _I, _P, _I, _I, _I, _U, _P]),
+    "w4a16_paged_attention_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
+    "w4a16_paged_attention": (_I, [_P, _I, _P, _P, _LL, _LL, _LL, _P, _I, _P, _P, _I, _P, _P, _SZ, _I, _I,
+                                   _I, _I, _I, _I, _I, _I, _F, _U, _P]),
+    "w4a16_moe_layer_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
+    "w4a16_moe_layer": (_I, [_P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _I, _P, _P, _P, _SZ, _I, _I,
+                             _I, _I, _I, _I, _I, _U, _P]),
 }
 for _name, (_res, _args) in _SIGNATURES.items():
     _fn = getattr(_lib, _name)
@@ -331,3 +346,73 @@ def w4a16_gemm_moe_blocks(a, b_packed_stack, c, scales_stack, zeros_stack, sorte
         max_padded, moe_block_size, top_k, int(bool(mul_topk_weights)), int(bool(is_ep)), n_experts,
         prob_m, n, k, group_size, weight_type, flags, _ptr(workspace), workspace_bytes,
         _stream(stream)))
+
+
+def _kv_strides(kv_strides, page_size: int, n_kv_heads: int, head_dim: int):
+    """(page, token, head) strides in elements; by default [page][token][head][head_dim]."""
+    if kv_strides is None:
+        return page_size * n_kv_heads * head_dim, n_kv_heads * head_dim, head_dim
+    return tuple(kv_strides)
+
+
+def w4a16_rope_append(q, k, v, q_out, k_cache, v_cache, cos_sin, positions, slots, status, n_tokens: int,
+                      n_heads: int, n_kv_heads: int, head_dim: int, rot_dim: int, sections, max_pos: int,
+                      page_size: int, n_pages: int, flags: int = 0, ldq: int | None = None,
+                      ldk: int | None = None, ldv: int | None = None, ldqo: int | None = None,
+                      ld_pos: int | None = None, kv_strides=None, stream=None) -> None:
+    """Rotary positions on q and k (axes by `sections`, a sequence of ints), k and v written into
+    the paged cache -- see include/w4a16.h.  `status`: device int32 for W4A16_DEV_* bits, or None."""
+    sec = np.ascontiguousarray(sections, dtype=np.int32)
+    ps, ts, hs = _kv_strides(kv_strides, page_size, n_kv_heads, head_dim)
+    _check("w4a16_rope_append", _lib.w4a16_rope_append(
+        _ptr(q), n_heads * head_dim if ldq is None else ldq,
+        _ptr(k), n_kv_heads * head_dim if ldk is None else ldk,
+        _ptr(v), n_kv_heads * head_dim if ldv is None else ldv,
+        _ptr(q_out), n_heads * head_dim if ldqo is None else ldqo, _ptr(k_cache), _ptr(v_cache), ps, ts, hs,
+        _ptr(cos_sin), max_pos, _ptr(positions), n_tokens if ld_pos is None else ld_pos, _ptr(slots),
+        _ptr(status), n_tokens, n_heads, n_kv_heads, head_dim, rot_dim, sec.ctypes.data, sec.size, page_size,
+        n_pages, flags, _stream(stream)))
+
+
+def w4a16_paged_attention_workspace_size(batch: int, n_heads: int, n_kv_heads: int, head_dim: int,
+                                         num_sms: int = 0) -> int:
+    return int(_lib.w4a16_paged_attention_workspace_size(batch, n_heads, n_kv_heads, head_dim, num_sms))
+
+
+def w4a16_paged_attention(q, k_cache, v_cache, out, block_table, seq_lens, workspace, batch: int, n_heads: int,
+                          n_kv_heads: int, head_dim: int, page_size: int, n_pages: int, max_pages: int,
+                          scale: float, flags: int = 0, window: int = 0, lse=None, ldq: int | None = None,
+                          ldo: int | None = None, ld_table: int | None = None, kv_strides=None,
+                          workspace_bytes: int | None = None, stream=None) -> None:
+    """One new token per sequence over the paged cache: out, and log-sum-exp into `lse` when given
+    -- see include/w4a16.h."""
+    ps, ts, hs = _kv_strides(kv_strides, page_size, n_kv_heads, head_dim)
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check("w4a16_paged_attention", _lib.w4a16_paged_attention(
+        _ptr(q), n_heads * head_dim if ldq is None else ldq, _ptr(k_cache), _ptr(v_cache), ps, ts, hs,
+        _ptr(out), n_heads * head_dim if ldo is None else ldo, _ptr(lse), _ptr(block_table),
+        max_pages if ld_table is None else ld_table, _ptr(seq_lens), _ptr(workspace), workspace_bytes,
+        batch, n_heads, n_kv_heads, head_dim, page_size, n_pages, max_pages, window, scale, flags,
+        _stream(stream)))
+
+
+def w4a16_moe_layer_workspace_size(n_tokens: int, hidden: int, inter: int, n_experts: int, top_k: int) -> int:
+    return int(_lib.w4a16_moe_layer_workspace_size(n_tokens, hidden, inter, n_experts, top_k))
+
+
+def w4a16_moe_layer(x, router, gate_up, gate_up_scales, gate_up_zeros, down, down_scales, down_zeros, y,
+                    workspace, n_tokens: int, hidden: int, inter: int, n_experts: int, top_k: int,
+                    group_size: int, weight_type: int, flags: int, residual=None, topk_ids=None,
+                    topk_weights=None, ldx: int | None = None, ldy: int | None = None, ldr: int | None = None,
+                    workspace_bytes: int | None = None, stream=None) -> None:
+    """A whole expert layer (router, top-k, gated products, down products, weighted sum, residual)
+    for up to 64 tokens with 4-bit weights -- see include/w4a16.h."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check("w4a16_moe_layer", _lib.w4a16_moe_layer(
+        _ptr(x), hidden if ldx is None else ldx, _ptr(router), _ptr(gate_up), _ptr(gate_up_scales),
+        _ptr(gate_up_zeros), _ptr(down), _ptr(down_scales), _ptr(down_zeros), _ptr(residual),
+        hidden if ldr is None else ldr, _ptr(y), hidden if ldy is None else ldy, _ptr(topk_ids),
+        _ptr(topk_weights), _ptr(workspace), workspace_bytes, n_tokens, hidden, inter, n_experts, top_k,
+        group_size, weight_type, flags, _stream(stream)))

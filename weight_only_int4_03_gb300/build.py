@@ -21,7 +21,8 @@ INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["w4a16_gemm.cu", "w4a16_decode.cu", "w4a16_aux.cu", "w4a16_api.cu", "w4a16_noalloc.cu",
-           "w4a16_loader.cu"]
+           "w4a16_loader.cu", "w4a16_rope.cu", "w4a16_attention.cu",
+           "w4a16_moe_layer.cu"]
 
 
 def _nvcc() -> str:

@@ -1,0 +1,830 @@
+// w4a16_moe_layer.cu -- a whole expert layer for a few tokens with 4-bit weights.
+//
+// For token t with input row x_t:
+//     l_e = router[e] . x_t,   P = softmax(l),   the top_k experts e_1 .. e_k of largest l (ties: the
+//     lowest index), weights w_j = P[e_j] (divided by their sum with W4A16_FLAG_MOE_RENORM),
+//     y_t = residual_t + sum_j w_j Wd_{e_j}^T h_j,   h_j = act(Wg_{e_j}^T x_t) * (Wu_{e_j}^T x_t),
+// with W = (q - z) s per group of rows.  Three launches, each starting while the one before drains:
+//   route    router product, softmax, top-k, and the pairs (token, j) grouped by expert;
+//   gate-up  h for every pair;
+//   down     the pairs' outputs in fp32, and per 32 output columns, by the last block to finish
+//            them, the weighted sum over a token's experts in the order of j.
+//
+// Bound by memory: each chosen expert's codes are read once for all of its tokens.  What would bound
+// it otherwise is the conversion of the codes, so the weights go into the MMA (m16n8k16, weights as
+// its 16 rows, tokens as its 8 columns) with as few instructions as they allow:
+//   fp16   a code in the low bits of an fp16 is the subnormal q 2^-24, and one nibble up 16 q 2^-24;
+//          the MMA takes both exactly, so a mask is the whole conversion.  The two kinds go into
+//          separate accumulators, joined as lo + hi / 16.
+//   bf16   a code or-ed into the fraction of 128.0 is 128 + q.
+// The zero point (and the 128) is then taken off the sums, sum (q - z) a = sum q a - z sum a, with
+// sum a from one more MMA whose weights are all ones, shared by the block's columns.  Every sum of a
+// 64-row block starts from zero and is scaled in fp32; (q - z) s is never rounded.
+// h keeps fp32's accuracy through the second product as a 16-bit value plus a 16-bit remainder, two
+// columns of the down MMA, whose eight columns are mostly empty for a few tokens.
+//
+// A unit of work is 32 columns of one expert over all of K, done by a team of 1 to 8 warps that take
+// its 128-row steps in turn.  A warp streams its steps through its own ring of cp.async stages, which
+// runs on into its next unit, so no block-wide barrier sits between a copy and its use and the ring
+// stays full across units.  Activations are read from L1/L2 in the MMA's fragment order.
+#include "w4a16_ops.cuh"
+
+namespace w4 {
+namespace ops {
+
+constexpr int MOE_MAX_TOKENS = 64;
+constexpr int MOE_MAX_EXPERTS = 512;
+constexpr int MOE_MAX_TOP = 16;
+constexpr int MOE_MAX_PAIRS = MOE_MAX_TOKENS * MOE_MAX_TOP;
+constexpr int MOE_WARPS = 8;
+constexpr int MOE_THREADS = MOE_WARPS * 32;
+constexpr int MOE_CHUNK = 4;   // tokens per routing block
+constexpr int MOE_COLS = 32;   // weight columns per unit
+constexpr int MOE_ROWS = 128;  // weight rows per step (two 64-row blocks)
+constexpr int MOE_W_BYTES = MOE_ROWS * MOE_COLS / 2;
+constexpr int MOE_SZ_BYTES = MOE_COLS * 2; // one scale (or zero) row of a unit
+constexpr int MOE_STAGE = MOE_W_BYTES + 4 * MOE_SZ_BYTES;
+
+// Element of a 64-row block in the order the MMA's lanes read it: lane t of a quad takes, for
+// i = 0, 1, the eight values of 16-byte chunk 4 i + t, which are rows 32 (t & 1) + 8 p +
+// 4 (t >> 1) + 2 i + {0, 1}, p = 0 .. 3 -- the rows of word 2 (t >> 1) + i of half t & 1.
+__host__ __device__ __forceinline__ int frag_index(int row)
+{
+    const int h = (row >> 5) & 1, p = (row >> 3) & 3, j = (row >> 1) & 3, e = row & 1;
+    return ((j & 1) * 4 + h + 2 * (j >> 1)) * 8 + 2 * p + e;
+}
+
+// Routing tables in the workspace.
+struct MoeTables {
+    int *n_active;   // [4]: active experts, gate-up units, down units
+    int *ex_id;      // [MOE_MAX_EXPERTS] active experts in increasing order
+    int *ex_off;     // [MOE_MAX_EXPERTS + 1] their pairs in `sorted`
+    int *pre_up;     // [MOE_MAX_EXPERTS + 1] units before each active expert
+    int *pre_down;
+    int *sorted;     // [pairs] pair ids t * top_k + j by expert, in increasing order within one
+    int *ids;        // [pairs]
+    float *weights;  // [pairs]
+};
+
+struct RouteParams {
+    const uint16_t *x, *router;
+    uint16_t *xf; // [tokens][hidden] in fragment order
+    float *logits;
+    int *topk_ids;
+    float *topk_weights;
+    int *counters; // [chunks], then one
+    MoeTables tab;
+    int ldx, tokens, hidden, experts, top, renorm;
+    int up_cols, down_cols; // units per expert and pass
+    int up_pass, down_pass; // pairs per pass
+};
+
+template <bool BF>
+__global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const RouteParams p)
+{
+    __shared__ int is_last;
+    __shared__ int ids[MOE_MAX_PAIRS];
+    __shared__ int count[MOE_MAX_EXPERTS], off_of[MOE_MAX_EXPERTS];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int t0 = blockIdx.y * MOE_CHUNK, nt = min(MOE_CHUNK, p.tokens - t0);
+    const int e = blockIdx.x * MOE_WARPS + warp;
+
+    if (blockIdx.x == 0) {
+        // The tokens' rows in fragment order.
+        const int chunks = p.hidden / 8;
+        for (int i = tid; i < nt * chunks; i += MOE_THREADS) {
+            const int tt = i / chunks, c = i - tt * chunks;
+            const int q = c & 7, t = q & 3, w = q >> 2;
+            const uint16_t *src = p.x + (long long)(t0 + tt) * p.ldx + (c >> 3) * 64 + 32 * (t & 1) + 4 * (t >> 1) + 2 * w;
+            uint4 v;
+            v.x = *reinterpret_cast<const uint32_t *>(src);
+            v.y = *reinterpret_cast<const uint32_t *>(src + 8);
+            v.z = *reinterpret_cast<const uint32_t *>(src + 16);
+            v.w = *reinterpret_cast<const uint32_t *>(src + 24);
+            *reinterpret_cast<uint4 *>(p.xf + (long long)(t0 + tt) * p.hidden + c * 8) = v;
+        }
+    }
+    if (e < p.experts) {
+        float acc[MOE_CHUNK] = {0.f, 0.f, 0.f, 0.f};
+        const uint16_t *r = p.router + (long long)e * p.hidden;
+#pragma unroll 4
+        for (int k = lane * 8; k < p.hidden; k += 256) {
+            const uint4 wv = *reinterpret_cast<const uint4 *>(r + k);
+            const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
+#pragma unroll
+            for (int tt = 0; tt < MOE_CHUNK; ++tt) {
+                if (tt >= nt)
+                    break;
+                const uint4 xv = *reinterpret_cast<const uint4 *>(p.x + (long long)(t0 + tt) * p.ldx + k);
+                const uint32_t xx[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 a = unpack2<BF>(ww[i]), b = unpack2<BF>(xx[i]);
+                    acc[tt] = fmaf(a.x, b.x, acc[tt]);
+                    acc[tt] = fmaf(a.y, b.y, acc[tt]);
+                }
+            }
+        }
+#pragma unroll
+        for (int tt = 0; tt < MOE_CHUNK; ++tt) {
+            float v = acc[tt];
+#pragma unroll
+            for (int d = 16; d; d >>= 1)
+                v += __shfl_xor_sync(0xffffffffu, v, d);
+            if (lane == 0 && tt < nt)
+                __stcg(p.logits + (long long)(t0 + tt) * p.experts + e, v);
+        }
+    }
+    __syncthreads();
+    if (tid == 0) {
+        const int last = arrive_counter(p.counters + blockIdx.y) == (int)gridDim.x - 1;
+        if (last)
+            p.counters[blockIdx.y] = 0;
+        is_last = last;
+    }
+    __syncthreads();
+    if (!is_last)
+        return;
+
+    // --- softmax and top-k of this chunk, a warp per token ------------------------------------
+    if (warp < nt) {
+        const int t = t0 + warp;
+        constexpr int PER = MOE_MAX_EXPERTS / 32;
+        float l[PER];
+        uint32_t taken = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            l[i] = i * 32 + lane < p.experts ? __ldcg(p.logits + (long long)t * p.experts + i * 32 + lane) : -INFINITY;
+        float top = 0.f, sum = 0.f, chosen = 0.f;
+        for (int j = 0; j < p.top; ++j) {
+            float best = -INFINITY;
+            int at = MOE_MAX_EXPERTS;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int idx = i * 32 + lane;
+                // A NaN counts as -inf here, so that top_k distinct experts come out whatever x holds.
+                const float v = l[i] == l[i] ? l[i] : -INFINITY;
+                if (idx < p.experts && !((taken >> i) & 1u) && (at == MOE_MAX_EXPERTS || v > best)) {
+                    best = v;
+                    at = idx;
+                }
+            }
+#pragma unroll
+            for (int d = 16; d; d >>= 1) {
+                const float ov = __shfl_xor_sync(0xffffffffu, best, d);
+                const int oa = __shfl_xor_sync(0xffffffffu, at, d);
+                if (oa < MOE_MAX_EXPERTS && (at == MOE_MAX_EXPERTS || ov > best || (ov == best && oa < at))) {
+                    best = ov;
+                    at = oa;
+                }
+            }
+            if (j == 0) {
+                top = best;
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                    if (i * 32 + lane < p.experts)
+                        sum += expf(l[i] - top);
+#pragma unroll
+                for (int d = 16; d; d >>= 1)
+                    sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            }
+            if ((at & 31) == lane)
+                taken |= 1u << (at >> 5);
+            const float w = expf(best - top) / sum;
+            chosen += w;
+            if (lane == 0) {
+                __stcg(p.tab.ids + t * p.top + j, at);
+                __stcg(p.tab.weights + t * p.top + j, w);
+                if (p.topk_ids)
+                    p.topk_ids[t * p.top + j] = at;
+            }
+        }
+        __syncwarp();
+        for (int j = lane; j < p.top; j += 32) {
+            float w = __ldcg(p.tab.weights + t * p.top + j);
+            if (p.renorm)
+                w /= chosen;
+            __stcg(p.tab.weights + t * p.top + j, w);
+            if (p.topk_weights)
+                p.topk_weights[t * p.top + j] = w;
+        }
+    }
+    __syncthreads();
+    if (tid == 0) {
+        const int last = arrive_counter(p.counters + gridDim.y) == (int)gridDim.y - 1;
+        if (last)
+            p.counters[gridDim.y] = 0;
+        is_last = last;
+    }
+    __syncthreads();
+    if (!is_last)
+        return;
+
+    // --- pairs by expert ----------------------------------------------------------------------
+    const int pairs = p.tokens * p.top;
+    for (int i = tid; i < pairs; i += MOE_THREADS)
+        ids[i] = __ldcg(p.tab.ids + i);
+    __syncthreads();
+    for (int x = tid; x < p.experts; x += MOE_THREADS) {
+        int n = 0;
+        for (int i = 0; i < pairs; ++i)
+            n += ids[i] == x ? 1 : 0;
+        count[x] = n;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int slots = 0, off = 0, up = 0, down = 0;
+        for (int base = 0; base < p.experts; base += 32) {
+            const int x = base + lane;
+            const int n = x < p.experts ? count[x] : 0;
+            const int has = n > 0 ? 1 : 0;
+            const int nu = (n + p.up_pass - 1) / p.up_pass * p.up_cols;
+            const int nd = (n + p.down_pass - 1) / p.down_pass * p.down_cols;
+            int s = has, o = n, u = nu, d = nd;
+#pragma unroll
+            for (int q = 1; q < 32; q <<= 1) {
+                const int s2 = __shfl_up_sync(0xffffffffu, s, q), o2 = __shfl_up_sync(0xffffffffu, o, q);
+                const int u2 = __shfl_up_sync(0xffffffffu, u, q), d2 = __shfl_up_sync(0xffffffffu, d, q);
+                if (lane >= q) {
+                    s += s2;
+                    o += o2;
+                    u += u2;
+                    d += d2;
+                }
+            }
+            if (has) {
+                const int at = slots + s - 1;
+                p.tab.ex_id[at] = x;
+                p.tab.ex_off[at] = off + o - n;
+                p.tab.pre_up[at] = up + u - nu;
+                p.tab.pre_down[at] = down + d - nd;
+            }
+            if (x < p.experts)
+                off_of[x] = off + o - n;
+            slots += __shfl_sync(0xffffffffu, s, 31);
+            off += __shfl_sync(0xffffffffu, o, 31);
+            up += __shfl_sync(0xffffffffu, u, 31);
+            down += __shfl_sync(0xffffffffu, d, 31);
+        }
+        if (lane == 0) {
+            p.tab.ex_off[slots] = off;
+            p.tab.pre_up[slots] = up;
+            p.tab.pre_down[slots] = down;
+            p.tab.n_active[0] = slots;
+        }
+    }
+    __syncthreads();
+    for (int x = tid; x < p.experts; x += MOE_THREADS) {
+        if (count[x] == 0)
+            continue;
+        int at = off_of[x];
+        for (int i = 0; i < pairs; ++i)
+            if (ids[i] == x)
+                p.tab.sorted[at++] = i;
+    }
+}
+
+struct MoeGemm {
+    const int32_t *w;        // packed tiles of every expert
+    const uint16_t *s, *z;   // [E][G][N]; z null: 8
+    const uint16_t *act;     // activation rows in fragment order, K values each
+    uint16_t *h;             // gate-up: the pairs' h, two rows (value, remainder) per pair
+    float *part;             // down: [pairs][N] fp32
+    const uint16_t *residual;
+    uint16_t *y;
+    int *counters;           // down: one per 32 columns
+    MoeTables tab;
+    const int *pre;          // units before each active expert
+    long long expert_words, expert_groups;
+    int k, n, steps;         // steps: 128-row steps of K
+    int kblocks, group_blocks; // 64-row blocks of K, and per group
+    int col_units;           // units per expert and pass
+    int team;                // warps per team
+    int tokens, top, inter, ldy, ldr, glu;
+};
+
+// Gated activations as g sigmoid(x): x = g for silu, 2 sqrt(2/pi) (g + 0.044715 g^3) for gelu_tanh
+// (1 + tanh t = 2 sigmoid(2 t)).
+__device__ __forceinline__ float gate_act(float g, int kind)
+{
+    float x = g;
+    if (kind != 1)
+        x = 2.0f * 0.7978845608028654f * (g + 0.044715f * g * g * g);
+    return g / (1.0f + expf(-x));
+}
+
+__device__ __forceinline__ void team_sync(int team_id, int threads)
+{
+    if (threads == 32)
+        __syncwarp();
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(team_id + 1), "r"(threads) : "memory");
+}
+
+// One unit of a team: an expert, a pass over its pairs and 32 columns.
+struct Unit {
+    int expert, col, first, cols; // first pair (in `sorted`), pairs of this pass
+};
+
+template <int NT, bool DOWN>
+__device__ __forceinline__ Unit find_unit(const MoeGemm &p, int u, int n_active)
+{
+    int lo = 0, hi = n_active - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.pre[mid] <= u)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    constexpr int PASS = DOWN ? 4 * NT : 8 * NT; // a pair takes two columns of the down MMA
+    const int local = u - p.pre[lo], pass = local / p.col_units;
+    Unit r;
+    r.expert = p.tab.ex_id[lo];
+    r.col = local - pass * p.col_units;
+    const int off = p.tab.ex_off[lo], end = p.tab.ex_off[lo + 1];
+    r.first = off + pass * PASS;
+    r.cols = min(PASS, end - r.first);
+    return r;
+}
+
+// NT: 8-column tiles of the MMA's token side.  DOWN false: gate-up, true: down.
+template <int NT, bool BF, bool DOWN>
+__global__ void __launch_bounds__(MOE_THREADS, NT <= 2 ? 2 : 1) moe_layer_gemm_kernel(const MoeGemm p)
+{
+    constexpr int STAGES = NT <= 2 ? 4 : 6;
+    constexpr int VALS = DOWN ? 2 * NT * 2 : 2 * NT * 4; // sums per lane that the warps join
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int last_sh[MOE_WARPS];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const int teams = MOE_WARPS / p.team, team = warp / p.team, member = warp - team * p.team;
+    const int team_threads = p.team * 32, team_tid = member * 32 + lane;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * STAGES * MOE_STAGE;
+    const uint8_t *ring_p = smem + warp * STAGES * MOE_STAGE;
+    float *red = reinterpret_cast<float *>(smem + MOE_WARPS * STAGES * MOE_STAGE); // [warp][VALS][32]
+    pdl_wait();
+    pdl_launch_dependents();
+    const int n_active = __ldcg(p.tab.n_active);
+    const int units = __ldcg(p.pre + n_active);
+    const int stride = gridDim.x * teams;
+    const int u0 = blockIdx.x * teams + team;
+    if (u0 >= units)
+        return; // the whole team leaves; the other teams of the block have barriers of their own
+
+    // --- the copying side: (unit, step) runs ahead of the computing side -----------------------
+    int iu = u0, is = member;
+    const int32_t *i_w = nullptr;
+    long long i_s = 0; // element of the expert's scale row 0 at this unit's first column
+    auto enter = [&]() {
+        if (iu < units) {
+            const Unit un = find_unit<NT, DOWN>(p, iu, n_active);
+            const int n0 = un.col * MOE_COLS;
+            i_w = p.w + un.expert * p.expert_words + (long long)(n0 >> 7) * p.kblocks * 1024 + (n0 & 127) * 4;
+            i_s = (un.expert * p.expert_groups) * p.n + n0;
+        }
+    };
+    if (is < p.steps)
+        enter();
+    else
+        iu = units; // a member without a step copies nothing
+    auto issue = [&](int stage) {
+        if (iu < units) {
+            const uint32_t st = ring + stage * MOE_STAGE;
+            const int32_t *w = i_w + (long long)is * 2048 + lane * 4;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) // (block r >> 1, half r & 1) of column `lane`
+                cp_async16(st + r * 512 + ((lane ^ ((r & 1) << 2)) << 4), w + r * 512, true);
+            // Scale (lanes 0-7) and zero (8-15) rows of the two blocks, four 16-byte chunks each.
+            if (lane < (p.z ? 16 : 8)) {
+                const int grp = (2 * is + ((lane >> 2) & 1)) / p.group_blocks;
+                const uint16_t *src = (lane < 8 ? p.s : p.z) + i_s + (long long)grp * p.n + (lane & 3) * 8;
+                cp_async16(st + MOE_W_BYTES + lane * 16, src, true);
+            }
+            is += p.team;
+            if (is >= p.steps) {
+                is = member;
+                iu += stride;
+                enter();
+            }
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s)
+        issue(s);
+
+    int stage = 0;
+    for (int u = u0; u < units; u += stride) {
+        const Unit un = find_unit<NT, DOWN>(p, u, n_active);
+        const int rows = DOWN ? 2 * un.cols : un.cols; // columns in use on the token side
+        const int nts = (rows + 7) >> 3;
+        // This lane's activation row of each 8-column tile (a column past the last repeats it).
+        const uint16_t *arow[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int c = min(n * 8 + g, rows - 1);
+            const int row = DOWN ? 2 * un.first + c : p.tab.sorted[un.first + c] / p.top;
+            arow[n] = p.act + (long long)row * p.k + t * 8;
+        }
+        float out[2][NT][4];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    out[m][n][i] = 0.f;
+
+        for (int step = member; step < p.steps; step += p.team) {
+            cp_async_wait<STAGES - 2>();
+            __syncwarp(); // every lane's copies have landed, and the stage before is free again
+            issue(stage == 0 ? STAGES - 1 : stage - 1);
+            const uint8_t *st = ring_p + stage * MOE_STAGE;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                uint2 w[2][2]; // [column tile][column g, g + 8]: words 2 (t >> 1), + 1 of half t & 1
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int col = (m * 16 + c * 8 + g) ^ ((t & 1) << 2);
+                        w[m][c] = *reinterpret_cast<const uint2 *>(st + b * 1024 + (t & 1) * 512 + col * 16 + (t >> 1) * 8);
+                    }
+                float sc[2][2], zp[2][2];
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int col = m * 16 + c * 8 + g;
+                        sc[m][c] = to_float<BF>(*reinterpret_cast<const uint16_t *>(st + MOE_W_BYTES + b * MOE_SZ_BYTES + col * 2));
+                        zp[m][c] = (p.z ? to_float<BF>(*reinterpret_cast<const uint16_t *>(
+                                              st + MOE_W_BYTES + (2 + b) * MOE_SZ_BYTES + col * 2))
+                                        : 8.f) + (BF ? 128.f : 0.f);
+                    }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    if (n > 0 && n >= nts)
+                        break;
+                    const uint4 *ap = reinterpret_cast<const uint4 *>(arow[n] + (long long)(2 * step + b) * 64);
+                    const uint4 v0 = ap[0], v1 = ap[4];
+                    const uint32_t bf[2][4] = {{v0.x, v0.y, v0.z, v0.w}, {v1.x, v1.y, v1.z, v1.w}};
+                    float lo[2][4], hi[2][4], sa[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        sa[i] = 0.f;
+                        lo[0][i] = lo[1][i] = hi[0][i] = hi[1][i] = 0.f;
+                    }
+                    constexpr uint32_t ONES = BF ? 0x3F803F80u : 0x3C003C00u;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        mma16816<BF>(sa, ONES, ONES, ONES, ONES, bf[i][0], bf[i][2]);
+                        mma16816<BF>(sa, ONES, ONES, ONES, ONES, bf[i][1], bf[i][3]);
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            const uint32_t x = i ? w[m][0].y : w[m][0].x, y = i ? w[m][1].y : w[m][1].x;
+                            if (BF) {
+                                constexpr uint32_t M = 0x000F000Fu, O = 0x43004300u;
+                                mma16816<BF>(lo[m], (x & M) | O, (y & M) | O, ((x >> 8) & M) | O,
+                                             ((y >> 8) & M) | O, bf[i][0], bf[i][2]);
+                                mma16816<BF>(hi[m], ((x >> 4) & M) | O, ((y >> 4) & M) | O,
+                                             ((x >> 12) & M) | O, ((y >> 12) & M) | O, bf[i][1], bf[i][3]);
+                            } else {
+                                constexpr uint32_t L = 0x000F000Fu, H = 0x00F000F0u;
+                                const uint32_t x8 = x >> 8, y8 = y >> 8;
+                                mma16816<BF>(lo[m], x & L, y & L, x8 & L, y8 & L, bf[i][0], bf[i][2]);
+                                mma16816<BF>(hi[m], x & H, y & H, x8 & H, y8 & H, bf[i][1], bf[i][3]);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int c = i >> 1; // accumulator rows: column g, then g + 8
+                            const float za = zp[m][c] * sa[i & 1];
+                            const float q = BF ? (lo[m][i] + hi[m][i]) - za
+                                               : fmaf(fmaf(hi[m][i], 0.0625f, lo[m][i]), 16777216.f, -za);
+                            out[m][n][i] = fmaf(sc[m][c], q, out[m][n][i]);
+                        }
+                }
+            }
+            stage = stage + 1 == STAGES ? 0 : stage + 1;
+        }
+
+        // --- the team's warps join their sums (fixed order) -----------------------------------
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                if (DOWN) { // columns 2 t and 2 t + 1 are a pair's value and remainder
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        red[(warp * VALS + (m * NT + n) * 2 + c) * 32 + lane] = out[m][n][2 * c] + out[m][n][2 * c + 1];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        red[(warp * VALS + (m * NT + n) * 4 + i) * 32 + lane] = out[m][n][i];
+                }
+            }
+        team_sync(team, team_threads);
+        const float *tr = red + team * p.team * VALS * 32;
+        auto joined = [&](int v, int ln) {
+            float s = 0.f;
+            for (int w = 0; w < p.team; ++w)
+                s += tr[(w * VALS + v) * 32 + ln];
+            return s;
+        };
+        if (!DOWN) {
+            // (tile n, register i, lane): gate column g + 8 (i >> 1) of the first 16, up of the last.
+            for (int x = team_tid; x < NT * 4 * 32; x += team_threads) {
+                const int ln = x & 31, v = x >> 5, n = v >> 2, i = v & 3;
+                const int pr = n * 8 + 2 * (ln & 3) + (i & 1);
+                if (pr >= un.cols)
+                    continue;
+                const float gate = joined(v, ln), up = joined(NT * 4 + v, ln);
+                const float hv = gate_act(gate, p.glu) * up;
+                const int f = un.col * 16 + (ln >> 2) + 8 * (i >> 1);
+                // fp16: the value part stops at the largest finite value and the remainder goes on
+                // from there (a NaN stays one).
+                const float hc = !BF && fabsf(hv) > 65504.f ? copysignf(65504.f, hv) : hv;
+                const uint16_t hb = from_float<BF>(hc);
+                uint16_t *dst = p.h + (long long)(2 * (un.first + pr)) * p.inter + (f & ~63) + frag_index(f & 63);
+                dst[0] = hb;
+                dst[p.inter] = from_float<BF>(hv - to_float<BF>(hb));
+            }
+        } else {
+            for (int x = team_tid; x < 2 * NT * 2 * 32; x += team_threads) {
+                const int ln = x & 31, v = x >> 5, c = v & 1, n = (v >> 1) % NT, m = (v >> 1) / NT;
+                const int pr = n * 4 + (ln & 3);
+                if (pr >= un.cols)
+                    continue;
+                const int pair = p.tab.sorted[un.first + pr];
+                __stcg(p.part + (long long)pair * p.n + un.col * MOE_COLS + m * 16 + c * 8 + (ln >> 2), joined(v, ln));
+            }
+        }
+        team_sync(team, team_threads); // `red` is free; the team's stores are done
+        if (DOWN) {
+            if (team_tid == 0) {
+                int *counter = p.counters + un.col;
+                const int last = arrive_counter(counter) == units / p.col_units - 1;
+                if (last)
+                    *counter = 0;
+                last_sh[team] = last;
+            }
+            team_sync(team, team_threads);
+            if (last_sh[team]) {
+                for (int x = team_tid; x < p.tokens * (MOE_COLS / 4); x += team_threads) {
+                    const int tok = x / (MOE_COLS / 4), col = un.col * MOE_COLS + (x % (MOE_COLS / 4)) * 4;
+                    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int j = 0; j < p.top; ++j) {
+                        const int pair = tok * p.top + j;
+                        const float wt = p.tab.weights[pair];
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part + (long long)pair * p.n + col));
+                        a.x = fmaf(wt, v.x, a.x);
+                        a.y = fmaf(wt, v.y, a.y);
+                        a.z = fmaf(wt, v.z, a.z);
+                        a.w = fmaf(wt, v.w, a.w);
+                    }
+                    if (p.residual) {
+                        const uint2 rv = *reinterpret_cast<const uint2 *>(p.residual + (long long)tok * p.ldr + col);
+                        const float2 r0 = unpack2<BF>(rv.x), r1 = unpack2<BF>(rv.y);
+                        a.x += r0.x;
+                        a.y += r0.y;
+                        a.z += r1.x;
+                        a.w += r1.y;
+                    }
+                    uint2 o;
+                    o.x = pack2<BF>(a.x, a.y);
+                    o.y = pack2<BF>(a.z, a.w);
+                    *reinterpret_cast<uint2 *>(p.y + (long long)tok * p.ldy + col) = o;
+                }
+            }
+        }
+    }
+    cp_async_wait<0>();
+}
+
+namespace {
+
+struct MoeLayout {
+    long long counters, logits, tables, xf, h, part, total;
+    MoeTables tab;
+};
+
+MoeLayout moe_layout(char *ws, int tokens, int hidden, int inter, int experts, int top)
+{
+    MoeLayout l;
+    const int chunks = (tokens + MOE_CHUNK - 1) / MOE_CHUNK, pairs = tokens * top;
+    l.counters = HEADER_BYTES;
+    l.logits = round_up(l.counters + 4LL * (chunks + 1 + hidden / MOE_COLS), 256);
+    l.tables = round_up(l.logits + 4LL * tokens * experts, 256);
+    long long at = l.tables;
+    auto take = [&](long long n) {
+        char *r = ws + at;
+        at += 4 * n;
+        return r;
+    };
+    l.tab.n_active = reinterpret_cast<int *>(take(4));
+    l.tab.ex_id = reinterpret_cast<int *>(take(MOE_MAX_EXPERTS));
+    l.tab.ex_off = reinterpret_cast<int *>(take(MOE_MAX_EXPERTS + 1));
+    l.tab.pre_up = reinterpret_cast<int *>(take(MOE_MAX_EXPERTS + 1));
+    l.tab.pre_down = reinterpret_cast<int *>(take(MOE_MAX_EXPERTS + 1));
+    l.tab.sorted = reinterpret_cast<int *>(take(pairs));
+    l.tab.ids = reinterpret_cast<int *>(take(pairs));
+    l.tab.weights = reinterpret_cast<float *>(take(pairs));
+    l.xf = round_up(at, 256);
+    l.h = round_up(l.xf + 2LL * tokens * hidden, 256);
+    l.part = round_up(l.h + 4LL * pairs * inter, 256);
+    l.total = round_up(l.part + 4LL * pairs * hidden, 256);
+    return l;
+}
+
+int check_layer_sizes(int tokens, int hidden, int inter, int experts, int top)
+{
+    if (tokens < 0 || hidden <= 0 || inter <= 0)
+        return status_of(STAGE_ARG, W4A16_ARG_SHAPE);
+    if (experts <= 0 || top <= 0 || top > experts)
+        return status_of(STAGE_ARG, W4A16_ARG_SCHEDULE);
+    if (tokens > MOE_MAX_TOKENS || hidden % 256 != 0 || inter % 128 != 0)
+        return status_of(STAGE_UNSUPPORTED, W4A16_ARG_SHAPE);
+    if (experts > MOE_MAX_EXPERTS || top > MOE_MAX_TOP)
+        return status_of(STAGE_UNSUPPORTED, W4A16_ARG_SCHEDULE);
+    if ((long long)experts * hidden * inter / 4 > (1LL << 40) || hidden > (1 << 20) || inter > (1 << 20))
+        return status_of(STAGE_ARG, W4A16_ARG_OVERFLOW);
+    return 0;
+}
+
+using GemmKernel = void (*)(MoeGemm);
+struct MoeFamily;
+
+constexpr int moe_smem(int nt, bool down)
+{
+    return MOE_WARPS * ((nt <= 2 ? 4 : 6) * MOE_STAGE + (down ? 2 * nt * 2 : 2 * nt * 4) * 32 * 4);
+}
+
+template <int NT>
+GemmKernel gemm_kernel(bool bf, bool down)
+{
+    if (bf)
+        return down ? moe_layer_gemm_kernel<NT, true, true> : moe_layer_gemm_kernel<NT, true, false>;
+    return down ? moe_layer_gemm_kernel<NT, false, true> : moe_layer_gemm_kernel<NT, false, false>;
+}
+
+// 8-column tiles of the token side: enough for every token on one expert, at most 4 (32 columns);
+// more pairs on an expert take further passes over its weights.
+int token_tiles(int columns)
+{
+    return columns <= 8 ? 1 : columns <= 16 ? 2 : 4;
+}
+
+// Warps per team: as many as have two steps each.
+int team_warps(int steps)
+{
+    int team = MOE_WARPS;
+    while (team > 1 && steps < 2 * team)
+        team /= 2;
+    return team;
+}
+
+cudaError_t launch_moe_gemm(MoeGemm &p, int nt, bool bf, bool down, int num_sms, cudaStream_t stream)
+{
+    const GemmKernel kernel = nt == 1 ? gemm_kernel<1>(bf, down) : nt == 2 ? gemm_kernel<2>(bf, down) : gemm_kernel<4>(bf, down);
+    const int smem = moe_smem(nt, down);
+    const int v = (nt == 1 ? 0 : nt == 2 ? 1 : 2) * 4 + (bf ? 2 : 0) + (down ? 1 : 0);
+    cudaError_t err = allow_smem<MoeFamily, 12>(reinterpret_cast<const void *>(kernel), v, smem);
+    if (err != cudaSuccess)
+        return err;
+    p.team = team_warps(p.steps);
+    return launch_pdl(kernel, dim3(num_sms * (nt <= 2 ? 2 : 1)), dim3(MOE_THREADS), (size_t)smem, stream, p);
+}
+
+} // namespace
+} // namespace ops
+} // namespace w4
+
+using namespace w4;
+using namespace w4::ops;
+
+extern "C" size_t w4a16_moe_layer_workspace_size(int n_tokens, int hidden, int inter, int n_experts, int top_k)
+{
+    if (check_layer_sizes(n_tokens, hidden, inter, n_experts, top_k) != 0)
+        return 0;
+    return (size_t)moe_layout(nullptr, n_tokens > 0 ? n_tokens : 1, hidden, inter, n_experts, top_k).total;
+}
+
+extern "C" int w4a16_moe_layer(const void *x, int ldx, const void *router, const int32_t *gate_up,
+                               const void *gate_up_scales, const void *gate_up_zeros, const int32_t *down,
+                               const void *down_scales, const void *down_zeros, const void *residual, int ldr,
+                               void *y, int ldy, int32_t *topk_ids, float *topk_weights, void *workspace,
+                               size_t workspace_bytes, int n_tokens, int hidden, int inter, int n_experts,
+                               int top_k, int group_size, int weight_type, unsigned flags, cudaStream_t stream)
+{
+    if (weight_type != W4A16_TYPE_U4 && weight_type != W4A16_TYPE_U4B8)
+        return status_of(STAGE_ARG, W4A16_ARG_TYPE);
+    const unsigned known = W4A16_FLAG_BF16 | W4A16_FLAG_IS_K_FULL | W4A16_FLAG_HAS_ZP | W4A16_FLAG_SWIGLU |
+                           W4A16_FLAG_GEGLU | W4A16_FLAG_MOE_RENORM;
+    const bool has_zp = (flags & W4A16_FLAG_HAS_ZP) != 0;
+    const bool sw = (flags & W4A16_FLAG_SWIGLU) != 0, ge = (flags & W4A16_FLAG_GEGLU) != 0;
+    if ((flags & ~known) || sw == ge || has_zp != (weight_type == W4A16_TYPE_U4) ||
+        has_zp != (gate_up_zeros != nullptr) || has_zp != (down_zeros != nullptr))
+        return status_of(STAGE_ARG, W4A16_ARG_FLAGS);
+    int st = check_layer_sizes(n_tokens, hidden, inter, n_experts, top_k);
+    if (st)
+        return st;
+    if (group_size != -1 &&
+        (group_size <= 0 || group_size % 64 != 0 || hidden % group_size != 0 || inter % group_size != 0))
+        return status_of(STAGE_ARG, W4A16_ARG_GROUP);
+    if (n_tokens == 0)
+        return 0;
+    if (!x || !router || !gate_up || !gate_up_scales || !down || !down_scales || !y || !workspace)
+        return status_of(STAGE_ARG, W4A16_ARG_NULL);
+    if (ldx < hidden || ldy < hidden || (residual && ldr < hidden))
+        return status_of(STAGE_ARG, W4A16_ARG_SHAPE);
+    if (ldx % 8 != 0 || ldy % 8 != 0 || (residual && ldr % 8 != 0) || !aligned(x, 16) || !aligned(router, 16) ||
+        !aligned(gate_up, 16) || !aligned(gate_up_scales, 16) || !aligned(gate_up_zeros, 16) ||
+        !aligned(down, 16) || !aligned(down_scales, 16) || !aligned(down_zeros, 16) || !aligned(residual, 16) ||
+        !aligned(y, 16) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4) || !aligned(workspace, 256))
+        return status_of(STAGE_ARG, W4A16_ARG_ALIGN);
+    char *ws = static_cast<char *>(workspace);
+    const MoeLayout lay = moe_layout(ws, n_tokens, hidden, inter, n_experts, top_k);
+    if (workspace_bytes < (size_t)lay.total)
+        return status_of(STAGE_ARG, W4A16_ARG_WORKSPACE);
+    int num_sms = 0;
+    cudaError_t err = sm_count(&num_sms);
+    if (err != cudaSuccess)
+        return status_of(STAGE_RESOURCE, err);
+
+    const bool bf = (flags & W4A16_FLAG_BF16) != 0;
+    const int chunks = (n_tokens + MOE_CHUNK - 1) / MOE_CHUNK;
+    const int nt_up = token_tiles(n_tokens), nt_down = token_tiles(2 * n_tokens);
+    int *counters = reinterpret_cast<int *>(ws + lay.counters);
+    RouteParams r;
+    r.x = static_cast<const uint16_t *>(x);
+    r.router = static_cast<const uint16_t *>(router);
+    r.xf = reinterpret_cast<uint16_t *>(ws + lay.xf);
+    r.logits = reinterpret_cast<float *>(ws + lay.logits);
+    r.topk_ids = topk_ids;
+    r.topk_weights = topk_weights;
+    r.counters = counters;
+    r.tab = lay.tab;
+    r.ldx = ldx;
+    r.tokens = n_tokens;
+    r.hidden = hidden;
+    r.experts = n_experts;
+    r.top = top_k;
+    r.renorm = (flags & W4A16_FLAG_MOE_RENORM) ? 1 : 0;
+    r.up_cols = 2 * inter / MOE_COLS;
+    r.down_cols = hidden / MOE_COLS;
+    r.up_pass = 8 * nt_up;
+    r.down_pass = 4 * nt_down;
+    const dim3 grid((n_experts + MOE_WARPS - 1) / MOE_WARPS, chunks);
+    err = bf ? launch_pdl(moe_layer_route_kernel<true>, grid, dim3(MOE_THREADS), 0, stream, r)
+             : launch_pdl(moe_layer_route_kernel<false>, grid, dim3(MOE_THREADS), 0, stream, r);
+    if (err != cudaSuccess)
+        return status_of(STAGE_LAUNCH, err);
+
+    MoeGemm m;
+    m.w = gate_up;
+    m.s = static_cast<const uint16_t *>(gate_up_scales);
+    m.z = static_cast<const uint16_t *>(gate_up_zeros);
+    m.act = r.xf;
+    m.h = reinterpret_cast<uint16_t *>(ws + lay.h);
+    m.part = reinterpret_cast<float *>(ws + lay.part);
+    m.residual = static_cast<const uint16_t *>(residual);
+    m.y = static_cast<uint16_t *>(y);
+    m.counters = counters + chunks + 1;
+    m.tab = lay.tab;
+    m.pre = lay.tab.pre_up;
+    m.k = hidden;
+    m.n = 2 * inter;
+    m.tokens = n_tokens;
+    m.top = top_k;
+    m.inter = inter;
+    m.ldy = ldy;
+    m.ldr = ldr;
+    m.glu = sw ? 1 : 2;
+    auto sizes = [&]() {
+        m.expert_words = (long long)m.k * m.n / 8;
+        m.steps = m.k / MOE_ROWS;
+        m.kblocks = m.k / 64;
+        m.group_blocks = group_size == -1 ? m.kblocks : group_size / 64;
+        m.expert_groups = m.kblocks / m.group_blocks;
+        m.col_units = m.n / MOE_COLS;
+    };
+    sizes();
+    err = launch_moe_gemm(m, nt_up, bf, false, num_sms, stream);
+    if (err != cudaSuccess)
+        return status_of(STAGE_LAUNCH, err);
+    m.w = down;
+    m.s = static_cast<const uint16_t *>(down_scales);
+    m.z = static_cast<const uint16_t *>(down_zeros);
+    m.act = m.h;
+    m.pre = lay.tab.pre_down;
+    m.k = inter;
+    m.n = hidden;
+    sizes();
+    return launch_status(launch_moe_gemm(m, nt_down, bf, true, num_sms, stream));
+}

@@ -1,0 +1,334 @@
+// w4a16_rope.cu -- rotary positions on q and k, and k and v written into a paged cache.
+//
+// For token t and pair i of the rotated part of a head (i < rot_dim / 2), with the axis a that the
+// sections give to pair i and (c, s) = table[positions[a][t]][i], [rot_dim / 2 + i]:
+//     (x1, x2) -> (x1 c - x2 s, x2 c + x1 s),
+// where (x1, x2) are values i and rot_dim / 2 + i of the head, or 2 i and 2 i + 1 (adjacent pairs).
+// The rest of a head is copied.  Two fp32 products and one fp32 sum per value, rounded once.
+//
+// Bound by memory: each value of q, k and v is read once and written once, with one row of the
+// table per token and axis.  A thread keeps the cosines and sines of eight pairs in registers and
+// applies them to HEADS heads of its token, so the table is read once for HEADS x 16 values and
+// there are 2 x HEADS 16-byte loads in flight per thread.
+#include "w4a16_ops.cuh"
+
+namespace w4 {
+namespace ops {
+
+constexpr int ROPE_MAX_AXES = 4;
+constexpr int ROPE_HEADS = 4;     // heads per thread (16-byte path)
+constexpr int ROPE_THREADS = 128; // threads a block is filled up to
+
+struct RopeParams {
+    const uint16_t *q, *k, *v;
+    uint16_t *q_out, *k_cache, *v_cache;
+    const float *table;       // [max_pos][rot]: cosines, then sines
+    const int32_t *positions; // [axes][ld_pos]
+    const long long *slots;   // [tokens]
+    int *status;
+    long long page_stride, token_stride, head_stride, total_slots;
+    int ldq, ldk, ldv, ldqo, ld_pos;
+    int tokens, heads, kv, dim, rot, axes, max_pos, page;
+    int cut[ROPE_MAX_AXES]; // pair i belongs to the first axis a with i < cut[a]
+    int adjacent;
+};
+
+__device__ __forceinline__ void report(const RopeParams &p, int bit)
+{
+    if (p.status)
+        atomicOr(p.status, bit);
+}
+
+// Position of pair `pair`'s axis, or -1 after reporting one outside the table.
+__device__ __forceinline__ int position_of(const RopeParams &p, int token, int pair)
+{
+    int axis = 0;
+#pragma unroll
+    for (int a = 0; a < ROPE_MAX_AXES - 1; ++a)
+        axis += (a < p.axes - 1 && pair >= p.cut[a]) ? 1 : 0;
+    const int pos = p.positions[(long long)axis * p.ld_pos + token];
+    if (pos < 0 || pos >= p.max_pos) {
+        report(p, W4A16_DEV_POSITION);
+        return -1;
+    }
+    return pos;
+}
+
+// Element offset of a token's cache row (head 0), or -1: a negative slot (not cached) or, after
+// reporting it, one past the cache.
+__device__ __forceinline__ long long cache_row(const RopeParams &p, int token)
+{
+    const long long slot = p.kv > 0 ? p.slots[token] : -1;
+    if (slot < 0)
+        return -1;
+    if (slot >= p.total_slots) {
+        report(p, W4A16_DEV_SLOT);
+        return -1;
+    }
+    const long long pg = slot / p.page;
+    return pg * p.page_stride + (slot - pg * p.page) * p.token_stride;
+}
+
+// Source and destination of head h of the joint list (q heads, k heads, v heads); dst null: the
+// head is not written.
+__device__ __forceinline__ void head_ptrs(const RopeParams &p, int token, int h, long long row,
+                                          const uint16_t *&src, uint16_t *&dst)
+{
+    if (h < p.heads) {
+        src = p.q + (long long)token * p.ldq + (long long)h * p.dim;
+        dst = p.q_out + (long long)token * p.ldqo + (long long)h * p.dim;
+        return;
+    }
+    const int kh = h - p.heads;
+    const bool is_k = kh < p.kv;
+    const int c = is_k ? kh : kh - p.kv;
+    src = is_k ? p.k + (long long)token * p.ldk + (long long)c * p.dim
+               : p.v + (long long)token * p.ldv + (long long)c * p.dim;
+    dst = row < 0 ? nullptr : (is_k ? p.k_cache : p.v_cache) + row + c * p.head_stride;
+}
+
+// 16-byte path: rows, strides and cache 16-byte aligned, dim and rot multiples of 16.  Thread
+// (chunk j, head group) of a token: chunk j < rot / 16 is eight pairs, a later one 16 values that
+// are copied.
+template <bool BF>
+__global__ void __launch_bounds__(256) rope_vec_kernel(const RopeParams p, int chunks, int groups)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    const int token = blockIdx.x * blockDim.y + threadIdx.y;
+    if (token >= p.tokens)
+        return;
+    const int all = p.heads + 2 * p.kv, half = p.rot / 2, turned = p.rot / 16;
+    const long long row = cache_row(p, token);
+    for (int item = threadIdx.x; item < chunks * groups; item += blockDim.x) {
+        const int g = item / chunks, j = item - g * chunks;
+        // Values of the two 16-byte pieces: pairs (i, half + i), or 16 values in a row.
+        const bool pairs = j < turned;
+        const int at0 = pairs && !p.adjacent ? 8 * j : 16 * j;
+        const int at1 = pairs && !p.adjacent ? half + 8 * j : 16 * j + 8;
+        float c[8], s[8];
+        bool known = true;
+        if (pairs) {
+            // A section may end inside the chunk; one lookup serves the pairs up to its end.
+            int pos = position_of(p, token, 8 * j), last = position_of(p, token, 8 * j + 7);
+            known = pos >= 0 && last >= 0;
+            if (known) {
+#pragma unroll
+                for (int i = 0; i < 8; i += 4) {
+                    *reinterpret_cast<float4 *>(c + i) =
+                        *reinterpret_cast<const float4 *>(p.table + (long long)pos * p.rot + 8 * j + i);
+                    *reinterpret_cast<float4 *>(s + i) =
+                        *reinterpret_cast<const float4 *>(p.table + (long long)pos * p.rot + half + 8 * j + i);
+                }
+                bool cuts = false;
+#pragma unroll
+                for (int a = 0; a < ROPE_MAX_AXES - 1; ++a)
+                    cuts |= a < p.axes - 1 && p.cut[a] > 8 * j && p.cut[a] < 8 * j + 8;
+                if (cuts) {
+#pragma unroll
+                    for (int i = 1; i < 8; ++i) {
+                        const int pi = position_of(p, token, 8 * j + i);
+                        if (pi < 0) {
+                            known = false;
+                        } else {
+                            c[i] = p.table[(long long)pi * p.rot + 8 * j + i];
+                            s[i] = p.table[(long long)pi * p.rot + half + 8 * j + i];
+                        }
+                    }
+                }
+            }
+        }
+        const uint16_t *src[ROPE_HEADS];
+        uint16_t *dst[ROPE_HEADS];
+        uint4 x0[ROPE_HEADS], x1[ROPE_HEADS];
+#pragma unroll
+        for (int n = 0; n < ROPE_HEADS; ++n) {
+            const int h = g * ROPE_HEADS + n;
+            dst[n] = nullptr;
+            if (h < all)
+                head_ptrs(p, token, h, row, src[n], dst[n]);
+            if (h < all - p.kv && !known)
+                dst[n] = nullptr; // values without a position are not written
+            if (dst[n]) {
+                x0[n] = *reinterpret_cast<const uint4 *>(src[n] + at0);
+                x1[n] = *reinterpret_cast<const uint4 *>(src[n] + at1);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < ROPE_HEADS; ++n) {
+            if (!dst[n])
+                continue;
+            const int h = g * ROPE_HEADS + n;
+            if (pairs && h < all - p.kv) {
+                uint32_t *w0 = reinterpret_cast<uint32_t *>(&x0[n]);
+                uint32_t *w1 = reinterpret_cast<uint32_t *>(&x1[n]);
+                if (p.adjacent) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 a = unpack2<BF>(w0[i]), b = unpack2<BF>(w1[i]);
+                        w0[i] = pack2<BF>(a.x * c[i] - a.y * s[i], a.y * c[i] + a.x * s[i]);
+                        w1[i] = pack2<BF>(b.x * c[4 + i] - b.y * s[4 + i], b.y * c[4 + i] + b.x * s[4 + i]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 a = unpack2<BF>(w0[i]), b = unpack2<BF>(w1[i]);
+                        const float c0 = c[2 * i], c1 = c[2 * i + 1], s0 = s[2 * i], s1 = s[2 * i + 1];
+                        w0[i] = pack2<BF>(a.x * c0 - b.x * s0, a.y * c1 - b.y * s1);
+                        w1[i] = pack2<BF>(b.x * c0 + a.x * s0, b.y * c1 + a.y * s1);
+                    }
+                }
+            }
+            *reinterpret_cast<uint4 *>(dst[n] + at0) = x0[n];
+            *reinterpret_cast<uint4 *>(dst[n] + at1) = x1[n];
+        }
+    }
+}
+
+// Any even rot, any dim, any strides: one pair (or two copied values) per thread and head.
+template <bool BF>
+__global__ void __launch_bounds__(256) rope_any_kernel(const RopeParams p)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    const int token = blockIdx.x;
+    const int all = p.heads + 2 * p.kv, half = p.rot / 2;
+    const int rest = p.dim - p.rot, items = half + (rest + 1) / 2;
+    const long long row = cache_row(p, token);
+    for (long long n = threadIdx.x; n < (long long)items * all; n += blockDim.x) {
+        const int h = (int)(n / items), i = (int)(n - (long long)h * items);
+        const uint16_t *src;
+        uint16_t *dst;
+        head_ptrs(p, token, h, row, src, dst);
+        const bool turn = h < all - p.kv;
+        int pos = 0;
+        if (turn && i < half)
+            pos = position_of(p, token, i);
+        if (!dst || pos < 0)
+            continue;
+        if (i < half) {
+            const int a = p.adjacent ? 2 * i : i, b = p.adjacent ? 2 * i + 1 : half + i;
+            uint16_t ra = src[a], rb = src[b];
+            if (turn) {
+                const float c = p.table[(long long)pos * p.rot + i], s = p.table[(long long)pos * p.rot + half + i];
+                const float x = to_float<BF>(ra), y = to_float<BF>(rb);
+                ra = from_float<BF>(x * c - y * s);
+                rb = from_float<BF>(y * c + x * s);
+            }
+            dst[a] = ra;
+            dst[b] = rb;
+        } else {
+            const int a = p.rot + 2 * (i - half);
+            dst[a] = src[a];
+            if (a + 1 < p.dim)
+                dst[a + 1] = src[a + 1];
+        }
+    }
+}
+
+} // namespace ops
+} // namespace w4
+
+using namespace w4;
+using namespace w4::ops;
+
+extern "C" int w4a16_rope_append(const void *q, int ldq, const void *k, int ldk, const void *v, int ldv,
+                                 void *q_out, int ldqo, void *k_cache, void *v_cache,
+                                 long long kv_page_stride, long long kv_token_stride,
+                                 long long kv_head_stride, const float *cos_sin, int max_pos,
+                                 const int32_t *positions, int ld_pos, const long long *slots,
+                                 int32_t *status, int n_tokens, int n_heads, int n_kv_heads,
+                                 int head_dim, int rot_dim, const int32_t *sections, int n_axes,
+                                 int page_size, int n_pages, unsigned flags, cudaStream_t stream)
+{
+    if (flags & ~(W4A16_FLAG_BF16 | W4A16_FLAG_ROPE_ADJACENT))
+        return status_of(STAGE_ARG, W4A16_ARG_FLAGS);
+    if (n_tokens < 0 || n_heads < 0 || n_kv_heads < 0 || n_heads + (long long)n_kv_heads <= 0 ||
+        head_dim <= 0 || rot_dim <= 0 || rot_dim % 2 != 0 || rot_dim > head_dim || max_pos <= 0 ||
+        n_axes <= 0 || n_axes > ROPE_MAX_AXES || (n_kv_heads > 0 && (page_size <= 0 || n_pages <= 0)))
+        return status_of(STAGE_ARG, W4A16_ARG_SHAPE);
+    if (!sections)
+        return status_of(STAGE_ARG, W4A16_ARG_NULL);
+    long long sum = 0;
+    for (int a = 0; a < n_axes; ++a) {
+        if (sections[a] < 0)
+            return status_of(STAGE_ARG, W4A16_ARG_SHAPE);
+        sum += sections[a];
+    }
+    if (sum != rot_dim / 2)
+        return status_of(STAGE_ARG, W4A16_ARG_SHAPE);
+    if (n_tokens == 0)
+        return 0;
+    if (!cos_sin || !positions || (n_heads > 0 && (!q || !q_out)) ||
+        (n_kv_heads > 0 && (!k || !v || !k_cache || !v_cache || !slots)))
+        return status_of(STAGE_ARG, W4A16_ARG_NULL);
+    const long long qw = (long long)n_heads * head_dim, kw = (long long)n_kv_heads * head_dim;
+    if (qw > 0x7FFFFFFFLL || kw > 0x7FFFFFFFLL || (long long)n_heads + 2LL * n_kv_heads > (1 << 20))
+        return status_of(STAGE_ARG, W4A16_ARG_OVERFLOW);
+    if (ldq < qw || ldqo < qw || ldk < kw || ldv < kw || ld_pos < n_tokens ||
+        (n_kv_heads > 0 && (kv_page_stride < 0 || kv_token_stride < 0 || kv_head_stride < 0)))
+        return status_of(STAGE_ARG, W4A16_ARG_SHAPE);
+    if (!aligned(q, 2) || !aligned(k, 2) || !aligned(v, 2) || !aligned(q_out, 2) || !aligned(k_cache, 2) ||
+        !aligned(v_cache, 2) || !aligned(cos_sin, 4) || !aligned(positions, 4) || !aligned(slots, 8) ||
+        !aligned(status, 4))
+        return status_of(STAGE_ARG, W4A16_ARG_ALIGN);
+
+    RopeParams p;
+    p.q = static_cast<const uint16_t *>(q);
+    p.k = static_cast<const uint16_t *>(k);
+    p.v = static_cast<const uint16_t *>(v);
+    p.q_out = static_cast<uint16_t *>(q_out);
+    p.k_cache = static_cast<uint16_t *>(k_cache);
+    p.v_cache = static_cast<uint16_t *>(v_cache);
+    p.table = cos_sin;
+    p.positions = positions;
+    p.slots = slots;
+    p.status = status;
+    p.page_stride = kv_page_stride;
+    p.token_stride = kv_token_stride;
+    p.head_stride = kv_head_stride;
+    p.total_slots = (long long)n_pages * page_size;
+    p.ldq = ldq;
+    p.ldk = ldk;
+    p.ldv = ldv;
+    p.ldqo = ldqo;
+    p.ld_pos = ld_pos;
+    p.tokens = n_tokens;
+    p.heads = n_heads;
+    p.kv = n_kv_heads;
+    p.dim = head_dim;
+    p.rot = rot_dim;
+    p.axes = n_axes;
+    p.max_pos = max_pos;
+    p.page = page_size;
+    p.adjacent = (flags & W4A16_FLAG_ROPE_ADJACENT) ? 1 : 0;
+    int cut = 0;
+    for (int a = 0; a < ROPE_MAX_AXES; ++a) {
+        if (a < n_axes)
+            cut += sections[a];
+        p.cut[a] = cut;
+    }
+    const bool bf = (flags & W4A16_FLAG_BF16) != 0;
+    const long long any = (n_heads ? (long long)(ldq | ldqo) : 0) |
+                          (n_kv_heads ? (ldk | ldv | kv_page_stride | kv_token_stride | kv_head_stride) : 0);
+    const bool vec = head_dim % 16 == 0 && rot_dim % 16 == 0 && any % 8 == 0 && aligned(q, 16) &&
+                     aligned(k, 16) && aligned(v, 16) && aligned(q_out, 16) && aligned(k_cache, 16) &&
+                     aligned(v_cache, 16) && aligned(cos_sin, 16);
+    if (vec) {
+        const int all = n_heads + 2 * n_kv_heads;
+        const int chunks = head_dim / 16, groups = (all + ROPE_HEADS - 1) / ROPE_HEADS;
+        const long long items = (long long)chunks * groups;
+        const int bx = items < 256 ? (int)items : 256;
+        int by = ROPE_THREADS / bx;
+        if (by < 1)
+            by = 1;
+        if (by > n_tokens)
+            by = n_tokens;
+        const dim3 grid((unsigned)((n_tokens + (long long)by - 1) / by)), block(bx, by);
+        return launch_status(bf ? launch_pdl(rope_vec_kernel<true>, grid, block, 0, stream, p, chunks, groups)
+                                : launch_pdl(rope_vec_kernel<false>, grid, block, 0, stream, p, chunks, groups));
+    }
+    const dim3 grid((unsigned)n_tokens), block(256);
+    return launch_status(bf ? launch_pdl(rope_any_kernel<true>, grid, block, 0, stream, p)
+                            : launch_pdl(rope_any_kernel<false>, grid, block, 0, stream, p));
+}
