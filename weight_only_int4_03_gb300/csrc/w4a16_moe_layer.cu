@@ -27,6 +27,8 @@
 // its 128-row steps in turn.  A warp streams its steps through its own ring of cp.async stages, which
 // runs on into its next unit, so no block-wide barrier sits between a copy and its use and the ring
 // stays full across units.  Activations are read from L1/L2 in the MMA's fragment order.
+#include <type_traits>
+
 #include "w4a16_ops.cuh"
 
 namespace w4 {
@@ -39,11 +41,8 @@ constexpr int MOE_MAX_PAIRS = MOE_MAX_TOKENS * MOE_MAX_TOP;
 constexpr int MOE_WARPS = 8;
 constexpr int MOE_THREADS = MOE_WARPS * 32;
 constexpr int MOE_CHUNK = 4;   // tokens per routing block
-constexpr int MOE_COLS = 32;   // weight columns per unit
+constexpr int MOE_COLS = 32;   // fewest weight columns per unit
 constexpr int MOE_ROWS = 128;  // weight rows per step (two 64-row blocks)
-constexpr int MOE_W_BYTES = MOE_ROWS * MOE_COLS / 2;
-constexpr int MOE_SZ_BYTES = MOE_COLS * 2; // one scale (or zero) row of a unit
-constexpr int MOE_STAGE = MOE_W_BYTES + 4 * MOE_SZ_BYTES;
 
 // Element of a 64-row block in the order the MMA's lanes read it: lane t of a quad takes, for
 // i = 0, 1, the eight values of 16-byte chunk 4 i + t, which are rows 32 (t & 1) + 8 p +
@@ -299,7 +298,9 @@ struct MoeGemm {
     const int *pre;          // units before each active expert
     long long expert_words, expert_groups;
     int k, n, steps;         // steps: 128-row steps of K
-    int kblocks, group_blocks; // 64-row blocks of K, and per group
+    int kblocks;             // 64-row blocks of K
+    uint32_t group_magic;    // group of block n: umulhi(n, group_magic), or n when 0
+    int per_block;           // groups of an odd number of blocks: scale every block's sums
     int col_units;           // units per expert and pass
     int team;                // warps per team
     int tokens, top, inter, ldy, ldr, glu;
@@ -323,7 +324,7 @@ __device__ __forceinline__ void team_sync(int team_id, int threads)
         asm volatile("bar.sync %0, %1;" ::"r"(team_id + 1), "r"(threads) : "memory");
 }
 
-// One unit of a team: an expert, a pass over its pairs and 32 columns.
+// One unit of a team: an expert, a pass over its pairs and a range of columns.
 struct Unit {
     int expert, col, first, cols; // first pair (in `sorted`), pairs of this pass
 };
@@ -350,21 +351,40 @@ __device__ __forceinline__ Unit find_unit(const MoeGemm &p, int u, int n_active)
     return r;
 }
 
-// NT: 8-column tiles of the MMA's token side.  DOWN false: gate-up, true: down.
+// Sizes of a kernel variant.  NT: 8-column tiles of the MMA's token side; MT: 16-column tiles of
+// weights, as many as the registers of 16 warps per SM hold beside NT tiles of sums (each activation
+// fragment then serves MT products).
+template <int NT>
+struct MoeGeom {
+    static constexpr int MT = NT <= 2 ? 4 : 2;
+    static constexpr int COLS = 16 * MT;
+    static constexpr int BLOCKS = 4 / MT; // 64-row blocks per stage: 2 KiB of codes
+    static constexpr int SZ = COLS * 2;   // bytes of one scale (or zero) row
+    static constexpr int STAGE = 2048 + 2 * BLOCKS * SZ;
+    static constexpr int STAGES = 4;
+    static constexpr int RING = STAGES * STAGE;
+    static constexpr int vals(bool down) { return MT * NT * (down ? 2 : 4); } // sums per lane to join
+    static constexpr int smem(bool down) { return MOE_WARPS * (RING + vals(down) * 32 * 4); }
+};
+
+// DOWN false: gate-up, true: down.
 template <int NT, bool BF, bool DOWN>
-__global__ void __launch_bounds__(MOE_THREADS, NT <= 2 ? 2 : 1) moe_layer_gemm_kernel(const MoeGemm p)
+__global__ void __launch_bounds__(MOE_THREADS, 2) moe_layer_gemm_kernel(const MoeGemm p)
 {
-    constexpr int STAGES = NT <= 2 ? 4 : 6;
-    constexpr int VALS = DOWN ? 2 * NT * 2 : 2 * NT * 4; // sums per lane that the warps join
+    using G = MoeGeom<NT>;
+    constexpr int MT = G::MT, COLS = G::COLS, STAGES = G::STAGES, VALS = G::vals(DOWN);
+    // fp16 with one token tile: the two nibble positions keep accumulators of their own, which
+    // saves two shifts a word; with more tiles the registers go to the tiles.
+    constexpr bool DUAL = !BF && NT == 1;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int last_sh[MOE_WARPS];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
     const int teams = MOE_WARPS / p.team, team = warp / p.team, member = warp - team * p.team;
     const int team_threads = p.team * 32, team_tid = member * 32 + lane;
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * STAGES * MOE_STAGE;
-    const uint8_t *ring_p = smem + warp * STAGES * MOE_STAGE;
-    float *red = reinterpret_cast<float *>(smem + MOE_WARPS * STAGES * MOE_STAGE); // [warp][VALS][32]
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * G::RING;
+    const uint8_t *ring_p = smem + warp * G::RING;
+    float *red = reinterpret_cast<float *>(smem + MOE_WARPS * G::RING); // [warp][VALS][32]
     pdl_wait();
     pdl_launch_dependents();
     const int n_active = __ldcg(p.tab.n_active);
@@ -374,38 +394,51 @@ __global__ void __launch_bounds__(MOE_THREADS, NT <= 2 ? 2 : 1) moe_layer_gemm_k
     if (u0 >= units)
         return; // the whole team leaves; the other teams of the block have barriers of their own
 
-    // --- the copying side: (unit, step) runs ahead of the computing side -----------------------
-    int iu = u0, is = member;
+    // --- the copying side: (unit, block) runs ahead of the computing side ----------------------
+    // A member takes the 128-row steps member, member + team, ..., each as 2 / BLOCKS stages.
+    int iu = u0, ib = 2 * member;
     const int32_t *i_w = nullptr;
-    long long i_s = 0; // element of the expert's scale row 0 at this unit's first column
+    const uint16_t *i_s = nullptr; // this lane's part of the expert's scale (or zero) row 0
+    // Lane l looks after chunk l % (SZ / 16) of a row; rows: scales of the stage's blocks, then zeros.
+    constexpr int SZ_CHUNKS = G::SZ / 16;
+    const int sz_row = lane / SZ_CHUNKS;
+    const bool sz_zero = sz_row >= G::BLOCKS;
+    const bool sz_mine = sz_row < G::BLOCKS * (p.z ? 2 : 1);
+    const int sz_block = sz_zero ? sz_row - G::BLOCKS : sz_row;
     auto enter = [&]() {
         if (iu < units) {
             const Unit un = find_unit<NT, DOWN>(p, iu, n_active);
-            const int n0 = un.col * MOE_COLS;
+            const int n0 = un.col * COLS;
             i_w = p.w + un.expert * p.expert_words + (long long)(n0 >> 7) * p.kblocks * 1024 + (n0 & 127) * 4;
-            i_s = (un.expert * p.expert_groups) * p.n + n0;
+            i_s = (sz_zero ? p.z : p.s) + un.expert * p.expert_groups * p.n + n0 + (lane % SZ_CHUNKS) * 8;
         }
     };
-    if (is < p.steps)
+    if (member < p.steps)
         enter();
     else
         iu = units; // a member without a step copies nothing
     auto issue = [&](int stage) {
         if (iu < units) {
-            const uint32_t st = ring + stage * MOE_STAGE;
-            const int32_t *w = i_w + (long long)is * 2048 + lane * 4;
+            const uint32_t st = ring + stage * G::STAGE;
+            const int32_t *w = i_w + (long long)ib * 1024;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) // (block r >> 1, half r & 1) of column `lane`
-                cp_async16(st + r * 512 + ((lane ^ ((r & 1) << 2)) << 4), w + r * 512, true);
-            // Scale (lanes 0-7) and zero (8-15) rows of the two blocks, four 16-byte chunks each.
-            if (lane < (p.z ? 16 : 8)) {
-                const int grp = (2 * is + ((lane >> 2) & 1)) / p.group_blocks;
-                const uint16_t *src = (lane < 8 ? p.s : p.z) + i_s + (long long)grp * p.n + (lane & 3) * 8;
-                cp_async16(st + MOE_W_BYTES + lane * 16, src, true);
+            for (int r = 0; r < 4; ++r) {
+                // 16-byte piece q of the stage: column q % COLS of half (q / COLS) % 2 of block
+                // q / (2 COLS); the columns of a half 1 are stored with bit 2 flipped, so that the
+                // fragment reads below fall on different banks.
+                const int q = r * 32 + lane, c = q % COLS, h = (q / COLS) & 1, blk = q / (2 * COLS);
+                cp_async16(st + ((q - c + (c ^ (h << 2))) << 4), w + blk * 1024 + h * 512 + c * 4, true);
             }
-            is += p.team;
-            if (is >= p.steps) {
-                is = member;
+            if (sz_mine) {
+                const int n = ib + sz_block;
+                const int grp = p.group_magic ? (int)__umulhi((uint32_t)n, p.group_magic) : n;
+                cp_async16(st + 2048 + lane * 16, i_s + (long long)grp * p.n, true);
+            }
+            ib += G::BLOCKS;
+            if (!(ib & 1))
+                ib += 2 * (p.team - 1);
+            if (ib >= p.kblocks) {
+                ib = 2 * member;
                 iu += stride;
                 enter();
             }
@@ -420,103 +453,154 @@ __global__ void __launch_bounds__(MOE_THREADS, NT <= 2 ? 2 : 1) moe_layer_gemm_k
     for (int u = u0; u < units; u += stride) {
         const Unit un = find_unit<NT, DOWN>(p, u, n_active);
         const int rows = DOWN ? 2 * un.cols : un.cols; // columns in use on the token side
-        const int nts = (rows + 7) >> 3;
-        // This lane's activation row of each 8-column tile (a column past the last repeats it).
-        const uint16_t *arow[NT];
+        float out[MT][NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int c = min(n * 8 + g, rows - 1);
-            const int row = DOWN ? 2 * un.first + c : p.tab.sorted[un.first + c] / p.top;
-            arow[n] = p.act + (long long)row * p.k + t * 8;
-        }
-        float out[2][NT][4];
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     out[m][n][i] = 0.f;
 
-        for (int step = member; step < p.steps; step += p.team) {
-            cp_async_wait<STAGES - 2>();
-            __syncwarp(); // every lane's copies have landed, and the stage before is free again
-            issue(stage == 0 ? STAGES - 1 : stage - 1);
-            const uint8_t *st = ring_p + stage * MOE_STAGE;
+        // The member's steps for ND token tiles.
+        auto sweep = [&](auto nd) {
+            constexpr int ND = decltype(nd)::value;
+            // This lane's activation row of each tile (a column past the last repeats it).
+            const uint16_t *arow[ND];
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                uint2 w[2][2]; // [column tile][column g, g + 8]: words 2 (t >> 1), + 1 of half t & 1
+            for (int n = 0; n < ND; ++n) {
+                const int c = min(n * 8 + g, rows - 1);
+                const int row = DOWN ? 2 * un.first + c : p.tab.sorted[un.first + c] / p.top;
+                arow[n] = p.act + (long long)row * p.k + t * 8;
+            }
+            for (int step = member; step < p.steps; step += p.team) {
+                float lo[MT][ND][4], hi[DUAL ? MT : 1][ND][4], sa[ND][4];
+                const uint8_t *st = nullptr;
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
+                for (int b = 0; b < 2; ++b) {
+                    uint4 bv[ND][2];
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const int col = (m * 16 + c * 8 + g) ^ ((t & 1) << 2);
-                        w[m][c] = *reinterpret_cast<const uint2 *>(st + b * 1024 + (t & 1) * 512 + col * 16 + (t >> 1) * 8);
+                    for (int n = 0; n < ND; ++n) {
+                        const uint4 *ap = reinterpret_cast<const uint4 *>(arow[n] + (long long)(2 * step + b) * 64);
+                        bv[n][0] = ap[0];
+                        bv[n][1] = ap[4];
                     }
-                float sc[2][2], zp[2][2];
-#pragma unroll
-                for (int m = 0; m < 2; ++m)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const int col = m * 16 + c * 8 + g;
-                        sc[m][c] = to_float<BF>(*reinterpret_cast<const uint16_t *>(st + MOE_W_BYTES + b * MOE_SZ_BYTES + col * 2));
-                        zp[m][c] = (p.z ? to_float<BF>(*reinterpret_cast<const uint16_t *>(
-                                              st + MOE_W_BYTES + (2 + b) * MOE_SZ_BYTES + col * 2))
-                                        : 8.f) + (BF ? 128.f : 0.f);
+                    if (b % G::BLOCKS == 0) {
+                        if (st)
+                            stage = stage + 1 == STAGES ? 0 : stage + 1;
+                        cp_async_wait<STAGES - 2>();
+                        __syncwarp(); // every lane's copies have landed, and the stage before is free
+                        issue(stage == 0 ? STAGES - 1 : stage - 1);
+                        st = ring_p + stage * G::STAGE;
                     }
+                    const uint8_t *wst = st + (b % G::BLOCKS) * (2 * COLS * 16);
+                    uint2 w[MT][2]; // column g, g + 8 of each tile: words 2 (t >> 1), + 1 of half t & 1
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    if (n > 0 && n >= nts)
-                        break;
-                    const uint4 *ap = reinterpret_cast<const uint4 *>(arow[n] + (long long)(2 * step + b) * 64);
-                    const uint4 v0 = ap[0], v1 = ap[4];
-                    const uint32_t bf[2][4] = {{v0.x, v0.y, v0.z, v0.w}, {v1.x, v1.y, v1.z, v1.w}};
-                    float lo[2][4], hi[2][4], sa[4];
+                    for (int m = 0; m < MT; ++m)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        sa[i] = 0.f;
-                        lo[0][i] = lo[1][i] = hi[0][i] = hi[1][i] = 0.f;
-                    }
+                        for (int c = 0; c < 2; ++c) {
+                            const int col = (m * 16 + c * 8 + g) ^ ((t & 1) << 2);
+                            w[m][c] = *reinterpret_cast<const uint2 *>(wst + (t & 1) * (COLS * 16) + col * 16 + (t >> 1) * 8);
+                        }
                     constexpr uint32_t ONES = BF ? 0x3F803F80u : 0x3C003C00u;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        mma16816<BF>(sa, ONES, ONES, ONES, ONES, bf[i][0], bf[i][2]);
-                        mma16816<BF>(sa, ONES, ONES, ONES, ONES, bf[i][1], bf[i][3]);
 #pragma unroll
-                        for (int m = 0; m < 2; ++m) {
+                        for (int n = 0; n < ND; ++n) {
+                            const uint4 v = bv[n][i];
+                            if (b == 0 && i == 0)
+                                mma16816_zero<BF>(sa[n], ONES, ONES, ONES, ONES, v.x, v.z);
+                            else
+                                mma16816<BF>(sa[n], ONES, ONES, ONES, ONES, v.x, v.z);
+                            mma16816<BF>(sa[n], ONES, ONES, ONES, ONES, v.y, v.w);
+                        }
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
                             const uint32_t x = i ? w[m][0].y : w[m][0].x, y = i ? w[m][1].y : w[m][1].x;
-                            if (BF) {
-                                constexpr uint32_t M = 0x000F000Fu, O = 0x43004300u;
-                                mma16816<BF>(lo[m], (x & M) | O, (y & M) | O, ((x >> 8) & M) | O,
-                                             ((y >> 8) & M) | O, bf[i][0], bf[i][2]);
-                                mma16816<BF>(hi[m], ((x >> 4) & M) | O, ((y >> 4) & M) | O,
-                                             ((x >> 12) & M) | O, ((y >> 12) & M) | O, bf[i][1], bf[i][3]);
+                            constexpr uint32_t L = 0x000F000Fu, H = 0x00F000F0u, O = BF ? 0x43004300u : 0u;
+                            const uint32_t x8 = x >> 8, y8 = y >> 8;
+                            const uint32_t a0 = (x & L) | O, a1 = (y & L) | O, a2 = (x8 & L) | O, a3 = (y8 & L) | O;
+                            uint32_t c0, c1, c2, c3;
+                            if (DUAL) {
+                                c0 = x & H;
+                                c1 = y & H;
+                                c2 = x8 & H;
+                                c3 = y8 & H;
                             } else {
-                                constexpr uint32_t L = 0x000F000Fu, H = 0x00F000F0u;
-                                const uint32_t x8 = x >> 8, y8 = y >> 8;
-                                mma16816<BF>(lo[m], x & L, y & L, x8 & L, y8 & L, bf[i][0], bf[i][2]);
-                                mma16816<BF>(hi[m], x & H, y & H, x8 & H, y8 & H, bf[i][1], bf[i][3]);
+                                c0 = ((x >> 4) & L) | O;
+                                c1 = ((y >> 4) & L) | O;
+                                c2 = ((x >> 12) & L) | O;
+                                c3 = ((y >> 12) & L) | O;
+                            }
+#pragma unroll
+                            for (int n = 0; n < ND; ++n) {
+                                const uint4 v = bv[n][i];
+                                float(&h4)[4] = DUAL ? hi[m % (DUAL ? MT : 1)][n] : lo[m][n];
+                                if (b == 0 && i == 0)
+                                    mma16816_zero<BF>(lo[m][n], a0, a1, a2, a3, v.x, v.z);
+                                else
+                                    mma16816<BF>(lo[m][n], a0, a1, a2, a3, v.x, v.z);
+                                if (DUAL && b == 0 && i == 0)
+                                    mma16816_zero<BF>(h4, c0, c1, c2, c3, v.y, v.w);
+                                else
+                                    mma16816<BF>(h4, c0, c1, c2, c3, v.y, v.w);
                             }
                         }
                     }
+                    // End of a group (or of a step, whose two blocks then share one): scale the sums.
+                    if (b == 1 || p.per_block) {
+                        const uint8_t *sz = st + 2048 + (b % G::BLOCKS) * G::SZ;
 #pragma unroll
-                    for (int m = 0; m < 2; ++m)
+                        for (int m = 0; m < MT; ++m)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int c = i >> 1; // accumulator rows: column g, then g + 8
-                            const float za = zp[m][c] * sa[i & 1];
-                            const float q = BF ? (lo[m][i] + hi[m][i]) - za
-                                               : fmaf(fmaf(hi[m][i], 0.0625f, lo[m][i]), 16777216.f, -za);
-                            out[m][n][i] = fmaf(sc[m][c], q, out[m][n][i]);
+                            for (int c = 0; c < 2; ++c) {
+                                const int col = m * 16 + c * 8 + g;
+                                const float sc = to_float<BF>(*reinterpret_cast<const uint16_t *>(sz + col * 2)) *
+                                                 (BF ? 1.f : 16777216.f);
+                                float z = p.z ? to_float<BF>(*reinterpret_cast<const uint16_t *>(sz + G::BLOCKS * G::SZ + col * 2)) : 8.f;
+                                z = BF ? z + 128.f : z * 5.9604644775390625e-8f; // 2^-24
+#pragma unroll
+                                for (int n = 0; n < ND; ++n)
+#pragma unroll
+                                    for (int e = 0; e < 2; ++e) {
+                                        const int i = 2 * c + e;
+                                        float q = lo[m][n][i];
+                                        if (DUAL)
+                                            q = fmaf(hi[m % (DUAL ? MT : 1)][n][i], 0.0625f, q);
+                                        q = fmaf(-z, sa[n][e], q);
+                                        out[m][n][i] = fmaf(sc, q, out[m][n][i]);
+                                        if (b == 0) {
+                                            lo[m][n][i] = 0.f;
+                                            if (DUAL)
+                                                hi[m % (DUAL ? MT : 1)][n][i] = 0.f;
+                                        }
+                                    }
+                            }
+                        if (b == 0) {
+#pragma unroll
+                            for (int n = 0; n < ND; ++n)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    sa[n][i] = 0.f;
                         }
+                    }
                 }
+                stage = stage + 1 == STAGES ? 0 : stage + 1;
             }
-            stage = stage + 1 == STAGES ? 0 : stage + 1;
-        }
+        };
+        const int nts = (rows + 7) >> 3;
+        if (NT == 1 || nts == 1)
+            sweep(std::integral_constant<int, 1>());
+        else if (NT == 2 || nts == 2)
+            sweep(std::integral_constant<int, NT < 2 ? 1 : 2>());
+        else if (nts == 3)
+            sweep(std::integral_constant<int, NT < 3 ? 1 : 3>());
+        else
+            sweep(std::integral_constant<int, NT>());
 
         // --- the team's warps join their sums (fixed order) -----------------------------------
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 if (DOWN) { // columns 2 t and 2 t + 1 are a pair's value and remainder
@@ -538,15 +622,17 @@ __global__ void __launch_bounds__(MOE_THREADS, NT <= 2 ? 2 : 1) moe_layer_gemm_k
             return s;
         };
         if (!DOWN) {
-            // (tile n, register i, lane): gate column g + 8 (i >> 1) of the first 16, up of the last.
-            for (int x = team_tid; x < NT * 4 * 32; x += team_threads) {
-                const int ln = x & 31, v = x >> 5, n = v >> 2, i = v & 3;
+            // (column tile pair f, token tile n, register i, lane): gate column g + 8 (i >> 1) of tile
+            // 2 f, up of tile 2 f + 1.
+            for (int x = team_tid; x < MT / 2 * NT * 4 * 32; x += team_threads) {
+                const int ln = x & 31, v = x >> 5, i = v & 3, n = (v >> 2) % NT, fm = (v >> 2) / NT;
                 const int pr = n * 8 + 2 * (ln & 3) + (i & 1);
                 if (pr >= un.cols)
                     continue;
-                const float gate = joined(v, ln), up = joined(NT * 4 + v, ln);
+                const float gate = joined((2 * fm * NT + n) * 4 + i, ln);
+                const float up = joined(((2 * fm + 1) * NT + n) * 4 + i, ln);
                 const float hv = gate_act(gate, p.glu) * up;
-                const int f = un.col * 16 + (ln >> 2) + 8 * (i >> 1);
+                const int f = un.col * (COLS / 2) + fm * 16 + (ln >> 2) + 8 * (i >> 1);
                 // fp16: the value part stops at the largest finite value and the remainder goes on
                 // from there (a NaN stays one).
                 const float hc = !BF && fabsf(hv) > 65504.f ? copysignf(65504.f, hv) : hv;
@@ -556,13 +642,13 @@ __global__ void __launch_bounds__(MOE_THREADS, NT <= 2 ? 2 : 1) moe_layer_gemm_k
                 dst[p.inter] = from_float<BF>(hv - to_float<BF>(hb));
             }
         } else {
-            for (int x = team_tid; x < 2 * NT * 2 * 32; x += team_threads) {
+            for (int x = team_tid; x < MT * NT * 2 * 32; x += team_threads) {
                 const int ln = x & 31, v = x >> 5, c = v & 1, n = (v >> 1) % NT, m = (v >> 1) / NT;
                 const int pr = n * 4 + (ln & 3);
                 if (pr >= un.cols)
                     continue;
                 const int pair = p.tab.sorted[un.first + pr];
-                __stcg(p.part + (long long)pair * p.n + un.col * MOE_COLS + m * 16 + c * 8 + (ln >> 2), joined(v, ln));
+                __stcg(p.part + (long long)pair * p.n + un.col * COLS + m * 16 + c * 8 + (ln >> 2), joined(v, ln));
             }
         }
         team_sync(team, team_threads); // `red` is free; the team's stores are done
@@ -576,8 +662,8 @@ __global__ void __launch_bounds__(MOE_THREADS, NT <= 2 ? 2 : 1) moe_layer_gemm_k
             }
             team_sync(team, team_threads);
             if (last_sh[team]) {
-                for (int x = team_tid; x < p.tokens * (MOE_COLS / 4); x += team_threads) {
-                    const int tok = x / (MOE_COLS / 4), col = un.col * MOE_COLS + (x % (MOE_COLS / 4)) * 4;
+                for (int x = team_tid; x < p.tokens * (COLS / 4); x += team_threads) {
+                    const int tok = x / (COLS / 4), col = un.col * COLS + (x % (COLS / 4)) * 4;
                     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
                     for (int j = 0; j < p.top; ++j) {
                         const int pair = tok * p.top + j;
@@ -660,9 +746,14 @@ int check_layer_sizes(int tokens, int hidden, int inter, int experts, int top)
 using GemmKernel = void (*)(MoeGemm);
 struct MoeFamily;
 
-constexpr int moe_smem(int nt, bool down)
+int unit_cols(int nt)
 {
-    return MOE_WARPS * ((nt <= 2 ? 4 : 6) * MOE_STAGE + (down ? 2 * nt * 2 : 2 * nt * 4) * 32 * 4);
+    return nt == 1 ? MoeGeom<1>::COLS : nt == 2 ? MoeGeom<2>::COLS : MoeGeom<4>::COLS;
+}
+
+int unit_smem(int nt, bool down)
+{
+    return nt == 1 ? MoeGeom<1>::smem(down) : nt == 2 ? MoeGeom<2>::smem(down) : MoeGeom<4>::smem(down);
 }
 
 template <int NT>
@@ -692,13 +783,14 @@ int team_warps(int steps)
 cudaError_t launch_moe_gemm(MoeGemm &p, int nt, bool bf, bool down, int num_sms, cudaStream_t stream)
 {
     const GemmKernel kernel = nt == 1 ? gemm_kernel<1>(bf, down) : nt == 2 ? gemm_kernel<2>(bf, down) : gemm_kernel<4>(bf, down);
-    const int smem = moe_smem(nt, down);
+    const int smem = unit_smem(nt, down);
     const int v = (nt == 1 ? 0 : nt == 2 ? 1 : 2) * 4 + (bf ? 2 : 0) + (down ? 1 : 0);
     cudaError_t err = allow_smem<MoeFamily, 12>(reinterpret_cast<const void *>(kernel), v, smem);
     if (err != cudaSuccess)
         return err;
     p.team = team_warps(p.steps);
-    return launch_pdl(kernel, dim3(num_sms * (nt <= 2 ? 2 : 1)), dim3(MOE_THREADS), (size_t)smem, stream, p);
+    p.col_units = p.n / unit_cols(nt);
+    return launch_pdl(kernel, dim3(num_sms * 2), dim3(MOE_THREADS), (size_t)smem, stream, p);
 }
 
 } // namespace
@@ -776,8 +868,8 @@ extern "C" int w4a16_moe_layer(const void *x, int ldx, const void *router, const
     r.experts = n_experts;
     r.top = top_k;
     r.renorm = (flags & W4A16_FLAG_MOE_RENORM) ? 1 : 0;
-    r.up_cols = 2 * inter / MOE_COLS;
-    r.down_cols = hidden / MOE_COLS;
+    r.up_cols = 2 * inter / unit_cols(nt_up);
+    r.down_cols = hidden / unit_cols(nt_down);
     r.up_pass = 8 * nt_up;
     r.down_pass = 4 * nt_down;
     const dim3 grid((n_experts + MOE_WARPS - 1) / MOE_WARPS, chunks);
@@ -810,9 +902,11 @@ extern "C" int w4a16_moe_layer(const void *x, int ldx, const void *router, const
         m.expert_words = (long long)m.k * m.n / 8;
         m.steps = m.k / MOE_ROWS;
         m.kblocks = m.k / 64;
-        m.group_blocks = group_size == -1 ? m.kblocks : group_size / 64;
-        m.expert_groups = m.kblocks / m.group_blocks;
-        m.col_units = m.n / MOE_COLS;
+        // n / blocks = umulhi(n, 2^32 / blocks + 1) while n blocks < 2^32 (both are below 2^15).
+        const int blocks = group_size == -1 ? m.kblocks : group_size / 64;
+        m.group_magic = blocks == 1 ? 0u : (uint32_t)((1ull << 32) / blocks + 1);
+        m.per_block = blocks % 2;
+        m.expert_groups = m.kblocks / blocks;
     };
     sizes();
     err = launch_moe_gemm(m, nt_up, bf, false, num_sms, stream);
