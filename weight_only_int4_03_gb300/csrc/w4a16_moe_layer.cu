@@ -43,14 +43,17 @@ constexpr int MOE_THREADS = MOE_WARPS * 32;
 constexpr int MOE_CHUNK = 4;   // tokens per routing block
 constexpr int MOE_COLS = 32;   // fewest weight columns per unit
 constexpr int MOE_ROWS = 128;  // weight rows per step (two 64-row blocks)
+constexpr float CODE_UNIT = 5.9604644775390625e-8f; // 2^-24: the fp16 value of the bits 1
 
 // Element of a 64-row block in the order the MMA's lanes read it: lane t of a quad takes, for
 // i = 0, 1, the eight values of 16-byte chunk 4 i + t, which are rows 32 (t & 1) + 8 p +
-// 4 (t >> 1) + 2 i + {0, 1}, p = 0 .. 3 -- the rows of word 2 (t >> 1) + i of half t & 1.
+// 4 (t >> 1) + 2 i + {0, 1}, p = 0, 2, 1, 3 -- the rows of word 2 (t >> 1) + i of half t & 1, those of
+// one nibble position (p even, p odd) side by side as the MMA wants its register pairs.
 __host__ __device__ __forceinline__ int frag_index(int row)
 {
     const int h = (row >> 5) & 1, p = (row >> 3) & 3, j = (row >> 1) & 3, e = row & 1;
-    return ((j & 1) * 4 + h + 2 * (j >> 1)) * 8 + 2 * p + e;
+    const int q = ((p & 1) << 1) | (p >> 1);
+    return ((j & 1) * 4 + h + 2 * (j >> 1)) * 8 + 2 * q + e;
 }
 
 // Routing tables in the workspace.
@@ -61,6 +64,7 @@ struct MoeTables {
     int *pre_up;     // [MOE_MAX_EXPERTS + 1] units before each active expert
     int *pre_down;
     int *sorted;     // [pairs] pair ids t * top_k + j by expert, in increasing order within one
+    int *token;      // [pairs] their tokens t
     int *ids;        // [pairs]
     float *weights;  // [pairs]
 };
@@ -82,42 +86,45 @@ template <bool BF>
 __global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const RouteParams p)
 {
     __shared__ int is_last;
+    __shared__ float partial[MOE_WARPS][MOE_CHUNK];
     __shared__ int ids[MOE_MAX_PAIRS];
     __shared__ int count[MOE_MAX_EXPERTS], off_of[MOE_MAX_EXPERTS];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_wait();
     pdl_launch_dependents();
     const int t0 = blockIdx.y * MOE_CHUNK, nt = min(MOE_CHUNK, p.tokens - t0);
-    const int e = blockIdx.x * MOE_WARPS + warp;
-
-    if (blockIdx.x == 0) {
-        // The tokens' rows in fragment order.
+    const int e = blockIdx.x;
+    {
+        // This block's share of the tokens' rows in fragment order.
         const int chunks = p.hidden / 8;
-        for (int i = tid; i < nt * chunks; i += MOE_THREADS) {
+        for (int i = blockIdx.x * MOE_THREADS + tid; i < nt * chunks; i += gridDim.x * MOE_THREADS) {
             const int tt = i / chunks, c = i - tt * chunks;
             const int q = c & 7, t = q & 3, w = q >> 2;
             const uint16_t *src = p.x + (long long)(t0 + tt) * p.ldx + (c >> 3) * 64 + 32 * (t & 1) + 4 * (t >> 1) + 2 * w;
             uint4 v;
             v.x = *reinterpret_cast<const uint32_t *>(src);
-            v.y = *reinterpret_cast<const uint32_t *>(src + 8);
-            v.z = *reinterpret_cast<const uint32_t *>(src + 16);
+            v.y = *reinterpret_cast<const uint32_t *>(src + 16);
+            v.z = *reinterpret_cast<const uint32_t *>(src + 8);
             v.w = *reinterpret_cast<const uint32_t *>(src + 24);
             *reinterpret_cast<uint4 *>(p.xf + (long long)(t0 + tt) * p.hidden + c * 8) = v;
         }
     }
-    if (e < p.experts) {
+    {
+        // The score of expert e for the chunk's tokens: the block's threads share the row.
         float acc[MOE_CHUNK] = {0.f, 0.f, 0.f, 0.f};
         const uint16_t *r = p.router + (long long)e * p.hidden;
-#pragma unroll 4
-        for (int k = lane * 8; k < p.hidden; k += 256) {
+#pragma unroll 2
+        for (int k = tid * 8; k < p.hidden; k += MOE_THREADS * 8) {
             const uint4 wv = *reinterpret_cast<const uint4 *>(r + k);
             const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
+            uint4 xv[MOE_CHUNK];
+#pragma unroll
+            for (int tt = 0; tt < MOE_CHUNK; ++tt)
+                xv[tt] = tt < nt ? *reinterpret_cast<const uint4 *>(p.x + (long long)(t0 + tt) * p.ldx + k)
+                                 : make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int tt = 0; tt < MOE_CHUNK; ++tt) {
-                if (tt >= nt)
-                    break;
-                const uint4 xv = *reinterpret_cast<const uint4 *>(p.x + (long long)(t0 + tt) * p.ldx + k);
-                const uint32_t xx[4] = {xv.x, xv.y, xv.z, xv.w};
+                const uint32_t xx[4] = {xv[tt].x, xv[tt].y, xv[tt].z, xv[tt].w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float2 a = unpack2<BF>(ww[i]), b = unpack2<BF>(xx[i]);
@@ -132,8 +139,16 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const Rout
 #pragma unroll
             for (int d = 16; d; d >>= 1)
                 v += __shfl_xor_sync(0xffffffffu, v, d);
-            if (lane == 0 && tt < nt)
-                __stcg(p.logits + (long long)(t0 + tt) * p.experts + e, v);
+            if (lane == 0)
+                partial[warp][tt] = v;
+        }
+        __syncthreads();
+        if (tid < nt) {
+            float v = 0.f;
+#pragma unroll
+            for (int w = 0; w < MOE_WARPS; ++w)
+                v += partial[w][tid];
+            __stcg(p.logits + (long long)(t0 + tid) * p.experts + e, v);
         }
     }
     __syncthreads();
@@ -280,8 +295,10 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const Rout
             continue;
         int at = off_of[x];
         for (int i = 0; i < pairs; ++i)
-            if (ids[i] == x)
-                p.tab.sorted[at++] = i;
+            if (ids[i] == x) {
+                p.tab.sorted[at] = i;
+                p.tab.token[at++] = i / p.top;
+            }
     }
 }
 
@@ -290,7 +307,7 @@ struct MoeGemm {
     const uint16_t *s, *z;   // [E][G][N]; z null: 8
     const uint16_t *act;     // activation rows in fragment order, K values each
     uint16_t *h;             // gate-up: the pairs' h, two rows (value, remainder) per pair
-    float *part;             // down: [pairs][N] fp32
+    float *part;             // down: [pairs][splits][N] fp32
     const uint16_t *residual;
     uint16_t *y;
     int *counters;           // down: one per 32 columns
@@ -301,7 +318,9 @@ struct MoeGemm {
     int kblocks;             // 64-row blocks of K
     uint32_t group_magic;    // group of block n: umulhi(n, group_magic), or n when 0
     int per_block;           // groups of an odd number of blocks: scale every block's sums
-    int col_units;           // units per expert and pass
+    int col_units;           // units per expert, pass and split (at least 2)
+    uint32_t col_magic;      // n / col_units = umulhi(n, col_magic)
+    int splits;              // down: parts of K with units and partial outputs of their own
     int team;                // warps per team
     int tokens, top, inter, ldy, ldr, glu;
 };
@@ -324,44 +343,51 @@ __device__ __forceinline__ void team_sync(int team_id, int threads)
         asm volatile("bar.sync %0, %1;" ::"r"(team_id + 1), "r"(threads) : "memory");
 }
 
-// One unit of a team: an expert, a pass over its pairs and a range of columns.
+// One unit of a team: an expert, a pass over its pairs, a range of columns and of 128-row steps.
 struct Unit {
     int expert, col, first, cols; // first pair (in `sorted`), pairs of this pass
+    int split, step0, step1;
 };
 
+// Unit u; `at` is the caller's place among the active experts, which only moves forward with u.
 template <int NT, bool DOWN>
-__device__ __forceinline__ Unit find_unit(const MoeGemm &p, int u, int n_active)
+__device__ __forceinline__ Unit find_unit(const MoeGemm &p, int u, int &at)
 {
-    int lo = 0, hi = n_active - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.pre[mid] <= u)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
+    int next = p.pre[at + 1];
+    while (next <= u)
+        next = p.pre[++at + 1];
     constexpr int PASS = DOWN ? 4 * NT : 8 * NT; // a pair takes two columns of the down MMA
-    const int local = u - p.pre[lo], pass = local / p.col_units;
+    const int local = u - p.pre[at], part = (int)__umulhi((uint32_t)local, p.col_magic);
     Unit r;
-    r.expert = p.tab.ex_id[lo];
-    r.col = local - pass * p.col_units;
-    const int off = p.tab.ex_off[lo], end = p.tab.ex_off[lo + 1];
+    r.expert = p.tab.ex_id[at];
+    r.col = local - part * p.col_units;
+    int pass = part;
+    r.split = 0;
+    r.step0 = 0;
+    r.step1 = p.steps;
+    if (DOWN && p.splits > 1) {
+        pass = part / p.splits;
+        r.split = part - pass * p.splits;
+        r.step0 = r.split * p.steps / p.splits;
+        r.step1 = (r.split + 1) * p.steps / p.splits;
+    }
+    const int off = p.tab.ex_off[at], end = p.tab.ex_off[at + 1];
     r.first = off + pass * PASS;
     r.cols = min(PASS, end - r.first);
     return r;
 }
 
 // Sizes of a kernel variant.  NT: 8-column tiles of the MMA's token side; MT: 16-column tiles of
-// weights, as many as the registers of 16 warps per SM hold beside NT tiles of sums (each activation
-// fragment then serves MT products).
+// weights (each activation fragment serves MT products).
 template <int NT>
 struct MoeGeom {
-    static constexpr int MT = NT <= 2 ? 4 : 2;
+    static constexpr int MT = 4;
+    static constexpr int CTAS = NT <= 2 ? 2 : 1; // blocks per SM
     static constexpr int COLS = 16 * MT;
     static constexpr int BLOCKS = 4 / MT; // 64-row blocks per stage: 2 KiB of codes
     static constexpr int SZ = COLS * 2;   // bytes of one scale (or zero) row
     static constexpr int STAGE = 2048 + 2 * BLOCKS * SZ;
-    static constexpr int STAGES = 4;
+    static constexpr int STAGES = NT <= 2 ? 4 : 8;
     static constexpr int RING = STAGES * STAGE;
     static constexpr int vals(bool down) { return MT * NT * (down ? 2 : 4); } // sums per lane to join
     static constexpr int smem(bool down) { return MOE_WARPS * (RING + vals(down) * 32 * 4); }
@@ -369,7 +395,7 @@ struct MoeGeom {
 
 // DOWN false: gate-up, true: down.
 template <int NT, bool BF, bool DOWN>
-__global__ void __launch_bounds__(MOE_THREADS, 2) moe_layer_gemm_kernel(const MoeGemm p)
+__global__ void __launch_bounds__(MOE_THREADS, MoeGeom<NT>::CTAS) moe_layer_gemm_kernel(const MoeGemm p)
 {
     using G = MoeGeom<NT>;
     constexpr int MT = G::MT, COLS = G::COLS, STAGES = G::STAGES, VALS = G::vals(DOWN);
@@ -396,8 +422,8 @@ __global__ void __launch_bounds__(MOE_THREADS, 2) moe_layer_gemm_kernel(const Mo
 
     // --- the copying side: (unit, block) runs ahead of the computing side ----------------------
     // A member takes the 128-row steps member, member + team, ..., each as 2 / BLOCKS stages.
-    int iu = u0, ib = 2 * member;
-    const int32_t *i_w = nullptr;
+    int iu = u0, i_at = 0, ib = 0, ib_end = 0;
+    const int32_t *i_w = nullptr; // this lane's piece of block 0, half 0 of the unit's columns
     const uint16_t *i_s = nullptr; // this lane's part of the expert's scale (or zero) row 0
     // Lane l looks after chunk l % (SZ / 16) of a row; rows: scales of the stage's blocks, then zeros.
     constexpr int SZ_CHUNKS = G::SZ / 16;
@@ -405,40 +431,47 @@ __global__ void __launch_bounds__(MOE_THREADS, 2) moe_layer_gemm_kernel(const Mo
     const bool sz_zero = sz_row >= G::BLOCKS;
     const bool sz_mine = sz_row < G::BLOCKS * (p.z ? 2 : 1);
     const int sz_block = sz_zero ? sz_row - G::BLOCKS : sz_row;
-    auto enter = [&]() {
-        if (iu < units) {
-            const Unit un = find_unit<NT, DOWN>(p, iu, n_active);
+    auto enter = [&]() { // the next unit in which this member has a step
+        for (; iu < units; iu += stride) {
+            const Unit un = find_unit<NT, DOWN>(p, iu, i_at);
+            ib = 2 * (un.step0 + member);
+            ib_end = 2 * un.step1;
+            if (ib >= ib_end)
+                continue;
             const int n0 = un.col * COLS;
-            i_w = p.w + un.expert * p.expert_words + (long long)(n0 >> 7) * p.kblocks * 1024 + (n0 & 127) * 4;
+            i_w = p.w + un.expert * p.expert_words + (long long)(n0 >> 7) * p.kblocks * 1024 + (n0 & 127) * 4 + lane * 4;
             i_s = (sz_zero ? p.z : p.s) + un.expert * p.expert_groups * p.n + n0 + (lane % SZ_CHUNKS) * 8;
+            return;
         }
     };
-    if (member < p.steps)
-        enter();
-    else
-        iu = units; // a member without a step copies nothing
+    enter();
+    // The columns of a half 1 are stored with bit 2 flipped, so that the fragment reads below fall on
+    // different banks.
+    const uint32_t dst0 = ring + lane * 16, dst1 = ring + (lane ^ 4) * 16;
     auto issue = [&](int stage) {
         if (iu < units) {
-            const uint32_t st = ring + stage * G::STAGE;
             const int32_t *w = i_w + (long long)ib * 1024;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                // 16-byte piece q of the stage: column q % COLS of half (q / COLS) % 2 of block
-                // q / (2 COLS); the columns of a half 1 are stored with bit 2 flipped, so that the
-                // fragment reads below fall on different banks.
-                const int q = r * 32 + lane, c = q % COLS, h = (q / COLS) & 1, blk = q / (2 * COLS);
-                cp_async16(st + ((q - c + (c ^ (h << 2))) << 4), w + blk * 1024 + h * 512 + c * 4, true);
+            const uint32_t d0 = dst0 + stage * G::STAGE, d1 = dst1 + stage * G::STAGE;
+            if (MT == 4) { // one block: 64 columns of half 0, then of half 1
+                cp_async16_at<0, 0>(d0, w);
+                cp_async16_at<512, 512>(d0, w);
+                cp_async16_at<1024, 2048>(d1, w);
+                cp_async16_at<1536, 2560>(d1, w);
+            } else { // two blocks of 32 columns
+                cp_async16_at<0, 0>(d0, w);
+                cp_async16_at<512, 2048>(d1, w);
+                cp_async16_at<1024, 4096>(d0, w);
+                cp_async16_at<1536, 6144>(d1, w);
             }
             if (sz_mine) {
                 const int n = ib + sz_block;
                 const int grp = p.group_magic ? (int)__umulhi((uint32_t)n, p.group_magic) : n;
-                cp_async16(st + 2048 + lane * 16, i_s + (long long)grp * p.n, true);
+                cp_async16_at<2048, 0>(d0, i_s + (long long)grp * p.n);
             }
             ib += G::BLOCKS;
             if (!(ib & 1))
                 ib += 2 * (p.team - 1);
-            if (ib >= p.kblocks) {
-                ib = 2 * member;
+            if (ib >= ib_end) {
                 iu += stride;
                 enter();
             }
@@ -449,9 +482,11 @@ __global__ void __launch_bounds__(MOE_THREADS, 2) moe_layer_gemm_kernel(const Mo
     for (int s = 0; s < STAGES - 1; ++s)
         issue(s);
 
-    int stage = 0;
+    // Half t & 1, column g (bit 2 flipped in half 1), words 2 (t >> 1) and the next.
+    const int w_lane = (t & 1) * (COLS * 16) + (g ^ ((t & 1) << 2)) * 16 + (t >> 1) * 8;
+    int stage = 0, at = 0;
     for (int u = u0; u < units; u += stride) {
-        const Unit un = find_unit<NT, DOWN>(p, u, n_active);
+        const Unit un = find_unit<NT, DOWN>(p, u, at);
         const int rows = DOWN ? 2 * un.cols : un.cols; // columns in use on the token side
         float out[MT][NT][4];
 #pragma unroll
@@ -470,10 +505,10 @@ __global__ void __launch_bounds__(MOE_THREADS, 2) moe_layer_gemm_kernel(const Mo
 #pragma unroll
             for (int n = 0; n < ND; ++n) {
                 const int c = min(n * 8 + g, rows - 1);
-                const int row = DOWN ? 2 * un.first + c : p.tab.sorted[un.first + c] / p.top;
-                arow[n] = p.act + (long long)row * p.k + t * 8;
+                const int row = DOWN ? 2 * un.first + c : p.tab.token[un.first + c];
+                arow[n] = p.act + (long long)row * p.k + (un.step0 + member) * MOE_ROWS + t * 8;
             }
-            for (int step = member; step < p.steps; step += p.team) {
+            for (int step = un.step0 + member; step < un.step1; step += p.team) {
                 float lo[MT][ND][4], hi[DUAL ? MT : 1][ND][4], sa[ND][4];
                 const uint8_t *st = nullptr;
 #pragma unroll
@@ -481,9 +516,11 @@ __global__ void __launch_bounds__(MOE_THREADS, 2) moe_layer_gemm_kernel(const Mo
                     uint4 bv[ND][2];
 #pragma unroll
                     for (int n = 0; n < ND; ++n) {
-                        const uint4 *ap = reinterpret_cast<const uint4 *>(arow[n] + (long long)(2 * step + b) * 64);
+                        const uint4 *ap = reinterpret_cast<const uint4 *>(arow[n]) + b * 8;
                         bv[n][0] = ap[0];
                         bv[n][1] = ap[4];
+                        if (b == 1)
+                            arow[n] += p.team * MOE_ROWS;
                     }
                     if (b % G::BLOCKS == 0) {
                         if (st)
@@ -499,8 +536,7 @@ __global__ void __launch_bounds__(MOE_THREADS, 2) moe_layer_gemm_kernel(const Mo
                     for (int m = 0; m < MT; ++m)
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            const int col = (m * 16 + c * 8 + g) ^ ((t & 1) << 2);
-                            w[m][c] = *reinterpret_cast<const uint2 *>(wst + (t & 1) * (COLS * 16) + col * 16 + (t >> 1) * 8);
+                            w[m][c] = *reinterpret_cast<const uint2 *>(wst + w_lane + (m * 16 + c * 8) * 16);
                         }
                     constexpr uint32_t ONES = BF ? 0x3F803F80u : 0x3C003C00u;
 #pragma unroll
@@ -509,10 +545,10 @@ __global__ void __launch_bounds__(MOE_THREADS, 2) moe_layer_gemm_kernel(const Mo
                         for (int n = 0; n < ND; ++n) {
                             const uint4 v = bv[n][i];
                             if (b == 0 && i == 0)
-                                mma16816_zero<BF>(sa[n], ONES, ONES, ONES, ONES, v.x, v.z);
+                                mma16816_zero<BF>(sa[n], ONES, ONES, ONES, ONES, v.x, v.y);
                             else
-                                mma16816<BF>(sa[n], ONES, ONES, ONES, ONES, v.x, v.z);
-                            mma16816<BF>(sa[n], ONES, ONES, ONES, ONES, v.y, v.w);
+                                mma16816<BF>(sa[n], ONES, ONES, ONES, ONES, v.x, v.y);
+                            mma16816<BF>(sa[n], ONES, ONES, ONES, ONES, v.z, v.w);
                         }
 #pragma unroll
                         for (int m = 0; m < MT; ++m) {
@@ -537,28 +573,29 @@ __global__ void __launch_bounds__(MOE_THREADS, 2) moe_layer_gemm_kernel(const Mo
                                 const uint4 v = bv[n][i];
                                 float(&h4)[4] = DUAL ? hi[m % (DUAL ? MT : 1)][n] : lo[m][n];
                                 if (b == 0 && i == 0)
-                                    mma16816_zero<BF>(lo[m][n], a0, a1, a2, a3, v.x, v.z);
+                                    mma16816_zero<BF>(lo[m][n], a0, a1, a2, a3, v.x, v.y);
                                 else
-                                    mma16816<BF>(lo[m][n], a0, a1, a2, a3, v.x, v.z);
+                                    mma16816<BF>(lo[m][n], a0, a1, a2, a3, v.x, v.y);
                                 if (DUAL && b == 0 && i == 0)
-                                    mma16816_zero<BF>(h4, c0, c1, c2, c3, v.y, v.w);
+                                    mma16816_zero<BF>(h4, c0, c1, c2, c3, v.z, v.w);
                                 else
-                                    mma16816<BF>(h4, c0, c1, c2, c3, v.y, v.w);
+                                    mma16816<BF>(h4, c0, c1, c2, c3, v.z, v.w);
                             }
                         }
                     }
                     // End of a group (or of a step, whose two blocks then share one): scale the sums.
-                    if (b == 1 || p.per_block) {
-                        const uint8_t *sz = st + 2048 + (b % G::BLOCKS) * G::SZ;
+                    const uint8_t *sz = st + 2048 + (b % G::BLOCKS) * G::SZ;
+                    auto flush = [&](auto zeros, bool again) {
 #pragma unroll
                         for (int m = 0; m < MT; ++m)
 #pragma unroll
                             for (int c = 0; c < 2; ++c) {
                                 const int col = m * 16 + c * 8 + g;
-                                const float sc = to_float<BF>(*reinterpret_cast<const uint16_t *>(sz + col * 2)) *
-                                                 (BF ? 1.f : 16777216.f);
-                                float z = p.z ? to_float<BF>(*reinterpret_cast<const uint16_t *>(sz + G::BLOCKS * G::SZ + col * 2)) : 8.f;
-                                z = BF ? z + 128.f : z * 5.9604644775390625e-8f; // 2^-24
+                                const float sc = to_float<BF>(*reinterpret_cast<const uint16_t *>(sz + col * 2));
+                                float z = 8.f;
+                                if (decltype(zeros)::value)
+                                    z = to_float<BF>(*reinterpret_cast<const uint16_t *>(sz + G::BLOCKS * G::SZ + col * 2));
+                                z = BF ? z + 128.f : z * CODE_UNIT;
 #pragma unroll
                                 for (int n = 0; n < ND; ++n)
 #pragma unroll
@@ -569,20 +606,26 @@ __global__ void __launch_bounds__(MOE_THREADS, 2) moe_layer_gemm_kernel(const Mo
                                             q = fmaf(hi[m % (DUAL ? MT : 1)][n][i], 0.0625f, q);
                                         q = fmaf(-z, sa[n][e], q);
                                         out[m][n][i] = fmaf(sc, q, out[m][n][i]);
-                                        if (b == 0) {
+                                        if (again) {
                                             lo[m][n][i] = 0.f;
                                             if (DUAL)
                                                 hi[m % (DUAL ? MT : 1)][n][i] = 0.f;
                                         }
                                     }
                             }
-                        if (b == 0) {
+                        if (again) {
 #pragma unroll
                             for (int n = 0; n < ND; ++n)
 #pragma unroll
                                 for (int i = 0; i < 4; ++i)
                                     sa[n][i] = 0.f;
                         }
+                    };
+                    if (b == 1 || p.per_block) {
+                        if (p.z)
+                            flush(std::true_type(), b == 0);
+                        else
+                            flush(std::false_type(), b == 0);
                     }
                 }
                 stage = stage + 1 == STAGES ? 0 : stage + 1;
@@ -619,7 +662,7 @@ __global__ void __launch_bounds__(MOE_THREADS, 2) moe_layer_gemm_kernel(const Mo
             float s = 0.f;
             for (int w = 0; w < p.team; ++w)
                 s += tr[(w * VALS + v) * 32 + ln];
-            return s;
+            return BF ? s : s * (1.f / CODE_UNIT);
         };
         if (!DOWN) {
             // (column tile pair f, token tile n, register i, lane): gate column g + 8 (i >> 1) of tile
@@ -648,7 +691,7 @@ __global__ void __launch_bounds__(MOE_THREADS, 2) moe_layer_gemm_kernel(const Mo
                 if (pr >= un.cols)
                     continue;
                 const int pair = p.tab.sorted[un.first + pr];
-                __stcg(p.part + (long long)pair * p.n + un.col * COLS + m * 16 + c * 8 + (ln >> 2), joined(v, ln));
+                __stcg(p.part + ((long long)pair * p.splits + un.split) * p.n + un.col * COLS + m * 16 + c * 8 + (ln >> 2), joined(v, ln));
             }
         }
         team_sync(team, team_threads); // `red` is free; the team's stores are done
@@ -668,7 +711,15 @@ __global__ void __launch_bounds__(MOE_THREADS, 2) moe_layer_gemm_kernel(const Mo
                     for (int j = 0; j < p.top; ++j) {
                         const int pair = tok * p.top + j;
                         const float wt = p.tab.weights[pair];
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part + (long long)pair * p.n + col));
+                        const float4 *src = reinterpret_cast<const float4 *>(p.part + (long long)pair * p.splits * p.n + col);
+                        float4 v = __ldcg(src);
+                        for (int s = 1; s < p.splits; ++s) {
+                            const float4 o = __ldcg(src + (long long)s * (p.n / 4));
+                            v.x += o.x;
+                            v.y += o.y;
+                            v.z += o.z;
+                            v.w += o.w;
+                        }
                         a.x = fmaf(wt, v.x, a.x);
                         a.y = fmaf(wt, v.y, a.y);
                         a.z = fmaf(wt, v.z, a.z);
@@ -700,6 +751,12 @@ struct MoeLayout {
     MoeTables tab;
 };
 
+// Parts of K that the partial outputs have room for.
+int max_splits(int pairs)
+{
+    return pairs >= 128 ? 1 : pairs >= 64 ? 2 : pairs >= 32 ? 4 : 8;
+}
+
 MoeLayout moe_layout(char *ws, int tokens, int hidden, int inter, int experts, int top)
 {
     MoeLayout l;
@@ -719,12 +776,13 @@ MoeLayout moe_layout(char *ws, int tokens, int hidden, int inter, int experts, i
     l.tab.pre_up = reinterpret_cast<int *>(take(MOE_MAX_EXPERTS + 1));
     l.tab.pre_down = reinterpret_cast<int *>(take(MOE_MAX_EXPERTS + 1));
     l.tab.sorted = reinterpret_cast<int *>(take(pairs));
+    l.tab.token = reinterpret_cast<int *>(take(pairs));
     l.tab.ids = reinterpret_cast<int *>(take(pairs));
     l.tab.weights = reinterpret_cast<float *>(take(pairs));
     l.xf = round_up(at, 256);
     l.h = round_up(l.xf + 2LL * tokens * hidden, 256);
     l.part = round_up(l.h + 4LL * pairs * inter, 256);
-    l.total = round_up(l.part + 4LL * pairs * hidden, 256);
+    l.total = round_up(l.part + 4LL * pairs * max_splits(pairs) * hidden, 256);
     return l;
 }
 
@@ -771,16 +829,64 @@ int token_tiles(int columns)
     return columns <= 8 ? 1 : columns <= 16 ? 2 : 4;
 }
 
-// Warps per team: as many as have two steps each.
-int team_warps(int steps)
+// Warps per team and parts of K of a product whose `units` units (expert, pass, columns) have
+// `steps` steps each: the pair with the least time on the busiest warp, counting the end of a unit
+// (joining the team's sums, storing) as two steps.
+struct MoeSplit {
+    int team, splits;
+};
+
+MoeSplit pick_split(double units, int steps, int warps, int max_splits, bool sure)
 {
-    int team = MOE_WARPS;
-    while (team > 1 && steps < 2 * team)
-        team /= 2;
-    return team;
+    MoeSplit best = {MOE_WARPS, 1};
+    double least = -1;
+    for (int team = MOE_WARPS; team >= 1; team /= 2)
+        for (int splits = 1; splits <= max_splits && splits <= steps; ++splits) {
+            const int teams = warps / team;
+            // Rounds of the busiest team: exact, or half a round more than the average.
+            const double rounds = sure ? (double)(((long long)(units + 0.5) * splits + teams - 1) / teams)
+                                       : units * splits / teams + 0.5;
+            const int part = (steps + splits - 1) / splits;
+            const double cost = (rounds < 1 ? 1 : rounds) * ((part + team - 1) / team + 2);
+            if (least < 0 || cost < least) {
+                least = cost;
+                best = {team, splits};
+            }
+        }
+    return best;
 }
 
-cudaError_t launch_moe_gemm(MoeGemm &p, int nt, bool bf, bool down, int num_sms, cudaStream_t stream)
+// Experts that a call reads, were each token's choice uniform.
+double expected_experts(int tokens, int experts, int top)
+{
+    double miss = 1.0;
+    for (int t = 0; t < tokens; ++t)
+        miss *= 1.0 - (double)top / experts;
+    const double n = experts * (1.0 - miss);
+    return n < top ? top : n;
+}
+
+struct MoePlan {
+    int nt_up, nt_down;
+    MoeSplit up, down;
+};
+
+MoePlan moe_plan(int tokens, int hidden, int inter, int experts, int top, int num_sms)
+{
+    MoePlan p;
+    p.nt_up = token_tiles(tokens);
+    p.nt_down = token_tiles(2 * tokens);
+    const double active = expected_experts(tokens, experts, top);
+    const int warps = num_sms * 2 * MOE_WARPS;
+    const bool sure = tokens == 1; // the number of units is known
+    p.up = pick_split(active * (2 * inter / unit_cols(p.nt_up)), hidden / MOE_ROWS, warps / (p.nt_up > 2 ? 2 : 1), 1, sure);
+    p.down = pick_split(active * (hidden / unit_cols(p.nt_down)), inter / MOE_ROWS,
+                        warps / (p.nt_down > 2 ? 2 : 1), max_splits(tokens * top), sure);
+    return p;
+}
+
+cudaError_t launch_moe_gemm(MoeGemm &p, int nt, MoeSplit split, bool bf, bool down, int num_sms,
+                            cudaStream_t stream)
 {
     const GemmKernel kernel = nt == 1 ? gemm_kernel<1>(bf, down) : nt == 2 ? gemm_kernel<2>(bf, down) : gemm_kernel<4>(bf, down);
     const int smem = unit_smem(nt, down);
@@ -788,9 +894,13 @@ cudaError_t launch_moe_gemm(MoeGemm &p, int nt, bool bf, bool down, int num_sms,
     cudaError_t err = allow_smem<MoeFamily, 12>(reinterpret_cast<const void *>(kernel), v, smem);
     if (err != cudaSuccess)
         return err;
-    p.team = team_warps(p.steps);
+    p.team = split.team;
+    p.splits = split.splits;
     p.col_units = p.n / unit_cols(nt);
-    return launch_pdl(kernel, dim3(num_sms * 2), dim3(MOE_THREADS), (size_t)smem, stream, p);
+    // Exact while n col_units < 2^32: local unit numbers are below 64 passes x 8 splits x col_units
+    // and col_units is at most 2^16.
+    p.col_magic = (uint32_t)((1ull << 32) / p.col_units + 1);
+    return launch_pdl(kernel, dim3(num_sms * (nt <= 2 ? 2 : 1)), dim3(MOE_THREADS), (size_t)smem, stream, p);
 }
 
 } // namespace
@@ -851,7 +961,7 @@ extern "C" int w4a16_moe_layer(const void *x, int ldx, const void *router, const
 
     const bool bf = (flags & W4A16_FLAG_BF16) != 0;
     const int chunks = (n_tokens + MOE_CHUNK - 1) / MOE_CHUNK;
-    const int nt_up = token_tiles(n_tokens), nt_down = token_tiles(2 * n_tokens);
+    const MoePlan plan = moe_plan(n_tokens, hidden, inter, n_experts, top_k, num_sms);
     int *counters = reinterpret_cast<int *>(ws + lay.counters);
     RouteParams r;
     r.x = static_cast<const uint16_t *>(x);
@@ -868,11 +978,11 @@ extern "C" int w4a16_moe_layer(const void *x, int ldx, const void *router, const
     r.experts = n_experts;
     r.top = top_k;
     r.renorm = (flags & W4A16_FLAG_MOE_RENORM) ? 1 : 0;
-    r.up_cols = 2 * inter / unit_cols(nt_up);
-    r.down_cols = hidden / unit_cols(nt_down);
-    r.up_pass = 8 * nt_up;
-    r.down_pass = 4 * nt_down;
-    const dim3 grid((n_experts + MOE_WARPS - 1) / MOE_WARPS, chunks);
+    r.up_cols = 2 * inter / unit_cols(plan.nt_up);
+    r.down_cols = hidden / unit_cols(plan.nt_down) * plan.down.splits;
+    r.up_pass = 8 * plan.nt_up;
+    r.down_pass = 4 * plan.nt_down;
+    const dim3 grid(n_experts, chunks);
     err = bf ? launch_pdl(moe_layer_route_kernel<true>, grid, dim3(MOE_THREADS), 0, stream, r)
              : launch_pdl(moe_layer_route_kernel<false>, grid, dim3(MOE_THREADS), 0, stream, r);
     if (err != cudaSuccess)
@@ -909,7 +1019,7 @@ extern "C" int w4a16_moe_layer(const void *x, int ldx, const void *router, const
         m.expert_groups = m.kblocks / blocks;
     };
     sizes();
-    err = launch_moe_gemm(m, nt_up, bf, false, num_sms, stream);
+    err = launch_moe_gemm(m, plan.nt_up, plan.up, bf, false, num_sms, stream);
     if (err != cudaSuccess)
         return status_of(STAGE_LAUNCH, err);
     m.w = down;
@@ -920,5 +1030,5 @@ extern "C" int w4a16_moe_layer(const void *x, int ldx, const void *router, const
     m.k = inter;
     m.n = hidden;
     sizes();
-    return launch_status(launch_moe_gemm(m, nt_down, bf, true, num_sms, stream));
+    return launch_status(launch_moe_gemm(m, plan.nt_down, plan.down, bf, true, num_sms, stream));
 }

@@ -192,6 +192,14 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool l
                  : "memory");
 }
 
+// The same with constant byte offsets on both sides.
+template <int DST, int SRC>
+__device__ __forceinline__ void cp_async16_at(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src), "n"(DST), "n"(SRC)
+                 : "memory");
+}
+
 __device__ __forceinline__ void cp_async_commit()
 {
     asm volatile("cp.async.commit_group;" ::: "memory");
