@@ -163,84 +163,106 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const Rout
         return;
 
     // --- softmax and top-k of this chunk, a warp per token ------------------------------------
+    const int pairs = p.tokens * p.top;
+    const bool one_chunk = gridDim.y == 1;
     if (warp < nt) {
         const int t = t0 + warp;
         constexpr int PER = MOE_MAX_EXPERTS / 32;
-        float l[PER];
-        uint32_t taken = 0;
+        // Scores as unsigned numbers of the same order; a NaN counts as the lowest, so that top_k
+        // distinct experts come out whatever x holds.  0: none left in this place.
+        uint32_t key[PER];
+        float sum = 0.f, top = 0.f;
+        {
+            float l[PER];
+            uint32_t most = 0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
-            l[i] = i * 32 + lane < p.experts ? __ldcg(p.logits + (long long)t * p.experts + i * 32 + lane) : -INFINITY;
-        float top = 0.f, sum = 0.f, chosen = 0.f;
+            for (int i = 0; i < PER; ++i) {
+                key[i] = 0;
+                if (i * 32 >= p.experts)
+                    break;
+                const int idx = i * 32 + lane;
+                l[i] = idx < p.experts ? __ldcg(p.logits + (long long)t * p.experts + idx) : -INFINITY;
+                const uint32_t bits = __float_as_uint(l[i] == 0.f ? 0.f : l[i]); // -0 and 0 are equal
+                if (idx < p.experts)
+                    key[i] = l[i] != l[i] ? 1u : max(2u, bits & 0x80000000u ? ~bits : bits | 0x80000000u);
+                most = max(most, key[i]);
+            }
+            most = __reduce_max_sync(0xffffffffu, most);
+            top = most <= 2u ? -INFINITY : __uint_as_float(most & 0x80000000u ? most & 0x7fffffffu : ~most);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                if (i * 32 >= p.experts)
+                    break;
+                if (i * 32 + lane < p.experts)
+                    sum += expf(l[i] - top);
+            }
+#pragma unroll
+            for (int d = 16; d; d >>= 1)
+                sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        }
+        float chosen = 0.f, mine = 0.f; // lane j keeps the j-th choice
+        int mine_at = 0;
         for (int j = 0; j < p.top; ++j) {
-            float best = -INFINITY;
+            uint32_t best = 0;
             int at = MOE_MAX_EXPERTS;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const int idx = i * 32 + lane;
-                // A NaN counts as -inf here, so that top_k distinct experts come out whatever x holds.
-                const float v = l[i] == l[i] ? l[i] : -INFINITY;
-                if (idx < p.experts && !((taken >> i) & 1u) && (at == MOE_MAX_EXPERTS || v > best)) {
-                    best = v;
-                    at = idx;
+                if (i * 32 >= p.experts)
+                    break;
+                if (key[i] > best) {
+                    best = key[i];
+                    at = i * 32 + lane;
                 }
             }
+            const uint32_t most = __reduce_max_sync(0xffffffffu, best);
+            at = (int)__reduce_min_sync(0xffffffffu, (uint32_t)(best == most ? at : MOE_MAX_EXPERTS));
 #pragma unroll
-            for (int d = 16; d; d >>= 1) {
-                const float ov = __shfl_xor_sync(0xffffffffu, best, d);
-                const int oa = __shfl_xor_sync(0xffffffffu, at, d);
-                if (oa < MOE_MAX_EXPERTS && (at == MOE_MAX_EXPERTS || ov > best || (ov == best && oa < at))) {
-                    best = ov;
-                    at = oa;
-                }
+            for (int i = 0; i < PER; ++i) {
+                if (i * 32 >= p.experts)
+                    break;
+                if (at == i * 32 + lane)
+                    key[i] = 0;
             }
-            if (j == 0) {
-                top = best;
-#pragma unroll
-                for (int i = 0; i < PER; ++i)
-                    if (i * 32 + lane < p.experts)
-                        sum += expf(l[i] - top);
-#pragma unroll
-                for (int d = 16; d; d >>= 1)
-                    sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            }
-            if ((at & 31) == lane)
-                taken |= 1u << (at >> 5);
-            const float w = expf(best - top) / sum;
+            const float score = most <= 2u ? (most == 1u ? NAN : -INFINITY)
+                                           : __uint_as_float(most & 0x80000000u ? most & 0x7fffffffu : ~most);
+            const float w = expf(score - top) / sum;
             chosen += w;
-            if (lane == 0) {
-                __stcg(p.tab.ids + t * p.top + j, at);
-                __stcg(p.tab.weights + t * p.top + j, w);
-                if (p.topk_ids)
-                    p.topk_ids[t * p.top + j] = at;
+            if (lane == j) {
+                mine = w;
+                mine_at = at;
             }
         }
-        __syncwarp();
-        for (int j = lane; j < p.top; j += 32) {
-            float w = __ldcg(p.tab.weights + t * p.top + j);
-            if (p.renorm)
-                w /= chosen;
-            __stcg(p.tab.weights + t * p.top + j, w);
+        if (lane < p.top) {
+            const float w = p.renorm ? mine / chosen : mine;
+            const int pair = t * p.top + lane;
+            p.tab.weights[pair] = w;
+            if (one_chunk)
+                ids[pair] = mine_at;
+            else
+                __stcg(p.tab.ids + pair, mine_at);
+            if (p.topk_ids)
+                p.topk_ids[pair] = mine_at;
             if (p.topk_weights)
-                p.topk_weights[t * p.top + j] = w;
+                p.topk_weights[pair] = w;
         }
     }
     __syncthreads();
-    if (tid == 0) {
-        const int last = arrive_counter(p.counters + gridDim.y) == (int)gridDim.y - 1;
-        if (last)
-            p.counters[gridDim.y] = 0;
-        is_last = last;
+    if (!one_chunk) {
+        if (tid == 0) {
+            const int last = arrive_counter(p.counters + gridDim.y) == (int)gridDim.y - 1;
+            if (last)
+                p.counters[gridDim.y] = 0;
+            is_last = last;
+        }
+        __syncthreads();
+        if (!is_last)
+            return;
+        for (int i = tid; i < pairs; i += MOE_THREADS)
+            ids[i] = __ldcg(p.tab.ids + i);
+        __syncthreads();
     }
-    __syncthreads();
-    if (!is_last)
-        return;
 
     // --- pairs by expert ----------------------------------------------------------------------
-    const int pairs = p.tokens * p.top;
-    for (int i = tid; i < pairs; i += MOE_THREADS)
-        ids[i] = __ldcg(p.tab.ids + i);
-    __syncthreads();
     for (int x = tid; x < p.experts; x += MOE_THREADS) {
         int n = 0;
         for (int i = 0; i < pairs; ++i)
@@ -482,6 +504,46 @@ __global__ void __launch_bounds__(MOE_THREADS, MoeGeom<NT>::CTAS) moe_layer_gemm
     for (int s = 0; s < STAGES - 1; ++s)
         issue(s);
 
+    // The output of the columns at which this team arrived last: every expert's part is there.
+    int arrived = -1;
+    auto finish = [&]() {
+        if (arrived < 0 || !last_sh[team])
+            return;
+        for (int x = team_tid; x < p.tokens * (COLS / 4); x += team_threads) {
+            const int tok = x / (COLS / 4), col = arrived * COLS + (x % (COLS / 4)) * 4;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int j = 0; j < p.top; ++j) {
+                const int pair = tok * p.top + j;
+                const float wt = p.tab.weights[pair];
+                const float4 *src = reinterpret_cast<const float4 *>(p.part + (long long)pair * p.splits * p.n + col);
+                float4 v = __ldcg(src);
+                for (int s = 1; s < p.splits; ++s) {
+                    const float4 o = __ldcg(src + (long long)s * (p.n / 4));
+                    v.x += o.x;
+                    v.y += o.y;
+                    v.z += o.z;
+                    v.w += o.w;
+                }
+                a.x = fmaf(wt, v.x, a.x);
+                a.y = fmaf(wt, v.y, a.y);
+                a.z = fmaf(wt, v.z, a.z);
+                a.w = fmaf(wt, v.w, a.w);
+            }
+            if (p.residual) {
+                const uint2 rv = *reinterpret_cast<const uint2 *>(p.residual + (long long)tok * p.ldr + col);
+                const float2 r0 = unpack2<BF>(rv.x), r1 = unpack2<BF>(rv.y);
+                a.x += r0.x;
+                a.y += r0.y;
+                a.z += r1.x;
+                a.w += r1.y;
+            }
+            uint2 o;
+            o.x = pack2<BF>(a.x, a.y);
+            o.y = pack2<BF>(a.z, a.w);
+            *reinterpret_cast<uint2 *>(p.y + (long long)tok * p.ldy + col) = o;
+        }
+    };
+
     // Half t & 1, column g (bit 2 flipped in half 1), words 2 (t >> 1) and the next.
     const int w_lane = (t & 1) * (COLS * 16) + (g ^ ((t & 1) << 2)) * 16 + (t >> 1) * 8;
     int stage = 0, at = 0;
@@ -508,19 +570,36 @@ __global__ void __launch_bounds__(MOE_THREADS, MoeGeom<NT>::CTAS) moe_layer_gemm
                 const int row = DOWN ? 2 * un.first + c : p.tab.token[un.first + c];
                 arow[n] = p.act + (long long)row * p.k + (un.step0 + member) * MOE_ROWS + t * 8;
             }
-            for (int step = un.step0 + member; step < un.step1; step += p.team) {
+            // With one tile the next block's activations are fetched a block ahead.
+            constexpr bool AHEAD = ND == 1;
+            const int first = un.step0 + member;
+            uint4 bv[ND][2];
+            if (AHEAD && first < un.step1) {
+                const uint4 *ap = reinterpret_cast<const uint4 *>(arow[0]);
+                bv[0][0] = ap[0];
+                bv[0][1] = ap[4];
+            }
+            for (int step = first; step < un.step1; step += p.team) {
                 float lo[MT][ND][4], hi[DUAL ? MT : 1][ND][4], sa[ND][4];
                 const uint8_t *st = nullptr;
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    uint4 bv[ND][2];
+                    uint4 nx[2];
+                    if (AHEAD) {
+                        if (b == 1) // the last step fetches its own first block again
+                            arow[0] += step + p.team < un.step1 ? p.team * MOE_ROWS : 0;
+                        const uint4 *ap = reinterpret_cast<const uint4 *>(arow[0]) + (b ? 0 : 8);
+                        nx[0] = ap[0];
+                        nx[1] = ap[4];
+                    } else {
 #pragma unroll
-                    for (int n = 0; n < ND; ++n) {
-                        const uint4 *ap = reinterpret_cast<const uint4 *>(arow[n]) + b * 8;
-                        bv[n][0] = ap[0];
-                        bv[n][1] = ap[4];
-                        if (b == 1)
-                            arow[n] += p.team * MOE_ROWS;
+                        for (int n = 0; n < ND; ++n) {
+                            const uint4 *ap = reinterpret_cast<const uint4 *>(arow[n]) + b * 8;
+                            bv[n][0] = ap[0];
+                            bv[n][1] = ap[4];
+                            if (b == 1)
+                                arow[n] += p.team * MOE_ROWS;
+                        }
                     }
                     if (b % G::BLOCKS == 0) {
                         if (st)
@@ -627,6 +706,10 @@ __global__ void __launch_bounds__(MOE_THREADS, MoeGeom<NT>::CTAS) moe_layer_gemm
                         else
                             flush(std::false_type(), b == 0);
                     }
+                    if (AHEAD) {
+                        bv[0][0] = nx[0];
+                        bv[0][1] = nx[1];
+                    }
                 }
                 stage = stage + 1 == STAGES ? 0 : stage + 1;
             }
@@ -657,6 +740,8 @@ __global__ void __launch_bounds__(MOE_THREADS, MoeGeom<NT>::CTAS) moe_layer_gemm
                 }
             }
         team_sync(team, team_threads);
+        if (DOWN)
+            finish();
         const float *tr = red + team * p.team * VALS * 32;
         auto joined = [&](int v, int ln) {
             float s = 0.f;
@@ -696,6 +781,7 @@ __global__ void __launch_bounds__(MOE_THREADS, MoeGeom<NT>::CTAS) moe_layer_gemm
         }
         team_sync(team, team_threads); // `red` is free; the team's stores are done
         if (DOWN) {
+            // The arrival's answer is looked at after the next unit, so that only one thread waits for it.
             if (team_tid == 0) {
                 int *counter = p.counters + un.col;
                 const int last = arrive_counter(counter) == units / p.col_units - 1;
@@ -703,43 +789,12 @@ __global__ void __launch_bounds__(MOE_THREADS, MoeGeom<NT>::CTAS) moe_layer_gemm
                     *counter = 0;
                 last_sh[team] = last;
             }
-            team_sync(team, team_threads);
-            if (last_sh[team]) {
-                for (int x = team_tid; x < p.tokens * (COLS / 4); x += team_threads) {
-                    const int tok = x / (COLS / 4), col = un.col * COLS + (x % (COLS / 4)) * 4;
-                    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int j = 0; j < p.top; ++j) {
-                        const int pair = tok * p.top + j;
-                        const float wt = p.tab.weights[pair];
-                        const float4 *src = reinterpret_cast<const float4 *>(p.part + (long long)pair * p.splits * p.n + col);
-                        float4 v = __ldcg(src);
-                        for (int s = 1; s < p.splits; ++s) {
-                            const float4 o = __ldcg(src + (long long)s * (p.n / 4));
-                            v.x += o.x;
-                            v.y += o.y;
-                            v.z += o.z;
-                            v.w += o.w;
-                        }
-                        a.x = fmaf(wt, v.x, a.x);
-                        a.y = fmaf(wt, v.y, a.y);
-                        a.z = fmaf(wt, v.z, a.z);
-                        a.w = fmaf(wt, v.w, a.w);
-                    }
-                    if (p.residual) {
-                        const uint2 rv = *reinterpret_cast<const uint2 *>(p.residual + (long long)tok * p.ldr + col);
-                        const float2 r0 = unpack2<BF>(rv.x), r1 = unpack2<BF>(rv.y);
-                        a.x += r0.x;
-                        a.y += r0.y;
-                        a.z += r1.x;
-                        a.w += r1.y;
-                    }
-                    uint2 o;
-                    o.x = pack2<BF>(a.x, a.y);
-                    o.y = pack2<BF>(a.z, a.w);
-                    *reinterpret_cast<uint2 *>(p.y + (long long)tok * p.ldy + col) = o;
-                }
-            }
+            arrived = un.col;
         }
+    }
+    if (DOWN) {
+        team_sync(team, team_threads);
+        finish();
     }
     cp_async_wait<0>();
 }
@@ -822,11 +877,12 @@ GemmKernel gemm_kernel(bool bf, bool down)
     return down ? moe_layer_gemm_kernel<NT, false, true> : moe_layer_gemm_kernel<NT, false, false>;
 }
 
-// 8-column tiles of the token side: enough for every token on one expert, at most 4 (32 columns);
-// more pairs on an expert take further passes over its weights.
-int token_tiles(int columns)
+// 8-column tiles of the token side, by the columns that an expert's pairs take on average and at most:
+// one, two or four.  An expert with more pairs takes further passes over its weights, which then come
+// from L2.
+int token_tiles(double mean, int most)
 {
-    return columns <= 8 ? 1 : columns <= 16 ? 2 : 4;
+    return most <= 8 || mean <= 4.5 ? 1 : most <= 16 || mean <= 11.0 ? 2 : 4;
 }
 
 // Warps per team and parts of K of a product whose `units` units (expert, pass, columns) have
@@ -874,9 +930,9 @@ struct MoePlan {
 MoePlan moe_plan(int tokens, int hidden, int inter, int experts, int top, int num_sms)
 {
     MoePlan p;
-    p.nt_up = token_tiles(tokens);
-    p.nt_down = token_tiles(2 * tokens);
-    const double active = expected_experts(tokens, experts, top);
+    const double active = expected_experts(tokens, experts, top), mean = tokens * (double)top / active;
+    p.nt_up = token_tiles(mean, tokens);
+    p.nt_down = token_tiles(2 * mean, 2 * tokens);
     const int warps = num_sms * 2 * MOE_WARPS;
     const bool sure = tokens == 1; // the number of units is known
     p.up = pick_split(active * (2 * inter / unit_cols(p.nt_up)), hidden / MOE_ROWS, warps / (p.nt_up > 2 ? 2 : 1), 1, sure);
