@@ -357,6 +357,14 @@ __device__ __forceinline__ float gate_act(float g, int kind)
     return g / (1.0f + expf(-x));
 }
 
+// (x & mask) | base in one instruction (the compiler spends two where both are constants).
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t base)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(mask), "r"(base));
+    return r;
+}
+
 __device__ __forceinline__ void team_sync(int team_id, int threads)
 {
     if (threads == 32)
@@ -544,6 +552,8 @@ __global__ void __launch_bounds__(MOE_THREADS, MoeGeom<NT>::CTAS) moe_layer_gemm
         }
     };
 
+    uint32_t nibble = 0x000F000Fu, base128 = 0x43004300u; // in registers, not known to the compiler
+    asm volatile("" : "+r"(nibble), "+r"(base128));
     // Half t & 1, column g (bit 2 flipped in half 1), words 2 (t >> 1) and the next.
     const int w_lane = (t & 1) * (COLS * 16) + (g ^ ((t & 1) << 2)) * 16 + (t >> 1) * 8;
     int stage = 0, at = 0;
@@ -632,20 +642,34 @@ __global__ void __launch_bounds__(MOE_THREADS, MoeGeom<NT>::CTAS) moe_layer_gemm
 #pragma unroll
                         for (int m = 0; m < MT; ++m) {
                             const uint32_t x = i ? w[m][0].y : w[m][0].x, y = i ? w[m][1].y : w[m][1].x;
-                            constexpr uint32_t L = 0x000F000Fu, H = 0x00F000F0u, O = BF ? 0x43004300u : 0u;
-                            const uint32_t x8 = x >> 8, y8 = y >> 8;
-                            const uint32_t a0 = (x & L) | O, a1 = (y & L) | O, a2 = (x8 & L) | O, a3 = (y8 & L) | O;
-                            uint32_t c0, c1, c2, c3;
-                            if (DUAL) {
-                                c0 = x & H;
-                                c1 = y & H;
-                                c2 = x8 & H;
-                                c3 = y8 & H;
+                            constexpr uint32_t L = 0x000F000Fu, H = 0x00F000F0u;
+                            uint32_t a0, a1, a2, a3, c0, c1, c2, c3;
+                            if (BF) {
+                                a0 = and_or(x, nibble, base128);
+                                a1 = and_or(y, nibble, base128);
+                                a2 = and_or((x >> 8), nibble, base128);
+                                a3 = and_or((y >> 8), nibble, base128);
+                                c0 = and_or((x >> 4), nibble, base128);
+                                c1 = and_or((y >> 4), nibble, base128);
+                                c2 = and_or((x >> 12), nibble, base128);
+                                c3 = and_or((y >> 12), nibble, base128);
                             } else {
-                                c0 = ((x >> 4) & L) | O;
-                                c1 = ((y >> 4) & L) | O;
-                                c2 = ((x >> 12) & L) | O;
-                                c3 = ((y >> 12) & L) | O;
+                                const uint32_t x8 = (x >> 8), y8 = (y >> 8);
+                                a0 = x & L;
+                                a1 = y & L;
+                                a2 = x8 & L;
+                                a3 = y8 & L;
+                                if (DUAL) {
+                                    c0 = x & H;
+                                    c1 = y & H;
+                                    c2 = x8 & H;
+                                    c3 = y8 & H;
+                                } else {
+                                    c0 = (x >> 4) & L;
+                                    c1 = (y >> 4) & L;
+                                    c2 = (x >> 12) & L;
+                                    c3 = (y >> 12) & L;
+                                }
                             }
 #pragma unroll
                             for (int n = 0; n < ND; ++n) {
@@ -745,38 +769,36 @@ __global__ void __launch_bounds__(MOE_THREADS, MoeGeom<NT>::CTAS) moe_layer_gemm
         const float *tr = red + team * p.team * VALS * 32;
         auto joined = [&](int v, int ln) {
             float s = 0.f;
-            for (int w = 0; w < p.team; ++w)
-                s += tr[(w * VALS + v) * 32 + ln];
+#pragma unroll
+            for (int w = 0; w < MOE_WARPS; ++w)
+                if (w < p.team)
+                    s += tr[(w * VALS + v) * 32 + ln];
             return BF ? s : s * (1.f / CODE_UNIT);
         };
         if (!DOWN) {
-            // (column tile pair f, token tile n, register i, lane): gate column g + 8 (i >> 1) of tile
-            // 2 f, up of tile 2 f + 1.
-            for (int x = team_tid; x < MT / 2 * NT * 4 * 32; x += team_threads) {
-                const int ln = x & 31, v = x >> 5, i = v & 3, n = (v >> 2) % NT, fm = (v >> 2) / NT;
-                const int pr = n * 8 + 2 * (ln & 3) + (i & 1);
-                if (pr >= un.cols)
-                    continue;
-                const float gate = joined((2 * fm * NT + n) * 4 + i, ln);
-                const float up = joined(((2 * fm + 1) * NT + n) * 4 + i, ln);
+            // Item: feature f of the unit's COLS / 2, pair pr.  Its gate sum is column f % 8 (+ 8) of
+            // tile 2 (f / 16), its up sum of the next tile.
+            for (int x = team_tid; x < un.cols * (COLS / 2); x += team_threads) {
+                const int f = x % (COLS / 2), pr = x / (COLS / 2);
+                const int ln = (f & 7) * 4 + ((pr >> 1) & 3), v = ((f >> 4) * 2 * NT + (pr >> 3)) * 4 + ((f >> 3) & 1) * 2 + (pr & 1);
+                const float gate = joined(v, ln), up = joined(v + NT * 4, ln);
                 const float hv = gate_act(gate, p.glu) * up;
-                const int f = un.col * (COLS / 2) + fm * 16 + (ln >> 2) + 8 * (i >> 1);
                 // fp16: the value part stops at the largest finite value and the remainder goes on
                 // from there (a NaN stays one).
                 const float hc = !BF && fabsf(hv) > 65504.f ? copysignf(65504.f, hv) : hv;
                 const uint16_t hb = from_float<BF>(hc);
-                uint16_t *dst = p.h + (long long)(2 * (un.first + pr)) * p.inter + (f & ~63) + frag_index(f & 63);
+                const int row = un.col * (COLS / 2) + f;
+                uint16_t *dst = p.h + (long long)(2 * (un.first + pr)) * p.inter + (row & ~63) + frag_index(row & 63);
                 dst[0] = hb;
                 dst[p.inter] = from_float<BF>(hv - to_float<BF>(hb));
             }
         } else {
-            for (int x = team_tid; x < MT * NT * 2 * 32; x += team_threads) {
-                const int ln = x & 31, v = x >> 5, c = v & 1, n = (v >> 1) % NT, m = (v >> 1) / NT;
-                const int pr = n * 4 + (ln & 3);
-                if (pr >= un.cols)
-                    continue;
+            // Item: column c of the unit, pair pr.
+            for (int x = team_tid; x < un.cols * COLS; x += team_threads) {
+                const int c = x % COLS, pr = x / COLS;
+                const int ln = (c & 7) * 4 + (pr & 3), v = ((c >> 4) * NT + (pr >> 2)) * 2 + ((c >> 3) & 1);
                 const int pair = p.tab.sorted[un.first + pr];
-                __stcg(p.part + ((long long)pair * p.splits + un.split) * p.n + un.col * COLS + m * 16 + c * 8 + (ln >> 2), joined(v, ln));
+                __stcg(p.part + ((long long)pair * p.splits + un.split) * p.n + un.col * COLS + c, joined(v, ln));
             }
         }
         team_sync(team, team_threads); // `red` is free; the team's stores are done
