@@ -38,7 +38,7 @@ constexpr int MOE_MAX_TOKENS = 64;
 constexpr int MOE_MAX_EXPERTS = 512;
 constexpr int MOE_MAX_TOP = 16;
 constexpr int MOE_MAX_PAIRS = MOE_MAX_TOKENS * MOE_MAX_TOP;
-constexpr int MOE_WARPS = 8;
+constexpr int MOE_WARPS = 8; // of a routing block
 constexpr int MOE_THREADS = MOE_WARPS * 32;
 constexpr int MOE_CHUNK = 4;   // tokens per routing block
 constexpr int MOE_COLS = 32;   // fewest weight columns per unit
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const Rout
 {
     __shared__ int is_last;
     __shared__ float partial[MOE_WARPS][MOE_CHUNK];
-    __shared__ int ids[MOE_MAX_PAIRS];
+    __shared__ int ids[MOE_MAX_PAIRS], rank[MOE_MAX_PAIRS];
     __shared__ int count[MOE_MAX_EXPERTS], off_of[MOE_MAX_EXPERTS];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_wait();
@@ -263,13 +263,27 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const Rout
     }
 
     // --- pairs by expert ----------------------------------------------------------------------
-    for (int x = tid; x < p.experts; x += MOE_THREADS) {
-        int n = 0;
-        for (int i = 0; i < pairs; ++i)
-            n += ids[i] == x ? 1 : 0;
-        count[x] = n;
-    }
+    // One warp walks the pairs in order: a pair's place among its expert's is the count so far plus
+    // its rank among the equal ones of its 32.
+    for (int x = tid; x < p.experts; x += MOE_THREADS)
+        count[x] = 0;
     __syncthreads();
+    if (warp == 0) {
+        for (int base = 0; base < pairs; base += 32) {
+            const int i = base + lane;
+            const int x = i < pairs ? ids[i] : -1 - lane;
+            const uint32_t same = __match_any_sync(0xffffffffu, x);
+            const int below = __popc(same & ((1u << lane) - 1u));
+            const int before = i < pairs ? count[x] : 0;
+            __syncwarp();
+            if (i < pairs) {
+                rank[i] = before + below;
+                if (below == 0)
+                    count[x] = before + __popc(same);
+            }
+            __syncwarp();
+        }
+    }
     if (warp == 0) {
         int slots = 0, off = 0, up = 0, down = 0;
         for (int base = 0; base < p.experts; base += 32) {
@@ -312,15 +326,10 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const Rout
         }
     }
     __syncthreads();
-    for (int x = tid; x < p.experts; x += MOE_THREADS) {
-        if (count[x] == 0)
-            continue;
-        int at = off_of[x];
-        for (int i = 0; i < pairs; ++i)
-            if (ids[i] == x) {
-                p.tab.sorted[at] = i;
-                p.tab.token[at++] = i / p.top;
-            }
+    for (int i = tid; i < pairs; i += MOE_THREADS) {
+        const int at = off_of[ids[i]] + rank[i];
+        p.tab.sorted[at] = i;
+        p.tab.token[at] = i / p.top;
     }
 }
 
@@ -412,20 +421,21 @@ __device__ __forceinline__ Unit find_unit(const MoeGemm &p, int u, int &at)
 template <int NT>
 struct MoeGeom {
     static constexpr int MT = 4;
-    static constexpr int CTAS = NT <= 2 ? 2 : 1; // blocks per SM
+    static constexpr int WARPS = NT == 2 ? 4 : 8;
+    static constexpr int CTAS = NT == 1 ? 2 : NT == 2 ? 3 : 1; // blocks per SM
     static constexpr int COLS = 16 * MT;
     static constexpr int BLOCKS = 4 / MT; // 64-row blocks per stage: 2 KiB of codes
     static constexpr int SZ = COLS * 2;   // bytes of one scale (or zero) row
     static constexpr int STAGE = 2048 + 2 * BLOCKS * SZ;
-    static constexpr int STAGES = NT <= 2 ? 4 : 8;
+    static constexpr int STAGES = NT <= 1 ? 4 : NT == 2 ? 5 : 8;
     static constexpr int RING = STAGES * STAGE;
     static constexpr int vals(bool down) { return MT * NT * (down ? 2 : 4); } // sums per lane to join
-    static constexpr int smem(bool down) { return MOE_WARPS * (RING + vals(down) * 32 * 4); }
+    static constexpr int smem(bool down) { return WARPS * (RING + vals(down) * 32 * 4); }
 };
 
 // DOWN false: gate-up, true: down.
 template <int NT, bool BF, bool DOWN>
-__global__ void __launch_bounds__(MOE_THREADS, MoeGeom<NT>::CTAS) moe_layer_gemm_kernel(const MoeGemm p)
+__global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) moe_layer_gemm_kernel(const MoeGemm p)
 {
     using G = MoeGeom<NT>;
     constexpr int MT = G::MT, COLS = G::COLS, STAGES = G::STAGES, VALS = G::vals(DOWN);
@@ -433,14 +443,14 @@ __global__ void __launch_bounds__(MOE_THREADS, MoeGeom<NT>::CTAS) moe_layer_gemm
     // saves two shifts a word; with more tiles the registers go to the tiles.
     constexpr bool DUAL = !BF && NT == 1;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int last_sh[MOE_WARPS];
+    __shared__ int last_sh[G::WARPS];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
-    const int teams = MOE_WARPS / p.team, team = warp / p.team, member = warp - team * p.team;
+    const int teams = G::WARPS / p.team, team = warp / p.team, member = warp - team * p.team;
     const int team_threads = p.team * 32, team_tid = member * 32 + lane;
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * G::RING;
     const uint8_t *ring_p = smem + warp * G::RING;
-    float *red = reinterpret_cast<float *>(smem + MOE_WARPS * G::RING); // [warp][VALS][32]
+    float *red = reinterpret_cast<float *>(smem + G::WARPS * G::RING); // [warp][VALS][32]
     pdl_wait();
     pdl_launch_dependents();
     const int n_active = __ldcg(p.tab.n_active);
@@ -770,7 +780,7 @@ __global__ void __launch_bounds__(MOE_THREADS, MoeGeom<NT>::CTAS) moe_layer_gemm
         auto joined = [&](int v, int ln) {
             float s = 0.f;
 #pragma unroll
-            for (int w = 0; w < MOE_WARPS; ++w)
+            for (int w = 0; w < G::WARPS; ++w)
                 if (w < p.team)
                     s += tr[(w * VALS + v) * 32 + ln];
             return BF ? s : s * (1.f / CODE_UNIT);
@@ -881,14 +891,21 @@ int check_layer_sizes(int tokens, int hidden, int inter, int experts, int top)
 using GemmKernel = void (*)(MoeGemm);
 struct MoeFamily;
 
-int unit_cols(int nt)
+// The geometry of a variant, by its number of tiles.
+struct MoeShape {
+    int cols, warps, ctas, smem_up, smem_down;
+};
+
+template <int NT>
+MoeShape shape()
 {
-    return nt == 1 ? MoeGeom<1>::COLS : nt == 2 ? MoeGeom<2>::COLS : MoeGeom<4>::COLS;
+    using G = MoeGeom<NT>;
+    return {G::COLS, G::WARPS, G::CTAS, G::smem(false), G::smem(true)};
 }
 
-int unit_smem(int nt, bool down)
+MoeShape shape_of(int nt)
 {
-    return nt == 1 ? MoeGeom<1>::smem(down) : nt == 2 ? MoeGeom<2>::smem(down) : MoeGeom<4>::smem(down);
+    return nt == 1 ? shape<1>() : nt == 2 ? shape<2>() : shape<4>();
 }
 
 template <int NT>
@@ -914,13 +931,13 @@ struct MoeSplit {
     int team, splits;
 };
 
-MoeSplit pick_split(double units, int steps, int warps, int max_splits, bool sure)
+MoeSplit pick_split(double units, int steps, const MoeShape &s, int num_sms, int max_splits, bool sure)
 {
-    MoeSplit best = {MOE_WARPS, 1};
+    MoeSplit best = {s.warps, 1};
     double least = -1;
-    for (int team = MOE_WARPS; team >= 1; team /= 2)
+    for (int team = s.warps; team >= 1; team /= 2)
         for (int splits = 1; splits <= max_splits && splits <= steps; ++splits) {
-            const int teams = warps / team;
+            const int teams = num_sms * s.ctas * (s.warps / team);
             // Rounds of the busiest team: exact, or half a round more than the average.
             const double rounds = sure ? (double)(((long long)(units + 0.5) * splits + teams - 1) / teams)
                                        : units * splits / teams + 0.5;
@@ -955,11 +972,10 @@ MoePlan moe_plan(int tokens, int hidden, int inter, int experts, int top, int nu
     const double active = expected_experts(tokens, experts, top), mean = tokens * (double)top / active;
     p.nt_up = token_tiles(mean, tokens);
     p.nt_down = token_tiles(2 * mean, 2 * tokens);
-    const int warps = num_sms * 2 * MOE_WARPS;
+    const MoeShape up = shape_of(p.nt_up), down = shape_of(p.nt_down);
     const bool sure = tokens == 1; // the number of units is known
-    p.up = pick_split(active * (2 * inter / unit_cols(p.nt_up)), hidden / MOE_ROWS, warps / (p.nt_up > 2 ? 2 : 1), 1, sure);
-    p.down = pick_split(active * (hidden / unit_cols(p.nt_down)), inter / MOE_ROWS,
-                        warps / (p.nt_down > 2 ? 2 : 1), max_splits(tokens * top), sure);
+    p.up = pick_split(active * (2 * inter / up.cols), hidden / MOE_ROWS, up, num_sms, 1, sure);
+    p.down = pick_split(active * (hidden / down.cols), inter / MOE_ROWS, down, num_sms, max_splits(tokens * top), sure);
     return p;
 }
 
@@ -967,18 +983,19 @@ cudaError_t launch_moe_gemm(MoeGemm &p, int nt, MoeSplit split, bool bf, bool do
                             cudaStream_t stream)
 {
     const GemmKernel kernel = nt == 1 ? gemm_kernel<1>(bf, down) : nt == 2 ? gemm_kernel<2>(bf, down) : gemm_kernel<4>(bf, down);
-    const int smem = unit_smem(nt, down);
+    const MoeShape s = shape_of(nt);
+    const int smem = down ? s.smem_down : s.smem_up;
     const int v = (nt == 1 ? 0 : nt == 2 ? 1 : 2) * 4 + (bf ? 2 : 0) + (down ? 1 : 0);
     cudaError_t err = allow_smem<MoeFamily, 12>(reinterpret_cast<const void *>(kernel), v, smem);
     if (err != cudaSuccess)
         return err;
     p.team = split.team;
     p.splits = split.splits;
-    p.col_units = p.n / unit_cols(nt);
+    p.col_units = p.n / s.cols;
     // Exact while n col_units < 2^32: local unit numbers are below 64 passes x 8 splits x col_units
     // and col_units is at most 2^16.
     p.col_magic = (uint32_t)((1ull << 32) / p.col_units + 1);
-    return launch_pdl(kernel, dim3(num_sms * (nt <= 2 ? 2 : 1)), dim3(MOE_THREADS), (size_t)smem, stream, p);
+    return launch_pdl(kernel, dim3(num_sms * s.ctas), dim3(s.warps * 32), (size_t)smem, stream, p);
 }
 
 } // namespace
@@ -1056,8 +1073,8 @@ extern "C" int w4a16_moe_layer(const void *x, int ldx, const void *router, const
     r.experts = n_experts;
     r.top = top_k;
     r.renorm = (flags & W4A16_FLAG_MOE_RENORM) ? 1 : 0;
-    r.up_cols = 2 * inter / unit_cols(plan.nt_up);
-    r.down_cols = hidden / unit_cols(plan.nt_down) * plan.down.splits;
+    r.up_cols = 2 * inter / shape_of(plan.nt_up).cols;
+    r.down_cols = hidden / shape_of(plan.nt_down).cols * plan.down.splits;
     r.up_pass = 8 * plan.nt_up;
     r.down_pass = 4 * plan.nt_down;
     const dim3 grid(n_experts, chunks);
