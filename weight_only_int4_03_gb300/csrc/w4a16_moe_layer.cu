@@ -58,7 +58,7 @@ __host__ __device__ __forceinline__ int frag_index(int row)
 
 // Routing tables in the workspace.
 struct MoeTables {
-    int *n_active;   // [4]: active experts, gate-up units, down units
+    int *head;       // [4]: active experts, gate-up units, down units
     int *ex_id;      // [MOE_MAX_EXPERTS] active experts in increasing order
     int *ex_off;     // [MOE_MAX_EXPERTS + 1] their pairs in `sorted`
     int *pre_up;     // [MOE_MAX_EXPERTS + 1] units before each active expert
@@ -93,7 +93,6 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const Rout
     pdl_wait();
     pdl_launch_dependents();
     const int t0 = blockIdx.y * MOE_CHUNK, nt = min(MOE_CHUNK, p.tokens - t0);
-    const int e = blockIdx.x;
     {
         // This block's share of the tokens' rows in fragment order.
         const int chunks = p.hidden / 8;
@@ -109,10 +108,11 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const Rout
             *reinterpret_cast<uint4 *>(p.xf + (long long)(t0 + tt) * p.hidden + c * 8) = v;
         }
     }
+    // Scores: a block shares expert blockIdx.x's row; the scores meet in global memory, where the
+    // chunk's last block picks them up.
     {
-        // The score of expert e for the chunk's tokens: the block's threads share the row.
         float acc[MOE_CHUNK] = {0.f, 0.f, 0.f, 0.f};
-        const uint16_t *r = p.router + (long long)e * p.hidden;
+        const uint16_t *r = p.router + (long long)blockIdx.x * p.hidden;
 #pragma unroll 2
         for (int k = tid * 8; k < p.hidden; k += MOE_THREADS * 8) {
             const uint4 wv = *reinterpret_cast<const uint4 *>(r + k);
@@ -142,21 +142,24 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const Rout
             if (lane == 0)
                 partial[warp][tt] = v;
         }
-        __syncthreads();
-        if (tid < nt) {
+    }
+    __syncthreads();
+    if (warp == 0) {
+        // The arriving thread's warp is the one that stored: a warp barrier orders it.
+        if (lane < nt) {
             float v = 0.f;
 #pragma unroll
             for (int w = 0; w < MOE_WARPS; ++w)
-                v += partial[w][tid];
-            __stcg(p.logits + (long long)(t0 + tid) * p.experts + e, v);
+                v += partial[w][lane];
+            __stcg(p.logits + (long long)(t0 + lane) * p.experts + blockIdx.x, v);
         }
-    }
-    __syncthreads();
-    if (tid == 0) {
-        const int last = arrive_counter(p.counters + blockIdx.y) == (int)gridDim.x - 1;
-        if (last)
-            p.counters[blockIdx.y] = 0;
-        is_last = last;
+        __syncwarp();
+        if (lane == 0) {
+            const int last = arrive_counter(p.counters + blockIdx.y) == (int)gridDim.x - 1;
+            if (last)
+                p.counters[blockIdx.y] = 0;
+            is_last = last;
+        }
     }
     __syncthreads();
     if (!is_last)
@@ -322,7 +325,7 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const Rout
             p.tab.ex_off[slots] = off;
             p.tab.pre_up[slots] = up;
             p.tab.pre_down[slots] = down;
-            p.tab.n_active[0] = slots;
+            *reinterpret_cast<int4 *>(p.tab.head) = make_int4(slots, up, down, 0);
         }
     }
     __syncthreads();
@@ -388,13 +391,19 @@ struct Unit {
     int split, step0, step1;
 };
 
-// Unit u; `at` is the caller's place among the active experts, which only moves forward with u.
+// Unit u (the same in every lane).  `at` is the caller's place among the active experts; where u is
+// past its units, the place is the number of experts whose units end at or before u, counted by the
+// warp's lanes together.
 template <int NT, bool DOWN>
-__device__ __forceinline__ Unit find_unit(const MoeGemm &p, int u, int &at)
+__device__ __forceinline__ Unit find_unit(const MoeGemm &p, int u, int n_active, int lane, int &at)
 {
-    int next = p.pre[at + 1];
-    while (next <= u)
-        next = p.pre[++at + 1];
+    if (p.pre[at + 1] <= u) {
+        at = 0;
+        for (int base = 0; base < n_active; base += 32) {
+            const int end = base + lane < n_active ? p.pre[base + lane + 1] : 0x7FFFFFFF;
+            at += __popc(__ballot_sync(0xffffffffu, end <= u));
+        }
+    }
     constexpr int PASS = DOWN ? 4 * NT : 8 * NT; // a pair takes two columns of the down MMA
     const int local = u - p.pre[at], part = (int)__umulhi((uint32_t)local, p.col_magic);
     Unit r;
@@ -421,13 +430,13 @@ __device__ __forceinline__ Unit find_unit(const MoeGemm &p, int u, int &at)
 template <int NT>
 struct MoeGeom {
     static constexpr int MT = 4;
-    static constexpr int WARPS = NT == 2 ? 4 : 8;
-    static constexpr int CTAS = NT == 1 ? 2 : NT == 2 ? 3 : 1; // blocks per SM
+    static constexpr int WARPS = NT == 1 ? 8 : 4;
+    static constexpr int CTAS = NT == 1 ? 2 : 3; // blocks per SM
     static constexpr int COLS = 16 * MT;
     static constexpr int BLOCKS = 4 / MT; // 64-row blocks per stage: 2 KiB of codes
     static constexpr int SZ = COLS * 2;   // bytes of one scale (or zero) row
     static constexpr int STAGE = 2048 + 2 * BLOCKS * SZ;
-    static constexpr int STAGES = NT <= 1 ? 4 : NT == 2 ? 5 : 8;
+    static constexpr int STAGES = NT == 1 ? 3 : 5;
     static constexpr int RING = STAGES * STAGE;
     static constexpr int vals(bool down) { return MT * NT * (down ? 2 : 4); } // sums per lane to join
     static constexpr int smem(bool down) { return WARPS * (RING + vals(down) * 32 * 4); }
@@ -439,8 +448,9 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
 {
     using G = MoeGeom<NT>;
     constexpr int MT = G::MT, COLS = G::COLS, STAGES = G::STAGES, VALS = G::vals(DOWN);
-    // fp16 with one token tile: the two nibble positions keep accumulators of their own, which
-    // saves two shifts a word; with more tiles the registers go to the tiles.
+    // One token tile: the two nibble positions keep accumulators of their own, which gives the MMAs
+    // twice as many independent chains and saves fp16 two shifts a word; with more tiles the
+    // registers go to the tiles.
     constexpr bool DUAL = !BF && NT == 1;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int last_sh[G::WARPS];
@@ -453,8 +463,8 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
     float *red = reinterpret_cast<float *>(smem + G::WARPS * G::RING); // [warp][VALS][32]
     pdl_wait();
     pdl_launch_dependents();
-    const int n_active = __ldcg(p.tab.n_active);
-    const int units = __ldcg(p.pre + n_active);
+    const int4 head = __ldcg(reinterpret_cast<const int4 *>(p.tab.head));
+    const int n_active = head.x, units = DOWN ? head.z : head.y;
     const int stride = gridDim.x * teams;
     const int u0 = blockIdx.x * teams + team;
     if (u0 >= units)
@@ -473,7 +483,7 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
     const int sz_block = sz_zero ? sz_row - G::BLOCKS : sz_row;
     auto enter = [&]() { // the next unit in which this member has a step
         for (; iu < units; iu += stride) {
-            const Unit un = find_unit<NT, DOWN>(p, iu, i_at);
+            const Unit un = find_unit<NT, DOWN>(p, iu, n_active, lane, i_at);
             ib = 2 * (un.step0 + member);
             ib_end = 2 * un.step1;
             if (ib >= ib_end)
@@ -529,23 +539,27 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
             return;
         for (int x = team_tid; x < p.tokens * (COLS / 4); x += team_threads) {
             const int tok = x / (COLS / 4), col = arrived * COLS + (x % (COLS / 4)) * 4;
+            // Parts in the order of (j, split), eight loads at a time.
+            const float4 *src = reinterpret_cast<const float4 *>(p.part + (long long)tok * p.top * p.splits * p.n + col);
+            const float *wts = p.tab.weights + tok * p.top;
+            const int parts = p.top * p.splits;
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int j = 0; j < p.top; ++j) {
-                const int pair = tok * p.top + j;
-                const float wt = p.tab.weights[pair];
-                const float4 *src = reinterpret_cast<const float4 *>(p.part + (long long)pair * p.splits * p.n + col);
-                float4 v = __ldcg(src);
-                for (int s = 1; s < p.splits; ++s) {
-                    const float4 o = __ldcg(src + (long long)s * (p.n / 4));
-                    v.x += o.x;
-                    v.y += o.y;
-                    v.z += o.z;
-                    v.w += o.w;
+            for (int q0 = 0; q0 < parts; q0 += 8) {
+                float4 v[8];
+                float wt[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const bool in = q0 + q < parts;
+                    v[q] = in ? __ldcg(src + (long long)(q0 + q) * (p.n / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    wt[q] = in ? wts[p.splits == 1 ? q0 + q : (q0 + q) / p.splits] : 0.f;
                 }
-                a.x = fmaf(wt, v.x, a.x);
-                a.y = fmaf(wt, v.y, a.y);
-                a.z = fmaf(wt, v.z, a.z);
-                a.w = fmaf(wt, v.w, a.w);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    a.x = fmaf(wt[q], v[q].x, a.x);
+                    a.y = fmaf(wt[q], v[q].y, a.y);
+                    a.z = fmaf(wt[q], v[q].z, a.z);
+                    a.w = fmaf(wt[q], v[q].w, a.w);
+                }
             }
             if (p.residual) {
                 const uint2 rv = *reinterpret_cast<const uint2 *>(p.residual + (long long)tok * p.ldr + col);
@@ -566,9 +580,9 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
     asm volatile("" : "+r"(nibble), "+r"(base128));
     // Half t & 1, column g (bit 2 flipped in half 1), words 2 (t >> 1) and the next.
     const int w_lane = (t & 1) * (COLS * 16) + (g ^ ((t & 1) << 2)) * 16 + (t >> 1) * 8;
-    int stage = 0, at = 0;
+    int stage = 0, u_at = 0;
     for (int u = u0; u < units; u += stride) {
-        const Unit un = find_unit<NT, DOWN>(p, u, at);
+        const Unit un = find_unit<NT, DOWN>(p, u, n_active, lane, u_at);
         const int rows = DOWN ? 2 * un.cols : un.cols; // columns in use on the token side
         float out[MT][NT][4];
 #pragma unroll
@@ -642,12 +656,10 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
                     for (int i = 0; i < 2; ++i) {
 #pragma unroll
                         for (int n = 0; n < ND; ++n) {
-                            const uint4 v = bv[n][i];
                             if (b == 0 && i == 0)
-                                mma16816_zero<BF>(sa[n], ONES, ONES, ONES, ONES, v.x, v.y);
+                                mma16816_zero<BF>(sa[n], ONES, ONES, ONES, ONES, bv[n][i].x, bv[n][i].y);
                             else
-                                mma16816<BF>(sa[n], ONES, ONES, ONES, ONES, v.x, v.y);
-                            mma16816<BF>(sa[n], ONES, ONES, ONES, ONES, v.z, v.w);
+                                mma16816<BF>(sa[n], ONES, ONES, ONES, ONES, bv[n][i].x, bv[n][i].y);
                         }
 #pragma unroll
                         for (int m = 0; m < MT; ++m) {
@@ -681,20 +693,27 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
                                     c3 = (y >> 12) & L;
                                 }
                             }
+                            // MMAs on one accumulator are kept apart: each waits for the one before.
 #pragma unroll
                             for (int n = 0; n < ND; ++n) {
-                                const uint4 v = bv[n][i];
-                                float(&h4)[4] = DUAL ? hi[m % (DUAL ? MT : 1)][n] : lo[m][n];
                                 if (b == 0 && i == 0)
-                                    mma16816_zero<BF>(lo[m][n], a0, a1, a2, a3, v.x, v.y);
+                                    mma16816_zero<BF>(lo[m][n], a0, a1, a2, a3, bv[n][i].x, bv[n][i].y);
                                 else
-                                    mma16816<BF>(lo[m][n], a0, a1, a2, a3, v.x, v.y);
-                                if (DUAL && b == 0 && i == 0)
-                                    mma16816_zero<BF>(h4, c0, c1, c2, c3, v.z, v.w);
+                                    mma16816<BF>(lo[m][n], a0, a1, a2, a3, bv[n][i].x, bv[n][i].y);
+                            }
+#pragma unroll
+                            for (int n = 0; n < ND; ++n) {
+                                if (!DUAL)
+                                    mma16816<BF>(lo[m][n], c0, c1, c2, c3, bv[n][i].z, bv[n][i].w);
+                                else if (b == 0 && i == 0)
+                                    mma16816_zero<BF>(hi[m % (DUAL ? MT : 1)][n], c0, c1, c2, c3, bv[n][i].z, bv[n][i].w);
                                 else
-                                    mma16816<BF>(h4, c0, c1, c2, c3, v.z, v.w);
+                                    mma16816<BF>(hi[m % (DUAL ? MT : 1)][n], c0, c1, c2, c3, bv[n][i].z, bv[n][i].w);
                             }
                         }
+#pragma unroll
+                        for (int n = 0; n < ND; ++n)
+                            mma16816<BF>(sa[n], ONES, ONES, ONES, ONES, bv[n][i].z, bv[n][i].w);
                     }
                     // End of a group (or of a step, whose two blocks then share one): scale the sums.
                     const uint8_t *sz = st + 2048 + (b % G::BLOCKS) * G::SZ;
@@ -716,7 +735,7 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
                                         const int i = 2 * c + e;
                                         float q = lo[m][n][i];
                                         if (DUAL)
-                                            q = fmaf(hi[m % (DUAL ? MT : 1)][n][i], 0.0625f, q);
+                                            q = BF ? q + hi[m % (DUAL ? MT : 1)][n][i] : fmaf(hi[m % (DUAL ? MT : 1)][n][i], 0.0625f, q);
                                         q = fmaf(-z, sa[n][e], q);
                                         out[m][n][i] = fmaf(sc, q, out[m][n][i]);
                                         if (again) {
@@ -748,13 +767,8 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
                 stage = stage + 1 == STAGES ? 0 : stage + 1;
             }
         };
-        const int nts = (rows + 7) >> 3;
-        if (NT == 1 || nts == 1)
+        if (NT == 1 || rows <= 8)
             sweep(std::integral_constant<int, 1>());
-        else if (NT == 2 || nts == 2)
-            sweep(std::integral_constant<int, NT < 2 ? 1 : 2>());
-        else if (nts == 3)
-            sweep(std::integral_constant<int, NT < 3 ? 1 : 3>());
         else
             sweep(std::integral_constant<int, NT>());
 
@@ -857,7 +871,7 @@ MoeLayout moe_layout(char *ws, int tokens, int hidden, int inter, int experts, i
         at += 4 * n;
         return r;
     };
-    l.tab.n_active = reinterpret_cast<int *>(take(4));
+    l.tab.head = reinterpret_cast<int *>(take(4));
     l.tab.ex_id = reinterpret_cast<int *>(take(MOE_MAX_EXPERTS));
     l.tab.ex_off = reinterpret_cast<int *>(take(MOE_MAX_EXPERTS + 1));
     l.tab.pre_up = reinterpret_cast<int *>(take(MOE_MAX_EXPERTS + 1));
@@ -905,7 +919,7 @@ MoeShape shape()
 
 MoeShape shape_of(int nt)
 {
-    return nt == 1 ? shape<1>() : nt == 2 ? shape<2>() : shape<4>();
+    return nt == 1 ? shape<1>() : shape<2>();
 }
 
 template <int NT>
@@ -917,11 +931,11 @@ GemmKernel gemm_kernel(bool bf, bool down)
 }
 
 // 8-column tiles of the token side, by the columns that an expert's pairs take on average and at most:
-// one, two or four.  An expert with more pairs takes further passes over its weights, which then come
-// from L2.
+// one or two.  An expert with more pairs takes further passes over its weights, which then come from
+// L2.
 int token_tiles(double mean, int most)
 {
-    return most <= 8 || mean <= 4.5 ? 1 : most <= 16 || mean <= 11.0 ? 2 : 4;
+    return most <= 8 || mean <= 8.5 ? 1 : 2;
 }
 
 // Warps per team and parts of K of a product whose `units` units (expert, pass, columns) have
@@ -982,11 +996,11 @@ MoePlan moe_plan(int tokens, int hidden, int inter, int experts, int top, int nu
 cudaError_t launch_moe_gemm(MoeGemm &p, int nt, MoeSplit split, bool bf, bool down, int num_sms,
                             cudaStream_t stream)
 {
-    const GemmKernel kernel = nt == 1 ? gemm_kernel<1>(bf, down) : nt == 2 ? gemm_kernel<2>(bf, down) : gemm_kernel<4>(bf, down);
+    const GemmKernel kernel = nt == 1 ? gemm_kernel<1>(bf, down) : gemm_kernel<2>(bf, down);
     const MoeShape s = shape_of(nt);
     const int smem = down ? s.smem_down : s.smem_up;
-    const int v = (nt == 1 ? 0 : nt == 2 ? 1 : 2) * 4 + (bf ? 2 : 0) + (down ? 1 : 0);
-    cudaError_t err = allow_smem<MoeFamily, 12>(reinterpret_cast<const void *>(kernel), v, smem);
+    const int v = (nt - 1) * 4 + (bf ? 2 : 0) + (down ? 1 : 0);
+    cudaError_t err = allow_smem<MoeFamily, 8>(reinterpret_cast<const void *>(kernel), v, smem);
     if (err != cudaSuccess)
         return err;
     p.team = split.team;
