@@ -27,6 +27,8 @@
 // its 128-row steps in turn.  A warp streams its steps through its own ring of cp.async stages, which
 // runs on into its next unit, so no block-wide barrier sits between a copy and its use and the ring
 // stays full across units.  Activations are read from L1/L2 in the MMA's fragment order.
+#include <math.h>
+
 #include <type_traits>
 
 #include "w4a16_ops.cuh"
@@ -58,11 +60,11 @@ __host__ __device__ __forceinline__ int frag_index(int row)
 
 // Routing tables in the workspace.
 struct MoeTables {
-    int *head;       // [4]: active experts, gate-up units, down units
-    int *ex_id;      // [MOE_MAX_EXPERTS] active experts in increasing order
-    int *ex_off;     // [MOE_MAX_EXPERTS + 1] their pairs in `sorted`
-    int *pre_up;     // [MOE_MAX_EXPERTS + 1] units before each active expert
-    int *pre_down;
+    // The active experts in increasing order: (first gate-up unit, first down unit, expert | pairs <<
+    // 16, first pair in `sorted`).  From the end of the list to the end of its last 32 entries, at
+    // least once: the totals of both kinds of units.
+    int4 *experts;
+    int chunks;      // 32-entry chunks of the list
     int *sorted;     // [pairs] pair ids t * top_k + j by expert, in increasing order within one
     int *token;      // [pairs] their tokens t
     int *ids;        // [pairs]
@@ -307,13 +309,8 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const Rout
                     d += d2;
                 }
             }
-            if (has) {
-                const int at = slots + s - 1;
-                p.tab.ex_id[at] = x;
-                p.tab.ex_off[at] = off + o - n;
-                p.tab.pre_up[at] = up + u - nu;
-                p.tab.pre_down[at] = down + d - nd;
-            }
+            if (has)
+                p.tab.experts[slots + s - 1] = make_int4(up + u - nu, down + d - nd, x | n << 16, off + o - n);
             if (x < p.experts)
                 off_of[x] = off + o - n;
             slots += __shfl_sync(0xffffffffu, s, 31);
@@ -321,12 +318,8 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const Rout
             up += __shfl_sync(0xffffffffu, u, 31);
             down += __shfl_sync(0xffffffffu, d, 31);
         }
-        if (lane == 0) {
-            p.tab.ex_off[slots] = off;
-            p.tab.pre_up[slots] = up;
-            p.tab.pre_down[slots] = down;
-            *reinterpret_cast<int4 *>(p.tab.head) = make_int4(slots, up, down, 0);
-        }
+        for (int i = slots + lane; i < p.tab.chunks * 32; i += 32)
+            p.tab.experts[i] = make_int4(up, down, 0, off);
     }
     __syncthreads();
     for (int i = tid; i < pairs; i += MOE_THREADS) {
@@ -346,7 +339,6 @@ struct MoeGemm {
     uint16_t *y;
     int *counters;           // down: one per 32 columns
     MoeTables tab;
-    const int *pre;          // units before each active expert
     long long expert_words, expert_groups;
     int k, n, steps;         // steps: 128-row steps of K
     int kblocks;             // 64-row blocks of K
@@ -391,23 +383,29 @@ struct Unit {
     int split, step0, step1;
 };
 
-// Unit u (the same in every lane).  `at` is the caller's place among the active experts; where u is
-// past its units, the place is the number of experts whose units end at or before u, counted by the
-// warp's lanes together.
+// Unit u (the same in every lane): its expert is the last of the list whose first unit is at or
+// before u, looked up by the warp's lanes together.
 template <int NT, bool DOWN>
-__device__ __forceinline__ Unit find_unit(const MoeGemm &p, int u, int n_active, int lane, int &at)
+__device__ __forceinline__ Unit find_unit(const MoeGemm &p, int u, int lane)
 {
-    if (p.pre[at + 1] <= u) {
-        at = 0;
-        for (int base = 0; base < n_active; base += 32) {
-            const int end = base + lane < n_active ? p.pre[base + lane + 1] : 0x7FFFFFFF;
-            at += __popc(__ballot_sync(0xffffffffu, end <= u));
-        }
+    int start = 0, id = 0, off = 0;
+    for (int c = 0; c < p.tab.chunks; ++c) {
+        const int4 e = p.tab.experts[c * 32 + lane];
+        const int first = DOWN ? e.y : e.x;
+        const uint32_t before = __ballot_sync(0xffffffffu, first <= u);
+        if (before == 0)
+            break;
+        const int src = 31 - __clz(before);
+        start = __shfl_sync(0xffffffffu, first, src);
+        id = __shfl_sync(0xffffffffu, e.z, src);
+        off = __shfl_sync(0xffffffffu, e.w, src);
+        if (before != 0xffffffffu)
+            break;
     }
     constexpr int PASS = DOWN ? 4 * NT : 8 * NT; // a pair takes two columns of the down MMA
-    const int local = u - p.pre[at], part = (int)__umulhi((uint32_t)local, p.col_magic);
+    const int local = u - start, part = (int)__umulhi((uint32_t)local, p.col_magic);
     Unit r;
-    r.expert = p.tab.ex_id[at];
+    r.expert = id & 0xFFFF;
     r.col = local - part * p.col_units;
     int pass = part;
     r.split = 0;
@@ -419,9 +417,8 @@ __device__ __forceinline__ Unit find_unit(const MoeGemm &p, int u, int n_active,
         r.step0 = r.split * p.steps / p.splits;
         r.step1 = (r.split + 1) * p.steps / p.splits;
     }
-    const int off = p.tab.ex_off[at], end = p.tab.ex_off[at + 1];
     r.first = off + pass * PASS;
-    r.cols = min(PASS, end - r.first);
+    r.cols = min(PASS, (id >> 16) - pass * PASS);
     return r;
 }
 
@@ -463,16 +460,17 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
     float *red = reinterpret_cast<float *>(smem + G::WARPS * G::RING); // [warp][VALS][32]
     pdl_wait();
     pdl_launch_dependents();
-    const int4 head = __ldcg(reinterpret_cast<const int4 *>(p.tab.head));
-    const int n_active = head.x, units = DOWN ? head.z : head.y;
+    const int4 total = p.tab.experts[p.tab.chunks * 32 - 1];
+    const int units = DOWN ? total.y : total.x;
+    // Consecutive units go to different blocks, so that a part round still reaches every SM.
     const int stride = gridDim.x * teams;
-    const int u0 = blockIdx.x * teams + team;
+    const int u0 = team * gridDim.x + blockIdx.x;
     if (u0 >= units)
         return; // the whole team leaves; the other teams of the block have barriers of their own
 
     // --- the copying side: (unit, block) runs ahead of the computing side ----------------------
     // A member takes the 128-row steps member, member + team, ..., each as 2 / BLOCKS stages.
-    int iu = u0, i_at = 0, ib = 0, ib_end = 0;
+    int iu = u0, ib = 0, ib_end = 0;
     const int32_t *i_w = nullptr; // this lane's piece of block 0, half 0 of the unit's columns
     const uint16_t *i_s = nullptr; // this lane's part of the expert's scale (or zero) row 0
     // Lane l looks after chunk l % (SZ / 16) of a row; rows: scales of the stage's blocks, then zeros.
@@ -483,7 +481,7 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
     const int sz_block = sz_zero ? sz_row - G::BLOCKS : sz_row;
     auto enter = [&]() { // the next unit in which this member has a step
         for (; iu < units; iu += stride) {
-            const Unit un = find_unit<NT, DOWN>(p, iu, n_active, lane, i_at);
+            const Unit un = find_unit<NT, DOWN>(p, iu, lane);
             ib = 2 * (un.step0 + member);
             ib_end = 2 * un.step1;
             if (ib >= ib_end)
@@ -532,6 +530,12 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
     for (int s = 0; s < STAGES - 1; ++s)
         issue(s);
 
+    // The team that arrives last at its columns adds the residual there: on its way into L2 meanwhile.
+    if (DOWN && p.residual) {
+        const int col = u0 % p.col_units * COLS;
+        for (int tok = team_tid; tok < p.tokens; tok += team_threads)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.residual + (long long)tok * p.ldr + col));
+    }
     // The output of the columns at which this team arrived last: every expert's part is there.
     int arrived = -1;
     auto finish = [&]() {
@@ -580,9 +584,9 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
     asm volatile("" : "+r"(nibble), "+r"(base128));
     // Half t & 1, column g (bit 2 flipped in half 1), words 2 (t >> 1) and the next.
     const int w_lane = (t & 1) * (COLS * 16) + (g ^ ((t & 1) << 2)) * 16 + (t >> 1) * 8;
-    int stage = 0, u_at = 0;
+    int stage = 0;
     for (int u = u0; u < units; u += stride) {
-        const Unit un = find_unit<NT, DOWN>(p, u, n_active, lane, u_at);
+        const Unit un = find_unit<NT, DOWN>(p, u, lane);
         const int rows = DOWN ? 2 * un.cols : un.cols; // columns in use on the token side
         float out[MT][NT][4];
 #pragma unroll
@@ -871,11 +875,8 @@ MoeLayout moe_layout(char *ws, int tokens, int hidden, int inter, int experts, i
         at += 4 * n;
         return r;
     };
-    l.tab.head = reinterpret_cast<int *>(take(4));
-    l.tab.ex_id = reinterpret_cast<int *>(take(MOE_MAX_EXPERTS));
-    l.tab.ex_off = reinterpret_cast<int *>(take(MOE_MAX_EXPERTS + 1));
-    l.tab.pre_up = reinterpret_cast<int *>(take(MOE_MAX_EXPERTS + 1));
-    l.tab.pre_down = reinterpret_cast<int *>(take(MOE_MAX_EXPERTS + 1));
+    l.tab.chunks = ((experts < pairs ? experts : pairs) + 32) / 32;
+    l.tab.experts = reinterpret_cast<int4 *>(take(4LL * 32 * l.tab.chunks));
     l.tab.sorted = reinterpret_cast<int *>(take(pairs));
     l.tab.token = reinterpret_cast<int *>(take(pairs));
     l.tab.ids = reinterpret_cast<int *>(take(pairs));
@@ -945,18 +946,16 @@ struct MoeSplit {
     int team, splits;
 };
 
-MoeSplit pick_split(double units, int steps, const MoeShape &s, int num_sms, int max_splits, bool sure)
+MoeSplit pick_split(double units, int steps, const MoeShape &s, int num_sms, int max_splits)
 {
     MoeSplit best = {s.warps, 1};
     double least = -1;
     for (int team = s.warps; team >= 1; team /= 2)
         for (int splits = 1; splits <= max_splits && splits <= steps; ++splits) {
             const int teams = num_sms * s.ctas * (s.warps / team);
-            // Rounds of the busiest team: exact, or half a round more than the average.
-            const double rounds = sure ? (double)(((long long)(units + 0.5) * splits + teams - 1) / teams)
-                                       : units * splits / teams + 0.5;
+            const double rounds = ceil(units * splits / teams - 0.001);
             const int part = (steps + splits - 1) / splits;
-            const double cost = (rounds < 1 ? 1 : rounds) * ((part + team - 1) / team + 2);
+            const double cost = rounds * ((part + team - 1) / team + 2);
             if (least < 0 || cost < least) {
                 least = cost;
                 best = {team, splits};
@@ -965,14 +964,22 @@ MoeSplit pick_split(double units, int steps, const MoeShape &s, int num_sms, int
     return best;
 }
 
-// Experts that a call reads, were each token's choice uniform.
-double expected_experts(int tokens, int experts, int top)
+// What a call's experts come to, were each token's choice uniform: the number of them that have
+// `pass` or fewer pairs counted once, up to twice that twice, and so on (an expert has n pairs with
+// the binomial probability).
+double expected_passes(int tokens, int experts, int top, int pass)
 {
-    double miss = 1.0;
+    const double q = (double)top / experts;
+    if (q >= 1.0)
+        return (double)experts * ((tokens + pass - 1) / pass);
+    double chance = 1.0, sum = 0.0; // of n pairs
     for (int t = 0; t < tokens; ++t)
-        miss *= 1.0 - (double)top / experts;
-    const double n = experts * (1.0 - miss);
-    return n < top ? top : n;
+        chance *= 1.0 - q;
+    for (int n = 1; n <= tokens; ++n) {
+        chance *= q / (1.0 - q) * (tokens - n + 1) / n;
+        sum += chance * ((n + pass - 1) / pass);
+    }
+    return experts * sum;
 }
 
 struct MoePlan {
@@ -983,13 +990,14 @@ struct MoePlan {
 MoePlan moe_plan(int tokens, int hidden, int inter, int experts, int top, int num_sms)
 {
     MoePlan p;
-    const double active = expected_experts(tokens, experts, top), mean = tokens * (double)top / active;
+    const double active = expected_passes(tokens, experts, top, tokens), mean = tokens * (double)top / active;
     p.nt_up = token_tiles(mean, tokens);
     p.nt_down = token_tiles(2 * mean, 2 * tokens);
     const MoeShape up = shape_of(p.nt_up), down = shape_of(p.nt_down);
-    const bool sure = tokens == 1; // the number of units is known
-    p.up = pick_split(active * (2 * inter / up.cols), hidden / MOE_ROWS, up, num_sms, 1, sure);
-    p.down = pick_split(active * (hidden / down.cols), inter / MOE_ROWS, down, num_sms, max_splits(tokens * top), sure);
+    p.up = pick_split(expected_passes(tokens, experts, top, 8 * p.nt_up) * (2 * inter / up.cols), hidden / MOE_ROWS,
+                      up, num_sms, 1);
+    p.down = pick_split(expected_passes(tokens, experts, top, 4 * p.nt_down) * (hidden / down.cols),
+                        inter / MOE_ROWS, down, num_sms, max_splits(tokens * top));
     return p;
 }
 
@@ -1108,7 +1116,6 @@ extern "C" int w4a16_moe_layer(const void *x, int ldx, const void *router, const
     m.y = static_cast<uint16_t *>(y);
     m.counters = counters + chunks + 1;
     m.tab = lay.tab;
-    m.pre = lay.tab.pre_up;
     m.k = hidden;
     m.n = 2 * inter;
     m.tokens = n_tokens;
@@ -1135,7 +1142,6 @@ extern "C" int w4a16_moe_layer(const void *x, int ldx, const void *router, const
     m.s = static_cast<const uint16_t *>(down_scales);
     m.z = static_cast<const uint16_t *>(down_zeros);
     m.act = m.h;
-    m.pre = lay.tab.pre_down;
     m.k = inter;
     m.n = hidden;
     sizes();
