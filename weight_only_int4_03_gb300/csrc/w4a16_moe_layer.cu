@@ -78,6 +78,7 @@ struct RouteParams {
     int *topk_ids;
     float *topk_weights;
     int *counters; // [chunks], then one
+    int *tickets;  // [2], zeroed for the products that follow
     MoeTables tab;
     int ldx, tokens, hidden, experts, top, renorm;
     int up_cols, down_cols; // units per expert and pass
@@ -318,6 +319,8 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const Rout
             up += __shfl_sync(0xffffffffu, u, 31);
             down += __shfl_sync(0xffffffffu, d, 31);
         }
+        if (lane < 2)
+            p.tickets[lane] = 0;
         for (int i = slots + lane; i < p.tab.chunks * 32; i += 32)
             p.tab.experts[i] = make_int4(up, down, 0, off);
     }
@@ -337,7 +340,8 @@ struct MoeGemm {
     float *part;             // down: [pairs][splits][N] fp32
     const uint16_t *residual;
     uint16_t *y;
-    int *counters;           // down: one per 32 columns
+    int *counters;           // down: one per range of columns
+    int *ticket;             // units drawn beyond each team's first two
     MoeTables tab;
     long long expert_words, expert_groups;
     int k, n, steps;         // steps: 128-row steps of K
@@ -433,7 +437,7 @@ struct MoeGeom {
     static constexpr int BLOCKS = 4 / MT; // 64-row blocks per stage: 2 KiB of codes
     static constexpr int SZ = COLS * 2;   // bytes of one scale (or zero) row
     static constexpr int STAGE = 2048 + 2 * BLOCKS * SZ;
-    static constexpr int STAGES = NT == 1 ? 3 : 5;
+    static constexpr int STAGES = 3; // two in flight: at most one step, so at most into the next unit
     static constexpr int RING = STAGES * STAGE;
     static constexpr int vals(bool down) { return MT * NT * (down ? 2 : 4); } // sums per lane to join
     static constexpr int smem(bool down) { return WARPS * (RING + vals(down) * 32 * 4); }
@@ -450,7 +454,7 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
     // registers go to the tiles.
     constexpr bool DUAL = !BF && NT == 1;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int last_sh[G::WARPS];
+    __shared__ int last_sh[G::WARPS], drawn[G::WARPS][2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
     const int teams = G::WARPS / p.team, team = warp / p.team, member = warp - team * p.team;
@@ -470,7 +474,7 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
 
     // --- the copying side: (unit, block) runs ahead of the computing side ----------------------
     // A member takes the 128-row steps member, member + team, ..., each as 2 / BLOCKS stages.
-    int iu = u0, ib = 0, ib_end = 0;
+    int iu = u0, ik = -1, ib = 0, ib_end = 0;
     const int32_t *i_w = nullptr; // this lane's piece of block 0, half 0 of the unit's columns
     const uint16_t *i_s = nullptr; // this lane's part of the expert's scale (or zero) row 0
     // Lane l looks after chunk l % (SZ / 16) of a row; rows: scales of the stage's blocks, then zeros.
@@ -479,24 +483,26 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
     const bool sz_zero = sz_row >= G::BLOCKS;
     const bool sz_mine = sz_row < G::BLOCKS * (p.z ? 2 : 1);
     const int sz_block = sz_zero ? sz_row - G::BLOCKS : sz_row;
-    auto enter = [&]() { // the next unit in which this member has a step
-        for (; iu < units; iu += stride) {
-            const Unit un = find_unit<NT, DOWN>(p, iu, lane);
-            ib = 2 * (un.step0 + member);
-            ib_end = 2 * un.step1;
-            if (ib >= ib_end)
-                continue;
-            const int n0 = un.col * COLS;
-            i_w = p.w + un.expert * p.expert_words + (long long)(n0 >> 7) * p.kblocks * 1024 + (n0 & 127) * 4 + lane * 4;
-            i_s = (sz_zero ? p.z : p.s) + un.expert * p.expert_groups * p.n + n0 + (lane % SZ_CHUNKS) * 8;
+    // The team's k-th unit: the first two follow from its number, the others are drawn from a common
+    // counter two units ahead, so that teams that got on faster do more.
+    auto unit_at = [&](int k) { return k == 0 ? u0 : k == 1 ? u0 + stride : drawn[team][k & 1]; };
+    auto enter = [&]() {
+        iu = unit_at(++ik);
+        if (iu >= units)
             return;
-        }
+        const Unit un = find_unit<NT, DOWN>(p, iu, lane);
+        ib = 2 * (un.step0 + member);
+        ib_end = 2 * un.step1;
+        const int n0 = un.col * COLS;
+        i_w = p.w + un.expert * p.expert_words + (long long)(n0 >> 7) * p.kblocks * 1024 + (n0 & 127) * 4 + lane * 4;
+        i_s = (sz_zero ? p.z : p.s) + un.expert * p.expert_groups * p.n + n0 + (lane % SZ_CHUNKS) * 8;
     };
-    enter();
     // The columns of a half 1 are stored with bit 2 flipped, so that the fragment reads below fall on
     // different banks.
     const uint32_t dst0 = ring + lane * 16, dst1 = ring + (lane ^ 4) * 16;
     auto issue = [&](int stage) {
+        if (iu < units && ib >= ib_end)
+            enter(); // every member has a step of every unit
         if (iu < units) {
             const int32_t *w = i_w + (long long)ib * 1024;
             const uint32_t d0 = dst0 + stage * G::STAGE, d1 = dst1 + stage * G::STAGE;
@@ -519,10 +525,6 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
             ib += G::BLOCKS;
             if (!(ib & 1))
                 ib += 2 * (p.team - 1);
-            if (ib >= ib_end) {
-                iu += stride;
-                enter();
-            }
         }
         cp_async_commit();
     };
@@ -585,7 +587,13 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
     // Half t & 1, column g (bit 2 flipped in half 1), words 2 (t >> 1) and the next.
     const int w_lane = (t & 1) * (COLS * 16) + (g ^ ((t & 1) << 2)) * 16 + (t >> 1) * 8;
     int stage = 0;
-    for (int u = u0; u < units; u += stride) {
+    for (int k = 0;; ++k) {
+        const int u = unit_at(k);
+        if (u >= units)
+            break;
+        int ticket = 0;
+        if (team_tid == 0)
+            ticket = atomicAdd(p.ticket, 1);
         const Unit un = find_unit<NT, DOWN>(p, u, lane);
         const int rows = DOWN ? 2 * un.cols : un.cols; // columns in use on the token side
         float out[MT][NT][4];
@@ -792,6 +800,8 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
                 }
             }
         team_sync(team, team_threads);
+        if (team_tid == 0)
+            drawn[team][k & 1] = 2 * stride + ticket; // unit k + 2, known to the team after the next barrier
         if (DOWN)
             finish();
         const float *tr = red + team * p.team * VALS * 32;
@@ -867,7 +877,7 @@ MoeLayout moe_layout(char *ws, int tokens, int hidden, int inter, int experts, i
     MoeLayout l;
     const int chunks = (tokens + MOE_CHUNK - 1) / MOE_CHUNK, pairs = tokens * top;
     l.counters = HEADER_BYTES;
-    l.logits = round_up(l.counters + 4LL * (chunks + 1 + hidden / MOE_COLS), 256);
+    l.logits = round_up(l.counters + 4LL * (chunks + 3 + hidden / MOE_COLS), 256);
     l.tables = round_up(l.logits + 4LL * tokens * experts, 256);
     long long at = l.tables;
     auto take = [&](long long n) {
@@ -948,10 +958,12 @@ struct MoeSplit {
 
 MoeSplit pick_split(double units, int steps, const MoeShape &s, int num_sms, int max_splits)
 {
-    MoeSplit best = {s.warps, 1};
+    MoeSplit best = {1, 1};
     double least = -1;
     for (int team = s.warps; team >= 1; team /= 2)
         for (int splits = 1; splits <= max_splits && splits <= steps; ++splits) {
+            if (team * splits > steps)
+                continue; // every member has a step
             const int teams = num_sms * s.ctas * (s.warps / team);
             const double rounds = ceil(units * splits / teams - 0.001);
             const int part = (steps + splits - 1) / splits;
@@ -1088,6 +1100,7 @@ extern "C" int w4a16_moe_layer(const void *x, int ldx, const void *router, const
     r.topk_ids = topk_ids;
     r.topk_weights = topk_weights;
     r.counters = counters;
+    r.tickets = counters + chunks + 1;
     r.tab = lay.tab;
     r.ldx = ldx;
     r.tokens = n_tokens;
@@ -1114,7 +1127,8 @@ extern "C" int w4a16_moe_layer(const void *x, int ldx, const void *router, const
     m.part = reinterpret_cast<float *>(ws + lay.part);
     m.residual = static_cast<const uint16_t *>(residual);
     m.y = static_cast<uint16_t *>(y);
-    m.counters = counters + chunks + 1;
+    m.counters = counters + chunks + 3;
+    m.ticket = counters + chunks + 1;
     m.tab = lay.tab;
     m.k = hidden;
     m.n = 2 * inter;
@@ -1142,6 +1156,7 @@ extern "C" int w4a16_moe_layer(const void *x, int ldx, const void *router, const
     m.s = static_cast<const uint16_t *>(down_scales);
     m.z = static_cast<const uint16_t *>(down_zeros);
     m.act = m.h;
+    m.ticket += 1;
     m.k = inter;
     m.n = hidden;
     sizes();
