@@ -485,14 +485,18 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
     const int sz_block = sz_zero ? sz_row - G::BLOCKS : sz_row;
     // The team's k-th unit: the first two follow from its number, the others are drawn from a common
     // counter two units ahead, so that teams that got on faster do more.
-    auto unit_at = [&](int k) { return k == 0 ? u0 : k == 1 ? u0 + stride : drawn[team][k & 1]; };
+    const bool more = units > 2 * stride;
+    auto unit_at = [&](int k) { return k == 0 ? u0 : k == 1 ? u0 + stride : more ? drawn[team][k & 1] : units; };
     auto enter = [&]() {
-        iu = unit_at(++ik);
-        if (iu >= units)
-            return;
-        const Unit un = find_unit<NT, DOWN>(p, iu, lane);
-        ib = 2 * (un.step0 + member);
-        ib_end = 2 * un.step1;
+        Unit un;
+        do { // a member may lack a step only where no unit is drawn (the plan sees to that)
+            iu = unit_at(++ik);
+            if (iu >= units)
+                return;
+            un = find_unit<NT, DOWN>(p, iu, lane);
+            ib = 2 * (un.step0 + member);
+            ib_end = 2 * un.step1;
+        } while (ib >= ib_end);
         const int n0 = un.col * COLS;
         i_w = p.w + un.expert * p.expert_words + (long long)(n0 >> 7) * p.kblocks * 1024 + (n0 & 127) * 4 + lane * 4;
         i_s = (sz_zero ? p.z : p.s) + un.expert * p.expert_groups * p.n + n0 + (lane % SZ_CHUNKS) * 8;
@@ -502,7 +506,7 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
     const uint32_t dst0 = ring + lane * 16, dst1 = ring + (lane ^ 4) * 16;
     auto issue = [&](int stage) {
         if (iu < units && ib >= ib_end)
-            enter(); // every member has a step of every unit
+            enter();
         if (iu < units) {
             const int32_t *w = i_w + (long long)ib * 1024;
             const uint32_t d0 = dst0 + stage * G::STAGE, d1 = dst1 + stage * G::STAGE;
@@ -593,7 +597,7 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
             break;
         int ticket = 0;
         if (team_tid == 0)
-            ticket = atomicAdd(p.ticket, 1);
+            ticket = more ? atomicAdd(p.ticket, 1) : 0;
         const Unit un = find_unit<NT, DOWN>(p, u, lane);
         const int rows = DOWN ? 2 * un.cols : un.cols; // columns in use on the token side
         float out[MT][NT][4];
@@ -949,23 +953,24 @@ int token_tiles(double mean, int most)
     return most <= 8 || mean <= 8.5 ? 1 : 2;
 }
 
-// Warps per team and parts of K of a product whose `units` units (expert, pass, columns) have
-// `steps` steps each: the pair with the least time on the busiest warp, counting the end of a unit
+// Warps per team and parts of K of a product whose `units` units (expert, pass, columns; at most
+// `most`) have `steps` steps each: the pair with the least time on the busiest warp, counting the end of a unit
 // (joining the team's sums, storing) as two steps.
 struct MoeSplit {
     int team, splits;
 };
 
-MoeSplit pick_split(double units, int steps, const MoeShape &s, int num_sms, int max_splits)
+MoeSplit pick_split(double units, int most, int steps, const MoeShape &s, int num_sms, int max_splits)
 {
     MoeSplit best = {1, 1};
     double least = -1;
     for (int team = s.warps; team >= 1; team /= 2)
         for (int splits = 1; splits <= max_splits && splits <= steps; ++splits) {
-            if (team * splits > steps)
-                continue; // every member has a step
             const int teams = num_sms * s.ctas * (s.warps / team);
-            const double rounds = ceil(units * splits / teams - 0.001);
+            if (team * splits > steps && (long long)most * splits > 2LL * teams)
+                continue; // where units are drawn every member has a step of each
+            const double even = units * splits / teams; // drawn units even out, but for the last
+            const double rounds = even > 4.0 ? even + 1.0 : ceil(even - 0.001);
             const int part = (steps + splits - 1) / splits;
             const double cost = rounds * ((part + team - 1) / team + 2);
             if (least < 0 || cost < least) {
@@ -1006,10 +1011,11 @@ MoePlan moe_plan(int tokens, int hidden, int inter, int experts, int top, int nu
     p.nt_up = token_tiles(mean, tokens);
     p.nt_down = token_tiles(2 * mean, 2 * tokens);
     const MoeShape up = shape_of(p.nt_up), down = shape_of(p.nt_down);
-    p.up = pick_split(expected_passes(tokens, experts, top, 8 * p.nt_up) * (2 * inter / up.cols), hidden / MOE_ROWS,
-                      up, num_sms, 1);
-    p.down = pick_split(expected_passes(tokens, experts, top, 4 * p.nt_down) * (hidden / down.cols),
-                        inter / MOE_ROWS, down, num_sms, max_splits(tokens * top));
+    const int pairs = tokens * top, up_cols = 2 * inter / up.cols, down_cols = hidden / down.cols;
+    p.up = pick_split(expected_passes(tokens, experts, top, 8 * p.nt_up) * up_cols, pairs * up_cols,
+                      hidden / MOE_ROWS, up, num_sms, 1);
+    p.down = pick_split(expected_passes(tokens, experts, top, 4 * p.nt_down) * down_cols, pairs * down_cols,
+                        inter / MOE_ROWS, down, num_sms, max_splits(pairs));
     return p;
 }
 
