@@ -9,6 +9,7 @@ runs in the library's CUDA kernels; there is no CPU path.  If the library has no
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -129,11 +130,10 @@ def library_path() -> str:
 def _ptr(x):
     if x is None:
         return None
-    if isinstance(x, int):
-        return x
-    if isinstance(x, np.ndarray):
-        return x.ctypes.data
-    return x.data_ptr()
+    data_ptr = getattr(x, "data_ptr", None)  # torch tensors first: the calls that count in microseconds
+    if data_ptr is not None:
+        return data_ptr()
+    return x if isinstance(x, int) else x.ctypes.data
 
 
 _current_stream = None
@@ -371,6 +371,11 @@ def _kv_strides(kv_strides, page_size: int, n_kv_heads: int, head_dim: int):
     return tuple(kv_strides)
 
 
+@functools.lru_cache(maxsize=64)
+def _int32_array(values):
+    return (ctypes.c_int32 * len(values))(*values)
+
+
 def w4a16_rope_append(q, k, v, q_out, k_cache, v_cache, cos_sin, positions, slots, status, n_tokens: int,
                       n_heads: int, n_kv_heads: int, head_dim: int, rot_dim: int, sections, max_pos: int,
                       page_size: int, n_pages: int, flags: int = 0, ldq: int | None = None,
@@ -378,7 +383,7 @@ def w4a16_rope_append(q, k, v, q_out, k_cache, v_cache, cos_sin, positions, slot
                       ld_pos: int | None = None, kv_strides=None, stream=None) -> None:
     """Rotary positions on q and k (axes by `sections`, a sequence of ints), k and v written into
     the paged cache -- see include/w4a16.h.  `status`: device int32 for W4A16_DEV_* bits, or None."""
-    sec = np.ascontiguousarray(sections, dtype=np.int32)
+    sec = _int32_array(tuple(map(int, sections)))
     ps, ts, hs = _kv_strides(kv_strides, page_size, n_kv_heads, head_dim)
     _check("w4a16_rope_append", _lib.w4a16_rope_append(
         _ptr(q), n_heads * head_dim if ldq is None else ldq,
@@ -386,8 +391,8 @@ def w4a16_rope_append(q, k, v, q_out, k_cache, v_cache, cos_sin, positions, slot
         _ptr(v), n_kv_heads * head_dim if ldv is None else ldv,
         _ptr(q_out), n_heads * head_dim if ldqo is None else ldqo, _ptr(k_cache), _ptr(v_cache), ps, ts, hs,
         _ptr(cos_sin), max_pos, _ptr(positions), n_tokens if ld_pos is None else ld_pos, _ptr(slots),
-        _ptr(status), n_tokens, n_heads, n_kv_heads, head_dim, rot_dim, sec.ctypes.data, sec.size, page_size,
-        n_pages, flags, _stream(stream)))
+        _ptr(status), n_tokens, n_heads, n_kv_heads, head_dim, rot_dim, sec, len(sec), page_size, n_pages,
+        flags, _stream(stream)))
 
 
 def w4a16_paged_attention_workspace_size(batch: int, n_heads: int, n_kv_heads: int, head_dim: int,
