@@ -8,10 +8,11 @@
 // Bound by memory: every live key and value row is read once, 4 head_dim bytes for 4 group
 // head_dim flops, far below the tensor rate.  So the design is about keeping copies in flight on
 // every SM whatever the lengths are:
-//   - The work is cut into units of 64 positions of one (sequence, KV head, head tile), numbered in
-//     that order, and block c of G takes the units [c U / G, (c + 1) U / G).  Lengths are read on
-//     the device, so no host copy of them is needed, ragged batches balance to one unit, and one
-//     long sequence spreads over the whole GPU.
+//   - The work is cut into units of 64 positions of one row (sequence, KV head, head tile), numbered
+//     in that order with a few numbers skipped before each row for what a row costs by itself, and
+//     block c of G takes the numbers [c U / G, (c + 1) U / G).  Lengths are read on the device, so no
+//     host copy of them is needed, ragged batches balance to one unit, and one long sequence spreads
+//     over the whole GPU.
 //   - A warp runs its own 16 positions of each unit: its own ring of cp.async stages, its own
 //     running maximum, sum and output, so the inner loop has no block-wide barrier.  The rows of a
 //     page may lie anywhere, so a row is copied by its own 16-byte copies; the page number of the
@@ -35,7 +36,6 @@ constexpr int ATT_STEP = 16;                    // positions per warp and step
 constexpr int ATT_UNIT = ATT_WARPS * ATT_STEP;  // positions per work unit
 constexpr int ATT_ROWS = 16;                    // query heads per head tile
 constexpr int ATT_MAX_BATCH = 4096;
-constexpr int ATT_CTAS_PER_SM = 2;
 
 struct AttParams {
     const uint16_t *q, *k, *v;
@@ -66,7 +66,11 @@ template <int D>
 struct AttGeom {
     static constexpr int ROW = D * 2;                  // bytes of a key or value row
     static constexpr int CHUNKS = D / 8;               // 16-byte chunks of a row
-    static constexpr int STAGES = D == 64 ? 6 : 3;
+    static constexpr int STAGES = D == 64 ? 4 : 3;
+    static constexpr int CTAS = D == 64 ? 3 : D == 128 ? 2 : 1; // blocks per SM
+    // What a row costs beside its units, in units: its queries, the start and the end of its copies
+    // and the joining of the warps take about as long as copying 64 KiB.
+    static constexpr int ROW_COST = D == 64 ? 4 : 2;
     static constexpr int STAGE = 2 * ATT_STEP * ROW;   // keys, then values
     static constexpr int WARP = STAGES * STAGE;
     static constexpr int SMEM = ATT_WARPS * WARP;
@@ -75,14 +79,14 @@ struct AttGeom {
 
 // PACK: at most eight heads in a tile.
 template <int D, bool BF, bool PACK>
-__global__ void __launch_bounds__(ATT_THREADS, D == 256 ? 1 : ATT_CTAS_PER_SM)
+__global__ void __launch_bounds__(ATT_THREADS, AttGeom<D>::CTAS)
     paged_attention_kernel(const AttParams p)
 {
     using G = AttGeom<D>;
     constexpr int KS = D / 16; // k steps of the score product
     constexpr int NT = D / 8;  // 8-wide output tiles
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int prefix[ATT_MAX_BATCH + 1]; // units of one (KV head, head tile) before sequence b
+    __shared__ int prefix[ATT_MAX_BATCH + 1]; // numbers of one (KV head, head tile) before sequence b
     __shared__ int warp_sum[ATT_WARPS];
     __shared__ uint32_t live_mask[ATT_WARPS][G::STAGES];
     __shared__ float stat[ATT_WARPS][ATT_ROWS][2];
@@ -102,6 +106,7 @@ __global__ void __launch_bounds__(ATT_THREADS, D == 256 ? 1 : ATT_CTAS_PER_SM)
             int first, len;
             live_range(p, b, first, len);
             n = (len - first + ATT_UNIT - 1) / ATT_UNIT;
+            n += n > 0 ? G::ROW_COST : 0;
         }
         int incl = n;
 #pragma unroll
@@ -158,12 +163,15 @@ __global__ void __launch_bounds__(ATT_THREADS, D == 256 ? 1 : ATT_CTAS_PER_SM)
             else
                 hi = mid - 1;
         }
-        const int b = lo, seq_units = prefix[b + 1] - prefix[b];
+        const int b = lo, span = prefix[b + 1] - prefix[b], seq_units = span - G::ROW_COST;
         const long long rem = u - (long long)prefix[b] * rows_per_seq;
-        const int row = (int)(rem / seq_units);             // (KV head, head tile)
-        const int unit0 = (int)(rem - (long long)row * seq_units);
-        const long long row_u0 = u - unit0;
-        const int unit1 = (int)min((long long)seq_units, unit0 + (u_end - u));
+        const int row = (int)(rem / span);                  // (KV head, head tile)
+        const long long row_u0 = u - (rem - (long long)row * span) + G::ROW_COST; // of unit 0
+        const int unit0 = (int)max(0LL, u - row_u0);
+        const int unit1 = (int)min((long long)seq_units, u_end - row_u0);
+        u = row_u0 + seq_units; // the row after this one
+        if (unit1 <= unit0)
+            break; // the range ends before the row's first unit
         const int c = row / p.tiles, h0 = (row - c * p.tiles) * ATT_ROWS;
         const int nh = min(ATT_ROWS, p.group - h0); // heads of this tile
         int first, len;
@@ -171,22 +179,6 @@ __global__ void __launch_bounds__(ATT_THREADS, D == 256 ? 1 : ATT_CTAS_PER_SM)
         const int steps = unit1 - unit0;
         const int pos0 = first + unit0 * ATT_UNIT + warp * ATT_STEP; // this warp's first position
 
-        // --- queries: A fragments of the score product ----------------------------------------
-        uint32_t qa[KS][PACK ? 2 : 4];
-        {
-            const uint16_t *qp = p.q + (long long)b * p.ldq + (long long)(c * p.group + h0) * D;
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                const uint16_t *r0 = qp + (long long)g * D + ks * 16 + 2 * t;
-                qa[ks][0] = g < nh ? *reinterpret_cast<const uint32_t *>(r0) : 0u;
-                qa[ks][1] = g < nh ? *reinterpret_cast<const uint32_t *>(r0 + 8) : 0u;
-                if (!PACK) {
-                    const uint16_t *r1 = r0 + 8 * D;
-                    qa[ks][2] = g + 8 < nh ? *reinterpret_cast<const uint32_t *>(r1) : 0u;
-                    qa[ks][3] = g + 8 < nh ? *reinterpret_cast<const uint32_t *>(r1 + 8) : 0u;
-                }
-            }
-        }
         float o[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -228,15 +220,33 @@ __global__ void __launch_bounds__(ATT_THREADS, D == 256 ? 1 : ATT_CTAS_PER_SM)
                 cp_async16(vst + dst, p.v + ro + ch * 8, live);
             }
         };
-        int next_page = fetch_page(0);
+        int pages[G::STAGES];
+#pragma unroll
+        for (int s = 0; s < G::STAGES; ++s)
+            pages[s] = fetch_page(s);
 #pragma unroll
         for (int s = 0; s < G::STAGES - 1; ++s) {
-            const int pg = next_page;
-            next_page = fetch_page(s + 1);
-            issue(s, s, pg);
+            issue(s, s, pages[s]);
             cp_async_commit();
         }
+        int next_page = pages[G::STAGES - 1];
 
+        // --- queries: A fragments of the score product ----------------------------------------
+        uint32_t qa[KS][PACK ? 2 : 4];
+        {
+            const uint16_t *qp = p.q + (long long)b * p.ldq + (long long)(c * p.group + h0) * D;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                const uint16_t *r0 = qp + (long long)g * D + ks * 16 + 2 * t;
+                qa[ks][0] = g < nh ? *reinterpret_cast<const uint32_t *>(r0) : 0u;
+                qa[ks][1] = g < nh ? *reinterpret_cast<const uint32_t *>(r0 + 8) : 0u;
+                if (!PACK) {
+                    const uint16_t *r1 = r0 + 8 * D;
+                    qa[ks][2] = g + 8 < nh ? *reinterpret_cast<const uint32_t *>(r1) : 0u;
+                    qa[ks][3] = g + 8 < nh ? *reinterpret_cast<const uint32_t *>(r1 + 8) : 0u;
+                }
+            }
+        }
         // --- the running softmax --------------------------------------------------------------
         int stage = 0;
         for (int step = 0; step < steps; ++step) {
@@ -410,38 +420,69 @@ __global__ void __launch_bounds__(ATT_THREADS, D == 256 ? 1 : ATT_CTAS_PER_SM)
             }
             __syncthreads();
             if (is_last) {
+                // Maxima and sums of all parts first, all loads at once; then each output's weighted
+                // sum in block order, eight loads at a time.
                 const long long lo_begin = (long long)c_lo * units / grid;
-                const int lo_slot = lo_begin >= row_u0 ? 0 : 1;
+                const int lo_slot = lo_begin >= row_u0 ? 0 : 1, parts = c_hi - c_lo + 1;
+                float2 *ml = reinterpret_cast<float2 *>(smem); // [part][head]
+                auto part_of = [&](int i) {
+                    return p.partials + ((long long)(c_lo + i) * 2 + (i == 0 ? lo_slot : 0)) * G::SLOT;
+                };
+                for (int i = tid; i < parts * nh; i += ATT_THREADS) {
+                    const int part_i = i / nh, h = i - part_i * nh;
+                    ml[i] = __ldcg(reinterpret_cast<const float2 *>(part_of(part_i) + ATT_ROWS * D + 2 * h));
+                }
+                __syncthreads();
+                for (int h = warp; h < nh; h += ATT_WARPS) {
+                    float m = -INFINITY, l = 0.f;
+                    for (int i = lane; i < parts; i += 32)
+                        m = fmaxf(m, ml[i * nh + h].x);
+#pragma unroll
+                    for (int d = 16; d; d >>= 1)
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+                    const float base = m == -INFINITY ? 0.f : m;
+                    for (int i = lane; i < parts; i += 32) {
+                        const float2 v = ml[i * nh + h];
+                        const float f = exp2f(v.x - base);
+                        l += f * v.y;
+                        ml[i * nh + h].x = f;
+                    }
+#pragma unroll
+                    for (int d = 16; d; d >>= 1)
+                        l += __shfl_xor_sync(0xffffffffu, l, d);
+                    if (lane == 0) {
+                        stat[0][h][0] = l == 0.f ? 0.f : 1.f / l;
+                        if (p.lse)
+                            p.lse[lse_at + h] = l == 0.f ? -INFINITY : (base + log2f(l)) * 0.6931471805599453f;
+                    }
+                }
+                __syncthreads();
                 for (int i = tid; i < nh * (D / 4); i += ATT_THREADS) {
                     const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
-                    float m = -INFINITY, l = 0.f;
                     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int cb = c_lo; cb <= c_hi; ++cb) {
-                        const float *pp =
-                            p.partials + ((long long)cb * 2 + (cb == c_lo ? lo_slot : 0)) * G::SLOT;
-                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(pp + ATT_ROWS * D + 2 * h));
-                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(pp + h * D + d));
-                        const float mn = fmaxf(m, ml.x);
-                        const float base = mn == -INFINITY ? 0.f : mn;
-                        const float fa = exp2f(m - base), fb = exp2f(ml.x - base);
-                        m = mn;
-                        l = l * fa + ml.y * fb;
-                        sum.x = sum.x * fa + x.x * fb;
-                        sum.y = sum.y * fa + x.y * fb;
-                        sum.z = sum.z * fa + x.z * fb;
-                        sum.w = sum.w * fa + x.w * fb;
+                    for (int q0 = 0; q0 < parts; q0 += 8) {
+                        float4 x[8];
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            x[q] = q0 + q < parts ? __ldcg(reinterpret_cast<const float4 *>(part_of(q0 + q) + h * D + d))
+                                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const float f = q0 + q < parts ? ml[(q0 + q) * nh + h].x : 0.f;
+                            sum.x = fmaf(f, x[q].x, sum.x);
+                            sum.y = fmaf(f, x[q].y, sum.y);
+                            sum.z = fmaf(f, x[q].z, sum.z);
+                            sum.w = fmaf(f, x[q].w, sum.w);
+                        }
                     }
-                    const float r = l == 0.f ? 0.f : 1.f / l;
+                    const float r = stat[0][h][0];
                     uint2 w2;
                     w2.x = pack2<BF>(sum.x * r, sum.y * r);
                     w2.y = pack2<BF>(sum.z * r, sum.w * r);
                     *reinterpret_cast<uint2 *>(out + (long long)h * D + d) = w2;
-                    if (d == 0 && p.lse)
-                        p.lse[lse_at + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
                 }
             }
         }
-        u += steps;
         if (u < u_end)
             __syncthreads(); // the ring and the statistics are read before the next segment fills them
     }
@@ -470,7 +511,7 @@ struct AttLayout {
 
 int att_grid(int num_sms, int head_dim)
 {
-    return num_sms * (head_dim == 256 ? 1 : ATT_CTAS_PER_SM);
+    return num_sms * (head_dim == 64 ? AttGeom<64>::CTAS : head_dim == 128 ? AttGeom<128>::CTAS : AttGeom<256>::CTAS);
 }
 
 AttLayout att_layout(int batch, int rows_per_seq, int head_dim, int grid)
@@ -544,7 +585,7 @@ extern "C" int w4a16_paged_attention(const void *q, int ldq, const void *k_cache
     // at most max_pages pages.
     const long long max_len = (long long)max_pages * page_size;
     if (max_len > 0x7FFFFFFFLL - 64 * ATT_UNIT ||
-        (max_len + ATT_UNIT - 1) / ATT_UNIT * batch > 0x7FFFFFFFLL)
+        ((max_len + ATT_UNIT - 1) / ATT_UNIT + 4) * batch > 0x7FFFFFFFLL)
         return status_of(STAGE_ARG, W4A16_ARG_OVERFLOW);
 
     int num_sms = 0;
