@@ -62,15 +62,21 @@ __device__ __forceinline__ void live_range(const AttParams &p, int b, int &first
     first = p.window > 0 && len > p.window ? len - p.window : 0;
 }
 
+// a / b for 0 <= a < 2^31 b: in 32 bits where both fit (64-bit division is a long sequence).
+__device__ __forceinline__ int quotient(long long a, long long b, bool small)
+{
+    return small ? (int)((uint32_t)a / (uint32_t)b) : (int)(a / b);
+}
+
 template <int D>
 struct AttGeom {
     static constexpr int ROW = D * 2;                  // bytes of a key or value row
     static constexpr int CHUNKS = D / 8;               // 16-byte chunks of a row
-    static constexpr int STAGES = D == 64 ? 4 : 3;
+    static constexpr int STAGES = 3;
     static constexpr int CTAS = D == 64 ? 3 : D == 128 ? 2 : 1; // blocks per SM
     // What a row costs beside its units, in units: its queries, the start and the end of its copies
-    // and the joining of the warps take about as long as copying 64 KiB.
-    static constexpr int ROW_COST = D == 64 ? 4 : 2;
+    // and the joining of the warps take about as long as copying 128 KiB.
+    static constexpr int ROW_COST = D == 64 ? 8 : 4;
     static constexpr int STAGE = 2 * ATT_STEP * ROW;   // keys, then values
     static constexpr int WARP = STAGES * STAGE;
     static constexpr int SMEM = ATT_WARPS * WARP;
@@ -149,8 +155,12 @@ __global__ void __launch_bounds__(ATT_THREADS, AttGeom<D>::CTAS)
     if ((int)blockIdx.x >= grid)
         return;
 
-    const long long u_begin = (long long)blockIdx.x * units / grid;
-    const long long u_end = (long long)(blockIdx.x + 1) * units / grid;
+    const bool small = units * (grid + 1LL) < (1LL << 32);
+    auto begin_of = [&](int c) {
+        return small ? (long long)((uint32_t)(c * (uint32_t)units) / (uint32_t)grid) : c * units / grid;
+    };
+    auto owner_of = [&](long long number) { return quotient((number + 1) * grid - 1, units, small); };
+    const long long u_begin = begin_of(blockIdx.x), u_end = begin_of(blockIdx.x + 1);
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * G::WARP;
 
     for (long long u = u_begin; u < u_end;) {
@@ -165,7 +175,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttGeom<D>::CTAS)
         }
         const int b = lo, span = prefix[b + 1] - prefix[b], seq_units = span - G::ROW_COST;
         const long long rem = u - (long long)prefix[b] * rows_per_seq;
-        const int row = (int)(rem / span);                  // (KV head, head tile)
+        const int row = quotient(rem, span, small);         // (KV head, head tile)
         const long long row_u0 = u - (rem - (long long)row * span) + G::ROW_COST; // of unit 0
         const int unit0 = (int)max(0LL, u - row_u0);
         const int unit1 = (int)min((long long)seq_units, u_end - row_u0);
@@ -224,12 +234,6 @@ __global__ void __launch_bounds__(ATT_THREADS, AttGeom<D>::CTAS)
 #pragma unroll
         for (int s = 0; s < G::STAGES; ++s)
             pages[s] = fetch_page(s);
-#pragma unroll
-        for (int s = 0; s < G::STAGES - 1; ++s) {
-            issue(s, s, pages[s]);
-            cp_async_commit();
-        }
-        int next_page = pages[G::STAGES - 1];
 
         // --- queries: A fragments of the score product ----------------------------------------
         uint32_t qa[KS][PACK ? 2 : 4];
@@ -247,6 +251,14 @@ __global__ void __launch_bounds__(ATT_THREADS, AttGeom<D>::CTAS)
                 }
             }
         }
+
+#pragma unroll
+        for (int s = 0; s < G::STAGES - 1; ++s) {
+            issue(s, s, pages[s]);
+            cp_async_commit();
+        }
+        int next_page = pages[G::STAGES - 1];
+
         // --- the running softmax --------------------------------------------------------------
         int stage = 0;
         for (int step = 0; step < steps; ++step) {
@@ -408,8 +420,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttGeom<D>::CTAS)
         if (!whole) {
             // Blocks that share this row: those of its first and its last unit and all between.
             const long long row_u1 = row_u0 + seq_units;
-            const int c_lo = (int)(((row_u0 + 1) * grid - 1) / units);
-            const int c_hi = (int)((row_u1 * grid - 1) / units);
+            const int c_lo = owner_of(row_u0), c_hi = owner_of(row_u1 - 1);
             __syncthreads();
             int *counter = p.counters + (long long)b * rows_per_seq + row;
             if (tid == 0) {
@@ -421,9 +432,8 @@ __global__ void __launch_bounds__(ATT_THREADS, AttGeom<D>::CTAS)
             __syncthreads();
             if (is_last) {
                 // Maxima and sums of all parts first, all loads at once; then each output's weighted
-                // sum in block order, eight loads at a time.
-                const long long lo_begin = (long long)c_lo * units / grid;
-                const int lo_slot = lo_begin >= row_u0 ? 0 : 1, parts = c_hi - c_lo + 1;
+                // sum in block order, sixteen loads at a time.
+                const int lo_slot = begin_of(c_lo) >= row_u0 ? 0 : 1, parts = c_hi - c_lo + 1;
                 float2 *ml = reinterpret_cast<float2 *>(smem); // [part][head]
                 auto part_of = [&](int i) {
                     return p.partials + ((long long)(c_lo + i) * 2 + (i == 0 ? lo_slot : 0)) * G::SLOT;
@@ -460,14 +470,14 @@ __global__ void __launch_bounds__(ATT_THREADS, AttGeom<D>::CTAS)
                 for (int i = tid; i < nh * (D / 4); i += ATT_THREADS) {
                     const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
                     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int q0 = 0; q0 < parts; q0 += 8) {
-                        float4 x[8];
+                    for (int q0 = 0; q0 < parts; q0 += 16) {
+                        float4 x[16];
 #pragma unroll
-                        for (int q = 0; q < 8; ++q)
+                        for (int q = 0; q < 16; ++q)
                             x[q] = q0 + q < parts ? __ldcg(reinterpret_cast<const float4 *>(part_of(q0 + q) + h * D + d))
                                                   : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) {
+                        for (int q = 0; q < 16; ++q) {
                             const float f = q0 + q < parts ? ml[(q0 + q) * nh + h].x : 0.f;
                             sum.x = fmaf(f, x[q].x, sum.x);
                             sum.y = fmaf(f, x[q].y, sum.y);
