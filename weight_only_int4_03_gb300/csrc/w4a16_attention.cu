@@ -431,65 +431,55 @@ __global__ void __launch_bounds__(ATT_THREADS, AttGeom<D>::CTAS)
             }
             __syncthreads();
             if (is_last) {
-                // Maxima and sums of all parts first, all loads at once; then each output's weighted
-                // sum in block order, sixteen loads at a time.
+                // A thread sums a quad of outputs over the parts in block order, the loads of sixteen
+                // parts in flight at once, rescaling as the maximum moves.
                 const int lo_slot = begin_of(c_lo) >= row_u0 ? 0 : 1, parts = c_hi - c_lo + 1;
-                float2 *ml = reinterpret_cast<float2 *>(smem); // [part][head]
-                auto part_of = [&](int i) {
-                    return p.partials + ((long long)(c_lo + i) * 2 + (i == 0 ? lo_slot : 0)) * G::SLOT;
-                };
-                for (int i = tid; i < parts * nh; i += ATT_THREADS) {
-                    const int part_i = i / nh, h = i - part_i * nh;
-                    ml[i] = __ldcg(reinterpret_cast<const float2 *>(part_of(part_i) + ATT_ROWS * D + 2 * h));
-                }
-                __syncthreads();
-                for (int h = warp; h < nh; h += ATT_WARPS) {
-                    float m = -INFINITY, l = 0.f;
-                    for (int i = lane; i < parts; i += 32)
-                        m = fmaxf(m, ml[i * nh + h].x);
-#pragma unroll
-                    for (int d = 16; d; d >>= 1)
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-                    const float base = m == -INFINITY ? 0.f : m;
-                    for (int i = lane; i < parts; i += 32) {
-                        const float2 v = ml[i * nh + h];
-                        const float f = exp2f(v.x - base);
-                        l += f * v.y;
-                        ml[i * nh + h].x = f;
-                    }
-#pragma unroll
-                    for (int d = 16; d; d >>= 1)
-                        l += __shfl_xor_sync(0xffffffffu, l, d);
-                    if (lane == 0) {
-                        stat[0][h][0] = l == 0.f ? 0.f : 1.f / l;
-                        if (p.lse)
-                            p.lse[lse_at + h] = l == 0.f ? -INFINITY : (base + log2f(l)) * 0.6931471805599453f;
-                    }
-                }
-                __syncthreads();
+                constexpr int AT_ONCE = 16;
                 for (int i = tid; i < nh * (D / 4); i += ATT_THREADS) {
-                    const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
+                    const int h = i / (D / 4);
+                    float m = -INFINITY, l = 0.f;
                     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int q0 = 0; q0 < parts; q0 += 16) {
-                        float4 x[16];
+                    for (int q0 = 0; q0 < parts; q0 += AT_ONCE) {
+                        float2 ml[AT_ONCE];
+                        float4 x[AT_ONCE];
 #pragma unroll
-                        for (int q = 0; q < 16; ++q)
-                            x[q] = q0 + q < parts ? __ldcg(reinterpret_cast<const float4 *>(part_of(q0 + q) + h * D + d))
-                                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+                        for (int q = 0; q < AT_ONCE; ++q) {
+                            const bool in = q0 + q < parts;
+                            const float *pp =
+                                p.partials + ((long long)(c_lo + q0 + q) * 2 + (q0 + q == 0 ? lo_slot : 0)) * G::SLOT;
+                            ml[q] = in ? __ldcg(reinterpret_cast<const float2 *>(pp + ATT_ROWS * D + 2 * h))
+                                       : make_float2(-INFINITY, 0.f);
+                            x[q] = in ? __ldcg(reinterpret_cast<const float4 *>(pp + 4 * i)) // quad i: row h's part of it
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+                        }
+                        float mn = m;
 #pragma unroll
-                        for (int q = 0; q < 16; ++q) {
-                            const float f = q0 + q < parts ? ml[(q0 + q) * nh + h].x : 0.f;
+                        for (int q = 0; q < AT_ONCE; ++q)
+                            mn = fmaxf(mn, ml[q].x);
+                        const float base = mn == -INFINITY ? 0.f : mn, f0 = exp2f(m - base);
+                        m = mn;
+                        l *= f0;
+                        sum.x *= f0;
+                        sum.y *= f0;
+                        sum.z *= f0;
+                        sum.w *= f0;
+#pragma unroll
+                        for (int q = 0; q < AT_ONCE; ++q) {
+                            const float f = exp2f(ml[q].x - base);
+                            l = fmaf(f, ml[q].y, l);
                             sum.x = fmaf(f, x[q].x, sum.x);
                             sum.y = fmaf(f, x[q].y, sum.y);
                             sum.z = fmaf(f, x[q].z, sum.z);
                             sum.w = fmaf(f, x[q].w, sum.w);
                         }
                     }
-                    const float r = stat[0][h][0];
+                    const float r = l == 0.f ? 0.f : 1.f / l;
                     uint2 w2;
                     w2.x = pack2<BF>(sum.x * r, sum.y * r);
                     w2.y = pack2<BF>(sum.z * r, sum.w * r);
-                    *reinterpret_cast<uint2 *>(out + (long long)h * D + d) = w2;
+                    *reinterpret_cast<uint2 *>(out + 4LL * i) = w2;
+                    if (p.lse && i % (D / 4) == 0)
+                        p.lse[lse_at + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
                 }
             }
         }
