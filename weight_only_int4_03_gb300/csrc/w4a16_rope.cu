@@ -7,17 +7,19 @@
 // The rest of a head is copied.  Two fp32 products and one fp32 sum per value, rounded once.
 //
 // Bound by memory: each value of q, k and v is read once and written once, with one row of the
-// table per token and axis.  A thread keeps the cosines and sines of eight pairs in registers and
-// applies them to HEADS heads of its token, so the table is read once for HEADS x 16 values and
-// there are 2 x HEADS 16-byte loads in flight per thread.
+// table per token and axis.  A thread looks after eight pairs of ROPE_HEADS heads: it keeps their
+// cosines and sines in registers for both heads and walks over tokens, with the next token's values,
+// position and slot on their way while it works on one, so that only the table's load waits for
+// another (the position's).
 #include "w4a16_ops.cuh"
 
 namespace w4 {
 namespace ops {
 
 constexpr int ROPE_MAX_AXES = 4;
-constexpr int ROPE_HEADS = 4;     // heads per thread (16-byte path)
+constexpr int ROPE_HEADS = 2;     // heads per thread (16-byte path)
 constexpr int ROPE_THREADS = 128; // threads a block is filled up to
+constexpr int ROPE_PER_SM = 768;  // threads per SM that a launch asks for and the registers allow
 
 struct RopeParams {
     const uint16_t *q, *k, *v;
@@ -39,14 +41,18 @@ __device__ __forceinline__ void report(const RopeParams &p, int bit)
         atomicOr(p.status, bit);
 }
 
-// Position of pair `pair`'s axis, or -1 after reporting one outside the table.
-__device__ __forceinline__ int position_of(const RopeParams &p, int token, int pair)
+__device__ __forceinline__ int axis_of(const RopeParams &p, int pair)
 {
     int axis = 0;
 #pragma unroll
     for (int a = 0; a < ROPE_MAX_AXES - 1; ++a)
         axis += (a < p.axes - 1 && pair >= p.cut[a]) ? 1 : 0;
-    const int pos = p.positions[(long long)axis * p.ld_pos + token];
+    return axis;
+}
+
+// A position inside the table, or -1 after reporting it.
+__device__ __forceinline__ int checked_position(const RopeParams &p, int pos)
+{
     if (pos < 0 || pos >= p.max_pos) {
         report(p, W4A16_DEV_POSITION);
         return -1;
@@ -54,112 +60,129 @@ __device__ __forceinline__ int position_of(const RopeParams &p, int token, int p
     return pos;
 }
 
-// Element offset of a token's cache row (head 0), or -1: a negative slot (not cached) or, after
-// reporting it, one past the cache.
-__device__ __forceinline__ long long cache_row(const RopeParams &p, int token)
+__device__ __forceinline__ int position_of(const RopeParams &p, int token, int pair)
 {
-    const long long slot = p.kv > 0 ? p.slots[token] : -1;
+    return checked_position(p, p.positions[(long long)axis_of(p, pair) * p.ld_pos + token]);
+}
+
+// Element offset of a slot's cache row (head 0), or -1: a negative slot (not cached) or, after
+// reporting it, one past the cache.
+__device__ __forceinline__ long long cache_row(const RopeParams &p, long long slot)
+{
     if (slot < 0)
         return -1;
     if (slot >= p.total_slots) {
         report(p, W4A16_DEV_SLOT);
         return -1;
     }
-    const long long pg = slot / p.page;
+    const long long pg = p.total_slots < (1LL << 31) ? (long long)((uint32_t)slot / (uint32_t)p.page) : slot / p.page;
     return pg * p.page_stride + (slot - pg * p.page) * p.token_stride;
 }
 
-// Source and destination of head h of the joint list (q heads, k heads, v heads); dst null: the
-// head is not written.
-__device__ __forceinline__ void head_ptrs(const RopeParams &p, int token, int h, long long row,
-                                          const uint16_t *&src, uint16_t *&dst)
+// Head h of the joint list (q heads, k heads, v heads): where it is read.
+__device__ __forceinline__ const uint16_t *head_src(const RopeParams &p, int token, int h)
 {
-    if (h < p.heads) {
-        src = p.q + (long long)token * p.ldq + (long long)h * p.dim;
-        dst = p.q_out + (long long)token * p.ldqo + (long long)h * p.dim;
-        return;
-    }
-    const int kh = h - p.heads;
-    const bool is_k = kh < p.kv;
-    const int c = is_k ? kh : kh - p.kv;
-    src = is_k ? p.k + (long long)token * p.ldk + (long long)c * p.dim
-               : p.v + (long long)token * p.ldv + (long long)c * p.dim;
-    dst = row < 0 ? nullptr : (is_k ? p.k_cache : p.v_cache) + row + c * p.head_stride;
+    if (h < p.heads)
+        return p.q + (long long)token * p.ldq + (long long)h * p.dim;
+    const int c = h - p.heads;
+    return c < p.kv ? p.k + (long long)token * p.ldk + (long long)c * p.dim
+                    : p.v + (long long)token * p.ldv + (long long)(c - p.kv) * p.dim;
 }
 
-// 16-byte path: rows, strides and cache 16-byte aligned, dim and rot multiples of 16.  Thread
-// (chunk j, head group) of a token: chunk j < rot / 16 is eight pairs, a later one 16 values that
-// are copied.
-template <bool BF>
-__global__ void __launch_bounds__(256) rope_vec_kernel(const RopeParams p, int chunks, int groups)
+// ... and where it is written (null: nowhere).
+__device__ __forceinline__ uint16_t *head_dst(const RopeParams &p, int token, int h, long long row)
+{
+    if (h < p.heads)
+        return p.q_out + (long long)token * p.ldqo + (long long)h * p.dim;
+    const int c = h - p.heads;
+    if (row < 0)
+        return nullptr;
+    return c < p.kv ? p.k_cache + row + c * p.head_stride : p.v_cache + row + (c - p.kv) * p.head_stride;
+}
+
+// 16-byte path: rows, strides and cache 16-byte aligned, dim and rot multiples of 16.  Item (chunk
+// j, head group g) of a thread: chunk j < rot / 16 is eight pairs, a later one 16 values that are
+// copied.  CUTS: some section ends inside a chunk, whose pairs are then looked up one by one.
+template <bool BF, bool CUTS>
+__global__ void __launch_bounds__(256, ROPE_PER_SM / 256) rope_vec_kernel(const RopeParams p, int chunks, int items)
 {
     pdl_wait();
     pdl_launch_dependents();
-    const int token = blockIdx.x * blockDim.y + threadIdx.y;
-    if (token >= p.tokens)
+    const int item = blockIdx.y * blockDim.x + threadIdx.x;
+    const int stride = gridDim.x * blockDim.y;
+    int token = blockIdx.x * blockDim.y + threadIdx.y;
+    if (item >= items || token >= p.tokens)
         return;
-    const int all = p.heads + 2 * p.kv, half = p.rot / 2, turned = p.rot / 16;
-    const long long row = cache_row(p, token);
-    for (int item = threadIdx.x; item < chunks * groups; item += blockDim.x) {
-        const int g = item / chunks, j = item - g * chunks;
-        // Values of the two 16-byte pieces: pairs (i, half + i), or 16 values in a row.
-        const bool pairs = j < turned;
-        const int at0 = pairs && !p.adjacent ? 8 * j : 16 * j;
-        const int at1 = pairs && !p.adjacent ? half + 8 * j : 16 * j + 8;
+    const int all = p.heads + 2 * p.kv, half = p.rot / 2;
+    const int g = item / chunks, j = item - g * chunks, h0 = g * ROPE_HEADS;
+    // Values of the two 16-byte pieces: pairs (i, half + i), or 16 values in a row.
+    const bool pairs = j < p.rot / 16 && h0 < all - p.kv;
+    const bool halves = j < p.rot / 16 && !p.adjacent;
+    const int at0 = halves ? 8 * j : 16 * j, at1 = halves ? half + 8 * j : 16 * j + 8;
+    const bool cached = h0 + ROPE_HEADS > p.heads;
+    const int32_t *positions = p.positions + (long long)axis_of(p, 8 * j) * p.ld_pos;
+    const bool cuts = CUTS && pairs && axis_of(p, 8 * j) != axis_of(p, 8 * j + 7);
+
+    int next_pos = 0;
+    long long next_slot = -1;
+    uint4 n0[ROPE_HEADS], n1[ROPE_HEADS];
+    auto fetch = [&](int t) {
+#pragma unroll
+        for (int n = 0; n < ROPE_HEADS; ++n)
+            if (h0 + n < all) {
+                const uint16_t *src = head_src(p, t, h0 + n);
+                n0[n] = *reinterpret_cast<const uint4 *>(src + at0);
+                n1[n] = *reinterpret_cast<const uint4 *>(src + at1);
+            }
+        if (pairs)
+            next_pos = positions[t];
+        if (cached)
+            next_slot = p.slots[t];
+    };
+    fetch(token);
+    for (;;) {
+        uint4 x0[ROPE_HEADS], x1[ROPE_HEADS];
+#pragma unroll
+        for (int n = 0; n < ROPE_HEADS; ++n) {
+            x0[n] = n0[n];
+            x1[n] = n1[n];
+        }
+        const int t = token, pos = pairs ? checked_position(p, next_pos) : 0;
+        const long long row = cached ? cache_row(p, next_slot) : -1;
+        bool known = pos >= 0;
         float c[8], s[8];
-        bool known = true;
-        if (pairs) {
-            // A section may end inside the chunk; one lookup serves the pairs up to its end.
-            int pos = position_of(p, token, 8 * j), last = position_of(p, token, 8 * j + 7);
-            known = pos >= 0 && last >= 0;
-            if (known) {
+        if (pairs && known) {
+            const float *entry = p.table + (long long)pos * p.rot + 8 * j;
 #pragma unroll
-                for (int i = 0; i < 8; i += 4) {
-                    *reinterpret_cast<float4 *>(c + i) =
-                        *reinterpret_cast<const float4 *>(p.table + (long long)pos * p.rot + 8 * j + i);
-                    *reinterpret_cast<float4 *>(s + i) =
-                        *reinterpret_cast<const float4 *>(p.table + (long long)pos * p.rot + half + 8 * j + i);
-                }
-                bool cuts = false;
+            for (int i = 0; i < 8; i += 4) {
+                *reinterpret_cast<float4 *>(c + i) = *reinterpret_cast<const float4 *>(entry + i);
+                *reinterpret_cast<float4 *>(s + i) = *reinterpret_cast<const float4 *>(entry + half + i);
+            }
+            if (cuts) {
 #pragma unroll
-                for (int a = 0; a < ROPE_MAX_AXES - 1; ++a)
-                    cuts |= a < p.axes - 1 && p.cut[a] > 8 * j && p.cut[a] < 8 * j + 8;
-                if (cuts) {
-#pragma unroll
-                    for (int i = 1; i < 8; ++i) {
-                        const int pi = position_of(p, token, 8 * j + i);
-                        if (pi < 0) {
-                            known = false;
-                        } else {
-                            c[i] = p.table[(long long)pi * p.rot + 8 * j + i];
-                            s[i] = p.table[(long long)pi * p.rot + half + 8 * j + i];
-                        }
+                for (int i = 1; i < 8; ++i) {
+                    const int pi = position_of(p, t, 8 * j + i);
+                    if (pi < 0) {
+                        known = false;
+                    } else {
+                        c[i] = p.table[(long long)pi * p.rot + 8 * j + i];
+                        s[i] = p.table[(long long)pi * p.rot + half + 8 * j + i];
                     }
                 }
             }
         }
-        const uint16_t *src[ROPE_HEADS];
-        uint16_t *dst[ROPE_HEADS];
-        uint4 x0[ROPE_HEADS], x1[ROPE_HEADS];
+        token += stride;
+        const bool more = token < p.tokens;
+        if (more)
+            fetch(token);
 #pragma unroll
         for (int n = 0; n < ROPE_HEADS; ++n) {
-            const int h = g * ROPE_HEADS + n;
-            dst[n] = nullptr;
-            if (h < all)
-                head_ptrs(p, token, h, row, src[n], dst[n]);
-            if (h < all - p.kv && !known)
-                dst[n] = nullptr; // values without a position are not written
-            if (dst[n]) {
-                x0[n] = *reinterpret_cast<const uint4 *>(src[n] + at0);
-                x1[n] = *reinterpret_cast<const uint4 *>(src[n] + at1);
-            }
-        }
-#pragma unroll
-        for (int n = 0; n < ROPE_HEADS; ++n) {
-            if (!dst[n])
+            const int h = h0 + n;
+            const bool turn = pairs && h < all - p.kv;
+            uint16_t *dst = h < all && (known || !turn) ? head_dst(p, t, h, row) : nullptr;
+            if (!dst)
                 continue;
-            const int h = g * ROPE_HEADS + n;
-            if (pairs && h < all - p.kv) {
+            if (turn) {
                 uint32_t *w0 = reinterpret_cast<uint32_t *>(&x0[n]);
                 uint32_t *w1 = reinterpret_cast<uint32_t *>(&x1[n]);
                 if (p.adjacent) {
@@ -179,9 +202,11 @@ __global__ void __launch_bounds__(256) rope_vec_kernel(const RopeParams p, int c
                     }
                 }
             }
-            *reinterpret_cast<uint4 *>(dst[n] + at0) = x0[n];
-            *reinterpret_cast<uint4 *>(dst[n] + at1) = x1[n];
+            *reinterpret_cast<uint4 *>(dst + at0) = x0[n];
+            *reinterpret_cast<uint4 *>(dst + at1) = x1[n];
         }
+        if (!more)
+            return;
     }
 }
 
@@ -194,12 +219,11 @@ __global__ void __launch_bounds__(256) rope_any_kernel(const RopeParams p)
     const int token = blockIdx.x;
     const int all = p.heads + 2 * p.kv, half = p.rot / 2;
     const int rest = p.dim - p.rot, items = half + (rest + 1) / 2;
-    const long long row = cache_row(p, token);
+    const long long row = p.kv > 0 ? cache_row(p, p.slots[token]) : -1;
     for (long long n = threadIdx.x; n < (long long)items * all; n += blockDim.x) {
         const int h = (int)(n / items), i = (int)(n - (long long)h * items);
-        const uint16_t *src;
-        uint16_t *dst;
-        head_ptrs(p, token, h, row, src, dst);
+        const uint16_t *src = head_src(p, token, h);
+        uint16_t *dst = head_dst(p, token, h, row);
         const bool turn = h < all - p.kv;
         int pos = 0;
         if (turn && i < half)
@@ -316,17 +340,29 @@ extern "C" int w4a16_rope_append(const void *q, int ldq, const void *k, int ldk,
                      aligned(v_cache, 16) && aligned(cos_sin, 16);
     if (vec) {
         const int all = n_heads + 2 * n_kv_heads;
-        const int chunks = head_dim / 16, groups = (all + ROPE_HEADS - 1) / ROPE_HEADS;
-        const long long items = (long long)chunks * groups;
+        const int chunks = head_dim / 16;
+        const long long items = (long long)chunks * ((all + ROPE_HEADS - 1) / ROPE_HEADS);
+        // Blocks of whole tokens up to ROPE_THREADS; wider tokens take blocks of their own side by side.
         const int bx = items < 256 ? (int)items : 256;
+        const long long side = (items + bx - 1) / bx;
+        if (side > 65535)
+            return status_of(STAGE_ARG, W4A16_ARG_OVERFLOW);
         int by = ROPE_THREADS / bx;
-        if (by < 1)
-            by = 1;
-        if (by > n_tokens)
-            by = n_tokens;
-        const dim3 grid((unsigned)((n_tokens + (long long)by - 1) / by)), block(bx, by);
-        return launch_status(bf ? launch_pdl(rope_vec_kernel<true>, grid, block, 0, stream, p, chunks, groups)
-                                : launch_pdl(rope_vec_kernel<false>, grid, block, 0, stream, p, chunks, groups));
+        by = by < 1 ? 1 : by > n_tokens ? n_tokens : by;
+        int num_sms = 0;
+        const cudaError_t err = sm_count(&num_sms);
+        if (err != cudaSuccess)
+            return status_of(STAGE_RESOURCE, err);
+        const long long groups = (n_tokens + (long long)by - 1) / by;
+        long long blocks = (long long)num_sms * (ROPE_PER_SM / (bx * by)) / side;
+        blocks = blocks < 1 ? 1 : blocks > groups ? groups : blocks;
+        const dim3 grid((unsigned)blocks, (unsigned)side), block(bx, by);
+        bool cuts = false;
+        for (int a = 0; a < n_axes - 1; ++a)
+            cuts |= p.cut[a] % 8 != 0;
+        const auto kernel = bf ? (cuts ? rope_vec_kernel<true, true> : rope_vec_kernel<true, false>)
+                               : (cuts ? rope_vec_kernel<false, true> : rope_vec_kernel<false, false>);
+        return launch_status(launch_pdl(kernel, grid, block, 0, stream, p, chunks, (int)items));
     }
     const dim3 grid((unsigned)n_tokens), block(256);
     return launch_status(bf ? launch_pdl(rope_any_kernel<true>, grid, block, 0, stream, p)
