@@ -394,7 +394,7 @@ __device__ __forceinline__ Unit find_unit(const MoeGemm &p, int u, int lane)
 {
     int start = 0, id = 0, off = 0;
     for (int c = 0; c < p.tab.chunks; ++c) {
-        const int4 e = p.tab.experts[c * 32 + lane];
+        const int4 e = __ldcg(p.tab.experts + c * 32 + lane);
         const int first = DOWN ? e.y : e.x;
         const uint32_t before = __ballot_sync(0xffffffffu, first <= u);
         if (before == 0)
@@ -462,15 +462,25 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * G::RING;
     const uint8_t *ring_p = smem + warp * G::RING;
     float *red = reinterpret_cast<float *>(smem + G::WARPS * G::RING); // [warp][VALS][32]
-    pdl_wait();
-    pdl_launch_dependents();
-    const int4 total = p.tab.experts[p.tab.chunks * 32 - 1];
+    // Down: the routing tables are those of the launch before the previous one, which had waited for
+    // everything older and was complete before the previous one read them; so the first copies of the
+    // weights, which only they decide, go out while the gate-up launch drains.  The tables are read
+    // past L1, which may hold lines of an earlier call.
+    if (!DOWN) {
+        pdl_wait();
+        pdl_launch_dependents();
+    }
+    const int4 total = __ldcg(p.tab.experts + p.tab.chunks * 32 - 1);
     const int units = DOWN ? total.y : total.x;
     // Consecutive units go to different blocks, so that a part round still reaches every SM.
     const int stride = gridDim.x * teams;
     const int u0 = team * gridDim.x + blockIdx.x;
-    if (u0 >= units)
-        return; // the whole team leaves; the other teams of the block have barriers of their own
+    if (u0 >= units) {
+        // The whole team leaves; the other teams of the block have barriers of their own.
+        if (DOWN)
+            pdl_wait();
+        return;
+    }
 
     // --- the copying side: (unit, block) runs ahead of the computing side ----------------------
     // A member takes the 128-row steps member, member + team, ..., each as 2 / BLOCKS stages.
@@ -535,6 +545,10 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s)
         issue(s);
+    if (DOWN) {
+        pdl_wait();
+        pdl_launch_dependents();
+    }
 
     // The team that arrives last at its columns adds the residual there: on its way into L2 meanwhile.
     if (DOWN && p.residual) {
