@@ -82,15 +82,85 @@ struct RouteParams {
     MoeTables tab;
     int ldx, tokens, hidden, experts, top, renorm;
     int up_cols, down_cols; // units per expert and pass
-    int up_pass, down_pass; // pairs per pass
+    int up_shift, down_shift; // log2 of the pairs per pass
 };
+
+// A score as an unsigned number of the same order; a NaN counts as the lowest, so that top_k distinct
+// experts come out whatever x holds.  0 is below every key.
+__device__ __forceinline__ uint32_t score_key(float l)
+{
+    if (l != l)
+        return 1u;
+    const uint32_t bits = __float_as_uint(l == 0.f ? 0.f : l); // -0 and 0 are equal
+    return bits & 0x80000000u ? ~bits : bits | 0x80000000u;    // -inf is 0x007FFFFF
+}
+
+__device__ __forceinline__ float key_score(uint32_t key)
+{
+    return key == 1u ? NAN : __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+
+// The top_k experts of one token by a warp, PER scores a lane: lane j gets the j-th one and its
+// weight.
+template <int PER>
+__device__ __forceinline__ void choose_experts(const float *scores, int experts, int top_k, int renorm,
+                                               int lane, int &at_out, float &w_out)
+{
+    float l[PER];
+    uint32_t key[PER], most = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        l[i] = i * 32 + lane < experts ? __ldcg(scores + i * 32 + lane) : -INFINITY;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        key[i] = i * 32 + lane < experts ? score_key(l[i]) : 0u;
+        most = max(most, key[i]);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    const float top = most == 1u ? -INFINITY : key_score(most);
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        sum += i * 32 + lane < experts ? expf(l[i] - top) : 0.f;
+#pragma unroll
+    for (int d = 16; d; d >>= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    uint32_t mine = 0;
+    at_out = 0;
+    for (int j = 0; j < top_k; ++j) {
+        uint32_t best = key[0];
+        int at = lane;
+#pragma unroll
+        for (int i = 1; i < PER; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                at = i * 32 + lane;
+            }
+        most = __reduce_max_sync(0xffffffffu, best);
+        at = (int)__reduce_min_sync(0xffffffffu, best == most ? (uint32_t)at : 0xffffffffu);
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            key[i] = at == i * 32 + lane ? 0u : key[i];
+        if (lane == j) {
+            mine = most;
+            at_out = at;
+        }
+    }
+    const float w = lane < top_k ? expf(key_score(mine) - top) / sum : 0.f;
+    float chosen = w;
+#pragma unroll
+    for (int d = 16; d; d >>= 1)
+        chosen += __shfl_xor_sync(0xffffffffu, chosen, d);
+    w_out = renorm ? w / chosen : w;
+}
 
 template <bool BF>
 __global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const RouteParams p)
 {
     __shared__ int is_last;
     __shared__ float partial[MOE_WARPS][MOE_CHUNK];
-    __shared__ int ids[MOE_MAX_PAIRS], rank[MOE_MAX_PAIRS];
+    __shared__ __align__(16) int ids[MOE_MAX_PAIRS];
+    __shared__ int rank[MOE_MAX_PAIRS];
     __shared__ int count[MOE_MAX_EXPERTS], off_of[MOE_MAX_EXPERTS];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_wait();
@@ -172,82 +242,24 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const Rout
     const int pairs = p.tokens * p.top;
     const bool one_chunk = gridDim.y == 1;
     if (warp < nt) {
-        const int t = t0 + warp;
-        constexpr int PER = MOE_MAX_EXPERTS / 32;
-        // Scores as unsigned numbers of the same order; a NaN counts as the lowest, so that top_k
-        // distinct experts come out whatever x holds.  0: none left in this place.
-        uint32_t key[PER];
-        float sum = 0.f, top = 0.f;
-        {
-            float l[PER];
-            uint32_t most = 0;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                key[i] = 0;
-                if (i * 32 >= p.experts)
-                    break;
-                const int idx = i * 32 + lane;
-                l[i] = idx < p.experts ? __ldcg(p.logits + (long long)t * p.experts + idx) : -INFINITY;
-                const uint32_t bits = __float_as_uint(l[i] == 0.f ? 0.f : l[i]); // -0 and 0 are equal
-                if (idx < p.experts)
-                    key[i] = l[i] != l[i] ? 1u : max(2u, bits & 0x80000000u ? ~bits : bits | 0x80000000u);
-                most = max(most, key[i]);
-            }
-            most = __reduce_max_sync(0xffffffffu, most);
-            top = most <= 2u ? -INFINITY : __uint_as_float(most & 0x80000000u ? most & 0x7fffffffu : ~most);
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                if (i * 32 >= p.experts)
-                    break;
-                if (i * 32 + lane < p.experts)
-                    sum += expf(l[i] - top);
-            }
-#pragma unroll
-            for (int d = 16; d; d >>= 1)
-                sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        }
-        float chosen = 0.f, mine = 0.f; // lane j keeps the j-th choice
-        int mine_at = 0;
-        for (int j = 0; j < p.top; ++j) {
-            uint32_t best = 0;
-            int at = MOE_MAX_EXPERTS;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                if (i * 32 >= p.experts)
-                    break;
-                if (key[i] > best) {
-                    best = key[i];
-                    at = i * 32 + lane;
-                }
-            }
-            const uint32_t most = __reduce_max_sync(0xffffffffu, best);
-            at = (int)__reduce_min_sync(0xffffffffu, (uint32_t)(best == most ? at : MOE_MAX_EXPERTS));
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                if (i * 32 >= p.experts)
-                    break;
-                if (at == i * 32 + lane)
-                    key[i] = 0;
-            }
-            const float score = most <= 2u ? (most == 1u ? NAN : -INFINITY)
-                                           : __uint_as_float(most & 0x80000000u ? most & 0x7fffffffu : ~most);
-            const float w = expf(score - top) / sum;
-            chosen += w;
-            if (lane == j) {
-                mine = w;
-                mine_at = at;
-            }
-        }
+        int at;
+        float w;
+        const float *l = p.logits + (long long)(t0 + warp) * p.experts;
+        if (p.experts <= 32)
+            choose_experts<1>(l, p.experts, p.top, p.renorm, lane, at, w);
+        else if (p.experts <= 128)
+            choose_experts<4>(l, p.experts, p.top, p.renorm, lane, at, w);
+        else
+            choose_experts<MOE_MAX_EXPERTS / 32>(l, p.experts, p.top, p.renorm, lane, at, w);
         if (lane < p.top) {
-            const float w = p.renorm ? mine / chosen : mine;
-            const int pair = t * p.top + lane;
+            const int pair = (t0 + warp) * p.top + lane;
             p.tab.weights[pair] = w;
             if (one_chunk)
-                ids[pair] = mine_at;
+                ids[pair] = at;
             else
-                __stcg(p.tab.ids + pair, mine_at);
+                __stcg(p.tab.ids + pair, at);
             if (p.topk_ids)
-                p.topk_ids[pair] = mine_at;
+                p.topk_ids[pair] = at;
             if (p.topk_weights)
                 p.topk_weights[pair] = w;
         }
@@ -269,60 +281,57 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const Rout
     }
 
     // --- pairs by expert ----------------------------------------------------------------------
-    // One warp walks the pairs in order: a pair's place among its expert's is the count so far plus
-    // its rank among the equal ones of its 32.
+    // A pair's place among its expert's is the number of equal ids before it.
     for (int x = tid; x < p.experts; x += MOE_THREADS)
         count[x] = 0;
+    for (int i = pairs + tid; i < (pairs + 3) / 4 * 4; i += MOE_THREADS)
+        ids[i] = -1;
+    __syncthreads();
+    for (int i = tid; i < pairs; i += MOE_THREADS) {
+        const int x = ids[i];
+        int before = 0;
+#pragma unroll 4
+        for (int q = 0; q * 4 < i; ++q) {
+            const int4 v = reinterpret_cast<const int4 *>(ids)[q];
+            before += (v.x == x && q * 4 < i) + (v.y == x && q * 4 + 1 < i) + (v.z == x && q * 4 + 2 < i) +
+                      (v.w == x && q * 4 + 3 < i);
+        }
+        rank[i] = before;
+        atomicAdd(&count[x], 1);
+    }
     __syncthreads();
     if (warp == 0) {
-        for (int base = 0; base < pairs; base += 32) {
-            const int i = base + lane;
-            const int x = i < pairs ? ids[i] : -1 - lane;
-            const uint32_t same = __match_any_sync(0xffffffffu, x);
-            const int below = __popc(same & ((1u << lane) - 1u));
-            const int before = i < pairs ? count[x] : 0;
-            __syncwarp();
-            if (i < pairs) {
-                rank[i] = before + below;
-                if (below == 0)
-                    count[x] = before + __popc(same);
-            }
-            __syncwarp();
-        }
-    }
-    if (warp == 0) {
-        int slots = 0, off = 0, up = 0, down = 0;
+        // Running sums in 16-bit halves: active experts and pairs; gate-up and down passes.  None
+        // passes 1024.
+        uint32_t list = 0, passes = 0;
         for (int base = 0; base < p.experts; base += 32) {
-            const int x = base + lane;
-            const int n = x < p.experts ? count[x] : 0;
-            const int has = n > 0 ? 1 : 0;
-            const int nu = (n + p.up_pass - 1) / p.up_pass * p.up_cols;
-            const int nd = (n + p.down_pass - 1) / p.down_pass * p.down_cols;
-            int s = has, o = n, u = nu, d = nd;
+            const int x = base + lane, n = x < p.experts ? count[x] : 0;
+            const uint32_t a = n > 0 ? 1u | (uint32_t)n << 16 : 0u;
+            const uint32_t b = (uint32_t)((n + (1 << p.up_shift) - 1) >> p.up_shift) |
+                               (uint32_t)((n + (1 << p.down_shift) - 1) >> p.down_shift) << 16;
+            uint32_t s = a, u = b;
 #pragma unroll
             for (int q = 1; q < 32; q <<= 1) {
-                const int s2 = __shfl_up_sync(0xffffffffu, s, q), o2 = __shfl_up_sync(0xffffffffu, o, q);
-                const int u2 = __shfl_up_sync(0xffffffffu, u, q), d2 = __shfl_up_sync(0xffffffffu, d, q);
+                const uint32_t s2 = __shfl_up_sync(0xffffffffu, s, q), u2 = __shfl_up_sync(0xffffffffu, u, q);
                 if (lane >= q) {
                     s += s2;
-                    o += o2;
                     u += u2;
-                    d += d2;
                 }
             }
-            if (has)
-                p.tab.experts[slots + s - 1] = make_int4(up + u - nu, down + d - nd, x | n << 16, off + o - n);
+            const uint32_t s0 = list + s - a, u0 = passes + u - b; // before this expert
+            if (n > 0)
+                p.tab.experts[s0 & 0xFFFF] = make_int4((int)(u0 & 0xFFFF) * p.up_cols, (int)(u0 >> 16) * p.down_cols,
+                                                       x | n << 16, (int)(s0 >> 16));
             if (x < p.experts)
-                off_of[x] = off + o - n;
-            slots += __shfl_sync(0xffffffffu, s, 31);
-            off += __shfl_sync(0xffffffffu, o, 31);
-            up += __shfl_sync(0xffffffffu, u, 31);
-            down += __shfl_sync(0xffffffffu, d, 31);
+                off_of[x] = (int)(s0 >> 16);
+            list += __shfl_sync(0xffffffffu, s, 31);
+            passes += __shfl_sync(0xffffffffu, u, 31);
         }
         if (lane < 2)
             p.tickets[lane] = 0;
-        for (int i = slots + lane; i < p.tab.chunks * 32; i += 32)
-            p.tab.experts[i] = make_int4(up, down, 0, off);
+        for (int i = (int)(list & 0xFFFF) + lane; i < p.tab.chunks * 32; i += 32)
+            p.tab.experts[i] = make_int4((int)(passes & 0xFFFF) * p.up_cols, (int)(passes >> 16) * p.down_cols, 0,
+                                         (int)(list >> 16));
     }
     __syncthreads();
     for (int i = tid; i < pairs; i += MOE_THREADS) {
@@ -342,6 +351,7 @@ struct MoeGemm {
     uint16_t *y;
     int *counters;           // down: one per range of columns
     int *ticket;             // units drawn beyond each team's first two
+    int *status;
     MoeTables tab;
     long long expert_words, expert_groups;
     int k, n, steps;         // steps: 128-row steps of K
@@ -496,6 +506,14 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
     // The team's k-th unit: the first two follow from its number, the others are drawn from a common
     // counter two units ahead, so that teams that got on faster do more.
     const bool more = units > 2 * stride;
+    if (more && p.team * p.splits > p.steps) {
+        // A member without a step would run ahead of the drawn units; the plan never comes to this.
+        if (team_tid == 0)
+            atomicOr(p.status, W4A16_DEV_SCHEDULE);
+        if (DOWN)
+            pdl_wait();
+        return;
+    }
     auto unit_at = [&](int k) { return k == 0 ? u0 : k == 1 ? u0 + stride : more ? drawn[team][k & 1] : units; };
     auto enter = [&]() {
         Unit un;
@@ -1130,8 +1148,8 @@ extern "C" int w4a16_moe_layer(const void *x, int ldx, const void *router, const
     r.renorm = (flags & W4A16_FLAG_MOE_RENORM) ? 1 : 0;
     r.up_cols = 2 * inter / shape_of(plan.nt_up).cols;
     r.down_cols = hidden / shape_of(plan.nt_down).cols * plan.down.splits;
-    r.up_pass = 8 * plan.nt_up;
-    r.down_pass = 4 * plan.nt_down;
+    r.up_shift = plan.nt_up == 1 ? 3 : 4;
+    r.down_shift = plan.nt_down == 1 ? 2 : 3;
     const dim3 grid(n_experts, chunks);
     err = bf ? launch_pdl(moe_layer_route_kernel<true>, grid, dim3(MOE_THREADS), 0, stream, r)
              : launch_pdl(moe_layer_route_kernel<false>, grid, dim3(MOE_THREADS), 0, stream, r);
@@ -1149,6 +1167,7 @@ extern "C" int w4a16_moe_layer(const void *x, int ldx, const void *router, const
     m.y = static_cast<uint16_t *>(y);
     m.counters = counters + chunks + 3;
     m.ticket = counters + chunks + 1;
+    m.status = reinterpret_cast<int *>(ws);
     m.tab = lay.tab;
     m.k = hidden;
     m.n = 2 * inter;
