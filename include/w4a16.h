@@ -499,7 +499,7 @@ size_t w4a16_moe_layer_workspace_size(int n_tokens, int hidden, int inter, int n
  *                  W4A16_TYPE_U4 only, with W4A16_FLAG_HAS_ZP, as for w4a16_gemm
  *   y              device 16-bit [n_tokens][ldy]; may be residual or x itself (same leading dimension)
  *   topk_ids, topk_weights  device int32 / fp32 [n_tokens][top_k] or NULL: the routing, written
- *   n_tokens       0 (a no-op) .. 64;  hidden % 256 == 0;  inter % 128 == 0
+ *   n_tokens       0 (a no-op) .. 64;  hidden % 256 == 0;  inter % 128 == 0;  both at most 65536
  *   n_experts      1 .. 512;  top_k 1 .. 16, at most n_experts
  *   group_size     -1, or a positive multiple of 64 that divides hidden and inter
  *   flags          exactly one of W4A16_FLAG_SWIGLU / _GEGLU; W4A16_FLAG_BF16, _HAS_ZP, _MOE_RENORM,

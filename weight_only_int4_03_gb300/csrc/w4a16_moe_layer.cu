@@ -944,7 +944,7 @@ int check_layer_sizes(int tokens, int hidden, int inter, int experts, int top)
         return status_of(STAGE_UNSUPPORTED, W4A16_ARG_SHAPE);
     if (experts > MOE_MAX_EXPERTS || top > MOE_MAX_TOP)
         return status_of(STAGE_UNSUPPORTED, W4A16_ARG_SCHEDULE);
-    if ((long long)experts * hidden * inter / 4 > (1LL << 40) || hidden > (1 << 20) || inter > (1 << 20))
+    if ((long long)experts * hidden * inter / 4 > (1LL << 40) || hidden > (1 << 16) || inter > (1 << 16))
         return status_of(STAGE_ARG, W4A16_ARG_OVERFLOW);
     return 0;
 }
@@ -1064,8 +1064,8 @@ cudaError_t launch_moe_gemm(MoeGemm &p, int nt, MoeSplit split, bool bf, bool do
     p.team = split.team;
     p.splits = split.splits;
     p.col_units = p.n / s.cols;
-    // Exact while n col_units < 2^32: local unit numbers are below 64 passes x 8 splits x col_units
-    // and col_units is at most 2^16.
+    // Exact while n col_units < 2^32: an expert's unit numbers are below 16 passes x 8 splits x
+    // col_units, and col_units is at most 2^11.
     p.col_magic = (uint32_t)((1ull << 32) / p.col_units + 1);
     return launch_pdl(kernel, dim3(num_sms * s.ctas), dim3(s.warps * 32), (size_t)smem, stream, p);
 }
