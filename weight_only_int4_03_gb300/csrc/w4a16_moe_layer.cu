@@ -43,6 +43,7 @@ constexpr int MOE_MAX_PAIRS = MOE_MAX_TOKENS * MOE_MAX_TOP;
 constexpr int MOE_WARPS = 8; // of a routing block
 constexpr int MOE_THREADS = MOE_WARPS * 32;
 constexpr int MOE_CHUNK = 4;   // tokens per routing block
+constexpr double MOE_SIDE_MEAN = 3.0; // pairs per expert up to which a down tile holds both parts of four pairs
 constexpr int MOE_COLS = 32;   // fewest weight columns per unit
 constexpr int MOE_ROWS = 128;  // weight rows per step (two 64-row blocks)
 constexpr float CODE_UNIT = 5.9604644775390625e-8f; // 2^-24: the fp16 value of the bits 1
@@ -391,6 +392,16 @@ __device__ __forceinline__ void team_sync(int team_id, int threads)
         asm volatile("bar.sync %0, %1;" ::"r"(team_id + 1), "r"(threads) : "memory");
 }
 
+// What a launch computes: the gated products; the down products with a pair's value and remainder
+// in two columns of the MMA (up to four pairs a tile, in one MMA); or with both in one column, one
+// after the other (up to eight pairs a tile, in two MMAs on the same weights).
+enum MoeMode { GATE_UP = 0, DOWN_SIDE = 1, DOWN_TWICE = 2 };
+
+__host__ __device__ constexpr int pairs_per_pass(int nt, int mode)
+{
+    return (mode == DOWN_SIDE ? 4 : 8) * nt;
+}
+
 // One unit of a team: an expert, a pass over its pairs, a range of columns and of 128-row steps.
 struct Unit {
     int expert, col, first, cols; // first pair (in `sorted`), pairs of this pass
@@ -399,13 +410,13 @@ struct Unit {
 
 // Unit u (the same in every lane): its expert is the last of the list whose first unit is at or
 // before u, looked up by the warp's lanes together.
-template <int NT, bool DOWN>
+template <int NT, int MODE>
 __device__ __forceinline__ Unit find_unit(const MoeGemm &p, int u, int lane)
 {
     int start = 0, id = 0, off = 0;
     for (int c = 0; c < p.tab.chunks; ++c) {
         const int4 e = __ldcg(p.tab.experts + c * 32 + lane);
-        const int first = DOWN ? e.y : e.x;
+        const int first = MODE != GATE_UP ? e.y : e.x;
         const uint32_t before = __ballot_sync(0xffffffffu, first <= u);
         if (before == 0)
             break;
@@ -416,7 +427,7 @@ __device__ __forceinline__ Unit find_unit(const MoeGemm &p, int u, int lane)
         if (before != 0xffffffffu)
             break;
     }
-    constexpr int PASS = DOWN ? 4 * NT : 8 * NT; // a pair takes two columns of the down MMA
+    constexpr int PASS = pairs_per_pass(NT, MODE);
     const int local = u - start, part = (int)__umulhi((uint32_t)local, p.col_magic);
     Unit r;
     r.expert = id & 0xFFFF;
@@ -425,7 +436,7 @@ __device__ __forceinline__ Unit find_unit(const MoeGemm &p, int u, int lane)
     r.split = 0;
     r.step0 = 0;
     r.step1 = p.steps;
-    if (DOWN && p.splits > 1) {
+    if (MODE != GATE_UP && p.splits > 1) {
         pass = part / p.splits;
         r.split = part - pass * p.splits;
         r.step0 = r.split * p.steps / p.splits;
@@ -449,16 +460,17 @@ struct MoeGeom {
     static constexpr int STAGE = 2048 + 2 * BLOCKS * SZ;
     static constexpr int STAGES = 3; // two in flight: at most one step, so at most into the next unit
     static constexpr int RING = STAGES * STAGE;
-    static constexpr int vals(bool down) { return MT * NT * (down ? 2 : 4); } // sums per lane to join
-    static constexpr int smem(bool down) { return WARPS * (RING + vals(down) * 32 * 4); }
+    static constexpr int vals(int mode) { return MT * NT * (mode == DOWN_SIDE ? 2 : 4); } // sums per lane to join
+    static constexpr int smem(int mode) { return WARPS * (RING + vals(mode) * 32 * 4); }
 };
 
-// DOWN false: gate-up, true: down.
-template <int NT, bool BF, bool DOWN>
+template <int NT, bool BF, int MODE>
 __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) moe_layer_gemm_kernel(const MoeGemm p)
 {
     using G = MoeGeom<NT>;
-    constexpr int MT = G::MT, COLS = G::COLS, STAGES = G::STAGES, VALS = G::vals(DOWN);
+    constexpr bool DOWN = MODE != GATE_UP;
+    constexpr int PARTS = MODE == DOWN_TWICE ? 2 : 1; // activation rows per column
+    constexpr int MT = G::MT, COLS = G::COLS, STAGES = G::STAGES, VALS = G::vals(MODE);
     // One token tile: the two nibble positions keep accumulators of their own, which gives the MMAs
     // twice as many independent chains and saves fp16 two shifts a word; with more tiles the
     // registers go to the tiles.
@@ -521,7 +533,7 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
             iu = unit_at(++ik);
             if (iu >= units)
                 return;
-            un = find_unit<NT, DOWN>(p, iu, lane);
+            un = find_unit<NT, MODE>(p, iu, lane);
             ib = 2 * (un.step0 + member);
             ib_end = 2 * un.step1;
         } while (ib >= ib_end);
@@ -630,8 +642,8 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
         int ticket = 0;
         if (team_tid == 0)
             ticket = more ? atomicAdd(p.ticket, 1) : 0;
-        const Unit un = find_unit<NT, DOWN>(p, u, lane);
-        const int rows = DOWN ? 2 * un.cols : un.cols; // columns in use on the token side
+        const Unit un = find_unit<NT, MODE>(p, u, lane);
+        const int rows = MODE == DOWN_SIDE ? 2 * un.cols : un.cols; // columns in use on the token side
         float out[MT][NT][4];
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -649,17 +661,19 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
 #pragma unroll
             for (int n = 0; n < ND; ++n) {
                 const int c = min(n * 8 + g, rows - 1);
-                const int row = DOWN ? 2 * un.first + c : p.tab.token[un.first + c];
+                const int row = MODE == GATE_UP     ? p.tab.token[un.first + c]
+                                : MODE == DOWN_SIDE ? 2 * un.first + c
+                                                    : 2 * (un.first + c);
                 arow[n] = p.act + (long long)row * p.k + (un.step0 + member) * MOE_ROWS + t * 8;
             }
             // With one tile the next block's activations are fetched a block ahead.
-            constexpr bool AHEAD = ND == 1;
+            constexpr bool AHEAD = ND == 1 && PARTS == 1;
             const int first = un.step0 + member;
-            uint4 bv[ND][2];
+            uint4 bv[PARTS][ND][2];
             if (AHEAD && first < un.step1) {
                 const uint4 *ap = reinterpret_cast<const uint4 *>(arow[0]);
-                bv[0][0] = ap[0];
-                bv[0][1] = ap[4];
+                bv[0][0][0] = ap[0];
+                bv[0][0][1] = ap[4];
             }
             for (int step = first; step < un.step1; step += p.team) {
                 float lo[MT][ND][4], hi[DUAL ? MT : 1][ND][4], sa[ND][4];
@@ -676,9 +690,12 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
                     } else {
 #pragma unroll
                         for (int n = 0; n < ND; ++n) {
-                            const uint4 *ap = reinterpret_cast<const uint4 *>(arow[n]) + b * 8;
-                            bv[n][0] = ap[0];
-                            bv[n][1] = ap[4];
+#pragma unroll
+                            for (int r = 0; r < PARTS; ++r) { // the remainder's row follows the value's
+                                const uint4 *ap = reinterpret_cast<const uint4 *>(arow[n] + r * p.k) + b * 8;
+                                bv[r][n][0] = ap[0];
+                                bv[r][n][1] = ap[4];
+                            }
                             if (b == 1)
                                 arow[n] += p.team * MOE_ROWS;
                         }
@@ -703,12 +720,14 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
 #pragma unroll
-                        for (int n = 0; n < ND; ++n) {
-                            if (b == 0 && i == 0)
-                                mma16816_zero<BF>(sa[n], ONES, ONES, ONES, ONES, bv[n][i].x, bv[n][i].y);
-                            else
-                                mma16816<BF>(sa[n], ONES, ONES, ONES, ONES, bv[n][i].x, bv[n][i].y);
-                        }
+                        for (int r = 0; r < PARTS; ++r)
+#pragma unroll
+                            for (int n = 0; n < ND; ++n) {
+                                if (b == 0 && i == 0 && r == 0)
+                                    mma16816_zero<BF>(sa[n], ONES, ONES, ONES, ONES, bv[r][n][i].x, bv[r][n][i].y);
+                                else
+                                    mma16816<BF>(sa[n], ONES, ONES, ONES, ONES, bv[r][n][i].x, bv[r][n][i].y);
+                            }
 #pragma unroll
                         for (int m = 0; m < MT; ++m) {
                             const uint32_t x = i ? w[m][0].y : w[m][0].x, y = i ? w[m][1].y : w[m][1].x;
@@ -743,25 +762,32 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
                             }
                             // MMAs on one accumulator are kept apart: each waits for the one before.
 #pragma unroll
-                            for (int n = 0; n < ND; ++n) {
-                                if (b == 0 && i == 0)
-                                    mma16816_zero<BF>(lo[m][n], a0, a1, a2, a3, bv[n][i].x, bv[n][i].y);
-                                else
-                                    mma16816<BF>(lo[m][n], a0, a1, a2, a3, bv[n][i].x, bv[n][i].y);
-                            }
+                            for (int r = 0; r < PARTS; ++r) {
 #pragma unroll
-                            for (int n = 0; n < ND; ++n) {
-                                if (!DUAL)
-                                    mma16816<BF>(lo[m][n], c0, c1, c2, c3, bv[n][i].z, bv[n][i].w);
-                                else if (b == 0 && i == 0)
-                                    mma16816_zero<BF>(hi[m % (DUAL ? MT : 1)][n], c0, c1, c2, c3, bv[n][i].z, bv[n][i].w);
-                                else
-                                    mma16816<BF>(hi[m % (DUAL ? MT : 1)][n], c0, c1, c2, c3, bv[n][i].z, bv[n][i].w);
+                                for (int n = 0; n < ND; ++n) {
+                                    const uint4 v = bv[r][n][i];
+                                    if (b == 0 && i == 0 && r == 0)
+                                        mma16816_zero<BF>(lo[m][n], a0, a1, a2, a3, v.x, v.y);
+                                    else
+                                        mma16816<BF>(lo[m][n], a0, a1, a2, a3, v.x, v.y);
+                                }
+#pragma unroll
+                                for (int n = 0; n < ND; ++n) {
+                                    const uint4 v = bv[r][n][i];
+                                    if (!DUAL)
+                                        mma16816<BF>(lo[m][n], c0, c1, c2, c3, v.z, v.w);
+                                    else if (b == 0 && i == 0 && r == 0)
+                                        mma16816_zero<BF>(hi[m % (DUAL ? MT : 1)][n], c0, c1, c2, c3, v.z, v.w);
+                                    else
+                                        mma16816<BF>(hi[m % (DUAL ? MT : 1)][n], c0, c1, c2, c3, v.z, v.w);
+                                }
                             }
                         }
 #pragma unroll
-                        for (int n = 0; n < ND; ++n)
-                            mma16816<BF>(sa[n], ONES, ONES, ONES, ONES, bv[n][i].z, bv[n][i].w);
+                        for (int r = 0; r < PARTS; ++r)
+#pragma unroll
+                            for (int n = 0; n < ND; ++n)
+                                mma16816<BF>(sa[n], ONES, ONES, ONES, ONES, bv[r][n][i].z, bv[r][n][i].w);
                     }
                     // End of a group (or of a step, whose two blocks then share one): scale the sums.
                     const uint8_t *sz = st + 2048 + (b % G::BLOCKS) * G::SZ;
@@ -808,8 +834,8 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
                             flush(std::false_type(), b == 0);
                     }
                     if (AHEAD) {
-                        bv[0][0] = nx[0];
-                        bv[0][1] = nx[1];
+                        bv[0][0][0] = nx[0];
+                        bv[0][0][1] = nx[1];
                     }
                 }
                 stage = stage + 1 == STAGES ? 0 : stage + 1;
@@ -825,7 +851,7 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                if (DOWN) { // columns 2 t and 2 t + 1 are a pair's value and remainder
+                if (MODE == DOWN_SIDE) { // columns 2 t and 2 t + 1 are a pair's value and remainder
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
                         red[(warp * VALS + (m * NT + n) * 2 + c) * 32 + lane] = out[m][n][2 * c] + out[m][n][2 * c + 1];
@@ -870,7 +896,10 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
             // Item: column c of the unit, pair pr.
             for (int x = team_tid; x < un.cols * COLS; x += team_threads) {
                 const int c = x % COLS, pr = x / COLS;
-                const int ln = (c & 7) * 4 + (pr & 3), v = ((c >> 4) * NT + (pr >> 2)) * 2 + ((c >> 3) & 1);
+                const int half = (c >> 3) & 1;
+                const int ln = (c & 7) * 4 + (MODE == DOWN_SIDE ? pr & 3 : (pr >> 1) & 3);
+                const int v = MODE == DOWN_SIDE ? ((c >> 4) * NT + (pr >> 2)) * 2 + half
+                                                : ((c >> 4) * NT + (pr >> 3)) * 4 + half * 2 + (pr & 1);
                 const int pair = p.tab.sorted[un.first + pr];
                 __stcg(p.part + ((long long)pair * p.splits + un.split) * p.n + un.col * COLS + c, joined(v, ln));
             }
@@ -954,14 +983,14 @@ struct MoeFamily;
 
 // The geometry of a variant, by its number of tiles.
 struct MoeShape {
-    int cols, warps, ctas, smem_up, smem_down;
+    int cols, warps, ctas, smem[3];
 };
 
 template <int NT>
 MoeShape shape()
 {
     using G = MoeGeom<NT>;
-    return {G::COLS, G::WARPS, G::CTAS, G::smem(false), G::smem(true)};
+    return {G::COLS, G::WARPS, G::CTAS, {G::smem(GATE_UP), G::smem(DOWN_SIDE), G::smem(DOWN_TWICE)}};
 }
 
 MoeShape shape_of(int nt)
@@ -969,12 +998,13 @@ MoeShape shape_of(int nt)
     return nt == 1 ? shape<1>() : shape<2>();
 }
 
-template <int NT>
-GemmKernel gemm_kernel(bool bf, bool down)
+template <int NT, bool BF>
+GemmKernel gemm_kernel(int mode)
 {
-    if (bf)
-        return down ? moe_layer_gemm_kernel<NT, true, true> : moe_layer_gemm_kernel<NT, true, false>;
-    return down ? moe_layer_gemm_kernel<NT, false, true> : moe_layer_gemm_kernel<NT, false, false>;
+    if constexpr (NT == 1) // two tiles mean more pairs than DOWN_SIDE is used for
+        if (mode == DOWN_SIDE)
+            return moe_layer_gemm_kernel<NT, BF, DOWN_SIDE>;
+    return mode == GATE_UP ? moe_layer_gemm_kernel<NT, BF, GATE_UP> : moe_layer_gemm_kernel<NT, BF, DOWN_TWICE>;
 }
 
 // 8-column tiles of the token side, by the columns that an expert's pairs take on average and at most:
@@ -1032,7 +1062,7 @@ double expected_passes(int tokens, int experts, int top, int pass)
 }
 
 struct MoePlan {
-    int nt_up, nt_down;
+    int nt_up, nt_down, mode_down;
     MoeSplit up, down;
 };
 
@@ -1041,24 +1071,26 @@ MoePlan moe_plan(int tokens, int hidden, int inter, int experts, int top, int nu
     MoePlan p;
     const double active = expected_passes(tokens, experts, top, tokens), mean = tokens * (double)top / active;
     p.nt_up = token_tiles(mean, tokens);
-    p.nt_down = token_tiles(2 * mean, 2 * tokens);
+    p.mode_down = tokens <= 4 || mean <= MOE_SIDE_MEAN ? DOWN_SIDE : DOWN_TWICE;
+    p.nt_down = p.mode_down == DOWN_SIDE ? 1 : token_tiles(mean, tokens);
     const MoeShape up = shape_of(p.nt_up), down = shape_of(p.nt_down);
     const int pairs = tokens * top, up_cols = 2 * inter / up.cols, down_cols = hidden / down.cols;
-    p.up = pick_split(expected_passes(tokens, experts, top, 8 * p.nt_up) * up_cols, pairs * up_cols,
+    p.up = pick_split(expected_passes(tokens, experts, top, pairs_per_pass(p.nt_up, GATE_UP)) * up_cols, pairs * up_cols,
                       hidden / MOE_ROWS, up, num_sms, 1);
-    p.down = pick_split(expected_passes(tokens, experts, top, 4 * p.nt_down) * down_cols, pairs * down_cols,
+    p.down = pick_split(expected_passes(tokens, experts, top, pairs_per_pass(p.nt_down, p.mode_down)) * down_cols, pairs * down_cols,
                         inter / MOE_ROWS, down, num_sms, max_splits(pairs));
     return p;
 }
 
-cudaError_t launch_moe_gemm(MoeGemm &p, int nt, MoeSplit split, bool bf, bool down, int num_sms,
+cudaError_t launch_moe_gemm(MoeGemm &p, int nt, MoeSplit split, bool bf, int mode, int num_sms,
                             cudaStream_t stream)
 {
-    const GemmKernel kernel = nt == 1 ? gemm_kernel<1>(bf, down) : gemm_kernel<2>(bf, down);
+    const GemmKernel kernel = nt == 1 ? (bf ? gemm_kernel<1, true>(mode) : gemm_kernel<1, false>(mode))
+                                      : (bf ? gemm_kernel<2, true>(mode) : gemm_kernel<2, false>(mode));
     const MoeShape s = shape_of(nt);
-    const int smem = down ? s.smem_down : s.smem_up;
-    const int v = (nt - 1) * 4 + (bf ? 2 : 0) + (down ? 1 : 0);
-    cudaError_t err = allow_smem<MoeFamily, 8>(reinterpret_cast<const void *>(kernel), v, smem);
+    const int smem = s.smem[mode];
+    const int v = (nt - 1) * 6 + (bf ? 3 : 0) + mode;
+    cudaError_t err = allow_smem<MoeFamily, 12>(reinterpret_cast<const void *>(kernel), v, smem);
     if (err != cudaSuccess)
         return err;
     p.team = split.team;
@@ -1149,7 +1181,7 @@ extern "C" int w4a16_moe_layer(const void *x, int ldx, const void *router, const
     r.up_cols = 2 * inter / shape_of(plan.nt_up).cols;
     r.down_cols = hidden / shape_of(plan.nt_down).cols * plan.down.splits;
     r.up_shift = plan.nt_up == 1 ? 3 : 4;
-    r.down_shift = plan.nt_down == 1 ? 2 : 3;
+    r.down_shift = plan.mode_down == DOWN_SIDE ? 2 : plan.nt_down == 1 ? 3 : 4;
     const dim3 grid(n_experts, chunks);
     err = bf ? launch_pdl(moe_layer_route_kernel<true>, grid, dim3(MOE_THREADS), 0, stream, r)
              : launch_pdl(moe_layer_route_kernel<false>, grid, dim3(MOE_THREADS), 0, stream, r);
@@ -1188,7 +1220,7 @@ extern "C" int w4a16_moe_layer(const void *x, int ldx, const void *router, const
         m.expert_groups = m.kblocks / blocks;
     };
     sizes();
-    err = launch_moe_gemm(m, plan.nt_up, plan.up, bf, false, num_sms, stream);
+    err = launch_moe_gemm(m, plan.nt_up, plan.up, bf, GATE_UP, num_sms, stream);
     if (err != cudaSuccess)
         return status_of(STAGE_LAUNCH, err);
     m.w = down;
@@ -1199,5 +1231,5 @@ extern "C" int w4a16_moe_layer(const void *x, int ldx, const void *router, const
     m.k = inter;
     m.n = hidden;
     sizes();
-    return launch_status(launch_moe_gemm(m, plan.nt_down, plan.down, bf, true, num_sms, stream));
+    return launch_status(launch_moe_gemm(m, plan.nt_down, plan.down, bf, plan.mode_down, num_sms, stream));
 }
