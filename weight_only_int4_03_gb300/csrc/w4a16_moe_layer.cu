@@ -43,7 +43,10 @@ constexpr int MOE_MAX_PAIRS = MOE_MAX_TOKENS * MOE_MAX_TOP;
 constexpr int MOE_WARPS = 8; // of a routing block
 constexpr int MOE_THREADS = MOE_WARPS * 32;
 constexpr int MOE_CHUNK = 4;   // tokens per routing block
-constexpr double MOE_SIDE_MEAN = 3.0; // pairs per expert up to which a down tile holds both parts of four pairs
+// Pairs per expert up to which a down tile holds both parts of four pairs side by side (7 tokens on 128
+// experts, 1.2 pairs each: 44.8 us against 46.4 us one after the other; 16 tokens on 8, four each: 175 us
+// against 167 us).
+constexpr double MOE_SIDE_MEAN = 3.0;
 constexpr int MOE_COLS = 32;   // fewest weight columns per unit
 constexpr int MOE_ROWS = 128;  // weight rows per step (two 64-row blocks)
 constexpr float CODE_UNIT = 5.9604644775390625e-8f; // 2^-24: the fp16 value of the bits 1
@@ -998,18 +1001,11 @@ MoeShape shape_of(int nt)
     return nt == 1 ? shape<1>() : shape<2>();
 }
 
-template <int NT, bool BF>
-GemmKernel gemm_kernel(int mode)
-{
-    if constexpr (NT == 1) // two tiles mean more pairs than DOWN_SIDE is used for
-        if (mode == DOWN_SIDE)
-            return moe_layer_gemm_kernel<NT, BF, DOWN_SIDE>;
-    return mode == GATE_UP ? moe_layer_gemm_kernel<NT, BF, GATE_UP> : moe_layer_gemm_kernel<NT, BF, DOWN_TWICE>;
-}
-
-// 8-column tiles of the token side, by the columns that an expert's pairs take on average and at most:
-// one or two.  An expert with more pairs takes further passes over its weights, which then come from
-// L2.
+// 8-column tiles of the gate-up MMA's token side, by the pairs that an expert has on average and at
+// most: one or two.  An expert with more pairs takes further passes over its weights, which then come
+// from L2.  Two tiles leave room for twelve warps per SM instead of sixteen and pay from about eight
+// pairs on (64 tokens on 8 experts of 4096 x 14336, two each: 390 us against 427 us with one tile);
+// the down product, whose tile takes two MMAs, stays at one (390 us against 429 us with two).
 int token_tiles(double mean, int most)
 {
     return most <= 8 || mean <= 8.5 ? 1 : 2;
@@ -1062,7 +1058,7 @@ double expected_passes(int tokens, int experts, int top, int pass)
 }
 
 struct MoePlan {
-    int nt_up, nt_down, mode_down;
+    int nt_up, mode_down;
     MoeSplit up, down;
 };
 
@@ -1072,12 +1068,11 @@ MoePlan moe_plan(int tokens, int hidden, int inter, int experts, int top, int nu
     const double active = expected_passes(tokens, experts, top, tokens), mean = tokens * (double)top / active;
     p.nt_up = token_tiles(mean, tokens);
     p.mode_down = tokens <= 4 || mean <= MOE_SIDE_MEAN ? DOWN_SIDE : DOWN_TWICE;
-    p.nt_down = p.mode_down == DOWN_SIDE ? 1 : token_tiles(mean, tokens);
-    const MoeShape up = shape_of(p.nt_up), down = shape_of(p.nt_down);
+    const MoeShape up = shape_of(p.nt_up), down = shape_of(1);
     const int pairs = tokens * top, up_cols = 2 * inter / up.cols, down_cols = hidden / down.cols;
     p.up = pick_split(expected_passes(tokens, experts, top, pairs_per_pass(p.nt_up, GATE_UP)) * up_cols, pairs * up_cols,
                       hidden / MOE_ROWS, up, num_sms, 1);
-    p.down = pick_split(expected_passes(tokens, experts, top, pairs_per_pass(p.nt_down, p.mode_down)) * down_cols, pairs * down_cols,
+    p.down = pick_split(expected_passes(tokens, experts, top, pairs_per_pass(1, p.mode_down)) * down_cols, pairs * down_cols,
                         inter / MOE_ROWS, down, num_sms, max_splits(pairs));
     return p;
 }
@@ -1085,12 +1080,18 @@ MoePlan moe_plan(int tokens, int hidden, int inter, int experts, int top, int nu
 cudaError_t launch_moe_gemm(MoeGemm &p, int nt, MoeSplit split, bool bf, int mode, int num_sms,
                             cudaStream_t stream)
 {
-    const GemmKernel kernel = nt == 1 ? (bf ? gemm_kernel<1, true>(mode) : gemm_kernel<1, false>(mode))
-                                      : (bf ? gemm_kernel<2, true>(mode) : gemm_kernel<2, false>(mode));
+    // [type][gate-up with two tiles, then the modes with one]
+    static const GemmKernel kernels[2][4] = {
+        {moe_layer_gemm_kernel<2, false, GATE_UP>, moe_layer_gemm_kernel<1, false, GATE_UP>,
+         moe_layer_gemm_kernel<1, false, DOWN_SIDE>, moe_layer_gemm_kernel<1, false, DOWN_TWICE>},
+        {moe_layer_gemm_kernel<2, true, GATE_UP>, moe_layer_gemm_kernel<1, true, GATE_UP>,
+         moe_layer_gemm_kernel<1, true, DOWN_SIDE>, moe_layer_gemm_kernel<1, true, DOWN_TWICE>}};
+    const int which = nt == 2 ? 0 : 1 + mode;
+    const GemmKernel kernel = kernels[bf ? 1 : 0][which];
     const MoeShape s = shape_of(nt);
     const int smem = s.smem[mode];
-    const int v = (nt - 1) * 6 + (bf ? 3 : 0) + mode;
-    cudaError_t err = allow_smem<MoeFamily, 12>(reinterpret_cast<const void *>(kernel), v, smem);
+    const int v = (bf ? 4 : 0) + which;
+    cudaError_t err = allow_smem<MoeFamily, 8>(reinterpret_cast<const void *>(kernel), v, smem);
     if (err != cudaSuccess)
         return err;
     p.team = split.team;
@@ -1179,9 +1180,9 @@ extern "C" int w4a16_moe_layer(const void *x, int ldx, const void *router, const
     r.top = top_k;
     r.renorm = (flags & W4A16_FLAG_MOE_RENORM) ? 1 : 0;
     r.up_cols = 2 * inter / shape_of(plan.nt_up).cols;
-    r.down_cols = hidden / shape_of(plan.nt_down).cols * plan.down.splits;
+    r.down_cols = hidden / shape_of(1).cols * plan.down.splits;
     r.up_shift = plan.nt_up == 1 ? 3 : 4;
-    r.down_shift = plan.mode_down == DOWN_SIDE ? 2 : plan.nt_down == 1 ? 3 : 4;
+    r.down_shift = plan.mode_down == DOWN_SIDE ? 2 : 3;
     const dim3 grid(n_experts, chunks);
     err = bf ? launch_pdl(moe_layer_route_kernel<true>, grid, dim3(MOE_THREADS), 0, stream, r)
              : launch_pdl(moe_layer_route_kernel<false>, grid, dim3(MOE_THREADS), 0, stream, r);
@@ -1231,5 +1232,5 @@ extern "C" int w4a16_moe_layer(const void *x, int ldx, const void *router, const
     m.k = inter;
     m.n = hidden;
     sizes();
-    return launch_status(launch_moe_gemm(m, plan.nt_down, plan.down, bf, plan.mode_down, num_sms, stream));
+    return launch_status(launch_moe_gemm(m, 1, plan.down, bf, plan.mode_down, num_sms, stream));
 }
