@@ -4,11 +4,14 @@
 //     l_e = router[e] . x_t,   P = softmax(l),   the top_k experts e_1 .. e_k of largest l (ties: the
 //     lowest index), weights w_j = P[e_j] (divided by their sum with W4A16_FLAG_MOE_RENORM),
 //     y_t = residual_t + sum_j w_j Wd_{e_j}^T h_j,   h_j = act(Wg_{e_j}^T x_t) * (Wu_{e_j}^T x_t),
-// with W = (q - z) s per group of rows.  Three launches, each starting while the one before drains:
+// with W = (q - z) s per group of rows.  Four launches, each starting while the one before drains:
 //   route    router product, softmax, top-k, and the pairs (token, j) grouped by expert;
 //   gate-up  h for every pair;
-//   down     the pairs' outputs in fp32, and per 32 output columns, by the last block to finish
-//            them, the weighted sum over a token's experts in the order of j.
+//   down     the pairs' outputs in fp32;
+//   combine  the weighted sum over a token's experts in the order of j, and the residual.
+// (Summing in the down launch, by the last team to finish a range of columns, took a fence and an
+// atomic per unit and left T x 64 outputs to one team: 73 us against 51 us for 52 tokens on 8
+// experts of 5120 x 1024.)
 //
 // Bound by memory: each chosen expert's codes are read once for all of its tokens.  What would bound
 // it otherwise is the conversion of the codes, so the weights go into the MMA (m16n8k16, weights as
@@ -23,7 +26,7 @@
 // h keeps fp32's accuracy through the second product as a 16-bit value plus a 16-bit remainder, two
 // columns of the down MMA, whose eight columns are mostly empty for a few tokens.
 //
-// A unit of work is 32 columns of one expert over all of K, done by a team of 1 to 8 warps that take
+// A unit of work is 64 columns of one expert over all of K (down: or a part of it), done by a team of 1 to 8 warps that take
 // its 128-row steps in turn.  A warp streams its steps through its own ring of cp.async stages, which
 // runs on into its next unit, so no block-wide barrier sits between a copy and its use and the ring
 // stays full across units.  Activations are read from L1/L2 in the MMA's fragment order.
@@ -47,7 +50,6 @@ constexpr int MOE_CHUNK = 4;   // tokens per routing block
 // experts, 1.2 pairs each: 44.8 us against 46.4 us one after the other; 16 tokens on 8, four each: 175 us
 // against 167 us).
 constexpr double MOE_SIDE_MEAN = 3.0;
-constexpr int MOE_COLS = 32;   // fewest weight columns per unit
 constexpr int MOE_ROWS = 128;  // weight rows per step (two 64-row blocks)
 constexpr float CODE_UNIT = 5.9604644775390625e-8f; // 2^-24: the fp16 value of the bits 1
 
@@ -351,9 +353,6 @@ struct MoeGemm {
     const uint16_t *act;     // activation rows in fragment order, K values each
     uint16_t *h;             // gate-up: the pairs' h, two rows (value, remainder) per pair
     float *part;             // down: [pairs][splits][N] fp32
-    const uint16_t *residual;
-    uint16_t *y;
-    int *counters;           // down: one per range of columns
     int *ticket;             // units drawn beyond each team's first two
     int *status;
     MoeTables tab;
@@ -366,7 +365,7 @@ struct MoeGemm {
     uint32_t col_magic;      // n / col_units = umulhi(n, col_magic)
     int splits;              // down: parts of K with units and partial outputs of their own
     int team;                // warps per team
-    int tokens, top, inter, ldy, ldr, glu;
+    int inter, glu;
 };
 
 // Gated activations as g sigmoid(x): x = g for silu, 2 sqrt(2/pi) (g + 0.044715 g^3) for gelu_tanh
@@ -479,7 +478,7 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
     // registers go to the tiles.
     constexpr bool DUAL = !BF && NT == 1;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int last_sh[G::WARPS], drawn[G::WARPS][2];
+    __shared__ int drawn[G::WARPS][2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
     const int teams = G::WARPS / p.team, team = warp / p.team, member = warp - team * p.team;
@@ -582,56 +581,6 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
         pdl_wait();
         pdl_launch_dependents();
     }
-
-    // The team that arrives last at its columns adds the residual there: on its way into L2 meanwhile.
-    if (DOWN && p.residual) {
-        const int col = u0 % p.col_units * COLS;
-        for (int tok = team_tid; tok < p.tokens; tok += team_threads)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.residual + (long long)tok * p.ldr + col));
-    }
-    // The output of the columns at which this team arrived last: every expert's part is there.
-    int arrived = -1;
-    auto finish = [&]() {
-        if (arrived < 0 || !last_sh[team])
-            return;
-        for (int x = team_tid; x < p.tokens * (COLS / 4); x += team_threads) {
-            const int tok = x / (COLS / 4), col = arrived * COLS + (x % (COLS / 4)) * 4;
-            // Parts in the order of (j, split), eight loads at a time.
-            const float4 *src = reinterpret_cast<const float4 *>(p.part + (long long)tok * p.top * p.splits * p.n + col);
-            const float *wts = p.tab.weights + tok * p.top;
-            const int parts = p.top * p.splits;
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int q0 = 0; q0 < parts; q0 += 8) {
-                float4 v[8];
-                float wt[8];
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const bool in = q0 + q < parts;
-                    v[q] = in ? __ldcg(src + (long long)(q0 + q) * (p.n / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    wt[q] = in ? wts[p.splits == 1 ? q0 + q : (q0 + q) / p.splits] : 0.f;
-                }
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    a.x = fmaf(wt[q], v[q].x, a.x);
-                    a.y = fmaf(wt[q], v[q].y, a.y);
-                    a.z = fmaf(wt[q], v[q].z, a.z);
-                    a.w = fmaf(wt[q], v[q].w, a.w);
-                }
-            }
-            if (p.residual) {
-                const uint2 rv = *reinterpret_cast<const uint2 *>(p.residual + (long long)tok * p.ldr + col);
-                const float2 r0 = unpack2<BF>(rv.x), r1 = unpack2<BF>(rv.y);
-                a.x += r0.x;
-                a.y += r0.y;
-                a.z += r1.x;
-                a.w += r1.y;
-            }
-            uint2 o;
-            o.x = pack2<BF>(a.x, a.y);
-            o.y = pack2<BF>(a.z, a.w);
-            *reinterpret_cast<uint2 *>(p.y + (long long)tok * p.ldy + col) = o;
-        }
-    };
 
     uint32_t nibble = 0x000F000Fu, base128 = 0x43004300u; // in registers, not known to the compiler
     asm volatile("" : "+r"(nibble), "+r"(base128));
@@ -867,8 +816,6 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
         team_sync(team, team_threads);
         if (team_tid == 0)
             drawn[team][k & 1] = 2 * stride + ticket; // unit k + 2, known to the team after the next barrier
-        if (DOWN)
-            finish();
         const float *tr = red + team * p.team * VALS * 32;
         auto joined = [&](int v, int ln) {
             float s = 0.f;
@@ -907,24 +854,60 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
                 __stcg(p.part + ((long long)pair * p.splits + un.split) * p.n + un.col * COLS + c, joined(v, ln));
             }
         }
-        team_sync(team, team_threads); // `red` is free; the team's stores are done
-        if (DOWN) {
-            // The arrival's answer is looked at after the next unit, so that only one thread waits for it.
-            if (team_tid == 0) {
-                int *counter = p.counters + un.col;
-                const int last = arrive_counter(counter) == units / p.col_units - 1;
-                if (last)
-                    *counter = 0;
-                last_sh[team] = last;
-            }
-            arrived = un.col;
-        }
-    }
-    if (DOWN) {
-        team_sync(team, team_threads);
-        finish();
+        team_sync(team, team_threads); // `red` is free
     }
     cp_async_wait<0>();
+}
+
+struct CombineParams {
+    const float *part; // [pairs][splits][hidden]
+    const float *weights;
+    const uint16_t *residual;
+    uint16_t *y;
+    int tokens, top, splits, hidden, ldy, ldr;
+};
+
+// y_t = residual_t + sum_j w_j (sum over the splits), in the order of j: a thread per quad of
+// columns of a token.  The residual is older than the layer's first launch, so it is fetched (past
+// L1, which may hold a line of an earlier call) before the down product is waited for.
+template <bool BF>
+__global__ void __launch_bounds__(128) moe_layer_combine_kernel(const CombineParams p)
+{
+    const int col = (blockIdx.x * 128 + threadIdx.x) * 4, tok = blockIdx.y;
+    const bool in = col < p.hidden;
+    uint2 rv = make_uint2(0, 0);
+    if (in && p.residual)
+        rv = __ldcg(reinterpret_cast<const uint2 *>(p.residual + (long long)tok * p.ldr + col));
+    pdl_wait();
+    pdl_launch_dependents();
+    if (!in)
+        return;
+    const float4 *src = reinterpret_cast<const float4 *>(p.part + (long long)tok * p.top * p.splits * p.hidden + col);
+    const float *wts = p.weights + tok * p.top;
+    const int parts = p.top * p.splits;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int q0 = 0; q0 < parts; q0 += 8) {
+        float4 v[8];
+        float wt[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const bool live = q0 + q < parts;
+            v[q] = live ? __ldcg(src + (long long)(q0 + q) * (p.hidden / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            wt[q] = live ? __ldcg(wts + (p.splits == 1 ? q0 + q : (q0 + q) / p.splits)) : 0.f;
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            a.x = fmaf(wt[q], v[q].x, a.x);
+            a.y = fmaf(wt[q], v[q].y, a.y);
+            a.z = fmaf(wt[q], v[q].z, a.z);
+            a.w = fmaf(wt[q], v[q].w, a.w);
+        }
+    }
+    const float2 r0 = unpack2<BF>(rv.x), r1 = unpack2<BF>(rv.y);
+    uint2 o;
+    o.x = pack2<BF>(a.x + r0.x, a.y + r0.y);
+    o.y = pack2<BF>(a.z + r1.x, a.w + r1.y);
+    *reinterpret_cast<uint2 *>(p.y + (long long)tok * p.ldy + col) = o;
 }
 
 namespace {
@@ -945,7 +928,7 @@ MoeLayout moe_layout(char *ws, int tokens, int hidden, int inter, int experts, i
     MoeLayout l;
     const int chunks = (tokens + MOE_CHUNK - 1) / MOE_CHUNK, pairs = tokens * top;
     l.counters = HEADER_BYTES;
-    l.logits = round_up(l.counters + 4LL * (chunks + 3 + hidden / MOE_COLS), 256);
+    l.logits = round_up(l.counters + 4LL * (chunks + 3), 256);
     l.tables = round_up(l.logits + 4LL * tokens * experts, 256);
     long long at = l.tables;
     auto take = [&](long long n) {
@@ -1196,19 +1179,12 @@ extern "C" int w4a16_moe_layer(const void *x, int ldx, const void *router, const
     m.act = r.xf;
     m.h = reinterpret_cast<uint16_t *>(ws + lay.h);
     m.part = reinterpret_cast<float *>(ws + lay.part);
-    m.residual = static_cast<const uint16_t *>(residual);
-    m.y = static_cast<uint16_t *>(y);
-    m.counters = counters + chunks + 3;
     m.ticket = counters + chunks + 1;
     m.status = reinterpret_cast<int *>(ws);
     m.tab = lay.tab;
     m.k = hidden;
     m.n = 2 * inter;
-    m.tokens = n_tokens;
-    m.top = top_k;
     m.inter = inter;
-    m.ldy = ldy;
-    m.ldr = ldr;
     m.glu = sw ? 1 : 2;
     auto sizes = [&]() {
         m.expert_words = (long long)m.k * m.n / 8;
@@ -1232,5 +1208,21 @@ extern "C" int w4a16_moe_layer(const void *x, int ldx, const void *router, const
     m.k = inter;
     m.n = hidden;
     sizes();
-    return launch_status(launch_moe_gemm(m, 1, plan.down, bf, plan.mode_down, num_sms, stream));
+    err = launch_moe_gemm(m, 1, plan.down, bf, plan.mode_down, num_sms, stream);
+    if (err != cudaSuccess)
+        return status_of(STAGE_LAUNCH, err);
+    CombineParams c;
+    c.part = m.part;
+    c.weights = lay.tab.weights;
+    c.residual = static_cast<const uint16_t *>(residual);
+    c.y = static_cast<uint16_t *>(y);
+    c.tokens = n_tokens;
+    c.top = top_k;
+    c.splits = plan.down.splits;
+    c.hidden = hidden;
+    c.ldy = ldy;
+    c.ldr = ldr;
+    const dim3 cgrid((hidden / 4 + 127) / 128, n_tokens);
+    return launch_status(bf ? launch_pdl(moe_layer_combine_kernel<true>, cgrid, dim3(128), 0, stream, c)
+                            : launch_pdl(moe_layer_combine_kernel<false>, cgrid, dim3(128), 0, stream, c));
 }

@@ -102,7 +102,7 @@ __device__ __forceinline__ uint16_t *head_dst(const RopeParams &p, int token, in
 
 // 16-byte path: rows, strides and cache 16-byte aligned, dim and rot multiples of 16.  Item (chunk
 // j, head group g) of a thread: chunk j < rot / 16 is eight pairs, a later one 16 values that are
-// copied.  CUTS: some section ends inside a chunk, whose pairs are then looked up one by one.
+// copied.  CUTS: some section ends inside a chunk.
 template <bool BF, bool CUTS>
 __global__ void __launch_bounds__(256, ROPE_PER_SM / 256) rope_vec_kernel(const RopeParams p, int chunks, int items)
 {
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(256, ROPE_PER_SM / 256) rope_vec_kernel(const 
     const int at0 = halves ? 8 * j : 16 * j, at1 = halves ? half + 8 * j : 16 * j + 8;
     const bool cached = h0 + ROPE_HEADS > p.heads;
     const int32_t *positions = p.positions + (long long)axis_of(p, 8 * j) * p.ld_pos;
-    const bool cuts = CUTS && pairs && axis_of(p, 8 * j) != axis_of(p, 8 * j + 7);
+    const int axis0 = axis_of(p, 8 * j), axis1 = CUTS && pairs ? axis_of(p, 8 * j + 7) : axis0;
 
     int next_pos = 0;
     long long next_slot = -1;
@@ -158,15 +158,27 @@ __global__ void __launch_bounds__(256, ROPE_PER_SM / 256) rope_vec_kernel(const 
                 *reinterpret_cast<float4 *>(c + i) = *reinterpret_cast<const float4 *>(entry + i);
                 *reinterpret_cast<float4 *>(s + i) = *reinterpret_cast<const float4 *>(entry + half + i);
             }
-            if (cuts) {
+            if (CUTS) {
+                // The pairs from a further section's start on take that axis's entries.
+#pragma unroll 1
+                for (int a = axis0 + 1; a <= axis1; ++a) {
+                    const int from = p.cut[a - 1] - 8 * j;
+                    if (p.cut[a] == p.cut[a - 1])
+                        continue;
+                    const int pa = checked_position(p, p.positions[(long long)a * p.ld_pos + t]);
+                    known &= pa >= 0;
+                    const float *other = p.table + (long long)max(pa, 0) * p.rot + 8 * j;
 #pragma unroll
-                for (int i = 1; i < 8; ++i) {
-                    const int pi = position_of(p, t, 8 * j + i);
-                    if (pi < 0) {
-                        known = false;
-                    } else {
-                        c[i] = p.table[(long long)pi * p.rot + 8 * j + i];
-                        s[i] = p.table[(long long)pi * p.rot + half + 8 * j + i];
+                    for (int i = 0; i < 8; i += 4) {
+                        const float4 c4 = *reinterpret_cast<const float4 *>(other + i);
+                        const float4 s4 = *reinterpret_cast<const float4 *>(other + half + i);
+                        const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, ss[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (i + q >= from) {
+                                c[i + q] = cc[q];
+                                s[i + q] = ss[q];
+                            }
                     }
                 }
             }
