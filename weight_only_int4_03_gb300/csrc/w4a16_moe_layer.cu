@@ -450,16 +450,15 @@ __device__ __forceinline__ Unit find_unit(const MoeGemm &p, int u, int lane)
 }
 
 // Sizes of a kernel variant.  NT: 8-column tiles of the MMA's token side; MT: 16-column tiles of
-// weights (each activation fragment serves MT products).
+// weights (each activation fragment serves MT products).  A stage is one 64-row block.
 template <int NT>
 struct MoeGeom {
     static constexpr int MT = 4;
     static constexpr int WARPS = NT == 1 ? 8 : 4;
     static constexpr int CTAS = NT == 1 ? 2 : 3; // blocks per SM
     static constexpr int COLS = 16 * MT;
-    static constexpr int BLOCKS = 4 / MT; // 64-row blocks per stage: 2 KiB of codes
-    static constexpr int SZ = COLS * 2;   // bytes of one scale (or zero) row
-    static constexpr int STAGE = 2048 + 2 * BLOCKS * SZ;
+    static constexpr int SZ = COLS * 2;        // bytes of one scale (or zero) row
+    static constexpr int STAGE = 2048 + 2 * SZ; // codes, scales, zeros
     static constexpr int STAGES = 3; // two in flight: at most one step, so at most into the next unit
     static constexpr int RING = STAGES * STAGE;
     static constexpr int vals(int mode) { return MT * NT * (mode == DOWN_SIDE ? 2 : 4); } // sums per lane to join
@@ -473,9 +472,8 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
     constexpr bool DOWN = MODE != GATE_UP;
     constexpr int PARTS = MODE == DOWN_TWICE ? 2 : 1; // activation rows per column
     constexpr int MT = G::MT, COLS = G::COLS, STAGES = G::STAGES, VALS = G::vals(MODE);
-    // One token tile: the two nibble positions keep accumulators of their own, which gives the MMAs
-    // twice as many independent chains and saves fp16 two shifts a word; with more tiles the
-    // registers go to the tiles.
+    // fp16 with one token tile: the two nibble positions keep accumulators of their own, which saves
+    // two shifts a word; with two tiles the registers go to the tiles.
     constexpr bool DUAL = !BF && NT == 1;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int drawn[G::WARPS][2];
@@ -507,16 +505,12 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
     }
 
     // --- the copying side: (unit, block) runs ahead of the computing side ----------------------
-    // A member takes the 128-row steps member, member + team, ..., each as 2 / BLOCKS stages.
+    // A member takes the 128-row steps member, member + team, ..., two stages each.
     int iu = u0, ik = -1, ib = 0, ib_end = 0;
     const int32_t *i_w = nullptr; // this lane's piece of block 0, half 0 of the unit's columns
-    const uint16_t *i_s = nullptr; // this lane's part of the expert's scale (or zero) row 0
-    // Lane l looks after chunk l % (SZ / 16) of a row; rows: scales of the stage's blocks, then zeros.
-    constexpr int SZ_CHUNKS = G::SZ / 16;
-    const int sz_row = lane / SZ_CHUNKS;
-    const bool sz_zero = sz_row >= G::BLOCKS;
-    const bool sz_mine = sz_row < G::BLOCKS * (p.z ? 2 : 1);
-    const int sz_block = sz_zero ? sz_row - G::BLOCKS : sz_row;
+    const uint16_t *i_s = nullptr; // lanes 0-7: chunk `lane` of the expert's scale row 0; 8-15: zeros
+    const bool sz_zero = lane >= 8;
+    const bool sz_mine = lane < (p.z ? 16 : 8);
     // The team's k-th unit: the first two follow from its number, the others are drawn from a common
     // counter two units ahead, so that teams that got on faster do more.
     const bool more = units > 2 * stride;
@@ -541,7 +535,7 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
         } while (ib >= ib_end);
         const int n0 = un.col * COLS;
         i_w = p.w + un.expert * p.expert_words + (long long)(n0 >> 7) * p.kblocks * 1024 + (n0 & 127) * 4 + lane * 4;
-        i_s = (sz_zero ? p.z : p.s) + un.expert * p.expert_groups * p.n + n0 + (lane % SZ_CHUNKS) * 8;
+        i_s = (sz_zero ? p.z : p.s) + un.expert * p.expert_groups * p.n + n0 + (lane & 7) * 8;
     };
     // The columns of a half 1 are stored with bit 2 flipped, so that the fragment reads below fall on
     // different banks.
@@ -552,23 +546,15 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
         if (iu < units) {
             const int32_t *w = i_w + (long long)ib * 1024;
             const uint32_t d0 = dst0 + stage * G::STAGE, d1 = dst1 + stage * G::STAGE;
-            if (MT == 4) { // one block: 64 columns of half 0, then of half 1
-                cp_async16_at<0, 0>(d0, w);
-                cp_async16_at<512, 512>(d0, w);
-                cp_async16_at<1024, 2048>(d1, w);
-                cp_async16_at<1536, 2560>(d1, w);
-            } else { // two blocks of 32 columns
-                cp_async16_at<0, 0>(d0, w);
-                cp_async16_at<512, 2048>(d1, w);
-                cp_async16_at<1024, 4096>(d0, w);
-                cp_async16_at<1536, 6144>(d1, w);
-            }
+            cp_async16_at<0, 0>(d0, w); // 64 columns of half 0, then of half 1
+            cp_async16_at<512, 512>(d0, w);
+            cp_async16_at<1024, 2048>(d1, w);
+            cp_async16_at<1536, 2560>(d1, w);
             if (sz_mine) {
-                const int n = ib + sz_block;
-                const int grp = p.group_magic ? (int)__umulhi((uint32_t)n, p.group_magic) : n;
+                const int grp = p.group_magic ? (int)__umulhi((uint32_t)ib, p.group_magic) : ib;
                 cp_async16_at<2048, 0>(d0, i_s + (long long)grp * p.n);
             }
-            ib += G::BLOCKS;
+            ++ib;
             if (!(ib & 1))
                 ib += 2 * (p.team - 1);
         }
@@ -629,7 +615,6 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
             }
             for (int step = first; step < un.step1; step += p.team) {
                 float lo[MT][ND][4], hi[DUAL ? MT : 1][ND][4], sa[ND][4];
-                const uint8_t *st = nullptr;
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     uint4 nx[2];
@@ -652,22 +637,17 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
                                 arow[n] += p.team * MOE_ROWS;
                         }
                     }
-                    if (b % G::BLOCKS == 0) {
-                        if (st)
-                            stage = stage + 1 == STAGES ? 0 : stage + 1;
-                        cp_async_wait<STAGES - 2>();
-                        __syncwarp(); // every lane's copies have landed, and the stage before is free
-                        issue(stage == 0 ? STAGES - 1 : stage - 1);
-                        st = ring_p + stage * G::STAGE;
-                    }
-                    const uint8_t *wst = st + (b % G::BLOCKS) * (2 * COLS * 16);
+                    cp_async_wait<STAGES - 2>();
+                    __syncwarp(); // every lane's copies have landed, and the stage before is free
+                    issue(stage == 0 ? STAGES - 1 : stage - 1);
+                    const uint8_t *st = ring_p + stage * G::STAGE;
+                    stage = stage + 1 == STAGES ? 0 : stage + 1;
                     uint2 w[MT][2]; // column g, g + 8 of each tile: words 2 (t >> 1), + 1 of half t & 1
 #pragma unroll
                     for (int m = 0; m < MT; ++m)
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            w[m][c] = *reinterpret_cast<const uint2 *>(wst + w_lane + (m * 16 + c * 8) * 16);
-                        }
+                        for (int c = 0; c < 2; ++c)
+                            w[m][c] = *reinterpret_cast<const uint2 *>(st + w_lane + (m * 16 + c * 8) * 16);
                     constexpr uint32_t ONES = BF ? 0x3F803F80u : 0x3C003C00u;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -688,14 +668,14 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
                             if (BF) {
                                 a0 = and_or(x, nibble, base128);
                                 a1 = and_or(y, nibble, base128);
-                                a2 = and_or((x >> 8), nibble, base128);
-                                a3 = and_or((y >> 8), nibble, base128);
-                                c0 = and_or((x >> 4), nibble, base128);
-                                c1 = and_or((y >> 4), nibble, base128);
-                                c2 = and_or((x >> 12), nibble, base128);
-                                c3 = and_or((y >> 12), nibble, base128);
+                                a2 = and_or(x >> 8, nibble, base128);
+                                a3 = and_or(y >> 8, nibble, base128);
+                                c0 = and_or(x >> 4, nibble, base128);
+                                c1 = and_or(y >> 4, nibble, base128);
+                                c2 = and_or(x >> 12, nibble, base128);
+                                c3 = and_or(y >> 12, nibble, base128);
                             } else {
-                                const uint32_t x8 = (x >> 8), y8 = (y >> 8);
+                                const uint32_t x8 = x >> 8, y8 = y >> 8;
                                 a0 = x & L;
                                 a1 = y & L;
                                 a2 = x8 & L;
@@ -742,7 +722,7 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
                                 mma16816<BF>(sa[n], ONES, ONES, ONES, ONES, bv[r][n][i].z, bv[r][n][i].w);
                     }
                     // End of a group (or of a step, whose two blocks then share one): scale the sums.
-                    const uint8_t *sz = st + 2048 + (b % G::BLOCKS) * G::SZ;
+                    const uint8_t *sz = st + 2048;
                     auto flush = [&](auto zeros, bool again) {
 #pragma unroll
                         for (int m = 0; m < MT; ++m)
@@ -752,7 +732,7 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
                                 const float sc = to_float<BF>(*reinterpret_cast<const uint16_t *>(sz + col * 2));
                                 float z = 8.f;
                                 if (decltype(zeros)::value)
-                                    z = to_float<BF>(*reinterpret_cast<const uint16_t *>(sz + G::BLOCKS * G::SZ + col * 2));
+                                    z = to_float<BF>(*reinterpret_cast<const uint16_t *>(sz + G::SZ + col * 2));
                                 z = BF ? z + 128.f : z * CODE_UNIT;
 #pragma unroll
                                 for (int n = 0; n < ND; ++n)
@@ -761,7 +741,7 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
                                         const int i = 2 * c + e;
                                         float q = lo[m][n][i];
                                         if (DUAL)
-                                            q = BF ? q + hi[m % (DUAL ? MT : 1)][n][i] : fmaf(hi[m % (DUAL ? MT : 1)][n][i], 0.0625f, q);
+                                            q = fmaf(hi[m % (DUAL ? MT : 1)][n][i], 0.0625f, q);
                                         q = fmaf(-z, sa[n][e], q);
                                         out[m][n][i] = fmaf(sc, q, out[m][n][i]);
                                         if (again) {
@@ -790,7 +770,6 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
                         bv[0][0][1] = nx[1];
                     }
                 }
-                stage = stage + 1 == STAGES ? 0 : stage + 1;
             }
         };
         if (NT == 1 || rows <= 8)
