@@ -84,6 +84,11 @@ struct AttGeom {
 };
 
 // PACK: at most eight heads in a tile.
+// bf16, 128 wide: 32 sequences of 2048 to 32768 positions, 64 / 8 heads, 235 us, 6.55 TB/s of keys and
+// values; one of 131071 with 40 / 8 heads 87.6 us, 6.13 TB/s (3 us pass before the first rows, 9 us
+// from the last to the end of the join of 38 parts a row).  fp16, 24 sequences of 5 to 9000 with a
+// window of 2048, 12 / 12 heads of 64: 17.6 us, of which half is the start and the join; one of 37
+// positions: 4.0 us of latencies.
 template <int D, bool BF, bool PACK>
 __global__ void __launch_bounds__(ATT_THREADS, AttGeom<D>::CTAS)
     paged_attention_kernel(const AttParams p)

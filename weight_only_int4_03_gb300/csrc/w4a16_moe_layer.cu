@@ -30,6 +30,12 @@
 // its 128-row steps in turn.  A warp streams its steps through its own ring of cp.async stages, which
 // runs on into its next unit, so no block-wide barrier sits between a copy and its use and the ring
 // stays full across units.  Activations are read from L1/L2 in the MMA's fragment order.
+//
+// Measured, the four launches together: one token, 8 experts of 4096 x 14336, two each, fp16: 46.8 us, 3.9
+// TB/s of weights (the copies themselves run at 5.4 to 6.0 TB/s; routing and the first copies take
+// 10 us); 16 tokens: 159 us, 4.7 TB/s; 64 tokens, bf16: 377 us, bound by the MMAs and the conversion;
+// 7 tokens on 128 experts of 2048 x 768, eight each, bf16: 39.0 us; one token on 1024 x 1792: 14.4 us of
+// latencies.
 #include <math.h>
 
 #include <type_traits>
@@ -160,6 +166,10 @@ __device__ __forceinline__ void choose_experts(const float *scores, int experts,
     w_out = renorm ? w / chosen : w;
 }
 
+// A block per expert and four tokens; the last of four tokens' blocks takes their softmax and top-k, the
+// last of those groups the pairs by expert.  Bound by latency, a chain of loads, two counters and scans:
+// 4 us for one token and 8 experts, 8 us for 7 tokens and 128.  (One block for all experts of a small
+// router did without a counter but read its rows one after the other: 61 us a layer instead of 50.)
 template <bool BF>
 __global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const RouteParams p)
 {
