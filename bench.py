@@ -188,7 +188,8 @@ def _code_only(text: str) -> str:
     return "\n".join(line.rstrip() for line in text.splitlines() if line.strip())
 
 
-OPERATOR_SOURCES = ("w4a16_ops.cuh", "w4a16_rope.cu", "w4a16_attention.cu", "w4a16_moe_layer.cu")
+OPERATOR_SOURCES = ("w4a16_ops.cuh", "w4a16_rope.cu", "w4a16_attention.cu", "w4a16_moe_layer.cu",
+                    "w4a16_call.cpp")
 
 
 def kernel_source_hash() -> str:

@@ -14,7 +14,7 @@ import os
 
 import numpy as np
 
-from .build import LIB_PATH
+from .build import CALL_PATH, LIB_PATH
 
 W4A16_TYPE_U4 = 4
 W4A16_TYPE_U4B8 = 5
@@ -373,7 +373,29 @@ def _kv_strides(kv_strides, page_size: int, n_kv_heads: int, head_dim: int):
 
 @functools.lru_cache(maxsize=64)
 def _int32_array(values):
-    return (ctypes.c_int32 * len(values))(*values)
+    array = (ctypes.c_int32 * len(values))(*map(int, values))
+    return array, ctypes.addressof(array)
+
+
+def _direct_calls():
+    """The decode-step operators' entries, taking tensors where they take pointers: from the extension
+    module beside the library, or through ctypes where that was not built for this interpreter."""
+    names = ("w4a16_rope_append", "w4a16_paged_attention", "w4a16_moe_layer")
+    if os.path.exists(CALL_PATH):
+        import importlib.util
+        spec = importlib.util.spec_from_file_location("_w4a16_call", CALL_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        return tuple(getattr(module, n) for n in names)
+    return tuple(map(_through_ctypes, names))
+
+
+def _through_ctypes(name):
+    fn = getattr(_lib, name)
+    return lambda *args: fn(*(a if isinstance(a, (int, float)) else _ptr(a) for a in args))
+
+
+_rope_append, _paged_attention, _moe_layer = _direct_calls()
 
 
 def w4a16_rope_append(q, k, v, q_out, k_cache, v_cache, cos_sin, positions, slots, status, n_tokens: int,
@@ -383,16 +405,14 @@ def w4a16_rope_append(q, k, v, q_out, k_cache, v_cache, cos_sin, positions, slot
                       ld_pos: int | None = None, kv_strides=None, stream=None) -> None:
     """Rotary positions on q and k (axes by `sections`, a sequence of ints), k and v written into
     the paged cache -- see include/w4a16.h.  `status`: device int32 for W4A16_DEV_* bits, or None."""
-    sec = _int32_array(tuple(map(int, sections)))
+    sec, sec_at = _int32_array(sections if type(sections) is tuple else tuple(sections))
     ps, ts, hs = _kv_strides(kv_strides, page_size, n_kv_heads, head_dim)
-    _check("w4a16_rope_append", _lib.w4a16_rope_append(
-        _ptr(q), n_heads * head_dim if ldq is None else ldq,
-        _ptr(k), n_kv_heads * head_dim if ldk is None else ldk,
-        _ptr(v), n_kv_heads * head_dim if ldv is None else ldv,
-        _ptr(q_out), n_heads * head_dim if ldqo is None else ldqo, _ptr(k_cache), _ptr(v_cache), ps, ts, hs,
-        _ptr(cos_sin), max_pos, _ptr(positions), n_tokens if ld_pos is None else ld_pos, _ptr(slots),
-        _ptr(status), n_tokens, n_heads, n_kv_heads, head_dim, rot_dim, sec, len(sec), page_size, n_pages,
-        flags, _stream(stream)))
+    _check("w4a16_rope_append", _rope_append(
+        q, n_heads * head_dim if ldq is None else ldq, k, n_kv_heads * head_dim if ldk is None else ldk,
+        v, n_kv_heads * head_dim if ldv is None else ldv, q_out, n_heads * head_dim if ldqo is None else ldqo,
+        k_cache, v_cache, ps, ts, hs, cos_sin, max_pos, positions, n_tokens if ld_pos is None else ld_pos, slots,
+        status, n_tokens, n_heads, n_kv_heads, head_dim, rot_dim, sec_at, len(sec), page_size, n_pages, flags,
+        _stream(stream)))
 
 
 def w4a16_paged_attention_workspace_size(batch: int, n_heads: int, n_kv_heads: int, head_dim: int,
@@ -410,12 +430,11 @@ def w4a16_paged_attention(q, k_cache, v_cache, out, block_table, seq_lens, works
     ps, ts, hs = _kv_strides(kv_strides, page_size, n_kv_heads, head_dim)
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check("w4a16_paged_attention", _lib.w4a16_paged_attention(
-        _ptr(q), n_heads * head_dim if ldq is None else ldq, _ptr(k_cache), _ptr(v_cache), ps, ts, hs,
-        _ptr(out), n_heads * head_dim if ldo is None else ldo, _ptr(lse), _ptr(block_table),
-        max_pages if ld_table is None else ld_table, _ptr(seq_lens), _ptr(workspace), workspace_bytes,
-        batch, n_heads, n_kv_heads, head_dim, page_size, n_pages, max_pages, window, scale, flags,
-        _stream(stream)))
+    _check("w4a16_paged_attention", _paged_attention(
+        q, n_heads * head_dim if ldq is None else ldq, k_cache, v_cache, ps, ts, hs,
+        out, n_heads * head_dim if ldo is None else ldo, lse, block_table,
+        max_pages if ld_table is None else ld_table, seq_lens, workspace, workspace_bytes, batch, n_heads,
+        n_kv_heads, head_dim, page_size, n_pages, max_pages, window, scale, flags, _stream(stream)))
 
 
 def w4a16_moe_layer_workspace_size(n_tokens: int, hidden: int, inter: int, n_experts: int, top_k: int) -> int:
@@ -431,9 +450,8 @@ def w4a16_moe_layer(x, router, gate_up, gate_up_scales, gate_up_zeros, down, dow
     for up to 64 tokens with 4-bit weights -- see include/w4a16.h."""
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check("w4a16_moe_layer", _lib.w4a16_moe_layer(
-        _ptr(x), hidden if ldx is None else ldx, _ptr(router), _ptr(gate_up), _ptr(gate_up_scales),
-        _ptr(gate_up_zeros), _ptr(down), _ptr(down_scales), _ptr(down_zeros), _ptr(residual),
-        hidden if ldr is None else ldr, _ptr(y), hidden if ldy is None else ldy, _ptr(topk_ids),
-        _ptr(topk_weights), _ptr(workspace), workspace_bytes, n_tokens, hidden, inter, n_experts, top_k,
-        group_size, weight_type, flags, _stream(stream)))
+    _check("w4a16_moe_layer", _moe_layer(
+        x, hidden if ldx is None else ldx, router, gate_up, gate_up_scales, gate_up_zeros, down, down_scales,
+        down_zeros, residual, hidden if ldr is None else ldr, y, hidden if ldy is None else ldy, topk_ids,
+        topk_weights, workspace, workspace_bytes, n_tokens, hidden, inter, n_experts, top_k, group_size,
+        weight_type, flags, _stream(stream)))

@@ -2,7 +2,9 @@
 
 Each .cu file compiles to an object in parallel, then one nvcc link makes the shared
 library under weight_only_int4_03_gb300/_lib/.  The CUDA runtime is linked statically, so the
-library needs only the driver at run time.
+library needs only the driver at run time.  Beside it comes a small extension module for the
+interpreter that builds (the decode-step operators called without ctypes), where Python's headers are
+installed.
 """
 from __future__ import annotations
 
@@ -10,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,7 +20,9 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libw4a16.so")
+CALL_PATH = os.path.join(LIB_DIR, "_w4a16_call" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 INCLUDE = os.path.join(ROOT, "include")
+PYTHON_INCLUDE = sysconfig.get_paths()["include"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["w4a16_gemm.cu", "w4a16_decode.cu", "w4a16_aux.cu", "w4a16_api.cu", "w4a16_noalloc.cu",
@@ -38,10 +43,15 @@ def _inputs() -> list[str]:
     return files
 
 
+def _has_python_headers() -> bool:
+    return os.path.exists(os.path.join(PYTHON_INCLUDE, "Python.h"))
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    outputs = [LIB_PATH, CALL_PATH] if _has_python_headers() else [LIB_PATH]
+    if not all(os.path.exists(f) for f in outputs):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(f) for f in outputs)
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -76,6 +86,12 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     subprocess.check_call([nvcc, "-shared", "-o", tmp] + objs + ARCH + ["-Xcompiler", "-fPIC"])
     os.replace(tmp, LIB_PATH)
+    if _has_python_headers():
+        tmp = CALL_PATH + f".tmp{os.getpid()}"
+        subprocess.check_call([nvcc, "-shared", "-cudart", "none", "-O2", "-std=c++17", "-Xcompiler", "-fPIC",
+                               "-I", INCLUDE, "-I", PYTHON_INCLUDE, os.path.join(CSRC, "w4a16_call.cpp"), "-o", tmp,
+                               "-L", LIB_DIR, "-lw4a16", "-Xlinker", "-rpath,$ORIGIN"])
+        os.replace(tmp, CALL_PATH)
     return LIB_PATH
 
 
