@@ -226,3 +226,27 @@ def test_offsets_past_32_bits(w4):
     case.run(w4, ws)
     case.check()
     assert w4.w4a16_status(ws) == 0
+
+
+@pytest.mark.parametrize("kw", [
+    dict(dtype="fp16", lens=[1024], heads=4, kv=1, dim=128, page=16),          # 16 parts on 152 SMs: joined at once
+    dict(dtype="bf16", lens=[1088], heads=8, kv=1, dim=128, page=16),          # 17: a group of 16 and one part
+    dict(dtype="fp16", lens=[1100, 3], heads=16, kv=1, dim=64, page=24),       # 18, shared with a further row
+    dict(dtype="bf16", lens=[2112, 0, 64, 1500], heads=12, kv=1, dim=256, page=64),
+    dict(dtype="fp16", lens=[30000], heads=8, kv=1, dim=256, page=32),         # as many parts as blocks
+    dict(dtype="bf16", lens=[30001, 17000], heads=20, kv=1, dim=128, page=16),
+    dict(dtype="fp16", lens=[41000], heads=3, kv=1, dim=64, page=128),
+    dict(dtype="bf16", lens=[9000, 70, 20000], heads=16, kv=2, dim=64, page=16, window=9001),
+], ids=lambda c: f"{c['dtype']}h{c['heads']}d{c['dim']}n{max(c['lens'])}b{len(c['lens'])}")
+def test_rows_in_many_parts(w4, kw):
+    import torch
+    case = Case(17, **kw)
+    ws = case.workspace(w4)
+    case.run(w4, ws)
+    case.check()
+    first, lse = case.out.clone(), case.lse.clone()
+    for _ in range(3):
+        case.run(w4, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(case.out, first) and torch.equal(case.lse, lse)
+    assert w4.w4a16_status(ws) == 0

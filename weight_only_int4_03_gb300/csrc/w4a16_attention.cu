@@ -20,11 +20,15 @@
 //   - Keys and values go through mma.sync m16n8k16 with the group's query heads as the rows, which
 //     is far from the tensor limit even with one head in sixteen rows.
 //   - The four warps' results meet in shared memory; a row covered by several blocks is joined by
-//     the last of them to arrive, in block order (bit-identical repeats).
+//     the last of them to arrive, in block order (bit-identical repeats).  One block reads 32 KiB of
+//     partial results at a time, so more than 16 parts are joined in two levels, sixteen at a time by as many
+//     blocks: 131072 positions of one KV head of 8 x 128 took 55 us with one level and take 25.
 // Softmax runs in fp32 in base 2.  p is not rounded to 16 bits for the value product: it goes in as
 // a 16-bit part and the 16-bit remainder (p - hi is exact in fp32), which keeps 2^-17 (bf16) or
 // better of p.  With at most eight heads per KV head the remainder takes the upper eight rows of
 // the same MMA, which are empty then; with more it costs a second MMA.
+#include <type_traits>
+
 #include "w4a16_ops.cuh"
 
 namespace w4 {
@@ -36,13 +40,15 @@ constexpr int ATT_STEP = 16;                    // positions per warp and step
 constexpr int ATT_UNIT = ATT_WARPS * ATT_STEP;  // positions per work unit
 constexpr int ATT_ROWS = 16;                    // query heads per head tile
 constexpr int ATT_MAX_BATCH = 4096;
+constexpr int ATT_FAN = 16;                     // parts of a row joined at once
+constexpr int ATT_SLOTS = 3;                    // partials of a block: first row, last row, joined group
 
 struct AttParams {
     const uint16_t *q, *k, *v;
     uint16_t *out;
     float *lse;
     const int32_t *table, *lens;
-    int *status, *counters;
+    int *status, *counters, *group_counters;
     float *partials;
     long long page_stride, token_stride, head_stride;
     int ldq, ldo, ld_table;
@@ -85,7 +91,7 @@ struct AttGeom {
 
 // PACK: at most eight heads in a tile.
 // bf16, 128 wide: 32 sequences of 2048 to 32768 positions, 64 / 8 heads, 235 us, 6.55 TB/s of keys and
-// values; one of 131071 with 40 / 8 heads 87.6 us, 6.13 TB/s (3 us pass before the first rows, 9 us
+// values; one of 131071 with 40 / 8 heads 86.3 us, 6.22 TB/s (3 us pass before the first rows, 8 us
 // from the last to the end of the join of 38 parts a row).  fp16, 24 sequences of 5 to 9000 with a
 // window of 2048, 12 / 12 heads of 64: 17.6 us, of which half is the start and the join; one of 37
 // positions: 4.0 us of latencies.
@@ -386,7 +392,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttGeom<D>::CTAS)
         __syncthreads();
         const bool whole = steps == seq_units;
         const int slot = u_begin >= row_u0 ? 0 : 1; // a block shares at most its first and its last row
-        float *part = p.partials + ((long long)blockIdx.x * 2 + slot) * G::SLOT;
+        float *part = p.partials + ((long long)blockIdx.x * ATT_SLOTS + slot) * G::SLOT;
         uint16_t *out = p.out + (long long)b * p.ldo + (long long)(c * p.group + h0) * D;
         const long long lse_at = (long long)b * p.heads + c * p.group + h0;
         for (int i = tid; i < nh * (D / 4); i += ATT_THREADS) {
@@ -423,69 +429,125 @@ __global__ void __launch_bounds__(ATT_THREADS, AttGeom<D>::CTAS)
             }
         }
         if (!whole) {
-            // Blocks that share this row: those of its first and its last unit and all between.
-            const long long row_u1 = row_u0 + seq_units;
-            const int c_lo = owner_of(row_u0), c_hi = owner_of(row_u1 - 1);
-            __syncthreads();
-            int *counter = p.counters + (long long)b * rows_per_seq + row;
-            if (tid == 0) {
-                const int last = arrive_counter(counter) == c_hi - c_lo;
-                if (last)
-                    *counter = 0;
-                is_last = last;
-            }
-            __syncthreads();
-            if (is_last) {
-                // A thread sums a quad of outputs over the parts in block order, the loads of sixteen
-                // parts in flight at once, rescaling as the maximum moves.
-                const int lo_slot = begin_of(c_lo) >= row_u0 ? 0 : 1, parts = c_hi - c_lo + 1;
-                constexpr int AT_ONCE = 16;
-                for (int i = tid; i < nh * (D / 4); i += ATT_THREADS) {
-                    const int h = i / (D / 4);
-                    float m = -INFINITY, l = 0.f;
-                    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int q0 = 0; q0 < parts; q0 += AT_ONCE) {
-                        float2 ml[AT_ONCE];
-                        float4 x[AT_ONCE];
+            // The parts of a row are those of the blocks c_lo to c_hi, the owners of its first and its
+            // last unit.  The last block to arrive joins them; where there are more than ATT_FAN, the
+            // last of every ATT_FAN of them joins those first, so that many blocks share the reading.
+            const int c_lo = owner_of(row_u0), c_hi = owner_of(row_u0 + seq_units - 1);
+            const int lo_slot = begin_of(c_lo) >= row_u0 ? 0 : 1, parts = c_hi - c_lo + 1;
+            const int group0 = ((int)blockIdx.x - c_lo) / ATT_FAN * ATT_FAN; // this block's group
+            bool last_level = parts <= ATT_FAN;
+            if (!last_level && group0 + 1 == parts)
+                last_level = true; // a group of one part is read as it is
+            for (;;) {
+                // Joined here: a row's parts, a group of them, or a row's groups.
+                const bool groups = last_level && parts > ATT_FAN;
+                const int n = groups       ? (parts + ATT_FAN - 1) / ATT_FAN
+                              : last_level ? parts
+                                           : min(ATT_FAN, parts - group0);
+                const int from = c_lo + (last_level ? 0 : group0);
+                __syncthreads();
+                if (tid == 0) {
+                    int *counter = last_level ? p.counters + (long long)b * rows_per_seq + row : p.group_counters + from;
+                    const int last = arrive_counter(counter) == n - 1;
+                    if (last)
+                        *counter = 0;
+                    is_last = last;
+                }
+                __syncthreads();
+                if (!is_last)
+                    break;
+                // A thread sums ITEMS quads of outputs over the parts in block order, the loads of AT
+                // parts in flight at once (sixteen loads in all: few parts of 16 heads of 256 take 11.2 us
+                // instead of 13.2 with one quad at a time), rescaling as the maximum moves.
+                auto join = [&](auto items_c, auto at_c) {
+                    constexpr int ITEMS = decltype(items_c)::value, AT = decltype(at_c)::value;
+                    const int quads = nh * (D / 4);
+                    for (int i0 = tid; i0 < quads; i0 += ITEMS * ATT_THREADS) {
+                        float m[ITEMS], l[ITEMS];
+                        float4 sum[ITEMS];
 #pragma unroll
-                        for (int q = 0; q < AT_ONCE; ++q) {
-                            const bool in = q0 + q < parts;
-                            const float *pp =
-                                p.partials + ((long long)(c_lo + q0 + q) * 2 + (q0 + q == 0 ? lo_slot : 0)) * G::SLOT;
-                            ml[q] = in ? __ldcg(reinterpret_cast<const float2 *>(pp + ATT_ROWS * D + 2 * h))
-                                       : make_float2(-INFINITY, 0.f);
-                            x[q] = in ? __ldcg(reinterpret_cast<const float4 *>(pp + 4 * i)) // quad i: row h's part of it
-                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+                        for (int k = 0; k < ITEMS; ++k) {
+                            m[k] = -INFINITY;
+                            l[k] = 0.f;
+                            sum[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                         }
-                        float mn = m;
+                        for (int q0 = 0; q0 < n; q0 += AT) {
+                            float2 ml[ITEMS][AT];
+                            float4 x[ITEMS][AT];
 #pragma unroll
-                        for (int q = 0; q < AT_ONCE; ++q)
-                            mn = fmaxf(mn, ml[q].x);
-                        const float base = mn == -INFINITY ? 0.f : mn, f0 = exp2f(m - base);
-                        m = mn;
-                        l *= f0;
-                        sum.x *= f0;
-                        sum.y *= f0;
-                        sum.z *= f0;
-                        sum.w *= f0;
+                            for (int q = 0; q < AT; ++q) {
+                                const int at = groups ? (q0 + q) * ATT_FAN : q0 + q;
+                                const int which = groups && at + 1 < parts ? ATT_SLOTS - 1 : from + at == c_lo ? lo_slot : 0;
+                                const float *pp = p.partials + ((long long)(from + at) * ATT_SLOTS + which) * G::SLOT;
 #pragma unroll
-                        for (int q = 0; q < AT_ONCE; ++q) {
-                            const float f = exp2f(ml[q].x - base);
-                            l = fmaf(f, ml[q].y, l);
-                            sum.x = fmaf(f, x[q].x, sum.x);
-                            sum.y = fmaf(f, x[q].y, sum.y);
-                            sum.z = fmaf(f, x[q].z, sum.z);
-                            sum.w = fmaf(f, x[q].w, sum.w);
+                                for (int k = 0; k < ITEMS; ++k) {
+                                    const int i = i0 + k * ATT_THREADS;
+                                    const bool in = q0 + q < n && i < quads;
+                                    ml[k][q] = in ? __ldcg(reinterpret_cast<const float2 *>(pp + ATT_ROWS * D) + i / (D / 4))
+                                                  : make_float2(-INFINITY, 0.f);
+                                    x[k][q] = in ? __ldcg(reinterpret_cast<const float4 *>(pp) + i)
+                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+                                }
+                            }
+#pragma unroll
+                            for (int k = 0; k < ITEMS; ++k) {
+                                float mn = m[k];
+#pragma unroll
+                                for (int q = 0; q < AT; ++q)
+                                    mn = fmaxf(mn, ml[k][q].x);
+                                const float base = mn == -INFINITY ? 0.f : mn, f0 = exp2f(m[k] - base);
+                                m[k] = mn;
+                                l[k] *= f0;
+                                sum[k].x *= f0;
+                                sum[k].y *= f0;
+                                sum[k].z *= f0;
+                                sum[k].w *= f0;
+#pragma unroll
+                                for (int q = 0; q < AT; ++q) {
+                                    const float f = exp2f(ml[k][q].x - base);
+                                    l[k] = fmaf(f, ml[k][q].y, l[k]);
+                                    sum[k].x = fmaf(f, x[k][q].x, sum[k].x);
+                                    sum[k].y = fmaf(f, x[k][q].y, sum[k].y);
+                                    sum[k].z = fmaf(f, x[k][q].z, sum[k].z);
+                                    sum[k].w = fmaf(f, x[k][q].w, sum[k].w);
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < ITEMS; ++k) {
+                            const int i = i0 + k * ATT_THREADS;
+                            if (i >= quads)
+                                continue;
+                            const bool first_quad = i % (D / 4) == 0;
+                            if (last_level) {
+                                const float r = l[k] == 0.f ? 0.f : 1.f / l[k];
+                                uint2 w2;
+                                w2.x = pack2<BF>(sum[k].x * r, sum[k].y * r);
+                                w2.y = pack2<BF>(sum[k].z * r, sum[k].w * r);
+                                *reinterpret_cast<uint2 *>(out + 4LL * i) = w2;
+                                if (p.lse && first_quad)
+                                    p.lse[lse_at + i / (D / 4)] =
+                                        l[k] == 0.f ? -INFINITY : (m[k] + log2f(l[k])) * 0.6931471805599453f;
+                            } else {
+                                float *to = p.partials + ((long long)from * ATT_SLOTS + ATT_SLOTS - 1) * G::SLOT;
+                                __stcg(reinterpret_cast<float4 *>(to) + i, sum[k]);
+                                if (first_quad)
+                                    __stcg(reinterpret_cast<float2 *>(to + ATT_ROWS * D) + i / (D / 4),
+                                           make_float2(m[k], l[k]));
+                            }
                         }
                     }
-                    const float r = l == 0.f ? 0.f : 1.f / l;
-                    uint2 w2;
-                    w2.x = pack2<BF>(sum.x * r, sum.y * r);
-                    w2.y = pack2<BF>(sum.z * r, sum.w * r);
-                    *reinterpret_cast<uint2 *>(out + 4LL * i) = w2;
-                    if (p.lse && i % (D / 4) == 0)
-                        p.lse[lse_at + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-                }
+                };
+                using std::integral_constant;
+                if (n <= 4)
+                    join(integral_constant<int, 4>(), integral_constant<int, 4>());
+                else if (n <= 8)
+                    join(integral_constant<int, 2>(), integral_constant<int, 8>());
+                else
+                    join(integral_constant<int, 1>(), integral_constant<int, 16>());
+                if (last_level)
+                    break;
+                last_level = true;
             }
         }
         if (u < u_end)
@@ -511,7 +573,7 @@ cudaError_t att_kernel(bool bf, bool pack, AttKernel &kernel, int &smem)
 }
 
 struct AttLayout {
-    long long counters, partials, total;
+    long long group_counters, counters, partials, total;
 };
 
 int att_grid(int num_sms, int head_dim)
@@ -522,9 +584,10 @@ int att_grid(int num_sms, int head_dim)
 AttLayout att_layout(int batch, int rows_per_seq, int head_dim, int grid)
 {
     AttLayout l;
-    l.counters = HEADER_BYTES;
+    l.group_counters = HEADER_BYTES;
+    l.counters = l.group_counters + 4LL * grid;
     l.partials = round_up(l.counters + 4LL * batch * rows_per_seq, 256);
-    l.total = l.partials + (long long)grid * 2 * ATT_ROWS * (head_dim + 2) * 4;
+    l.total = l.partials + (long long)grid * ATT_SLOTS * ATT_ROWS * (head_dim + 2) * 4;
     return l;
 }
 
@@ -590,7 +653,7 @@ extern "C" int w4a16_paged_attention(const void *q, int ldq, const void *k_cache
     // at most max_pages pages.
     const long long max_len = (long long)max_pages * page_size;
     if (max_len > 0x7FFFFFFFLL - 64 * ATT_UNIT ||
-        ((max_len + ATT_UNIT - 1) / ATT_UNIT + 4) * batch > 0x7FFFFFFFLL)
+        ((max_len + ATT_UNIT - 1) / ATT_UNIT + 8) * batch > 0x7FFFFFFFLL)
         return status_of(STAGE_ARG, W4A16_ARG_OVERFLOW);
 
     int num_sms = 0;
@@ -613,6 +676,7 @@ extern "C" int w4a16_paged_attention(const void *q, int ldq, const void *k_cache
     p.lens = seq_lens;
     p.status = reinterpret_cast<int *>(ws);
     p.counters = reinterpret_cast<int *>(ws + lay.counters);
+    p.group_counters = reinterpret_cast<int *>(ws + lay.group_counters);
     p.partials = reinterpret_cast<float *>(ws + lay.partials);
     p.page_stride = kv_page_stride;
     p.token_stride = kv_token_stride;
