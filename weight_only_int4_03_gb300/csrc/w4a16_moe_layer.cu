@@ -31,10 +31,10 @@
 // runs on into its next unit, so no block-wide barrier sits between a copy and its use and the ring
 // stays full across units.  Activations are read from L1/L2 in the MMA's fragment order.
 //
-// Measured, the four launches together: one token, 8 experts of 4096 x 14336, two each, fp16: 46.8 us, 3.9
+// Measured, the four launches together: one token, 8 experts of 4096 x 14336, two each, fp16: 46.2 us, 3.9
 // TB/s of weights (the copies themselves run at 5.4 to 6.0 TB/s; routing and the first copies take
-// 10 us); 16 tokens: 159 us, 4.7 TB/s; 64 tokens, bf16: 377 us, bound by the MMAs and the conversion;
-// 7 tokens on 128 experts of 2048 x 768, eight each, bf16: 39.0 us; one token on 1024 x 1792: 14.4 us of
+// 10 us); 16 tokens: 159 us, 4.7 TB/s; 64 tokens, bf16: 374 us, bound by the MMAs and the conversion;
+// 7 tokens on 128 experts of 2048 x 768, eight each, bf16: 38.1 us; one token on 1024 x 1792: 13.2 us of
 // latencies.
 #include <math.h>
 
@@ -52,10 +52,13 @@ constexpr int MOE_MAX_PAIRS = MOE_MAX_TOKENS * MOE_MAX_TOP;
 constexpr int MOE_WARPS = 8; // of a routing block
 constexpr int MOE_THREADS = MOE_WARPS * 32;
 constexpr int MOE_CHUNK = 4;   // tokens per routing block
+constexpr int MOE_ONE_LEVEL = MOE_WARPS; // tokens whose softmax and top-k one block does
 // Pairs per expert up to which a down tile holds both parts of four pairs side by side (7 tokens on 128
 // experts, 1.2 pairs each: 44.8 us against 46.4 us one after the other; 16 tokens on 8, four each: 175 us
 // against 167 us).
 constexpr double MOE_SIDE_MEAN = 3.0;
+// Bytes of the tables that a product keeps in shared memory, at most.
+constexpr int MOE_TABLES_MOST = (MOE_MAX_EXPERTS / 32 + 1) * 512 + MOE_MAX_PAIRS * 4;
 constexpr int MOE_ROWS = 128;  // weight rows per step (two 64-row blocks)
 constexpr float CODE_UNIT = 5.9604644775390625e-8f; // 2^-24: the fp16 value of the bits 1
 
@@ -166,9 +169,9 @@ __device__ __forceinline__ void choose_experts(const float *scores, int experts,
     w_out = renorm ? w / chosen : w;
 }
 
-// A block per expert and four tokens; the last of four tokens' blocks takes their softmax and top-k, the
-// last of those groups the pairs by expert.  Bound by latency, a chain of loads, two counters and scans:
-// 4 us for one token and 8 experts, 8 us for 7 tokens and 128.  (One block for all experts of a small
+// A block per expert and four tokens; the last of four tokens' blocks (up to MOE_ONE_LEVEL tokens: of
+// all) takes their softmax and top-k, the last of those groups the pairs by expert.  Bound by latency, a
+// chain of loads, one or two counters and scans: 4 us for one token and 8 experts, 7 us for 7 tokens and 128.  (One block for all experts of a small
 // router did without a counter but read its rows one after the other: 61 us a layer instead of 50.)
 template <bool BF>
 __global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const RouteParams p)
@@ -182,6 +185,7 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const Rout
     pdl_wait();
     pdl_launch_dependents();
     const int t0 = blockIdx.y * MOE_CHUNK, nt = min(MOE_CHUNK, p.tokens - t0);
+    const bool one_level = p.tokens <= MOE_ONE_LEVEL;
     {
         // This block's share of the tokens' rows in fragment order.
         const int chunks = p.hidden / 8;
@@ -244,9 +248,10 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const Rout
         }
         __syncwarp();
         if (lane == 0) {
-            const int last = arrive_counter(p.counters + blockIdx.y) == (int)gridDim.x - 1;
+            int *counter = p.counters + (one_level ? 0 : blockIdx.y);
+            const int last = arrive_counter(counter) == (int)(one_level ? gridDim.x * gridDim.y : gridDim.x) - 1;
             if (last)
-                p.counters[blockIdx.y] = 0;
+                *counter = 0;
             is_last = last;
         }
     }
@@ -254,13 +259,13 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const Rout
     if (!is_last)
         return;
 
-    // --- softmax and top-k of this chunk, a warp per token ------------------------------------
+    // --- softmax and top-k of this chunk (or of all tokens), a warp per token -----------------
     const int pairs = p.tokens * p.top;
-    const bool one_chunk = gridDim.y == 1;
-    if (warp < nt) {
+    const int tok = (one_level ? 0 : t0) + warp;
+    if (tok < (one_level ? p.tokens : t0 + nt)) {
         int at;
         float w;
-        const float *l = p.logits + (long long)(t0 + warp) * p.experts;
+        const float *l = p.logits + (long long)tok * p.experts;
         if (p.experts <= 32)
             choose_experts<1>(l, p.experts, p.top, p.renorm, lane, at, w);
         else if (p.experts <= 128)
@@ -268,9 +273,9 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const Rout
         else
             choose_experts<MOE_MAX_EXPERTS / 32>(l, p.experts, p.top, p.renorm, lane, at, w);
         if (lane < p.top) {
-            const int pair = (t0 + warp) * p.top + lane;
+            const int pair = tok * p.top + lane;
             p.tab.weights[pair] = w;
-            if (one_chunk)
+            if (one_level)
                 ids[pair] = at;
             else
                 __stcg(p.tab.ids + pair, at);
@@ -281,7 +286,7 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const Rout
         }
     }
     __syncthreads();
-    if (!one_chunk) {
+    if (!one_level) {
         if (tid == 0) {
             const int last = arrive_counter(p.counters + gridDim.y) == (int)gridDim.y - 1;
             if (last)
@@ -297,7 +302,43 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const Rout
     }
 
     // --- pairs by expert ----------------------------------------------------------------------
-    // A pair's place among its expert's is the number of equal ids before it.
+    if (pairs <= 32) { // by one warp, a pair per lane
+        if (warp == 0) {
+            const bool in = lane < pairs;
+            const int x = in ? ids[lane] : MOE_MAX_EXPERTS;
+            const uint32_t same = __match_any_sync(0xffffffffu, x);
+            const int n = __popc(same), before = __popc(same & ((1u << lane) - 1u));
+            const bool leader = in && before == 0;
+            const uint32_t passes = !leader ? 0u : (uint32_t)((n + (1 << p.up_shift) - 1) >> p.up_shift) |
+                                                   (uint32_t)((n + (1 << p.down_shift) - 1) >> p.down_shift) << 16;
+            int at = 0, order = 0; // pairs and experts before this lane's expert
+            uint32_t sum = 0, total = 0;
+            for (int j = 0; j < pairs; ++j) {
+                const int xj = __shfl_sync(0xffffffffu, x, j);
+                const uint32_t pj = __shfl_sync(0xffffffffu, passes, j);
+                total += pj;
+                if (xj < x) {
+                    ++at;
+                    order += pj != 0;
+                    sum += pj;
+                }
+            }
+            if (leader)
+                p.tab.experts[order] = make_int4((int)(sum & 0xFFFF) * p.up_cols, (int)(sum >> 16) * p.down_cols,
+                                                 x | n << 16, at);
+            for (int i = __popc(__ballot_sync(0xffffffffu, leader)) + lane; i < p.tab.chunks * 32; i += 32)
+                p.tab.experts[i] = make_int4((int)(total & 0xFFFF) * p.up_cols, (int)(total >> 16) * p.down_cols, 0, pairs);
+            if (in) {
+                p.tab.sorted[at + before] = lane;
+                p.tab.token[at + before] = lane / p.top;
+            }
+            if (lane < 2)
+                p.tickets[lane] = 0;
+        }
+        return;
+    }
+    // More pairs (7 tokens on 60 experts, two each: 25.7 us with this way, one level less and the way
+    // above: 24.2 us).  A pair's place among its expert's is the number of equal ids before it.
     for (int x = tid; x < p.experts; x += MOE_THREADS)
         count[x] = 0;
     for (int i = pairs + tid; i < (pairs + 3) / 4 * 4; i += MOE_THREADS)
@@ -375,6 +416,7 @@ struct MoeGemm {
     uint32_t col_magic;      // n / col_units = umulhi(n, col_magic)
     int splits;              // down: parts of K with units and partial outputs of their own
     int team;                // warps per team
+    int pairs;
     int inter, glu;
 };
 
@@ -423,11 +465,11 @@ struct Unit {
 // Unit u (the same in every lane): its expert is the last of the list whose first unit is at or
 // before u, looked up by the warp's lanes together.
 template <int NT, int MODE>
-__device__ __forceinline__ Unit find_unit(const MoeGemm &p, int u, int lane)
+__device__ __forceinline__ Unit find_unit(const MoeGemm &p, const int4 *list, int u, int lane)
 {
     int start = 0, id = 0, off = 0;
     for (int c = 0; c < p.tab.chunks; ++c) {
-        const int4 e = __ldcg(p.tab.experts + c * 32 + lane);
+        const int4 e = list[c * 32 + lane];
         const int first = MODE != GATE_UP ? e.y : e.x;
         const uint32_t before = __ballot_sync(0xffffffffu, first <= u);
         if (before == 0)
@@ -502,7 +544,18 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
         pdl_wait();
         pdl_launch_dependents();
     }
-    const int4 total = __ldcg(p.tab.experts + p.tab.chunks * 32 - 1);
+    // The list of experts and the tokens of the pairs go to shared memory at once: a look-up in L2 for
+    // each unit, and another for its tokens, would hold up the first products by a microsecond (one
+    // token on 8 experts of 1024 x 1792: 13.9 us without this, 13.2 us with it).
+    int4 *list = reinterpret_cast<int4 *>(smem + G::smem(MODE));
+    int *token = reinterpret_cast<int *>(list + p.tab.chunks * 32);
+    for (int i = tid; i < p.tab.chunks * 32; i += G::WARPS * 32)
+        list[i] = __ldcg(p.tab.experts + i);
+    if (!DOWN)
+        for (int i = tid; i < p.pairs; i += G::WARPS * 32)
+            token[i] = __ldcg(p.tab.token + i);
+    __syncthreads();
+    const int4 total = list[p.tab.chunks * 32 - 1];
     const int units = DOWN ? total.y : total.x;
     // Consecutive units go to different blocks, so that a part round still reaches every SM.
     const int stride = gridDim.x * teams;
@@ -539,7 +592,7 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
             iu = unit_at(++ik);
             if (iu >= units)
                 return;
-            un = find_unit<NT, MODE>(p, iu, lane);
+            un = find_unit<NT, MODE>(p, list, iu, lane);
             ib = 2 * (un.step0 + member);
             ib_end = 2 * un.step1;
         } while (ib >= ib_end);
@@ -590,7 +643,7 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
         int ticket = 0;
         if (team_tid == 0)
             ticket = more ? atomicAdd(p.ticket, 1) : 0;
-        const Unit un = find_unit<NT, MODE>(p, u, lane);
+        const Unit un = find_unit<NT, MODE>(p, list, u, lane);
         const int rows = MODE == DOWN_SIDE ? 2 * un.cols : un.cols; // columns in use on the token side
         float out[MT][NT][4];
 #pragma unroll
@@ -609,7 +662,7 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
 #pragma unroll
             for (int n = 0; n < ND; ++n) {
                 const int c = min(n * 8 + g, rows - 1);
-                const int row = MODE == GATE_UP     ? p.tab.token[un.first + c]
+                const int row = MODE == GATE_UP     ? token[un.first + c]
                                 : MODE == DOWN_SIDE ? 2 * un.first + c
                                                     : 2 * (un.first + c);
                 arow[n] = p.act + (long long)row * p.k + (un.step0 + member) * MOE_ROWS + t * 8;
@@ -1063,7 +1116,7 @@ cudaError_t launch_moe_gemm(MoeGemm &p, int nt, MoeSplit split, bool bf, int mod
     const MoeShape s = shape_of(nt);
     const int smem = s.smem[mode];
     const int v = (bf ? 4 : 0) + which;
-    cudaError_t err = allow_smem<MoeFamily, 8>(reinterpret_cast<const void *>(kernel), v, smem);
+    cudaError_t err = allow_smem<MoeFamily, 8>(reinterpret_cast<const void *>(kernel), v, smem + MOE_TABLES_MOST);
     if (err != cudaSuccess)
         return err;
     p.team = split.team;
@@ -1072,7 +1125,8 @@ cudaError_t launch_moe_gemm(MoeGemm &p, int nt, MoeSplit split, bool bf, int mod
     // Exact while n col_units < 2^32: an expert's unit numbers are below 16 passes x 8 splits x
     // col_units, and col_units is at most 2^11.
     p.col_magic = (uint32_t)((1ull << 32) / p.col_units + 1);
-    return launch_pdl(kernel, dim3(num_sms * s.ctas), dim3(s.warps * 32), (size_t)smem, stream, p);
+    const int tables = p.tab.chunks * 32 * (int)sizeof(int4) + (mode == GATE_UP ? p.pairs * 4 : 0);
+    return launch_pdl(kernel, dim3(num_sms * s.ctas), dim3(s.warps * 32), (size_t)(smem + tables), stream, p);
 }
 
 } // namespace
@@ -1171,6 +1225,7 @@ extern "C" int w4a16_moe_layer(const void *x, int ldx, const void *router, const
     m.ticket = counters + chunks + 1;
     m.status = reinterpret_cast<int *>(ws);
     m.tab = lay.tab;
+    m.pairs = n_tokens * top_k;
     m.k = hidden;
     m.n = 2 * inter;
     m.inter = inter;
