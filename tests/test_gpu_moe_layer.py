@@ -234,3 +234,16 @@ def test_large_inner_activations_stay_finite_in_fp16(w4):
     layer.run()
     assert bool(torch.isfinite(layer.y).all())
     layer.check()
+
+
+@pytest.mark.parametrize("dtype,tokens,experts,top", [
+    ("fp16", 8, 8, 4), ("bf16", 2, 512, 16), ("fp16", 1, 16, 16),   # up to 32 pairs: grouped by one warp
+    ("fp16", 11, 3, 3), ("bf16", 8, 60, 5), ("fp16", 9, 16, 4),     # more; one level of routing, and two
+    ("bf16", 64, 512, 16), ("fp16", 64, 16, 16),                    # the largest tables; every expert 64 pairs
+])
+def test_routing_sizes(w4, dtype, tokens, experts, top):
+    layer = Layer(w4, 26, dtype, tokens, 256, 128, experts, top, group_size=64, router_sigma=1.0)
+    for _ in range(2):
+        layer.y.fill_(float("nan"))
+        layer.run()
+        layer.check()
