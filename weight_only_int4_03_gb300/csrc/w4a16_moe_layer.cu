@@ -29,7 +29,9 @@
 // A unit of work is 64 columns of one expert over all of K (down: or a part of it), done by a team of 1 to 8 warps that take
 // its 128-row steps in turn.  A warp streams its steps through its own ring of cp.async stages, which
 // runs on into its next unit, so no block-wide barrier sits between a copy and its use and the ring
-// stays full across units.  Activations are read from L1/L2 in the MMA's fragment order.
+// stays full across units.  Activations lie in the MMA's fragment order and come through the same ring, each lane's
+// own fragments by its own copies (read from L1/L2 a block ahead they cost a wait per block: one token 46.2
+// us against 44.9, 16 tokens 159 us against 155); columns that no token uses are not copied.
 //
 // Measured, the four launches together: one token, 8 experts of 4096 x 14336, two each, fp16: 46.2 us, 3.9
 // TB/s of weights (the copies themselves run at 5.4 to 6.0 TB/s; routing and the first copies take
@@ -510,11 +512,11 @@ struct MoeGeom {
     static constexpr int CTAS = NT == 1 ? 2 : 3; // blocks per SM
     static constexpr int COLS = 16 * MT;
     static constexpr int SZ = COLS * 2;        // bytes of one scale (or zero) row
-    static constexpr int STAGE = 2048 + 2 * SZ; // codes, scales, zeros
+    static constexpr int WEIGHTS = 2048 + 2 * SZ; // codes, scales, zeros
+    static constexpr int ACT = 1024;              // a tile's activations of a block (one part of them)
     static constexpr int STAGES = 3; // two in flight: at most one step, so at most into the next unit
-    static constexpr int RING = STAGES * STAGE;
-    static constexpr int vals(int mode) { return MT * NT * (mode == DOWN_SIDE ? 2 : 4); } // sums per lane to join
-    static constexpr int smem(int mode) { return WARPS * (RING + vals(mode) * 32 * 4); }
+    static constexpr int stage(int mode) { return WEIGHTS + ACT * (mode == DOWN_TWICE ? 2 : NT); }
+    static constexpr int smem(int mode) { return WARPS * STAGES * stage(mode); }
 };
 
 template <int NT, bool BF, int MODE>
@@ -523,19 +525,20 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
     using G = MoeGeom<NT>;
     constexpr bool DOWN = MODE != GATE_UP;
     constexpr int PARTS = MODE == DOWN_TWICE ? 2 : 1; // activation rows per column
-    constexpr int MT = G::MT, COLS = G::COLS, STAGES = G::STAGES, VALS = G::vals(MODE);
+    constexpr int MT = G::MT, COLS = G::COLS, STAGES = G::STAGES;
+    constexpr int STAGE = G::stage(MODE), RING = STAGES * STAGE;
     // fp16 with one token tile: the two nibble positions keep accumulators of their own, which saves
     // two shifts a word; with two tiles the registers go to the tiles.
     constexpr bool DUAL = !BF && NT == 1;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int drawn[G::WARPS][2];
+    __shared__ int spot[G::WARPS]; // where a warp's sums of the unit lie, in floats
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
     const int teams = G::WARPS / p.team, team = warp / p.team, member = warp - team * p.team;
     const int team_threads = p.team * 32, team_tid = member * 32 + lane;
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * G::RING;
-    const uint8_t *ring_p = smem + warp * G::RING;
-    float *red = reinterpret_cast<float *>(smem + G::WARPS * G::RING); // [warp][VALS][32]
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * RING;
+    const uint8_t *ring_p = smem + warp * RING;
     // Down: the routing tables are those of the launch before the previous one, which had waited for
     // everything older and was complete before the previous one read them; so the first copies of the
     // weights, which only they decide, go out while the gate-up launch drains.  The tables are read
@@ -572,6 +575,10 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
     int iu = u0, ik = -1, ib = 0, ib_end = 0;
     const int32_t *i_w = nullptr; // this lane's piece of block 0, half 0 of the unit's columns
     const uint16_t *i_s = nullptr; // lanes 0-7: chunk `lane` of the expert's scale row 0; 8-15: zeros
+    // This lane's chunk of its activation row's block 0 in each tile.  Columns past the last are not copied:
+    // what the stage holds there goes into sums that nobody reads.
+    const uint16_t *i_a[NT];
+    int i_rows = 0; // columns in use on the token side
     const bool sz_zero = lane >= 8;
     const bool sz_mine = lane < (p.z ? 16 : 8);
     // The team's k-th unit: the first two follow from its number, the others are drawn from a common
@@ -599,36 +606,86 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
         const int n0 = un.col * COLS;
         i_w = p.w + un.expert * p.expert_words + (long long)(n0 >> 7) * p.kblocks * 1024 + (n0 & 127) * 4 + lane * 4;
         i_s = (sz_zero ? p.z : p.s) + un.expert * p.expert_groups * p.n + n0 + (lane & 7) * 8;
+        i_rows = MODE == DOWN_SIDE ? 2 * un.cols : un.cols;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int c = min(n * 8 + g, i_rows - 1);
+            const int row = MODE == GATE_UP     ? token[un.first + c]
+                            : MODE == DOWN_SIDE ? 2 * un.first + c
+                                                : 2 * (un.first + c);
+            i_a[n] = p.act + (long long)row * p.k + t * 8;
+        }
     };
     // The columns of a half 1 are stored with bit 2 flipped, so that the fragment reads below fall on
     // different banks.
     const uint32_t dst0 = ring + lane * 16, dst1 = ring + (lane ^ 4) * 16;
+    auto copy_weights = [&](int stage) {
+        const int32_t *w = i_w + (long long)ib * 1024;
+        const uint32_t d0 = dst0 + stage * STAGE, d1 = dst1 + stage * STAGE;
+        cp_async16_at<0, 0>(d0, w); // 64 columns of half 0, then of half 1
+        cp_async16_at<512, 512>(d0, w);
+        cp_async16_at<1024, 2048>(d1, w);
+        cp_async16_at<1536, 2560>(d1, w);
+        if (sz_mine) {
+            const int grp = p.group_magic ? (int)__umulhi((uint32_t)ib, p.group_magic) : ib;
+            cp_async16_at<2048, 0>(d0, i_s + (long long)grp * p.n);
+        }
+    };
+    // The lane's own fragments: chunks t and 4 + t of its rows.
+    auto copy_activations = [&](int stage, int block) {
+        const uint32_t d = dst0 + stage * STAGE + G::WEIGHTS;
+        const uint16_t *a = i_a[0] + block * 64;
+        if (g < i_rows) {
+            cp_async16_at<0, 0>(d, a);
+            cp_async16_at<512, 64>(d, a);
+            if (MODE == DOWN_TWICE) { // the remainder's row follows the value's
+                cp_async16_at<G::ACT, 0>(d, a + p.k);
+                cp_async16_at<G::ACT + 512, 64>(d, a + p.k);
+            }
+        }
+        if (NT == 2 && 8 + g < i_rows) {
+            a = i_a[NT - 1] + block * 64;
+            cp_async16_at<G::ACT, 0>(d, a);
+            cp_async16_at<G::ACT + 512, 64>(d, a);
+        }
+    };
+    auto advance = [&]() {
+        ++ib;
+        if (!(ib & 1))
+            ib += 2 * (p.team - 1);
+    };
     auto issue = [&](int stage) {
         if (iu < units && ib >= ib_end)
             enter();
         if (iu < units) {
-            const int32_t *w = i_w + (long long)ib * 1024;
-            const uint32_t d0 = dst0 + stage * G::STAGE, d1 = dst1 + stage * G::STAGE;
-            cp_async16_at<0, 0>(d0, w); // 64 columns of half 0, then of half 1
-            cp_async16_at<512, 512>(d0, w);
-            cp_async16_at<1024, 2048>(d1, w);
-            cp_async16_at<1536, 2560>(d1, w);
-            if (sz_mine) {
-                const int grp = p.group_magic ? (int)__umulhi((uint32_t)ib, p.group_magic) : ib;
-                cp_async16_at<2048, 0>(d0, i_s + (long long)grp * p.n);
-            }
-            ++ib;
-            if (!(ib & 1))
-                ib += 2 * (p.team - 1);
+            copy_weights(stage);
+            copy_activations(stage, ib);
+            advance();
         }
         cp_async_commit();
     };
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s)
-        issue(s);
-    if (DOWN) {
-        pdl_wait();
-        pdl_launch_dependents();
+    // The first step, two stages: its weights, and once they are there its activations.
+    static_assert(STAGES == 3, "the copies ahead are one step's");
+    enter();
+    {
+        const int block = ib;
+        const bool any = iu < units;
+        if (any) {
+            copy_weights(0);
+            advance();
+            copy_weights(1);
+            advance();
+        }
+        if (DOWN) {
+            pdl_wait();
+            pdl_launch_dependents();
+        }
+        if (any)
+            copy_activations(0, block);
+        cp_async_commit();
+        if (any)
+            copy_activations(1, block + 1);
+        cp_async_commit();
     }
 
     uint32_t nibble = 0x000F000Fu, base128 = 0x43004300u; // in registers, not known to the compiler
@@ -657,53 +714,15 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
         // The member's steps for ND token tiles.
         auto sweep = [&](auto nd) {
             constexpr int ND = decltype(nd)::value;
-            // This lane's activation row of each tile (a column past the last repeats it).
-            const uint16_t *arow[ND];
-#pragma unroll
-            for (int n = 0; n < ND; ++n) {
-                const int c = min(n * 8 + g, rows - 1);
-                const int row = MODE == GATE_UP     ? token[un.first + c]
-                                : MODE == DOWN_SIDE ? 2 * un.first + c
-                                                    : 2 * (un.first + c);
-                arow[n] = p.act + (long long)row * p.k + (un.step0 + member) * MOE_ROWS + t * 8;
-            }
-            // With one tile the next block's activations are fetched a block ahead.
-            constexpr bool AHEAD = ND == 1 && PARTS == 1;
             const int first = un.step0 + member;
-            uint4 bv[PARTS][ND][2];
-            if (AHEAD && first < un.step1) {
-                const uint4 *ap = reinterpret_cast<const uint4 *>(arow[0]);
-                bv[0][0][0] = ap[0];
-                bv[0][0][1] = ap[4];
-            }
             for (int step = first; step < un.step1; step += p.team) {
                 float lo[MT][ND][4], hi[DUAL ? MT : 1][ND][4], sa[ND][4];
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    uint4 nx[2];
-                    if (AHEAD) {
-                        if (b == 1) // the last step fetches its own first block again
-                            arow[0] += step + p.team < un.step1 ? p.team * MOE_ROWS : 0;
-                        const uint4 *ap = reinterpret_cast<const uint4 *>(arow[0]) + (b ? 0 : 8);
-                        nx[0] = ap[0];
-                        nx[1] = ap[4];
-                    } else {
-#pragma unroll
-                        for (int n = 0; n < ND; ++n) {
-#pragma unroll
-                            for (int r = 0; r < PARTS; ++r) { // the remainder's row follows the value's
-                                const uint4 *ap = reinterpret_cast<const uint4 *>(arow[n] + r * p.k) + b * 8;
-                                bv[r][n][0] = ap[0];
-                                bv[r][n][1] = ap[4];
-                            }
-                            if (b == 1)
-                                arow[n] += p.team * MOE_ROWS;
-                        }
-                    }
                     cp_async_wait<STAGES - 2>();
                     __syncwarp(); // every lane's copies have landed, and the stage before is free
                     issue(stage == 0 ? STAGES - 1 : stage - 1);
-                    const uint8_t *st = ring_p + stage * G::STAGE;
+                    const uint8_t *st = ring_p + stage * STAGE;
                     stage = stage + 1 == STAGES ? 0 : stage + 1;
                     uint2 w[MT][2]; // column g, g + 8 of each tile: words 2 (t >> 1), + 1 of half t & 1
 #pragma unroll
@@ -714,14 +733,20 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
                     constexpr uint32_t ONES = BF ? 0x3F803F80u : 0x3C003C00u;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
+                        uint4 bv[PARTS][ND];
+#pragma unroll
+                        for (int r = 0; r < PARTS; ++r)
+#pragma unroll
+                            for (int n = 0; n < ND; ++n)
+                                bv[r][n] = *reinterpret_cast<const uint4 *>(st + G::WEIGHTS + (r + n) * G::ACT + i * 512 + lane * 16);
 #pragma unroll
                         for (int r = 0; r < PARTS; ++r)
 #pragma unroll
                             for (int n = 0; n < ND; ++n) {
                                 if (b == 0 && i == 0 && r == 0)
-                                    mma16816_zero<BF>(sa[n], ONES, ONES, ONES, ONES, bv[r][n][i].x, bv[r][n][i].y);
+                                    mma16816_zero<BF>(sa[n], ONES, ONES, ONES, ONES, bv[r][n].x, bv[r][n].y);
                                 else
-                                    mma16816<BF>(sa[n], ONES, ONES, ONES, ONES, bv[r][n][i].x, bv[r][n][i].y);
+                                    mma16816<BF>(sa[n], ONES, ONES, ONES, ONES, bv[r][n].x, bv[r][n].y);
                             }
 #pragma unroll
                         for (int m = 0; m < MT; ++m) {
@@ -760,7 +785,7 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
                             for (int r = 0; r < PARTS; ++r) {
 #pragma unroll
                                 for (int n = 0; n < ND; ++n) {
-                                    const uint4 v = bv[r][n][i];
+                                    const uint4 v = bv[r][n];
                                     if (b == 0 && i == 0 && r == 0)
                                         mma16816_zero<BF>(lo[m][n], a0, a1, a2, a3, v.x, v.y);
                                     else
@@ -768,7 +793,7 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
                                 }
 #pragma unroll
                                 for (int n = 0; n < ND; ++n) {
-                                    const uint4 v = bv[r][n][i];
+                                    const uint4 v = bv[r][n];
                                     if (!DUAL)
                                         mma16816<BF>(lo[m][n], c0, c1, c2, c3, v.z, v.w);
                                     else if (b == 0 && i == 0 && r == 0)
@@ -782,7 +807,7 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
                         for (int r = 0; r < PARTS; ++r)
 #pragma unroll
                             for (int n = 0; n < ND; ++n)
-                                mma16816<BF>(sa[n], ONES, ONES, ONES, ONES, bv[r][n][i].z, bv[r][n][i].w);
+                                mma16816<BF>(sa[n], ONES, ONES, ONES, ONES, bv[r][n].z, bv[r][n].w);
                     }
                     // End of a group (or of a step, whose two blocks then share one): scale the sums.
                     const uint8_t *sz = st + 2048;
@@ -828,10 +853,6 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
                         else
                             flush(std::false_type(), b == 0);
                     }
-                    if (AHEAD) {
-                        bv[0][0][0] = nx[0];
-                        bv[0][0][1] = nx[1];
-                    }
                 }
             }
         };
@@ -840,7 +861,13 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
         else
             sweep(std::integral_constant<int, NT>());
 
-        // --- the team's warps join their sums (fixed order) -----------------------------------
+        // --- the team's warps join their sums (fixed order), in their free stages ---------------
+        const int free_stage = stage == 0 ? STAGES - 1 : stage - 1;
+        float *red = reinterpret_cast<float *>(smem + warp * RING + free_stage * STAGE); // [sum][lane]
+        static_assert(MT * NT * (MODE == DOWN_SIDE ? 2 : 4) * 128 <= STAGE, "the sums fit a stage");
+        __syncwarp(); // every lane has read the stage
+        if (lane == 0)
+            spot[warp] = (warp * RING + free_stage * STAGE) / 4;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -848,23 +875,23 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
                 if (MODE == DOWN_SIDE) { // columns 2 t and 2 t + 1 are a pair's value and remainder
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
-                        red[(warp * VALS + (m * NT + n) * 2 + c) * 32 + lane] = out[m][n][2 * c] + out[m][n][2 * c + 1];
+                        red[((m * NT + n) * 2 + c) * 32 + lane] = out[m][n][2 * c] + out[m][n][2 * c + 1];
                 } else {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        red[(warp * VALS + (m * NT + n) * 4 + i) * 32 + lane] = out[m][n][i];
+                        red[((m * NT + n) * 4 + i) * 32 + lane] = out[m][n][i];
                 }
             }
         team_sync(team, team_threads);
         if (team_tid == 0)
             drawn[team][k & 1] = 2 * stride + ticket; // unit k + 2, known to the team after the next barrier
-        const float *tr = red + team * p.team * VALS * 32;
+        const float *sums = reinterpret_cast<const float *>(smem);
         auto joined = [&](int v, int ln) {
             float s = 0.f;
 #pragma unroll
             for (int w = 0; w < G::WARPS; ++w)
                 if (w < p.team)
-                    s += tr[(w * VALS + v) * 32 + ln];
+                    s += sums[spot[team * p.team + w] + v * 32 + ln];
             return BF ? s : s * (1.f / CODE_UNIT);
         };
         if (!DOWN) {
@@ -896,7 +923,7 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
                 __stcg(p.part + ((long long)pair * p.splits + un.split) * p.n + un.col * COLS + c, joined(v, ln));
             }
         }
-        team_sync(team, team_threads); // `red` is free
+        team_sync(team, team_threads); // the stages are free
     }
     cp_async_wait<0>();
 }
