@@ -247,3 +247,22 @@ def test_routing_sizes(w4, dtype, tokens, experts, top):
         layer.y.fill_(float("nan"))
         layer.run()
         layer.check()
+
+
+@pytest.mark.parametrize("dtype,tokens,experts,top", [("fp16", 1, 8, 2), ("bf16", 6, 16, 4), ("fp16", 20, 4, 2)])
+def test_new_inputs_in_one_workspace(w4, dtype, tokens, experts, top):
+    """Nothing of a call is left in the next: the same layer on other rows, back to back."""
+    import torch
+    layer = Layer(w4, 27, dtype, tokens, 512, 384, experts, top, zeros=True)
+    rows = [torch.randn_like(layer.x) * s for s in (1.0, 0.5, 2.0, 1.0)]
+    outs = [torch.empty_like(layer.y) for _ in rows]
+    for x, y in zip(rows, outs):
+        layer.x.copy_(x)
+        layer.run(y=y)
+    for x, y in zip(rows, outs):
+        layer.x.copy_(x)
+        layer.ws.zero_()
+        layer.run()
+        torch.cuda.synchronize()
+        assert torch.equal(layer.y, y)
+        layer.check()
