@@ -33,10 +33,10 @@
 // own fragments by its own copies (read from L1/L2 a block ahead they cost a wait per block: one token 46.2
 // us against 44.9, 16 tokens 159 us against 155); columns that no token uses are not copied.
 //
-// Measured, the four launches together: one token, 8 experts of 4096 x 14336, two each, fp16: 46.2 us, 3.9
+// Measured, the four launches together: one token, 8 experts of 4096 x 14336, two each, fp16: 44.8 us, 4.1
 // TB/s of weights (the copies themselves run at 5.4 to 6.0 TB/s; routing and the first copies take
-// 10 us); 16 tokens: 159 us, 4.7 TB/s; 64 tokens, bf16: 374 us, bound by the MMAs and the conversion;
-// 7 tokens on 128 experts of 2048 x 768, eight each, bf16: 38.1 us; one token on 1024 x 1792: 13.2 us of
+// 10 us); 16 tokens: 155 us, 4.8 TB/s; 64 tokens, bf16: 369 us, bound by the MMAs and the conversion;
+// 7 tokens on 128 experts of 2048 x 768, eight each, bf16: 37.6 us; one token on 1024 x 1792: 12.8 us of
 // latencies.
 #include <math.h>
 
