@@ -54,6 +54,11 @@ constexpr int MOE_MAX_PAIRS = MOE_MAX_TOKENS * MOE_MAX_TOP;
 constexpr int MOE_WARPS = 8; // of a routing block
 constexpr int MOE_THREADS = MOE_WARPS * 32;
 constexpr int MOE_CHUNK = 4;   // tokens per routing block
+// The counters of a workspace lie at its start, each at a place that no size of a call moves: a call of
+// other sizes finds zeros where one before it has arrived and left, and draws from its own.
+constexpr int MOE_ALL_CHUNKS = MOE_MAX_TOKENS / MOE_CHUNK; // arrivals of a chunk's blocks, then of the chunks
+constexpr int MOE_TICKETS = MOE_ALL_CHUNKS + 1;            // units drawn by the two products
+constexpr int MOE_COUNTERS = MOE_TICKETS + 2;
 constexpr int MOE_ONE_LEVEL = MOE_WARPS; // tokens whose softmax and top-k one block does
 // Pairs per expert up to which a down tile holds both parts of four pairs side by side (7 tokens on 128
 // experts, 1.2 pairs each: 44.8 us against 46.4 us one after the other; 16 tokens on 8, four each: 175 us
@@ -94,8 +99,7 @@ struct RouteParams {
     float *logits;
     int *topk_ids;
     float *topk_weights;
-    int *counters; // [chunks], then one
-    int *tickets;  // [2], zeroed for the products that follow
+    int *counters; // [MOE_COUNTERS]; the tickets are zeroed for the products that follow
     MoeTables tab;
     int ldx, tokens, hidden, experts, top, renorm;
     int up_cols, down_cols; // units per expert and pass
@@ -290,9 +294,9 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const Rout
     __syncthreads();
     if (!one_level) {
         if (tid == 0) {
-            const int last = arrive_counter(p.counters + gridDim.y) == (int)gridDim.y - 1;
+            const int last = arrive_counter(p.counters + MOE_ALL_CHUNKS) == (int)gridDim.y - 1;
             if (last)
-                p.counters[gridDim.y] = 0;
+                p.counters[MOE_ALL_CHUNKS] = 0;
             is_last = last;
         }
         __syncthreads();
@@ -335,7 +339,7 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const Rout
                 p.tab.token[at + before] = lane / p.top;
             }
             if (lane < 2)
-                p.tickets[lane] = 0;
+                p.counters[MOE_TICKETS + lane] = 0;
         }
         return;
     }
@@ -387,7 +391,7 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const Rout
             passes += __shfl_sync(0xffffffffu, u, 31);
         }
         if (lane < 2)
-            p.tickets[lane] = 0;
+            p.counters[MOE_TICKETS + lane] = 0;
         for (int i = (int)(list & 0xFFFF) + lane; i < p.tab.chunks * 32; i += 32)
             p.tab.experts[i] = make_int4((int)(passes & 0xFFFF) * p.up_cols, (int)(passes >> 16) * p.down_cols, 0,
                                          (int)(list >> 16));
@@ -995,9 +999,9 @@ int max_splits(int pairs)
 MoeLayout moe_layout(char *ws, int tokens, int hidden, int inter, int experts, int top)
 {
     MoeLayout l;
-    const int chunks = (tokens + MOE_CHUNK - 1) / MOE_CHUNK, pairs = tokens * top;
+    const int pairs = tokens * top;
     l.counters = HEADER_BYTES;
-    l.logits = round_up(l.counters + 4LL * (chunks + 3), 256);
+    l.logits = round_up(l.counters + 4LL * MOE_COUNTERS, 256);
     l.tables = round_up(l.logits + 4LL * tokens * experts, 256);
     long long at = l.tables;
     auto take = [&](long long n) {
@@ -1224,7 +1228,6 @@ extern "C" int w4a16_moe_layer(const void *x, int ldx, const void *router, const
     r.topk_ids = topk_ids;
     r.topk_weights = topk_weights;
     r.counters = counters;
-    r.tickets = counters + chunks + 1;
     r.tab = lay.tab;
     r.ldx = ldx;
     r.tokens = n_tokens;
@@ -1249,7 +1252,7 @@ extern "C" int w4a16_moe_layer(const void *x, int ldx, const void *router, const
     m.act = r.xf;
     m.h = reinterpret_cast<uint16_t *>(ws + lay.h);
     m.part = reinterpret_cast<float *>(ws + lay.part);
-    m.ticket = counters + chunks + 1;
+    m.ticket = counters + MOE_TICKETS;
     m.status = reinterpret_cast<int *>(ws);
     m.tab = lay.tab;
     m.pairs = n_tokens * top_k;
