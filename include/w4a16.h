@@ -443,8 +443,8 @@ int w4a16_rope_append(const void *q, int ldq, const void *k, int ldk, const void
                       unsigned flags, cudaStream_t stream);
 
 /* Workspace bytes of w4a16_paged_attention (num_sms <= 0: the current device; 0 for sizes that it
- * rejects).  Zero-filled once after allocation, as w4a16_gemm's; calls that run concurrently need
- * separate workspaces. */
+ * rejects).  Zero-filled once after allocation, after which it serves calls of any sizes that need no
+ * more bytes, in any order; calls that run concurrently need separate workspaces. */
 size_t w4a16_paged_attention_workspace_size(int batch, int n_heads, int n_kv_heads, int head_dim,
                                             int num_sms);
 
@@ -477,7 +477,8 @@ int w4a16_paged_attention(const void *q, int ldq, const void *k_cache, const voi
                           int window, float scale, unsigned flags, cudaStream_t stream);
 
 /* Workspace bytes of w4a16_moe_layer (0 for sizes that it rejects).  Zero-filled once after
- * allocation; calls that run concurrently need separate workspaces. */
+ * allocation, after which it serves calls of any sizes that need no more bytes, in any order; calls that
+ * run concurrently need separate workspaces. */
 size_t w4a16_moe_layer_workspace_size(int n_tokens, int hidden, int inter, int n_experts, int top_k);
 
 /* A whole expert layer with 4-bit weights for a few tokens: router product, softmax, top-k, the

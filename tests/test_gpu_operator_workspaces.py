@@ -3,6 +3,7 @@ changes: every call gives the bits that it gives in a zeroed workspace of its ow
 operator's (the tolerances are those of the operators' own tests)."""
 import pytest
 
+from test_gpu_attention import Case
 from test_gpu_moe_layer import Layer
 
 pytestmark = pytest.mark.gpu
@@ -44,3 +45,31 @@ def test_expert_layer_at_changing_token_counts(w4, kw):
             torch.cuda.synchronize()
             assert torch.equal(layer.y, alone), f"{t} tokens"
         assert w4.w4a16_status(shared) == 0
+
+
+def test_attention_at_changing_batches_and_widths(w4):
+    """Partial results of one call never lie where another call counts arrivals: single long sequences
+    between batches of thousands of rows, three head widths."""
+    import torch
+    cases = dict(
+        long=Case(41, "bf16", [9001], 40, 8, 128, 32),
+        wide=Case(42, "fp16", [37 * i % 700 for i in range(300)], 16, 8, 128, 16),
+        d256=Case(43, "fp16", [5000, 17], 8, 2, 256, 16),
+        many=Case(44, "bf16", [53 * i % 300 for i in range(1500)], 8, 4, 64, 16),
+        one=Case(45, "fp16", [20000], 8, 1, 64, 64),
+        two=Case(46, "bf16", [20000, 9], 8, 1, 256, 64, window=15000),
+    )
+    alone = {}
+    for name, case in cases.items():
+        case.run(w4, case.workspace(w4))
+        case.check()
+        alone[name] = case.out.clone(), case.lse.clone()
+    shared = max((case.workspace(w4) for case in cases.values()), key=lambda ws: ws.numel())
+    for name in ("long", "wide", "d256", "many", "long", "one", "many", "two", "wide", "d256", "many", "one", "wide"):
+        case = cases[name]
+        for x in (case.out, case.lse):
+            x.fill_(float("nan"))
+        case.run(w4, shared)
+        torch.cuda.synchronize()
+        assert torch.equal(case.out, alone[name][0]) and torch.equal(case.lse, alone[name][1]), name
+    assert w4.w4a16_status(shared) == 0

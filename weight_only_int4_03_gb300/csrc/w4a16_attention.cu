@@ -452,6 +452,9 @@ __global__ void __launch_bounds__(ATT_THREADS, AttGeom<D>::CTAS)
             // The parts of a row are those of the blocks c_lo to c_hi, the owners of its first and its
             // last unit.  The last block to arrive joins them; where there are more than ATT_FAN, the
             // last of every ATT_FAN of them joins those first, so that many blocks share the reading.
+            // A row's counter is that of its first block, in which no other row of several parts starts;
+            // a group's likewise (a group of one part, which could share its block with the next row's
+            // first, does not count).
             const int c_lo = owner_of(row_u0), c_hi = owner_of(row_u0 + seq_units - 1);
             const int lo_slot = begin_of(c_lo) >= row_u0 ? 0 : 1, parts = c_hi - c_lo + 1;
             const int group0 = ((int)blockIdx.x - c_lo) / ATT_FAN * ATT_FAN; // this block's group
@@ -467,7 +470,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttGeom<D>::CTAS)
                 const int from = c_lo + (last_level ? 0 : group0);
                 __syncthreads();
                 if (tid == 0) {
-                    int *counter = last_level ? p.counters + (long long)b * rows_per_seq + row : p.group_counters + from;
+                    int *counter = last_level ? p.counters + c_lo : p.group_counters + from;
                     const int last = arrive_counter(counter) == n - 1;
                     if (last)
                         *counter = 0;
@@ -592,22 +595,27 @@ cudaError_t att_kernel(bool bf, bool pack, AttKernel &kernel, int &smem)
     return allow_smem<AttGeom<D>, 4>(reinterpret_cast<const void *>(kernel), v, smem);
 }
 
-struct AttLayout {
-    long long group_counters, counters, partials, total;
-};
-
 int att_grid(int num_sms, int head_dim)
 {
     return num_sms * (head_dim == 64 ? AttGeom<64>::CTAS : head_dim == 128 ? AttGeom<128>::CTAS : AttGeom<256>::CTAS);
 }
 
-AttLayout att_layout(int batch, int rows_per_seq, int head_dim, int grid)
+// A workspace: status, the counters, the partials.  The counters' places are the same for calls of all
+// sizes on a device (a counter per block of the largest grid), so that no call's partials lie where
+// another one's counters have to be zero.
+struct AttLayout {
+    long long group_counters, counters, partials, total;
+};
+
+AttLayout att_layout(int head_dim, int num_sms)
 {
     AttLayout l;
+    const long long blocks = att_grid(num_sms, 64);
+    static_assert(AttGeom<64>::CTAS >= AttGeom<128>::CTAS && AttGeom<64>::CTAS >= AttGeom<256>::CTAS, "the largest grid");
     l.group_counters = HEADER_BYTES;
-    l.counters = l.group_counters + 4LL * grid;
-    l.partials = round_up(l.counters + 4LL * batch * rows_per_seq, 256);
-    l.total = l.partials + (long long)grid * ATT_SLOTS * ATT_ROWS * (head_dim + 2) * 4;
+    l.counters = l.group_counters + 4 * blocks;
+    l.partials = round_up(l.counters + 4 * blocks, 256);
+    l.total = l.partials + (long long)att_grid(num_sms, head_dim) * ATT_SLOTS * ATT_ROWS * (head_dim + 2) * 4;
     return l;
 }
 
@@ -637,8 +645,7 @@ extern "C" size_t w4a16_paged_attention_workspace_size(int batch, int n_heads, i
         return 0;
     if (num_sms <= 0 && sm_count(&num_sms) != cudaSuccess)
         return 0;
-    const int tiles = (n_heads / n_kv_heads + ATT_ROWS - 1) / ATT_ROWS;
-    return (size_t)att_layout(batch, n_kv_heads * tiles, head_dim, att_grid(num_sms, head_dim)).total;
+    return (size_t)att_layout(head_dim, num_sms).total;
 }
 
 extern "C" int w4a16_paged_attention(const void *q, int ldq, const void *k_cache, const void *v_cache,
@@ -682,7 +689,7 @@ extern "C" int w4a16_paged_attention(const void *q, int ldq, const void *k_cache
         return status_of(STAGE_RESOURCE, err);
     const int group = n_heads / n_kv_heads, tiles = (group + ATT_ROWS - 1) / ATT_ROWS;
     const int grid = att_grid(num_sms, head_dim);
-    const AttLayout lay = att_layout(batch, n_kv_heads * tiles, head_dim, grid);
+    const AttLayout lay = att_layout(head_dim, num_sms);
     if (workspace_bytes < (size_t)lay.total)
         return status_of(STAGE_ARG, W4A16_ARG_WORKSPACE);
     char *ws = static_cast<char *>(workspace);
