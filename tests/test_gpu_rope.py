@@ -201,3 +201,20 @@ def test_side_stream_and_graph(w4):
         graph.replay()
     side.synchronize()
     check(case, case.q_out, *before)
+
+
+@pytest.mark.parametrize("heads", [1, 3, 5, 8])
+@pytest.mark.parametrize("dim,rot", [(64, 64), (40, 12)])
+def test_q_alone_looks_at_no_cache_argument(w4, heads, dim, rot):
+    """Without KV heads the slots and the cache's sizes mean nothing, whatever the number of heads."""
+    import torch
+    case = Case(6, "fp16", 9, heads, 1, dim, rot, [rot // 2], 8)
+    q = case.parts()[0]
+    for slots in (None, torch.full((9,), 1 << 40, dtype=torch.int64, device="cuda")):
+        case.q_out.fill_(float("nan"))
+        w4.w4a16_rope_append(q, None, None, case.q_out, None, None, case.table, case.positions, slots, case.status, 9,
+                             heads, 0, dim, rot, [rot // 2], case.max_pos, 1, 1, ldq=case.ld)
+        torch.cuda.synchronize()
+        y, tol, _ = case.reference()
+        assert bool(((case.q_out.double() - y[:, :heads]).abs() <= tol[:, :heads] + 2.0 ** -25).all())
+        assert int(case.status.item()) == 0

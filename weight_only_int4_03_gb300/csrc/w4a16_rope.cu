@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(256, ROPE_PER_SM / 256) rope_vec_kernel(const 
     const bool pairs = j < p.rot / 16 && h0 < all - p.kv;
     const bool halves = j < p.rot / 16 && !p.adjacent;
     const int at0 = halves ? 8 * j : 16 * j, at1 = halves ? half + 8 * j : 16 * j + 8;
-    const bool cached = h0 + ROPE_HEADS > p.heads;
+    const bool cached = p.kv > 0 && h0 + ROPE_HEADS > p.heads;
     const int32_t *positions = p.positions + (long long)axis_of(p, 8 * j) * p.ld_pos;
     const int axis0 = axis_of(p, 8 * j), axis1 = CUTS && pairs ? axis_of(p, 8 * j + 7) : axis0;
 
