@@ -148,3 +148,14 @@ def test_moe_layer_nothing_to_do_and_workspace(w4):
     assert size(65, 512, 384, 8, 2) == 0 and size(3, 500, 384, 8, 2) == 0 and size(3, 512, 384, 8, 9) == 0
     # Enough for the pairs' activations (two rows each) and outputs.
     assert size(64, 512, 384, 8, 2) >= 128 * (384 * 4 + 512 * 4)
+
+
+# Heads too wide for one launch: refused after every look at a pointer, before any at the device.
+@pytest.mark.parametrize("kw", [
+    dict(heads=1 << 20, kv=0, k=P + 1, v=P + 1, kc=P + 1, vc=P + 1, slots=P + 1, page=0, n_pages=-1),
+    dict(heads=1 << 20, kv=0, k=None, v=None, kc=None, vc=None, slots=None),
+    dict(heads=0, kv=1 << 19, q=P + 1, q_out=P + 1),
+], ids=("q_alone_odd", "q_alone_null", "kv_alone_odd"))
+def test_rope_pointers_of_absent_heads_are_not_looked_at(w4, kw):
+    wide = dict(dim=1024, rot=1024, sections=[512], ldq=1 << 30, ldqo=1 << 30, ldk=1 << 30, ldv=1 << 30)
+    assert staged(rope_status(w4, **{**wide, **kw})) == (1, OVERFLOW)

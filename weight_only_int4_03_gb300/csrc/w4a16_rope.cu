@@ -303,6 +303,10 @@ extern "C" int w4a16_rope_append(const void *q, int ldq, const void *k, int ldk,
     if (!cos_sin || !positions || (n_heads > 0 && (!q || !q_out)) ||
         (n_kv_heads > 0 && (!k || !v || !k_cache || !v_cache || !slots)))
         return status_of(STAGE_ARG, W4A16_ARG_NULL);
+    if (n_heads == 0) // what absent heads would use is not looked at, its alignment included
+        q = nullptr, q_out = nullptr;
+    if (n_kv_heads == 0)
+        k = nullptr, v = nullptr, k_cache = nullptr, v_cache = nullptr, slots = nullptr;
     const long long qw = (long long)n_heads * head_dim, kw = (long long)n_kv_heads * head_dim;
     if (qw > 0x7FFFFFFFLL || kw > 0x7FFFFFFFLL || (long long)n_heads + 2LL * n_kv_heads > (1 << 20))
         return status_of(STAGE_ARG, W4A16_ARG_OVERFLOW);
