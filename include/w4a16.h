@@ -478,7 +478,7 @@ int w4a16_paged_attention(const void *q, int ldq, const void *k_cache, const voi
 
 /* Workspace bytes of w4a16_moe_layer (0 for sizes that it rejects).  Zero-filled once after
  * allocation, after which it serves calls of any sizes that need no more bytes, in any order; calls that
- * run concurrently need separate workspaces. */
+ * run concurrently need separate workspaces.  More tokens never need fewer bytes. */
 size_t w4a16_moe_layer_workspace_size(int n_tokens, int hidden, int inter, int n_experts, int top_k);
 
 /* A whole expert layer with 4-bit weights for a few tokens: router product, softmax, top-k, the

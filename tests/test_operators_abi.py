@@ -159,3 +159,11 @@ def test_moe_layer_nothing_to_do_and_workspace(w4):
 def test_rope_pointers_of_absent_heads_are_not_looked_at(w4, kw):
     wide = dict(dim=1024, rot=1024, sections=[512], ldq=1 << 30, ldqo=1 << 30, ldk=1 << 30, ldv=1 << 30)
     assert staged(rope_status(w4, **{**wide, **kw})) == (1, OVERFLOW)
+
+
+@pytest.mark.parametrize("hidden,inter,experts,top", [(2048, 768, 128, 8), (4096, 14336, 8, 2), (256, 128, 1, 1),
+                                                      (512, 256, 60, 5), (256, 128, 512, 16)])
+def test_moe_layer_workspace_never_shrinks_with_tokens(w4, hidden, inter, experts, top):
+    """A workspace for the most tokens of a program serves its smaller calls."""
+    sizes = [w4.w4a16_moe_layer_workspace_size(t, hidden, inter, experts, top) for t in range(1, 65)]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))

@@ -996,6 +996,13 @@ int max_splits(int pairs)
     return pairs >= 128 ? 1 : pairs >= 64 ? 2 : pairs >= 32 ? 4 : 8;
 }
 
+// Rows of partial outputs that a workspace has room for: what these pairs need in as many parts, and
+// what any fewer pairs need, so that a workspace for the most tokens serves fewer.
+long long part_rows(int pairs)
+{
+    return pairs < 32 ? 8LL * pairs : pairs < 256 ? 256 : pairs;
+}
+
 MoeLayout moe_layout(char *ws, int tokens, int hidden, int inter, int experts, int top)
 {
     MoeLayout l;
@@ -1018,7 +1025,7 @@ MoeLayout moe_layout(char *ws, int tokens, int hidden, int inter, int experts, i
     l.xf = round_up(at, 256);
     l.h = round_up(l.xf + 2LL * tokens * hidden, 256);
     l.part = round_up(l.h + 4LL * pairs * inter, 256);
-    l.total = round_up(l.part + 4LL * pairs * max_splits(pairs) * hidden, 256);
+    l.total = round_up(l.part + 4LL * part_rows(pairs) * hidden, 256);
     return l;
 }
 
