@@ -250,3 +250,48 @@ def test_rows_in_many_parts(w4, kw):
     torch.cuda.synchronize()
     assert torch.equal(case.out, first) and torch.equal(case.lse, lse)
     assert w4.w4a16_status(ws) == 0
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("dim,heads,kv,batch", [(64, 8, 4, 120), (64, 64, 4, 120), (128, 8, 4, 80), (128, 48, 4, 80),
+                                                (256, 8, 4, 40), (256, 64, 4, 40)])
+@pytest.mark.parametrize("gap", [12.0, 17.4, 21.0])
+def test_a_long_tail_under_dominant_positions_counts(w4, dtype, dim, heads, kv, batch, gap):
+    """A few keys `gap` above thousands of equal ones whose values carry the output: the tail's p, 2^-17 to
+    2^-30, is held as in l.
+
+    Tolerance: the scores are single products, so p is off by 2^-20 of itself at most (the score's rounding in
+    base 2 at 30, and exp2), plus 2^-17 (bf16's two parts), or 2^-23 and an absolute 2^-40 (fp16's): together
+    below 2^-16 of the output and, fp16, 2^-40 / p.  Sums of equal signs and their join: 2^-13 at most (the
+    MMA cuts off at 2^-23 of the sum, 16 positions at a time).  Then the last rounding.
+    """
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(18)
+    dt = torch.float16 if dtype == "fp16" else torch.bfloat16
+    n, page, scale = 2500, 128, dim ** -0.5
+    pages = -(-n // page)
+    dense = lambda: torch.randn((batch, n, kv, dim), generator=g, device="cuda", dtype=dt)
+    k, v = dense(), dense().abs_().add_(1).mul_(8192)
+    q = torch.zeros((batch, heads, dim), dtype=dt, device="cuda")
+    q[:, :, 0] = 16
+    k[..., 0] = 0
+    k[:, :64:16, :, 0] = gap / (16 * scale)  # one in the first sixteen positions of every warp
+    v[:, :64:16] = 0
+    pad = lambda x: torch.cat([x, torch.full_like(x[:, :pages * page - n], float("nan"))], 1).view(-1, page, kv, dim)
+    out, lse = torch.empty_like(q), torch.empty((batch, heads), device="cuda")
+    table = torch.arange(batch * pages, device="cuda", dtype=torch.int32).view(batch, pages)
+    lens = torch.full((batch,), n, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(w4.w4a16_paged_attention_workspace_size(batch, heads, kv, dim), dtype=torch.uint8, device="cuda")
+    w4.w4a16_paged_attention(q, pad(k), pad(v), out, table, lens, ws, batch, heads, kv, dim, page, batch * pages, pages,
+                             scale, w4.W4A16_FLAG_BF16 if dtype == "bf16" else 0, lse=lse)
+    torch.cuda.synchronize()
+    logits = k[..., 0].double() * 16 * scale  # [batch, n, kv]
+    p = torch.exp(logits - logits.amax(1, keepdim=True))
+    ref = torch.einsum("bnc,bncd->bcd", p, v.double()) / p.sum(1)[..., None]
+    ref = ref.repeat_interleave(heads // kv, 1)
+    err = ((out.double() - ref).abs() / ref).max()
+    tol = UNIT[dtype] + 2.0 ** -16 + 2.0 ** -13 + (2.0 ** -40 / float(p.min()) if dtype == "fp16" else 0.0)
+    subnormal = 2.0 ** -25 / float(ref.min()) if dtype == "fp16" else 0.0
+    assert float(err) <= tol + subnormal, (float(err), tol)
+    want = torch.logsumexp(logits, 1).repeat_interleave(heads // kv, 1)
+    assert bool(((lse.double() - want).abs() <= 2.0 ** -14 + 2.0 ** -22 * want.abs()).all())

@@ -24,9 +24,12 @@
 //     partial results at a time, so more than 16 parts are joined in two levels, sixteen at a time by as many
 //     blocks: 131072 positions of one KV head of 8 x 128 took 55 us with one level and take 25.
 // Softmax runs in fp32 in base 2.  p is not rounded to 16 bits for the value product: it goes in as
-// a 16-bit part and the 16-bit remainder (p - hi is exact in fp32), which keeps 2^-17 (bf16) or
-// better of p.  With at most eight heads per KV head the remainder takes the upper eight rows of
-// the same MMA, which are empty then; with more it costs a second MMA.
+// a 16-bit part and the 16-bit remainder (p - hi is exact in fp32).  bf16 keeps 2^-17 of any p so, the
+// two parts' sixteen bits; a third part would take a further MMA.  fp16's parts hold 22 bits but end at
+// 2^-25, so p goes in times 2^15 (exact, and p <= 1 stays in range), which keeps 2^-23 of p down to 2^-17
+// and an absolute 2^-40 below: a long tail under one dominant position counts in the output as it does in l
+// (without the factor, p below 2^-25 was in l alone).  With at most eight heads per KV head the remainder
+// takes the upper eight rows of the same MMA, which are empty then; with more it costs a second MMA.
 #include <type_traits>
 
 #include "w4a16_ops.cuh"
@@ -103,6 +106,8 @@ __global__ void __launch_bounds__(ATT_THREADS, AttGeom<D>::CTAS)
     using G = AttGeom<D>;
     constexpr int KS = D / 16; // k steps of the score product
     constexpr int NT = D / 8;  // 8-wide output tiles
+    // What p is multiplied by for the value product, and its inverse for the outputs.
+    constexpr float UP = BF ? 1.f : 32768.f, DOWN = 1.f / UP;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int prefix[ATT_MAX_BATCH + 1]; // numbers of one (KV head, head tile) before sequence b
     __shared__ int warp_sum[ATT_WARPS];
@@ -340,11 +345,12 @@ __global__ void __launch_bounds__(ATT_THREADS, AttGeom<D>::CTAS)
                 const float pa = exp2f(a - base), pb = exp2f(b2 - base), pc = exp2f(c2 - base),
                             pd = exp2f(d2 - base);
                 l = l * f + ((pa + pb) + (pc + pd));
-                h_lo = pack2<BF>(pa, pb);
-                h_hi = pack2<BF>(pc, pd);
+                const float sa = pa * UP, sb = pb * UP, sc = pc * UP, sd = pd * UP;
+                h_lo = pack2<BF>(sa, sb);
+                h_hi = pack2<BF>(sc, sd);
                 const float2 ra = unpack2<BF>(h_lo), rc = unpack2<BF>(h_hi);
-                r_lo = pack2<BF>(pa - ra.x, pb - ra.y);
-                r_hi = pack2<BF>(pc - rc.x, pd - rc.y);
+                r_lo = pack2<BF>(sa - ra.x, sb - ra.y);
+                r_hi = pack2<BF>(sc - rc.x, sd - rc.y);
             };
             soften(m0, l0, s0[0], s0[1], s1[0], s1[1], f0, hi0, hi1, lo0, lo1);
             if (!PACK)
@@ -435,7 +441,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttGeom<D>::CTAS)
                 sum.w += f * x.w;
             }
             if (whole) {
-                const float r = l == 0.f ? 0.f : 1.f / l;
+                const float r = l == 0.f ? 0.f : DOWN / l;
                 uint2 w2;
                 w2.x = pack2<BF>(sum.x * r, sum.y * r);
                 w2.y = pack2<BF>(sum.z * r, sum.w * r);
@@ -543,7 +549,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttGeom<D>::CTAS)
                                 continue;
                             const bool first_quad = i % (D / 4) == 0;
                             if (last_level) {
-                                const float r = l[k] == 0.f ? 0.f : 1.f / l[k];
+                                const float r = l[k] == 0.f ? 0.f : DOWN / l[k];
                                 uint2 w2;
                                 w2.x = pack2<BF>(sum[k].x * r, sum[k].y * r);
                                 w2.y = pack2<BF>(sum[k].z * r, sum[k].w * r);
