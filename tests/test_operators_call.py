@@ -104,3 +104,57 @@ def test_wrapper_raises_the_library_error(w4):
     with pytest.raises(w4.W4A16Error) as e:
         w4.w4a16_rope_append(P, P, P, P, P, P, P, P, P, None, 4, 4, 2, 128, 128, [60], 100, 16, 8, stream=0)
     assert e.value.status == (1 << 16) | 3
+
+
+def outcome(call, args):
+    try:
+        return call(*args)
+    except Exception as e:
+        return type(e)
+
+
+class Whole:
+    def __index__(self):
+        return 63
+
+
+@pytest.mark.parametrize("name,spoil,want", [
+    # numpy's scalars and whatever counts as an integer or a number
+    ("w4a16_rope_append", dict(a23=np.int64(63)), SHAPE), ("w4a16_rope_append", dict(a23=np.uint8(63)), SHAPE),
+    ("w4a16_rope_append", dict(a23=Whole()), SHAPE), ("w4a16_rope_append", dict(a28=True, a23=63), FLAGS),
+    ("w4a16_paged_attention", dict(a23=np.float32(0.5), a24=8), FLAGS),
+    ("w4a16_paged_attention", dict(a23=np.int32(1), a24=8), FLAGS),
+    ("w4a16_paged_attention", dict(a23=1, a14=np.int64(0), a24=8), FLAGS),
+    # what a parameter does not hold (in calls that are refused for another reason, were it taken)
+    ("w4a16_rope_append", dict(a23=63, a19=(1 << 32) - 1), OverflowError),
+    ("w4a16_rope_append", dict(a23=63, a28=1 << 32), OverflowError),
+    ("w4a16_rope_append", dict(a23=63, a28=np.int64(-1)), OverflowError),
+    ("w4a16_rope_append", dict(a23=63, a10=1 << 63), OverflowError),
+    ("w4a16_rope_append", dict(a23=63, a0=1 << 64), OverflowError),
+    ("w4a16_rope_append", dict(a23=63, a0=-(1 << 63) - 1), OverflowError),
+    ("w4a16_paged_attention", dict(a14=1 << 64, a24=8), OverflowError),
+    ("w4a16_paged_attention", dict(a14=-1, a24=8), OverflowError),
+    # what is no number, or no buffer
+    ("w4a16_rope_append", dict(a23=63, a19=4.0), TypeError),
+    ("w4a16_rope_append", dict(a23=63, a19=None), TypeError),
+    ("w4a16_rope_append", dict(a23=63, a19="4"), TypeError),
+    ("w4a16_paged_attention", dict(a23="0.1", a24=8), TypeError),
+    ("w4a16_paged_attention", dict(a23=None, a24=8), TypeError),
+    ("w4a16_rope_append", dict(a23=63, a0="q"), AttributeError),
+    ("w4a16_rope_append", dict(a23=63, a0=0.5), AttributeError),
+    ("w4a16_rope_append", dict(a23=63, a0=np.int64(P)), AttributeError),
+    ("w4a16_moe_layer", dict(a0=np.float32(1), a22=48), AttributeError),
+], ids=lambda v: str(v))
+def test_both_ways_take_and_refuse_the_same(w4, calls, name, spoil, want):
+    a, _keep = args_of(name, **spoil)
+    assert outcome(calls[name], a) == want
+    assert outcome(w4._through_ctypes(name), a) == want
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_both_ways_count_their_arguments(w4, calls, name):
+    a, _keep = args_of(name)
+    a[-2] = 1 << 30  # a flag that no entry has, whatever the count
+    for args in (a[:-1], a + [0]):
+        assert outcome(calls[name], args) is TypeError
+        assert outcome(w4._through_ctypes(name), args) is TypeError

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 
 import numpy as np
@@ -390,9 +391,37 @@ def _direct_calls():
     return tuple(map(_through_ctypes, names))
 
 
+def _pointer(x):
+    x = _ptr(x)
+    if x is not None and not -1 << 63 <= x < 1 << 64:
+        raise OverflowError("an address does not fit a pointer")
+    return x
+
+
+def _integer(lowest: int, highest: int):
+    def convert(x):
+        x = operator.index(x)
+        if not lowest <= x <= highest:
+            raise OverflowError("an argument does not fit its parameter")
+        return x
+    return convert
+
+
+# What the extension module does with an argument, by its C type: ctypes alone would cut integers off.
+_CONVERT = {_P: _pointer, _F: lambda x: ctypes.c_double(x).value}
+_CONVERT.update({c: _integer(-(1 << 8 * ctypes.sizeof(c) - 1), (1 << 8 * ctypes.sizeof(c) - 1) - 1) for c in (_I, _LL)})
+_CONVERT.update({c: _integer(0, (1 << 8 * ctypes.sizeof(c)) - 1) for c in (_U, _SZ)})
+
+
 def _through_ctypes(name):
     fn = getattr(_lib, name)
-    return lambda *args: fn(*(a if isinstance(a, (int, float)) else _ptr(a) for a in args))
+    convert = tuple(_CONVERT[t] for t in fn.argtypes)
+
+    def call(*args):
+        if len(args) != len(convert):
+            raise TypeError(f"{len(convert)} arguments expected, {len(args)} given")
+        return fn(*(c(a) for c, a in zip(convert, args)))
+    return call
 
 
 _rope_append, _paged_attention, _moe_layer = _direct_calls()

@@ -57,7 +57,11 @@ bool convert(PyObject *o, T &out)
         out = static_cast<T>(d);
         return d != -1.0 || !PyErr_Occurred();
     } else if constexpr (std::is_same_v<T, size_t>) {
-        out = PyLong_AsSize_t(o);
+        PyObject *i = PyNumber_Index(o); // PyLong_AsSize_t takes ints alone, PyLong_AsLongLong what counts as one
+        if (!i)
+            return false;
+        out = PyLong_AsSize_t(i);
+        Py_DECREF(i);
         return out != static_cast<size_t>(-1) || !PyErr_Occurred();
     } else {
         static_assert(std::is_integral_v<T>);
