@@ -113,8 +113,11 @@ class DecodeLayer:
         """One new token per sequence: x [batch, hidden] -> the layer's output (a buffer of its own)."""
         b, h, kv, d, page = self.batch, self.heads, self.kv, self.dim, self.page
         positions = self.lens  # the new token's position is the number of those before it
-        pages = self.table.gather(1, (positions // page).long()[:, None]).squeeze(1)
-        slots = pages.long() * page + (positions % page).long()
+        # Past max_len there is no page to look up: the token is not cached, and the operators report its position
+        # and length in their status words.
+        at = (positions // page).clamp(max=self.max_pages - 1).long()
+        pages = self.table.gather(1, at[:, None]).squeeze(1)
+        slots = torch.where(positions < self.max_len, pages.long() * page + (positions % page).long(), -1)
         qkv = self.qkv(rms_norm(x), self.qkv_out)
         width = qkv.shape[1]
         w4.w4a16_rope_append(qkv, qkv[:, h * d:], qkv[:, (h + kv) * d:], self.q, self.k_cache, self.v_cache,

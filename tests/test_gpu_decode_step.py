@@ -117,3 +117,24 @@ def test_a_captured_step_serves_every_token(example):
 def test_main_runs(example, capsys):
     example.main(["--batch", "2", "--steps", "4", "--hidden", "512", "--inter", "256", "--experts", "4", "--top-k", "2"])
     assert "device status 0" in capsys.readouterr().out
+
+
+def test_steps_past_the_longest_length_are_reported(example):
+    """The cache's end: no page is looked up beyond the table, what is cached stays, and the status words
+    tell; up to there a layer with a longer cache gives the same bits."""
+    import torch
+    kw = dict(hidden=512, heads=4, kv_heads=2, head_dim=64, inter=256, experts=4, top_k=2, seed=5)
+    layer, longer = example.DecodeLayer(2, 20, **kw), example.DecodeLayer(2, 80, **kw)
+    g = torch.Generator(device="cuda").manual_seed(10)
+    for _ in range(20):
+        x = torch.randn((2, 512), generator=g, device="cuda", dtype=torch.float16)
+        assert torch.equal(layer.step(x), longer.step(x))
+    assert int(layer.status.item()) == 0
+    caches = layer.k_cache.clone(), layer.v_cache.clone()
+    for _ in range(25):
+        layer.step(x)
+    torch.cuda.synchronize()
+    assert torch.equal(layer.k_cache, caches[0]) and torch.equal(layer.v_cache, caches[1])
+    assert int(layer.status.item()) == example.w4.W4A16_DEV_POSITION
+    assert example.w4.w4a16_status(layer.workspace) == example.w4.W4A16_DEV_LENGTH
+    assert example.w4.w4a16_status(longer.workspace) == 0
