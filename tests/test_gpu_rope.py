@@ -218,3 +218,32 @@ def test_q_alone_looks_at_no_cache_argument(w4, heads, dim, rot):
         y, tol, _ = case.reference()
         assert bool(((case.q_out.double() - y[:, :heads]).abs() <= tol[:, :heads] + 2.0 ** -25).all())
         assert int(case.status.item()) == 0
+
+
+def test_as_many_tokens_as_an_int_counts(w4):
+    """The walk over tokens ends at the last one, not past it: 2^31 - 1 rows of one narrow head, in place."""
+    import torch
+    torch.cuda.empty_cache()
+    n, dim = (1 << 31) - 1, 16
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 80 GB")
+    g = torch.Generator(device="cuda").manual_seed(7)
+    x = torch.zeros((n, dim), dtype=torch.float16, device="cuda")
+    rows = torch.tensor([0, 1, 1 << 20, (1 << 31) - 250000, (1 << 31) - 120000, (1 << 31) - 116737, n - 116000, n - 2,
+                         n - 1], device="cuda")
+    x[rows] = torch.randn((rows.numel(), dim), generator=g, device="cuda", dtype=torch.float16)
+    before = x[rows].double()
+    table = torch.randn((2, dim), generator=g, device="cuda")
+    positions = torch.ones(n, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    w4.w4a16_rope_append(x, None, None, x, None, None, table, positions, None, status, n, 1, 0, dim, dim, [8], 2, 1, 1)
+    torch.cuda.synchronize()
+    c, s = table[1, :8].double(), table[1, 8:].double()
+    a, b = before[:, :8], before[:, 8:]
+    ref = torch.cat([a * c - b * s, b * c + a * s], 1)
+    mag = (a.abs() + b.abs()) * (c.abs() + s.abs())
+    tol = UNIT["fp16"] * ref.abs() + 2.0 ** -21 * torch.cat([mag, mag], 1) + 2.0 ** -25
+    assert bool(((x[rows].double() - ref).abs() <= tol).all())
+    assert int(status.item()) == 0
+    del x, positions
+    torch.cuda.empty_cache()

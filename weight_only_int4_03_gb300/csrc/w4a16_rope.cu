@@ -187,10 +187,11 @@ __global__ void __launch_bounds__(256, ROPE_PER_SM / 256) rope_vec_kernel(const 
                 }
             }
         }
-        token += stride;
-        const bool more = token < p.tokens;
-        if (more)
+        const bool more = p.tokens - token > stride; // (the sum may pass 31 bits)
+        if (more) {
+            token += stride;
             fetch(token);
+        }
 #pragma unroll
         for (int n = 0; n < ROPE_HEADS; ++n) {
             const int h = h0 + n;
