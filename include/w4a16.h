@@ -487,8 +487,10 @@ size_t w4a16_moe_layer_workspace_size(int n_tokens, int hidden, int inter, int n
  *     lowest index where scores are equal);   w_j = P[e_j], divided by the sum of the chosen ones
  *     with W4A16_FLAG_MOE_RENORM;
  *     y_t = residual_t + sum_j w_j down_{e_j}( act(gate_{e_j} x_t) * (up_{e_j} x_t) )
- * with act silu (W4A16_FLAG_SWIGLU) or gelu_tanh (W4A16_FLAG_GEGLU).  All sums are fp32, (q - z) s and
- * the inner activations are not rounded to 16 bits, y is rounded once.  Routing runs on the device:
+ * with act silu (W4A16_FLAG_SWIGLU) or gelu_tanh (W4A16_FLAG_GEGLU).  All sums are fp32, (q - z) s is
+ * not rounded, y is rounded once.  The inner activations go on as a 16-bit value plus a 16-bit remainder:
+ * to 2^-17 of themselves in bf16; in fp16 to 2^-23, or to an absolute 2^-25 where that is more, and
+ * whatever lies beyond 131008 is added in fp32 (a call that has such values takes longer).  Routing runs on the device:
  * no host synchronisation, and the call can be captured in a graph.  For more tokens than
  * 64 use the grouped entry points.
  *   x              device 16-bit [n_tokens][ldx];  residual 16-bit [n_tokens][ldr] or NULL

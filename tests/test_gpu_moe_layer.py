@@ -266,3 +266,43 @@ def test_new_inputs_in_one_workspace(w4, dtype, tokens, experts, top):
         torch.cuda.synchronize()
         assert torch.equal(layer.y, y)
         layer.check()
+
+
+@pytest.mark.parametrize("most", [2e5, 1e7])
+@pytest.mark.parametrize("kw", [
+    dict(tokens=1, hidden=256, inter=384, experts=1, top=1),
+    dict(tokens=4, hidden=512, inter=256, experts=8, top=2, group_size=64, act="gelu"),
+    dict(tokens=20, hidden=256, inter=512, experts=4, top=2, zeros=True),
+    dict(tokens=64, hidden=256, inter=256, experts=3, top=2, group_size=-1, renorm=False, pad=8),
+], ids=lambda c: f"t{c['tokens']}e{c['experts']}" if isinstance(c, dict) else f"{c:g}")
+def test_inner_activations_of_any_size_in_fp16(w4, kw, most):
+    """h far beyond both of its 16-bit parts in every third token, beside tokens of ordinary size: the
+    outputs are finite and within the tolerance of every other call, and calls repeat their bits."""
+    import torch
+    layer = Layer(w4, 28, "fp16", residual=False, router_sigma=1e-3, **kw)
+    layer.weights[1][1].mul_(2.0 ** -9)  # the down scales: outputs inside fp16's range
+    rows = torch.arange(layer.tokens, device="cuda") % 3 == 0
+    base = layer.x[rows].double()
+
+    def h_of(x):
+        gu = x[:, :layer.hidden].double() @ layer.matrix(0, 0)
+        gate, up = gu[:, :layer.inter], gu[:, layer.inter:]
+        return (gate * torch.sigmoid(gate) * up).abs().max()
+
+    c = 1.0
+    for _ in range(8):
+        layer.x[rows] = (base * c).half()
+        c *= math.sqrt(most / float(h_of(layer.x[rows])))
+    assert float(h_of(layer.x[rows])) > 0.9 * most > 131008
+    layer.run()
+    assert bool(torch.isfinite(layer.y[:, :layer.hidden]).all())
+    layer.check()
+    first = layer.y.clone()
+    for _ in range(3):
+        layer.run()
+    torch.cuda.synchronize()
+    assert torch.equal(layer.y[:, :layer.hidden], first[:, :layer.hidden])
+    # Nothing of it is left in the next call.
+    layer.x[rows] = base.half()
+    layer.run()
+    layer.check()

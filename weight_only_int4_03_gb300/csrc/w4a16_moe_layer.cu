@@ -23,8 +23,12 @@
 // The zero point (and the 128) is then taken off the sums, sum (q - z) a = sum q a - z sum a, with
 // sum a from one more MMA whose weights are all ones, shared by the block's columns.  Every sum of a
 // 64-row block starts from zero and is scaled in fp32; (q - z) s is never rounded.
-// h keeps fp32's accuracy through the second product as a 16-bit value plus a 16-bit remainder, two
-// columns of the down MMA, whose eight columns are mostly empty for a few tokens.
+// h goes through the second product as a 16-bit value plus a 16-bit remainder, two columns of the down
+// MMA, whose eight columns are mostly empty for a few tokens.  bf16's parts keep 2^-17 of any h (a third
+// would take another MMA); fp16's keep 2^-23 of it, or an absolute 2^-25 where that is more.  fp16's parts
+// end at 2 x 65504: what a value has beyond that is put down in fp32, its pair is marked beside its weight,
+// and the combine launch adds it to the pair's outputs in fp32 (a search through the pair's h, in calls that
+// have such values alone; the marks cost the other calls 0.1 us).
 //
 // A unit of work is 64 columns of one expert over all of K (down: or a part of it), done by a team of 1 to 8 warps that take
 // its 128-row steps in turn.  A warp streams its steps through its own ring of cp.async stages, which
@@ -80,6 +84,13 @@ __host__ __device__ __forceinline__ int frag_index(int row)
     return ((j & 1) * 4 + h + 2 * (j >> 1)) * 8 + 2 * q + e;
 }
 
+// Row of a 64-row block at place `at` of that order.
+__host__ __device__ __forceinline__ int frag_row(int at)
+{
+    const int c = at >> 3, q = (at >> 1) & 3, p = ((q & 1) << 1) | (q >> 1);
+    return (c & 1) * 32 + p * 8 + ((c >> 1) & 1) * 4 + (c >> 2) * 2 + (at & 1);
+}
+
 // Routing tables in the workspace.
 struct MoeTables {
     // The active experts in increasing order: (first gate-up unit, first down unit, expert | pairs <<
@@ -90,8 +101,12 @@ struct MoeTables {
     int *sorted;     // [pairs] pair ids t * top_k + j by expert, in increasing order within one
     int *token;      // [pairs] their tokens t
     int *ids;        // [pairs]
-    float *weights;  // [pairs]
+    // [pairs] weights, each with a mark's bits beside it: 0, or for a pair with values of h beyond fp16's parts
+    // OVER | place in `sorted` << 9 | expert.
+    float2 *weights;
 };
+constexpr int OVER = 1 << 20;
+static_assert(MOE_MAX_EXPERTS <= 512 && MOE_MAX_PAIRS <= 1024, "a mark holds an expert and a place");
 
 struct RouteParams {
     const uint16_t *x, *router;
@@ -280,7 +295,7 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_layer_route_kernel(const Rout
             choose_experts<MOE_MAX_EXPERTS / 32>(l, p.experts, p.top, p.renorm, lane, at, w);
         if (lane < p.top) {
             const int pair = tok * p.top + lane;
-            p.tab.weights[pair] = w;
+            p.tab.weights[pair] = make_float2(w, 0.f);
             if (one_level)
                 ids[pair] = at;
             else
@@ -409,6 +424,7 @@ struct MoeGemm {
     const uint16_t *s, *z;   // [E][G][N]; z null: 8
     const uint16_t *act;     // activation rows in fragment order, K values each
     uint16_t *h;             // gate-up: the pairs' h, two rows (value, remainder) per pair
+    float *excess;           // gate-up, fp16: [pairs][inter] what h has beyond both, where its remainder is +-65504
     float *part;             // down: [pairs][splits][N] fp32
     int *ticket;             // units drawn beyond each team's first two
     int *status;
@@ -425,6 +441,17 @@ struct MoeGemm {
     int pairs;
     int inter, glu;
 };
+
+// x, or fp16's largest finite value in its place; and whether an fp16 is that.
+__device__ __forceinline__ float within(float x)
+{
+    return fabsf(x) > 65504.f ? copysignf(65504.f, x) : x;
+}
+
+__device__ __forceinline__ bool is_most(uint32_t bits)
+{
+    return (bits & 0x7FFFu) == 0x7BFFu;
+}
 
 // Gated activations as g sigmoid(x): x = g for silu, 2 sqrt(2/pi) (g + 0.044715 g^3) for gelu_tanh
 // (1 + tanh t = 2 sigmoid(2 t)).
@@ -907,13 +934,18 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
                 const float gate = joined(v, ln), up = joined(v + NT * 4, ln);
                 const float hv = gate_act(gate, p.glu) * up;
                 // fp16: the value part stops at the largest finite value and the remainder goes on
-                // from there (a NaN stays one).
-                const float hc = !BF && fabsf(hv) > 65504.f ? copysignf(65504.f, hv) : hv;
-                const uint16_t hb = from_float<BF>(hc);
-                const int row = un.col * (COLS / 2) + f;
-                uint16_t *dst = p.h + (long long)(2 * (un.first + pr)) * p.inter + (row & ~63) + frag_index(row & 63);
+                // from there, as far again (a NaN stays one).
+                const uint16_t hb = from_float<BF>(BF ? hv : within(hv));
+                const float rest = hv - to_float<BF>(hb);
+                const uint16_t lb = from_float<BF>(BF ? rest : within(rest));
+                const int row = un.col * (COLS / 2) + f, place = un.first + pr;
+                uint16_t *dst = p.h + (long long)(2 * place) * p.inter + (row & ~63) + frag_index(row & 63);
                 dst[0] = hb;
-                dst[p.inter] = from_float<BF>(hv - to_float<BF>(hb));
+                dst[p.inter] = lb;
+                if (!BF && is_most(lb)) {
+                    p.excess[(long long)place * p.inter + row] = rest - to_float<BF>(lb);
+                    p.tab.weights[__ldcg(p.tab.sorted + place)].y = __int_as_float(OVER | place << 9 | un.expert);
+                }
             }
         } else {
             // Item: column c of the unit, pair pr.
@@ -934,11 +966,47 @@ __global__ void __launch_bounds__(MoeGeom<NT>::WARPS * 32, MoeGeom<NT>::CTAS) mo
 
 struct CombineParams {
     const float *part; // [pairs][splits][hidden]
-    const float *weights;
+    const float2 *weights;
     const uint16_t *residual;
     uint16_t *y;
     int tokens, top, splits, hidden, ldy, ldr;
+    // The down product's operands, for values of h beyond fp16's parts.
+    const uint16_t *h;
+    const float *excess;
+    const int32_t *w;
+    const uint16_t *s, *z;
+    long long expert_words, expert_groups;
+    int k, group_rows;
 };
+
+// The outputs of columns col to col + 3 that the values of a marked pair's h beyond both their parts have:
+// sum over such rows of excess (q - z) s, in the order of h's places.
+__device__ __forceinline__ float4 excess_outputs(const CombineParams &p, int mark, int col)
+{
+    const int expert = mark & 511, place = (mark >> 9) & 1023;
+    const uint4 *rest = reinterpret_cast<const uint4 *>(p.h + (2LL * place + 1) * p.k);
+    const float *excess = p.excess + (long long)place * p.k;
+    const int32_t *tiles = p.w + expert * p.expert_words + (long long)(col >> 7) * (p.k / 64) * 1024 + (col & 127) * 4;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < p.k / 8; ++c) {
+        const uint4 v = __ldcg(rest + c);
+        const uint32_t parts[4] = {v.x, v.y, v.z, v.w};
+        for (int i = 0; i < 8; ++i) {
+            if (!is_most(parts[i >> 1] >> (16 * (i & 1))))
+                continue;
+            const int r = frag_row((c & 7) * 8 + i), row = (c >> 3) * 64 + r;
+            const float x = __ldcg(excess + row);
+            const int32_t *words = tiles + (c >> 3) * 1024 + (r >> 5) * 512 + ((r >> 1) & 3);
+            const int shift = 4 * ((r >> 3) & 3) + 16 * (r & 1);
+            const long long at = (expert * p.expert_groups + row / p.group_rows) * p.hidden + col;
+            for (int j = 0; j < 4; ++j) {
+                const float q = (float)((words[4 * j] >> shift) & 15), z = p.z ? to_float<false>(p.z[at + j]) : 8.f;
+                sum[j] = fmaf(x, (q - z) * to_float<false>(p.s[at + j]), sum[j]);
+            }
+        }
+    }
+    return make_float4(sum[0], sum[1], sum[2], sum[3]);
+}
 
 // y_t = residual_t + sum_j w_j (sum over the splits), in the order of j: a thread per quad of
 // columns of a token.  The residual is older than the layer's first launch, so it is fetched (past
@@ -956,24 +1024,38 @@ __global__ void __launch_bounds__(128) moe_layer_combine_kernel(const CombinePar
     if (!in)
         return;
     const float4 *src = reinterpret_cast<const float4 *>(p.part + (long long)tok * p.top * p.splits * p.hidden + col);
-    const float *wts = p.weights + tok * p.top;
+    const float2 *wts = p.weights + tok * p.top;
     const int parts = p.top * p.splits;
+    int marked = 0;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int q0 = 0; q0 < parts; q0 += 8) {
         float4 v[8];
-        float wt[8];
+        float2 wt[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
             const bool live = q0 + q < parts;
             v[q] = live ? __ldcg(src + (long long)(q0 + q) * (p.hidden / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
-            wt[q] = live ? __ldcg(wts + (p.splits == 1 ? q0 + q : (q0 + q) / p.splits)) : 0.f;
+            wt[q] = live ? __ldcg(wts + (p.splits == 1 ? q0 + q : (q0 + q) / p.splits)) : make_float2(0.f, 0.f);
         }
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-            a.x = fmaf(wt[q], v[q].x, a.x);
-            a.y = fmaf(wt[q], v[q].y, a.y);
-            a.z = fmaf(wt[q], v[q].z, a.z);
-            a.w = fmaf(wt[q], v[q].w, a.w);
+            a.x = fmaf(wt[q].x, v[q].x, a.x);
+            a.y = fmaf(wt[q].x, v[q].y, a.y);
+            a.z = fmaf(wt[q].x, v[q].z, a.z);
+            a.w = fmaf(wt[q].x, v[q].w, a.w);
+            marked |= __float_as_int(wt[q].y);
+        }
+    }
+    if (!BF && marked) {
+        for (int j = 0; j < p.top; ++j) {
+            const float2 wt = __ldcg(wts + j);
+            if (__float_as_int(wt.y) == 0)
+                continue;
+            const float4 e = excess_outputs(p, __float_as_int(wt.y), col);
+            a.x = fmaf(wt.x, e.x, a.x);
+            a.y = fmaf(wt.x, e.y, a.y);
+            a.z = fmaf(wt.x, e.z, a.z);
+            a.w = fmaf(wt.x, e.w, a.w);
         }
     }
     const float2 r0 = unpack2<BF>(rv.x), r1 = unpack2<BF>(rv.y);
@@ -986,7 +1068,7 @@ __global__ void __launch_bounds__(128) moe_layer_combine_kernel(const CombinePar
 namespace {
 
 struct MoeLayout {
-    long long counters, logits, tables, xf, h, part, total;
+    long long counters, logits, tables, xf, h, part, excess, total;
     MoeTables tab;
 };
 
@@ -1018,14 +1100,15 @@ MoeLayout moe_layout(char *ws, int tokens, int hidden, int inter, int experts, i
     };
     l.tab.chunks = ((experts < pairs ? experts : pairs) + 32) / 32;
     l.tab.experts = reinterpret_cast<int4 *>(take(4LL * 32 * l.tab.chunks));
+    l.tab.weights = reinterpret_cast<float2 *>(take(2LL * pairs));
     l.tab.sorted = reinterpret_cast<int *>(take(pairs));
     l.tab.token = reinterpret_cast<int *>(take(pairs));
     l.tab.ids = reinterpret_cast<int *>(take(pairs));
-    l.tab.weights = reinterpret_cast<float *>(take(pairs));
     l.xf = round_up(at, 256);
     l.h = round_up(l.xf + 2LL * tokens * hidden, 256);
     l.part = round_up(l.h + 4LL * pairs * inter, 256);
-    l.total = round_up(l.part + 4LL * part_rows(pairs) * hidden, 256);
+    l.excess = round_up(l.part + 4LL * part_rows(pairs) * hidden, 256);
+    l.total = round_up(l.excess + 4LL * pairs * inter, 256);
     return l;
 }
 
@@ -1259,6 +1342,7 @@ extern "C" int w4a16_moe_layer(const void *x, int ldx, const void *router, const
     m.act = r.xf;
     m.h = reinterpret_cast<uint16_t *>(ws + lay.h);
     m.part = reinterpret_cast<float *>(ws + lay.part);
+    m.excess = reinterpret_cast<float *>(ws + lay.excess);
     m.ticket = counters + MOE_TICKETS;
     m.status = reinterpret_cast<int *>(ws);
     m.tab = lay.tab;
@@ -1303,6 +1387,15 @@ extern "C" int w4a16_moe_layer(const void *x, int ldx, const void *router, const
     c.hidden = hidden;
     c.ldy = ldy;
     c.ldr = ldr;
+    c.h = m.h;
+    c.excess = m.excess;
+    c.w = m.w;
+    c.s = m.s;
+    c.z = m.z;
+    c.expert_words = m.expert_words;
+    c.expert_groups = m.expert_groups;
+    c.k = inter;
+    c.group_rows = group_size == -1 ? inter : group_size;
     const dim3 cgrid((hidden / 4 + 127) / 128, n_tokens);
     return launch_status(bf ? launch_pdl(moe_layer_combine_kernel<true>, cgrid, dim3(128), 0, stream, c)
                             : launch_pdl(moe_layer_combine_kernel<false>, cgrid, dim3(128), 0, stream, c));
