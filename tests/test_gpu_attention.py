@@ -295,3 +295,15 @@ def test_a_long_tail_under_dominant_positions_counts(w4, dtype, dim, heads, kv, 
     assert float(err) <= tol + subnormal, (float(err), tol)
     want = torch.logsumexp(logits, 1).repeat_interleave(heads // kv, 1)
     assert bool(((lse.double() - want).abs() <= 2.0 ** -14 + 2.0 ** -22 * want.abs()).all())
+
+
+@pytest.mark.parametrize("kw", [
+    dict(dtype="fp16", lens=[7 * i % 130 for i in range(4096)], heads=4, kv=1, dim=64, page=16),
+    dict(dtype="bf16", lens=[3000] + [1 + i % 40 for i in range(1200)] + [2000], heads=8, kv=2, dim=128, page=32),
+], ids=("4096_short", "1202_between_long"))
+def test_large_batches(w4, kw):
+    case = Case(19, **kw)
+    ws = case.workspace(w4)
+    case.run(w4, ws)
+    case.check()
+    assert w4.w4a16_status(ws) == 0

@@ -306,3 +306,25 @@ def test_inner_activations_of_any_size_in_fp16(w4, kw, most):
     layer.x[rows] = base.half()
     layer.run()
     layer.check()
+
+
+@pytest.mark.parametrize("dtype,tokens,hidden,inter,experts,favoured", [
+    ("fp16", 64, 512, 16384, 32, (3, 30)),   # 64 pairs on each of two experts where four are expected; drawn units
+    ("bf16", 64, 512, 1024, 128, (0, 127)),
+    ("fp16", 33, 256, 2048, 128, (64,)),     # one expert for every token
+    ("bf16", 9, 1024, 512, 60, (7, 8, 9)),
+])
+def test_skewed_routing(w4, dtype, tokens, hidden, inter, experts, favoured):
+    """Every token chooses the same few experts: many times the pairs of an even spread on each."""
+    import torch
+    layer = Layer(w4, 29, dtype, tokens, hidden, inter, experts, len(favoured), group_size=64, router_sigma=0.5)
+    g = torch.Generator(device="cuda").manual_seed(30)
+    common = torch.randn(hidden, generator=g, device="cuda")
+    layer.x += common.to(layer.x.dtype)
+    for i, e in enumerate(favoured):
+        layer.router[e] = ((6 + 0.25 * i) * common / hidden).to(layer.router.dtype)
+    for _ in range(2):
+        layer.y.fill_(float("nan"))
+        layer.run()
+        layer.check()
+    assert sorted(set(layer.ids.flatten().tolist())) == sorted(favoured)
