@@ -205,8 +205,9 @@ int w4_unpack(const int32_t *b_packed, int32_t *qweight, int k, int n, cudaStrea
  * multiprocessors (num_sms <= 0: query the current device; returns 0 if that fails or the
  * sizes are invalid).  The workspace holds a status word, the split-K tile counters, the
  * fp32 partial tiles and, with act-order, the gathered copy of A.  It must be zero-filled
- * once after allocation; the kernels leave it ready for the next call (counters reset
- * themselves), so no per-call memset is needed.  The one exception: after w4a16_status has
+ * once after allocation; the kernels leave it ready for the next call, of these or any other
+ * sizes that need no more bytes, dense or grouped (counters reset themselves), so no per-call
+ * memset is needed.  The one exception: after w4a16_status has
  * reported W4A16_DEV_TIMEOUT, a CTA that gave up may have left its tile counters part-way, and
  * the next call would then reduce the wrong partials -- zero-fill the whole workspace again
  * (cudaMemsetAsync over its size) before reusing it.  Calls that run concurrently need
@@ -277,7 +278,7 @@ int w4a16_kernel_for(int m, int n, int k, int group_size, unsigned flags, int nu
  * It holds the tcgen05 kernel's token tiles to at most 192 rows (w4a16_gemm goes up to 256),
  * so that their partial-tile slots stay small; M above 192 then runs in tiles of 192 rows, a
  * little slower than w4a16_gemm where that would pick taller tiles.  The scratch a call needs
- * is the status header, one counter per output tile, two fp32 partial slots per CTA (SM count
+ * is the status header, one counter per CTA, two fp32 partial slots per CTA (SM count
  * x tile rows x 128 columns each) and, with act-order, the copy of A (M*K*2 bytes); a call for
  * which these exceed W4A16_NOALLOC_SCRATCH_BYTES (an act-order call with a large M*K, a very
  * large M, or a part with many more SMs) returns stage 2 with detail W4A16_ARG_SCRATCH and

@@ -73,3 +73,41 @@ def test_attention_at_changing_batches_and_widths(w4):
         torch.cuda.synchronize()
         assert torch.equal(case.out, alone[name][0]) and torch.equal(case.lse, alone[name][1]), name
     assert w4.w4a16_status(shared) == 0
+
+
+@pytest.mark.parametrize("n,k", [(28672, 4096), (4096, 4096), (12288, 1024), (4096, 14336)])
+def test_gemm_at_changing_row_counts(w4, n, k):
+    """The products around the operators, from a single token to prompts and back, dense and grouped."""
+    import torch
+    flags, wt = w4.W4A16_FLAG_IS_K_FULL, w4.W4A16_TYPE_U4B8
+    g = torch.Generator(device="cuda").manual_seed(47)
+    words = torch.randint(-2 ** 31, 2 ** 31 - 1, (k // 8, n), generator=g, device="cuda", dtype=torch.int32)
+    scales = torch.rand((k // 128, n), generator=g, device="cuda").mul_(0.02).half()
+    packed = torch.empty(k * n // 8, dtype=torch.int32, device="cuda")
+    w4.w4_repack(words, None, packed, k, n)
+    # Two experts with the same weights: every token once, split unevenly.
+    packed2, scales2 = packed.repeat(2), scales.repeat(2, 1, 1)
+    zeroed = lambda size: torch.zeros(size, dtype=torch.uint8, device="cuda")
+
+    def dense(m, x, out, ws):
+        w4.w4a16_gemm(x, packed, out, scales, None, None, None, ws, m, n, k, 128, wt, flags)
+
+    def grouped(m, x, out, ws):
+        off = torch.tensor([0, m // 3, m], dtype=torch.int32, device="cuda")
+        ids, rows = (torch.arange(c, dtype=torch.int32, device="cuda") for c in (2, m))
+        w4.w4a16_gemm_grouped(x, packed2, out, scales2, None, ids, off, rows, rows, 2, 2, m, m, n, k, 128, wt, flags, ws)
+
+    calls = {dense: lambda m: w4.w4a16_workspace_size(m, n, k, 128, flags),
+             grouped: lambda m: w4.w4a16_grouped_workspace_size(m, 2, n, k, 128, flags)}
+    counts = (1, 16, 512, 33, 1000, 4096, 64, 2000, 7)
+    shared = zeroed(max(size(m) for size in calls.values() for m in counts))
+    for m in counts:
+        x = torch.randn((m, k), generator=g, device="cuda", dtype=torch.float16)
+        for call, size in calls.items():
+            alone, out = (torch.full((m, n), float("nan"), dtype=torch.float16, device="cuda") for _ in range(2))
+            call(m, x, alone, zeroed(size(m)))
+            call(m, x, out, shared)
+            torch.cuda.synchronize()
+            assert bool(torch.isfinite(alone).all())
+            assert torch.equal(out, alone), (call.__name__, m)
+    assert w4.w4a16_status(shared) == 0

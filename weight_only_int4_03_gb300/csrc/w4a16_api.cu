@@ -34,7 +34,6 @@ inline long long round_up(long long v, long long a)
     return (v + a - 1) / a * a;
 }
 
-constexpr long long HEADER_BYTES = 256;
 constexpr unsigned long long WAIT_LIMIT_NS = 2000000000ull; // 2 s per bounded wait
 
 // Group-size rule: transformer.rs `marlin_num_groups` (-1 or a positive divisor of K) with
@@ -51,7 +50,7 @@ int num_groups(int k, int group_size)
 }
 
 struct Plan {
-    int nt_max, m_tiles, tiles_bound, grid;
+    int nt_max, m_tiles, grid;
     int kbs, sg_box, act_kb_bytes, packed_off, scales_off, zeros_off;
     int stages, stage_bytes, acc_bufs, acc_col0, tmem_cols, smem_bytes, seg_off, epi_off, a_slots;
     bool a_tmem, mma; // mma: a small-M register-fragment kernel instead of tcgen05
@@ -62,16 +61,16 @@ struct Plan {
     int tile_bytes = TILE_BYTES; // one packed 64 x 128 tile (FP8: twice as large)
     int split = 0;    // tile-aligned split factor (0: stream-K)
     int n_slices = 0, slice_per = 0;
-    long long counters_off, partials_off, a_off, total;
+    long long partials_off, a_off, total;
 };
 
-// Workspace carving (byte offsets), shared by the size queries and the launches.  The
+// Workspace carving (byte offsets), shared by the size queries and the launches.  The partial tiles
+// start behind the counters of every call, so that calls of other sizes find those zero.  The
 // partial-tile area holds two [slot_rows x 128] fp32 slots per CTA: slot_cta_rows is the
 // largest (CTAs x tile rows) of the kernels the call may pick.
 void carve(Plan &pl, long long slot_cta_rows, long long a_bytes)
 {
-    pl.counters_off = HEADER_BYTES;
-    pl.partials_off = round_up(pl.counters_off + 4LL * pl.tiles_bound, 256);
+    pl.partials_off = HEADER_BYTES + COUNTER_BYTES;
     pl.a_off = round_up(pl.partials_off + slot_cta_rows * 2 * TILE_N * 4, 256);
     pl.total = round_up(pl.a_off + a_bytes, 256);
 }
@@ -606,6 +605,12 @@ int choose_kernel(int m, int n, int gs, unsigned flags, int num_sms)
     return m <= decode_rows_default() ? 1 : 0;
 }
 
+// CTAs of a launch whose split tiles the workspace's counters can count.
+int at_most_counted(int ctas)
+{
+    return ctas < MAX_CTAS ? ctas : MAX_CTAS;
+}
+
 // Dense plan.  The workspace is carved for the larger tile of the two kernels, so a size
 // query answers for whichever kernel the call then picks.
 void dense_plan(Plan &pl, int m, int n, int k, unsigned flags, int num_sms, int kernel,
@@ -619,13 +624,12 @@ void dense_plan(Plan &pl, int m, int n, int k, unsigned flags, int num_sms, int 
     const TcTile tc = pick_tc_tile(m, tile_cap, (flags & W4A16_FLAG_A_SMEM) == 0);
     const int nt_tc = tc.rows;
     const int nt_mma = mma_ok || pl.slice ? pick_nt_mma(m) : nt_tc;
-    const int nt_small = nt_tc < nt_mma ? nt_tc : nt_mma;
     pl.nt_max = mma ? nt_mma : nt_tc;
     pl.halves = mma ? 1 : tc.halves;
     pl.nt_half = mma ? nt_mma : tc.half;
     pl.m_tiles = (m + pl.nt_max - 1) / pl.nt_max;
     const long long units = (long long)pl.m_tiles * (n / TILE_N) * (k / KBLK);
-    const int ctas = mma ? num_sms * decode_grid_per_sm() : num_sms;
+    const int ctas = at_most_counted(mma ? num_sms * decode_grid_per_sm() : num_sms);
     pl.grid = aligned_grid(pl.m_tiles * (n / TILE_N), k / KBLK, ctas, &pl.split);
     pl.act_rows = pl.slice ? m : pl.halves > 1 ? pl.nt_half : pl.nt_max;
     if (pl.slice) {
@@ -636,9 +640,8 @@ void dense_plan(Plan &pl, int m, int n, int k, unsigned flags, int num_sms, int 
         pl.grid = (pl.n_slices + pl.slice_per - 1) / pl.slice_per;
         pl.split = 0;
     }
-    // The workspace serves whichever kernel a call picks: counters for the smaller tile
-    // height, partial slots for the larger CTA count x tile height.
-    pl.tiles_bound = ((m + nt_small - 1) / nt_small) * (n / TILE_N);
+    // The workspace serves whichever kernel a call picks: partial slots for the larger CTA count x tile
+    // height.
     long long slot_rows = (long long)num_sms * nt_tc;
     if (mma_ok) {
         const long long r = (long long)num_sms * decode_ctas_per_sm() * nt_mma;
@@ -673,8 +676,7 @@ void grouped_plan(Plan &pl, int n_pairs, int n_active, int n, int k, unsigned fl
     pl.halves = 1;
     pl.nt_half = pl.nt_max;
     pl.m_tiles = 0;
-    pl.tiles_bound = ((n_pairs + pl.nt_max - 1) / pl.nt_max + n_active) * (n / TILE_N);
-    pl.grid = num_sms;
+    pl.grid = at_most_counted(num_sms);
     carve(pl, (long long)num_sms * pl.nt_max, (long long)n_pairs * k * 2);
 }
 
@@ -700,8 +702,7 @@ void moe_blocks_plan(Plan &pl, MoePlan &mp, int max_padded, int block_size, int 
     pl.halves = 1;
     pl.nt_half = pl.nt_max;
     pl.m_tiles = 0;
-    pl.tiles_bound = ((max_padded + pl.nt_max - 1) / pl.nt_max + mp.seg_cap) * (n / TILE_N);
-    pl.grid = num_sms;
+    pl.grid = at_most_counted(num_sms);
     carve(pl, (long long)num_sms * pl.nt_max, (long long)max_padded * k * 2);
     mp.off_off = pl.total;
     mp.ids_off = round_up(mp.off_off + 4LL * (mp.seg_cap + 1), 256);
@@ -886,7 +887,7 @@ int dense_gemm(const void *a, int lda, const int32_t *b_packed, void *c, int ldc
         p.m_outer = (a_bytes > w_bytes && a_bytes * 2 > l2_bytes()) ? 1 : 0;
     }
     p.status = reinterpret_cast<int *>(ws);
-    p.counters = reinterpret_cast<int *>(ws + pl.counters_off);
+    p.counters = reinterpret_cast<int *>(ws + HEADER_BYTES);
     p.partials = reinterpret_cast<float *>(ws + pl.partials_off);
 
     const __half *a_src = static_cast<const __half *>(a);
@@ -1143,7 +1144,7 @@ int w4a16_gemm_grouped(const void *a, int lda, const int32_t *b_packed_stack, vo
     p.ldc = ldy;
     p.glu = glu;
     p.status = reinterpret_cast<int *>(ws);
-    p.counters = reinterpret_cast<int *>(ws + pl.counters_off);
+    p.counters = reinterpret_cast<int *>(ws + HEADER_BYTES);
     p.partials = reinterpret_cast<float *>(ws + pl.partials_off);
     p.ex_off = ex_off;
     p.ex_ids = ex_ids;
@@ -1253,7 +1254,7 @@ int w4a16_gemm_moe_blocks(const void *a, int lda, const int32_t *b_packed_stack,
     p.ldc = ldc;
     p.glu = glu;
     p.status = reinterpret_cast<int *>(ws);
-    p.counters = reinterpret_cast<int *>(ws + pl.counters_off);
+    p.counters = reinterpret_cast<int *>(ws + HEADER_BYTES);
     p.partials = reinterpret_cast<float *>(ws + pl.partials_off);
     p.ex_off = ex_off;
     p.ex_ids = ex_ids;

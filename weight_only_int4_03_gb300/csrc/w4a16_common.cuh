@@ -423,7 +423,7 @@ static __device__ void prefetch_first_codes(const GemmParams &p, SCHED sched, ui
 // and number of tiles; returns the total tile count.  The offsets must form a non-decreasing
 // chain inside [0, n_pairs] and the expert ids must be in range; otherwise the whole schedule
 // is treated as empty and W4A16_DEV_SCHEDULE is reported, so no tile can index past the
-// workspace's counters.
+// activations.
 static __device__ int build_segments(const GemmParams &p, SegTable &seg, int lane)
 {
     bool bad = false;
@@ -534,7 +534,8 @@ __device__ __forceinline__ Contributors contributors(const GemmParams &p, const 
     return c;
 }
 
-// Split-tile counter: one acquire-release atomic at GPU scope.  The CTA's partial stores
+// Split-tile counter, that of the tile's first contributor (no other split tile starts in the same
+// CTA's range): one acquire-release atomic at GPU scope.  The CTA's partial stores
 // happen before it through the CTA-wide rendezvous that precedes it, and release is
 // cumulative, so they are visible to whoever reads the counter's later value; the acquire half
 // makes the other contributors' partials visible to the last arriver (and, through the

@@ -461,7 +461,7 @@ __device__ void run_compute(const GemmParams &p, Sched sched, uint8_t *smem, Dec
             return;
         const Contributors cb = contributors(p, sched, st_tile);
         if (w == 0 && lane == 0) {
-            const int old = split_counter_arrive(&p.counters[tile]);
+            const int old = split_counter_arrive(&p.counters[cb.lo]);
             const int last = old == (cb.hi - cb.lo);
             *last_flag = last;
         }
@@ -471,7 +471,7 @@ __device__ void run_compute(const GemmParams &p, Sched sched, uint8_t *smem, Dec
             continue;
         reduce_tile<(NT <= 2 ? 2 : 1)>(p, ti, cb, w * 32 + lane, DEC_WARPS * 32); // lighter: no spills
         if (w == 0 && lane == 0)
-            p.counters[tile] = 0;
+            p.counters[cb.lo] = 0;
     }
 }
 

@@ -592,7 +592,7 @@ __device__ void run_epilogue(const GemmParams &p, const SegTable &seg, Sched sch
                 if (!mbar_wait(&bars.split_done[n_seen], 0, ctl, W4A16_DEV_TIMEOUT))
                     return;
                 const Contributors cb = contributors(p, sched, st_tile);
-                const int old = split_counter_arrive(&p.counters[tile]);
+                const int old = split_counter_arrive(&p.counters[cb.lo]);
                 split_tiles[*n_split] = tile;
                 split_last[*n_split] = old == (cb.hi - cb.lo);
                 ++*n_split;
@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (threadIdx.x < n_split && last_sh[threadIdx.x] < 0) {
         const int tile = split_tiles_sh[threadIdx.x];
         const Contributors cb = contributors(p, sched, (long long)tile - sched.dp_tiles);
-        const int old = split_counter_arrive(&p.counters[tile]);
+        const int old = split_counter_arrive(&p.counters[cb.lo]);
         last_sh[threadIdx.x] = old == (cb.hi - cb.lo);
     }
     __syncthreads();
@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             // Taller tiles (2-3 contributors): 8 items x 2 contributors in flight per thread.
             reduce_tile<8, 2>(p, ti, cb, threadIdx.x, NUM_THREADS);
         if (threadIdx.x == 0)
-            p.counters[tile] = 0;
+            p.counters[cb.lo] = 0;
     }
 }
 

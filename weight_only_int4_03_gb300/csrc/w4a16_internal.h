@@ -44,6 +44,12 @@ constexpr int EPI_STAGE_BYTES = 4 * EPI_ROWS * 32 * 2;     // per warp: 32 rows 
 
 constexpr int MAX_SEGMENTS = 1024;
 
+// A workspace begins with the status word and the split tiles' arrival counters, one per CTA, at places
+// that no size of a call moves (what follows them need not be zero).
+constexpr long long HEADER_BYTES = 256;
+constexpr int MAX_CTAS = 1024; // of a launch that splits tiles
+constexpr long long COUNTER_BYTES = 4LL * MAX_CTAS;
+
 // Column-slice small-M kernel: 16 weight columns over all of K per work item; a pipeline
 // stage holds slice_bpw consecutive blocks for each of the 8 compute warps.
 constexpr int SLICE_N = 16;

@@ -22,9 +22,6 @@ static __device__ __align__(256) unsigned char g_scratch[W4A16_NOALLOC_SCRATCH_B
 namespace {
 
 constexpr int MAX_DEVICES = 64;
-constexpr size_t HEADER_BYTES = 256; // the workspace starts with the status word ...
-constexpr int TILE_COLS = 128;       // ... then one counter per (token tile, 128-column tile)
-constexpr int MIN_TILE_ROWS = 8;     // the smallest token tile either kernel uses
 
 std::mutex g_mu;
 void *g_scratch_ptr[MAX_DEVICES];
@@ -84,12 +81,7 @@ extern "C" int w4a16_gemm_noalloc(const void *a, int lda, const int32_t *b_packe
 
     // The status word and the tile counters must start at zero.  A call that completes leaves
     // them so, but one that gave up on a bounded wait may not: clear them on every call.
-    const size_t tiles_bound =
-        (size_t)((m + MIN_TILE_ROWS - 1) / MIN_TILE_ROWS) * (size_t)(n / TILE_COLS);
-    size_t clear = HEADER_BYTES + 4 * tiles_bound;
-    if (clear > need)
-        clear = need;
-    err = cudaMemsetAsync(ws, 0, clear, stream);
+    err = cudaMemsetAsync(ws, 0, w4::HEADER_BYTES + w4::COUNTER_BYTES, stream);
     if (err != cudaSuccess)
         return (6 << 16) | (err & 0xFFFF);
 
