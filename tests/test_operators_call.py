@@ -158,3 +158,10 @@ def test_both_ways_count_their_arguments(w4, calls, name):
     for args in (a[:-1], a + [0]):
         assert outcome(calls[name], args) is TypeError
         assert outcome(w4._through_ctypes(name), args) is TypeError
+
+
+@pytest.mark.parametrize("sections,error", [([30.5, 33.5], TypeError), ([1 << 32, 64], OverflowError), (["64"], TypeError)])
+def test_sections_are_32_bit_integers(w4, sections, error):
+    """Not cut to them: 30 and 33 of 30.5 and 33.5, or 0 of 2^32, would be other axes."""
+    with pytest.raises(error):  # the flag is one that no entry has
+        w4.w4a16_rope_append(P, P, P, P, P, P, P, P, P, None, 4, 4, 2, 128, 128, sections, 100, 16, 8, flags=1 << 30, stream=0)

@@ -374,7 +374,7 @@ def _kv_strides(kv_strides, page_size: int, n_kv_heads: int, head_dim: int):
 
 @functools.lru_cache(maxsize=64)
 def _int32_array(values):
-    array = (ctypes.c_int32 * len(values))(*map(int, values))
+    array = (ctypes.c_int32 * len(values))(*map(_CONVERT[_I], values))
     return array, ctypes.addressof(array)
 
 
