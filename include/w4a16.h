@@ -427,7 +427,8 @@ int w4a16_csr_from_token_routes(int n_expert, int n_tokens, int experts_per_toke
  *   slots        device int64 [n_tokens]: page * page_size + token in the page; negative: the
  *                token's k and v are not written (padding).  Two tokens must not share a slot
  *   status       device int32 or NULL: W4A16_DEV_POSITION is OR-ed in when a position is outside
- *                [0, max_pos) (values that need it are not written), W4A16_DEV_SLOT when a slot is
+ *                [0, max_pos) (values that need it are not written, nor, with 16-byte copies and a section
+ *                that ends inside them, the rest of their eight pairs), W4A16_DEV_SLOT when a slot is
  *                past the cache (that token's k and v are not written)
  *   sections     host int32 [n_axes], non-negative, with sum rot_dim / 2;  n_axes 1..4
  *   n_heads, n_kv_heads  either may be 0 (its pointers are then not looked at)
@@ -454,9 +455,12 @@ size_t w4a16_paged_attention_workspace_size(int batch, int n_heads, int n_kv_hea
  * c = h / (n_heads / n_kv_heads), over positions i in [max(0, len - window), len) (window 0: all):
  *     out[b][h] = sum_i p_i v_i,   p = softmax(scale q . k_i),   lse[b][h] = log sum_i e^(scale q . k_i)
  * The new token's own key and value are part of the cache (w4a16_rope_append writes them first).
- * A sequence of length 0 gets zeros and lse = -inf.  Rows of the cache past a length are never
- * read, whatever they hold.  Softmax and sums are fp32; p enters the value product as a 16-bit
- * value plus a 16-bit remainder, so a live value that is infinite gives NaN.
+ * A sequence of length 0 (or with scores of -inf alone) gets zeros and lse = -inf.  Rows of the cache
+ * past a length are never read, whatever they hold.  Softmax and sums are fp32 (the scores of 256-wide
+ * heads, at most eight per KV head, in one chain of tensor-core sums, which are cut off instead of rounded:
+ * up to a bit and a half less than elsewhere).  p enters the value product as a 16-bit value plus a 16-bit
+ * remainder, to 2^-17 (bf16) or 2^-23 (fp16; to 2^-40 absolute) of itself; a live value that is infinite
+ * therefore gives NaN.
  *   q            device 16-bit [batch][ldq], head h at h * head_dim;  ldq % 8 == 0
  *   out          device 16-bit [batch][ldo];  ldo % 8 == 0;  lse  device fp32 [batch][n_heads] or NULL
  *   block_table  device int32 [batch][ld_table], ld_table >= max_pages; entries past a sequence's
@@ -505,7 +509,8 @@ size_t w4a16_moe_layer_workspace_size(int n_tokens, int hidden, int inter, int n
  *   topk_ids, topk_weights  device int32 / fp32 [n_tokens][top_k] or NULL: the routing, written
  *   n_tokens       0 (a no-op) .. 64;  hidden % 256 == 0;  inter % 128 == 0;  both at most 65536
  *   n_experts      1 .. 512;  top_k 1 .. 16, at most n_experts
- *   group_size     -1, or a positive multiple of 64 that divides hidden and inter
+ *   group_size     -1, or a positive multiple of 64 that divides hidden and inter (sums are scaled per
+ *                  64-row block: no groups of 16 or 32); no act-order
  *   flags          exactly one of W4A16_FLAG_SWIGLU / _GEGLU; W4A16_FLAG_BF16, _HAS_ZP, _MOE_RENORM,
  *                  _IS_K_FULL
  * 16-byte aligned buffers, leading dimensions multiples of 8.  A NaN score counts as the lowest when
