@@ -207,7 +207,8 @@ int w4_unpack(const int32_t *b_packed, int32_t *qweight, int k, int n, cudaStrea
  * fp32 partial tiles and, with act-order, the gathered copy of A.  It must be zero-filled
  * once after allocation; the kernels leave it ready for the next call, of these or any other
  * sizes that need no more bytes, dense or grouped (counters reset themselves), so no per-call
- * memset is needed.  The one exception: after w4a16_status has
+ * memset is needed.  The size follows the token tile's height and can fall as m rises (257 rows
+ * need more than 448): take the largest of the row counts in use.  The one exception: after w4a16_status has
  * reported W4A16_DEV_TIMEOUT, a CTA that gave up may have left its tile counters part-way, and
  * the next call would then reduce the wrong partials -- zero-fill the whole workspace again
  * (cudaMemsetAsync over its size) before reusing it.  Calls that run concurrently need
