@@ -96,7 +96,7 @@ extern "C" {
                                            once to bf16 (8 significant bits), products sum in
                                            fp32 and C is rounded once to bf16               */
 
-#define W4A16_FLAG_ROPE_ADJACENT (1u << 17) /* w4a16_rope_append: a pair is values 2i and 2i + 1 of the
+#define W4A16_FLAG_ROPE_ADJACENT (1u << 17) /* rotary appends: a pair is values 2i and 2i + 1 of the
                                            rotated part, not i and rot_dim / 2 + i          */
 #define W4A16_FLAG_MOE_RENORM (1u << 18) /* w4a16_moe_layer: the chosen experts' probabilities are
                                            divided by their sum                             */
@@ -123,10 +123,11 @@ extern "C" {
 #define W4A16_DEV_SCHEDULE 8    /* a CSR entry was outside its range                           */
 #define W4A16_DEV_ZERO 16       /* w4a16_zero_points_check: a zero point is not an integer in
                                    [0, 15]                                                   */
-#define W4A16_DEV_POSITION 32   /* w4a16_rope_append: a position outside [0, max_pos)          */
-#define W4A16_DEV_SLOT 64       /* w4a16_rope_append: a slot past the cache                    */
-#define W4A16_DEV_LENGTH 128    /* w4a16_paged_attention: a length outside [0, max_pages x page] */
-#define W4A16_DEV_PAGE 256      /* w4a16_paged_attention: a page number outside [0, n_pages)   */
+#define W4A16_DEV_POSITION 32   /* rotary appends: a position outside [0, max_pos)             */
+#define W4A16_DEV_SLOT 64       /* rotary appends: a slot past the cache                       */
+#define W4A16_DEV_LENGTH 128    /* paged attentions: a length outside [0, max_pages x page]    */
+#define W4A16_DEV_PAGE 256      /* paged attentions: a page number outside [0, n_pages)        */
+#define W4A16_DEV_SETTING 512   /* w4a16_sample: a row's settings outside their ranges         */
 
 /* ------------------------------------------------------------------------------------------
  * Packed tile layout (this library's own; the pages only say the kernel layout is a
@@ -481,6 +482,104 @@ int w4a16_paged_attention(const void *q, int ldq, const void *k_cache, const voi
                           void *workspace, size_t workspace_bytes, int batch, int n_heads,
                           int n_kv_heads, int head_dim, int page_size, int n_pages, int max_pages,
                           int window, float scale, unsigned flags, cudaStream_t stream);
+
+/* w4a16_rope_append with the heads of q and k normalised first, in the same launch:
+ *     y = x rsqrt(mean(x^2) + eps) w
+ * over a head's head_dim values, with the weights w = q_norm or k_norm; v is copied.  Sums are fp32 and nothing
+ * is rounded between the norm and the rotation.  As w4a16_rope_append, but for:
+ *   q_norm, k_norm  device 16-bit [head_dim], or NULL: those heads are not normalised
+ *   eps          finite, not negative
+ *   rot_dim      even, 0 .. head_dim; 0: no rotation, with n_axes 0 (cos_sin, positions and sections are then not
+ *                looked at)
+ * 16-byte copies also need q_norm and k_norm 16-byte aligned and head_dim at most 512. */
+int w4a16_norm_rope_append(const void *q, int ldq, const void *k, int ldk, const void *v, int ldv,
+                           const void *q_norm, const void *k_norm, float eps, void *q_out, int ldqo,
+                           void *k_cache, void *v_cache, long long kv_page_stride,
+                           long long kv_token_stride, long long kv_head_stride, const float *cos_sin,
+                           int max_pos, const int32_t *positions, int ld_pos, const long long *slots,
+                           int32_t *status, int n_tokens, int n_heads, int n_kv_heads, int head_dim,
+                           int rot_dim, const int32_t *sections, int n_axes, int page_size, int n_pages,
+                           unsigned flags, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * A paged cache held in 4 bits.  Each group of group_size values of a head (one token's) has a step s and a base b
+ * of 16 bits (fp16, or bf16 with W4A16_FLAG_BF16), and each value a code in 0..15 that stands for code s + b:
+ *     b = r(min),  s = r((max - min) / 15),  code = (x - b) / s to the nearest integer (ties to even), cut to 0..15
+ * where r rounds to nearest even; a group whose range rounds to 0 (bf16: to a subnormal number) has s = 0 and code 0.
+ * A group without a finite range (it holds an infinity or a NaN, or its step or base rounds to infinity) reads as NaN.
+ * Page p begins at byte p * page_stride, with one record per KV head, of w4a16_kv4_record_bytes bytes each:
+ *     key codes [page_size][head_dim / 8] words, value codes the same, key (s, b) pairs
+ *     [page_size][head_dim / group_size], value pairs the same
+ * A word holds the codes of eight values in a row, value 8 w + i at bits 4 i .. 4 i + 3 of word w.  Words of a
+ * row do not lie in order: with B = head_dim / 64, key word 8 b + 2 t + i (b < B, t < 4, i < 2) is at place
+ * 16 (b / 2) + 4 t + 2 (b % 2) + i (B = 1: in order), value word 8 b + g (g < 8) at place g B + b.
+ * head_dim 64, 128 or 256; group_size -1 (the head) or a multiple of 64 that divides head_dim; page_size
+ * 1 .. W4A16_KV4_MAX_PAGE.  Position i of a sequence is token i % page_size of page block_table[i / page_size].
+ * ---------------------------------------------------------------------------------------- */
+#define W4A16_KV4_MAX_PAGE 65536
+
+/* Bytes of one head's record in a page, a multiple of 16; 0 for sizes that the cache does not take. */
+size_t w4a16_kv4_record_bytes(int page_size, int head_dim, int group_size);
+
+/* w4a16_norm_rope_append into a cache held in 4 bits: keys are coded from the fp32 results of norm and rotation.
+ * As w4a16_norm_rope_append, but for:
+ *   cache        device, 16-byte aligned; page_stride in bytes, a multiple of 16, at least n_kv_heads records
+ *   k_out, v_out device 16-bit, token t's heads at t * ldko (ldvo), or NULL: what the cache now stands for, rounded
+ *                once, for a prompt's own attention.  Written for tokens without a slot too; may be k and v
+ *                themselves (same leading dimensions)
+ *   n_heads      may be 0;  n_kv_heads positive
+ *   rot_dim      a multiple of 16
+ * All 16-bit buffers and cos_sin 16-byte aligned, leading dimensions multiples of 8.  A key one of whose positions is
+ * out of range (W4A16_DEV_POSITION) is not written at all, in no place. */
+int w4a16_kv4_append(const void *q, int ldq, const void *k, int ldk, const void *v, int ldv,
+                     const void *q_norm, const void *k_norm, float eps, void *q_out, int ldqo, void *cache,
+                     long long page_stride, void *k_out, int ldko, void *v_out, int ldvo,
+                     const float *cos_sin, int max_pos, const int32_t *positions, int ld_pos,
+                     const long long *slots, int32_t *status, int n_tokens, int n_heads, int n_kv_heads,
+                     int head_dim, int rot_dim, const int32_t *sections, int n_axes, int page_size,
+                     int n_pages, int group_size, unsigned flags, cudaStream_t stream);
+
+/* Workspace bytes of w4a16_kv4_attention: as w4a16_paged_attention_workspace_size, with the same rules. */
+size_t w4a16_kv4_attention_workspace_size(int batch, int n_heads, int n_kv_heads, int head_dim, int num_sms);
+
+/* w4a16_paged_attention over a cache held in 4 bits, whose values code s + b are used as they are: products and sums
+ * are fp32, no key or value is rounded to 16 bits.  q and out are fp16, or bf16 with W4A16_FLAG_BF16, as are the
+ * cache's steps and bases.  As w4a16_paged_attention, but for the cache (above) and these points: queries go in as fp16
+ * scaled by a power of two per head, exact down to 2^-38 of the head's largest (in bf16, queries beyond 2^112 are too
+ * large); p s goes into the value product to 2^-22 of itself, or to 2^-38 of the largest step of the values
+ * seen.  A group that reads as NaN makes NaN of what it touches.  page_size at most W4A16_KV4_MAX_PAGE. */
+int w4a16_kv4_attention(const void *q, int ldq, const void *cache, long long page_stride, void *out,
+                        int ldo, float *lse, const int32_t *block_table, int ld_table,
+                        const int32_t *seq_lens, void *workspace, size_t workspace_bytes, int batch,
+                        int n_heads, int n_kv_heads, int head_dim, int page_size, int n_pages,
+                        int max_pages, int group_size, int window, float scale, unsigned flags,
+                        cudaStream_t stream);
+
+/* The next token of each row of logits, from given uniform numbers.  With P_i = e^((l_i - max l) / T) and tokens
+ * ordered by (logit falling, index rising):
+ *     top_k keeps the first top_k; top_p, of these, the shortest beginning whose sum of P reaches top_p times their sum
+ *     (one token at least); min_p, of these, those with P_i >= min_p;
+ *     token = the first index i at which the sum of the kept P_j, j <= i, exceeds uniform times the sum of all kept.
+ * P is held as a multiple of 2^-43, to 2^-30 of itself, and sums are exact: results do not depend on the batch and
+ * repeats are identical.  One launch, no workspace.
+ *   logits       device 16-bit [batch][ld] (fp16, or bf16 with W4A16_FLAG_BF16), 2-byte aligned (rows of 16-byte
+ *                alignment are read in 16-byte loads); a NaN counts as -inf, and -inf is never chosen
+ *   uniform      device fp32 [batch], in [0, 1)
+ *   temperature  device fp32 [batch] or NULL (1): finite, not negative; 0 takes the largest logit (the lowest index
+ *                where some are equal) whatever the other settings
+ *   top_k        device int32 [batch] or NULL: 0 and below: no limit
+ *   top_p, min_p device fp32 [batch] or NULL (1, 0): top_p of 1 and above and min_p of 0 and below: no limit; min_p
+ *                above 1 counts as 1
+ *   tokens       device int32 [batch]
+ *   logprobs     device fp32 [batch] or NULL: log of the token's share of the kept sum
+ *   status       device int32 or NULL: W4A16_DEV_SETTING is OR-ed in for a row with a setting out of range or NaN; its
+ *                token is -1 and its logprob NaN
+ *   batch        0 (a no-op) .. 2^24;  vocab 1 .. 524288, ld >= vocab
+ * A row without a logit above -inf gets token -1 and logprob -inf. */
+int w4a16_sample(const void *logits, int ld, const float *uniform, const float *temperature,
+                 const int32_t *top_k, const float *top_p, const float *min_p, int32_t *tokens,
+                 float *logprobs, int32_t *status, int batch, int vocab, unsigned flags,
+                 cudaStream_t stream);
 
 /* Workspace bytes of w4a16_moe_layer (0 for sizes that it rejects).  Zero-filled once after
  * allocation, after which it serves calls of any sizes that need no more bytes, in any order; calls that

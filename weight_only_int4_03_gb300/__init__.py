@@ -45,9 +45,11 @@ W4A16_DEV_POSITION = 32
 W4A16_DEV_SLOT = 64
 W4A16_DEV_LENGTH = 128
 W4A16_DEV_PAGE = 256
+W4A16_DEV_SETTING = 512
 
 W4A16_MAX_SEGMENTS = 1024
 W4A16_MOE_MAX_BLOCKS = 4096
+W4A16_KV4_MAX_PAGE = 65536
 W4A16_ARG_SCRATCH = 10
 W4A16_ARG_QZERO = 11
 W4A16_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
@@ -94,6 +96,15 @@ _SIGNATURES = {
     "w4a16_paged_attention_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
     "w4a16_paged_attention": (_I, [_P, _I, _P, _P, _LL, _LL, _LL, _P, _I, _P, _P, _I, _P, _P, _SZ, _I, _I,
                                    _I, _I, _I, _I, _I, _I, _F, _U, _P]),
+    "w4a16_norm_rope_append": (_I, [_P, _I, _P, _I, _P, _I, _P, _P, _F, _P, _I, _P, _P, _LL, _LL, _LL, _P, _I, _P,
+                                    _I, _P, _P, _I, _I, _I, _I, _I, _P, _I, _I, _I, _U, _P]),
+    "w4a16_kv4_record_bytes": (_SZ, [_I, _I, _I]),
+    "w4a16_kv4_append": (_I, [_P, _I, _P, _I, _P, _I, _P, _P, _F, _P, _I, _P, _LL, _P, _I, _P, _I, _P, _I, _P, _I,
+                              _P, _P, _I, _I, _I, _I, _I, _P, _I, _I, _I, _I, _U, _P]),
+    "w4a16_kv4_attention_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
+    "w4a16_kv4_attention": (_I, [_P, _I, _P, _LL, _P, _I, _P, _P, _I, _P, _P, _SZ, _I, _I, _I, _I, _I, _I, _I, _I,
+                                 _I, _F, _U, _P]),
+    "w4a16_sample": (_I, [_P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _U, _P]),
     "w4a16_moe_layer_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
     "w4a16_moe_layer": (_I, [_P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _I, _P, _P, _P, _SZ, _I, _I,
                              _I, _I, _I, _I, _I, _U, _P]),
@@ -381,7 +392,8 @@ def _int32_array(values):
 def _direct_calls():
     """The decode-step operators' entries, taking tensors where they take pointers: from the extension
     module beside the library, or through ctypes where that was not built for this interpreter."""
-    names = ("w4a16_rope_append", "w4a16_paged_attention", "w4a16_moe_layer")
+    names = ("w4a16_rope_append", "w4a16_paged_attention", "w4a16_moe_layer", "w4a16_norm_rope_append",
+             "w4a16_kv4_append", "w4a16_kv4_attention", "w4a16_sample")
     if os.path.exists(CALL_PATH):
         import importlib.util
         spec = importlib.util.spec_from_file_location("_w4a16_call", CALL_PATH)
@@ -424,7 +436,8 @@ def _through_ctypes(name):
     return call
 
 
-_rope_append, _paged_attention, _moe_layer = _direct_calls()
+(_rope_append, _paged_attention, _moe_layer, _norm_rope_append, _kv4_append, _kv4_attention,
+ _sample) = _direct_calls()
 
 
 def w4a16_rope_append(q, k, v, q_out, k_cache, v_cache, cos_sin, positions, slots, status, n_tokens: int,
@@ -464,6 +477,83 @@ def w4a16_paged_attention(q, k_cache, v_cache, out, block_table, seq_lens, works
         out, n_heads * head_dim if ldo is None else ldo, lse, block_table,
         max_pages if ld_table is None else ld_table, seq_lens, workspace, workspace_bytes, batch, n_heads,
         n_kv_heads, head_dim, page_size, n_pages, max_pages, window, scale, flags, _stream(stream)))
+
+
+def w4a16_norm_rope_append(q, k, v, q_norm, k_norm, eps: float, q_out, k_cache, v_cache, cos_sin, positions, slots,
+                           status, n_tokens: int, n_heads: int, n_kv_heads: int, head_dim: int, rot_dim: int,
+                           sections, max_pos: int, page_size: int, n_pages: int, flags: int = 0,
+                           ldq: int | None = None, ldk: int | None = None, ldv: int | None = None,
+                           ldqo: int | None = None, ld_pos: int | None = None, kv_strides=None, stream=None) -> None:
+    """w4a16_rope_append with the heads of q and k normalised first (weights `q_norm`, `k_norm` [head_dim], or
+    None) -- see include/w4a16.h."""
+    sec, sec_at = _int32_array(sections if type(sections) is tuple else tuple(sections))
+    ps, ts, hs = _kv_strides(kv_strides, page_size, n_kv_heads, head_dim)
+    _check("w4a16_norm_rope_append", _norm_rope_append(
+        q, n_heads * head_dim if ldq is None else ldq, k, n_kv_heads * head_dim if ldk is None else ldk,
+        v, n_kv_heads * head_dim if ldv is None else ldv, q_norm, k_norm, eps, q_out,
+        n_heads * head_dim if ldqo is None else ldqo, k_cache, v_cache, ps, ts, hs, cos_sin, max_pos, positions,
+        n_tokens if ld_pos is None else ld_pos, slots, status, n_tokens, n_heads, n_kv_heads, head_dim, rot_dim,
+        sec_at, len(sec), page_size, n_pages, flags, _stream(stream)))
+
+
+def w4a16_kv4_record_bytes(page_size: int, head_dim: int, group_size: int) -> int:
+    """Bytes of one KV head's record in a page of the cache held in 4 bits; 0 for sizes that it does not take."""
+    return int(_lib.w4a16_kv4_record_bytes(page_size, head_dim, group_size))
+
+
+def _kv4_page_stride(page_stride, page_size: int, n_kv_heads: int, head_dim: int, group_size: int) -> int:
+    """Bytes from page to page; by default the records of all heads and nothing between."""
+    return n_kv_heads * w4a16_kv4_record_bytes(page_size, head_dim, group_size) if page_stride is None else page_stride
+
+
+def w4a16_kv4_append(q, k, v, q_norm, k_norm, eps: float, q_out, cache, cos_sin, positions, slots, status,
+                     n_tokens: int, n_heads: int, n_kv_heads: int, head_dim: int, rot_dim: int, sections,
+                     max_pos: int, page_size: int, n_pages: int, group_size: int, flags: int = 0, k_out=None,
+                     v_out=None, ldq: int | None = None, ldk: int | None = None, ldv: int | None = None,
+                     ldqo: int | None = None, ldko: int | None = None, ldvo: int | None = None,
+                     ld_pos: int | None = None, page_stride: int | None = None, stream=None) -> None:
+    """w4a16_norm_rope_append into a paged cache held in 4 bits; `k_out`, `v_out` receive what the cache stands
+    for -- see include/w4a16.h."""
+    sec, sec_at = _int32_array(sections if type(sections) is tuple else tuple(sections))
+    width = n_kv_heads * head_dim
+    _check("w4a16_kv4_append", _kv4_append(
+        q, n_heads * head_dim if ldq is None else ldq, k, width if ldk is None else ldk, v,
+        width if ldv is None else ldv, q_norm, k_norm, eps, q_out, n_heads * head_dim if ldqo is None else ldqo,
+        cache, _kv4_page_stride(page_stride, page_size, n_kv_heads, head_dim, group_size), k_out,
+        width if ldko is None else ldko, v_out, width if ldvo is None else ldvo, cos_sin, max_pos, positions,
+        n_tokens if ld_pos is None else ld_pos, slots, status, n_tokens, n_heads, n_kv_heads, head_dim, rot_dim,
+        sec_at, len(sec), page_size, n_pages, group_size, flags, _stream(stream)))
+
+
+def w4a16_kv4_attention_workspace_size(batch: int, n_heads: int, n_kv_heads: int, head_dim: int,
+                                       num_sms: int = 0) -> int:
+    return int(_lib.w4a16_kv4_attention_workspace_size(batch, n_heads, n_kv_heads, head_dim, num_sms))
+
+
+def w4a16_kv4_attention(q, cache, out, block_table, seq_lens, workspace, batch: int, n_heads: int, n_kv_heads: int,
+                        head_dim: int, page_size: int, n_pages: int, max_pages: int, group_size: int, scale: float,
+                        flags: int = 0, window: int = 0, lse=None, ldq: int | None = None, ldo: int | None = None,
+                        ld_table: int | None = None, page_stride: int | None = None,
+                        workspace_bytes: int | None = None, stream=None) -> None:
+    """One new token per sequence over a paged cache held in 4 bits: out, and log-sum-exp into `lse` when given
+    -- see include/w4a16.h."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check("w4a16_kv4_attention", _kv4_attention(
+        q, n_heads * head_dim if ldq is None else ldq, cache,
+        _kv4_page_stride(page_stride, page_size, n_kv_heads, head_dim, group_size), out,
+        n_heads * head_dim if ldo is None else ldo, lse, block_table, max_pages if ld_table is None else ld_table,
+        seq_lens, workspace, workspace_bytes, batch, n_heads, n_kv_heads, head_dim, page_size, n_pages, max_pages,
+        group_size, window, scale, flags, _stream(stream)))
+
+
+def w4a16_sample(logits, uniform, tokens, batch: int, vocab: int, flags: int = 0, temperature=None, top_k=None,
+                 top_p=None, min_p=None, logprobs=None, status=None, ld: int | None = None, stream=None) -> None:
+    """The next token of each row of 16-bit logits, from uniform numbers in [0, 1) and each row's settings
+    (device tensors [batch], or None) -- see include/w4a16.h."""
+    _check("w4a16_sample", _sample(
+        logits, vocab if ld is None else ld, uniform, temperature, top_k, top_p, min_p, tokens, logprobs, status, batch,
+        vocab, flags, _stream(stream)))
 
 
 def w4a16_moe_layer_workspace_size(n_tokens: int, hidden: int, inter: int, n_experts: int, top_k: int) -> int:

@@ -27,7 +27,7 @@ PYTHON_INCLUDE = sysconfig.get_paths()["include"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["w4a16_gemm.cu", "w4a16_decode.cu", "w4a16_aux.cu", "w4a16_api.cu", "w4a16_noalloc.cu",
            "w4a16_loader.cu", "w4a16_rope.cu", "w4a16_attention.cu",
-           "w4a16_moe_layer.cu"]
+           "w4a16_moe_layer.cu", "w4a16_norm_rope.cu", "w4a16_kv4_attention.cu", "w4a16_sample.cu"]
 
 
 def _nvcc() -> str:

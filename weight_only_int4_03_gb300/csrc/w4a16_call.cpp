@@ -116,6 +116,10 @@ PyMethodDef methods[] = {
     method<&w4a16_rope_append>("w4a16_rope_append"),
     method<&w4a16_paged_attention>("w4a16_paged_attention"),
     method<&w4a16_moe_layer>("w4a16_moe_layer"),
+    method<&w4a16_norm_rope_append>("w4a16_norm_rope_append"),
+    method<&w4a16_kv4_append>("w4a16_kv4_append"),
+    method<&w4a16_kv4_attention>("w4a16_kv4_attention"),
+    method<&w4a16_sample>("w4a16_sample"),
     {nullptr, nullptr, 0, nullptr},
 };
 

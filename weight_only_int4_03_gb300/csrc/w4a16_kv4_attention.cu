@@ -1,0 +1,740 @@
+// w4a16_kv4_attention.cu -- attention of one new token per sequence over a paged cache held in 4 bits.
+//
+// For sequence b, query head h of KV head c, over the positions i in [first, len), with the codes k, v in
+// 0..15 and the steps s and bases a of the groups of values (w4a16_kv4.cuh):
+//     x_i = scale sum_groups (s_i (q . k_i) + a_i sum q),   p_i = e^(x_i - max x),   l = sum p_i,
+//     out = sum_i ((p_i s_i) (v_i - 8) + p_i (a_i + 8 s_i)) / l,   lse = max x + log l.
+// So neither side is turned back into 16-bit values: codes go into the products as they are, steps and bases
+// are applied in fp32 to sums and to p.  That values are v - 8 keeps the sums over a long axis near zero.
+//
+// Bound by memory in principle, by instructions in fact: a position of a KV head of 128 is 136 bytes,
+// which at the copy rate leaves an SM 6 cycles for it.  What the design does about it:
+//   - A code is the fp16 number q 2^-24 (or q 2^-20, four bits higher) as soon as the others are masked
+//     off, so that a pair costs one instruction and a shift for every second.  Values q 2^-20 meet queries a
+//     sixteenth as large, and outputs of their own factor.  That holds for fp16 alone, so queries are
+//     scaled to fp16 by a power of two per head (their values are exact down to 2^-38 of the largest), whatever
+//     the cache's type.
+//   - Positions are the rows of the score product (S^T = K Q^T) and value dims those of the value product
+//     (O^T = V^T P^T), so that eight heads fill an m16n8k16.  P^T is the scores' fragment transposed by
+//     movmatrix.  p s goes in as a 16-bit value and the 16-bit remainder, times a power of two that
+//     keeps it below 2^15: to 2^-22 of itself and 2^-38 of the largest step's.
+//   - The maximum is lazy: it moves only when a score passes it by a factor of 4, and a step of 32 positions
+//     asks for that by one vote; sums of p and of p a are kept per lane until the end.
+//   - A value product starts from -8 sum p s (one MMA against constants makes it) and is added to the outputs in
+//     fp32 every 32 positions: the MMA cuts sums off, which over many positions of one sign would show.
+//   - The words of a row lie in the order of the lanes, so that a lane's share of a row is one load; keys are
+//     copied to places that only the copying lane reads.
+// The work is split as in the 16-bit cache's attention (w4a16_split.cuh).
+#include <type_traits>
+
+#include "w4a16_kv4.cuh"
+#include "w4a16_split.cuh"
+
+namespace w4 {
+namespace ops {
+
+constexpr int KV4_STEP = 32;                           // positions per warp and step
+constexpr int KV4_UNIT = SPLIT_WARPS * KV4_STEP;       // positions per work unit
+constexpr float KV4_UP = 8192.f;                       // what p s / reference is multiplied by for the value product
+constexpr float KV4_LAZY = 2.f;                        // by how much (log2) a score may pass the maximum
+
+struct Kv4AttParams {
+    const uint16_t *q;
+    const uint8_t *cache;
+    uint16_t *out;
+    float *lse;
+    const int32_t *table;
+    SplitParams split;
+    long long page_stride;
+    Kv4Record rec;
+    int ldq, ldo, ld_table;
+    int heads, group, tiles;
+    int page, n_pages;
+    uint32_t page_magic, page_shift; // position / page = umulhi(position, magic) >> shift; magic 0: page 1
+    float scale_log2;
+};
+
+template <int D, int G, int NT>
+struct Kv4Geom {
+    static constexpr int BLOCKS = D / 64;
+    static constexpr int ROW = D / 2;                  // bytes of a row of codes
+    static constexpr int LANE = ROW / 4;               // a lane's bytes of a key row
+    static constexpr int KEYS = 16 * ROW;              // a sub-step's keys, and as many bytes of values
+    static constexpr int PARAMS = 16 * 4 * G;          // a sub-step's steps and bases of one side
+    static constexpr int SUB = 2 * KEYS + 2 * PARAMS;
+    static constexpr int STAGE = 2 * SUB;
+    static constexpr int STAGES = D == 256 ? 2 : 3;    // three of 256-wide rows leave room for one block
+    static constexpr int CTAS = D * NT > 128 ? 2 : 3;  // blocks per SM
+    static constexpr int ROW_COST = 4;                 // of a row by itself, in units
+    static constexpr int HEADS = 8 * NT;
+    static constexpr int SMEM = SPLIT_WARPS * STAGES * STAGE > SPLIT_WARPS * HEADS * D * 4 ? SPLIT_WARPS * STAGES * STAGE
+                                                                                          : SPLIT_WARPS * HEADS * D * 4;
+};
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a)
+{
+    uint32_t d;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+
+// N bytes from global to shared memory, or N zero bytes when `live` is false.
+template <int N>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void *src, bool live)
+{
+    if (N == 16)
+        cp_async16(dst, src, live);
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(live ? N : 0)
+                     : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t a)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+
+template <int WORDS>
+__device__ __forceinline__ void lds_words(uint32_t a, uint32_t *w)
+{
+    if (WORDS == 1) {
+        w[0] = lds32(a);
+    } else if (WORDS == 2) {
+        const uint2 v = lds64(a);
+        w[0] = v.x;
+        w[1] = v.y;
+    } else {
+        const uint4 v = lds128(a);
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2] = v.z;
+        w[3] = v.w;
+    }
+}
+
+// Where the 16-byte chunk `chunk` of value row `row` of a sub-step lies: spread so that the four rows which a load
+// of all lanes touches lie in different banks.
+template <int D>
+__device__ __forceinline__ int value_chunk(int row, int chunk)
+{
+    return D == 64 ? chunk : D == 128 ? chunk ^ (row & 2) : chunk ^ (2 * (row & 3));
+}
+
+template <int D, int G, int NT, bool BF>
+__global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_attention_kernel(const Kv4AttParams p)
+{
+    using M = Kv4Geom<D, G, NT>;
+    constexpr int BLOCKS = M::BLOCKS, TILES = 4 * BLOCKS; // 16-wide tiles of the output dims
+    constexpr int PER = BLOCKS / G;                       // blocks of 64 per group
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ SplitShared shared;
+    __shared__ uint8_t live_bits[M::STAGES][SPLIT_THREADS];
+    __shared__ float stat[SPLIT_WARPS][M::HEADS][2];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const int row_of = (g >> 1) + 4 * (g & 1); // the position of the eight that is row g of the score product
+    pdl_wait();
+    pdl_launch_dependents();
+
+    Split<KV4_UNIT, M::ROW_COST> split(p.split, shared);
+    // Sequences without a position: zeros and -inf.
+    for (int b = blockIdx.x; b < p.split.batch; b += gridDim.x) {
+        if (!split.empty(b))
+            continue;
+        for (int i = tid; i < p.heads * D / 8; i += SPLIT_THREADS)
+            *reinterpret_cast<uint4 *>(p.out + (long long)b * p.ldo + 8 * i) = make_uint4(0, 0, 0, 0);
+        if (p.lse)
+            for (int h = tid; h < p.heads; h += SPLIT_THREADS)
+                p.lse[(long long)b * p.heads + h] = -INFINITY;
+    }
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * (M::STAGES * M::STAGE);
+
+    SplitSegment seg;
+    while (split.next(seg)) {
+        const int b = seg.b, c = seg.row / p.tiles, h0 = (seg.row - c * p.tiles) * M::HEADS;
+        const int nh = min(M::HEADS, p.group - h0); // heads of this tile
+        const int len = seg.len, steps = seg.unit1 - seg.unit0;
+        const int pos0 = seg.first + seg.unit0 * KV4_UNIT + warp * KV4_STEP + row_of; // this lane's first position
+
+        // --- copies ---------------------------------------------------------------------------
+        // A lane looks after positions pos0 + 8 i of a step: pages are looked up one step before they are used.
+        const int32_t *tab = p.table + (long long)b * p.ld_table;
+        const uint8_t *head = p.cache + c * p.rec.bytes;
+        int next_page[4], next_token[4];
+        auto look_up = [&](int step) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int pos = pos0 + step * KV4_UNIT + 8 * i;
+                const bool in = step < steps && pos < len;
+                const int at = p.page_magic ? (int)(__umulhi((uint32_t)pos, p.page_magic) >> p.page_shift) : pos;
+                next_page[i] = in ? tab[at] : -1;
+                next_token[i] = pos - at * p.page;
+            }
+        };
+        auto issue = [&](int step, int stage) {
+            uint32_t bits = 0;
+            const uint8_t *rec[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool in = step < steps && pos0 + step * KV4_UNIT + 8 * i < len;
+                const bool ok = in && next_page[i] >= 0 && next_page[i] < p.n_pages;
+                if (in && !ok)
+                    atomicOr(p.split.status, W4A16_DEV_PAGE);
+                rec[i] = head + (ok ? (long long)next_page[i] * p.page_stride : 0);
+                bits |= (ok ? 1u : 0u) << i;
+            }
+            live_bits[stage][tid] = (uint8_t)bits;
+            const uint32_t st = ring + stage * M::STAGE;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = i & 1, row = row_of + 8 * r;
+                const uint32_t sub = st + (i >> 1) * M::SUB;
+                const bool ok = (bits >> i) & 1u;
+                const long long at = ok ? (long long)next_token[i] * M::ROW : 0;
+                const uint8_t *keys = rec[i] + at, *values = keys + p.rec.values;
+                if (D == 64) {
+                    cp_async<8>(sub + r * 256 + lane * 8, keys + t * 8, ok);
+                    cp_async<8>(sub + M::KEYS + row * M::ROW + t * 8, values + t * 8, ok);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < D / 128; ++h) {
+                        const int ch = t + 4 * h;
+                        cp_async<16>(sub + (r * (D / 128) + h) * 512 + lane * 16, keys + ch * 16, ok);
+                        cp_async<16>(sub + M::KEYS + row * M::ROW + value_chunk<D>(row, ch) * 16, values + ch * 16, ok);
+                    }
+                }
+            }
+            // Steps and bases: a lane copies those of one of its two positions of a sub-step, of one side.
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const bool second = t & 1;
+                const bool ok = (bits >> (2 * u + (second ? 1 : 0))) & 1u;
+                const uint8_t *src = (second ? rec[2 * u + 1] : rec[2 * u]) + (t >> 1 ? p.rec.value_params : p.rec.key_params) +
+                                     (ok ? (long long)(second ? next_token[2 * u + 1] : next_token[2 * u]) * (4 * G) : 0);
+                cp_async<4 * G>(st + u * M::SUB + 2 * M::KEYS + (t >> 1) * M::PARAMS + (row_of + 8 * (t & 1)) * (4 * G), src, ok);
+            }
+        };
+
+        look_up(0);
+        // --- queries: B fragments of the score product ------------------------------------------
+        uint32_t qf[NT][BLOCKS][2][4]; // [word of a block]: values 0 4, 2 6; a sixteenth of 1 5, 3 7
+        float fac[NT][2], qs[NT][2][G];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const bool in = nt * 8 + g < nh;
+            const uint16_t *qp = p.q + (long long)b * p.ldq + (long long)(c * p.group + h0 + (in ? nt * 8 + g : 0)) * D + 16 * t;
+            uint4 raw[BLOCKS][2];
+            float top = 0.f, sum[G];
+#pragma unroll
+            for (int k = 0; k < BLOCKS; ++k) {
+                if (k % PER == 0)
+                    sum[k / PER] = 0.f;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    raw[k][i] = in ? *reinterpret_cast<const uint4 *>(qp + 64 * k + 8 * i) : make_uint4(0, 0, 0, 0);
+                    const uint32_t w[4] = {raw[k][i].x, raw[k][i].y, raw[k][i].z, raw[k][i].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 f = unpack2<BF>(w[e]);
+                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                        sum[k / PER] += f.x + f.y;
+                    }
+                }
+            }
+#pragma unroll
+            for (int d = 1; d < 4; d <<= 1) {
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+#pragma unroll
+                for (int e = 0; e < G; ++e)
+                    sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], d);
+            }
+            const int up = min(max(13 - ((int)(__float_as_uint(top) >> 23) - 127), -100), 100);
+            const float f0 = __uint_as_float((uint32_t)(up + 127) << 23), f1 = 0.0625f * f0;
+#pragma unroll
+            for (int k = 0; k < BLOCKS; ++k)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float2 v01 = unpack2<BF>(raw[k][i].x), v23 = unpack2<BF>(raw[k][i].y),
+                                 v45 = unpack2<BF>(raw[k][i].z), v67 = unpack2<BF>(raw[k][i].w);
+                    qf[nt][k][i][0] = pack2<false>(v01.x * f0, v45.x * f0);
+                    qf[nt][k][i][1] = pack2<false>(v23.x * f0, v67.x * f0);
+                    qf[nt][k][i][2] = pack2<false>(v01.y * f1, v45.y * f1);
+                    qf[nt][k][i][3] = pack2<false>(v23.y * f1, v67.y * f1);
+                }
+            // This lane's columns are heads 2 t and 2 t + 1: their factor and sums.
+            const float mine = p.scale_log2 * __uint_as_float((uint32_t)(24 - up + 127) << 23);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                fac[nt][e] = __shfl_sync(0xffffffffu, mine, (2 * t + e) * 4);
+#pragma unroll
+                for (int q = 0; q < G; ++q)
+                    qs[nt][e][q] = p.scale_log2 * __shfl_sync(0xffffffffu, sum[q], (2 * t + e) * 4);
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < M::STAGES - 1; ++s) {
+            issue(s, s);
+            cp_async_commit();
+            look_up(s + 1);
+        }
+
+        // --- the running softmax ----------------------------------------------------------------
+        float o[NT][TILES][4], m[NT][2], l[NT][2], base[NT][2][G];
+        float ref = 0.f, up = 0.f; // the power of two above every value step so far, and KV4_UP over it
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int n = 0; n < TILES; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[nt][n][e] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                m[nt][e] = -3.402823466e38f; // not -inf: nothing live yet then gives p = 0
+                l[nt][e] = 0.f;
+#pragma unroll
+                for (int q = 0; q < G; ++q)
+                    base[nt][e][q] = 0.f;
+            }
+        }
+        int stage = 0;
+        for (int step = 0; step < steps; ++step) {
+            cp_async_wait<M::STAGES - 2>();
+            __syncwarp(); // every lane's copies of this stage have landed; the next one is free
+            {
+                int ns = stage + M::STAGES - 1;
+                ns = ns >= M::STAGES ? ns - M::STAGES : ns;
+                issue(step + M::STAGES - 1, ns);
+                cp_async_commit();
+                look_up(step + M::STAGES);
+            }
+            const uint32_t st = ring + stage * M::STAGE;
+            const uint32_t bits = live_bits[stage][tid];
+
+            // Scores x[sub-step][tile][row, column] of positions row_of + 16 u (+ 8), heads 2 t and 2 t + 1.
+            float x[2][NT][4], vs[2][2][G], va[2][2][G];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const uint32_t sub = st + u * M::SUB;
+                uint32_t kw[2][BLOCKS * 2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    if (D == 64) {
+                        lds_words<2>(sub + r * 256 + lane * 8, kw[r]);
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < D / 128; ++h)
+                            lds_words<4>(sub + (r * (D / 128) + h) * 512 + lane * 16, kw[r] + 4 * h);
+                    }
+                }
+                float ks[2][G], ka[2][G];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    uint32_t w[G];
+                    lds_words<G>(sub + 2 * M::KEYS + (row_of + 8 * r) * (4 * G), w);
+#pragma unroll
+                    for (int q = 0; q < G; ++q) {
+                        const float2 f = unpack2<BF>(w[q]);
+                        ks[r][q] = f.x;
+                        ka[r][q] = f.y;
+                    }
+                    lds_words<G>(sub + 2 * M::KEYS + M::PARAMS + (row_of + 8 * r) * (4 * G), w);
+#pragma unroll
+                    for (int q = 0; q < G; ++q) {
+                        const float2 f = unpack2<BF>(w[q]);
+                        vs[u][r][q] = f.x;
+                        va[u][r][q] = fmaf(8.f, f.x, f.y);
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < G; ++q) {
+                    float acc[NT][4];
+#pragma unroll
+                    for (int k = 0; k < PER; ++k)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int blk = q * PER + k;
+                            const uint32_t w0 = kw[0][2 * blk + i], w1 = kw[1][2 * blk + i], v0 = w0 >> 8, v1 = w1 >> 8;
+                            const uint32_t lo = 0x000f000fu, hi = 0x00f000f0u;
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                const uint32_t *f = qf[nt][blk][i];
+                                if (k == 0 && i == 0)
+                                    mma16816_zero<false>(acc[nt], w0 & lo, w1 & lo, v0 & lo, v1 & lo, f[0], f[1]);
+                                else
+                                    mma16816<false>(acc[nt], w0 & lo, w1 & lo, v0 & lo, v1 & lo, f[0], f[1]);
+                                mma16816<false>(acc[nt], w0 & hi, w1 & hi, v0 & hi, v1 & hi, f[2], f[3]);
+                            }
+                        }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float y = fmaf(acc[nt][e] * ks[e >> 1][q], fac[nt][e & 1], ka[e >> 1][q] * qs[nt][e & 1][q]);
+                            x[u][nt][e] = q == 0 ? y : x[u][nt][e] + y;
+                        }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        x[u][nt][e] = (bits >> (2 * u + (e >> 1))) & 1u ? x[u][nt][e] : -INFINITY;
+            }
+
+            // Does a maximum or the reference of the value steps have to move?
+            bool moves = false;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        moves |= x[u][nt][e] - KV4_LAZY > m[nt][e & 1];
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int q = 0; q < G; ++q)
+                        moves |= vs[u][r][q] > ref;
+            }
+            if (__any_sync(0xffffffffu, moves)) {
+                float step_top = ref;
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+#pragma unroll
+                        for (int q = 0; q < G; ++q)
+                            step_top = fmaxf(step_top, vs[u][r][q]);
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1)
+                    step_top = fmaxf(step_top, __shfl_xor_sync(0xffffffffu, step_top, d));
+                float turn = 1.f;
+                if (step_top > ref) {
+                    // The next power of two (2^-100 at least, whose inverse fp32 holds with room).
+                    const float to = fmaxf(__uint_as_float(((__float_as_uint(step_top) >> 23) + 1) << 23), 7.888609052e-31f);
+                    turn = ref / to;
+                    ref = to;
+                    up = KV4_UP / to;
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float top = fmaxf(fmaxf(x[0][nt][e], x[0][nt][2 + e]), fmaxf(x[1][nt][e], x[1][nt][2 + e]));
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1)
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                        const float to = fmaxf(m[nt][e], top), f = ex2(m[nt][e] - to), fo = f * turn;
+                        m[nt][e] = to;
+                        l[nt][e] *= f;
+#pragma unroll
+                        for (int q = 0; q < G; ++q)
+                            base[nt][e][q] *= f;
+#pragma unroll
+                        for (int n = 0; n < TILES; ++n) {
+                            o[nt][n][e] *= fo;
+                            o[nt][n][2 + e] *= fo;
+                        }
+                    }
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float pe = ex2(x[u][nt][e] - m[nt][e & 1]);
+                        x[u][nt][e] = pe;
+                        l[nt][e & 1] += pe;
+#pragma unroll
+                        for (int q = 0; q < G; ++q)
+                            base[nt][e & 1][q] = fmaf(pe, va[u][e >> 1][q], base[nt][e & 1][q]);
+                    }
+
+            // The value product, group by group.
+            uint32_t vw[2][4][BLOCKS]; // words of positions t, t + 4, t + 8, t + 12 of a sub-step
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int row = t + 4 * e;
+                    const uint32_t a = st + u * M::SUB + M::KEYS + row * M::ROW;
+                    if (D == 64)
+                        lds_words<1>(a + g * 4, vw[u][e]);
+                    else if (D == 128)
+                        lds_words<2>(a + value_chunk<D>(row, g >> 1) * 16 + (g & 1) * 8, vw[u][e]);
+                    else
+                        lds_words<4>(a + value_chunk<D>(row, g) * 16, vw[u][e]);
+                }
+#pragma unroll
+            for (int q = 0; q < G; ++q) {
+                uint32_t hi[2][NT][2], lo[2][NT][2];
+                float start[NT][4]; // -8 sum p s, as the codes' rows are scaled
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const float f = vs[u][r][q] * up;
+                            const float a = x[u][nt][2 * r] * f, bb = x[u][nt][2 * r + 1] * f;
+                            const uint32_t h = pack2<false>(a, bb);
+                            const float2 back = unpack2<false>(h);
+                            hi[u][nt][r] = transpose8x8(h);
+                            lo[u][nt][r] = transpose8x8(pack2<false>(a - back.x, bb - back.y));
+                        }
+                        constexpr uint32_t E = 0x80088008u, S = 0x80808080u; // -8 2^-24 and -8 2^-20, twice
+                        if (u == 0)
+                            mma16816_zero<false>(start[nt], E, S, E, S, hi[u][nt][0], hi[u][nt][1]);
+                        else
+                            mma16816<false>(start[nt], E, S, E, S, hi[u][nt][0], hi[u][nt][1]);
+                        mma16816<false>(start[nt], E, S, E, S, lo[u][nt][0], lo[u][nt][1]);
+                    }
+#pragma unroll
+                for (int k = 0; k < PER; ++k) {
+                    const int blk = q * PER + k;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t w01[2], w23[2]; // codes 4 half .. 4 half + 3 of two positions each
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            w01[u] = __byte_perm(vw[u][0][blk], vw[u][1][blk], half ? 0x7632 : 0x5410);
+                            w23[u] = __byte_perm(vw[u][2][blk], vw[u][3][blk], half ? 0x7632 : 0x5410);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t ml = 0x000f000fu, mh = 0x00f000f0u;
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                float d[4] = {start[nt][0], start[nt][1], start[nt][2], start[nt][3]};
+#pragma unroll
+                                for (int u = 0; u < 2; ++u) {
+                                    const uint32_t a = w01[u] >> (8 * j), e = w23[u] >> (8 * j);
+                                    mma16816<false>(d, a & ml, a & mh, e & ml, e & mh, hi[u][nt][0], hi[u][nt][1]);
+                                    mma16816<false>(d, a & ml, a & mh, e & ml, e & mh, lo[u][nt][0], lo[u][nt][1]);
+                                }
+                                float(&acc)[4] = o[nt][4 * blk + 2 * half + j];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    acc[i] += d[i];
+                            }
+                        }
+                    }
+                }
+            }
+            stage = stage + 1 == M::STAGES ? 0 : stage + 1;
+        }
+        cp_async_wait<0>();
+
+        // --- the warps' results meet in shared memory (the ring is free) -----------------------
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) {
+                    l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], d);
+#pragma unroll
+                    for (int q = 0; q < G; ++q)
+                        base[nt][e][q] += __shfl_xor_sync(0xffffffffu, base[nt][e][q], d);
+                }
+        __syncthreads();
+        float *acc = reinterpret_cast<float *>(smem); // [warp][head][D]
+        const float f_even = ref * (16777216.f / KV4_UP), f_odd = ref * (1048576.f / KV4_UP);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float *mine = acc + (warp * M::HEADS + nt * 8 + 2 * t + e) * D + 8 * g;
+#pragma unroll
+                for (int n = 0; n < TILES; n += 2) { // values 2 n % 8 .. + 3 of block n / 4
+                    const float a = base[nt][e][n / 4 / PER];
+                    const float4 v = make_float4(fmaf(o[nt][n][e], f_even, a), fmaf(o[nt][n][2 + e], f_odd, a),
+                                                 fmaf(o[nt][n + 1][e], f_even, a), fmaf(o[nt][n + 1][2 + e], f_odd, a));
+                    *reinterpret_cast<float4 *>(mine + 64 * (n / 4) + 2 * (n % 4)) = v;
+                }
+                if (g == 0) {
+                    stat[warp][nt * 8 + 2 * t + e][0] = m[nt][e];
+                    stat[warp][nt * 8 + 2 * t + e][1] = l[nt][e];
+                }
+            }
+        __syncthreads();
+        uint16_t *out = p.out + (long long)b * p.ldo + (long long)(c * p.group + h0) * D;
+        float *lse = p.lse ? p.lse + (long long)b * p.heads + c * p.group + h0 : nullptr;
+        split.template finish<D, M::HEADS, BF>(seg, acc, &stat[0][0][0], nh, out, lse);
+    }
+}
+
+namespace {
+
+using Kv4Kernel = void (*)(Kv4AttParams);
+
+template <int D, int G, int NT>
+cudaError_t kv4_kernel(bool bf, Kv4Kernel &kernel, int &smem)
+{
+    static const Kv4Kernel kernels[2] = {kv4_attention_kernel<D, G, NT, false>, kv4_attention_kernel<D, G, NT, true>};
+    kernel = kernels[bf];
+    smem = Kv4Geom<D, G, NT>::SMEM;
+    return allow_smem<Kv4Geom<D, G, NT>, 2>(reinterpret_cast<const void *>(kernel), bf, smem);
+}
+
+constexpr int KV4_MAX_CTAS = 3;
+
+// Query heads of a tile, and blocks per SM.
+int kv4_heads(int head_dim, int group)
+{
+    return head_dim < 256 && group > 8 ? 16 : 8;
+}
+
+int kv4_ctas(int head_dim, int heads)
+{
+    return head_dim == 256 || head_dim * heads > 1024 ? 2 : 3;
+}
+static_assert(Kv4Geom<64, 1, 1>::CTAS == 3 && Kv4Geom<64, 1, 2>::CTAS == 3 && Kv4Geom<128, 1, 1>::CTAS == 3 &&
+                  Kv4Geom<128, 1, 2>::CTAS == 2 && Kv4Geom<256, 1, 1>::CTAS == 2,
+              "kv4_ctas");
+
+SplitLayout kv4_layout(int head_dim, int heads, int num_sms)
+{
+    return split_layout((long long)num_sms * KV4_MAX_CTAS, (long long)num_sms * kv4_ctas(head_dim, heads),
+                        heads * (head_dim + 2));
+}
+
+int kv4_check_sizes(int batch, int n_heads, int n_kv_heads, int head_dim)
+{
+    if (batch < 0 || n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || n_heads % n_kv_heads != 0)
+        return status_of(STAGE_ARG, W4A16_ARG_SHAPE);
+    if (!kv4_dim(head_dim) || batch > SPLIT_MAX_BATCH)
+        return status_of(STAGE_UNSUPPORTED, W4A16_ARG_SHAPE);
+    if ((long long)n_heads * head_dim > 0x3FFFFFFFLL || (long long)batch * n_heads > 0x7FFFFFFFLL)
+        return status_of(STAGE_ARG, W4A16_ARG_OVERFLOW);
+    return 0;
+}
+
+} // namespace
+} // namespace ops
+} // namespace w4
+
+using namespace w4;
+using namespace w4::ops;
+
+extern "C" size_t w4a16_kv4_attention_workspace_size(int batch, int n_heads, int n_kv_heads, int head_dim, int num_sms)
+{
+    if (kv4_check_sizes(batch, n_heads, n_kv_heads, head_dim) != 0)
+        return 0;
+    if (num_sms <= 0 && sm_count(&num_sms) != cudaSuccess)
+        return 0;
+    return (size_t)kv4_layout(head_dim, kv4_heads(head_dim, n_heads / n_kv_heads), num_sms).total;
+}
+
+extern "C" int w4a16_kv4_attention(const void *q, int ldq, const void *cache, long long page_stride, void *out, int ldo,
+                                   float *lse, const int32_t *block_table, int ld_table, const int32_t *seq_lens,
+                                   void *workspace, size_t workspace_bytes, int batch, int n_heads, int n_kv_heads,
+                                   int head_dim, int page_size, int n_pages, int max_pages, int group_size, int window,
+                                   float scale, unsigned flags, cudaStream_t stream)
+{
+    if (flags & ~W4A16_FLAG_BF16)
+        return status_of(STAGE_ARG, W4A16_ARG_FLAGS);
+    int st = kv4_check_sizes(batch, n_heads, n_kv_heads, head_dim);
+    if (st)
+        return st;
+    if (page_size <= 0 || n_pages <= 0 || max_pages <= 0 || window < 0)
+        return status_of(STAGE_ARG, W4A16_ARG_SHAPE);
+    if (page_size > W4A16_KV4_MAX_PAGE)
+        return status_of(STAGE_UNSUPPORTED, W4A16_ARG_SHAPE);
+    const int groups = kv4_groups(head_dim, group_size);
+    if (groups == 0)
+        return status_of(STAGE_ARG, W4A16_ARG_GROUP);
+    if (batch == 0)
+        return 0;
+    if (!q || !cache || !out || !block_table || !seq_lens || !workspace)
+        return status_of(STAGE_ARG, W4A16_ARG_NULL);
+    Kv4AttParams p;
+    p.rec = kv4_record(page_size, head_dim, groups);
+    if (ldq < n_heads * head_dim || ldo < n_heads * head_dim || ld_table < max_pages ||
+        page_stride < n_kv_heads * p.rec.bytes)
+        return status_of(STAGE_ARG, W4A16_ARG_SHAPE);
+    if (ldq % 8 != 0 || ldo % 8 != 0 || page_stride % 16 != 0 || !aligned(q, 16) || !aligned(cache, 16) ||
+        !aligned(out, 16) || !aligned(lse, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
+        !aligned(workspace, 256))
+        return status_of(STAGE_ARG, W4A16_ARG_ALIGN);
+    // Positions and units are counted in 32 bits (offsets into the cache in 64): a sequence holds
+    // at most max_pages pages.
+    const long long max_len = (long long)max_pages * page_size;
+    if (max_len > 0x7FFFFFFFLL - 64 * KV4_UNIT ||
+        ((max_len + KV4_UNIT - 1) / KV4_UNIT + 8) * batch > 0x7FFFFFFFLL)
+        return status_of(STAGE_ARG, W4A16_ARG_OVERFLOW);
+
+    int num_sms = 0;
+    cudaError_t err = sm_count(&num_sms);
+    if (err != cudaSuccess)
+        return status_of(STAGE_RESOURCE, err);
+    const int group = n_heads / n_kv_heads, heads = kv4_heads(head_dim, group);
+    const SplitLayout lay = kv4_layout(head_dim, heads, num_sms);
+    if (workspace_bytes < (size_t)lay.total)
+        return status_of(STAGE_ARG, W4A16_ARG_WORKSPACE);
+    p.q = static_cast<const uint16_t *>(q);
+    p.cache = static_cast<const uint8_t *>(cache);
+    p.out = static_cast<uint16_t *>(out);
+    p.lse = lse;
+    p.table = block_table;
+    p.page_stride = page_stride;
+    p.ldq = ldq;
+    p.ldo = ldo;
+    p.ld_table = ld_table;
+    p.heads = n_heads;
+    p.group = group;
+    p.tiles = (group + heads - 1) / heads;
+    p.page = page_size;
+    p.n_pages = n_pages;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    split_params(p.split, lay, workspace, seq_lens, batch, n_kv_heads * p.tiles, (int)max_len, window);
+    // n / page for n < 2^31: with 2^(s - 1) < page <= 2^s, floor(n ceil(2^(31 + s) / page) / 2^(31 + s)).
+    int s = 0;
+    while ((1 << s) < page_size)
+        ++s;
+    p.page_magic = page_size == 1 ? 0 : (uint32_t)(((1ULL << (31 + s)) + page_size - 1) / page_size);
+    p.page_shift = page_size == 1 ? 0 : s - 1;
+
+    const bool bf = (flags & W4A16_FLAG_BF16) != 0;
+    Kv4Kernel kernel;
+    int smem;
+    if (head_dim == 64)
+        err = heads == 8 ? kv4_kernel<64, 1, 1>(bf, kernel, smem) : kv4_kernel<64, 1, 2>(bf, kernel, smem);
+    else if (head_dim == 128 && heads == 8)
+        err = groups == 1 ? kv4_kernel<128, 1, 1>(bf, kernel, smem) : kv4_kernel<128, 2, 1>(bf, kernel, smem);
+    else if (head_dim == 128)
+        err = groups == 1 ? kv4_kernel<128, 1, 2>(bf, kernel, smem) : kv4_kernel<128, 2, 2>(bf, kernel, smem);
+    else
+        err = groups == 1   ? kv4_kernel<256, 1, 1>(bf, kernel, smem)
+              : groups == 2 ? kv4_kernel<256, 2, 1>(bf, kernel, smem)
+                            : kv4_kernel<256, 4, 1>(bf, kernel, smem);
+    if (err != cudaSuccess)
+        return status_of(STAGE_RESOURCE, err);
+    const int grid = num_sms * kv4_ctas(head_dim, heads);
+    return launch_status(launch_pdl(kernel, dim3(grid), dim3(SPLIT_THREADS), (size_t)smem, stream, p));
+}

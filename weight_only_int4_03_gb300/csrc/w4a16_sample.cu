@@ -1,0 +1,610 @@
+// w4a16_sample.cu -- the next token of each row of logits by temperature, top-k, top-p and min-p.
+//
+// With P_i = e^((l_i - max l) / T), tokens ordered by (logit falling, index rising):
+//     top-k keeps the first k; top-p, of these, the shortest beginning whose sum reaches top_p times their sum;
+//     min-p, of these, those with P_i >= min_p;
+//     token = the first index i at which the sum of the kept P_j, j <= i, exceeds u times the sum of all kept.
+// The kept tokens are those above a threshold logit and, of those at it, the first r by index.
+//
+// Where sums decide (which token's share holds u, where top-p ends), rounding would show: P is therefore a 64-bit
+// integer, a multiple of 2^-43 good to 2^-30 of itself, and all sums are exact, in whatever order they are
+// taken.  So results do not depend on the split, and atomics do no harm.  P comes from a table of 2^(-j/64) and a
+// polynomial for the rest (the table-driven exponential of Tang, 1989); (l - max) / T is kept in two fp32 parts.
+//
+// A cluster of up to eight blocks holds a row: the logits are read from memory once, as 16-bit keys in
+// their order, and stay in shared memory.  The threshold is found by the keys' high bytes and then the low bytes of
+// one of them (256-bin histograms of counts and sums); blocks read one another's bins.  Last, each warp sums
+// its own range of indices, and the warp whose range holds u walks it.  What bounds it: for few rows the chain of
+// cluster barriers, for many the instructions per logit (P twice, histogram atomics).
+#include <cooperative_groups.h>
+
+#include "w4a16_ops.cuh"
+
+namespace w4 {
+namespace ops {
+
+namespace cg = cooperative_groups;
+
+constexpr int SAMPLE_THREADS = 512;
+constexpr int SAMPLE_WARPS = SAMPLE_THREADS / 32;
+constexpr int SAMPLE_CLUSTER = 8;      // blocks of a row, at most
+constexpr int SAMPLE_SLICE = 65536;    // logits of a block, at most (a bin's sums of 32-bit parts rely on it)
+constexpr int SAMPLE_BITS = 43;        // P = 1 is 2^43: 2^19 tokens sum below 2^62
+constexpr int SAMPLE_COPIES = 4;       // of a histogram, against lanes that meet at a bin
+
+// 2^31 2^(-j/64).
+__constant__ uint32_t SAMPLE_EXP[64] = {
+    2147483648u, 2124350982u, 2101467502u, 2078830522u, 2056437387u, 2034285470u, 2012372174u, 1990694927u,
+    1969251188u, 1948038440u, 1927054196u, 1906295993u, 1885761398u, 1865448001u, 1845353420u, 1825475297u,
+    1805811301u, 1786359126u, 1767116489u, 1748081133u, 1729250827u, 1710623359u, 1692196547u, 1673968228u,
+    1655936265u, 1638098541u, 1620452965u, 1602997467u, 1585730000u, 1568648537u, 1551751076u, 1535035634u,
+    1518500250u, 1502142985u, 1485961921u, 1469955159u, 1454120821u, 1438457051u, 1422962010u, 1407633882u,
+    1392470869u, 1377471191u, 1362633090u, 1347954824u, 1333434672u, 1319070932u, 1304861917u, 1290805962u,
+    1276901417u, 1263146652u, 1249540052u, 1236080024u, 1222764986u, 1209593378u, 1196563654u, 1183674286u,
+    1170923762u, 1158310587u, 1145833280u, 1133490379u, 1121280436u, 1109202018u, 1097253708u, 1085434106u,
+};
+
+struct SampleParams {
+    const uint16_t *logits;
+    const float *uniform, *temperature, *top_p, *min_p;
+    const int32_t *top_k;
+    int32_t *tokens, *status;
+    float *logprobs;
+    long long ld;
+    int vocab, slice;
+    int wide; // rows can be read 16 bytes at a time
+};
+
+struct SampleShared {
+    uint32_t exp[64];
+    uint32_t count[256 * SAMPLE_COPIES], low[256 * SAMPLE_COPIES], high[256 * SAMPLE_COPIES];
+    // This block's bins, read by the cluster's other blocks; two sets in turn, so that a set is written again only
+    // after a barrier which all of its readers have reached.
+    unsigned long long bin_sum[2][256];
+    uint32_t bin_count[2][256];
+    unsigned long long all_sum[256]; // of all blocks: the last histogram that asked for them
+    uint32_t all_count[256];
+    // Written by every block of the cluster.
+    uint32_t top[SAMPLE_CLUSTER];
+    unsigned long long above[SAMPLE_CLUSTER];
+    uint32_t ties[SAMPLE_CLUSTER];
+    // Of this block's warps.
+    uint32_t warp_top[SAMPLE_WARPS];
+    unsigned long long warp_above[SAMPLE_WARPS];
+    uint32_t warp_ties[SAMPLE_WARPS];
+    // A search's result.
+    unsigned long long found_above, found_other, total, total_other;
+    uint32_t found;
+};
+
+// 16-bit numbers as integers in the same order; NaN counts as -inf, -0 as 0.  Two at a time.
+template <bool BF>
+__device__ __forceinline__ uint32_t keys_of(uint32_t w)
+{
+    constexpr uint32_t INF = BF ? 0x7F807F80u : 0x7C007C00u;
+    const uint32_t size = w & 0x7FFF7FFFu;
+    const uint32_t nan = __vcmpgtu2(size, INF), zero = __vcmpeq2(size, 0);
+    w = (w & ~nan) | ((INF | 0x80008000u) & nan);
+    w &= ~zero;
+    const uint32_t negative = ((w >> 15) & 0x00010001u) * 0xFFFFu;
+    return w ^ (negative | 0x80008000u);
+}
+
+template <bool BF>
+__device__ __forceinline__ float number_of(uint32_t key)
+{
+    const uint32_t w = key & 0x8000u ? key ^ 0x8000u : ~key & 0xFFFFu;
+    return to_float<BF>((uint16_t)w);
+}
+
+template <bool BF>
+__device__ __forceinline__ constexpr uint32_t lowest_key() // of -inf
+{
+    return BF ? 0x007Fu : 0x03FFu;
+}
+
+// P of a logit, in units of 2^-43.
+template <bool BF>
+struct Share {
+    float top, c_hi, c_lo; // the largest logit; log2(e) / T in two parts
+    const uint32_t *exp;
+
+    __device__ __forceinline__ unsigned long long operator()(uint32_t key) const
+    {
+        const float l = number_of<BF>(key);
+        if (l == top)
+            return 1ULL << SAMPLE_BITS;
+        const float d = top - l, rest = (top - d) - l; // d + rest is the difference
+        const float y = d * c_hi;
+        if (!(y < (float)SAMPLE_BITS + 1.f))
+            return 0;
+        const float y_lo = fmaf(d, c_hi, -y) + fmaf(d, c_lo, rest * c_hi);
+        const float k = rintf(y * 64.f);
+        const float z = (fmaf(k, -0.015625f, y) + y_lo) * 0.6931471805599453f; // at most ln 2 / 128
+        const float q = z * fmaf(z, fmaf(z, fmaf(z, 1.f / 24.f, -1.f / 6.f), 0.5f), -1.f); // e^-z - 1
+        const int n = (int)k >> 6;
+        const uint32_t t = exp[(int)k & 63];
+        const uint32_t v = t + (uint32_t)__float2int_rn((float)t * q); // 2^31 2^n P
+        return n <= 12 ? (unsigned long long)v << (12 - n) : ((unsigned long long)v + (1ULL << (n - 13))) >> (n - 12);
+    }
+};
+
+// Adds `sum` to a bin's 64-bit sum of two 32-bit halves.
+__device__ __forceinline__ void add_sum(uint32_t *low, uint32_t *high, unsigned long long sum)
+{
+    const uint32_t a = (uint32_t)sum, old = atomicAdd(low, a);
+    const uint32_t carry = (uint32_t)(sum >> 32) + (old + a < a ? 1u : 0u);
+    if (carry)
+        atomicAdd(high, carry);
+}
+
+template <bool BF>
+struct Sampler {
+    SampleShared &s;
+    const uint4 *keys; // the slice, eight keys at a time
+    int vectors;       // of them
+    cg::cluster_group cluster;
+    Share<BF> share;
+
+    int histograms;    // made so far
+
+    // Histogram of the keys that `bin` gives a bin (and P > 0), merged over the cluster into all_count and all_sum.
+    template <class Bin>
+    __device__ __forceinline__ void histogram(bool counts, bool sums, Bin bin)
+    {
+        const int tid = threadIdx.x, copy = tid % SAMPLE_COPIES, set = histograms++ & 1;
+        for (int i = tid; i < 256 * SAMPLE_COPIES; i += SAMPLE_THREADS)
+            s.count[i] = s.low[i] = s.high[i] = 0;
+        __syncthreads();
+        for (int v = tid; v < vectors; v += SAMPLE_THREADS) {
+            const uint4 k4 = keys[v];
+            const uint32_t w[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t key = (w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
+                const int b = bin(key);
+                if (b < 0)
+                    continue;
+                const unsigned long long x = share(key);
+                if (x == 0)
+                    continue;
+                if (counts)
+                    atomicAdd(&s.count[b * SAMPLE_COPIES + copy], 1u);
+                if (sums)
+                    add_sum(&s.low[b * SAMPLE_COPIES + copy], &s.high[b * SAMPLE_COPIES + copy], x);
+            }
+        }
+        __syncthreads();
+        if (tid < 256) {
+            uint32_t n = 0;
+            unsigned long long sum = 0;
+#pragma unroll
+            for (int c = 0; c < SAMPLE_COPIES; ++c) {
+                n += s.count[tid * SAMPLE_COPIES + c];
+                sum += s.low[tid * SAMPLE_COPIES + c] + ((unsigned long long)s.high[tid * SAMPLE_COPIES + c] << 32);
+            }
+            s.bin_count[set][tid] = n;
+            s.bin_sum[set][tid] = sum;
+        }
+        cluster.sync();
+        if (tid < 256) {
+            uint32_t n = 0;
+            unsigned long long sum = 0;
+            for (unsigned r = 0; r < cluster.num_blocks(); ++r) {
+                if (counts)
+                    n += *cluster.map_shared_rank(&s.bin_count[set][tid], r);
+                if (sums)
+                    sum += *cluster.map_shared_rank(&s.bin_sum[set][tid], r);
+            }
+            if (counts)
+                s.all_count[tid] = n;
+            if (sums)
+                s.all_sum[tid] = sum;
+        }
+        __syncthreads();
+    }
+
+    // The highest bin which, with `before` and the bins above it, has at least `want` of a measure (`weigh(bin)`).
+    // Leaves the bin in found (256: there is not as much), what lies above it in found_above (with `before`), and the
+    // sum of `other(bin)` above it in found_other; total and total_other are those of all bins.  Warp 0 searches,
+    // eight bins a lane.
+    template <class Weigh, class Other>
+    __device__ __forceinline__ void search(unsigned long long before, unsigned long long want, Weigh weigh, Other other)
+    {
+        if (threadIdx.x < 32) {
+            const int lane = threadIdx.x;
+            unsigned long long mine[8], sum = 0, sum2 = 0; // lane 0 has the highest eight bins, the highest first
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                mine[i] = weigh(255 - (8 * lane + i));
+                sum += mine[i];
+                sum2 += other(255 - (8 * lane + i));
+            }
+            unsigned long long incl = sum, incl2 = sum2;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const unsigned long long o = __shfl_up_sync(0xffffffffu, incl, d), o2 = __shfl_up_sync(0xffffffffu, incl2, d);
+                if (lane >= d) {
+                    incl += o;
+                    incl2 += o2;
+                }
+            }
+            const uint32_t has = __ballot_sync(0xffffffffu, before + incl >= want);
+            if (has != 0 && lane == __ffs(has) - 1) {
+                unsigned long long above = before + incl - sum, above2 = incl2 - sum2;
+                int i = 0;
+                for (; i < 7 && above + mine[i] < want; ++i) {
+                    above += mine[i];
+                    above2 += other(255 - (8 * lane + i));
+                }
+                s.found = 255 - (8 * lane + i);
+                s.found_above = above;
+                s.found_other = above2;
+            }
+            if (lane == 31) {
+                if (has == 0)
+                    s.found = 256;
+                s.total = incl;
+                s.total_other = incl2;
+            }
+        }
+        __syncthreads();
+    }
+};
+
+template <bool BF>
+__global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleParams p)
+{
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ SampleShared s;
+    uint4 *keys = reinterpret_cast<uint4 *>(smem);
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), blocks = (int)cluster.num_blocks();
+    const int row = blockIdx.x / blocks, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid < 64)
+        s.exp[tid] = SAMPLE_EXP[tid];
+    pdl_wait();
+    pdl_launch_dependents();
+
+    // --- the row's settings ----------------------------------------------------------------------
+    const float temperature = p.temperature ? p.temperature[row] : 1.f;
+    const float top_p = p.top_p ? p.top_p[row] : 1.f, min_p = p.min_p ? p.min_p[row] : 0.f;
+    const float u = p.uniform[row];
+    int top_k = p.top_k ? p.top_k[row] : 0;
+    const bool greedy = temperature == 0.f;
+    if (!(temperature >= 0.f && temperature < INFINITY) || top_p != top_p || min_p != min_p ||
+        (!greedy && !(u >= 0.f && u < 1.f))) { // the whole cluster leaves
+        if (rank == 0 && tid == 0) {
+            p.tokens[row] = -1;
+            if (p.logprobs)
+                p.logprobs[row] = NAN;
+            if (p.status)
+                atomicOr(p.status, W4A16_DEV_SETTING);
+        }
+        return;
+    }
+    if (greedy)
+        top_k = 1;
+    cluster.barrier_arrive(); // waited for before the first look at another block's memory
+
+    // --- the slice, as keys, and the largest ----------------------------------------------------
+    const int begin = rank * p.slice, size = max(0, min(p.slice, p.vocab - begin));
+    const int vectors = (size + 7) / 8;
+    const uint16_t *src = p.logits + row * p.ld + begin;
+    uint32_t best = 0;
+    for (int v = tid; v < vectors; v += SAMPLE_THREADS) {
+        uint4 w;
+        if (p.wide && 8 * v + 8 <= size) {
+            w = *reinterpret_cast<const uint4 *>(src + 8 * v);
+        } else {
+            constexpr uint32_t NONE = BF ? 0xFF80u : 0xFC00u; // -inf
+            uint32_t h[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                h[e] = 8 * v + e < size ? src[8 * v + e] : NONE;
+            w = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+        }
+        w = make_uint4(keys_of<BF>(w.x), keys_of<BF>(w.y), keys_of<BF>(w.z), keys_of<BF>(w.w));
+        keys[v] = w;
+        best = __vmaxu2(best, __vmaxu2(__vmaxu2(w.x, w.y), __vmaxu2(w.z, w.w)));
+    }
+    best = max(best & 0xFFFFu, best >> 16);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        best = max(best, __shfl_xor_sync(0xffffffffu, best, d));
+    if (lane == 0)
+        s.warp_top[warp] = best;
+    __syncthreads();
+    cluster.barrier_wait();
+    if (tid < blocks) {
+        best = 0;
+        for (int w = 0; w < SAMPLE_WARPS; ++w)
+            best = max(best, s.warp_top[w]);
+        *cluster.map_shared_rank(&s.top[rank], tid) = best;
+    }
+    cluster.sync();
+    best = 0;
+    for (int r = 0; r < blocks; ++r)
+        best = max(best, s.top[r]);
+    if (best <= lowest_key<BF>()) { // nothing to choose from
+        if (rank == 0 && tid == 0) {
+            p.tokens[row] = -1;
+            if (p.logprobs)
+                p.logprobs[row] = -INFINITY;
+        }
+        return;
+    }
+
+    Sampler<BF> f{s, keys, vectors, cluster, {}, 0};
+    f.share.top = number_of<BF>(best);
+    const double c = 1.4426950408889634 / (greedy ? 1.0 : (double)temperature);
+    f.share.c_hi = (float)c;
+    f.share.c_lo = (float)(c - (double)f.share.c_hi);
+    f.share.exp = s.exp;
+
+    // --- the threshold: keys above it are kept, and the first `ties` of those at it --------------
+    uint32_t threshold = 0, ties = 0; // no key is 0
+    if (top_k == 1) {
+        threshold = best;
+        ties = 1;
+    } else if (top_k > 0 || top_p < 1.f) {
+        const bool by_sum = top_p < 1.f;
+        const auto counts = [&s = s](int b) { return (unsigned long long)s.all_count[b]; };
+        const auto sums = [&s = s](int b) { return s.all_sum[b]; };
+        f.histogram(top_k > 0, by_sum, [](uint32_t key) { return (int)(key >> 8); });
+        int bin = -1;                     // high byte of the keys that the counts at hand are of
+        unsigned long long above_bin = 0; // sum of the keys above them
+        unsigned long long total = 0;     // sum of what top-k keeps
+        if (top_k > 0) {
+            if (by_sum)
+                f.search(0, (unsigned long long)top_k, counts, sums);
+            else
+                f.search(0, (unsigned long long)top_k, counts, [](int) { return 0ULL; });
+            total = s.total_other;
+            if (s.found < 256) {
+                bin = (int)s.found;
+                above_bin = s.found_other;
+                const unsigned long long count_above = s.found_above;
+                f.histogram(true, false, [bin](uint32_t key) { return (int)(key >> 8) == bin ? (int)(key & 255) : -1; });
+                f.search(count_above, (unsigned long long)top_k, counts, [](int) { return 0ULL; });
+                threshold = (uint32_t)bin << 8 | s.found;
+                ties = (uint32_t)(top_k - s.found_above);
+            }
+        }
+        if (by_sum) {
+            const uint32_t last = threshold, last_ties = ties; // what top-k keeps ends here
+            // Sum of the kept keys of high byte `at` with low byte b, by the counts at hand.
+            int at = bin;
+            const auto kept = [&](int b) {
+                const uint32_t key = (uint32_t)at << 8 | (uint32_t)b;
+                const uint32_t n = key > last ? s.all_count[b] : key == last ? last_ties : 0u;
+                return n ? n * f.share(key) : 0ULL;
+            };
+            if (bin >= 0) {
+                __syncthreads(); // found is read before the search that writes it again
+                f.search(0, ~0ULL, kept, [](int) { return 0ULL; });
+                total = above_bin + s.total;
+            } else if (top_k <= 0) {
+                f.search(0, ~0ULL, sums, [](int) { return 0ULL; });
+                total = s.total;
+            }
+            const unsigned long long want =
+                max(1ULL, (unsigned long long)ceil(fmax((double)top_p, 0.0) * (double)total));
+            unsigned long long above = above_bin;
+            __syncthreads();
+            if (bin < 0 || above_bin >= want) { // it ends above the counts at hand
+                f.search(0, want, [&](int b) { return b > bin ? s.all_sum[b] : 0ULL; }, [](int) { return 0ULL; });
+                at = (int)s.found;
+                above = s.found_above;
+                const int byte = at;
+                f.histogram(true, false, [byte](uint32_t key) { return (int)(key >> 8) == byte ? (int)(key & 255) : -1; });
+            }
+            f.search(above, want, kept, [](int) { return 0ULL; });
+            threshold = (uint32_t)at << 8 | s.found;
+            const unsigned long long x = f.share(threshold);
+            const uint32_t n = (uint32_t)((want - s.found_above + x - 1) / x); // those whose sum before is below want
+            ties = min(n, threshold == last ? last_ties : s.all_count[s.found]);
+        }
+    }
+
+    // --- sums of the kept, by warp and block, in the order of the indices -----------------------
+    const unsigned long long least = (unsigned long long)ceil(fmin(fmax((double)min_p, 0.0), 1.0) * (double)(1ULL << SAMPLE_BITS));
+    const unsigned long long tie_share = threshold ? f.share(threshold) : 0;
+    const bool ties_count = tie_share >= least && tie_share > 0;
+    // A warp's range: whole steps of 32 vectors.
+    const int steps = (vectors + 31) / 32, per_warp = (steps + SAMPLE_WARPS - 1) / SAMPLE_WARPS;
+    const int from = warp * per_warp, to = min(steps, from + per_warp);
+    auto value = [&](uint32_t key) {
+        if (key <= threshold)
+            return 0ULL;
+        const unsigned long long x = f.share(key);
+        return x >= least ? x : 0ULL;
+    };
+    unsigned long long above = 0;
+    uint32_t at_it = 0;
+    for (int st = from; st < to; ++st) {
+        const int v = st * 32 + lane;
+        if (v < vectors) {
+            const uint4 k4 = keys[v];
+            const uint32_t w[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t key = (w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
+                above += value(key);
+                at_it += key == threshold;
+            }
+        }
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        above += __shfl_xor_sync(0xffffffffu, above, d);
+        at_it += __shfl_xor_sync(0xffffffffu, at_it, d);
+    }
+    if (lane == 0) {
+        s.warp_above[warp] = above;
+        s.warp_ties[warp] = at_it;
+    }
+    __syncthreads();
+    if (tid < blocks) {
+        unsigned long long a = 0;
+        uint32_t n = 0;
+        for (int w = 0; w < SAMPLE_WARPS; ++w) {
+            a += s.warp_above[w];
+            n += s.warp_ties[w];
+        }
+        *cluster.map_shared_rank(&s.above[rank], tid) = a;
+        *cluster.map_shared_rank(&s.ties[rank], tid) = n;
+    }
+    cluster.sync(); // the last: from here no block looks at another's memory
+
+    // --- the range that holds u, walked by its warp ----------------------------------------------
+    auto kept_ties = [&](uint32_t before, uint32_t n) { // of n ties after `before` others
+        return ties_count ? min(n, ties > before ? ties - before : 0u) : 0u;
+    };
+    unsigned long long all = 0, sum = 0; // of all kept; of those before this warp's range
+    uint32_t seen = 0, ties_before = 0;
+    for (int r = 0; r < blocks; ++r) {
+        const unsigned long long x = s.above[r] + kept_ties(seen, s.ties[r]) * tie_share;
+        if (r < rank)
+            sum += x;
+        if (r == rank)
+            ties_before = seen;
+        all += x;
+        seen += s.ties[r];
+    }
+    for (int w = 0; w < warp; ++w) {
+        sum += s.warp_above[w] + kept_ties(ties_before, s.warp_ties[w]) * tie_share;
+        ties_before += s.warp_ties[w];
+    }
+    const unsigned long long want = greedy ? 0 : (unsigned long long)((double)u * (double)all);
+    const unsigned long long mine = s.warp_above[warp] + kept_ties(ties_before, s.warp_ties[warp]) * tie_share;
+    if (!(sum <= want && want < sum + mine))
+        return;
+    for (int st = from; st < to; ++st) {
+        const int v = st * 32 + lane;
+        uint32_t key[8];
+        uint32_t n = 0;
+        unsigned long long x = 0;
+        const uint4 k4 = v < vectors ? keys[v] : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            key[e] = (w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
+            x += value(key[e]);
+            n += key[e] == threshold && v < vectors;
+        }
+        uint32_t n_incl = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t o = __shfl_up_sync(0xffffffffu, n_incl, d);
+            if (lane >= d)
+                n_incl += o;
+        }
+        uint32_t before = ties_before + n_incl - n;
+        x += kept_ties(before, n) * tie_share;
+        unsigned long long incl = x;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const unsigned long long o = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d)
+                incl += o;
+        }
+        const uint32_t has = __ballot_sync(0xffffffffu, sum + incl > want);
+        if (has) {
+            if (lane == __ffs(has) - 1) {
+                unsigned long long at = sum + incl - x;
+                bool done = false;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (!done) {
+                        unsigned long long y = value(key[e]);
+                        if (key[e] == threshold) {
+                            y = kept_ties(before, 1) * tie_share;
+                            ++before;
+                        }
+                        at += y;
+                        if (at > want) {
+                            done = true;
+                            p.tokens[row] = begin + 8 * v + e;
+                            if (p.logprobs)
+                                p.logprobs[row] = y == all ? 0.f : (float)log((double)y / (double)all);
+                        }
+                    }
+            }
+            return;
+        }
+        sum += __shfl_sync(0xffffffffu, incl, 31);
+        ties_before += __shfl_sync(0xffffffffu, n_incl, 31);
+    }
+}
+
+namespace {
+
+struct SampleFamily {};
+
+} // namespace
+} // namespace ops
+} // namespace w4
+
+using namespace w4;
+using namespace w4::ops;
+
+extern "C" int w4a16_sample(const void *logits, int ld, const float *uniform, const float *temperature,
+                            const int32_t *top_k, const float *top_p, const float *min_p, int32_t *tokens,
+                            float *logprobs, int32_t *status, int batch, int vocab, unsigned flags, cudaStream_t stream)
+{
+    if (flags & ~W4A16_FLAG_BF16)
+        return status_of(STAGE_ARG, W4A16_ARG_FLAGS);
+    if (batch < 0 || vocab <= 0 || ld < vocab)
+        return status_of(STAGE_ARG, W4A16_ARG_SHAPE);
+    if (vocab > SAMPLE_CLUSTER * SAMPLE_SLICE || batch > (1 << 24))
+        return status_of(STAGE_UNSUPPORTED, W4A16_ARG_SHAPE);
+    if (batch == 0)
+        return 0;
+    if (!logits || !uniform || !tokens)
+        return status_of(STAGE_ARG, W4A16_ARG_NULL);
+    if (!aligned(logits, 2) || !aligned(uniform, 4) || !aligned(temperature, 4) || !aligned(top_k, 4) ||
+        !aligned(top_p, 4) || !aligned(min_p, 4) || !aligned(tokens, 4) || !aligned(logprobs, 4) || !aligned(status, 4))
+        return status_of(STAGE_ARG, W4A16_ARG_ALIGN);
+    int num_sms = 0;
+    cudaError_t err = sm_count(&num_sms);
+    if (err != cudaSuccess)
+        return status_of(STAGE_RESOURCE, err);
+    // Blocks of a row: slices of 32768 logits at most where eight suffice, smaller ones while all fit on the GPU at once.
+    int blocks = 1;
+    while (blocks < SAMPLE_CLUSTER && (vocab > blocks * 32768 || (batch * 2LL * blocks <= 2LL * num_sms && vocab > blocks * 2048)))
+        blocks *= 2;
+    SampleParams p;
+    p.logits = static_cast<const uint16_t *>(logits);
+    p.uniform = uniform;
+    p.temperature = temperature;
+    p.top_p = top_p;
+    p.min_p = min_p;
+    p.top_k = top_k;
+    p.tokens = tokens;
+    p.status = status;
+    p.logprobs = logprobs;
+    p.ld = ld;
+    p.vocab = vocab;
+    p.slice = (int)round_up((vocab + blocks - 1) / blocks, 8);
+    p.wide = ld % 8 == 0 && aligned(logits, 16);
+    const bool bf = (flags & W4A16_FLAG_BF16) != 0;
+    const auto kernel = bf ? sample_kernel<true> : sample_kernel<false>;
+    err = allow_smem<SampleFamily, 2>(reinterpret_cast<const void *>(kernel), bf, 2 * SAMPLE_SLICE);
+    if (err != cudaSuccess)
+        return status_of(STAGE_RESOURCE, err);
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3((unsigned)(batch * blocks));
+    lc.blockDim = dim3(SAMPLE_THREADS);
+    lc.dynamicSmemBytes = (size_t)p.slice * 2;
+    lc.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = blocks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 2;
+    return launch_status(cudaLaunchKernelEx(&lc, kernel, p));
+}
