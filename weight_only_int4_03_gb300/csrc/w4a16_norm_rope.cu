@@ -9,21 +9,27 @@
 //     b = r(min),  s = r((max - min) / 15),  code = (x - b) / s to the nearest integer, ties to even, in 0..15
 // (r: to the cache's 16-bit type), which stands for code s + b.
 //
-// Bound by memory: each value is read once and written once.  A thread holds 16 values of a head
-// (eight pairs) of NORM_HEADS heads of one kind (q, k or v), so that the weights stay in registers and a
-// position's cosines and sines serve all of them; the D / 16 threads of a head lie in one warp and
-// meet in shuffles for the sum of squares and for the groups' smallest and largest values.  Threads walk over
-// tokens with the next token's values on their way.
+// Bound by memory: each value is read once and written once.  A head belongs to D / 16 neighbouring threads of 16
+// values (eight pairs) each, which meet in shuffles for the sum of squares and for the groups' smallest and largest
+// values; a warp works on 32 / that many heads of one kind, with the next ones' values on their way, and a block on a
+// token.  Arithmetic goes two values to an instruction, as instructions are what the 4-bit kernel is bound by.
+// 6007 tokens of 32 / 8 heads of 128, bf16, 16-bit cache: 29.6 us, 5.1 TB/s of reads and writes; 8191 tokens with three
+// axes into 4 bits (groups of 64, with k_out and v_out): 52 us, 4.1 TB/s; one token 3.2 us of latencies.
+//
+// Codes are those of exact arithmetic: a value next to the border of two codes, or a base or step next to the border of
+// two 16-bit numbers, would fall on either side in fp32 (measured: two keys in 10^6).  So keys that are to be coded are
+// computed in two fp32 parts throughout, from the sum of squares to the remainder of the division (one key in 10^7).
+#include <type_traits>
+
 #include "w4a16_kv4.cuh"
 
 namespace w4 {
 namespace ops {
 
 constexpr int NORM_MAX_AXES = 4;
-constexpr int NORM_HEADS = 2;
-constexpr int NORM_THREADS = 128; // threads a block is filled up to
-constexpr int NORM_PER_SM = 512;  // threads per SM that a launch asks for and the registers allow
-constexpr int NORM_WARPS = 4;     // any-size kernel: warps of a block
+constexpr int NORM_WARPS = 4;   // of a block of the any-size kernel
+constexpr int NORM_MOST = 512;  // threads of a block where tokens are few
+constexpr int NORM_PER_SM = 16; // warps that an SM holds
 
 struct NormParams {
     const uint16_t *q, *k, *v;
@@ -38,11 +44,11 @@ struct NormParams {
     long long page_stride, token_stride, head_stride; // elements; 4 bits: bytes, unused, bytes of a record
     long long total_slots;
     Kv4Record rec;
-    float eps;
+    float eps, per_dim; // per_dim: 1 / dim
     int ldq, ldk, ldv, ldqo, ldko, ldvo, ld_pos;
     int tokens, heads, kv, dim, rot, axes, max_pos, page;
     int cut[NORM_MAX_AXES]; // pair i belongs to the first axis a with i < cut[a]
-    int adjacent;
+    int adjacent, cuts; // cuts: some section ends inside eight pairs
 };
 
 enum { KIND_Q = 0, KIND_K = 1, KIND_V = 2 };
@@ -119,308 +125,595 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return r;
 }
 
-// How a group of values is coded: the step and base as stored, and what coding needs of them.
-struct Step {
-    uint32_t stored;   // step, base (16 bits each)
-    float s, b;        // as numbers; both NaN where the group has no finite range
-    float from, inv, half;
+// Pairs of fp32 numbers: one instruction for two, each rounded by itself and never joined with another.
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 add(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 mul(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 sub(float2 a, float2 b) { return __ffma2_rn(b, both(-1.f), a); }
+
+// A value in two parts, hi + lo, the second below half a unit of the first (or a few of them).
+struct Two {
+    float hi, lo;
 };
 
+// a + b exactly.
+__device__ __forceinline__ Two two_sum(float a, float b)
+{
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+
+__device__ __forceinline__ void two_sum(float2 a, float2 b, float2 &s, float2 &off)
+{
+    s = add(a, b);
+    const float2 t = sub(s, a);
+    off = add(sub(a, sub(s, t)), sub(b, t));
+}
+
+// x / 15, correctly rounded (for results that are not subnormal).
+__device__ __forceinline__ float fifteenth(float x)
+{
+    const float q = x * (1.f / 15.f);
+    return fmaf(fmaf(-q, 15.f, x), 1.f / 15.f, q);
+}
+
+// How a group of values is coded: the step and base as stored, and what coding needs of them.
+struct Step {
+    uint32_t stored;       // step, base (16 bits each)
+    float s, b;            // as numbers; both NaN where the group has no finite range
+    float size, from, inv; // for coding: step and base, 0 where there are none, and 1 / step (to a unit) or 0
+};
+
+// lo: the smallest value, step: (largest - smallest) / 15.
 template <bool BF>
-__device__ __forceinline__ Step step_of(float lo, float hi)
+__device__ __forceinline__ Step step_of(float lo, float step)
 {
     Step st;
-    uint16_t sb = from_float<BF>((hi - lo) / 15.f), bb = from_float<BF>(lo);
+    uint32_t sb = from_float<BF>(step), bb = from_float<BF>(lo);
     if (BF && (sb & 0x7F80) == 0)
         sb = 0; // a subnormal bf16 step has no inverse in fp32
-    st.s = to_float<BF>(sb);
-    st.b = to_float<BF>(bb);
+    st.s = to_float<BF>((uint16_t)sb);
+    st.b = to_float<BF>((uint16_t)bb);
     const bool fine = fabsf(st.s) < INFINITY && fabsf(st.b) < INFINITY; // false for NaN too
+    st.size = fine ? st.s : 0.f;
     st.from = fine ? st.b : 0.f;
-    st.inv = fine && st.s > 0.f ? 1.f / st.s : 0.f;
-    st.half = fine && st.s > 0.f ? 0.5f * st.s : INFINITY;
+    float inv;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(st.size));
+    inv = fmaf(fmaf(-st.size, inv, 1.f), inv, inv);
+    st.inv = st.size > 0.f ? inv : 0.f;
     if (!fine) {
         st.s = st.b = NAN;
         sb = bb = 0x7FFF; // NaN in both types
     }
-    st.stored = (uint32_t)sb | (uint32_t)bb << 16;
+    st.stored = sb | bb << 16;
     return st;
 }
 
-// The code of x: (x - b) / s to the nearest integer, ties to even.  The product with 1 / s is off by a few
-// 2^-24, which decides wrongly only next to the middle between two codes: there the exact rest
-// d - q s says which it is (values of the 16-bit types do lie on the middle).
-__device__ __forceinline__ uint32_t code_of(float x, const Step &st)
+// Adding this rounds a number below 2^22 to the nearest integer, ties to even, into the lowest bits.
+constexpr float ROUND = 12582912.f;
+constexpr uint32_t ROUND_BITS = 0x4B400000u;
+
+// Eight times ROUND_BITS, shifted by 0, 4, .. 28 bits: what a word of codes on ROUND has too much.
+constexpr uint32_t ROUND_WORD = ROUND_BITS * 0x11111111u;
+
+// Two codes (as numbers on ROUND) of values 2 i and 2 i + 1, cut to 0..15 and put into a word, which starts as
+// -ROUND_WORD; the numbers they stand for.  FROM_0: the codes are not negative.
+template <bool FROM_0>
+__device__ __forceinline__ float2 put(float2 t, int i, const Step &st, uint32_t &word)
 {
-    const float d = x - st.from;
-    float q = rintf(d * st.inv);
-    const float r = fmaf(-q, st.s, d);
-    if (fabsf(r) >= st.half) {
-        const bool odd = ((int)q & 1) != 0;
-        if (r > st.half || (r == st.half && odd))
-            q += 1.f;
-        else if (r < -st.half || (r == -st.half && odd))
-            q -= 1.f;
-    }
-    return (uint32_t)(int)fminf(fmaxf(q, 0.f), 15.f);
+    t.x = fminf(FROM_0 ? t.x : fmaxf(t.x, ROUND), ROUND + 15.f);
+    t.y = fminf(FROM_0 ? t.y : fmaxf(t.y, ROUND), ROUND + 15.f);
+    word += __float_as_uint(t.x) << (8 * i);
+    word += __float_as_uint(t.y) << (8 * i + 4);
+    return fma(add(t, both(-ROUND)), both(st.s), both(st.b));
 }
 
-// Eight values at 8 * word of a row: coded into its word, and replaced by what the codes stand for.
-__device__ __forceinline__ uint32_t code_eight(float *x, const Step &st)
+// Eight 16-bit values coded into a word, and replaced by what the codes stand for.  d = x - b is exact where
+// its digits fit, and the quotient correctly rounded (a Newton step on d / s, whose remainder is exact): values on the
+// middle between two codes, which 16-bit numbers do hit, are seen as such and go to the even one.  The base is the
+// smallest value itself.
+__device__ __forceinline__ uint32_t code_values(float2 *x, const Step &st)
 {
-    uint32_t word = 0;
+    uint32_t word = 0u - ROUND_WORD;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t c = code_of(x[i], st);
-        word |= c << (4 * i);
-        x[i] = fmaf((float)c, st.s, st.b);
+    for (int i = 0; i < 4; ++i) {
+        const float2 d = add(x[i], both(-st.from));
+        const float2 q = mul(d, both(st.inv));
+        const float2 exact = fma(fma(q, both(-st.size), d), both(st.inv), q);
+        x[i] = put<true>(add(exact, both(ROUND)), i, st, word);
     }
     return word;
 }
 
-template <bool BF>
-__device__ __forceinline__ void unpack8(const uint4 &v, float *x)
+// Eight keys r z in two parts, coded; x: what the codes stand for.  The first guess at a code is off by one at most;
+// of the remainder r z - (b + q s) fp32 keeps 24 bits however small it is, and its quotient by s, correctly rounded as
+// above, corrects the guess with ties to even.
+__device__ __forceinline__ uint32_t code_keys(const float2 *z, const float2 *z_lo, const Two &r, float2 *x, const Step &st)
 {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t word = 0u - ROUND_WORD;
+    const float2 scale = both(r.hi * st.inv), start = both(-st.from * st.inv);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack2<BF>(w[i]);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
+        const float2 t = add(fma(z[i], scale, start), both(ROUND));
+        const float2 minus = fma(add(t, both(-ROUND)), both(-st.size), both(-st.from)); // -(b + q s)
+        const float2 rest =
+            fma(both(r.hi), z_lo[i], fma(both(r.lo), z[i], fma(both(r.hi), z[i], minus)));
+        const float2 q = mul(rest, both(st.inv));
+        const float2 exact = fma(fma(q, both(-st.size), rest), both(st.inv), q);
+        x[i] = put<false>(add(t, exact), i, st, word);
+    }
+    return word;
+}
+
+// Codes of values 0 2 4 6 ... of sixteen in a row and of 1 3 5 7 ... -> their two words in order.
+__device__ __forceinline__ void interleave(uint32_t &even, uint32_t &odd)
+{
+    auto spread = [](uint32_t v) { // four codes to the low halves of four bytes
+        v = (v | v << 8) & 0x00FF00FFu;
+        return (v | v << 4) & 0x0F0F0F0Fu;
+    };
+    const uint32_t first = spread(even & 0xFFFFu) | spread(odd & 0xFFFFu) << 4;
+    odd = spread(even >> 16) | spread(odd >> 16) << 4;
+    even = first;
+}
+
+// Sixteen 16-bit values as they lie -> first members of eight pairs, second members, where pairs lie side by side;
+// and back.
+__device__ __forceinline__ void apart(uint4 &a, uint4 &b)
+{
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    a = make_uint4(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410), __byte_perm(w[4], w[5], 0x5410),
+                   __byte_perm(w[6], w[7], 0x5410));
+    b = make_uint4(__byte_perm(w[0], w[1], 0x7632), __byte_perm(w[2], w[3], 0x7632), __byte_perm(w[4], w[5], 0x7632),
+                   __byte_perm(w[6], w[7], 0x7632));
+}
+
+__device__ __forceinline__ void together(uint4 &a, uint4 &b)
+{
+    const uint32_t f[4] = {a.x, a.y, a.z, a.w}, s[4] = {b.x, b.y, b.z, b.w};
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[2 * i] = __byte_perm(f[i], s[i], 0x5410);
+        w[2 * i + 1] = __byte_perm(f[i], s[i], 0x7632);
+    }
+    a = make_uint4(w[0], w[1], w[2], w[3]);
+    b = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+template <bool BF>
+__device__ __forceinline__ void unpack16(const uint4 &a, const uint4 &b, float2 (&x)[8])
+{
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        x[i] = BF ? make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)) : unpack2<BF>(w[i]);
+}
+
+template <bool BF>
+__device__ __forceinline__ uint4 pack8(const float2 *x)
+{
+    return make_uint4(pack2<BF>(x[0].x, x[0].y), pack2<BF>(x[1].x, x[1].y), pack2<BF>(x[2].x, x[2].y),
+                      pack2<BF>(x[3].x, x[3].y));
+}
+
+__device__ __forceinline__ float min3(float a, float b, float c) // NaN where one is
+{
+    float r;
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// The cosines and sines of eight pairs from 8 j on, by their token's positions; false where one is out of range.
+__device__ __forceinline__ bool angles(const NormParams &p, int token, int j, int pos, float2 (&c2)[4], float2 (&s2)[4])
+{
+    const int half = p.rot / 2;
+    pos = checked_position(p, pos);
+    const float *entry = p.table + (long long)max(pos, 0) * p.rot + 8 * j;
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+        const float4 c = *reinterpret_cast<const float4 *>(entry + 2 * i);
+        const float4 s = *reinterpret_cast<const float4 *>(entry + half + 2 * i);
+        c2[i] = make_float2(c.x, c.y);
+        c2[i + 1] = make_float2(c.z, c.w);
+        s2[i] = make_float2(s.x, s.y);
+        s2[i + 1] = make_float2(s.z, s.w);
+    }
+    bool known = pos >= 0;
+    if (p.cuts) {
+        // The pairs from a further section's start on take that axis's entries.
+        const int last = axis_of(p, 8 * j + 7);
+#pragma unroll 1
+        for (int a = axis_of(p, 8 * j) + 1; a <= last; ++a) {
+            const int from = p.cut[a - 1] - 8 * j;
+            if (p.cut[a] == p.cut[a - 1])
+                continue;
+            const int pa = checked_position(p, p.positions[(long long)a * p.ld_pos + token]);
+            known &= pa >= 0;
+            const float *other = p.table + (long long)max(pa, 0) * p.rot + 8 * j;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i >= from) {
+                    (i & 1 ? c2[i / 2].y : c2[i / 2].x) = other[i];
+                    (i & 1 ? s2[i / 2].y : s2[i / 2].x) = other[half + i];
+                }
+        }
+    }
+    return known;
+}
+
+// Whether a number that may be off by `off` could round to another 16-bit number.
+template <bool BF>
+__device__ __forceinline__ bool in_doubt(float x, float off)
+{
+    return from_float<BF>(x - off) != from_float<BF>(x + off);
+}
+
+// What a token's heads share in a thread (chunk j of a head).
+struct TokenOf {
+    float2 c[4], s[4]; // the angles of its eight pairs
+    long long pg;      // its place in the cache
+    int token, in_page, j;
+    bool live, known;  // it has a place; its positions are in range
+    bool held, turns;  // the thread has values; ... pairs
+};
+
+template <int LANES>
+__device__ __forceinline__ float sum_lanes(float x)
+{
+#pragma unroll
+    for (int d = 1; d < LANES; d <<= 1)
+        x += __shfl_xor_sync(0xffffffffu, x, d);
+    return x;
+}
+
+// Stores sixteen values as the head holds them.
+template <bool BF>
+__device__ __forceinline__ void store16(uint16_t *dst, int apart_by, bool beside, const float2 (&x)[8])
+{
+    uint4 a = pack8<BF>(x), b = pack8<BF>(x + 4);
+    if (beside)
+        together(a, b);
+    *reinterpret_cast<uint4 *>(dst) = a;
+    *reinterpret_cast<uint4 *>(dst + apart_by) = b;
+}
+
+// One head of q, or of k for the 16-bit cache: dst null: not written.
+template <bool BF, int LANES>
+__device__ __forceinline__ void plain_head(const NormParams &p, const TokenOf &t, uint4 x0, uint4 x1, const uint16_t *norm,
+                                           uint16_t *dst)
+{
+    const bool beside = t.turns && p.adjacent;
+    const int at0 = t.turns && !beside ? 8 * t.j : 16 * t.j, apart_by = t.turns && !beside ? p.rot / 2 : 8;
+    if (beside)
+        apart(x0, x1);
+    float2 x[8];
+    unpack16<BF>(x0, x1, x);
+    if (norm) {
+        uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
+        if (t.held) {
+            w0 = *reinterpret_cast<const uint4 *>(norm + at0);
+            w1 = *reinterpret_cast<const uint4 *>(norm + at0 + apart_by);
+        }
+        if (beside)
+            apart(w0, w1);
+        float2 sum = mul(x[0], x[0]), w[8];
+#pragma unroll
+        for (int i = 1; i < 8; ++i)
+            sum = fma(x[i], x[i], sum);
+        unpack16<BF>(w0, w1, w);
+        const float2 r = both(rsqrtf(fmaf(sum_lanes<LANES>(sum.x + sum.y), p.per_dim, p.eps)));
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            x[i] = mul(mul(x[i], r), w[i]);
+    }
+    if (t.turns) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 a = x[i], b = x[4 + i];
+            x[i] = fma(a, t.c[i], mul(b, make_float2(-t.s[i].x, -t.s[i].y)));
+            x[4 + i] = fma(b, t.c[i], mul(a, t.s[i]));
+        }
+    }
+    if (dst && t.held && t.known)
+        store16<BF>(dst + at0, apart_by, beside, x);
+}
+
+// The smallest and the largest value of the groups to which a thread's two halves belong.
+template <int GROUPS, int LANES>
+__device__ __forceinline__ void extremes(const float2 (&x)[8], bool held, int g0, int g1, float (&lo)[2], float (&hi)[2])
+{
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const float2 *v = x + 4 * e;
+        lo[e] = min3(min3(v[0].x, v[0].y, v[1].x), min3(v[1].y, v[2].x, v[2].y), min_nan(v[3].x, v[3].y));
+        hi[e] = max3(max3(v[0].x, v[0].y, v[1].x), max3(v[1].y, v[2].x, v[2].y), max_nan(v[3].x, v[3].y));
+    }
+    const float lo0 = lo[0], lo1 = lo[1], hi0 = hi[0], hi1 = hi[1];
+#pragma unroll
+    for (int q = 0; q < GROUPS; ++q) {
+        float l = held && g0 == q ? lo0 : INFINITY, m = held && g0 == q ? hi0 : -INFINITY;
+        if (held && g1 == q) {
+            l = min_nan(l, lo1);
+            m = max_nan(m, hi1);
+        }
+#pragma unroll
+        for (int d = 1; d < LANES; d <<= 1) {
+            l = min_nan(l, __shfl_xor_sync(0xffffffffu, l, d));
+            m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
+        }
+        if (q == 0 || g0 == q) {
+            lo[0] = l;
+            hi[0] = m;
+        }
+        if (q == 0 || g1 == q) {
+            lo[1] = l;
+            hi[1] = m;
+        }
     }
 }
 
-template <bool BF>
-__device__ __forceinline__ uint4 pack8(const float *x)
+// One head of k or v into the 4-bit cache; dst: where what it stands for goes, or null.
+template <bool BF, int GROUPS, int LANES, bool KEY>
+__device__ __forceinline__ void coded_head(const NormParams &p, const TokenOf &t, uint4 x0, uint4 x1, bool valid, int h,
+                                           uint16_t *dst)
 {
-    return make_uint4(pack2<BF>(x[0], x[1]), pack2<BF>(x[2], x[3]), pack2<BF>(x[4], x[5]), pack2<BF>(x[6], x[7]));
+    const bool turns = KEY && t.turns, beside = turns && p.adjacent;
+    const int at0 = turns && !beside ? 8 * t.j : 16 * t.j, apart_by = turns && !beside ? p.rot / 2 : 8, at1 = at0 + apart_by;
+    if (beside)
+        apart(x0, x1);
+    float2 x[8];
+    unpack16<BF>(x0, x1, x);
+    // Groups are whole blocks of 64 values, and each half of a thread's lies in one of them.
+    const int size = p.dim / GROUPS; // powers of two
+    const int shift = GROUPS == 1 ? 31 : 31 - __clz(size), g0 = at0 >> shift, g1 = at1 >> shift;
+    uint32_t word0, word1;
+    Step st0, st1;
+    float lo[2], hi[2];
+    if (!KEY) {
+        extremes<GROUPS, LANES>(x, t.held, g0, g1, lo, hi);
+        st0 = step_of<BF>(lo[0], fifteenth(hi[0] - lo[0]));
+        st1 = GROUPS == 1 ? st0 : step_of<BF>(lo[1], fifteenth(hi[1] - lo[1]));
+        word0 = code_values(x, st0);
+        word1 = code_values(x + 4, st1);
+    } else {
+        // Keys in two parts: r z with z = the turned x w (x w is exact).
+        Two r = {1.f, 0.f};
+        if (p.k_norm) {
+            uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
+            if (t.held) {
+                w0 = *reinterpret_cast<const uint4 *>(p.k_norm + at0);
+                w1 = *reinterpret_cast<const uint4 *>(p.k_norm + at1);
+            }
+            if (beside)
+                apart(w0, w1);
+            float2 sum = mul(x[0], x[0]), off = both(0.f); // (the squares are exact)
+#pragma unroll
+            for (int i = 1; i < 8; ++i) {
+                float2 e;
+                two_sum(sum, mul(x[i], x[i]), sum, e);
+                off = add(off, e);
+            }
+            Two total = two_sum(sum.x, sum.y);
+            total.lo += off.x + off.y;
+#pragma unroll
+            for (int d = 1; d < LANES; d <<= 1) {
+                const float o = __shfl_xor_sync(0xffffffffu, total.hi, d), ol = __shfl_xor_sync(0xffffffffu, total.lo, d);
+                const Two e = two_sum(total.hi, o);
+                total = {e.hi, (total.lo + ol) + e.lo};
+            }
+            Two a = two_sum(total.hi * p.per_dim, p.eps); // (dim is a power of two)
+            a.lo += total.lo * p.per_dim;
+            r.hi = rsqrtf(a.hi);
+            const float sq = __fmul_rn(r.hi, r.hi), sq_lo = fmaf(r.hi, r.hi, -sq);
+            const float rest = fmaf(-a.lo, sq, fmaf(-a.hi, sq_lo, fmaf(-a.hi, sq, 1.f))); // 1 - a r^2
+            r.lo = 0.5f * r.hi * rest;
+            if (!(fabsf(r.lo) < r.hi))
+                r.lo = 0.f; // sums of zero or infinity
+            float2 w[8];
+            unpack16<BF>(w0, w1, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                x[i] = mul(x[i], w[i]);
+        }
+        float2 z_lo[8]; // (x: the first parts)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            z_lo[i] = both(0.f);
+        if (turns) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 a = x[i], b = x[4 + i], c = t.c[i], s = t.s[i];
+                const float2 ns = make_float2(-s.x, -s.y), nc = make_float2(-c.x, -c.y);
+                const float2 ac = mul(a, c), bs = mul(b, ns), bc = mul(b, c), as = mul(a, s);
+                // The products' remainders, with the sign turned.
+                const float2 ac_off = fma(a, nc, ac), bs_off = fma(b, s, bs), bc_off = fma(b, nc, bc), as_off = fma(a, ns, as);
+                float2 e;
+                two_sum(ac, bs, x[i], e);
+                z_lo[i] = sub(e, add(ac_off, bs_off));
+                two_sum(bc, as, x[4 + i], e);
+                z_lo[4 + i] = sub(e, add(bc_off, as_off));
+            }
+        }
+        extremes<GROUPS, LANES>(x, t.held, g0, g1, lo, hi); // r is positive: the extreme z are the extreme keys'
+        // Base and step in fp32 are off by below 2^-21 of the larger extreme, and an eighth of that: mostly that does
+        // not matter to their 16-bit numbers.
+        float low[2], step[2];
+        bool doubt = false;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float off = fmaxf(fabsf(lo[e]), fabsf(hi[e])) * r.hi * 0x1p-21f;
+            low[e] = r.hi * lo[e];
+            step[e] = r.hi * fifteenth(hi[e] - lo[e]);
+            if (e < GROUPS)
+                doubt |= in_doubt<BF>(low[e], off) || in_doubt<BF>(step[e], 0.125f * off);
+        }
+        if (__any_sync(0xffffffffu, doubt)) {
+#pragma unroll 1
+            for (int q = 0; q < GROUPS; ++q) {
+                float l = INFINITY, m = -INFINITY; // the extremes' second parts, from whoever holds these
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (t.held && (e ? g1 : g0) == q)
+#pragma unroll
+                        for (int i = 4 * e; i < 4 * e + 4; ++i) {
+                            l = fminf(l, fminf(x[i].x == lo[e] ? z_lo[i].x : INFINITY, x[i].y == lo[e] ? z_lo[i].y : INFINITY));
+                            m = fmaxf(m, fmaxf(x[i].x == hi[e] ? z_lo[i].x : -INFINITY, x[i].y == hi[e] ? z_lo[i].y : -INFINITY));
+                        }
+#pragma unroll
+                for (int d = 1; d < LANES; d <<= 1) {
+                    l = fminf(l, __shfl_xor_sync(0xffffffffu, l, d));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if ((e ? g1 : g0) != q)
+                        continue;
+                    // The smallest key and the range over 15, each rounded once to fp32.
+                    const float first = __fmul_rn(r.hi, lo[e]);
+                    low[e] = first + fmaf(r.hi, l, fmaf(r.lo, lo[e], fmaf(r.hi, lo[e], -first)));
+                    Two range = two_sum(hi[e], -lo[e]);
+                    range.lo += m - l;
+                    const float width = __fmul_rn(r.hi, range.hi);
+                    const float rest = fmaf(r.hi, range.lo, fmaf(r.lo, range.hi, fmaf(r.hi, range.hi, -width)));
+                    const float part = fifteenth(width);
+                    step[e] = part + (fmaf(-part, 15.f, width) + rest) * (1.f / 15.f);
+                }
+            }
+        }
+        st0 = step_of<BF>(low[0], step[0]);
+        st1 = GROUPS == 1 ? st0 : step_of<BF>(low[1], step[1]);
+        float2 out[8];
+        word0 = code_keys(x, z_lo, r, out, st0);
+        word1 = code_keys(x + 4, z_lo + 4, r, out + 4, st1);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            x[i] = out[i];
+        if (beside)
+            interleave(word0, word1);
+    }
+    if (!valid || !t.held || (KEY && !t.known))
+        return;
+    if (t.live) {
+        uint8_t *row = p.cache + t.pg * p.page_stride + h * p.head_stride;
+        uint32_t *codes = reinterpret_cast<uint32_t *>(row + (KEY ? 0 : p.rec.values)) + (long long)t.in_page * (p.dim / 8);
+        const int blocks = p.dim / 64;
+        codes[KEY ? kv4_key_place(at0 / 8, blocks) : kv4_value_place(at0 / 8, blocks)] = word0;
+        codes[KEY ? kv4_key_place(at1 / 8, blocks) : kv4_value_place(at1 / 8, blocks)] = word1;
+        // Whoever has a group's first value stores its step and base.
+        uint32_t *params =
+            reinterpret_cast<uint32_t *>(row + (KEY ? p.rec.key_params : p.rec.value_params)) + (long long)t.in_page * GROUPS;
+        if ((at0 & (size - 1)) == 0)
+            params[g0] = st0.stored;
+        if ((at1 & (size - 1)) == 0)
+            params[g1] = st1.stored;
+    }
+    if (dst)
+        store16<BF>(dst + at0, apart_by, beside, x);
 }
 
-// 16-byte path.  Item (kind, head group, chunk j) of a thread: chunk j < rot / 16 of q and k is eight pairs, any
-// other 16 values in a row.  `lanes` threads, a power of two, belong to a head; those past dim / 16 only take part
-// in the shuffles.  GROUPS: groups of a row in the 4-bit cache, 0: the 16-bit cache.  CUTS: some section ends
-// inside a chunk.
-template <bool BF, int GROUPS, bool CUTS>
-__global__ void __launch_bounds__(256, NORM_PER_SM / 256)
-    norm_rope_kernel(const NormParams p, int lanes, int q_groups, int kv_groups)
+// 16-byte path: a block per token, of a warp where there are many (what belongs to a token is then looked up once for
+// all of its heads: 6007 tokens of 32 / 8 heads of 128 take 29.2 us, 31.3 with two warps a block and 36.1 with four), of as
+// many as it has items where all of these run at once (FEW).  Thread j of a head's LANES: chunk j < rot / 16 of q and k is eight pairs, any
+// other 16 values in a row; threads past dim / 16, and past a kind's heads, only take part in the shuffles.  A warp
+// takes items of 32 / LANES heads of one kind, q_items of q, then kv_items of k, then as many of v.  GROUPS: groups of
+// a row in the 4-bit cache, 0: the 16-bit cache.
+template <bool BF, int GROUPS, int LANES, bool FEW>
+__global__ void __launch_bounds__(FEW ? NORM_MOST : 32, FEW ? 1 : GROUPS ? 18 : 20)
+    norm_rope_kernel(const NormParams p, int q_items, int kv_items)
 {
     pdl_wait();
     pdl_launch_dependents();
-    const int item = blockIdx.y * blockDim.x + threadIdx.x;
-    const int stride = gridDim.x * blockDim.y;
-    int token = blockIdx.x * blockDim.y + threadIdx.y;
-    int g = item / lanes;
-    const int j = item - g * lanes;
-    if (g >= q_groups + 2 * kv_groups || token >= p.tokens)
-        return; // whole groups of lanes
-    const uint32_t lane_id = (threadIdx.y * blockDim.x + threadIdx.x) & 31;
-    const uint32_t mask = (lanes == 32 ? 0xffffffffu : (1u << lanes) - 1) << (lane_id & ~(uint32_t)(lanes - 1));
-    const int kind = g < q_groups ? KIND_Q : g < q_groups + kv_groups ? KIND_K : KIND_V;
-    g -= kind == KIND_Q ? 0 : kind == KIND_K ? q_groups : q_groups + kv_groups;
-    const int h0 = g * NORM_HEADS, heads = kind == KIND_Q ? p.heads : p.kv;
-    const int half = p.rot / 2;
-    const bool held = 16 * j < p.dim;                       // this thread has values
-    const bool pairs = kind != KIND_V && j < p.rot / 16;
-    const bool halves = pairs && !p.adjacent;
-    const int at0 = halves ? 8 * j : 16 * j, at1 = halves ? half + 8 * j : 16 * j + 8;
-    const bool cached = kind != KIND_Q;
-    const int axis0 = pairs ? axis_of(p, 8 * j) : 0, axis1 = CUTS && pairs ? axis_of(p, 8 * j + 7) : axis0;
-    const int32_t *positions = p.positions + (long long)axis0 * p.ld_pos;
-    const uint16_t *norm = kind == KIND_Q ? p.q_norm : kind == KIND_K ? p.k_norm : nullptr;
-    uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
-    if (norm && held) {
-        w0 = *reinterpret_cast<const uint4 *>(norm + at0);
-        w1 = *reinterpret_cast<const uint4 *>(norm + at1);
-    }
+    constexpr int AT_ONCE = 32 / LANES;
+    const int lane = threadIdx.x & 31, mine = lane / LANES, warps = FEW ? blockDim.x >> 5 : 1;
+    TokenOf t;
+    t.token = blockIdx.x;
+    t.j = lane % LANES;
+    t.held = 16 * t.j < p.dim;
+    t.turns = t.j < p.rot / 16;
+    t.known = true;
+    t.live = false;
+    t.pg = 0;
+    t.in_page = 0;
+    int pos = 0;
+    long long slot = -1;
+    if (t.turns)
+        pos = p.positions[(long long)axis_of(p, 8 * t.j) * p.ld_pos + t.token];
+    if (p.kv > 0)
+        slot = p.slots[t.token];
 
-    int next_pos = 0;
-    long long next_slot = -1;
-    uint4 n0[NORM_HEADS], n1[NORM_HEADS];
-#pragma unroll
-    for (int n = 0; n < NORM_HEADS; ++n)
-        n0[n] = n1[n] = make_uint4(0, 0, 0, 0);
-    auto fetch = [&](int t) {
-#pragma unroll
-        for (int n = 0; n < NORM_HEADS; ++n)
-            if (held && h0 + n < heads) {
-                const uint16_t *src = head_src(p, kind, t, h0 + n);
-                n0[n] = *reinterpret_cast<const uint4 *>(src + at0);
-                n1[n] = *reinterpret_cast<const uint4 *>(src + at1);
+    const uint32_t lanes = (LANES == 32 ? 0xffffffffu : (1u << LANES % 32) - 1) << (lane - t.j);
+    bool all_known = true;
+
+    // All items of a kind that are this warp's, with the next one's values on their way.
+    auto each = [&](auto kind_c, int item, int of_kind, const uint16_t *src, int ld, int heads, auto before, auto work) {
+        constexpr int KIND = decltype(kind_c)::value;
+        const bool halves = KIND != KIND_V && t.turns && !p.adjacent;
+        const int apart_by = halves ? p.rot / 2 : 8, step = warps * AT_ONCE;
+        int h = item * AT_ONCE + mine;
+        src += (long long)t.token * ld + (long long)h * p.dim + (halves ? 8 : 16) * t.j;
+        uint4 n0 = make_uint4(0, 0, 0, 0), n1 = n0;
+        auto fetch = [&](int head) {
+            if (t.held && head < heads) { // (past the heads: whatever was loaded last)
+                n0 = *reinterpret_cast<const uint4 *>(src);
+                n1 = *reinterpret_cast<const uint4 *>(src + apart_by);
+                src += (long long)step * p.dim;
             }
-        if (pairs)
-            next_pos = positions[t];
-        if (cached)
-            next_slot = p.slots[t];
+        };
+        fetch(h);
+        before();
+        for (; item < of_kind; item += warps, h += step) {
+            const uint4 x0 = n0, x1 = n1;
+            fetch(h + step);
+            work(x0, x1, h);
+        }
     };
-    fetch(token);
-    for (;;) {
-        uint4 x0[NORM_HEADS], x1[NORM_HEADS];
-#pragma unroll
-        for (int n = 0; n < NORM_HEADS; ++n) {
-            x0[n] = n0[n];
-            x1[n] = n1[n];
-        }
-        const int t = token, pos = pairs ? checked_position(p, next_pos) : 0;
-        long long pg = 0;
-        int in_page = 0;
-        const bool live = cached && page_of(p, next_slot, pg, in_page);
-        bool known = pos >= 0;
-        float c[8], s[8];
-        if (pairs && known) {
-            const float *entry = p.table + (long long)pos * p.rot + 8 * j;
-#pragma unroll
-            for (int i = 0; i < 8; i += 4) {
-                *reinterpret_cast<float4 *>(c + i) = *reinterpret_cast<const float4 *>(entry + i);
-                *reinterpret_cast<float4 *>(s + i) = *reinterpret_cast<const float4 *>(entry + half + i);
+    // What waits for the token's position and slot, behind the first loads of values.
+    auto look_up = [&]() {
+        if (t.turns)
+            t.known = angles(p, t.token, t.j, pos, t.c, t.s);
+        t.live = p.kv > 0 && page_of(p, slot, t.pg, t.in_page);
+        all_known = (__ballot_sync(0xffffffffu, t.known) & lanes) == lanes; // what a coded key needs
+    };
+    const int warp = FEW ? threadIdx.x >> 5 : 0;
+    each(std::integral_constant<int, KIND_Q>(), warp, q_items, p.q, p.ldq, p.heads, look_up, [&](uint4 x0, uint4 x1, int h) {
+        uint16_t *dst = p.q_out + (long long)t.token * p.ldqo + (long long)h * p.dim;
+        plain_head<BF, LANES>(p, t, x0, x1, p.q_norm, h < p.heads ? dst : nullptr);
+    });
+    // (a warp's turn: the kinds follow one another)
+    const int first_k = (warp + warps - q_items % warps) % warps, first_v = (first_k + warps - kv_items % warps) % warps;
+    auto nothing = [] {};
+    const long long row = t.pg * p.page_stride + t.in_page * p.token_stride;
+    if constexpr (GROUPS == 0) {
+        each(std::integral_constant<int, KIND_K>(), first_k, kv_items, p.k, p.ldk, p.kv, nothing, [&](uint4 x0, uint4 x1, int h) {
+            uint16_t *dst = p.k_cache + row + h * p.head_stride;
+            plain_head<BF, LANES>(p, t, x0, x1, p.k_norm, h < p.kv && t.live ? dst : nullptr);
+        });
+        each(std::integral_constant<int, KIND_V>(), first_v, kv_items, p.v, p.ldv, p.kv, nothing, [&](uint4 x0, uint4 x1, int h) {
+            if (h < p.kv && t.live && t.held) { // copied as it is
+                uint16_t *dst = p.v_cache + row + h * p.head_stride + 16 * t.j;
+                *reinterpret_cast<uint4 *>(dst) = x0;
+                *reinterpret_cast<uint4 *>(dst + 8) = x1;
             }
-            if (CUTS) {
-                // The pairs from a further section's start on take that axis's entries.
-#pragma unroll 1
-                for (int a = axis0 + 1; a <= axis1; ++a) {
-                    const int from = p.cut[a - 1] - 8 * j;
-                    if (p.cut[a] == p.cut[a - 1])
-                        continue;
-                    const int pa = checked_position(p, p.positions[(long long)a * p.ld_pos + t]);
-                    known &= pa >= 0;
-                    const float *other = p.table + (long long)max(pa, 0) * p.rot + 8 * j;
-#pragma unroll
-                    for (int i = 0; i < 8; i += 4) {
-                        const float4 c4 = *reinterpret_cast<const float4 *>(other + i);
-                        const float4 s4 = *reinterpret_cast<const float4 *>(other + half + i);
-                        const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, ss[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            if (i + q >= from) {
-                                c[i + q] = cc[q];
-                                s[i + q] = ss[q];
-                            }
-                    }
-                }
-            }
-        }
-        const bool more = p.tokens - token > stride; // (the sum may pass 31 bits)
-        if (more) {
-            token += stride;
-            fetch(token);
-        }
-        // A key in 4 bits needs all of its positions, as its groups are coded together.
-        const bool whole = GROUPS > 0 && kind == KIND_K ? __all_sync(mask, known) != 0 : known;
-#pragma unroll
-        for (int n = 0; n < NORM_HEADS; ++n) {
-            const int h = h0 + n;
-            if (h >= heads)
-                break; // whole groups of lanes
-            if (GROUPS == 0 && kind == KIND_V) { // copied as it is
-                if (live && held) {
-                    uint16_t *dst = p.v_cache + pg * p.page_stride + in_page * p.token_stride + h * p.head_stride;
-                    *reinterpret_cast<uint4 *>(dst + at0) = x0[n];
-                    *reinterpret_cast<uint4 *>(dst + at1) = x1[n];
-                }
-                continue;
-            }
-            float x[16];
-            unpack8<BF>(x0[n], x);
-            unpack8<BF>(x1[n], x + 8);
-            if (norm) {
-                float sum = 0.f;
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    sum = fmaf(x[i], x[i], sum);
-                for (int d = 1; d < lanes; d <<= 1)
-                    sum += __shfl_xor_sync(mask, sum, d);
-                const float r = rsqrtf(sum / (float)p.dim + p.eps);
-                float w[16];
-                unpack8<BF>(w0, w);
-                unpack8<BF>(w1, w + 8);
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    x[i] = x[i] * r * w[i];
-            }
-            if (pairs && whole) {
-                if (p.adjacent) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float a = x[2 * i], b = x[2 * i + 1];
-                        x[2 * i] = turned_first(a, b, c[i], s[i]);
-                        x[2 * i + 1] = turned_second(a, b, c[i], s[i]);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float a = x[i], b = x[8 + i];
-                        x[i] = turned_first(a, b, c[i], s[i]);
-                        x[8 + i] = turned_second(a, b, c[i], s[i]);
-                    }
-                }
-            }
-            uint16_t *dst = nullptr; // 16-bit results
-            if (kind == KIND_Q)
-                dst = p.q_out + (long long)t * p.ldqo + (long long)h * p.dim;
-            else if (GROUPS == 0)
-                dst = live ? p.k_cache + pg * p.page_stride + in_page * p.token_stride + h * p.head_stride : nullptr;
-            else if (kind == KIND_K)
-                dst = p.k_out ? p.k_out + (long long)t * p.ldko + (long long)h * p.dim : nullptr;
-            else
-                dst = p.v_out ? p.v_out + (long long)t * p.ldvo + (long long)h * p.dim : nullptr;
-            if (GROUPS > 0 && kind != KIND_Q) {
-                constexpr int N = GROUPS > 0 ? GROUPS : 1;
-                // Groups are whole blocks of 64 values, and each half of a thread's values lies in one of them.
-                const int size = p.dim / N, g0 = at0 / size, g1 = at1 / size;
-                float lo[2] = {x[0], x[8]}, hi[2] = {x[0], x[8]};
-#pragma unroll
-                for (int i = 1; i < 8; ++i)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        lo[e] = min_nan(lo[e], x[8 * e + i]);
-                        hi[e] = max_nan(hi[e], x[8 * e + i]);
-                    }
-                Step st0, st1;
-                uint32_t stored = 0;
-#pragma unroll
-                for (int q = 0; q < N; ++q) {
-                    float l = INFINITY, m = -INFINITY;
-                    if (held && g0 == q) {
-                        l = lo[0];
-                        m = hi[0];
-                    }
-                    if (held && g1 == q) {
-                        l = min_nan(l, lo[1]);
-                        m = max_nan(m, hi[1]);
-                    }
-                    for (int d = 1; d < lanes; d <<= 1) {
-                        l = min_nan(l, __shfl_xor_sync(mask, l, d));
-                        m = max_nan(m, __shfl_xor_sync(mask, m, d));
-                    }
-                    const Step st = step_of<BF>(l, m);
-                    if (q == 0 || g0 == q)
-                        st0 = st;
-                    if (q == 0 || g1 == q)
-                        st1 = st;
-                    if (j == q)
-                        stored = st.stored;
-                }
-                const uint32_t word0 = code_eight(x, st0), word1 = code_eight(x + 8, st1);
-                if (live && held && whole) {
-                    uint8_t *row = p.cache + pg * p.page_stride + h * p.head_stride;
-                    uint32_t *codes = reinterpret_cast<uint32_t *>(row + (kind == KIND_V ? p.rec.values : 0)) +
-                                      (long long)in_page * (p.dim / 8);
-                    const int blocks = p.dim / 64;
-                    const int a0 = kind == KIND_K ? kv4_key_place(at0 / 8, blocks) : kv4_value_place(at0 / 8, blocks);
-                    const int a1 = kind == KIND_K ? kv4_key_place(at1 / 8, blocks) : kv4_value_place(at1 / 8, blocks);
-                    codes[a0] = word0;
-                    codes[a1] = word1;
-                    if (j < N)
-                        reinterpret_cast<uint32_t *>(row + (kind == KIND_K ? p.rec.key_params : p.rec.value_params))
-                            [(long long)in_page * N + j] = stored;
-                }
-            }
-            if (dst && held && whole) {
-                *reinterpret_cast<uint4 *>(dst + at0) = pack8<BF>(x);
-                *reinterpret_cast<uint4 *>(dst + at1) = pack8<BF>(x + 8);
-            }
-        }
-        if (!more)
-            return;
+        });
+    } else {
+        t.known = all_known;
+        each(std::integral_constant<int, KIND_K>(), first_k, kv_items, p.k, p.ldk, p.kv, nothing, [&](uint4 x0, uint4 x1, int h) {
+            uint16_t *dst = p.k_out ? p.k_out + (long long)t.token * p.ldko + (long long)h * p.dim : nullptr;
+            coded_head<BF, GROUPS, LANES, true>(p, t, x0, x1, h < p.kv, h, dst);
+        });
+        each(std::integral_constant<int, KIND_V>(), first_v, kv_items, p.v, p.ldv, p.kv, nothing, [&](uint4 x0, uint4 x1, int h) {
+            uint16_t *dst = p.v_out ? p.v_out + (long long)t.token * p.ldvo + (long long)h * p.dim : nullptr;
+            coded_head<BF, GROUPS, LANES, false>(p, t, x0, x1, h < p.kv, h, dst);
+        });
     }
 }
 
@@ -462,7 +755,7 @@ __global__ void __launch_bounds__(32 * NORM_WARPS) norm_rope_any_kernel(const No
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1)
                 sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            r = rsqrtf(sum / (float)p.dim + p.eps);
+            r = rsqrtf(fmaf(sum, p.per_dim, p.eps));
         }
         const int half = p.rot / 2, items = half + (p.dim - p.rot + 1) / 2;
         for (int i = lane; i < items; i += 32) {
@@ -564,34 +857,30 @@ bool wide(const NormParams &p)
            aligned(p.table, 16);
 }
 
-template <bool BF, int GROUPS>
-int launch_wide(const NormParams &p, cudaStream_t stream)
+template <bool BF, int GROUPS, int LANES>
+int launch_lanes(const NormParams &p, cudaStream_t stream)
 {
-    int lanes = 1;
-    while (16 * lanes < p.dim)
-        lanes *= 2;
-    const int q_groups = (p.heads + NORM_HEADS - 1) / NORM_HEADS, kv_groups = (p.kv + NORM_HEADS - 1) / NORM_HEADS;
-    const long long items = (long long)lanes * (q_groups + 2LL * kv_groups);
-    // Blocks of whole tokens up to NORM_THREADS; wider tokens take blocks of their own side by side.
-    const int bx = items < 256 ? (int)items : 256;
-    const long long side = (items + bx - 1) / bx;
-    if (side > 65535)
-        return status_of(STAGE_ARG, W4A16_ARG_OVERFLOW);
-    int by = NORM_THREADS / bx;
-    by = by < 1 ? 1 : by > p.tokens ? p.tokens : by;
     int num_sms = 0;
     const cudaError_t err = sm_count(&num_sms);
     if (err != cudaSuccess)
         return status_of(STAGE_RESOURCE, err);
-    const long long groups = (p.tokens + (long long)by - 1) / by;
-    long long blocks = (long long)num_sms * (NORM_PER_SM / (bx * by)) / side;
-    blocks = blocks < 1 ? 1 : blocks > groups ? groups : blocks;
-    bool cuts = false;
-    for (int a = 0; a < p.axes - 1; ++a)
-        cuts |= p.cut[a] % 8 != 0;
-    const auto kernel = cuts ? norm_rope_kernel<BF, GROUPS, true> : norm_rope_kernel<BF, GROUPS, false>;
-    return launch_status(launch_pdl(kernel, dim3((unsigned)blocks, (unsigned)side), dim3(bx, by), 0, stream, p, lanes,
-                                    q_groups, kv_groups));
+    constexpr int AT_ONCE = 32 / LANES; // heads of a warp
+    const int q_items = (p.heads + AT_ONCE - 1) / AT_ONCE, kv_items = (p.kv + AT_ONCE - 1) / AT_ONCE;
+    const int items = q_items + 2 * kv_items;
+    // A warp per item while the GPU has room for all of them: a call of few tokens is as long as its longest warp.
+    if ((long long)p.tokens * items <= (long long)num_sms * NORM_PER_SM) {
+        const int warps = items < NORM_MOST / 32 ? items : NORM_MOST / 32;
+        return launch_status(launch_pdl(norm_rope_kernel<BF, GROUPS, LANES, true>, dim3((unsigned)p.tokens),
+                                        dim3(32 * warps), 0, stream, p, q_items, kv_items));
+    }
+    return launch_status(launch_pdl(norm_rope_kernel<BF, GROUPS, LANES, false>, dim3((unsigned)p.tokens), dim3(32), 0,
+                                    stream, p, q_items, kv_items));
+}
+
+template <int GROUPS, int LANES>
+int launch_type(bool bf, const NormParams &p, cudaStream_t stream)
+{
+    return bf ? launch_lanes<true, GROUPS, LANES>(p, stream) : launch_lanes<false, GROUPS, LANES>(p, stream);
 }
 
 NormParams params(const void *q, int ldq, const void *k, int ldk, const void *v, int ldv, const void *q_norm,
@@ -613,6 +902,7 @@ NormParams params(const void *q, int ldq, const void *k, int ldk, const void *v,
     p.status = status;
     p.total_slots = (long long)n_pages * page_size;
     p.eps = eps;
+    p.per_dim = head_dim > 0 ? 1.f / (float)head_dim : 0.f;
     p.ldq = ldq;
     p.ldk = ldk;
     p.ldv = ldv;
@@ -638,6 +928,9 @@ void set_cuts(NormParams &p, const int32_t *sections)
             cut += sections[a];
         p.cut[a] = cut;
     }
+    p.cuts = 0;
+    for (int a = 0; a < p.axes - 1; ++a)
+        p.cuts |= p.cut[a] % 8 != 0;
 }
 
 } // namespace
@@ -685,7 +978,10 @@ extern "C" int w4a16_norm_rope_append(const void *q, int ldq, const void *k, int
     const bool bf = (flags & W4A16_FLAG_BF16) != 0;
     const long long strides = n_kv_heads ? kv_page_stride | kv_token_stride | kv_head_stride : 0;
     if (wide(p) && strides % 8 == 0 && aligned(p.k_cache, 16) && aligned(p.v_cache, 16))
-        return bf ? launch_wide<true, 0>(p, stream) : launch_wide<false, 0>(p, stream);
+        return head_dim <= 64    ? launch_type<0, 4>(bf, p, stream)
+               : head_dim <= 128 ? launch_type<0, 8>(bf, p, stream)
+               : head_dim <= 256 ? launch_type<0, 16>(bf, p, stream)
+                                 : launch_type<0, 32>(bf, p, stream);
     int num_sms = 0;
     const cudaError_t err = sm_count(&num_sms);
     if (err != cudaSuccess)
@@ -750,11 +1046,12 @@ extern "C" int w4a16_kv4_append(const void *q, int ldq, const void *k, int ldk, 
     p.page_stride = page_stride;
     p.head_stride = p.rec.bytes;
     set_cuts(p, sections);
-    if (flags & W4A16_FLAG_BF16)
-        return groups == 1   ? launch_wide<true, 1>(p, stream)
-               : groups == 2 ? launch_wide<true, 2>(p, stream)
-                             : launch_wide<true, 4>(p, stream);
-    return groups == 1   ? launch_wide<false, 1>(p, stream)
-           : groups == 2 ? launch_wide<false, 2>(p, stream)
-                         : launch_wide<false, 4>(p, stream);
+    const bool bf = (flags & W4A16_FLAG_BF16) != 0;
+    if (head_dim == 64)
+        return launch_type<1, 4>(bf, p, stream);
+    if (head_dim == 128)
+        return groups == 1 ? launch_type<1, 8>(bf, p, stream) : launch_type<2, 8>(bf, p, stream);
+    return groups == 1   ? launch_type<1, 16>(bf, p, stream)
+           : groups == 2 ? launch_type<2, 16>(bf, p, stream)
+                         : launch_type<4, 16>(bf, p, stream);
 }
