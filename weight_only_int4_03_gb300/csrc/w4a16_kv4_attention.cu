@@ -85,6 +85,16 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a)
     return d;
 }
 
+// D = A * B + C, apart from D.
+__device__ __forceinline__ void mma16816_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1, const float (&c)[4])
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+
 // N bytes from global to shared memory, or N zero bytes when `live` is false.
 template <int N>
 __device__ __forceinline__ void cp_async(uint32_t dst, const void *src, bool live)
@@ -143,7 +153,8 @@ __device__ __forceinline__ int value_chunk(int row, int chunk)
     return D == 64 ? chunk : D == 128 ? chunk ^ (row & 2) : chunk ^ (2 * (row & 3));
 }
 
-template <int D, int G, int NT, bool BF>
+// WHOLE: pages hold multiples of 16 positions, so that a sub-step lies in one of them.
+template <int D, int G, int NT, bool BF, bool WHOLE>
 __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_attention_kernel(const Kv4AttParams p)
 {
     using M = Kv4Geom<D, G, NT>;
@@ -151,7 +162,6 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
     constexpr int PER = BLOCKS / G;                       // blocks of 64 per group
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ SplitShared shared;
-    __shared__ uint8_t live_bits[M::STAGES][SPLIT_THREADS];
     __shared__ float stat[SPLIT_WARPS][M::HEADS][2];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -160,7 +170,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
     pdl_wait();
     pdl_launch_dependents();
 
-    Split<KV4_UNIT, M::ROW_COST> split(p.split, shared);
+    Split<KV4_UNIT, M::ROW_COST, true> split(p.split, shared);
     // Sequences without a position: zeros and -inf.
     for (int b = blockIdx.x; b < p.split.batch; b += gridDim.x) {
         if (!split.empty(b))
@@ -177,64 +187,105 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
     while (split.next(seg)) {
         const int b = seg.b, c = seg.row / p.tiles, h0 = (seg.row - c * p.tiles) * M::HEADS;
         const int nh = min(M::HEADS, p.group - h0); // heads of this tile
-        const int len = seg.len, steps = seg.unit1 - seg.unit0;
-        const int pos0 = seg.first + seg.unit0 * KV4_UNIT + warp * KV4_STEP + row_of; // this lane's first position
+        const int first = seg.first, len = seg.len, steps = seg.unit1 - seg.unit0;
+        const int pos0 = seg.start + seg.unit0 * KV4_UNIT + warp * KV4_STEP; // this warp's first position
 
         // --- copies ---------------------------------------------------------------------------
-        // A lane looks after positions pos0 + 8 i of a step: pages are looked up one step before they are used.
+        // A lane looks after positions row_of + 8 i, i < 4, of a step.  Pages are looked up one step before they are used:
+        // those of the two sub-steps, or of each lane's four positions.
+        constexpr int LOOK = WHOLE ? 2 : 4;
         const int32_t *tab = p.table + (long long)b * p.ld_table;
         const uint8_t *head = p.cache + c * p.rec.bytes;
-        int next_page[4], next_token[4];
+        int next_page[LOOK], next_token[LOOK];
         auto look_up = [&](int step) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int pos = pos0 + step * KV4_UNIT + 8 * i;
-                const bool in = step < steps && pos < len;
+            for (int i = 0; i < LOOK; ++i) {
+                const int pos = pos0 + step * KV4_UNIT + (WHOLE ? 16 * i : row_of + 8 * i);
+                const bool in = step < steps && pos < len && (WHOLE ? pos + 16 > first : pos >= first);
                 const int at = p.page_magic ? (int)(__umulhi((uint32_t)pos, p.page_magic) >> p.page_shift) : pos;
                 next_page[i] = in ? tab[at] : -1;
                 next_token[i] = pos - at * p.page;
             }
         };
+        // What is live of the steps in flight, the newest in the lowest five bits: this lane's positions, and whether all
+        // of the step is.
+        uint32_t flight = 0;
         auto issue = [&](int step, int stage) {
-            uint32_t bits = 0;
+            flight <<= 5;
+            if (step >= steps)
+                return;
+            const int pos = pos0 + step * KV4_UNIT;
+            const uint32_t st = ring + stage * M::STAGE;
+            constexpr int HALVES = D / 128; // 16-byte chunks of a lane in a row
+            if (WHOLE && pos >= first && pos + KV4_STEP <= len && (uint32_t)next_page[0] < (uint32_t)p.n_pages &&
+                (uint32_t)next_page[LOOK / 2] < (uint32_t)p.n_pages) {
+                flight |= 31;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const uint8_t *rec = head + (long long)next_page[u * LOOK / 2 % LOOK] * p.page_stride;
+                    const int token = next_token[u * LOOK / 2 % LOOK] + row_of;
+                    const uint8_t *keys = rec + (long long)token * M::ROW + (D == 64 ? 8 : 16) * t, *values = keys + p.rec.values;
+                    const uint32_t sub = st + u * M::SUB;
+                    const uint32_t key_to = sub + lane * (D == 64 ? 8 : 16), value_to = sub + M::KEYS + row_of * M::ROW;
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        if (D == 64) {
+                            cp_async<8>(key_to + r * 256, keys + r * 8 * M::ROW, true);
+                            cp_async<8>(value_to + r * 8 * M::ROW + t * 8, values + r * 8 * M::ROW, true);
+                        } else {
+#pragma unroll
+                            for (int h = 0; h < HALVES; ++h) {
+                                cp_async<16>(key_to + (r * HALVES + h) * 512, keys + r * 8 * M::ROW + h * 64, true);
+                                cp_async<16>(value_to + r * 8 * M::ROW + value_chunk<D>(row_of, t + 4 * h) * 16,
+                                             values + r * 8 * M::ROW + h * 64, true);
+                            }
+                        }
+                    }
+                    // Steps and bases: a lane copies those of one of its two positions of a sub-step, of one side.
+                    const int row = token + 8 * (t & 1);
+                    cp_async<4 * G>(sub + 2 * M::KEYS + (t >> 1) * M::PARAMS + (row_of + 8 * (t & 1)) * (4 * G),
+                                    rec + (t >> 1 ? p.rec.value_params : p.rec.key_params) + (long long)row * (4 * G), true);
+                }
+                return;
+            }
             const uint8_t *rec[4];
+            uint32_t bits = 0;
+            int token[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const bool in = step < steps && pos0 + step * KV4_UNIT + 8 * i < len;
-                const bool ok = in && next_page[i] >= 0 && next_page[i] < p.n_pages;
+                const int at = pos + row_of + 8 * i, page = next_page[WHOLE ? i / 2 : i];
+                const bool in = at >= first && at < len, ok = in && page >= 0 && page < p.n_pages;
                 if (in && !ok)
                     atomicOr(p.split.status, W4A16_DEV_PAGE);
-                rec[i] = head + (ok ? (long long)next_page[i] * p.page_stride : 0);
+                rec[i] = head + (ok ? (long long)page * p.page_stride : 0);
+                token[i] = ok ? next_token[WHOLE ? i / 2 : i] + (WHOLE ? row_of + 8 * (i & 1) : 0) : 0;
                 bits |= (ok ? 1u : 0u) << i;
             }
-            live_bits[stage][tid] = (uint8_t)bits;
-            const uint32_t st = ring + stage * M::STAGE;
+            flight |= bits;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int r = i & 1, row = row_of + 8 * r;
                 const uint32_t sub = st + (i >> 1) * M::SUB;
                 const bool ok = (bits >> i) & 1u;
-                const long long at = ok ? (long long)next_token[i] * M::ROW : 0;
-                const uint8_t *keys = rec[i] + at, *values = keys + p.rec.values;
+                const uint8_t *keys = rec[i] + (long long)token[i] * M::ROW, *values = keys + p.rec.values;
                 if (D == 64) {
                     cp_async<8>(sub + r * 256 + lane * 8, keys + t * 8, ok);
                     cp_async<8>(sub + M::KEYS + row * M::ROW + t * 8, values + t * 8, ok);
                 } else {
 #pragma unroll
-                    for (int h = 0; h < D / 128; ++h) {
+                    for (int h = 0; h < HALVES; ++h) {
                         const int ch = t + 4 * h;
-                        cp_async<16>(sub + (r * (D / 128) + h) * 512 + lane * 16, keys + ch * 16, ok);
+                        cp_async<16>(sub + (r * HALVES + h) * 512 + lane * 16, keys + ch * 16, ok);
                         cp_async<16>(sub + M::KEYS + row * M::ROW + value_chunk<D>(row, ch) * 16, values + ch * 16, ok);
                     }
                 }
             }
-            // Steps and bases: a lane copies those of one of its two positions of a sub-step, of one side.
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const bool second = t & 1;
-                const bool ok = (bits >> (2 * u + (second ? 1 : 0))) & 1u;
-                const uint8_t *src = (second ? rec[2 * u + 1] : rec[2 * u]) + (t >> 1 ? p.rec.value_params : p.rec.key_params) +
-                                     (ok ? (long long)(second ? next_token[2 * u + 1] : next_token[2 * u]) * (4 * G) : 0);
+                const int i = 2 * u + (t & 1);
+                const bool ok = (bits >> i) & 1u;
+                const uint8_t *src = (t & 1 ? rec[2 * u + 1] : rec[2 * u]) + (t >> 1 ? p.rec.value_params : p.rec.key_params) +
+                                     (long long)(t & 1 ? token[2 * u + 1] : token[2 * u]) * (4 * G);
                 cp_async<4 * G>(st + u * M::SUB + 2 * M::KEYS + (t >> 1) * M::PARAMS + (row_of + 8 * (t & 1)) * (4 * G), src, ok);
             }
         };
@@ -242,7 +293,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
         look_up(0);
         // --- queries: B fragments of the score product ------------------------------------------
         uint32_t qf[NT][BLOCKS][2][4]; // [word of a block]: values 0 4, 2 6; a sixteenth of 1 5, 3 7
-        float fac[NT][2], qs[NT][2][G];
+        float2 fac[NT], qs[NT][G];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const bool in = nt * 8 + g < nh;
@@ -287,13 +338,13 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
                 }
             // This lane's columns are heads 2 t and 2 t + 1: their factor and sums.
             const float mine = p.scale_log2 * __uint_as_float((uint32_t)(24 - up + 127) << 23);
+            const auto columns = [&](float v) {
+                return make_float2(__shfl_sync(0xffffffffu, v, 8 * t), __shfl_sync(0xffffffffu, v, 8 * t + 4));
+            };
+            fac[nt] = columns(mine);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                fac[nt][e] = __shfl_sync(0xffffffffu, mine, (2 * t + e) * 4);
-#pragma unroll
-                for (int q = 0; q < G; ++q)
-                    qs[nt][e][q] = p.scale_log2 * __shfl_sync(0xffffffffu, sum[q], (2 * t + e) * 4);
-            }
+            for (int q = 0; q < G; ++q)
+                qs[nt][q] = columns(p.scale_log2 * sum[q]);
         }
 #pragma unroll
         for (int s = 0; s < M::STAGES - 1; ++s) {
@@ -303,28 +354,25 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
         }
 
         // --- the running softmax ----------------------------------------------------------------
-        float o[NT][TILES][4], m[NT][2], l[NT][2], base[NT][2][G];
+        // Pairs: heads 2 t and 2 t + 1.
+        float2 o[NT][TILES][2], m[NT], l[NT], base[NT][G];
         float ref = 0.f, up = 0.f; // the power of two above every value step so far, and KV4_UP over it
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int n = 0; n < TILES; ++n)
+                o[nt][n][0] = o[nt][n][1] = both(0.f);
+            m[nt] = both(-3.402823466e38f); // not -inf: nothing live yet then gives p = 0
+            l[nt] = both(0.f);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    o[nt][n][e] = 0.f;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                m[nt][e] = -3.402823466e38f; // not -inf: nothing live yet then gives p = 0
-                l[nt][e] = 0.f;
-#pragma unroll
-                for (int q = 0; q < G; ++q)
-                    base[nt][e][q] = 0.f;
-            }
+            for (int q = 0; q < G; ++q)
+                base[nt][q] = both(0.f);
         }
         int stage = 0;
         for (int step = 0; step < steps; ++step) {
             cp_async_wait<M::STAGES - 2>();
             __syncwarp(); // every lane's copies of this stage have landed; the next one is free
+            const uint32_t live = flight >> (5 * (M::STAGES - 2));
             {
                 int ns = stage + M::STAGES - 1;
                 ns = ns >= M::STAGES ? ns - M::STAGES : ns;
@@ -333,10 +381,10 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
                 look_up(step + M::STAGES);
             }
             const uint32_t st = ring + stage * M::STAGE;
-            const uint32_t bits = live_bits[stage][tid];
 
-            // Scores x[sub-step][tile][row, column] of positions row_of + 16 u (+ 8), heads 2 t and 2 t + 1.
-            float x[2][NT][4], vs[2][2][G], va[2][2][G];
+            // Scores x[sub-step][tile][row] of positions row_of + 16 u (+ 8).
+            float2 x[2][NT][2];
+            float vs[2][2][G], va[2][2][G];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const uint32_t sub = st + u * M::SUB;
@@ -393,42 +441,39 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float y = fmaf(acc[nt][e] * ks[e >> 1][q], fac[nt][e & 1], ka[e >> 1][q] * qs[nt][e & 1][q]);
-                            x[u][nt][e] = q == 0 ? y : x[u][nt][e] + y;
+                        for (int r = 0; r < 2; ++r) {
+                            const float2 sum = mul(make_float2(acc[nt][2 * r], acc[nt][2 * r + 1]), both(ks[r][q]));
+                            const float2 y = fma(sum, fac[nt], mul(both(ka[r][q]), qs[nt][q]));
+                            x[u][nt][r] = q == 0 ? y : add(x[u][nt][r], y);
                         }
                 }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        x[u][nt][e] = (bits >> (2 * u + (e >> 1))) & 1u ? x[u][nt][e] : -INFINITY;
             }
-
-            // Does a maximum or the reference of the value steps have to move?
-            bool moves = false;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        moves |= x[u][nt][e] - KV4_LAZY > m[nt][e & 1];
-#pragma unroll
-                for (int r = 0; r < 2; ++r)
-#pragma unroll
-                    for (int q = 0; q < G; ++q)
-                        moves |= vs[u][r][q] > ref;
-            }
-            if (__any_sync(0xffffffffu, moves)) {
-                float step_top = ref;
+            if (!(live & 16u)) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int r = 0; r < 2; ++r)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int q = 0; q < G; ++q)
-                            step_top = fmaxf(step_top, vs[u][r][q]);
+                        for (int r = 0; r < 2; ++r)
+                            if (!((live >> (2 * u + r)) & 1u))
+                                x[u][nt][r] = both(-INFINITY);
+            }
+
+            // Does a maximum or the reference of the value steps have to move?  (A NaN does not move anything.)
+            float step_top = ref;
+#pragma unroll
+            for (int q = 0; q < G; ++q)
+                step_top = fmaxf(step_top, fmaxf(fmaxf(vs[0][0][q], vs[0][1][q]), fmaxf(vs[1][0][q], vs[1][1][q])));
+            bool moves = step_top > ref;
+            float2 top[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                top[nt].x = fmaxf(fmaxf(x[0][nt][0].x, x[0][nt][1].x), fmaxf(x[1][nt][0].x, x[1][nt][1].x));
+                top[nt].y = fmaxf(fmaxf(x[0][nt][0].y, x[0][nt][1].y), fmaxf(x[1][nt][0].y, x[1][nt][1].y));
+                const float2 over = sub(top[nt], m[nt]);
+                moves |= over.x > KV4_LAZY || over.y > KV4_LAZY;
+            }
+            if (__any_sync(0xffffffffu, moves)) {
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1)
                     step_top = fmaxf(step_top, __shfl_xor_sync(0xffffffffu, step_top, d));
@@ -441,38 +486,39 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
                     up = KV4_UP / to;
                 }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float top = fmaxf(fmaxf(x[0][nt][e], x[0][nt][2 + e]), fmaxf(x[1][nt][e], x[1][nt][2 + e]));
-#pragma unroll
-                        for (int d = 4; d < 32; d <<= 1)
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                        const float to = fmaxf(m[nt][e], top), f = ex2(m[nt][e] - to), fo = f * turn;
-                        m[nt][e] = to;
-                        l[nt][e] *= f;
-#pragma unroll
-                        for (int q = 0; q < G; ++q)
-                            base[nt][e][q] *= f;
-#pragma unroll
-                        for (int n = 0; n < TILES; ++n) {
-                            o[nt][n][e] *= fo;
-                            o[nt][n][2 + e] *= fo;
-                        }
+                    for (int d = 4; d < 32; d <<= 1) {
+                        top[nt].x = fmaxf(top[nt].x, __shfl_xor_sync(0xffffffffu, top[nt].x, d));
+                        top[nt].y = fmaxf(top[nt].y, __shfl_xor_sync(0xffffffffu, top[nt].y, d));
                     }
+                    const float2 to = make_float2(fmaxf(m[nt].x, top[nt].x), fmaxf(m[nt].y, top[nt].y));
+                    const float2 f = make_float2(ex2(m[nt].x - to.x), ex2(m[nt].y - to.y)), fo = mul(f, both(turn));
+                    m[nt] = to;
+                    l[nt] = mul(l[nt], f);
+#pragma unroll
+                    for (int q = 0; q < G; ++q)
+                        base[nt][q] = mul(base[nt][q], f);
+#pragma unroll
+                    for (int n = 0; n < TILES; ++n) {
+                        o[nt][n][0] = mul(o[nt][n][0], fo);
+                        o[nt][n][1] = mul(o[nt][n][1], fo);
+                    }
+                }
             }
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float pe = ex2(x[u][nt][e] - m[nt][e & 1]);
-                        x[u][nt][e] = pe;
-                        l[nt][e & 1] += pe;
+                    for (int r = 0; r < 2; ++r) {
+                        const float2 y = sub(x[u][nt][r], m[nt]);
+                        const float2 pe = make_float2(ex2(y.x), ex2(y.y));
+                        x[u][nt][r] = pe;
+                        l[nt] = add(l[nt], pe);
 #pragma unroll
                         for (int q = 0; q < G; ++q)
-                            base[nt][e & 1][q] = fmaf(pe, va[u][e >> 1][q], base[nt][e & 1][q]);
+                            base[nt][q] = fma(pe, both(va[u][r][q]), base[nt][q]);
                     }
 
             // The value product, group by group.
@@ -500,12 +546,11 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
                     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
-                            const float f = vs[u][r][q] * up;
-                            const float a = x[u][nt][2 * r] * f, bb = x[u][nt][2 * r + 1] * f;
-                            const uint32_t h = pack2<false>(a, bb);
-                            const float2 back = unpack2<false>(h);
+                            const float2 a = mul(x[u][nt][r], both(vs[u][r][q] * up));
+                            const uint32_t h = pack2<false>(a.x, a.y);
+                            const float2 rest = sub(a, unpack2<false>(h));
                             hi[u][nt][r] = transpose8x8(h);
-                            lo[u][nt][r] = transpose8x8(pack2<false>(a - back.x, bb - back.y));
+                            lo[u][nt][r] = transpose8x8(pack2<false>(rest.x, rest.y));
                         }
                         constexpr uint32_t E = 0x80088008u, S = 0x80808080u; // -8 2^-24 and -8 2^-20, twice
                         if (u == 0)
@@ -530,17 +575,19 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
                             const uint32_t ml = 0x000f000fu, mh = 0x00f000f0u;
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
-                                float d[4] = {start[nt][0], start[nt][1], start[nt][2], start[nt][3]};
+                                float d[4];
 #pragma unroll
                                 for (int u = 0; u < 2; ++u) {
                                     const uint32_t a = w01[u] >> (8 * j), e = w23[u] >> (8 * j);
-                                    mma16816<false>(d, a & ml, a & mh, e & ml, e & mh, hi[u][nt][0], hi[u][nt][1]);
+                                    if (u == 0)
+                                        mma16816_from(d, a & ml, a & mh, e & ml, e & mh, hi[u][nt][0], hi[u][nt][1], start[nt]);
+                                    else
+                                        mma16816<false>(d, a & ml, a & mh, e & ml, e & mh, hi[u][nt][0], hi[u][nt][1]);
                                     mma16816<false>(d, a & ml, a & mh, e & ml, e & mh, lo[u][nt][0], lo[u][nt][1]);
                                 }
-                                float(&acc)[4] = o[nt][4 * blk + 2 * half + j];
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    acc[i] += d[i];
+                                float2(&acc)[2] = o[nt][4 * blk + 2 * half + j];
+                                acc[0] = add(acc[0], make_float2(d[0], d[1]));
+                                acc[1] = add(acc[1], make_float2(d[2], d[3]));
                             }
                         }
                     }
@@ -554,14 +601,15 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+            for (int d = 4; d < 32; d <<= 1) {
+                const auto lanes = [&](float2 v) {
+                    return add(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, d), __shfl_xor_sync(0xffffffffu, v.y, d)));
+                };
+                l[nt] = lanes(l[nt]);
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) {
-                    l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], d);
-#pragma unroll
-                    for (int q = 0; q < G; ++q)
-                        base[nt][e][q] += __shfl_xor_sync(0xffffffffu, base[nt][e][q], d);
-                }
+                for (int q = 0; q < G; ++q)
+                    base[nt][q] = lanes(base[nt][q]);
+            }
         __syncthreads();
         float *acc = reinterpret_cast<float *>(smem); // [warp][head][D]
         const float f_even = ref * (16777216.f / KV4_UP), f_odd = ref * (1048576.f / KV4_UP);
@@ -569,17 +617,18 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
+                const auto of = [e](float2 v) { return e ? v.y : v.x; };
                 float *mine = acc + (warp * M::HEADS + nt * 8 + 2 * t + e) * D + 8 * g;
 #pragma unroll
                 for (int n = 0; n < TILES; n += 2) { // values 2 n % 8 .. + 3 of block n / 4
-                    const float a = base[nt][e][n / 4 / PER];
-                    const float4 v = make_float4(fmaf(o[nt][n][e], f_even, a), fmaf(o[nt][n][2 + e], f_odd, a),
-                                                 fmaf(o[nt][n + 1][e], f_even, a), fmaf(o[nt][n + 1][2 + e], f_odd, a));
+                    const float a = of(base[nt][n / 4 / PER]);
+                    const float4 v = make_float4(fmaf(of(o[nt][n][0]), f_even, a), fmaf(of(o[nt][n][1]), f_odd, a),
+                                                 fmaf(of(o[nt][n + 1][0]), f_even, a), fmaf(of(o[nt][n + 1][1]), f_odd, a));
                     *reinterpret_cast<float4 *>(mine + 64 * (n / 4) + 2 * (n % 4)) = v;
                 }
                 if (g == 0) {
-                    stat[warp][nt * 8 + 2 * t + e][0] = m[nt][e];
-                    stat[warp][nt * 8 + 2 * t + e][1] = l[nt][e];
+                    stat[warp][nt * 8 + 2 * t + e][0] = of(m[nt]);
+                    stat[warp][nt * 8 + 2 * t + e][1] = of(l[nt]);
                 }
             }
         __syncthreads();
@@ -594,12 +643,14 @@ namespace {
 using Kv4Kernel = void (*)(Kv4AttParams);
 
 template <int D, int G, int NT>
-cudaError_t kv4_kernel(bool bf, Kv4Kernel &kernel, int &smem)
+cudaError_t kv4_kernel(bool bf, bool whole, Kv4Kernel &kernel, int &smem)
 {
-    static const Kv4Kernel kernels[2] = {kv4_attention_kernel<D, G, NT, false>, kv4_attention_kernel<D, G, NT, true>};
-    kernel = kernels[bf];
+    static const Kv4Kernel kernels[4] = {kv4_attention_kernel<D, G, NT, false, false>, kv4_attention_kernel<D, G, NT, false, true>,
+                                         kv4_attention_kernel<D, G, NT, true, false>, kv4_attention_kernel<D, G, NT, true, true>};
+    const int v = 2 * bf + whole;
+    kernel = kernels[v];
     smem = Kv4Geom<D, G, NT>::SMEM;
-    return allow_smem<Kv4Geom<D, G, NT>, 2>(reinterpret_cast<const void *>(kernel), bf, smem);
+    return allow_smem<Kv4Geom<D, G, NT>, 4>(reinterpret_cast<const void *>(kernel), v, smem);
 }
 
 constexpr int KV4_MAX_CTAS = 3;
@@ -720,19 +771,19 @@ extern "C" int w4a16_kv4_attention(const void *q, int ldq, const void *cache, lo
     p.page_magic = page_size == 1 ? 0 : (uint32_t)(((1ULL << (31 + s)) + page_size - 1) / page_size);
     p.page_shift = page_size == 1 ? 0 : s - 1;
 
-    const bool bf = (flags & W4A16_FLAG_BF16) != 0;
+    const bool bf = (flags & W4A16_FLAG_BF16) != 0, whole = page_size % 16 == 0;
     Kv4Kernel kernel;
     int smem;
     if (head_dim == 64)
-        err = heads == 8 ? kv4_kernel<64, 1, 1>(bf, kernel, smem) : kv4_kernel<64, 1, 2>(bf, kernel, smem);
+        err = heads == 8 ? kv4_kernel<64, 1, 1>(bf, whole, kernel, smem) : kv4_kernel<64, 1, 2>(bf, whole, kernel, smem);
     else if (head_dim == 128 && heads == 8)
-        err = groups == 1 ? kv4_kernel<128, 1, 1>(bf, kernel, smem) : kv4_kernel<128, 2, 1>(bf, kernel, smem);
+        err = groups == 1 ? kv4_kernel<128, 1, 1>(bf, whole, kernel, smem) : kv4_kernel<128, 2, 1>(bf, whole, kernel, smem);
     else if (head_dim == 128)
-        err = groups == 1 ? kv4_kernel<128, 1, 2>(bf, kernel, smem) : kv4_kernel<128, 2, 2>(bf, kernel, smem);
+        err = groups == 1 ? kv4_kernel<128, 1, 2>(bf, whole, kernel, smem) : kv4_kernel<128, 2, 2>(bf, whole, kernel, smem);
     else
-        err = groups == 1   ? kv4_kernel<256, 1, 1>(bf, kernel, smem)
-              : groups == 2 ? kv4_kernel<256, 2, 1>(bf, kernel, smem)
-                            : kv4_kernel<256, 4, 1>(bf, kernel, smem);
+        err = groups == 1   ? kv4_kernel<256, 1, 1>(bf, whole, kernel, smem)
+              : groups == 2 ? kv4_kernel<256, 2, 1>(bf, whole, kernel, smem)
+                            : kv4_kernel<256, 4, 1>(bf, whole, kernel, smem);
     if (err != cudaSuccess)
         return status_of(STAGE_RESOURCE, err);
     const int grid = num_sms * kv4_ctas(head_dim, heads);

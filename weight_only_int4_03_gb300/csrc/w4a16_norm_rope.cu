@@ -125,13 +125,6 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return r;
 }
 
-// Pairs of fp32 numbers: one instruction for two, each rounded by itself and never joined with another.
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-__device__ __forceinline__ float2 add(float2 a, float2 b) { return __fadd2_rn(a, b); }
-__device__ __forceinline__ float2 mul(float2 a, float2 b) { return __fmul2_rn(a, b); }
-__device__ __forceinline__ float2 fma(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
-__device__ __forceinline__ float2 sub(float2 a, float2 b) { return __ffma2_rn(b, both(-1.f), a); }
-
 // A value in two parts, hi + lo, the second below half a unit of the first (or a few of them).
 struct Two {
     float hi, lo;

@@ -40,6 +40,7 @@ struct SplitShared {
 struct SplitSegment {
     long long row_u0; // number of the row's unit 0
     int b, row, first, len;
+    int start; // of unit 0: first, or the multiple of a unit before it
     int unit0, unit1, units;
     bool more; // another segment of this block may follow
 };
@@ -85,7 +86,8 @@ __device__ __forceinline__ int split_quotient(long long a, long long b, bool sma
     return small ? (int)((uint32_t)a / (uint32_t)b) : (int)(a / b);
 }
 
-template <int UNIT, int COST>
+// ALIGNED: units begin at multiples of their size in the sequence, so that the first may hold positions before `first`.
+template <int UNIT, int COST, bool ALIGNED>
 struct Split {
     const SplitParams &p;
     SplitShared &s;
@@ -103,6 +105,8 @@ struct Split {
         }
         first = p.window > 0 && len > p.window ? len - p.window : 0;
     }
+
+    static __device__ __forceinline__ int start_of(int first) { return ALIGNED ? first / UNIT * UNIT : first; }
 
     __device__ __forceinline__ long long begin_of(int c) const
     {
@@ -127,7 +131,7 @@ struct Split {
             if (b < p.batch) {
                 int first, len;
                 live_range(b, first, len);
-                n = (len - first + UNIT - 1) / UNIT;
+                n = (len - start_of(first) + UNIT - 1) / UNIT;
                 n += n > 0 ? COST : 0;
             }
             int incl = n;
@@ -191,6 +195,7 @@ struct Split {
         if (seg.unit1 <= seg.unit0)
             return false; // the range ends before the row's first unit
         live_range(lo, seg.first, seg.len);
+        seg.start = start_of(seg.first);
         return true;
     }
 
