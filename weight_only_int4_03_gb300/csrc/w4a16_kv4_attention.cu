@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
     using M = Kv4Geom<D, G, NT>;
     constexpr int BLOCKS = M::BLOCKS, TILES = 4 * BLOCKS; // 16-wide tiles of the output dims
     constexpr int PER = BLOCKS / G;                       // blocks of 64 per group
+    constexpr bool REST = !BF;                            // p s goes in with a remainder
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ SplitShared shared;
     __shared__ float stat[SPLIT_WARPS][M::HEADS][2];
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
                 }
 #pragma unroll
                 for (int q = 0; q < G; ++q) {
-                    float acc[NT][4];
+                    float acc[NT][4], acc2[NT][4]; // two chains of sums
 #pragma unroll
                     for (int k = 0; k < PER; ++k)
 #pragma unroll
@@ -431,18 +432,22 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
                                 const uint32_t *f = qf[nt][blk][i];
-                                if (k == 0 && i == 0)
+                                if (k == 0 && i == 0) {
                                     mma16816_zero<false>(acc[nt], w0 & lo, w1 & lo, v0 & lo, v1 & lo, f[0], f[1]);
-                                else
+                                    mma16816_zero<false>(acc2[nt], w0 & hi, w1 & hi, v0 & hi, v1 & hi, f[2], f[3]);
+                                } else {
                                     mma16816<false>(acc[nt], w0 & lo, w1 & lo, v0 & lo, v1 & lo, f[0], f[1]);
-                                mma16816<false>(acc[nt], w0 & hi, w1 & hi, v0 & hi, v1 & hi, f[2], f[3]);
+                                    mma16816<false>(acc2[nt], w0 & hi, w1 & hi, v0 & hi, v1 & hi, f[2], f[3]);
+                                }
                             }
                         }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
-                            const float2 sum = mul(make_float2(acc[nt][2 * r], acc[nt][2 * r + 1]), both(ks[r][q]));
+                            const float2 sum = mul(add(make_float2(acc[nt][2 * r], acc[nt][2 * r + 1]),
+                                                       make_float2(acc2[nt][2 * r], acc2[nt][2 * r + 1])),
+                                                   both(ks[r][q]));
                             const float2 y = fma(sum, fac[nt], mul(both(ka[r][q]), qs[nt][q]));
                             x[u][nt][r] = q == 0 ? y : add(x[u][nt][r], y);
                         }
@@ -548,16 +553,19 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
                         for (int r = 0; r < 2; ++r) {
                             const float2 a = mul(x[u][nt][r], both(vs[u][r][q] * up));
                             const uint32_t h = pack2<false>(a.x, a.y);
-                            const float2 rest = sub(a, unpack2<false>(h));
                             hi[u][nt][r] = transpose8x8(h);
-                            lo[u][nt][r] = transpose8x8(pack2<false>(rest.x, rest.y));
+                            if (REST) {
+                                const float2 rest = sub(a, unpack2<false>(h));
+                                lo[u][nt][r] = transpose8x8(pack2<false>(rest.x, rest.y));
+                            }
                         }
                         constexpr uint32_t E = 0x80088008u, S = 0x80808080u; // -8 2^-24 and -8 2^-20, twice
                         if (u == 0)
                             mma16816_zero<false>(start[nt], E, S, E, S, hi[u][nt][0], hi[u][nt][1]);
                         else
                             mma16816<false>(start[nt], E, S, E, S, hi[u][nt][0], hi[u][nt][1]);
-                        mma16816<false>(start[nt], E, S, E, S, lo[u][nt][0], lo[u][nt][1]);
+                        if (REST)
+                            mma16816<false>(start[nt], E, S, E, S, lo[u][nt][0], lo[u][nt][1]);
                     }
 #pragma unroll
                 for (int k = 0; k < PER; ++k) {
@@ -583,7 +591,8 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
                                         mma16816_from(d, a & ml, a & mh, e & ml, e & mh, hi[u][nt][0], hi[u][nt][1], start[nt]);
                                     else
                                         mma16816<false>(d, a & ml, a & mh, e & ml, e & mh, hi[u][nt][0], hi[u][nt][1]);
-                                    mma16816<false>(d, a & ml, a & mh, e & ml, e & mh, lo[u][nt][0], lo[u][nt][1]);
+                                    if (REST)
+                                        mma16816<false>(d, a & ml, a & mh, e & ml, e & mh, lo[u][nt][0], lo[u][nt][1]);
                                 }
                                 float2(&acc)[2] = o[nt][4 * blk + 2 * half + j];
                                 acc[0] = add(acc[0], make_float2(d[0], d[1]));
