@@ -33,8 +33,6 @@
 namespace w4 {
 namespace ops {
 
-constexpr int KV4_STEP = 32;                           // positions per warp and step
-constexpr int KV4_UNIT = SPLIT_WARPS * KV4_STEP;       // positions per work unit
 constexpr float KV4_UP = 8192.f;                       // what p s / reference is multiplied by for the value product
 constexpr float KV4_LAZY = 2.f;                        // by how much (log2) a score may pass the maximum
 
@@ -62,9 +60,14 @@ struct Kv4Geom {
     static constexpr int KEYS = 16 * ROW;              // a sub-step's keys, and as many bytes of values
     static constexpr int PARAMS = 16 * 4 * G;          // a sub-step's steps and bases of one side
     static constexpr int SUB = 2 * KEYS + 2 * PARAMS;
-    static constexpr int STAGE = 2 * SUB;
-    static constexpr int STAGES = D == 256 ? 2 : 3;    // three of 256-wide rows leave room for one block
-    static constexpr int CTAS = D * NT > 128 ? 2 : 3;  // blocks per SM
+    // Sub-steps of 16 positions that a warp takes at once: what a step costs by itself (pages, the vote, adding up the
+    // outputs) is shared by them, and more of them are in one another's shadow, as far as the registers go.
+    static constexpr int SUBS = D == 128 && NT == 1 ? 4 : 2;
+    static constexpr int STEP = 16 * SUBS;
+    static constexpr int UNIT = SPLIT_WARPS * STEP;    // positions per work unit: a step of each warp
+    static constexpr int STAGE = SUBS * SUB;
+    static constexpr int STAGES = D == 256 || SUBS == 4 ? 2 : 3; // (shared memory for two blocks at least)
+    static constexpr int CTAS = D * NT > 64 ? 2 : 3;   // blocks per SM
     static constexpr int ROW_COST = 4;                 // of a row by itself, in units
     static constexpr int HEADS = 8 * NT;
     static constexpr int SMEM = SPLIT_WARPS * STAGES * STAGE > SPLIT_WARPS * HEADS * D * 4 ? SPLIT_WARPS * STAGES * STAGE
@@ -165,13 +168,13 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
     __shared__ SplitShared shared;
     __shared__ float stat[SPLIT_WARPS][M::HEADS][2];
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31; // (warp: the same in all lanes)
     const int g = lane >> 2, t = lane & 3;
     const int row_of = (g >> 1) + 4 * (g & 1); // the position of the eight that is row g of the score product
     pdl_wait();
     pdl_launch_dependents();
 
-    Split<KV4_UNIT, M::ROW_COST, true> split(p.split, shared);
+    Split<M::UNIT, M::ROW_COST, true> split(p.split, shared);
     // Sequences without a position: zeros and -inf.
     for (int b = blockIdx.x; b < p.split.batch; b += gridDim.x) {
         if (!split.empty(b))
@@ -189,42 +192,45 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
         const int b = seg.b, c = seg.row / p.tiles, h0 = (seg.row - c * p.tiles) * M::HEADS;
         const int nh = min(M::HEADS, p.group - h0); // heads of this tile
         const int first = seg.first, len = seg.len, steps = seg.unit1 - seg.unit0;
-        const int pos0 = seg.start + seg.unit0 * KV4_UNIT + warp * KV4_STEP; // this warp's first position
+        const int pos0 = seg.start + seg.unit0 * M::UNIT + warp * M::STEP; // this warp's first position
 
         // --- copies ---------------------------------------------------------------------------
-        // A lane looks after positions row_of + 8 i, i < 4, of a step.  Pages are looked up one step before they are used:
-        // those of the two sub-steps, or of each lane's four positions.
-        constexpr int LOOK = WHOLE ? 2 : 4;
+        // A lane looks after positions row_of + 8 i, i < 2 SUBS, of a step.  Pages are looked up one step before they are used:
+        // those of the sub-steps, or of each lane's positions.
+        constexpr int SUBS = M::SUBS, LOOK = WHOLE ? SUBS : 2 * SUBS;
         const int32_t *tab = p.table + (long long)b * p.ld_table;
         const uint8_t *head = p.cache + c * p.rec.bytes;
         int next_page[LOOK], next_token[LOOK];
         auto look_up = [&](int step) {
 #pragma unroll
             for (int i = 0; i < LOOK; ++i) {
-                const int pos = pos0 + step * KV4_UNIT + (WHOLE ? 16 * i : row_of + 8 * i);
+                const int pos = pos0 + step * M::UNIT + (WHOLE ? 16 * i : row_of + 8 * i);
                 const bool in = step < steps && pos < len && (WHOLE ? pos + 16 > first : pos >= first);
                 const int at = p.page_magic ? (int)(__umulhi((uint32_t)pos, p.page_magic) >> p.page_shift) : pos;
                 next_page[i] = in ? tab[at] : -1;
                 next_token[i] = pos - at * p.page;
             }
         };
-        // What is live of the steps in flight, the newest in the lowest five bits: this lane's positions, and whether all
-        // of the step is.
+        // What is live of the steps in flight, the newest in the lowest bits: this lane's positions, and above them whether
+        // all of the step is.
         uint32_t flight = 0;
         auto issue = [&](int step, int stage) {
-            flight <<= 5;
+            flight <<= 2 * SUBS + 1;
             if (step >= steps)
                 return;
-            const int pos = pos0 + step * KV4_UNIT;
+            const int pos = pos0 + step * M::UNIT;
             const uint32_t st = ring + stage * M::STAGE;
             constexpr int HALVES = D / 128; // 16-byte chunks of a lane in a row
-            if (WHOLE && pos >= first && pos + KV4_STEP <= len && (uint32_t)next_page[0] < (uint32_t)p.n_pages &&
-                (uint32_t)next_page[LOOK / 2] < (uint32_t)p.n_pages) {
-                flight |= 31;
+            bool fine = WHOLE && pos >= first && pos + M::STEP <= len;
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const uint8_t *rec = head + (long long)next_page[u * LOOK / 2 % LOOK] * p.page_stride;
-                    const int token = next_token[u * LOOK / 2 % LOOK] + row_of;
+            for (int u = 0; u < (WHOLE ? SUBS : 0); ++u)
+                fine = fine && (uint32_t)next_page[u] < (uint32_t)p.n_pages;
+            if (fine) {
+                flight |= (2u << 2 * SUBS) - 1;
+#pragma unroll
+                for (int u = 0; u < SUBS; ++u) {
+                    const uint8_t *rec = head + (long long)next_page[u % LOOK] * p.page_stride;
+                    const int token = next_token[u % LOOK] + row_of;
                     const uint8_t *keys = rec + (long long)token * M::ROW + (D == 64 ? 8 : 16) * t, *values = keys + p.rec.values;
                     const uint32_t sub = st + u * M::SUB;
                     const uint32_t key_to = sub + lane * (D == 64 ? 8 : 16), value_to = sub + M::KEYS + row_of * M::ROW;
@@ -249,11 +255,11 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
                 }
                 return;
             }
-            const uint8_t *rec[4];
+            const uint8_t *rec[2 * SUBS];
             uint32_t bits = 0;
-            int token[4];
+            int token[2 * SUBS];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2 * SUBS; ++i) {
                 const int at = pos + row_of + 8 * i, page = next_page[WHOLE ? i / 2 : i];
                 const bool in = at >= first && at < len, ok = in && page >= 0 && page < p.n_pages;
                 if (in && !ok)
@@ -264,7 +270,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
             }
             flight |= bits;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2 * SUBS; ++i) {
                 const int r = i & 1, row = row_of + 8 * r;
                 const uint32_t sub = st + (i >> 1) * M::SUB;
                 const bool ok = (bits >> i) & 1u;
@@ -282,7 +288,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
                 }
             }
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < SUBS; ++u) {
                 const int i = 2 * u + (t & 1);
                 const bool ok = (bits >> i) & 1u;
                 const uint8_t *src = (t & 1 ? rec[2 * u + 1] : rec[2 * u]) + (t >> 1 ? p.rec.value_params : p.rec.key_params) +
@@ -373,7 +379,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
         for (int step = 0; step < steps; ++step) {
             cp_async_wait<M::STAGES - 2>();
             __syncwarp(); // every lane's copies of this stage have landed; the next one is free
-            const uint32_t live = flight >> (5 * (M::STAGES - 2));
+            const uint32_t live = flight >> ((2 * SUBS + 1) * (M::STAGES - 2));
             {
                 int ns = stage + M::STAGES - 1;
                 ns = ns >= M::STAGES ? ns - M::STAGES : ns;
@@ -384,10 +390,10 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
             const uint32_t st = ring + stage * M::STAGE;
 
             // Scores x[sub-step][tile][row] of positions row_of + 16 u (+ 8).
-            float2 x[2][NT][2];
-            float vs[2][2][G], va[2][2][G];
+            float2 x[SUBS][NT][2];
+            float vs[SUBS][2][G], va[SUBS][2][G];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < SUBS; ++u) {
                 const uint32_t sub = st + u * M::SUB;
                 uint32_t kw[2][BLOCKS * 2];
 #pragma unroll
@@ -453,9 +459,9 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
                         }
                 }
             }
-            if (!(live & 16u)) {
+            if (!((live >> 2 * SUBS) & 1u)) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+                for (int u = 0; u < SUBS; ++u)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -467,14 +473,20 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
             // Does a maximum or the reference of the value steps have to move?  (A NaN does not move anything.)
             float step_top = ref;
 #pragma unroll
-            for (int q = 0; q < G; ++q)
-                step_top = fmaxf(step_top, fmaxf(fmaxf(vs[0][0][q], vs[0][1][q]), fmaxf(vs[1][0][q], vs[1][1][q])));
+            for (int u = 0; u < SUBS; ++u)
+#pragma unroll
+                for (int q = 0; q < G; ++q)
+                    step_top = fmaxf(step_top, fmaxf(vs[u][0][q], vs[u][1][q]));
             bool moves = step_top > ref;
             float2 top[NT];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                top[nt].x = fmaxf(fmaxf(x[0][nt][0].x, x[0][nt][1].x), fmaxf(x[1][nt][0].x, x[1][nt][1].x));
-                top[nt].y = fmaxf(fmaxf(x[0][nt][0].y, x[0][nt][1].y), fmaxf(x[1][nt][0].y, x[1][nt][1].y));
+                top[nt] = both(-INFINITY);
+#pragma unroll
+                for (int u = 0; u < SUBS; ++u) {
+                    top[nt].x = fmaxf(top[nt].x, fmaxf(x[u][nt][0].x, x[u][nt][1].x));
+                    top[nt].y = fmaxf(top[nt].y, fmaxf(x[u][nt][0].y, x[u][nt][1].y));
+                }
                 const float2 over = sub(top[nt], m[nt]);
                 moves |= over.x > KV4_LAZY || over.y > KV4_LAZY;
             }
@@ -512,7 +524,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
                 }
             }
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < SUBS; ++u)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -527,9 +539,9 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
                     }
 
             // The value product, group by group.
-            uint32_t vw[2][4][BLOCKS]; // words of positions t, t + 4, t + 8, t + 12 of a sub-step
+            uint32_t vw[SUBS][4][BLOCKS]; // words of positions t, t + 4, t + 8, t + 12 of a sub-step
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < SUBS; ++u)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int row = t + 4 * e;
@@ -543,10 +555,10 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
                 }
 #pragma unroll
             for (int q = 0; q < G; ++q) {
-                uint32_t hi[2][NT][2], lo[2][NT][2];
+                uint32_t hi[SUBS][NT][2], lo[SUBS][NT][2];
                 float start[NT][4]; // -8 sum p s, as the codes' rows are scaled
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+                for (int u = 0; u < SUBS; ++u)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -572,9 +584,9 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
                     const int blk = q * PER + k;
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        uint32_t w01[2], w23[2]; // codes 4 half .. 4 half + 3 of two positions each
+                        uint32_t w01[SUBS], w23[SUBS]; // codes 4 half .. 4 half + 3 of two positions each
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
+                        for (int u = 0; u < SUBS; ++u) {
                             w01[u] = __byte_perm(vw[u][0][blk], vw[u][1][blk], half ? 0x7632 : 0x5410);
                             w23[u] = __byte_perm(vw[u][2][blk], vw[u][3][blk], half ? 0x7632 : 0x5410);
                         }
@@ -585,7 +597,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
                             for (int nt = 0; nt < NT; ++nt) {
                                 float d[4];
 #pragma unroll
-                                for (int u = 0; u < 2; ++u) {
+                                for (int u = 0; u < SUBS; ++u) {
                                     const uint32_t a = w01[u] >> (8 * j), e = w23[u] >> (8 * j);
                                     if (u == 0)
                                         mma16816_from(d, a & ml, a & mh, e & ml, e & mh, hi[u][nt][0], hi[u][nt][1], start[nt]);
@@ -672,12 +684,10 @@ int kv4_heads(int head_dim, int group)
 
 int kv4_ctas(int head_dim, int heads)
 {
-    return head_dim == 256 || head_dim * heads > 1024 ? 2 : 3;
+    return head_dim == 64    ? heads == 8 ? Kv4Geom<64, 1, 1>::CTAS : Kv4Geom<64, 1, 2>::CTAS
+           : head_dim == 128 ? heads == 8 ? Kv4Geom<128, 1, 1>::CTAS : Kv4Geom<128, 1, 2>::CTAS
+                             : Kv4Geom<256, 1, 1>::CTAS;
 }
-static_assert(Kv4Geom<64, 1, 1>::CTAS == 3 && Kv4Geom<64, 1, 2>::CTAS == 3 && Kv4Geom<128, 1, 1>::CTAS == 3 &&
-                  Kv4Geom<128, 1, 2>::CTAS == 2 && Kv4Geom<256, 1, 1>::CTAS == 2,
-              "kv4_ctas");
-
 SplitLayout kv4_layout(int head_dim, int heads, int num_sms)
 {
     return split_layout((long long)num_sms * KV4_MAX_CTAS, (long long)num_sms * kv4_ctas(head_dim, heads),
@@ -745,8 +755,8 @@ extern "C" int w4a16_kv4_attention(const void *q, int ldq, const void *cache, lo
     // Positions and units are counted in 32 bits (offsets into the cache in 64): a sequence holds
     // at most max_pages pages.
     const long long max_len = (long long)max_pages * page_size;
-    if (max_len > 0x7FFFFFFFLL - 64 * KV4_UNIT ||
-        ((max_len + KV4_UNIT - 1) / KV4_UNIT + 8) * batch > 0x7FFFFFFFLL)
+    constexpr int UNIT = Kv4Geom<64, 1, 1>::UNIT; // the smallest
+    if (max_len > 0x7FFFFFFFLL - 64 * UNIT || ((max_len + UNIT - 1) / UNIT + 8) * batch > 0x7FFFFFFFLL)
         return status_of(STAGE_ARG, W4A16_ARG_OVERFLOW);
 
     int num_sms = 0;
