@@ -61,12 +61,5 @@ __device__ __forceinline__ int kv4_value_place(int word, int blocks)
     return (word & 7) * blocks + (word >> 3);
 }
 
-// Pairs of fp32 numbers: one instruction for two, each rounded by itself and never joined with another.
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-__device__ __forceinline__ float2 add(float2 a, float2 b) { return __fadd2_rn(a, b); }
-__device__ __forceinline__ float2 mul(float2 a, float2 b) { return __fmul2_rn(a, b); }
-__device__ __forceinline__ float2 fma(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
-__device__ __forceinline__ float2 sub(float2 a, float2 b) { return __ffma2_rn(b, both(-1.f), a); }
-
 } // namespace ops
 } // namespace w4

@@ -8,14 +8,15 @@
 //
 // Where sums decide (which token's share holds u, where top-p ends), rounding would show: P is therefore a 64-bit
 // integer, a multiple of 2^-43 good to 2^-30 of itself, and all sums are exact, in whatever order they are
-// taken.  So results do not depend on the split, and atomics do no harm.  P comes from a table of 2^(-j/64) and a
+// taken.  So results do not depend on the split, and atomics do no harm.  P comes from a table of 2^(-j/256) and a
 // polynomial for the rest (the table-driven exponential of Tang, 1989); (l - max) / T is kept in two fp32 parts.
 //
 // A cluster of up to eight blocks holds a row: the logits are read from memory once, as 16-bit keys in
 // their order, and stay in shared memory.  The threshold is found by the keys' high bytes and then the low bytes of
-// one of them (256-bin histograms of counts and sums); blocks read one another's bins.  Last, each warp sums
-// its own range of indices, and the warp whose range holds u walks it.  What bounds it: for few rows the chain of
-// cluster barriers, for many the instructions per logit (P twice, histogram atomics).
+// one of them (256-bin histograms of counts and sums); blocks read one another's bins.  Top-k looks only at keys not below
+// the k-th largest of the threads' largest ones, of which there are few.  Last, each warp sums its own range of indices,
+// and the warp whose range holds u walks it; below the threshold no P is computed.  What bounds it: for few rows
+// the chain of cluster barriers, for many the instructions per logit (about thirty for a P).
 #include <cooperative_groups.h>
 
 #include "w4a16_ops.cuh"
@@ -31,17 +32,45 @@ constexpr int SAMPLE_CLUSTER = 8;      // blocks of a row, at most
 constexpr int SAMPLE_SLICE = 65536;    // logits of a block, at most (a bin's sums of 32-bit parts rely on it)
 constexpr int SAMPLE_BITS = 43;        // P = 1 is 2^43: 2^19 tokens sum below 2^62
 constexpr int SAMPLE_COPIES = 4;       // of a histogram, against lanes that meet at a bin
+constexpr int SAMPLE_TABLE = 256;
+constexpr float SAMPLE_ROUND = 12582912.f; // rounds what is added to it to integers (ties to even), in its lowest bits
+constexpr uint32_t SAMPLE_ROUND_BITS = 0x4B400000u;
+constexpr float SAMPLE_HOTTEST = 0x1p100f; // temperature, at most
 
-// 2^31 2^(-j/64).
-__constant__ uint32_t SAMPLE_EXP[64] = {
-    2147483648u, 2124350982u, 2101467502u, 2078830522u, 2056437387u, 2034285470u, 2012372174u, 1990694927u,
-    1969251188u, 1948038440u, 1927054196u, 1906295993u, 1885761398u, 1865448001u, 1845353420u, 1825475297u,
-    1805811301u, 1786359126u, 1767116489u, 1748081133u, 1729250827u, 1710623359u, 1692196547u, 1673968228u,
-    1655936265u, 1638098541u, 1620452965u, 1602997467u, 1585730000u, 1568648537u, 1551751076u, 1535035634u,
-    1518500250u, 1502142985u, 1485961921u, 1469955159u, 1454120821u, 1438457051u, 1422962010u, 1407633882u,
-    1392470869u, 1377471191u, 1362633090u, 1347954824u, 1333434672u, 1319070932u, 1304861917u, 1290805962u,
-    1276901417u, 1263146652u, 1249540052u, 1236080024u, 1222764986u, 1209593378u, 1196563654u, 1183674286u,
-    1170923762u, 1158310587u, 1145833280u, 1133490379u, 1121280436u, 1109202018u, 1097253708u, 1085434106u,
+// 2^31 2^(-j/256).
+__device__ const uint32_t SAMPLE_EXP[SAMPLE_TABLE] = {
+    2147483648u, 2141676973u, 2135885998u, 2130110682u, 2124350982u, 2118606857u, 2112878262u, 2107165158u,
+    2101467502u, 2095785251u, 2090118366u, 2084466803u, 2078830522u, 2073209480u, 2067603638u, 2062012954u,
+    2056437387u, 2050876895u, 2045331439u, 2039800978u, 2034285470u, 2028784876u, 2023299156u, 2017828268u,
+    2012372174u, 2006930832u, 2001504204u, 1996092249u, 1990694927u, 1985312200u, 1979944027u, 1974590370u,
+    1969251188u, 1963926443u, 1958616096u, 1953320108u, 1948038440u, 1942771053u, 1937517909u, 1932278970u,
+    1927054196u, 1921843549u, 1916646992u, 1911464486u, 1906295993u, 1901141476u, 1896000896u, 1890874216u,
+    1885761398u, 1880662405u, 1875577199u, 1870505744u, 1865448001u, 1860403934u, 1855373507u, 1850356681u,
+    1845353420u, 1840363688u, 1835387448u, 1830424663u, 1825475297u, 1820539314u, 1815616678u, 1810707353u,
+    1805811301u, 1800928489u, 1796058879u, 1791202437u, 1786359126u, 1781528911u, 1776711757u, 1771907628u,
+    1767116489u, 1762338305u, 1757573041u, 1752820662u, 1748081133u, 1743354420u, 1738640488u, 1733939301u,
+    1729250827u, 1724575029u, 1719911875u, 1715261330u, 1710623359u, 1705997930u, 1701385007u, 1696784557u,
+    1692196547u, 1687620943u, 1683057710u, 1678506817u, 1673968228u, 1669441912u, 1664927835u, 1660425963u,
+    1655936265u, 1651458706u, 1646993254u, 1642539877u, 1638098541u, 1633669214u, 1629251865u, 1624846459u,
+    1620452965u, 1616071351u, 1611701585u, 1607343634u, 1602997467u, 1598663052u, 1594340357u, 1590029350u,
+    1585730000u, 1581442275u, 1577166143u, 1572901575u, 1568648537u, 1564406999u, 1560176931u, 1555958300u,
+    1551751076u, 1547555228u, 1543370725u, 1539197537u, 1535035634u, 1530884983u, 1526745556u, 1522617322u,
+    1518500250u, 1514394310u, 1510299473u, 1506215708u, 1502142985u, 1498081275u, 1494030547u, 1489990772u,
+    1485961921u, 1481943963u, 1477936870u, 1473940611u, 1469955159u, 1465980482u, 1462016553u, 1458063343u,
+    1454120821u, 1450188960u, 1446267730u, 1442357104u, 1438457051u, 1434567544u, 1430688553u, 1426820052u,
+    1422962010u, 1419114401u, 1415277195u, 1411450365u, 1407633882u, 1403827719u, 1400031848u, 1396246240u,
+    1392470869u, 1388705706u, 1384950723u, 1381205894u, 1377471191u, 1373746586u, 1370032052u, 1366327563u,
+    1362633090u, 1358948606u, 1355274085u, 1351609500u, 1347954824u, 1344310030u, 1340675091u, 1337049980u,
+    1333434672u, 1329829140u, 1326233356u, 1322647296u, 1319070932u, 1315504238u, 1311947188u, 1308399756u,
+    1304861917u, 1301333643u, 1297814910u, 1294305692u, 1290805962u, 1287315695u, 1283834865u, 1280363448u,
+    1276901417u, 1273448747u, 1270005413u, 1266571390u, 1263146652u, 1259731174u, 1256324931u, 1252927899u,
+    1249540052u, 1246161366u, 1242791816u, 1239431376u, 1236080024u, 1232737732u, 1229404479u, 1226080238u,
+    1222764986u, 1219458698u, 1216161350u, 1212872918u, 1209593378u, 1206322705u, 1203060876u, 1199807867u,
+    1196563654u, 1193328213u, 1190101520u, 1186883552u, 1183674286u, 1180473697u, 1177281762u, 1174098458u,
+    1170923762u, 1167757650u, 1164600099u, 1161451085u, 1158310587u, 1155178580u, 1152055042u, 1148939949u,
+    1145833280u, 1142735011u, 1139645120u, 1136563583u, 1133490379u, 1130425485u, 1127368878u, 1124320536u,
+    1121280436u, 1118248556u, 1115224875u, 1112209370u, 1109202018u, 1106202798u, 1103211687u, 1100228665u,
+    1097253708u, 1094286796u, 1091327906u, 1088377016u, 1085434106u, 1082499153u, 1079572136u, 1076653033u,
 };
 
 struct SampleParams {
@@ -56,7 +85,7 @@ struct SampleParams {
 };
 
 struct SampleShared {
-    uint32_t exp[64];
+    uint2 exp[SAMPLE_TABLE]; // 2^31 2^(-j/256) as an integer (less SAMPLE_ROUND_BITS) and as a number
     uint32_t count[256 * SAMPLE_COPIES], low[256 * SAMPLE_COPIES], high[256 * SAMPLE_COPIES];
     // This block's bins, read by the cluster's other blocks; two sets in turn, so that a set is written again only
     // after a barrier which all of its readers have reached.
@@ -90,11 +119,12 @@ __device__ __forceinline__ uint32_t keys_of(uint32_t w)
     return w ^ (negative | 0x80008000u);
 }
 
+// Two keys' numbers.
 template <bool BF>
-__device__ __forceinline__ float number_of(uint32_t key)
+__device__ __forceinline__ float2 numbers_of(uint32_t keys)
 {
-    const uint32_t w = key & 0x8000u ? key ^ 0x8000u : ~key & 0xFFFFu;
-    return to_float<BF>((uint16_t)w);
+    const uint32_t negative = (~keys >> 15 & 0x00010001u) * 0xFFFFu;
+    return unpack2<BF>(keys ^ (negative | 0x80008000u));
 }
 
 template <bool BF>
@@ -103,31 +133,54 @@ __device__ __forceinline__ constexpr uint32_t lowest_key() // of -inf
     return BF ? 0x007Fu : 0x03FFu;
 }
 
-// P of a logit, in units of 2^-43.
+// P of logits, in units of 2^-43.
 template <bool BF>
 struct Share {
-    float top, c_hi, c_lo; // the largest logit; log2(e) / T in two parts
-    const uint32_t *exp;
+    float top, c_hi, c_lo; // the largest logit (finite); log2(e) / T in two parts
+    const uint2 *exp;
+
+    // 2^-y, y = n + j / 256 + a rest: kk holds n and j, z the rest times ln 2 (at most ln 2 / 512), fine: y < 44.5.
+    __device__ __forceinline__ unsigned long long scaled(float kk, float z, bool fine) const
+    {
+        const uint32_t k = __float_as_uint(kk) - SAMPLE_ROUND_BITS;
+        const uint2 e = exp[k & (SAMPLE_TABLE - 1)];
+        const float q = z * fmaf(z, fmaf(z, -1.f / 6.f, 0.5f), -1.f); // e^-z - 1, to z^4 / 24 < 2^-42
+        const uint32_t v = e.x + __float_as_uint(fmaf(__uint_as_float(e.y), q, SAMPLE_ROUND)); // 2^31 2^(n - y)
+        const uint32_t n = k / SAMPLE_TABLE;
+        // v 2^(12 - n), rounded where that is a shift to the right.
+        const unsigned long long large = (unsigned long long)v << ((12 - n) & 31);
+        const uint32_t small = (uint32_t)(((unsigned long long)v << ((44 - n) & 31)) + 0x80000000u >> 32);
+        return !fine ? 0 : n <= 12 ? large : small;
+    }
+
+    __device__ __forceinline__ void operator()(uint32_t keys, unsigned long long &first, unsigned long long &second) const
+    {
+        const float2 l = numbers_of<BF>(keys), t = both(top);
+        const float2 d = sub(t, l), rest = sub(sub(t, d), l); // d + rest is the difference
+        const float2 y = mul(d, both(c_hi));
+        const float2 y_lo = add(fma(d, both(c_hi), make_float2(-y.x, -y.y)), fma(d, both(c_lo), mul(rest, both(c_hi))));
+        const float2 kk = fma(y, both((float)SAMPLE_TABLE), both(SAMPLE_ROUND)), k = add(kk, both(-SAMPLE_ROUND));
+        const float2 z = mul(add(fma(k, both(-1.f / SAMPLE_TABLE), y), y_lo), both(0.6931471805599453f));
+        first = scaled(kk.x, z.x, y.x < 44.5f);
+        second = scaled(kk.y, z.y, y.y < 44.5f);
+    }
 
     __device__ __forceinline__ unsigned long long operator()(uint32_t key) const
     {
-        const float l = number_of<BF>(key);
-        if (l == top)
-            return 1ULL << SAMPLE_BITS;
-        const float d = top - l, rest = (top - d) - l; // d + rest is the difference
-        const float y = d * c_hi;
-        if (!(y < (float)SAMPLE_BITS + 1.f))
-            return 0;
-        const float y_lo = fmaf(d, c_hi, -y) + fmaf(d, c_lo, rest * c_hi);
-        const float k = rintf(y * 64.f);
-        const float z = (fmaf(k, -0.015625f, y) + y_lo) * 0.6931471805599453f; // at most ln 2 / 128
-        const float q = z * fmaf(z, fmaf(z, fmaf(z, 1.f / 24.f, -1.f / 6.f), 0.5f), -1.f); // e^-z - 1
-        const int n = (int)k >> 6;
-        const uint32_t t = exp[(int)k & 63];
-        const uint32_t v = t + (uint32_t)__float2int_rn((float)t * q); // 2^31 2^n P
-        return n <= 12 ? (unsigned long long)v << (12 - n) : ((unsigned long long)v + (1ULL << (n - 13))) >> (n - 12);
+        unsigned long long p, ignored;
+        (*this)(key * 0x10001u, p, ignored);
+        return p;
     }
 };
+
+// A number in [0, 1) as a multiple of 2^-64, cut off (0 for those below 0).
+__device__ __forceinline__ unsigned long long fraction(float x)
+{
+    const uint32_t bits = __float_as_uint(x);
+    const int e = (int)(bits >> 23);
+    const unsigned long long m = (bits & 0x7FFFFFu) | 0x800000u; // x = m 2^(e - 150)
+    return !(x > 0.f) || e <= 86 - 24 ? 0 : e >= 86 ? m << min(e - 86, 40) : m >> (86 - e);
+}
 
 // Adds `sum` to a bin's 64-bit sum of two 32-bit halves.
 __device__ __forceinline__ void add_sum(uint32_t *low, uint32_t *high, unsigned long long sum)
@@ -136,6 +189,13 @@ __device__ __forceinline__ void add_sum(uint32_t *low, uint32_t *high, unsigned 
     const uint32_t carry = (uint32_t)(sum >> 32) + (old + a < a ? 1u : 0u);
     if (carry)
         atomicAdd(high, carry);
+}
+
+// The largest of eight keys.
+__device__ __forceinline__ uint32_t largest(const uint4 &k)
+{
+    const uint32_t m = __vmaxu2(__vmaxu2(k.x, k.y), __vmaxu2(k.z, k.w));
+    return max(m & 0xFFFFu, m >> 16);
 }
 
 template <bool BF>
@@ -148,32 +208,20 @@ struct Sampler {
 
     int histograms;    // made so far
 
-    // Histogram of the keys that `bin` gives a bin (and P > 0), merged over the cluster into all_count and all_sum.
-    template <class Bin>
-    __device__ __forceinline__ void histogram(bool counts, bool sums, Bin bin)
+    __device__ __forceinline__ void clear(bool sums)
     {
-        const int tid = threadIdx.x, copy = tid % SAMPLE_COPIES, set = histograms++ & 1;
-        for (int i = tid; i < 256 * SAMPLE_COPIES; i += SAMPLE_THREADS)
-            s.count[i] = s.low[i] = s.high[i] = 0;
-        __syncthreads();
-        for (int v = tid; v < vectors; v += SAMPLE_THREADS) {
-            const uint4 k4 = keys[v];
-            const uint32_t w[4] = {k4.x, k4.y, k4.z, k4.w};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t key = (w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
-                const int b = bin(key);
-                if (b < 0)
-                    continue;
-                const unsigned long long x = share(key);
-                if (x == 0)
-                    continue;
-                if (counts)
-                    atomicAdd(&s.count[b * SAMPLE_COPIES + copy], 1u);
-                if (sums)
-                    add_sum(&s.low[b * SAMPLE_COPIES + copy], &s.high[b * SAMPLE_COPIES + copy], x);
-            }
+        for (int i = threadIdx.x; i < 256 * SAMPLE_COPIES; i += SAMPLE_THREADS) {
+            s.count[i] = 0;
+            if (sums)
+                s.low[i] = s.high[i] = 0;
         }
+        __syncthreads();
+    }
+
+    // Merges the bins over copies and blocks into all_count and all_sum.
+    __device__ __forceinline__ void merge(bool counts, bool sums)
+    {
+        const int tid = threadIdx.x, set = histograms++ & 1;
         __syncthreads();
         if (tid < 256) {
             uint32_t n = 0;
@@ -181,7 +229,8 @@ struct Sampler {
 #pragma unroll
             for (int c = 0; c < SAMPLE_COPIES; ++c) {
                 n += s.count[tid * SAMPLE_COPIES + c];
-                sum += s.low[tid * SAMPLE_COPIES + c] + ((unsigned long long)s.high[tid * SAMPLE_COPIES + c] << 32);
+                if (sums)
+                    sum += s.low[tid * SAMPLE_COPIES + c] + ((unsigned long long)s.high[tid * SAMPLE_COPIES + c] << 32);
             }
             s.bin_count[set][tid] = n;
             s.bin_sum[set][tid] = sum;
@@ -202,6 +251,67 @@ struct Sampler {
                 s.all_sum[tid] = sum;
         }
         __syncthreads();
+    }
+
+    // Histogram of one key a thread, by high bytes.
+    __device__ __forceinline__ void of_threads(uint32_t key)
+    {
+        clear(false);
+        if (key > lowest_key<BF>())
+            atomicAdd(&s.count[(key >> 8) * SAMPLE_COPIES + threadIdx.x % SAMPLE_COPIES], 1u);
+        merge(true, false);
+    }
+
+    // Histogram of the keys of at least `least`, by high bytes: of counts, and of sums.
+    __device__ __forceinline__ void coarse(uint32_t least, bool counts, bool sums)
+    {
+        const int copy = threadIdx.x % SAMPLE_COPIES;
+        least = max(least, lowest_key<BF>() + 1);
+        clear(sums);
+        for (int v = threadIdx.x; v < vectors; v += SAMPLE_THREADS) {
+            const uint4 k4 = keys[v];
+            const uint32_t w[4] = {k4.x, k4.y, k4.z, k4.w};
+            if (largest(k4) < least)
+                continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t k[2] = {w[e] & 0xFFFFu, w[e] >> 16};
+                unsigned long long x[2] = {1, 1};
+                if (sums)
+                    share(w[e], x[0], x[1]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (k[i] < least)
+                        continue;
+                    const uint32_t at = (k[i] >> 8) * SAMPLE_COPIES + copy;
+                    if (counts)
+                        atomicAdd(&s.count[at], 1u);
+                    if (sums && x[i])
+                        add_sum(&s.low[at], &s.high[at], x[i]);
+                }
+            }
+        }
+        merge(counts, sums);
+    }
+
+    // Histogram of the low bytes of the keys with high byte `byte`.
+    __device__ __forceinline__ void fine(uint32_t byte)
+    {
+        const int copy = threadIdx.x % SAMPLE_COPIES;
+        clear(false);
+        for (int v = threadIdx.x; v < vectors; v += SAMPLE_THREADS) {
+            const uint4 k4 = keys[v];
+            if (largest(k4) >> 8 < byte)
+                continue;
+            const uint32_t w[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t key = (w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
+                if (key >> 8 == byte && key > lowest_key<BF>())
+                    atomicAdd(&s.count[(key & 255) * SAMPLE_COPIES + copy], 1u);
+            }
+        }
+        merge(true, false);
     }
 
     // The highest bin which, with `before` and the bins above it, has at least `want` of a measure (`weigh(bin)`).
@@ -261,8 +371,10 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), blocks = (int)cluster.num_blocks();
     const int row = blockIdx.x / blocks, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (tid < 64)
-        s.exp[tid] = SAMPLE_EXP[tid];
+    if (tid < SAMPLE_TABLE) {
+        const uint32_t e = SAMPLE_EXP[tid];
+        s.exp[tid] = make_uint2(e - SAMPLE_ROUND_BITS, __float_as_uint((float)e));
+    }
     pdl_wait();
     pdl_launch_dependents();
 
@@ -272,7 +384,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
     const float u = p.uniform[row];
     int top_k = p.top_k ? p.top_k[row] : 0;
     const bool greedy = temperature == 0.f;
-    if (!(temperature >= 0.f && temperature < INFINITY) || top_p != top_p || min_p != min_p ||
+    if (!(temperature >= 0.f && temperature <= SAMPLE_HOTTEST) || top_p != top_p || min_p != min_p ||
         (!greedy && !(u >= 0.f && u < 1.f))) { // the whole cluster leaves
         if (rank == 0 && tid == 0) {
             p.tokens[row] = -1;
@@ -291,7 +403,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
     const int begin = rank * p.slice, size = max(0, min(p.slice, p.vocab - begin));
     const int vectors = (size + 7) / 8;
     const uint16_t *src = p.logits + row * p.ld + begin;
-    uint32_t best = 0;
+    uint32_t best = 0; // two keys
     for (int v = tid; v < vectors; v += SAMPLE_THREADS) {
         uint4 w;
         if (p.wide && 8 * v + 8 <= size) {
@@ -308,7 +420,8 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
         keys[v] = w;
         best = __vmaxu2(best, __vmaxu2(__vmaxu2(w.x, w.y), __vmaxu2(w.z, w.w)));
     }
-    best = max(best & 0xFFFFu, best >> 16);
+    const uint32_t mine_best = max(best & 0xFFFFu, best >> 16);
+    best = mine_best;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1)
         best = max(best, __shfl_xor_sync(0xffffffffu, best, d));
@@ -335,11 +448,29 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
         return;
     }
 
+    if (best == (BF ? 0xFF80u : 0xFC00u)) { // infinite logits share everything: as zeros among nothing
+        for (int v = tid; v < vectors; v += SAMPLE_THREADS) {
+            uint4 w = keys[v];
+            uint32_t *k = reinterpret_cast<uint32_t *>(&w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t top = __vcmpeq2(k[e], best * 0x10001u);
+                k[e] = (top & 0x80008000u) | (~top & lowest_key<BF>() * 0x10001u);
+            }
+            keys[v] = w;
+        }
+        best = 0x8000u;
+        __syncthreads();
+    }
+
     Sampler<BF> f{s, keys, vectors, cluster, {}, 0};
-    f.share.top = number_of<BF>(best);
-    const double c = 1.4426950408889634 / (greedy ? 1.0 : (double)temperature);
-    f.share.c_hi = (float)c;
-    f.share.c_lo = (float)(c - (double)f.share.c_hi);
+    f.share.top = numbers_of<BF>(best).x;
+    // log2(e) = LOG + LOG_LO over T.  (The smallest temperatures' inverse is cut to what fp32 holds: every other logit's P
+    // is 0 by far.)
+    constexpr float LOG = 1.44269502162933349609375f, LOG_LO = 1.92596299112661747e-8f;
+    const float t = greedy ? 1.f : temperature, c = LOG / t;
+    f.share.c_hi = fminf(c, 1e38f);
+    f.share.c_lo = c < 1e38f ? (fmaf(-c, t, LOG) + LOG_LO) / t : 0.f;
     f.share.exp = s.exp;
 
     // --- the threshold: keys above it are kept, and the first `ties` of those at it --------------
@@ -351,7 +482,14 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
         const bool by_sum = top_p < 1.f;
         const auto counts = [&s = s](int b) { return (unsigned long long)s.all_count[b]; };
         const auto sums = [&s = s](int b) { return s.all_sum[b]; };
-        f.histogram(top_k > 0, by_sum, [](uint32_t key) { return (int)(key >> 8); });
+        const auto none = [](int) { return 0ULL; };
+        uint32_t least = 0; // no key below it is kept
+        if (top_k > 0 && top_k <= SAMPLE_THREADS) {
+            f.of_threads(mine_best);
+            f.search(0, (unsigned long long)top_k, counts, none);
+            least = s.found < 256 ? s.found << 8 : 0;
+        }
+        f.coarse(least, top_k > 0, by_sum);
         int bin = -1;                     // high byte of the keys that the counts at hand are of
         unsigned long long above_bin = 0; // sum of the keys above them
         unsigned long long total = 0;     // sum of what top-k keeps
@@ -359,14 +497,14 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
             if (by_sum)
                 f.search(0, (unsigned long long)top_k, counts, sums);
             else
-                f.search(0, (unsigned long long)top_k, counts, [](int) { return 0ULL; });
+                f.search(0, (unsigned long long)top_k, counts, none);
             total = s.total_other;
             if (s.found < 256) {
                 bin = (int)s.found;
                 above_bin = s.found_other;
                 const unsigned long long count_above = s.found_above;
-                f.histogram(true, false, [bin](uint32_t key) { return (int)(key >> 8) == bin ? (int)(key & 255) : -1; });
-                f.search(count_above, (unsigned long long)top_k, counts, [](int) { return 0ULL; });
+                f.fine((uint32_t)bin);
+                f.search(count_above, (unsigned long long)top_k, counts, none);
                 threshold = (uint32_t)bin << 8 | s.found;
                 ties = (uint32_t)(top_k - s.found_above);
             }
@@ -382,24 +520,23 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
             };
             if (bin >= 0) {
                 __syncthreads(); // found is read before the search that writes it again
-                f.search(0, ~0ULL, kept, [](int) { return 0ULL; });
+                f.search(0, ~0ULL, kept, none);
                 total = above_bin + s.total;
             } else if (top_k <= 0) {
-                f.search(0, ~0ULL, sums, [](int) { return 0ULL; });
+                f.search(0, ~0ULL, sums, none);
                 total = s.total;
             }
-            const unsigned long long want =
-                max(1ULL, (unsigned long long)ceil(fmax((double)top_p, 0.0) * (double)total));
+            const unsigned long long part = fraction(top_p);
+            const unsigned long long want = max(1ULL, __umul64hi(part, total) + (part * total != 0)); // rounded up
             unsigned long long above = above_bin;
             __syncthreads();
             if (bin < 0 || above_bin >= want) { // it ends above the counts at hand
-                f.search(0, want, [&](int b) { return b > bin ? s.all_sum[b] : 0ULL; }, [](int) { return 0ULL; });
+                f.search(0, want, [&](int b) { return b > bin ? s.all_sum[b] : 0ULL; }, none);
                 at = (int)s.found;
                 above = s.found_above;
-                const int byte = at;
-                f.histogram(true, false, [byte](uint32_t key) { return (int)(key >> 8) == byte ? (int)(key & 255) : -1; });
+                f.fine((uint32_t)at);
             }
-            f.search(above, want, kept, [](int) { return 0ULL; });
+            f.search(above, want, kept, none);
             threshold = (uint32_t)at << 8 | s.found;
             const unsigned long long x = f.share(threshold);
             const uint32_t n = (uint32_t)((want - s.found_above + x - 1) / x); // those whose sum before is below want
@@ -408,14 +545,18 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
     }
 
     // --- sums of the kept, by warp and block, in the order of the indices -----------------------
-    const unsigned long long least = (unsigned long long)ceil(fmin(fmax((double)min_p, 0.0), 1.0) * (double)(1ULL << SAMPLE_BITS));
+    const unsigned long long part = fraction(min_p);
+    const unsigned long long least =
+        min_p >= 1.f ? 1ULL << SAMPLE_BITS
+                     : (part >> (64 - SAMPLE_BITS)) + ((part & ((1ULL << (64 - SAMPLE_BITS)) - 1)) != 0); // rounded up
     const unsigned long long tie_share = threshold ? f.share(threshold) : 0;
     const bool ties_count = tie_share >= least && tie_share > 0;
     // A warp's range: whole steps of 32 vectors.
     const int steps = (vectors + 31) / 32, per_warp = (steps + SAMPLE_WARPS - 1) / SAMPLE_WARPS;
     const int from = warp * per_warp, to = min(steps, from + per_warp);
+    const uint32_t lowest = max(threshold, lowest_key<BF>() + 1); // of what counts
     auto value = [&](uint32_t key) {
-        if (key <= threshold)
+        if (key <= threshold || key < lowest)
             return 0ULL;
         const unsigned long long x = f.share(key);
         return x >= least ? x : 0ULL;
@@ -424,15 +565,22 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
     uint32_t at_it = 0;
     for (int st = from; st < to; ++st) {
         const int v = st * 32 + lane;
-        if (v < vectors) {
-            const uint4 k4 = keys[v];
-            const uint32_t w[4] = {k4.x, k4.y, k4.z, k4.w};
+        if (v >= vectors)
+            break;
+        const uint4 k4 = keys[v];
+        if (largest(k4) < lowest)
+            continue;
+        const uint32_t w[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t key = (w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
-                above += value(key);
-                at_it += key == threshold;
-            }
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t first = w[e] & 0xFFFFu, second = w[e] >> 16;
+            if (max(first, second) < lowest)
+                continue;
+            unsigned long long x, y;
+            f.share(w[e], x, y);
+            above += first > threshold && x >= least ? x : 0;
+            above += second > threshold && y >= least ? y : 0;
+            at_it += (first == threshold) + (second == threshold);
         }
     }
 #pragma unroll
@@ -476,7 +624,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
         sum += s.warp_above[w] + kept_ties(ties_before, s.warp_ties[w]) * tie_share;
         ties_before += s.warp_ties[w];
     }
-    const unsigned long long want = greedy ? 0 : (unsigned long long)((double)u * (double)all);
+    const unsigned long long want = greedy ? 0 : __umul64hi(fraction(u), all);
     const unsigned long long mine = s.warp_above[warp] + kept_ties(ties_before, s.warp_ties[warp]) * tie_share;
     if (!(sum <= want && want < sum + mine))
         return;
@@ -526,8 +674,9 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
                         if (at > want) {
                             done = true;
                             p.tokens[row] = begin + 8 * v + e;
-                            if (p.logprobs)
-                                p.logprobs[row] = y == all ? 0.f : (float)log((double)y / (double)all);
+                            if (p.logprobs) // (near 1 by what is missing)
+                                p.logprobs[row] = y > all / 2 ? log1pf(-((float)(all - y) / (float)all))
+                                                              : logf((float)y / (float)all);
                         }
                     }
             }
