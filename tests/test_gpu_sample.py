@@ -186,6 +186,13 @@ def test_infinities_nan_zeros_and_rows_of_nothing(w4, dtype):
     case.check()
     assert case.tokens[:3].tolist() == [-1, -1, -1] and case.tokens[12] == 4999
     assert int(case.status.item()) == 0
+    # Rows whose largest logits are infinite, with each kind of setting.
+    case = Case(9, dtype, 24, 5000, temperature=[1.0], top_k=[0, 1, 2, 40, 200, 3000], top_p=[1.0, 1.0, 1.0, 0.5])
+    for i in range(24):
+        case.logits[i, 11 + i:11 + 200 * (1 + i % 7):3] = float("inf")
+    case.run(w4)
+    case.check()
+    assert int(case.status.item()) == 0
 
 
 def test_settings_out_of_range_are_reported(w4):

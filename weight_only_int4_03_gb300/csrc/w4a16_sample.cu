@@ -33,6 +33,8 @@ constexpr int SAMPLE_SLICE = 65536;    // logits of a block, at most (a bin's su
 constexpr int SAMPLE_BITS = 43;        // P = 1 is 2^43: 2^19 tokens sum below 2^62
 constexpr int SAMPLE_COPIES = 4;       // of a histogram, against lanes that meet at a bin
 constexpr int SAMPLE_TABLE = 256;
+constexpr int SAMPLE_FEW = 128;        // top_k up to which the tokens in question are gathered in one block
+constexpr int SAMPLE_LIST = 1024;      // of these, at most
 constexpr float SAMPLE_ROUND = 12582912.f; // rounds what is added to it to integers (ties to even), in its lowest bits
 constexpr uint32_t SAMPLE_ROUND_BITS = 0x4B400000u;
 constexpr float SAMPLE_HOTTEST = 0x1p100f; // temperature, at most
@@ -94,37 +96,62 @@ struct SampleShared {
     unsigned long long all_sum[256]; // of all blocks: the last histogram that asked for them
     uint32_t all_count[256];
     // Written by every block of the cluster.
-    uint32_t top[SAMPLE_CLUSTER];
+    uint32_t top[SAMPLE_CLUSTER], bound[SAMPLE_CLUSTER], listed_by[SAMPLE_CLUSTER];
     unsigned long long above[SAMPLE_CLUSTER];
     uint32_t ties[SAMPLE_CLUSTER];
     // Of this block's warps.
     uint32_t warp_top[SAMPLE_WARPS];
     unsigned long long warp_above[SAMPLE_WARPS];
     uint32_t warp_ties[SAMPLE_WARPS];
-    // A search's result.
+    // A search's result, and its sums by warp.
     unsigned long long found_above, found_other, total, total_other;
+    unsigned long long of_warp[8], other_of_warp[8];
+    // Tokens in question, key << 32 | ~index, so that the better one is larger: of this block, then (block 0) of all; the
+    // kept ones of these, and their P.
+    unsigned long long list[SAMPLE_LIST], gathered[SAMPLE_LIST], kept[SAMPLE_FEW], kept_share[SAMPLE_FEW];
+    uint32_t listed, n_kept;
     uint32_t found;
 };
 
-// 16-bit numbers as integers in the same order; NaN counts as -inf, -0 as 0.  Two at a time.
-template <bool BF>
+// 0xFFFF for each half whose highest bit is set.
+__device__ __forceinline__ uint32_t signs(uint32_t w)
+{
+    uint32_t r;
+    asm("prmt.b32 %0, %1, 0, 0xBB99;" : "=r"(r) : "r"(w));
+    return r;
+}
+
+// 16-bit numbers as integers in the same order, two at a time; -0 counts as 0.
 __device__ __forceinline__ uint32_t keys_of(uint32_t w)
 {
-    constexpr uint32_t INF = BF ? 0x7F807F80u : 0x7C007C00u;
     const uint32_t size = w & 0x7FFF7FFFu;
-    const uint32_t nan = __vcmpgtu2(size, INF), zero = __vcmpeq2(size, 0);
-    w = (w & ~nan) | ((INF | 0x80008000u) & nan);
-    w &= ~zero;
-    const uint32_t negative = ((w >> 15) & 0x00010001u) * 0xFFFFu;
-    return w ^ (negative | 0x80008000u);
+    w = size | (w & (size + 0x7FFF7FFFu) & 0x80008000u); // no sign without a size
+    return w ^ (signs(w) | 0x80008000u);
+}
+
+// Whether one of eight numbers is a NaN; and these as -inf.
+template <bool BF>
+__device__ __forceinline__ bool has_nan(const uint4 &w)
+{
+    constexpr uint32_t ABOVE = BF ? 0x007F007Fu : 0x03FF03FFu; // what takes the size of a NaN to the sign's place
+    const uint32_t any = ((w.x & 0x7FFF7FFFu) + ABOVE) | ((w.y & 0x7FFF7FFFu) + ABOVE) | ((w.z & 0x7FFF7FFFu) + ABOVE) |
+                         ((w.w & 0x7FFF7FFFu) + ABOVE);
+    return (any & 0x80008000u) != 0;
+}
+
+template <bool BF>
+__device__ __forceinline__ uint32_t without_nan(uint32_t w)
+{
+    const uint32_t nan = signs((w & 0x7FFF7FFFu) + (BF ? 0x007F007Fu : 0x03FF03FFu));
+    return (w & ~nan) | ((BF ? 0xFF80FF80u : 0xFC00FC00u) & nan);
 }
 
 // Two keys' numbers.
 template <bool BF>
 __device__ __forceinline__ float2 numbers_of(uint32_t keys)
 {
-    const uint32_t negative = (~keys >> 15 & 0x00010001u) * 0xFFFFu;
-    return unpack2<BF>(keys ^ (negative | 0x80008000u));
+    const uint32_t w = keys ^ (~signs(keys) | 0x80008000u);
+    return BF ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)) : unpack2<BF>(w);
 }
 
 template <bool BF>
@@ -147,10 +174,10 @@ struct Share {
         const float q = z * fmaf(z, fmaf(z, -1.f / 6.f, 0.5f), -1.f); // e^-z - 1, to z^4 / 24 < 2^-42
         const uint32_t v = e.x + __float_as_uint(fmaf(__uint_as_float(e.y), q, SAMPLE_ROUND)); // 2^31 2^(n - y)
         const uint32_t n = k / SAMPLE_TABLE;
-        // v 2^(12 - n), rounded where that is a shift to the right.
-        const unsigned long long large = (unsigned long long)v << ((12 - n) & 31);
-        const uint32_t small = (uint32_t)(((unsigned long long)v << ((44 - n) & 31)) + 0x80000000u >> 32);
-        return !fine ? 0 : n <= 12 ? large : small;
+        // v 2^(12 - n): by a product, which where that is a shift to the right lies 32 bits higher, to be rounded.
+        const bool small = n > 12;
+        const unsigned long long r = (unsigned long long)v * (1u << ((12 - n) & 31)) + (small ? 0x80000000u : 0u);
+        return !fine ? 0 : small ? r >> 32 : r;
     }
 
     __device__ __forceinline__ void operator()(uint32_t keys, unsigned long long &first, unsigned long long &second) const
@@ -182,6 +209,12 @@ __device__ __forceinline__ unsigned long long fraction(float x)
     return !(x > 0.f) || e <= 86 - 24 ? 0 : e >= 86 ? m << min(e - 86, 40) : m >> (86 - e);
 }
 
+// log(part / all), near 1 by what is missing.
+__device__ __forceinline__ float log_share(unsigned long long part, unsigned long long all)
+{
+    return part > all / 2 ? log1pf(-((float)(all - part) / (float)all)) : logf((float)part / (float)all);
+}
+
 // Adds `sum` to a bin's 64-bit sum of two 32-bit halves.
 __device__ __forceinline__ void add_sum(uint32_t *low, uint32_t *high, unsigned long long sum)
 {
@@ -196,6 +229,52 @@ __device__ __forceinline__ uint32_t largest(const uint4 &k)
 {
     const uint32_t m = __vmaxu2(__vmaxu2(k.x, k.y), __vmaxu2(k.z, k.w));
     return max(m & 0xFFFFu, m >> 16);
+}
+
+// The highest bin which, with `before` and the bins above it, has at least `want` of a measure: `weight` is that of bin
+// 255 - thread.  Leaves the bin in found (256: there is not as much), what lies above it in found_above (with `before`),
+// and the sum of `other` above it in found_other; total and total_other are those of all bins.
+__device__ __noinline__ void find(SampleShared &s, unsigned long long weight, unsigned long long other,
+                                  unsigned long long before, unsigned long long want)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    unsigned long long incl = weight, incl2 = other;
+    if (tid < 256) {
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const unsigned long long o = __shfl_up_sync(0xffffffffu, incl, d), o2 = __shfl_up_sync(0xffffffffu, incl2, d);
+            if (lane >= d) {
+                incl += o;
+                incl2 += o2;
+            }
+        }
+        if (lane == 31) {
+            s.of_warp[warp] = incl;
+            s.other_of_warp[warp] = incl2;
+        }
+        if (tid == 0)
+            s.found = 256;
+    }
+    __syncthreads();
+    if (tid < 256) {
+#pragma unroll
+        for (int w = 0; w < 8; ++w)
+            if (w < warp) {
+                incl += s.of_warp[w];
+                incl2 += s.other_of_warp[w];
+            }
+        if (tid == 255) {
+            s.total = incl;
+            s.total_other = incl2;
+        }
+        incl += before;
+        if (incl >= want && incl - weight < want) {
+            s.found = 255 - tid;
+            s.found_above = incl - weight;
+            s.found_other = incl2 - other;
+        }
+    }
+    __syncthreads();
 }
 
 template <bool BF>
@@ -239,12 +318,13 @@ struct Sampler {
         if (tid < 256) {
             uint32_t n = 0;
             unsigned long long sum = 0;
-            for (unsigned r = 0; r < cluster.num_blocks(); ++r) {
-                if (counts)
-                    n += *cluster.map_shared_rank(&s.bin_count[set][tid], r);
-                if (sums)
-                    sum += *cluster.map_shared_rank(&s.bin_sum[set][tid], r);
-            }
+            const unsigned blocks = cluster.num_blocks();
+#pragma unroll
+            for (unsigned r = 0; r < SAMPLE_CLUSTER; ++r)
+                if (r < blocks) {
+                    n += counts ? *cluster.map_shared_rank(&s.bin_count[set][tid], r) : 0;
+                    sum += sums ? *cluster.map_shared_rank(&s.bin_sum[set][tid], r) : 0;
+                }
             if (counts)
                 s.all_count[tid] = n;
             if (sums)
@@ -253,20 +333,11 @@ struct Sampler {
         __syncthreads();
     }
 
-    // Histogram of one key a thread, by high bytes.
-    __device__ __forceinline__ void of_threads(uint32_t key)
-    {
-        clear(false);
-        if (key > lowest_key<BF>())
-            atomicAdd(&s.count[(key >> 8) * SAMPLE_COPIES + threadIdx.x % SAMPLE_COPIES], 1u);
-        merge(true, false);
-    }
-
-    // Histogram of the keys of at least `least`, by high bytes: of counts, and of sums.
-    __device__ __forceinline__ void coarse(uint32_t least, bool counts, bool sums)
+    // Histogram of the keys by high bytes: of counts, and of sums.
+    __device__ __forceinline__ void coarse(bool counts, bool sums)
     {
         const int copy = threadIdx.x % SAMPLE_COPIES;
-        least = max(least, lowest_key<BF>() + 1);
+        constexpr uint32_t least = lowest_key<BF>() + 1;
         clear(sums);
         for (int v = threadIdx.x; v < vectors; v += SAMPLE_THREADS) {
             const uint4 k4 = keys[v];
@@ -314,51 +385,82 @@ struct Sampler {
         merge(true, false);
     }
 
-    // The highest bin which, with `before` and the bins above it, has at least `want` of a measure (`weigh(bin)`).
-    // Leaves the bin in found (256: there is not as much), what lies above it in found_above (with `before`), and the
-    // sum of `other(bin)` above it in found_other; total and total_other are those of all bins.  Warp 0 searches,
-    // eight bins a lane.
+    // find() over weigh(bin), with other(bin).
     template <class Weigh, class Other>
     __device__ __forceinline__ void search(unsigned long long before, unsigned long long want, Weigh weigh, Other other)
     {
-        if (threadIdx.x < 32) {
-            const int lane = threadIdx.x;
-            unsigned long long mine[8], sum = 0, sum2 = 0; // lane 0 has the highest eight bins, the highest first
+        const int bin = 255 - (int)threadIdx.x;
+        find(s, bin >= 0 ? weigh(bin) : 0, bin >= 0 ? other(bin) : 0, before, want);
+    }
+
+    // The token of a row of which top-k keeps a few, in block 0: `n` candidates lie in s.gathered, the kept ones among them.
+    __device__ __forceinline__ void choose(int n, int top_k, float top_p, unsigned long long least, float u, int32_t *token,
+                                           float *logprob)
+    {
+        const int tid = threadIdx.x;
+        static_assert(SAMPLE_LIST == 2 * SAMPLE_THREADS, "two candidates a thread");
+        const unsigned long long mine[2] = {tid < n ? s.gathered[tid] : 0,
+                                            tid + SAMPLE_THREADS < n ? s.gathered[tid + SAMPLE_THREADS] : 0};
+        const uint32_t key[2] = {(uint32_t)(mine[0] >> 32), (uint32_t)(mine[1] >> 32)};
+        auto count = [&](uint32_t at) { // of keys of at least `at`
+            return __syncthreads_count(key[0] >= at) + (n > SAMPLE_THREADS ? __syncthreads_count(key[1] >= at) : 0);
+        };
+        // The top_k-th key (0: there are fewer), and how many of it are kept.
+        uint32_t last = 0;
+#pragma unroll 1
+        for (uint32_t bit = 1u << 15; bit; bit >>= 1)
+            if (count(last | bit) >= top_k)
+                last |= bit;
+        const int above = count(last + 1), ties = top_k - above;
+        if (tid == 0)
+            s.n_kept = 0;
+        const bool all_ties = last == 0 || count(last) == top_k;
+        __syncthreads();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                mine[i] = weigh(255 - (8 * lane + i));
-                sum += mine[i];
-                sum2 += other(255 - (8 * lane + i));
-            }
-            unsigned long long incl = sum, incl2 = sum2;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const unsigned long long o = __shfl_up_sync(0xffffffffu, incl, d), o2 = __shfl_up_sync(0xffffffffu, incl2, d);
-                if (lane >= d) {
-                    incl += o;
-                    incl2 += o2;
+        for (int i = 0; i < 2; ++i) {
+            bool keep = mine[i] != 0 && key[i] >= last;
+            if (keep && key[i] == last && !all_ties) {
+                int better = 0; // ties of a lower index
+                for (int j = 0; j < n; ++j) {
+                    const unsigned long long o = s.gathered[j];
+                    better += (uint32_t)(o >> 32) == last && o > mine[i];
                 }
+                keep = better < ties;
             }
-            const uint32_t has = __ballot_sync(0xffffffffu, before + incl >= want);
-            if (has != 0 && lane == __ffs(has) - 1) {
-                unsigned long long above = before + incl - sum, above2 = incl2 - sum2;
-                int i = 0;
-                for (; i < 7 && above + mine[i] < want; ++i) {
-                    above += mine[i];
-                    above2 += other(255 - (8 * lane + i));
-                }
-                s.found = 255 - (8 * lane + i);
-                s.found_above = above;
-                s.found_other = above2;
-            }
-            if (lane == 31) {
-                if (has == 0)
-                    s.found = 256;
-                s.total = incl;
-                s.total_other = incl2;
-            }
+            if (keep)
+                s.kept[atomicAdd(&s.n_kept, 1u)] = mine[i];
         }
         __syncthreads();
+        const int kept = (int)s.n_kept;
+        const unsigned long long me = tid < kept ? s.kept[tid] : 0, x = tid < kept ? share((uint32_t)(me >> 32)) : 0;
+        if (tid < kept)
+            s.kept_share[tid] = x;
+        __syncthreads();
+        unsigned long long before = 0, total = 0;
+        for (int j = 0; j < kept; ++j) {
+            const unsigned long long y = s.kept_share[j];
+            total += y;
+            before += s.kept[j] > me ? y : 0;
+        }
+        const unsigned long long part = fraction(top_p);
+        const unsigned long long want = max(1ULL, __umul64hi(part, total) + (part * total != 0)); // rounded up
+        const bool stays = tid < kept && x >= least && (top_p >= 1.f || before < want);
+        __syncthreads();
+        if (tid < kept)
+            s.kept_share[tid] = stays ? x : 0;
+        __syncthreads();
+        unsigned long long all = 0, until = 0; // of all that stay; of those up to this index
+        for (int j = 0; j < kept; ++j) {
+            const unsigned long long y = s.kept_share[j];
+            all += y;
+            until += (uint32_t)s.kept[j] >= (uint32_t)me ? y : 0;
+        }
+        const unsigned long long at = __umul64hi(fraction(u), all);
+        if (stays && x > 0 && until - x <= at && at < until) {
+            *token = (int)~(uint32_t)me;
+            if (logprob)
+                *logprob = log_share(x, all);
+        }
     }
 };
 
@@ -384,17 +486,6 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
     const float u = p.uniform[row];
     int top_k = p.top_k ? p.top_k[row] : 0;
     const bool greedy = temperature == 0.f;
-    if (!(temperature >= 0.f && temperature <= SAMPLE_HOTTEST) || top_p != top_p || min_p != min_p ||
-        (!greedy && !(u >= 0.f && u < 1.f))) { // the whole cluster leaves
-        if (rank == 0 && tid == 0) {
-            p.tokens[row] = -1;
-            if (p.logprobs)
-                p.logprobs[row] = NAN;
-            if (p.status)
-                atomicOr(p.status, W4A16_DEV_SETTING);
-        }
-        return;
-    }
     if (greedy)
         top_k = 1;
     cluster.barrier_arrive(); // waited for before the first look at another block's memory
@@ -416,7 +507,9 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
                 h[e] = 8 * v + e < size ? src[8 * v + e] : NONE;
             w = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
         }
-        w = make_uint4(keys_of<BF>(w.x), keys_of<BF>(w.y), keys_of<BF>(w.z), keys_of<BF>(w.w));
+        if (has_nan<BF>(w))
+            w = make_uint4(without_nan<BF>(w.x), without_nan<BF>(w.y), without_nan<BF>(w.z), without_nan<BF>(w.w));
+        w = make_uint4(keys_of(w.x), keys_of(w.y), keys_of(w.z), keys_of(w.w));
         keys[v] = w;
         best = __vmaxu2(best, __vmaxu2(__vmaxu2(w.x, w.y), __vmaxu2(w.z, w.w)));
     }
@@ -427,18 +520,44 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
         best = max(best, __shfl_xor_sync(0xffffffffu, best, d));
     if (lane == 0)
         s.warp_top[warp] = best;
+    if (tid == 0)
+        s.listed = 0;
     __syncthreads();
     cluster.barrier_wait();
+    if (!(temperature >= 0.f && temperature <= SAMPLE_HOTTEST) || top_p != top_p || min_p != min_p ||
+        (!greedy && !(u >= 0.f && u < 1.f))) { // the whole cluster leaves
+        if (rank == 0 && tid == 0) {
+            p.tokens[row] = -1;
+            if (p.logprobs)
+                p.logprobs[row] = NAN;
+            if (p.status)
+                atomicOr(p.status, W4A16_DEV_SETTING);
+        }
+        return;
+    }
+    // Where top-k keeps a few: the top_k-th largest of this block's threads' largest keys.  That many of the row's keys
+    // are not below it, so no smaller one is kept.
+    const bool few = top_k > 0 && top_k <= SAMPLE_FEW;
+    uint32_t bound = 0;
+    if (few) {
+#pragma unroll 1
+        for (uint32_t bit = 1u << 15; bit; bit >>= 1)
+            if (__syncthreads_count(mine_best >= (bound | bit)) >= top_k)
+                bound |= bit;
+    }
     if (tid < blocks) {
         best = 0;
         for (int w = 0; w < SAMPLE_WARPS; ++w)
             best = max(best, s.warp_top[w]);
         *cluster.map_shared_rank(&s.top[rank], tid) = best;
+        *cluster.map_shared_rank(&s.bound[rank], tid) = bound;
     }
     cluster.sync();
     best = 0;
-    for (int r = 0; r < blocks; ++r)
+    for (int r = 0; r < blocks; ++r) {
         best = max(best, s.top[r]);
+        bound = max(bound, s.bound[r]);
+    }
     if (best <= lowest_key<BF>()) { // nothing to choose from
         if (rank == 0 && tid == 0) {
             p.tokens[row] = -1;
@@ -448,23 +567,10 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
         return;
     }
 
-    if (best == (BF ? 0xFF80u : 0xFC00u)) { // infinite logits share everything: as zeros among nothing
-        for (int v = tid; v < vectors; v += SAMPLE_THREADS) {
-            uint4 w = keys[v];
-            uint32_t *k = reinterpret_cast<uint32_t *>(&w);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t top = __vcmpeq2(k[e], best * 0x10001u);
-                k[e] = (top & 0x80008000u) | (~top & lowest_key<BF>() * 0x10001u);
-            }
-            keys[v] = w;
-        }
-        best = 0x8000u;
-        __syncthreads();
-    }
-
+    const bool infinite = best == (BF ? 0xFF80u : 0xFC00u);
+    constexpr uint32_t ZERO = 0x8000u; // the key of 0
     Sampler<BF> f{s, keys, vectors, cluster, {}, 0};
-    f.share.top = numbers_of<BF>(best).x;
+    f.share.top = infinite ? 0.f : numbers_of<BF>(best).x;
     // log2(e) = LOG + LOG_LO over T.  (The smallest temperatures' inverse is cut to what fp32 holds: every other logit's P
     // is 0 by far.)
     constexpr float LOG = 1.44269502162933349609375f, LOG_LO = 1.92596299112661747e-8f;
@@ -472,6 +578,64 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
     f.share.c_hi = fminf(c, 1e38f);
     f.share.c_lo = c < 1e38f ? (fmaf(-c, t, LOG) + LOG_LO) / t : 0.f;
     f.share.exp = s.exp;
+    const unsigned long long part = fraction(min_p);
+    const unsigned long long least =
+        min_p >= 1.f ? 1ULL << SAMPLE_BITS
+                     : (part >> (64 - SAMPLE_BITS)) + ((part & ((1ULL << (64 - SAMPLE_BITS)) - 1)) != 0); // rounded up
+
+    // --- a few tokens: gathered and chosen from in block 0 ---------------------------------------
+    if (few) {
+        // (infinite logits share everything, as zeros)
+        bound = infinite ? best : max(bound, lowest_key<BF>() + 1);
+        for (int v = tid; v < vectors; v += SAMPLE_THREADS) {
+            const uint4 k4 = keys[v];
+            if (largest(k4) < bound)
+                continue;
+            const uint32_t w[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t key = (w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
+                if (key < bound)
+                    continue;
+                const uint32_t at = atomicAdd(&s.listed, 1u);
+                if (at < SAMPLE_LIST)
+                    s.list[at] = (unsigned long long)(infinite ? ZERO : key) << 32 | (uint32_t)~(begin + 8 * v + e);
+            }
+        }
+        __syncthreads();
+        if (tid < blocks)
+            *cluster.map_shared_rank(&s.listed_by[rank], tid) = s.listed;
+        cluster.sync();
+        uint32_t n = 0, at = 0;
+        for (int r = 0; r < blocks; ++r) {
+            at = r == rank ? n : at;
+            n += s.listed_by[r]; // (at most the vocabulary in all)
+        }
+        if (n <= SAMPLE_LIST) {
+            unsigned long long *to = cluster.map_shared_rank(s.gathered, 0);
+            for (uint32_t i = tid; i < s.listed; i += SAMPLE_THREADS)
+                to[at + i] = s.list[i];
+            cluster.sync(); // the last
+            if (rank == 0)
+                f.choose((int)n, top_k, top_p, least, u, p.tokens + row, p.logprobs ? p.logprobs + row : nullptr);
+            return;
+        }
+        // (too many are equal or nearly so)
+    }
+    if (infinite) { // zeros among nothing
+        for (int v = tid; v < vectors; v += SAMPLE_THREADS) {
+            uint4 w = keys[v];
+            uint32_t *k = reinterpret_cast<uint32_t *>(&w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t top = __vcmpeq2(k[e], best * 0x10001u);
+                k[e] = (top & (ZERO * 0x10001u)) | (~top & lowest_key<BF>() * 0x10001u);
+            }
+            keys[v] = w;
+        }
+        best = ZERO;
+        __syncthreads();
+    }
 
     // --- the threshold: keys above it are kept, and the first `ties` of those at it --------------
     uint32_t threshold = 0, ties = 0; // no key is 0
@@ -483,13 +647,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
         const auto counts = [&s = s](int b) { return (unsigned long long)s.all_count[b]; };
         const auto sums = [&s = s](int b) { return s.all_sum[b]; };
         const auto none = [](int) { return 0ULL; };
-        uint32_t least = 0; // no key below it is kept
-        if (top_k > 0 && top_k <= SAMPLE_THREADS) {
-            f.of_threads(mine_best);
-            f.search(0, (unsigned long long)top_k, counts, none);
-            least = s.found < 256 ? s.found << 8 : 0;
-        }
-        f.coarse(least, top_k > 0, by_sum);
+        f.coarse(top_k > 0, by_sum);
         int bin = -1;                     // high byte of the keys that the counts at hand are of
         unsigned long long above_bin = 0; // sum of the keys above them
         unsigned long long total = 0;     // sum of what top-k keeps
@@ -520,10 +678,10 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
             };
             if (bin >= 0) {
                 __syncthreads(); // found is read before the search that writes it again
-                f.search(0, ~0ULL, kept, none);
+                f.search(0, ~0ULL, kept, none); // (for its total)
                 total = above_bin + s.total;
             } else if (top_k <= 0) {
-                f.search(0, ~0ULL, sums, none);
+                f.search(0, ~0ULL, sums, none); // (for its total)
                 total = s.total;
             }
             const unsigned long long part = fraction(top_p);
@@ -545,10 +703,6 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
     }
 
     // --- sums of the kept, by warp and block, in the order of the indices -----------------------
-    const unsigned long long part = fraction(min_p);
-    const unsigned long long least =
-        min_p >= 1.f ? 1ULL << SAMPLE_BITS
-                     : (part >> (64 - SAMPLE_BITS)) + ((part & ((1ULL << (64 - SAMPLE_BITS)) - 1)) != 0); // rounded up
     const unsigned long long tie_share = threshold ? f.share(threshold) : 0;
     const bool ties_count = tie_share >= least && tie_share > 0;
     // A warp's range: whole steps of 32 vectors.
@@ -568,19 +722,30 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
         if (v >= vectors)
             break;
         const uint4 k4 = keys[v];
-        if (largest(k4) < lowest)
-            continue;
         const uint32_t w[4] = {k4.x, k4.y, k4.z, k4.w};
+        if (threshold) { // few of the keys count: those alone, one after the other
+            uint32_t which = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t first = w[e] & 0xFFFFu, second = w[e] >> 16;
-            if (max(first, second) < lowest)
+            for (int e = 0; e < 4; ++e)
+                which |= (w[e] << 16 >= lowest << 16 ? 1u : 0u) << (2 * e) | (w[e] >= lowest << 16 ? 2u : 0u) << (2 * e);
+            while (which) {
+                const int e = __ffs(which) - 1;
+                which &= which - 1;
+                const uint32_t pair = e & 4 ? (e & 2 ? w[3] : w[2]) : (e & 2 ? w[1] : w[0]);
+                const uint32_t key = e & 1 ? pair >> 16 : pair & 0xFFFFu;
+                above += value(key);
+                at_it += key == threshold;
+            }
+        } else {
+            if (largest(k4) < lowest)
                 continue;
-            unsigned long long x, y;
-            f.share(w[e], x, y);
-            above += first > threshold && x >= least ? x : 0;
-            above += second > threshold && y >= least ? y : 0;
-            at_it += (first == threshold) + (second == threshold);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                unsigned long long x, y;
+                f.share(w[e], x, y);
+                above += x >= least ? x : 0;
+                above += y >= least ? y : 0;
+            }
         }
     }
 #pragma unroll
@@ -674,9 +839,8 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
                         if (at > want) {
                             done = true;
                             p.tokens[row] = begin + 8 * v + e;
-                            if (p.logprobs) // (near 1 by what is missing)
-                                p.logprobs[row] = y > all / 2 ? log1pf(-((float)(all - y) / (float)all))
-                                                              : logf((float)y / (float)all);
+                            if (p.logprobs)
+                                p.logprobs[row] = log_share(y, all);
                         }
                     }
             }
@@ -721,7 +885,7 @@ extern "C" int w4a16_sample(const void *logits, int ld, const float *uniform, co
         return status_of(STAGE_RESOURCE, err);
     // Blocks of a row: slices of 32768 logits at most where eight suffice, smaller ones while all fit on the GPU at once.
     int blocks = 1;
-    while (blocks < SAMPLE_CLUSTER && (vocab > blocks * 32768 || (batch * 2LL * blocks <= 2LL * num_sms && vocab > blocks * 2048)))
+    while (blocks < SAMPLE_CLUSTER && (vocab > blocks * 32768 || (batch * 2LL * blocks <= 4LL * num_sms && vocab > blocks * 4096)))
         blocks *= 2;
     SampleParams p;
     p.logits = static_cast<const uint16_t *>(logits);
