@@ -33,6 +33,7 @@ constexpr int SAMPLE_SLICE = 65536;    // logits of a block, at most (a bin's su
 constexpr int SAMPLE_BITS = 43;        // P = 1 is 2^43: 2^19 tokens sum below 2^62
 constexpr int SAMPLE_COPIES = 4;       // of a histogram, against lanes that meet at a bin
 constexpr int SAMPLE_TABLE = 256;
+constexpr int SAMPLE_SPARSE = 4;       // of eight logits, up to which a warp takes them one by one
 constexpr int SAMPLE_FEW = 128;        // top_k up to which the tokens in question are gathered in one block
 constexpr int SAMPLE_LIST = 1024;      // of these, at most
 constexpr float SAMPLE_ROUND = 12582912.f; // rounds what is added to it to integers (ties to even), in its lowest bits
@@ -224,6 +225,23 @@ __device__ __forceinline__ void add_sum(uint32_t *low, uint32_t *high, unsigned 
         atomicAdd(high, carry);
 }
 
+// Which of eight keys are at least `least`, a bit each.
+__device__ __forceinline__ uint32_t at_least(const uint32_t (&w)[4], uint32_t least)
+{
+    uint32_t which = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        which |= (w[e] << 16 >= least << 16 ? 1u : 0u) << (2 * e) | (w[e] >= least << 16 ? 2u : 0u) << (2 * e);
+    return which;
+}
+
+// Key e of eight, e not known before.
+__device__ __forceinline__ uint32_t pick(const uint32_t (&w)[4], int e)
+{
+    const uint32_t pair = e & 4 ? (e & 2 ? w[3] : w[2]) : (e & 2 ? w[1] : w[0]);
+    return e & 1 ? pair >> 16 : pair & 0xFFFFu;
+}
+
 // The largest of eight keys.
 __device__ __forceinline__ uint32_t largest(const uint4 &k)
 {
@@ -342,8 +360,19 @@ struct Sampler {
         for (int v = threadIdx.x; v < vectors; v += SAMPLE_THREADS) {
             const uint4 k4 = keys[v];
             const uint32_t w[4] = {k4.x, k4.y, k4.z, k4.w};
-            if (largest(k4) < least)
+            uint32_t which = at_least(w, least);
+            if (!__any_sync(__activemask(), __popc(which) > SAMPLE_SPARSE)) { // most are masked: the others one by one
+                while (which) {
+                    const uint32_t key = pick(w, __ffs(which) - 1), at = (key >> 8) * SAMPLE_COPIES + copy;
+                    which &= which - 1;
+                    if (counts)
+                        atomicAdd(&s.count[at], 1u);
+                    const unsigned long long x = sums ? share(key) : 0;
+                    if (x)
+                        add_sum(&s.low[at], &s.high[at], x);
+                }
                 continue;
+            }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const uint32_t k[2] = {w[e] & 0xFFFFu, w[e] >> 16};
@@ -393,29 +422,38 @@ struct Sampler {
         find(s, bin >= 0 ? weigh(bin) : 0, bin >= 0 ? other(bin) : 0, before, want);
     }
 
-    // The token of a row of which top-k keeps a few, in block 0: `n` candidates lie in s.gathered, the kept ones among them.
-    __device__ __forceinline__ void choose(int n, int top_k, float top_p, unsigned long long least, float u, int32_t *token,
-                                           float *logprob)
+    // The token of a row of which top-k keeps a few, in block 0: `n` candidates lie in s.gathered, the kept ones among
+    // them; their keys are from `low` to `high`.
+    __device__ __forceinline__ void choose(int n, uint32_t low, uint32_t high, int top_k, float top_p, unsigned long long least,
+                                           float u, int32_t *token, float *logprob)
     {
         const int tid = threadIdx.x;
-        static_assert(SAMPLE_LIST == 2 * SAMPLE_THREADS, "two candidates a thread");
+        static_assert(SAMPLE_LIST == 2 * SAMPLE_THREADS && SAMPLE_FEW <= SAMPLE_THREADS, "two candidates a thread");
         const unsigned long long mine[2] = {tid < n ? s.gathered[tid] : 0,
                                             tid + SAMPLE_THREADS < n ? s.gathered[tid + SAMPLE_THREADS] : 0};
         const uint32_t key[2] = {(uint32_t)(mine[0] >> 32), (uint32_t)(mine[1] >> 32)};
-        auto count = [&](uint32_t at) { // of keys of at least `at`
-            return __syncthreads_count(key[0] >= at) + (n > SAMPLE_THREADS ? __syncthreads_count(key[1] >= at) : 0);
-        };
-        // The top_k-th key (0: there are fewer), and how many of it are kept.
-        uint32_t last = 0;
-#pragma unroll 1
-        for (uint32_t bit = 1u << 15; bit; bit >>= 1)
-            if (count(last | bit) >= top_k)
-                last |= bit;
-        const int above = count(last + 1), ties = top_k - above;
+        if (tid < SAMPLE_FEW)
+            s.kept[tid] = s.kept_share[tid] = 0;
         if (tid == 0)
             s.n_kept = 0;
-        const bool all_ties = last == 0 || count(last) == top_k;
+        // The top_k-th key (0: all are kept), and how many of it are kept.
+        uint32_t last = 0;
+        int ties = 0;
+        bool all_ties = true;
         __syncthreads();
+        if (n > top_k) {
+            auto count = [&](uint32_t at) { // of keys of at least `at`
+                return __syncthreads_count(key[0] >= at) + (n > SAMPLE_THREADS ? __syncthreads_count(key[1] >= at) : 0);
+            };
+            uint32_t bit = low == high ? 0 : 1u << (31 - __clz(low ^ high)); // the first in which keys differ
+            last = bit ? low & ~(2 * bit - 1) : low;
+#pragma unroll 1
+            for (; bit; bit >>= 1)
+                if (count(last | bit) >= top_k)
+                    last |= bit;
+            ties = top_k - count(last + 1);
+            all_ties = count(last) == top_k;
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             bool keep = mine[i] != 0 && key[i] >= last;
@@ -431,25 +469,32 @@ struct Sampler {
                 s.kept[atomicAdd(&s.n_kept, 1u)] = mine[i];
         }
         __syncthreads();
+        // A thread each for the kept ones: the other warps leave.
+        if (tid >= SAMPLE_FEW)
+            return;
+        const auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(SAMPLE_FEW) : "memory"); };
         const int kept = (int)s.n_kept;
-        const unsigned long long me = tid < kept ? s.kept[tid] : 0, x = tid < kept ? share((uint32_t)(me >> 32)) : 0;
-        if (tid < kept)
+        const unsigned long long me = s.kept[tid], x = tid < kept ? share((uint32_t)(me >> 32)) : 0;
+        bool stays = tid < kept && x >= least;
+        if (top_p < 1.f) {
             s.kept_share[tid] = x;
-        __syncthreads();
-        unsigned long long before = 0, total = 0;
-        for (int j = 0; j < kept; ++j) {
-            const unsigned long long y = s.kept_share[j];
-            total += y;
-            before += s.kept[j] > me ? y : 0;
+            sync();
+            unsigned long long before = 0, total = 0;
+#pragma unroll 4
+            for (int j = 0; j < kept; ++j) {
+                const unsigned long long y = s.kept_share[j];
+                total += y;
+                before += s.kept[j] > me ? y : 0;
+            }
+            const unsigned long long part = fraction(top_p);
+            const unsigned long long want = max(1ULL, __umul64hi(part, total) + (part * total != 0)); // rounded up
+            stays = stays && before < want;
+            sync();
         }
-        const unsigned long long part = fraction(top_p);
-        const unsigned long long want = max(1ULL, __umul64hi(part, total) + (part * total != 0)); // rounded up
-        const bool stays = tid < kept && x >= least && (top_p >= 1.f || before < want);
-        __syncthreads();
-        if (tid < kept)
-            s.kept_share[tid] = stays ? x : 0;
-        __syncthreads();
+        s.kept_share[tid] = stays ? x : 0;
+        sync();
         unsigned long long all = 0, until = 0; // of all that stay; of those up to this index
+#pragma unroll 4
         for (int j = 0; j < kept; ++j) {
             const unsigned long long y = s.kept_share[j];
             all += y;
@@ -617,7 +662,8 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
                 to[at + i] = s.list[i];
             cluster.sync(); // the last
             if (rank == 0)
-                f.choose((int)n, top_k, top_p, least, u, p.tokens + row, p.logprobs ? p.logprobs + row : nullptr);
+                f.choose((int)n, infinite ? ZERO : bound, infinite ? ZERO : best, top_k, top_p, least, u, p.tokens + row,
+                         p.logprobs ? p.logprobs + row : nullptr);
             return;
         }
         // (too many are equal or nearly so)
@@ -723,22 +769,15 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
             break;
         const uint4 k4 = keys[v];
         const uint32_t w[4] = {k4.x, k4.y, k4.z, k4.w};
-        if (threshold) { // few of the keys count: those alone, one after the other
-            uint32_t which = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                which |= (w[e] << 16 >= lowest << 16 ? 1u : 0u) << (2 * e) | (w[e] >= lowest << 16 ? 2u : 0u) << (2 * e);
+        uint32_t which = at_least(w, lowest);
+        if (threshold || !__any_sync(__activemask(), __popc(which) > SAMPLE_SPARSE)) { // few count: one by one
             while (which) {
-                const int e = __ffs(which) - 1;
+                const uint32_t key = pick(w, __ffs(which) - 1);
                 which &= which - 1;
-                const uint32_t pair = e & 4 ? (e & 2 ? w[3] : w[2]) : (e & 2 ? w[1] : w[0]);
-                const uint32_t key = e & 1 ? pair >> 16 : pair & 0xFFFFu;
                 above += value(key);
                 at_it += key == threshold;
             }
         } else {
-            if (largest(k4) < lowest)
-                continue;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 unsigned long long x, y;
