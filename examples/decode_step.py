@@ -8,7 +8,14 @@ Every sequence of the batch gets one new token: its key and value go into the pa
 attends to everything before it, and the layer's output is the next step's input.  Lengths,
 positions and slots live on the device, so one captured CUDA graph serves every step.
 
-    python examples/decode_step.py [--batch 8] [--steps 32] [--hidden 2048] ...
+With --kv4 the heads of q and k are normalised, the cache is held in 4 bits, and the step goes from tokens to tokens:
+
+    x       = embedding[tokens]
+    h       = x + O( attention( norm, rope( QKV( norm x ) ) ) )    w4a16_kv4_append, w4a16_kv4_attention
+    x_new   = h + experts( norm h )
+    tokens  = sample( head( norm x_new ) )                         w4a16_gemm, w4a16_sample
+
+    python examples/decode_step.py [--kv4] [--batch 8] [--steps 32] [--hidden 2048] ...
 """
 import argparse
 import os
@@ -96,11 +103,9 @@ class DecodeLayer:
         self.max_pages = (max_len + page - 1) // page
         n_pages = batch * self.max_pages
         self.table = torch.randperm(n_pages, generator=g, device=DEV).to(torch.int32).view(batch, self.max_pages)
-        self.k_cache = torch.zeros((n_pages, page, kv_heads, head_dim), dtype=torch.float16, device=DEV)
-        self.v_cache = torch.zeros_like(self.k_cache)
+        self.n_pages = n_pages
+        self.make_cache(g)
         self.lens = torch.zeros(batch, dtype=torch.int32, device=DEV)  # tokens cached so far
-        size = w4.w4a16_paged_attention_workspace_size(batch, heads, kv_heads, head_dim)
-        self.workspace = torch.zeros(size, dtype=torch.uint8, device=DEV)
         self.status = torch.zeros(1, dtype=torch.int32, device=DEV)
         half = dict(dtype=torch.float16, device=DEV)
         self.qkv_out = torch.empty((batch, width), **half)
@@ -109,29 +114,109 @@ class DecodeLayer:
         self.proj = torch.empty((batch, hidden), **half)
         self.out = torch.empty((batch, hidden), **half)
 
+    def make_cache(self, g):
+        b, h, kv, d = self.batch, self.heads, self.kv, self.dim
+        self.k_cache = torch.zeros((self.n_pages, self.page, kv, d), dtype=torch.float16, device=DEV)
+        self.v_cache = torch.zeros_like(self.k_cache)
+        size = w4.w4a16_paged_attention_workspace_size(b, h, kv, d)
+        self.workspace = torch.zeros(size, dtype=torch.uint8, device=DEV)
+
+    def append(self, qkv, positions, slots):
+        """q into its buffer; k and v into the cache."""
+        b, h, kv, d, width = self.batch, self.heads, self.kv, self.dim, qkv.shape[1]
+        w4.w4a16_rope_append(qkv, qkv[:, h * d:], qkv[:, (h + kv) * d:], self.q, self.k_cache, self.v_cache,
+                             self.cos_sin, positions, slots, self.status, b, h, kv, d, d, [d // 2],
+                             self.max_len, self.page, self.n_pages, ldq=width, ldk=width, ldv=width)
+
+    def attend(self):
+        d = self.dim
+        w4.w4a16_paged_attention(self.q, self.k_cache, self.v_cache, self.att, self.table, self.lens,
+                                 self.workspace, self.batch, self.heads, self.kv, d, self.page, self.n_pages,
+                                 self.max_pages, d ** -0.5)
+
     def step(self, x):
         """One new token per sequence: x [batch, hidden] -> the layer's output (a buffer of its own)."""
-        b, h, kv, d, page = self.batch, self.heads, self.kv, self.dim, self.page
+        page = self.page
         positions = self.lens  # the new token's position is the number of those before it
         # Past max_len there is no page to look up: the token is not cached, and the operators report its position
         # and length in their status words.
         at = (positions // page).clamp(max=self.max_pages - 1).long()
         pages = self.table.gather(1, at[:, None]).squeeze(1)
         slots = torch.where(positions < self.max_len, pages.long() * page + (positions % page).long(), -1)
-        qkv = self.qkv(rms_norm(x), self.qkv_out)
-        width = qkv.shape[1]
-        w4.w4a16_rope_append(qkv, qkv[:, h * d:], qkv[:, (h + kv) * d:], self.q, self.k_cache, self.v_cache,
-                             self.cos_sin, positions, slots, self.status, b, h, kv, d, d, [d // 2],
-                             self.max_len, page, self.k_cache.shape[0], ldq=width, ldk=width, ldv=width)
+        self.append(self.qkv(rms_norm(x), self.qkv_out), positions, slots)
         self.lens += 1
-        w4.w4a16_paged_attention(self.q, self.k_cache, self.v_cache, self.att, self.table, self.lens,
-                                 self.workspace, b, h, kv, d, page, self.k_cache.shape[0], self.max_pages, d ** -0.5)
+        self.attend()
         mid = x + self.o(self.att, self.proj)
         return self.experts(rms_norm(mid), mid, self.out)
 
 
+class Kv4DecodeLayer(DecodeLayer):
+    """The layer with normalised heads of q and k, and its cache in 4 bits (groups of 64 values)."""
+
+    group_size, eps = 64, 1e-6
+
+    def make_cache(self, g):
+        b, h, kv, d = self.batch, self.heads, self.kv, self.dim
+        record = w4.w4a16_kv4_record_bytes(self.page, d, self.group_size)
+        self.cache = torch.zeros((self.n_pages, kv * record), dtype=torch.uint8, device=DEV)
+        self.q_norm, self.k_norm = (1 + 0.2 * torch.randn((2, d), generator=g, device=DEV)).half()
+        size = w4.w4a16_kv4_attention_workspace_size(b, h, kv, d)
+        self.workspace = torch.zeros(size, dtype=torch.uint8, device=DEV)
+
+    def append(self, qkv, positions, slots):
+        b, h, kv, d, width = self.batch, self.heads, self.kv, self.dim, qkv.shape[1]
+        w4.w4a16_kv4_append(qkv, qkv[:, h * d:], qkv[:, (h + kv) * d:], self.q_norm, self.k_norm, self.eps, self.q,
+                            self.cache, self.cos_sin, positions, slots, self.status, b, h, kv, d, d, (d // 2,),
+                            self.max_len, self.page, self.n_pages, self.group_size, ldq=width, ldk=width, ldv=width)
+
+    def attend(self):
+        d = self.dim
+        w4.w4a16_kv4_attention(self.q, self.cache, self.att, self.table, self.lens, self.workspace, self.batch,
+                               self.heads, self.kv, d, self.page, self.n_pages, self.max_pages, self.group_size,
+                               d ** -0.5)
+
+
+class Sampler4:
+    """The product with the vocabulary's 4-bit weights, and the next token of every sequence."""
+
+    def __init__(self, g, hidden, vocab, batch, temperature=0.8, top_k=50, top_p=0.95, min_p=0.0):
+        self.head = Linear4(g, hidden, vocab, batch)
+        self.batch, self.vocab = batch, vocab
+        self.logits = torch.empty((batch, vocab), dtype=torch.float16, device=DEV)
+        self.tokens = torch.empty(batch, dtype=torch.int32, device=DEV)
+        self.logprobs = torch.empty(batch, dtype=torch.float32, device=DEV)
+        self.status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        full = lambda v, dt: torch.full((batch,), v, dtype=dt, device=DEV)
+        self.settings = dict(temperature=full(temperature, torch.float32), top_k=full(top_k, torch.int32),
+                             top_p=full(top_p, torch.float32), min_p=full(min_p, torch.float32))
+
+    def __call__(self, x, uniform):
+        self.head(rms_norm(x), self.logits)
+        w4.w4a16_sample(self.logits, uniform, self.tokens, self.batch, self.vocab, logprobs=self.logprobs,
+                        status=self.status, **self.settings)
+        return self.tokens
+
+
+class TokenStep:
+    """From a token per sequence to the next ones: embedding, layer, head, sampling."""
+
+    def __init__(self, batch, max_len, vocab=32000, seed=0, **sizes):
+        self.layer = Kv4DecodeLayer(batch, max_len, seed=seed, **sizes)
+        g = torch.Generator(device=DEV).manual_seed(seed + 1)
+        hidden = self.layer.hidden
+        self.embedding = torch.randn((vocab, hidden), generator=g, device=DEV, dtype=torch.float16)
+        self.sampler = Sampler4(g, hidden, vocab, batch)
+        self.tokens = torch.randint(0, vocab, (batch,), generator=g, device=DEV, dtype=torch.int32)
+
+    def step(self, uniform):
+        x = self.layer.step(self.embedding.index_select(0, self.tokens))
+        self.tokens.copy_(self.sampler(x, uniform))
+        return self.tokens
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser()
+    ap.add_argument("--kv4", action="store_true", help="cache in 4 bits, normalised heads, tokens to tokens")
     ap.add_argument("--batch", type=int, default=8)
     ap.add_argument("--steps", type=int, default=32)
     ap.add_argument("--hidden", type=int, default=2048)
@@ -139,16 +224,25 @@ def main(argv=None):
     ap.add_argument("--experts", type=int, default=16)
     ap.add_argument("--top-k", type=int, default=4)
     args = ap.parse_args(argv)
-    layer = DecodeLayer(args.batch, args.steps + 16, hidden=args.hidden, inter=args.inter, experts=args.experts,
-                        top_k=args.top_k)
-    x = torch.randn((args.batch, args.hidden), dtype=torch.float16, device=DEV)
+    sizes = dict(hidden=args.hidden, inter=args.inter, experts=args.experts, top_k=args.top_k)
+    if args.kv4:
+        chain = TokenStep(args.batch, args.steps + 16, **sizes)
+        layer, state = chain.layer, chain.tokens
+        uniforms = torch.rand((args.steps + 16, args.batch), device=DEV)
+        step = lambda: chain.step(uniforms.index_select(0, layer.lens[:1]).squeeze(0))
+    else:
+        layer = DecodeLayer(args.batch, args.steps + 16, **sizes)
+        state = torch.randn((args.batch, args.hidden), dtype=torch.float16, device=DEV)
+        step = lambda: state.copy_(rms_norm(layer.step(state)))  # stands in for the next tokens
+    start_state = state.clone()
     for _ in range(3):  # warm up outside the graph
-        layer.step(x)
+        step()
     layer.lens.zero_()
+    state.copy_(start_state)
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        x.copy_(rms_norm(layer.step(x)))  # stands in for the next tokens
+        step()
     start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     start.record()
     for _ in range(args.steps):
@@ -156,8 +250,11 @@ def main(argv=None):
     end.record()
     torch.cuda.synchronize()
     bits = int(layer.status.item()) | w4.w4a16_status(layer.workspace)
+    if args.kv4:
+        bits |= int(chain.sampler.status.item())
     print(f"{args.steps} steps of {args.batch} sequences: {start.elapsed_time(end) / args.steps * 1e3:.1f} us a step, "
-          f"lengths now {layer.lens.tolist()}, device status {bits}, |x| {float(x.float().abs().mean()):.3f}")
+          f"lengths now {layer.lens.tolist()}, device status {bits}, " +
+          (f"tokens {state.tolist()}" if args.kv4 else f"|x| {float(state.float().abs().mean()):.3f}"))
 
 
 if __name__ == "__main__":
