@@ -34,8 +34,8 @@ def reference_step(layer, weights, x, t, got):
     pages = L.table.long()[:, at // L.page]  # [b, t + 1]
     k, v = (side[pages, (at % L.page)[None, :]] for side in stands)  # [b, t + 1, kv, d]
     step = params[..., 0].double().repeat_interleave(L.group_size, -1)[:, pages, (at % L.page)[None, :]][:, :, t]
-    for got, want, st in ((k[:, t], turned[:, h:], step[0]), (v[:, t], qkv[:, h + kv:], step[1])):
-        assert bool(((got - want).abs() <= 0.5 * st + 2.0 ** -7 * want.abs().amax()).all())
+    for new, want, st in ((k[:, t], turned[:, h:], step[0]), (v[:, t], qkv[:, h + kv:], step[1])):
+        assert bool(((new - want).abs() <= 0.5 * st + 2.0 ** -7 * want.abs().amax()).all())
     q = turned[:, :h].view(b, kv, h // kv, d)
     p = torch.softmax(torch.einsum("bcgd,btcd->bcgt", q, k) * d ** -0.5, -1)
     mid = x + torch.einsum("bcgt,btcd->bcgd", p, v).reshape(b, h * d) @ wo
