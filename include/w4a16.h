@@ -505,7 +505,7 @@ int w4a16_norm_rope_append(const void *q, int ldq, const void *k, int ldk, const
  * A paged cache held in 4 bits.  Each group of group_size values of a head (one token's) has a step s and a base b
  * of 16 bits (fp16, or bf16 with W4A16_FLAG_BF16), and each value a code in 0..15 that stands for code s + b:
  *     b = r(min),  s = r((max - min) / 15),  code = (x - b) / s to the nearest integer (ties to even), cut to 0..15
- * where r rounds to nearest even; a group whose range rounds to 0 (bf16: to a subnormal number) has s = 0 and code 0.
+ * where r rounds to nearest even, from fp32; a group whose range rounds to 0 (bf16: to a subnormal number) has s = 0 and code 0.
  * A group without a finite range (it holds an infinity or a NaN, or its step or base rounds to infinity) reads as NaN.
  * Page p begins at byte p * page_stride, with one record per KV head, of w4a16_kv4_record_bytes bytes each:
  *     key codes [page_size][head_dim / 8] words, value codes the same, key (s, b) pairs
@@ -546,8 +546,9 @@ size_t w4a16_kv4_attention_workspace_size(int batch, int n_heads, int n_kv_heads
  * are fp32, no key or value is rounded to 16 bits.  q and out are fp16, or bf16 with W4A16_FLAG_BF16, as are the
  * cache's steps and bases.  As w4a16_paged_attention, but for the cache (above) and these points: queries go in as fp16
  * scaled by a power of two per head, exact down to 2^-38 of the head's largest (in bf16, queries beyond 2^112 are too
- * large); p s goes into the value product to 2^-22 of itself, or to 2^-38 of the largest step of the values
- * seen.  A group that reads as NaN makes NaN of what it touches.  page_size at most W4A16_KV4_MAX_PAGE. */
+ * large); p s goes into the value product to 2^-22 of itself (bf16: 2^-12, an eighth of the outputs' own rounding), or to
+ * 2^-38 of the largest step of the values seen.  A group that reads as NaN makes NaN of what it touches.  page_size at
+ * most W4A16_KV4_MAX_PAGE. */
 int w4a16_kv4_attention(const void *q, int ldq, const void *cache, long long page_stride, void *out,
                         int ldo, float *lse, const int32_t *block_table, int ld_table,
                         const int32_t *seq_lens, void *workspace, size_t workspace_bytes, int batch,
@@ -565,7 +566,7 @@ int w4a16_kv4_attention(const void *q, int ldq, const void *cache, long long pag
  *   logits       device 16-bit [batch][ld] (fp16, or bf16 with W4A16_FLAG_BF16), 2-byte aligned (rows of 16-byte
  *                alignment are read in 16-byte loads); a NaN counts as -inf, and -inf is never chosen
  *   uniform      device fp32 [batch], in [0, 1)
- *   temperature  device fp32 [batch] or NULL (1): finite, not negative; 0 takes the largest logit (the lowest index
+ *   temperature  device fp32 [batch] or NULL (1): 0 .. 2^100; 0 takes the largest logit (the lowest index
  *                where some are equal) whatever the other settings
  *   top_k        device int32 [batch] or NULL: 0 and below: no limit
  *   top_p, min_p device fp32 [batch] or NULL (1, 0): top_p of 1 and above and min_p of 0 and below: no limit; min_p

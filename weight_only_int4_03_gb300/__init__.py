@@ -496,6 +496,7 @@ def w4a16_norm_rope_append(q, k, v, q_norm, k_norm, eps: float, q_out, k_cache, 
         sec_at, len(sec), page_size, n_pages, flags, _stream(stream)))
 
 
+@functools.lru_cache(maxsize=64)
 def w4a16_kv4_record_bytes(page_size: int, head_dim: int, group_size: int) -> int:
     """Bytes of one KV head's record in a page of the cache held in 4 bits; 0 for sizes that it does not take."""
     return int(_lib.w4a16_kv4_record_bytes(page_size, head_dim, group_size))

@@ -16,14 +16,22 @@
 //     the cache's type.
 //   - Positions are the rows of the score product (S^T = K Q^T) and value dims those of the value product
 //     (O^T = V^T P^T), so that eight heads fill an m16n8k16.  P^T is the scores' fragment transposed by
-//     movmatrix.  p s goes in as a 16-bit value and the 16-bit remainder, times a power of two that
-//     keeps it below 2^15: to 2^-22 of itself and 2^-38 of the largest step's.
-//   - The maximum is lazy: it moves only when a score passes it by a factor of 4, and a step of 32 positions
+//     movmatrix.  p s goes in as fp16, times a power of two that keeps it below 2^15, which holds 2^-12 of it down to
+//     2^-27 of the largest step's and 2^-38 of that below: in bf16 that is an eighth of what the outputs' own rounding
+//     takes; in fp16, where it would be as much as that, the 16-bit remainder goes in too (2^-22).
+//   - The maximum is lazy: it moves only when a score passes it by a factor of 4, and a step of 32 or 64 positions
 //     asks for that by one vote; sums of p and of p a are kept per lane until the end.
-//   - A value product starts from -8 sum p s (one MMA against constants makes it) and is added to the outputs in
-//     fp32 every 32 positions: the MMA cuts sums off, which over many positions of one sign would show.
+//   - A value product starts from -8 sum p s (an MMA against constants makes it) and is added to the outputs in
+//     fp32 every step: the MMA cuts sums off, which over many positions of one sign would show.
 //   - The words of a row lie in the order of the lanes, so that a lane's share of a row is one load; keys are
-//     copied to places that only the copying lane reads.
+//     copied to places that only the copying lane reads.  Where pages hold multiples of 16 positions, a page is
+//     looked up once for 16 of them, and masks are applied only in steps that have something to mask.
+// bf16, 128 wide: 48 sequences of 2048 to 32768 positions, 64 / 8 heads, 106 us, 5.6 TB/s of codes and parameters (the
+// 16-bit cache's bytes would take 327 us at the copy rate); one of 131071 with 40 / 8 heads and groups of 64 38.3 us, 4.0
+// TB/s, of which about 10 us pass before the first rows and in the join; fp16, 24 sequences of 5 to 9000 with a window of
+// 2048, 12 / 12 heads of 64: 14.2 us, of which most is the start and the join; one of 41 positions: 5.3 us of latencies.
+// Per 16 positions of 128 values: 16 score and value MMAs and two for the start (twice the latter in fp16), 88 conversions
+// of codes, 250 instructions in all; the ALU (54 % busy) and the issue slots (51 %) are the first to run out.
 // The work is split as in the 16-bit cache's attention (w4a16_split.cuh).
 #include <type_traits>
 

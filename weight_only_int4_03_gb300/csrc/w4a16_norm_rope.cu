@@ -620,7 +620,7 @@ __device__ __forceinline__ void coded_head(const NormParams &p, const TokenOf &t
 // takes items of 32 / LANES heads of one kind, q_items of q, then kv_items of k, then as many of v.  GROUPS: groups of
 // a row in the 4-bit cache, 0: the 16-bit cache.
 template <bool BF, int GROUPS, int LANES, bool FEW>
-__global__ void __launch_bounds__(FEW ? NORM_MOST : 32, FEW ? 1 : GROUPS ? 18 : 20)
+__global__ void __launch_bounds__(FEW ? NORM_MOST : 32, FEW ? 1 : GROUPS ? (LANES == 16 ? 14 : 18) : 20)
     norm_rope_kernel(const NormParams p, int q_items, int kv_items)
 {
     pdl_wait();

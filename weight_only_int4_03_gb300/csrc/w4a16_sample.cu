@@ -782,8 +782,11 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
             for (int e = 0; e < 4; ++e) {
                 unsigned long long x, y;
                 f.share(w[e], x, y);
-                above += x >= least ? x : 0;
-                above += y >= least ? y : 0;
+                if (least) {
+                    x = x >= least ? x : 0;
+                    y = y >= least ? y : 0;
+                }
+                above += x + y;
             }
         }
     }
@@ -922,10 +925,14 @@ extern "C" int w4a16_sample(const void *logits, int ld, const float *uniform, co
     cudaError_t err = sm_count(&num_sms);
     if (err != cudaSuccess)
         return status_of(STAGE_RESOURCE, err);
-    // Blocks of a row: slices of 32768 logits at most where eight suffice, smaller ones while all fit on the GPU at once.
-    int blocks = 1;
-    while (blocks < SAMPLE_CLUSTER && (vocab > blocks * 32768 || (batch * 2LL * blocks <= 4LL * num_sms && vocab > blocks * 4096)))
-        blocks *= 2;
+    // Blocks of a row: up to three an SM in all, of which two run at once (rows differ in work: 48 mixed rows of 131071
+    // take 43.6 us with eight blocks, 49 with the six that run in one go, 58 with four); no slices below 4096 logits (one
+    // row of 32000 takes 8.7 us with 4096, 10 with 8192), nor above 32768 where eight blocks allow, so that two blocks fit
+    // an SM's shared memory (256 masked rows of 100003: 86 us with four blocks, 102 with six, 115 with two).
+    const long long at_once = 3LL * num_sms / batch, useful = (vocab + 4095) / 4096, needed = (vocab + 32767) / 32768;
+    long long blocks64 = at_once < useful ? at_once : useful;
+    blocks64 = blocks64 < needed ? needed : blocks64;
+    const int blocks = (int)(blocks64 < SAMPLE_CLUSTER ? blocks64 : SAMPLE_CLUSTER);
     SampleParams p;
     p.logits = static_cast<const uint16_t *>(logits);
     p.uniform = uniform;
