@@ -16,8 +16,8 @@
 //     the cache's type.
 //   - Positions are the rows of the score product (S^T = K Q^T) and value dims those of the value product
 //     (O^T = V^T P^T), so that eight heads fill an m16n8k16.  P^T is the scores' fragment transposed by
-//     movmatrix.  p s goes in as fp16, times a power of two that keeps it below 2^15, which holds 2^-12 of it down to
-//     2^-27 of the largest step's and 2^-38 of that below: in bf16 that is an eighth of what the outputs' own rounding
+//     movmatrix.  p s goes in as fp16, times a power of two that keeps it below 2^15, which keeps it to 2^-11 of itself down to
+//     2^-27 of the largest step's, and to 2^-38 of that below: in bf16 that is an eighth of what the outputs' own rounding
 //     takes; in fp16, where it would be as much as that, the 16-bit remainder goes in too (2^-22).
 //   - The maximum is lazy: it moves only when a score passes it by a factor of 4, and a step of 32 or 64 positions
 //     asks for that by one vote; sums of p and of p a are kept per lane until the end.
