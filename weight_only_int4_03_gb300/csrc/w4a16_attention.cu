@@ -30,53 +30,27 @@
 // and an absolute 2^-40 below: a long tail under one dominant position counts in the output as it does in l
 // (without the factor, p below 2^-25 was in l alone).  With at most eight heads per KV head the remainder
 // takes the upper eight rows of the same MMA, which are empty then; with more it costs a second MMA.
-#include <type_traits>
-
-#include "w4a16_ops.cuh"
+#include "w4a16_split.cuh"
 
 namespace w4 {
 namespace ops {
 
-constexpr int ATT_WARPS = 4;
-constexpr int ATT_THREADS = ATT_WARPS * 32;
-constexpr int ATT_STEP = 16;                    // positions per warp and step
-constexpr int ATT_UNIT = ATT_WARPS * ATT_STEP;  // positions per work unit
-constexpr int ATT_ROWS = 16;                    // query heads per head tile
-constexpr int ATT_MAX_BATCH = 4096;
-constexpr float LN2 = 0.6931471805599453f;
-constexpr int ATT_FAN = 16;                     // parts of a row joined at once
-constexpr int ATT_SLOTS = 3;                    // partials of a block: first row, last row, joined group
+constexpr int ATT_STEP = 16;                     // positions per warp and step
+constexpr int ATT_UNIT = SPLIT_WARPS * ATT_STEP; // positions per work unit
+constexpr int ATT_ROWS = 16;                     // query heads per head tile
 
 struct AttParams {
     const uint16_t *q, *k, *v;
     uint16_t *out;
     float *lse;
-    const int32_t *table, *lens;
-    int *status, *counters, *group_counters;
-    float *partials;
+    const int32_t *table;
+    SplitParams split;
     long long page_stride, token_stride, head_stride;
     int ldq, ldo, ld_table;
-    int batch, heads, kv, group, tiles; // tiles: head tiles of a KV head's group
-    int page, n_pages, max_len, window;
+    int heads, group, tiles; // tiles: head tiles of a KV head's group
+    int page, n_pages;
     float scale_log2; // scale * log2(e)
 };
-
-// Positions [first, len) of sequence b; a length outside [0, max_len] is reported and clamped.
-__device__ __forceinline__ void live_range(const AttParams &p, int b, int &first, int &len)
-{
-    len = p.lens[b];
-    if (len < 0 || len > p.max_len) {
-        atomicOr(p.status, W4A16_DEV_LENGTH);
-        len = len < 0 ? 0 : p.max_len;
-    }
-    first = p.window > 0 && len > p.window ? len - p.window : 0;
-}
-
-// a / b for 0 <= a < 2^31 b: in 32 bits where both fit (64-bit division is a long sequence).
-__device__ __forceinline__ int quotient(long long a, long long b, bool small)
-{
-    return small ? (int)((uint32_t)a / (uint32_t)b) : (int)(a / b);
-}
 
 template <int D>
 struct AttGeom {
@@ -89,8 +63,7 @@ struct AttGeom {
     static constexpr int ROW_COST = D == 64 ? 8 : 4;
     static constexpr int STAGE = 2 * ATT_STEP * ROW;   // keys, then values
     static constexpr int WARP = STAGES * STAGE;
-    static constexpr int SMEM = ATT_WARPS * WARP;
-    static constexpr int SLOT = ATT_ROWS * (D + 2);    // floats of a partial: rows, then (m, l)
+    static constexpr int SMEM = SPLIT_WARPS * WARP;
 };
 
 // PACK: at most eight heads in a tile.
@@ -100,7 +73,7 @@ struct AttGeom {
 // window of 2048, 12 / 12 heads of 64: 17.6 us, of which half is the start and the join; one of 37
 // positions: 4.0 us of latencies.
 template <int D, bool BF, bool PACK>
-__global__ void __launch_bounds__(ATT_THREADS, AttGeom<D>::CTAS)
+__global__ void __launch_bounds__(SPLIT_THREADS, AttGeom<D>::CTAS)
     paged_attention_kernel(const AttParams p)
 {
     using G = AttGeom<D>;
@@ -109,102 +82,35 @@ __global__ void __launch_bounds__(ATT_THREADS, AttGeom<D>::CTAS)
     // What p is multiplied by for the value product, and its inverse for the outputs.
     constexpr float UP = BF ? 1.f : 32768.f, DOWN = 1.f / UP;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int prefix[ATT_MAX_BATCH + 1]; // numbers of one (KV head, head tile) before sequence b
-    __shared__ int warp_sum[ATT_WARPS];
-    __shared__ uint32_t live_mask[ATT_WARPS][G::STAGES];
-    __shared__ float stat[ATT_WARPS][ATT_ROWS][2];
-    __shared__ int is_last;
+    constexpr int R = PACK ? 8 : 16;
+    __shared__ SplitShared shared;
+    __shared__ uint32_t live_mask[SPLIT_WARPS][G::STAGES];
+    __shared__ float stat[SPLIT_WARPS][R][2];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
     pdl_wait();
     pdl_launch_dependents();
 
-    // --- the schedule: units before each sequence ---------------------------------------------
-    int run = 0;
-    for (int base = 0; base < p.batch; base += ATT_THREADS) {
-        const int b = base + tid;
-        int n = 0;
-        if (b < p.batch) {
-            int first, len;
-            live_range(p, b, first, len);
-            n = (len - first + ATT_UNIT - 1) / ATT_UNIT;
-            n += n > 0 ? G::ROW_COST : 0;
-        }
-        int incl = n;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d)
-                incl += o;
-        }
-        if (lane == 31)
-            warp_sum[warp] = incl;
-        __syncthreads();
-        int before = run;
-#pragma unroll
-        for (int w = 0; w < ATT_WARPS; ++w) {
-            if (w < warp)
-                before += warp_sum[w];
-            run += warp_sum[w];
-        }
-        if (b < p.batch)
-            prefix[b] = before + incl - n;
-        __syncthreads();
-    }
-    if (tid == 0)
-        prefix[p.batch] = run;
-    __syncthreads();
-    const int rows_per_seq = p.kv * p.tiles;
-    const long long units = (long long)run * rows_per_seq;
-    const int grid = (int)min((long long)gridDim.x, units);
-
+    Split<ATT_UNIT, G::ROW_COST, false> split(p.split, shared);
     // Sequences without a position: zeros and -inf.
-    for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
-        if (prefix[b + 1] != prefix[b])
+    for (int b = blockIdx.x; b < p.split.batch; b += gridDim.x) {
+        if (!split.empty(b))
             continue;
-        for (int i = tid; i < p.heads * D / 8; i += ATT_THREADS)
+        for (int i = tid; i < p.heads * D / 8; i += SPLIT_THREADS)
             *reinterpret_cast<uint4 *>(p.out + (long long)b * p.ldo + 8 * i) = make_uint4(0, 0, 0, 0);
         if (p.lse)
-            for (int h = tid; h < p.heads; h += ATT_THREADS)
+            for (int h = tid; h < p.heads; h += SPLIT_THREADS)
                 p.lse[(long long)b * p.heads + h] = -INFINITY;
     }
-    if ((int)blockIdx.x >= grid)
-        return;
-
-    const bool small = units * (grid + 1LL) < (1LL << 32);
-    auto begin_of = [&](int c) {
-        return small ? (long long)((uint32_t)(c * (uint32_t)units) / (uint32_t)grid) : c * units / grid;
-    };
-    auto owner_of = [&](long long number) { return quotient((number + 1) * grid - 1, units, small); };
-    const long long u_begin = begin_of(blockIdx.x), u_end = begin_of(blockIdx.x + 1);
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * G::WARP;
 
-    for (long long u = u_begin; u < u_end;) {
-        // --- the row of this segment and its positions ----------------------------------------
-        int lo = 0, hi = p.batch - 1; // last b with prefix[b] * rows_per_seq <= u
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if ((long long)prefix[mid] * rows_per_seq <= u)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-        const int b = lo, span = prefix[b + 1] - prefix[b], seq_units = span - G::ROW_COST;
-        const long long rem = u - (long long)prefix[b] * rows_per_seq;
-        const int row = quotient(rem, span, small);         // (KV head, head tile)
-        const long long row_u0 = u - (rem - (long long)row * span) + G::ROW_COST; // of unit 0
-        const int unit0 = (int)max(0LL, u - row_u0);
-        const int unit1 = (int)min((long long)seq_units, u_end - row_u0);
-        u = row_u0 + seq_units; // the row after this one
-        if (unit1 <= unit0)
-            break; // the range ends before the row's first unit
-        const int c = row / p.tiles, h0 = (row - c * p.tiles) * ATT_ROWS;
+    SplitSegment seg;
+    while (split.next(seg)) {
+        const int b = seg.b, c = seg.row / p.tiles, h0 = (seg.row - c * p.tiles) * ATT_ROWS;
         const int nh = min(ATT_ROWS, p.group - h0); // heads of this tile
-        int first, len;
-        live_range(p, b, first, len);
-        const int steps = unit1 - unit0;
-        const int pos0 = first + unit0 * ATT_UNIT + warp * ATT_STEP; // this warp's first position
+        const int len = seg.len, steps = seg.unit1 - seg.unit0;
+        const int pos0 = seg.start + seg.unit0 * ATT_UNIT + warp * ATT_STEP; // this warp's first position
 
         float o[NT][4];
 #pragma unroll
@@ -228,7 +134,7 @@ __global__ void __launch_bounds__(ATT_THREADS, AttGeom<D>::CTAS)
             const bool in = step < steps && pos < len;
             bool ok = in && pg >= 0 && pg < p.n_pages;
             if (in && !ok)
-                atomicOr(p.status, W4A16_DEV_PAGE);
+                atomicOr(p.split.status, W4A16_DEV_PAGE);
             const long long off =
                 ok ? head_off + (long long)pg * p.page_stride + (long long)(pos % p.page) * p.token_stride : 0;
             const uint32_t mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;
@@ -395,7 +301,6 @@ __global__ void __launch_bounds__(ATT_THREADS, AttGeom<D>::CTAS)
         l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
         __syncthreads();
         float *acc = reinterpret_cast<float *>(smem); // [warp][row][D]
-        constexpr int R = PACK ? 8 : 16;
         {
             float *mine = acc + warp * R * D;
 #pragma unroll
@@ -416,171 +321,9 @@ __global__ void __launch_bounds__(ATT_THREADS, AttGeom<D>::CTAS)
             }
         }
         __syncthreads();
-        const bool whole = steps == seq_units;
-        const int slot = u_begin >= row_u0 ? 0 : 1; // a block shares at most its first and its last row
-        float *part = p.partials + ((long long)blockIdx.x * ATT_SLOTS + slot) * G::SLOT;
         uint16_t *out = p.out + (long long)b * p.ldo + (long long)(c * p.group + h0) * D;
-        const long long lse_at = (long long)b * p.heads + c * p.group + h0;
-        for (int i = tid; i < nh * (D / 4); i += ATT_THREADS) {
-            const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
-            float mx = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < ATT_WARPS; ++w)
-                mx = fmaxf(mx, stat[w][h][0]);
-            const float base = mx == -INFINITY ? 0.f : mx;
-            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-            float l = 0.f;
-#pragma unroll
-            for (int w = 0; w < ATT_WARPS; ++w) {
-                const float f = exp2f(stat[w][h][0] - base);
-                const float4 x = *reinterpret_cast<const float4 *>(acc + (w * R + h) * D + d);
-                l += f * stat[w][h][1];
-                sum.x += f * x.x;
-                sum.y += f * x.y;
-                sum.z += f * x.z;
-                sum.w += f * x.w;
-            }
-            if (whole) {
-                const float r = l == 0.f ? 0.f : DOWN / l;
-                uint2 w2;
-                w2.x = pack2<BF>(sum.x * r, sum.y * r);
-                w2.y = pack2<BF>(sum.z * r, sum.w * r);
-                *reinterpret_cast<uint2 *>(out + (long long)h * D + d) = w2;
-                if (d == 0 && p.lse)
-                    p.lse[lse_at + h] = l == 0.f ? -INFINITY : fmaf(base, LN2, logf(l));
-            } else {
-                __stcg(reinterpret_cast<float4 *>(part + h * D + d), sum);
-                if (d == 0)
-                    __stcg(reinterpret_cast<float2 *>(part + ATT_ROWS * D + 2 * h), make_float2(mx, l));
-            }
-        }
-        if (!whole) {
-            // The parts of a row are those of the blocks c_lo to c_hi, the owners of its first and its
-            // last unit.  The last block to arrive joins them; where there are more than ATT_FAN, the
-            // last of every ATT_FAN of them joins those first, so that many blocks share the reading.
-            // A row's counter is that of its first block, in which no other row of several parts starts;
-            // a group's likewise (a group of one part, which could share its block with the next row's
-            // first, does not count).
-            const int c_lo = owner_of(row_u0), c_hi = owner_of(row_u0 + seq_units - 1);
-            const int lo_slot = begin_of(c_lo) >= row_u0 ? 0 : 1, parts = c_hi - c_lo + 1;
-            const int group0 = ((int)blockIdx.x - c_lo) / ATT_FAN * ATT_FAN; // this block's group
-            bool last_level = parts <= ATT_FAN;
-            if (!last_level && group0 + 1 == parts)
-                last_level = true; // a group of one part is read as it is
-            for (;;) {
-                // Joined here: a row's parts, a group of them, or a row's groups.
-                const bool groups = last_level && parts > ATT_FAN;
-                const int n = groups       ? (parts + ATT_FAN - 1) / ATT_FAN
-                              : last_level ? parts
-                                           : min(ATT_FAN, parts - group0);
-                const int from = c_lo + (last_level ? 0 : group0);
-                __syncthreads();
-                if (tid == 0) {
-                    int *counter = last_level ? p.counters + c_lo : p.group_counters + from;
-                    const int last = arrive_counter(counter) == n - 1;
-                    if (last)
-                        *counter = 0;
-                    is_last = last;
-                }
-                __syncthreads();
-                if (!is_last)
-                    break;
-                // A thread sums ITEMS quads of outputs over the parts in block order, the loads of AT
-                // parts in flight at once (sixteen loads in all: few parts of 16 heads of 256 take 11.2 us
-                // instead of 13.2 with one quad at a time), rescaling as the maximum moves.
-                auto join = [&](auto items_c, auto at_c) {
-                    constexpr int ITEMS = decltype(items_c)::value, AT = decltype(at_c)::value;
-                    const int quads = nh * (D / 4);
-                    for (int i0 = tid; i0 < quads; i0 += ITEMS * ATT_THREADS) {
-                        float m[ITEMS], l[ITEMS];
-                        float4 sum[ITEMS];
-#pragma unroll
-                        for (int k = 0; k < ITEMS; ++k) {
-                            m[k] = -INFINITY;
-                            l[k] = 0.f;
-                            sum[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        }
-                        for (int q0 = 0; q0 < n; q0 += AT) {
-                            float2 ml[ITEMS][AT];
-                            float4 x[ITEMS][AT];
-#pragma unroll
-                            for (int q = 0; q < AT; ++q) {
-                                const int at = groups ? (q0 + q) * ATT_FAN : q0 + q;
-                                const int which = groups && at + 1 < parts ? ATT_SLOTS - 1 : from + at == c_lo ? lo_slot : 0;
-                                const float *pp = p.partials + ((long long)(from + at) * ATT_SLOTS + which) * G::SLOT;
-#pragma unroll
-                                for (int k = 0; k < ITEMS; ++k) {
-                                    const int i = i0 + k * ATT_THREADS;
-                                    const bool in = q0 + q < n && i < quads;
-                                    ml[k][q] = in ? __ldcg(reinterpret_cast<const float2 *>(pp + ATT_ROWS * D) + i / (D / 4))
-                                                  : make_float2(-INFINITY, 0.f);
-                                    x[k][q] = in ? __ldcg(reinterpret_cast<const float4 *>(pp) + i)
-                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
-                                }
-                            }
-#pragma unroll
-                            for (int k = 0; k < ITEMS; ++k) {
-                                float mn = m[k];
-#pragma unroll
-                                for (int q = 0; q < AT; ++q)
-                                    mn = fmaxf(mn, ml[k][q].x);
-                                const float base = mn == -INFINITY ? 0.f : mn, f0 = exp2f(m[k] - base);
-                                m[k] = mn;
-                                l[k] *= f0;
-                                sum[k].x *= f0;
-                                sum[k].y *= f0;
-                                sum[k].z *= f0;
-                                sum[k].w *= f0;
-#pragma unroll
-                                for (int q = 0; q < AT; ++q) {
-                                    const float f = exp2f(ml[k][q].x - base);
-                                    l[k] = fmaf(f, ml[k][q].y, l[k]);
-                                    sum[k].x = fmaf(f, x[k][q].x, sum[k].x);
-                                    sum[k].y = fmaf(f, x[k][q].y, sum[k].y);
-                                    sum[k].z = fmaf(f, x[k][q].z, sum[k].z);
-                                    sum[k].w = fmaf(f, x[k][q].w, sum[k].w);
-                                }
-                            }
-                        }
-#pragma unroll
-                        for (int k = 0; k < ITEMS; ++k) {
-                            const int i = i0 + k * ATT_THREADS;
-                            if (i >= quads)
-                                continue;
-                            const bool first_quad = i % (D / 4) == 0;
-                            if (last_level) {
-                                const float r = l[k] == 0.f ? 0.f : DOWN / l[k];
-                                uint2 w2;
-                                w2.x = pack2<BF>(sum[k].x * r, sum[k].y * r);
-                                w2.y = pack2<BF>(sum[k].z * r, sum[k].w * r);
-                                *reinterpret_cast<uint2 *>(out + 4LL * i) = w2;
-                                if (p.lse && first_quad)
-                                    p.lse[lse_at + i / (D / 4)] =
-                                        l[k] == 0.f ? -INFINITY : fmaf(m[k], LN2, logf(l[k]));
-                            } else {
-                                float *to = p.partials + ((long long)from * ATT_SLOTS + ATT_SLOTS - 1) * G::SLOT;
-                                __stcg(reinterpret_cast<float4 *>(to) + i, sum[k]);
-                                if (first_quad)
-                                    __stcg(reinterpret_cast<float2 *>(to + ATT_ROWS * D) + i / (D / 4),
-                                           make_float2(m[k], l[k]));
-                            }
-                        }
-                    }
-                };
-                using std::integral_constant;
-                if (n <= 4)
-                    join(integral_constant<int, 4>(), integral_constant<int, 4>());
-                else if (n <= 8)
-                    join(integral_constant<int, 2>(), integral_constant<int, 8>());
-                else
-                    join(integral_constant<int, 1>(), integral_constant<int, 16>());
-                if (last_level)
-                    break;
-                last_level = true;
-            }
-        }
-        if (u < u_end)
-            __syncthreads(); // the ring and the statistics are read before the next segment fills them
+        float *lse = p.lse ? p.lse + (long long)b * p.heads + c * p.group + h0 : nullptr;
+        split.template finish<D, R, BF>(seg, acc, &stat[0][0][0], nh, out, lse, DOWN);
     }
 }
 
@@ -606,23 +349,10 @@ int att_grid(int num_sms, int head_dim)
     return num_sms * (head_dim == 64 ? AttGeom<64>::CTAS : head_dim == 128 ? AttGeom<128>::CTAS : AttGeom<256>::CTAS);
 }
 
-// A workspace: status, the counters, the partials.  The counters' places are the same for calls of all
-// sizes on a device (a counter per block of the largest grid), so that no call's partials lie where
-// another one's counters have to be zero.
-struct AttLayout {
-    long long group_counters, counters, partials, total;
-};
-
-AttLayout att_layout(int head_dim, int num_sms)
+SplitLayout att_layout(int head_dim, int num_sms)
 {
-    AttLayout l;
-    const long long blocks = att_grid(num_sms, 64);
     static_assert(AttGeom<64>::CTAS >= AttGeom<128>::CTAS && AttGeom<64>::CTAS >= AttGeom<256>::CTAS, "the largest grid");
-    l.group_counters = HEADER_BYTES;
-    l.counters = l.group_counters + 4 * blocks;
-    l.partials = round_up(l.counters + 4 * blocks, 256);
-    l.total = l.partials + (long long)att_grid(num_sms, head_dim) * ATT_SLOTS * ATT_ROWS * (head_dim + 2) * 4;
-    return l;
+    return split_layout(att_grid(num_sms, 64), att_grid(num_sms, head_dim), ATT_ROWS * (head_dim + 2));
 }
 
 // Sizes that do not depend on a buffer; 0 or a status.
@@ -630,7 +360,7 @@ int check_sizes(int batch, int n_heads, int n_kv_heads, int head_dim)
 {
     if (batch < 0 || n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || n_heads % n_kv_heads != 0)
         return status_of(STAGE_ARG, W4A16_ARG_SHAPE);
-    if ((head_dim != 64 && head_dim != 128 && head_dim != 256) || batch > ATT_MAX_BATCH)
+    if ((head_dim != 64 && head_dim != 128 && head_dim != 256) || batch > SPLIT_MAX_BATCH)
         return status_of(STAGE_UNSUPPORTED, W4A16_ARG_SHAPE);
     if ((long long)n_heads * head_dim > 0x3FFFFFFFLL || (long long)batch * n_heads > 0x7FFFFFFFLL)
         return status_of(STAGE_ARG, W4A16_ARG_OVERFLOW);
@@ -695,10 +425,9 @@ extern "C" int w4a16_paged_attention(const void *q, int ldq, const void *k_cache
         return status_of(STAGE_RESOURCE, err);
     const int group = n_heads / n_kv_heads, tiles = (group + ATT_ROWS - 1) / ATT_ROWS;
     const int grid = att_grid(num_sms, head_dim);
-    const AttLayout lay = att_layout(head_dim, num_sms);
+    const SplitLayout lay = att_layout(head_dim, num_sms);
     if (workspace_bytes < (size_t)lay.total)
         return status_of(STAGE_ARG, W4A16_ARG_WORKSPACE);
-    char *ws = static_cast<char *>(workspace);
     AttParams p;
     p.q = static_cast<const uint16_t *>(q);
     p.k = static_cast<const uint16_t *>(k_cache);
@@ -706,26 +435,18 @@ extern "C" int w4a16_paged_attention(const void *q, int ldq, const void *k_cache
     p.out = static_cast<uint16_t *>(out);
     p.lse = lse;
     p.table = block_table;
-    p.lens = seq_lens;
-    p.status = reinterpret_cast<int *>(ws);
-    p.counters = reinterpret_cast<int *>(ws + lay.counters);
-    p.group_counters = reinterpret_cast<int *>(ws + lay.group_counters);
-    p.partials = reinterpret_cast<float *>(ws + lay.partials);
+    split_params(p.split, lay, workspace, seq_lens, batch, n_kv_heads * tiles, (int)max_len, window);
     p.page_stride = kv_page_stride;
     p.token_stride = kv_token_stride;
     p.head_stride = kv_head_stride;
     p.ldq = ldq;
     p.ldo = ldo;
     p.ld_table = ld_table;
-    p.batch = batch;
     p.heads = n_heads;
-    p.kv = n_kv_heads;
     p.group = group;
     p.tiles = tiles;
     p.page = page_size;
     p.n_pages = n_pages;
-    p.max_len = (int)max_len;
-    p.window = window;
     p.scale_log2 = scale * 1.4426950408889634f;
     const bool bf = (flags & W4A16_FLAG_BF16) != 0, pack = group <= 8;
     AttKernel kernel;
@@ -735,5 +456,5 @@ extern "C" int w4a16_paged_attention(const void *q, int ldq, const void *k_cache
                             : att_kernel<256>(bf, pack, kernel, smem);
     if (err != cudaSuccess)
         return status_of(STAGE_RESOURCE, err);
-    return launch_status(launch_pdl(kernel, dim3(grid), dim3(ATT_THREADS), (size_t)smem, stream, p));
+    return launch_status(launch_pdl(kernel, dim3(grid), dim3(SPLIT_THREADS), (size_t)smem, stream, p));
 }
