@@ -506,7 +506,8 @@ int w4a16_norm_rope_append(const void *q, int ldq, const void *k, int ldk, const
  * of 16 bits (fp16, or bf16 with W4A16_FLAG_BF16), and each value a code in 0..15 that stands for code s + b:
  *     b = r(min),  s = r((max - min) / 15),  code = (x - b) / s to the nearest integer (ties to even), cut to 0..15
  * where r rounds to nearest even, from fp32; a group whose range rounds to 0 (bf16: to a subnormal number) has s = 0 and code 0.
- * A group without a finite range (it holds an infinity or a NaN, or its step or base rounds to infinity) reads as NaN.
+ * A group without a finite range (it holds an infinity or a NaN, or max - min is beyond fp32, or its step or base rounds to
+ * infinity) reads as NaN.  Records may be written by others too, with steps of either sign.
  * Page p begins at byte p * page_stride, with one record per KV head, of w4a16_kv4_record_bytes bytes each:
  *     key codes [page_size][head_dim / 8] words, value codes the same, key (s, b) pairs
  *     [page_size][head_dim / group_size], value pairs the same
@@ -539,7 +540,8 @@ int w4a16_kv4_append(const void *q, int ldq, const void *k, int ldk, const void 
                      int head_dim, int rot_dim, const int32_t *sections, int n_axes, int page_size,
                      int n_pages, int group_size, unsigned flags, cudaStream_t stream);
 
-/* Workspace bytes of w4a16_kv4_attention: as w4a16_paged_attention_workspace_size, with the same rules. */
+/* Workspace bytes of w4a16_kv4_attention: as w4a16_paged_attention_workspace_size, with the same rules.  One workspace
+ * may serve calls of both. */
 size_t w4a16_kv4_attention_workspace_size(int batch, int n_heads, int n_kv_heads, int head_dim, int num_sms);
 
 /* w4a16_paged_attention over a cache held in 4 bits, whose values code s + b are used as they are: products and sums
@@ -574,7 +576,7 @@ int w4a16_kv4_attention(const void *q, int ldq, const void *cache, long long pag
  *   tokens       device int32 [batch]
  *   logprobs     device fp32 [batch] or NULL: log of the token's share of the kept sum
  *   status       device int32 or NULL: W4A16_DEV_SETTING is OR-ed in for a row with a setting out of range or NaN; its
- *                token is -1 and its logprob NaN
+ *                token is -1 and its logprob NaN (with temperature 0: for a NaN in top_p or min_p alone)
  *   batch        0 (a no-op) .. 2^24;  vocab 1 .. 524288, ld >= vocab
  * A row without a logit above -inf gets token -1 and logprob -inf. */
 int w4a16_sample(const void *logits, int ld, const float *uniform, const float *temperature,

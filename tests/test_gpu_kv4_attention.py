@@ -2,10 +2,10 @@
 
 Tolerance.  A score is scale (s (q . c) + b sum q), its first part a chain of at most head_dim / 16 tensor-core sums,
 each cut off at 2^-23, then four fp32 roundings: off by at most E = (D / 16 + 6) 2^-23 B with
-B = scale max_i sum |q| (s c + |b|), taken from the data.  So p is off by a factor e^(2 E) at most (score and
+B = scale max_i sum |q| (|s| c + |b|), taken from the data.  So p is off by a factor e^(2 E) at most (score and
 maximum), and exp2 adds 2^-22.  p s goes on with 2^-22 of itself, in bf16 with 2^-11, times codes less 8, and a part's
 sums (of codes less 8: at most 8 steps, and a + 8 s) are cut off at 2^-23 in six products of 32 positions and rounded at
-2^-24 once for these; the joins add fewer.  With R the largest of |value| and 16 s, all of that is below
+2^-24 once for these; the joins add fewer.  With R the largest of |value| and 16 |s|, all of that is below
 (4 E + 2^-17) R, and the rounding of bf16's p s below 2^-12 R (8 s is half of 16 s).  So
 |out - ref| <= u |ref| + (4 E + 2^-17) R, plus 2^-12 R in bf16, with u half a step of the type, and
 |lse - ref| <= E + 2^-20 + 2^-22 |ref|.
@@ -102,10 +102,10 @@ class Case:
             ref = torch.einsum("cgn,ncd->cgd", torch.softmax(logits, -1), sides[1]).reshape(self.heads, self.dim)
             lse = torch.logsumexp(logits, -1).reshape(self.heads)
             s, b = (params[0][at][..., j].double() for j in range(2))
-            weight = (codes[0][at].unflatten(-1, (s.shape[-1], -1)) * s.unsqueeze(-1) + b.abs().unsqueeze(-1)).flatten(-2)
+            weight = (codes[0][at].unflatten(-1, (s.shape[-1], -1)) * s.abs().unsqueeze(-1) + b.abs().unsqueeze(-1)).flatten(-2)
             bound = float((torch.einsum("cgd,ncd->cgn", q.abs(), weight) * self.scale).max())
             e = (self.dim / 16 + 6) * 2.0 ** -23 * bound
-            r = max(float(sides[1].abs().max()), 16 * float(params[1][at][..., 0].double().max()))
+            r = max(float(sides[1].abs().max()), 16 * float(params[1][at][..., 0].double().abs().max()))
             part = 2.0 ** -17 + (2.0 ** -12 if self.dtype == "bf16" else 0.0)
             tol = kv4.UNIT[self.dtype] * ref.abs() + (4 * e + part) * r + 2.0 ** -25
             err = (got - ref).abs()
@@ -253,3 +253,76 @@ def test_a_cache_past_32_bits(w4):
     case.run(ws)
     case.check()
     assert w4.w4a16_status(ws) == 0
+
+
+@pytest.mark.parametrize("dtype,dim,group_size", [("fp16", 128, -1), ("bf16", 128, 64), ("fp16", 64, -1)])
+def test_records_with_negative_steps(w4, dtype, dim, group_size):
+    """Values may as well be coded from the largest down."""
+    case = Case(w4, 22, dtype, [700, 33], 8, 2, dim, 16, group_size)
+    record = w4.w4a16_kv4_record_bytes(16, dim, group_size)
+    rec = case.cache[:, :2 * record].view(-1, 2, record)
+    rec[..., :16 * dim] ^= 0xFF
+    sb = rec[..., 16 * dim:16 * dim + 32 * kv4.groups_of(dim, group_size) * 4].contiguous().view(kv4.TYPES[dtype])
+    sb[..., 1::2] = (sb[..., 1::2].double() + 15 * sb[..., ::2].double()).to(sb.dtype)
+    sb[..., ::2] *= -1
+    import torch
+    rec[..., 16 * dim:16 * dim + sb.shape[-1] * 2] = sb.view(torch.uint8)
+    ws = case.workspace()
+    case.run(ws)
+    case.check()
+    assert w4.w4a16_status(ws) == 0
+
+
+def test_both_caches_attentions_in_one_workspace(w4):
+    """The bits of workspaces of their own, in any order."""
+    import torch
+    case = Case(w4, 23, "fp16", [9000, 40, 2500], 32, 4, 128, 16)
+    k, v = (torch.randn((case.n_pages, 16, 4, 128), device="cuda").half() for _ in range(2))
+    out = torch.empty((3, 32 * 128), device="cuda", dtype=torch.float16)
+
+    def paged(ws):
+        w4.w4a16_paged_attention(case.q, k, v, out, case.table, case.lens, ws, 3, 32, 4, 128, 16, case.n_pages,
+                                 case.max_pages, case.scale)
+
+    size = w4.w4a16_paged_attention_workspace_size(3, 32, 4, 128)
+    case.run(case.workspace())
+    paged(torch.zeros(size, dtype=torch.uint8, device="cuda"))
+    want = case.out.clone(), out.clone()
+    shared = torch.zeros(max(size, case.workspace().numel()), dtype=torch.uint8, device="cuda")
+    for turn in (0, 1, 0, 0, 1, 1, 0, 1):
+        case.out.zero_()
+        out.zero_()
+        paged(shared) if turn else case.run(shared)
+        torch.cuda.synchronize()
+        assert torch.equal((case.out, out)[turn], want[turn])
+    assert w4.w4a16_status(shared) == 0
+
+
+def test_calls_side_by_side(w4):
+    """Two streams, a workspace each: the bits of calls by themselves, directly and from graphs."""
+    import torch
+    cases = [Case(w4, 24, "fp16", [9000, 70], 32, 8, 128, 16), Case(w4, 25, "bf16", [300, 8000, 12], 16, 4, 128, 32, 64)]
+    spaces = [case.workspace() for case in cases]
+    want = []
+    for case, ws in zip(cases, spaces):
+        case.run(ws)
+        torch.cuda.synchronize()
+        want.append((case.out.clone(), case.lse.clone()))
+        case.out.zero_()
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    graphs = []
+    for case, ws, stream in zip(cases, spaces, streams):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            for _ in range(5):
+                case.run(ws, stream=stream)
+        graphs.append(graph)
+    for _ in range(10):
+        for case, ws, stream, graph in zip(cases, spaces, streams, graphs):
+            with torch.cuda.stream(stream):
+                case.run(ws, stream=stream)
+                graph.replay()
+    torch.cuda.synchronize()
+    for case, (out, lse) in zip(cases, want):
+        assert torch.equal(case.out, out) and torch.equal(case.lse, lse)

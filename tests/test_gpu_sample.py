@@ -217,6 +217,13 @@ def test_settings_out_of_range_are_reported(w4):
     assert int(case.status.item()) == 0
 
 
+def test_many_rows_of_few_tokens(w4):
+    case = Case(10, "fp16", 70001, 9, pad=2, shift=3, **ALL)
+    case.run(w4)
+    case.check(rows=range(0, 70001, 101))
+    assert int(case.status.item()) == 0 and bool((case.tokens >= 0).all())
+
+
 def test_repeats_batches_and_graphs_agree(w4):
     """A row's token does not depend on the other rows, the stream or the number of blocks that hold it."""
     import torch

@@ -351,8 +351,9 @@ int att_grid(int num_sms, int head_dim)
 
 SplitLayout att_layout(int head_dim, int num_sms)
 {
-    static_assert(AttGeom<64>::CTAS >= AttGeom<128>::CTAS && AttGeom<64>::CTAS >= AttGeom<256>::CTAS, "the largest grid");
-    return split_layout(att_grid(num_sms, 64), att_grid(num_sms, head_dim), ATT_ROWS * (head_dim + 2));
+    static_assert(AttGeom<64>::CTAS <= SPLIT_MAX_CTAS && AttGeom<128>::CTAS <= SPLIT_MAX_CTAS && AttGeom<256>::CTAS <= SPLIT_MAX_CTAS,
+                  "a counter per block");
+    return split_layout((long long)num_sms * SPLIT_MAX_CTAS, att_grid(num_sms, head_dim), ATT_ROWS * (head_dim + 2));
 }
 
 // Sizes that do not depend on a buffer; 0 or a status.

@@ -76,6 +76,7 @@ struct Kv4Geom {
     static constexpr int STAGE = SUBS * SUB;
     static constexpr int STAGES = D == 256 || SUBS == 4 ? 2 : 3; // (shared memory for two blocks at least)
     static constexpr int CTAS = D * NT > 64 ? 2 : 3;   // blocks per SM
+    static_assert(CTAS <= SPLIT_MAX_CTAS, "a counter per block");
     static constexpr int ROW_COST = 4;                 // of a row by itself, in units
     static constexpr int HEADS = 8 * NT;
     static constexpr int SMEM = SPLIT_WARPS * STAGES * STAGE > SPLIT_WARPS * HEADS * D * 4 ? SPLIT_WARPS * STAGES * STAGE
@@ -484,7 +485,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
             for (int u = 0; u < SUBS; ++u)
 #pragma unroll
                 for (int q = 0; q < G; ++q)
-                    step_top = fmaxf(step_top, fmaxf(vs[u][0][q], vs[u][1][q]));
+                    step_top = fmaxf(step_top, fmaxf(fabsf(vs[u][0][q]), fabsf(vs[u][1][q])));
             bool moves = step_top > ref;
             float2 top[NT];
 #pragma unroll
@@ -682,8 +683,6 @@ cudaError_t kv4_kernel(bool bf, bool whole, Kv4Kernel &kernel, int &smem)
     return allow_smem<Kv4Geom<D, G, NT>, 4>(reinterpret_cast<const void *>(kernel), v, smem);
 }
 
-constexpr int KV4_MAX_CTAS = 3;
-
 // Query heads of a tile, and blocks per SM.
 int kv4_heads(int head_dim, int group)
 {
@@ -698,7 +697,7 @@ int kv4_ctas(int head_dim, int heads)
 }
 SplitLayout kv4_layout(int head_dim, int heads, int num_sms)
 {
-    return split_layout((long long)num_sms * KV4_MAX_CTAS, (long long)num_sms * kv4_ctas(head_dim, heads),
+    return split_layout((long long)num_sms * SPLIT_MAX_CTAS, (long long)num_sms * kv4_ctas(head_dim, heads),
                         heads * (head_dim + 2));
 }
 

@@ -18,6 +18,7 @@ namespace ops {
 constexpr int SPLIT_WARPS = 4;
 constexpr int SPLIT_THREADS = SPLIT_WARPS * 32;
 constexpr int SPLIT_MAX_BATCH = 4096;
+constexpr int SPLIT_MAX_CTAS = 3; // blocks per SM of any kernel that is split like this
 constexpr int SPLIT_FAN = 16;  // parts of a row joined at once
 constexpr int SPLIT_SLOTS = 3; // partials of a block: first row, last row, joined group
 constexpr float SPLIT_LN2 = 0.6931471805599453f;
@@ -45,8 +46,8 @@ struct SplitSegment {
     bool more; // another segment of this block may follow
 };
 
-// A workspace: status, the counters, the partials.  The counters' places are the same for calls of all sizes on a
-// device (a counter per block of the largest grid), so that no call's partials lie where another one's counters
+// A workspace: status, the counters, the partials.  The counters' places are the same for calls of all sizes and
+// both kinds of cache on a device (a counter per block of the largest grid), so that no call's partials lie where another one's counters
 // have to be zero.
 struct SplitLayout {
     long long group_counters, counters, partials, total;
