@@ -116,7 +116,7 @@ struct SampleShared {
     // Tokens in question, key << 32 | ~index, so that the better one is larger: of this block, then (block 0) of all; the
     // kept ones of these, and their P.
     unsigned long long list[SAMPLE_LIST], gathered[SAMPLE_LIST], kept[SAMPLE_FEW], kept_share[SAMPLE_FEW];
-    uint32_t listed, n_kept;
+    uint32_t listed, place, n_gathered, n_kept; // (n_gathered: block 0's)
     uint32_t found;
 };
 
@@ -442,7 +442,7 @@ struct Sampler {
             s.kept[tid] = s.kept_share[tid] = 0;
         if (tid == 0)
             s.n_kept = 0;
-        // The top_k-th key (0: all are kept), and how many of it are kept.
+        // The top_k-th key or one with which as many are kept (0: all are), and how many of it are where not all are.
         uint32_t last = 0;
         int ties = 0;
         bool all_ties = true;
@@ -454,11 +454,14 @@ struct Sampler {
             uint32_t bit = low == high ? 0 : 1u << (31 - __clz(low ^ high)); // the first in which keys differ
             last = bit ? low & ~(2 * bit - 1) : low;
 #pragma unroll 1
-            for (; bit; bit >>= 1)
-                if (count(last | bit) >= top_k)
+            for (all_ties = false; bit && !all_ties; bit >>= 1) {
+                const int n_at = count(last | bit);
+                if (n_at >= top_k)
                     last |= bit;
-            ties = top_k - count(last + 1);
-            all_ties = count(last) == top_k;
+                all_ties = n_at == top_k; // (`last` then lies between the top_k-th key and the next one)
+            }
+            if (!all_ties)
+                ties = top_k - count(last + 1);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -572,7 +575,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
     if (lane == 0)
         s.warp_top[warp] = best;
     if (tid == 0)
-        s.listed = 0;
+        s.listed = s.n_gathered = 0;
     __syncthreads();
     cluster.barrier_wait();
     if (!(temperature >= 0.f && temperature <= SAMPLE_HOTTEST) || top_p != top_p || min_p != min_p ||
@@ -586,15 +589,19 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
         }
         return;
     }
-    // Where top-k keeps a few: the top_k-th largest of this block's threads' largest keys.  That many of the row's keys
-    // are not below it, so no smaller one is kept.
+    // Where top-k keeps a few: the top_k-th largest of this block's threads' largest keys, or one that not many more of
+    // these reach.  That many of the row's keys are not below it, so no smaller one is kept.
     const bool few = top_k > 0 && top_k <= SAMPLE_FEW;
     uint32_t bound = 0;
     if (few) {
 #pragma unroll 1
-        for (uint32_t bit = 1u << 15; bit; bit >>= 1)
-            if (__syncthreads_count(mine_best >= (bound | bit)) >= top_k)
+        for (uint32_t bit = 1u << 15; bit; bit >>= 1) {
+            const int n = __syncthreads_count(mine_best >= (bound | bit));
+            if (n >= top_k)
                 bound |= bit;
+            if (n >= top_k && n <= top_k + top_k / 4 + 8)
+                break;
+        }
     }
     if (tid < blocks) {
         best = 0;
@@ -656,17 +663,17 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
         __syncthreads();
         if (tid < blocks)
             *cluster.map_shared_rank(&s.listed_by[rank], tid) = s.listed;
-        cluster.sync();
-        uint32_t n = 0, at = 0;
-        for (int r = 0; r < blocks; ++r) {
-            at = r == rank ? n : at;
+        if (tid == 0) // a place in block 0's list, in any order
+            s.place = atomicAdd(cluster.map_shared_rank(&s.n_gathered, 0), s.listed);
+        __syncthreads();
+        unsigned long long *to = cluster.map_shared_rank(s.gathered, 0);
+        for (uint32_t i = tid; i < s.listed && s.place + i < SAMPLE_LIST; i += SAMPLE_THREADS)
+            to[s.place + i] = s.list[i];
+        cluster.sync(); // the last of rows that are decided here
+        uint32_t n = 0;
+        for (int r = 0; r < blocks; ++r)
             n += s.listed_by[r]; // (at most the vocabulary in all)
-        }
         if (n <= SAMPLE_LIST) {
-            unsigned long long *to = cluster.map_shared_rank(s.gathered, 0);
-            for (uint32_t i = tid; i < s.listed; i += SAMPLE_THREADS)
-                to[at + i] = s.list[i];
-            cluster.sync(); // the last
             if (rank == 0)
                 f.choose((int)n, infinite ? ZERO : bound, infinite ? ZERO : best, top_k, top_p, least, u, p.tokens + row,
                          p.logprobs ? p.logprobs + row : nullptr);
