@@ -19,9 +19,9 @@
 // indices, and the warp whose range holds u walks it; below the threshold no P is computed.
 //
 // What bounds it: for few rows the chain of cluster barriers, for many the instructions per logit (about thirty for a P).
-// Measured (device): one row of 32000 8.7 us; 48 x 131071 with all kinds of limits 43 (a row with top-p alone takes
+// Measured (device): one row of 32000 7.5 us; 48 x 131071 with all kinds of limits 42 (a row with top-p alone takes
 // about 22 by itself: a P and the histogram's atomics for each logit); 32 x 256000 without top-k or top-p 32; 256 x 100003
-// nine tenths masked 86, 7 us of which the reading would take.  64-bit atomics in the histogram instead of three of 32
+// nine tenths masked 85, 7 us of which the reading would take.  64-bit atomics in the histogram instead of three of 32
 // bits: 96 for the second; 256 or 1024 threads: slower.
 #include <cooperative_groups.h>
 
@@ -222,13 +222,17 @@ __device__ __forceinline__ float log_share(unsigned long long part, unsigned lon
     return part > all / 2 ? log1pf(-((float)(all - part) / (float)all)) : logf((float)part / (float)all);
 }
 
-// Adds `sum` to a bin's 64-bit sum of two 32-bit halves.
-__device__ __forceinline__ void add_sum(uint32_t *low, uint32_t *high, unsigned long long sum)
+// Adds `sum` to a bin's 64-bit sum of two 32-bit halves: the high one and the carry, when the low one was `old`; or all.
+__device__ __forceinline__ void add_carry(uint32_t *high, unsigned long long sum, uint32_t old)
 {
-    const uint32_t a = (uint32_t)sum, old = atomicAdd(low, a);
-    const uint32_t carry = (uint32_t)(sum >> 32) + (old + a < a ? 1u : 0u);
+    const uint32_t carry = (uint32_t)(sum >> 32) + (old + (uint32_t)sum < old ? 1u : 0u);
     if (carry)
         atomicAdd(high, carry);
+}
+
+__device__ __forceinline__ void add_sum(uint32_t *low, uint32_t *high, unsigned long long sum)
+{
+    add_carry(high, sum, atomicAdd(low, (uint32_t)sum));
 }
 
 // Which of eight keys are at least `least`, a bit each.
@@ -381,19 +385,25 @@ struct Sampler {
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const uint32_t k[2] = {w[e] & 0xFFFFu, w[e] >> 16};
-                unsigned long long x[2] = {1, 1};
-                if (sums)
-                    share(w[e], x[0], x[1]);
+                const uint32_t key[2] = {w[e] & 0xFFFFu, w[e] >> 16};
+                const uint32_t at[2] = {(key[0] >> 8) * SAMPLE_COPIES + copy, (key[1] >> 8) * SAMPLE_COPIES + copy};
+                if (counts) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (k[i] < least)
-                        continue;
-                    const uint32_t at = (k[i] >> 8) * SAMPLE_COPIES + copy;
-                    if (counts)
-                        atomicAdd(&s.count[at], 1u);
-                    if (sums && x[i])
-                        add_sum(&s.low[at], &s.high[at], x[i]);
+                    for (int i = 0; i < 2; ++i)
+                        if (key[i] >= least)
+                            atomicAdd(&s.count[at[i]], 1u);
+                }
+                if (sums) { // both low halves before the carries, which wait for them
+                    unsigned long long x[2];
+                    uint32_t old[2] = {0, 0};
+                    share(w[e], x[0], x[1]); // (0 for -inf)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if ((uint32_t)x[i])
+                            old[i] = atomicAdd(&s.low[at[i]], (uint32_t)x[i]);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        add_carry(&s.high[at[i]], x[i], old[i]);
                 }
             }
         }
@@ -939,9 +949,9 @@ extern "C" int w4a16_sample(const void *logits, int ld, const float *uniform, co
     if (err != cudaSuccess)
         return status_of(STAGE_RESOURCE, err);
     // Blocks of a row: up to three an SM in all, of which two run at once (rows differ in work: 48 mixed rows of 131071
-    // take 43.6 us with eight blocks, 49 with the six that run in one go, 58 with four); no slices below 4096 logits (one
-    // row of 32000 takes 8.7 us with 4096, 10 with 8192), nor above 32768 where eight blocks allow, so that two blocks fit
-    // an SM's shared memory (256 masked rows of 100003: 86 us with four blocks, 102 with six, 115 with two).
+    // take 43.6 us with eight blocks, 48.3 with the six that run in one go, 58 with four); no slices below 4096 logits (one
+    // row of 32000 takes 7.5 us with 4096, 8.1 with 8192), nor above 32768 where eight blocks allow, so that two blocks fit
+    // an SM's shared memory (256 masked rows of 100003: 85 us with four blocks, 109 with seven, 115 with two).
     const long long at_once = 3LL * num_sms / batch, useful = (vocab + 4095) / 4096, needed = (vocab + 32767) / 32768;
     long long blocks64 = at_once < useful ? at_once : useful;
     blocks64 = blocks64 < needed ? needed : blocks64;
