@@ -135,6 +135,9 @@ CASES = [
     dict(dtype="bf16", lens=[100, 5000, 640], heads=8, kv=2, dim=64, page=16, window=640),
     dict(dtype="fp16", lens=[65, 700], heads=8, kv=4, dim=128, page=16, q_pad=64, o_pad=8, page_pad=48),
     dict(dtype="fp16", lens=[3 * i % 97 for i in range(300)], heads=4, kv=2, dim=64, page=16),
+    dict(dtype="bf16", lens=[7 * i % 41 for i in range(4096)], heads=2, kv=1, dim=64, page=16),  # the largest batch
+    dict(dtype="fp16", lens=[66000, 3, 65536], heads=4, kv=1, dim=64, page=65536),  # the largest pages
+    dict(dtype="bf16", lens=[66000, 3, 65535], heads=4, kv=1, dim=128, page=65535, window=600),
     dict(dtype="bf16", lens=[900, 40], heads=8, kv=2, dim=128, page=16, sigma=8.0),  # sharp softmax
     dict(dtype="fp16", lens=[3000, 40], heads=8, kv=2, dim=128, page=16, offset=3.0),  # values of one sign
     dict(dtype="bf16", lens=[700, 40], heads=8, kv=2, dim=128, page=16, group_size=64, q_sigma=2.0 ** 60, sigma=2.0 ** -60),
