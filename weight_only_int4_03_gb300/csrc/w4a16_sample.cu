@@ -19,9 +19,9 @@
 // indices, and the warp whose range holds u walks it; below the threshold no P is computed.
 //
 // What bounds it: for few rows the chain of cluster barriers, for many the instructions per logit (about thirty for a P).
-// Measured (device): one row of 32000 7.5 us; 48 x 131071 with all kinds of limits 42 (a row with top-p alone takes
-// about 22 by itself: a P and the histogram's atomics for each logit); 32 x 256000 without top-k or top-p 32; 256 x 100003
-// nine tenths masked 85, 7 us of which the reading would take.  64-bit atomics in the histogram instead of three of 32
+// Measured (device): one row of 32000 7.5 us; 48 x 131071 with all kinds of limits 41 (a row with top-p alone takes
+// about 22 by itself: a P and the histogram's atomics for each logit); 32 x 256000 without top-k or top-p 31; 256 x 100003
+// nine tenths masked 83, 7 us of which the reading would take.  64-bit atomics in the histogram instead of three of 32
 // bits: 96 for the second; 256 or 1024 threads: slower.
 #include <cooperative_groups.h>
 
@@ -252,6 +252,18 @@ __device__ __forceinline__ uint32_t pick(const uint32_t (&w)[4], int e)
     return e & 1 ? pair >> 16 : pair & 0xFFFFu;
 }
 
+// Whether some lane's eight keys are all at least `least`, or more than SAMPLE_SPARSE of them; if not, `which` of them are.
+__device__ __forceinline__ bool dense(const uint4 &k, uint32_t least, uint32_t &which)
+{
+    const uint32_t m = __vminu2(__vminu2(k.x, k.y), __vminu2(k.z, k.w));
+    which = 0;
+    if (__any_sync(__activemask(), min(m & 0xFFFFu, m >> 16) >= least))
+        return true;
+    const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+    which = at_least(w, least);
+    return __any_sync(__activemask(), __popc(which) > SAMPLE_SPARSE);
+}
+
 // The largest of eight keys.
 __device__ __forceinline__ uint32_t largest(const uint4 &k)
 {
@@ -370,8 +382,8 @@ struct Sampler {
         for (int v = threadIdx.x; v < vectors; v += SAMPLE_THREADS) {
             const uint4 k4 = keys[v];
             const uint32_t w[4] = {k4.x, k4.y, k4.z, k4.w};
-            uint32_t which = at_least(w, least);
-            if (!__any_sync(__activemask(), __popc(which) > SAMPLE_SPARSE)) { // most are masked: the others one by one
+            uint32_t which;
+            if (!dense(k4, least, which)) { // most are masked: the others one by one
                 while (which) {
                     const uint32_t key = pick(w, __ffs(which) - 1), at = (key >> 8) * SAMPLE_COPIES + copy;
                     which &= which - 1;
@@ -792,8 +804,10 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
             break;
         const uint4 k4 = keys[v];
         const uint32_t w[4] = {k4.x, k4.y, k4.z, k4.w};
-        uint32_t which = at_least(w, lowest);
-        if (threshold || !__any_sync(__activemask(), __popc(which) > SAMPLE_SPARSE)) { // few count: one by one
+        uint32_t which;
+        if (threshold)
+            which = at_least(w, lowest);
+        if (threshold || !dense(k4, lowest, which)) { // few count: one by one
             while (which) {
                 const uint32_t key = pick(w, __ffs(which) - 1);
                 which &= which - 1;
