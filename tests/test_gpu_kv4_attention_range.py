@@ -1,0 +1,54 @@
+"""w4a16_kv4_attention where precision and range could run out: weights in bf16, large steps, queries of a wide range.
+
+Tolerance, as beside the operator's other tests but for p s, which goes on with 2^-22 of itself in both types:
+|out - ref| <= u |ref| + (4 E + 2^-17) R and |lse - ref| <= E + 2^-20 + 2^-22 |ref|, with R the largest of |value| and
+16 |s|, u half a step of the type and E what a score is off by: (D / 16 + 6) 2^-23 B, B = scale max_i sum |q| (|s| c + |b|),
+and what queries lose on their way to fp16.  The largest of a head is scaled to [2^13, 2^14), every second value to a
+sixteenth of that; half a unit of the smallest fp16 numbers, 2^-25, is then at most 2^-25 16 / 2^13 = 2^-34 of the largest
+query, and meets codes times steps: 2^-34 scale max |q| max_i sum |s| c.
+"""
+import pytest
+
+import kv4
+from test_gpu_kv4_attention import Case, w4  # noqa: F401  (a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def check(case):
+    import torch
+    torch.cuda.synchronize()
+    group = case.heads // case.kv
+    codes, params = (x.flatten(1, 2) for x in kv4.read(case.cache, case.page, case.kv, case.dim, case.group_size, case.dtype))
+    for i, n in enumerate(case.lens_list):
+        at = case.slots[i]
+        sides = [kv4.values(codes[s][at], params[s][at]) for s in range(2)]
+        got = case.out[i].view(case.heads, case.dim).double()
+        q = case.q[i].view(case.kv, group, case.dim).double()
+        logits = torch.einsum("cgd,ncd->cgn", q, sides[0]) * case.scale
+        ref = torch.einsum("cgn,ncd->cgd", torch.softmax(logits, -1), sides[1]).reshape(case.heads, case.dim)
+        lse = torch.logsumexp(logits, -1).reshape(case.heads)
+        s, b = (params[0][at][..., j].double() for j in range(2))
+        steps = codes[0][at].unflatten(-1, (s.shape[-1], -1)) * s.abs().unsqueeze(-1)
+        weight = (steps + b.abs().unsqueeze(-1)).flatten(-2)
+        bound = float((torch.einsum("cgd,ncd->cgn", q.abs(), weight) * case.scale).max())
+        lost = 2.0 ** -34 * case.scale * float(q.abs().max()) * float(steps.flatten(-2).sum(-1).max())
+        e = (case.dim / 16 + 6) * 2.0 ** -23 * bound + lost
+        r = max(float(sides[1].abs().max()), 16 * float(params[1][at][..., 0].double().abs().max()))
+        tol = kv4.UNIT[case.dtype] * ref.abs() + (4 * e + 2.0 ** -17) * r + 2.0 ** -25
+        err = (got - ref).abs()
+        assert bool((err <= tol).all()), f"sequence {i} (length {n}): {float((err / tol).max())} times the tolerance"
+        off = (case.lse[i].double() - lse).abs()
+        assert bool((off <= e + 2.0 ** -20 + 2.0 ** -22 * lse.abs()).all()), (i, float(off.max()), e)
+
+
+@pytest.mark.parametrize("heads,kv,dim,group_size", [(8, 2, 128, -1), (10, 2, 128, 64), (6, 6, 64, -1), (12, 1, 64, -1),
+                                                     (16, 1, 128, 64), (8, 1, 256, -1), (6, 2, 256, 128), (4, 1, 256, 64)])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_values_that_nearly_cancel(w4, dtype, heads, kv, dim, group_size):  # noqa: F811
+    """A few positions of nearly equal weights: outputs near zero show what each weight was rounded to."""
+    case = Case(w4, 31, dtype, [2 + i % 9 for i in range(40)] + [700], heads, kv, dim, 16, group_size, q_sigma=2.0 ** -4)
+    ws = case.workspace()
+    case.run(ws)
+    check(case)
+    assert w4.w4a16_status(ws) == 0

@@ -16,9 +16,9 @@
 //     the cache's type.
 //   - Positions are the rows of the score product (S^T = K Q^T) and value dims those of the value product
 //     (O^T = V^T P^T), so that eight heads fill an m16n8k16.  P^T is the scores' fragment transposed by
-//     movmatrix.  p s goes in as fp16, times a power of two that keeps it below 2^15, which keeps it to 2^-11 of itself down to
-//     2^-27 of the largest step's, and to 2^-38 of that below: in bf16 that is an eighth of what the outputs' own rounding
-//     takes; in fp16, where it would be as much as that, the 16-bit remainder goes in too (2^-22).
+//     movmatrix.  p s goes in as fp16, times a power of two that keeps it below 2^15, and the 16-bit remainder: 2^-22 of
+//     itself down to 2^-16 of the largest step's, and 2^-38 of that below.  (Without the remainder, in bf16, the two long
+//     cases below took 38 and 106 us; 2^-11 shows where outputs nearly cancel.)
 //   - The maximum is lazy: it moves only when a score passes it by a factor of 4, and a step of 32 or 64 positions
 //     asks for that by one vote; sums of p and of p a are kept per lane until the end.
 //   - A value product starts from -8 sum p s (an MMA against constants makes it) and is added to the outputs in
@@ -26,12 +26,11 @@
 //   - The words of a row lie in the order of the lanes, so that a lane's share of a row is one load; keys are
 //     copied to places that only the copying lane reads.  Where pages hold multiples of 16 positions, a page is
 //     looked up once for 16 of them, and masks are applied only in steps that have something to mask.
-// bf16, 128 wide: 48 sequences of 2048 to 32768 positions, 64 / 8 heads, 106 us, 5.6 TB/s of codes and parameters (the
-// 16-bit cache's bytes would take 327 us at the copy rate); one of 131071 with 40 / 8 heads and groups of 64 38.3 us, 4.0
+// bf16, 128 wide: 48 sequences of 2048 to 32768 positions, 64 / 8 heads, 123 us, 4.8 TB/s of codes and parameters (the
+// 16-bit cache's bytes would take 327 us at the copy rate); one of 131071 with 40 / 8 heads and groups of 64 44 us, 3.4
 // TB/s, of which about 10 us pass before the first rows and in the join; fp16, 24 sequences of 5 to 9000 with a window of
-// 2048, 12 / 12 heads of 64: 14.2 us, of which most is the start and the join; one of 41 positions: 5.3 us of latencies.
-// Per 16 positions of 128 values: 16 score and value MMAs and two for the start (twice the latter in fp16), 88 conversions
-// of codes, 250 instructions in all; the ALU (54 % busy) and the issue slots (51 %) are the first to run out.
+// 2048, 12 / 12 heads of 64: 14.2 us, of which most is the start and the join; one of 41 positions: 5.6 us of latencies.
+// Per 16 positions of 128 values: 8 score MMAs, 16 value MMAs and two for the start of each group, 88 conversions of codes.
 // The work is split as in the 16-bit cache's attention (w4a16_split.cuh).
 #include <type_traits>
 
@@ -69,8 +68,9 @@ struct Kv4Geom {
     static constexpr int PARAMS = 16 * 4 * G;          // a sub-step's steps and bases of one side
     static constexpr int SUB = 2 * KEYS + 2 * PARAMS;
     // Sub-steps of 16 positions that a warp takes at once: what a step costs by itself (pages, the vote, adding up the
-    // outputs) is shared by them, and more of them are in one another's shadow, as far as the registers go.
-    static constexpr int SUBS = D == 128 && NT == 1 ? 4 : 2;
+    // outputs) is shared by them, and more of them are in one another's shadow, as far as the registers go (one group: the 48
+    // sequences take 123 us with four, 129 with two; groups of 64, which spill with four: the long one 46 and 44).
+    static constexpr int SUBS = D == 128 && NT == 1 && G == 1 ? 4 : 2;
     static constexpr int STEP = 16 * SUBS;
     static constexpr int UNIT = SPLIT_WARPS * STEP;    // positions per work unit: a step of each warp
     static constexpr int STAGE = SUBS * SUB;
@@ -172,7 +172,6 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
     using M = Kv4Geom<D, G, NT>;
     constexpr int BLOCKS = M::BLOCKS, TILES = 4 * BLOCKS; // 16-wide tiles of the output dims
     constexpr int PER = BLOCKS / G;                       // blocks of 64 per group
-    constexpr bool REST = !BF;                            // p s goes in with a remainder
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ SplitShared shared;
     __shared__ float stat[SPLIT_WARPS][M::HEADS][2];
@@ -564,7 +563,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
                 }
 #pragma unroll
             for (int q = 0; q < G; ++q) {
-                uint32_t hi[SUBS][NT][2], lo[SUBS][NT][2];
+                uint32_t hi[SUBS][NT][2], lo[SUBS][NT][2]; // p s in two parts
                 float start[NT][4]; // -8 sum p s, as the codes' rows are scaled
 #pragma unroll
                 for (int u = 0; u < SUBS; ++u)
@@ -575,18 +574,15 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
                             const float2 a = mul(x[u][nt][r], both(vs[u][r][q] * up));
                             const uint32_t h = pack2<false>(a.x, a.y);
                             hi[u][nt][r] = transpose8x8(h);
-                            if (REST) {
-                                const float2 rest = sub(a, unpack2<false>(h));
-                                lo[u][nt][r] = transpose8x8(pack2<false>(rest.x, rest.y));
-                            }
+                            const float2 rest = sub(a, unpack2<false>(h));
+                            lo[u][nt][r] = transpose8x8(pack2<false>(rest.x, rest.y));
                         }
                         constexpr uint32_t E = 0x80088008u, S = 0x80808080u; // -8 2^-24 and -8 2^-20, twice
                         if (u == 0)
                             mma16816_zero<false>(start[nt], E, S, E, S, hi[u][nt][0], hi[u][nt][1]);
                         else
                             mma16816<false>(start[nt], E, S, E, S, hi[u][nt][0], hi[u][nt][1]);
-                        if (REST)
-                            mma16816<false>(start[nt], E, S, E, S, lo[u][nt][0], lo[u][nt][1]);
+                        mma16816<false>(start[nt], E, S, E, S, lo[u][nt][0], lo[u][nt][1]);
                     }
 #pragma unroll
                 for (int k = 0; k < PER; ++k) {
@@ -612,8 +608,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
                                         mma16816_from(d, a & ml, a & mh, e & ml, e & mh, hi[u][nt][0], hi[u][nt][1], start[nt]);
                                     else
                                         mma16816<false>(d, a & ml, a & mh, e & ml, e & mh, hi[u][nt][0], hi[u][nt][1]);
-                                    if (REST)
-                                        mma16816<false>(d, a & ml, a & mh, e & ml, e & mh, lo[u][nt][0], lo[u][nt][1]);
+                                    mma16816<false>(d, a & ml, a & mh, e & ml, e & mh, lo[u][nt][0], lo[u][nt][1]);
                                 }
                                 float2(&acc)[2] = o[nt][4 * blk + 2 * half + j];
                                 acc[0] = add(acc[0], make_float2(d[0], d[1]));
