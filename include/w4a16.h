@@ -507,7 +507,8 @@ int w4a16_norm_rope_append(const void *q, int ldq, const void *k, int ldk, const
  *     b = r(min),  s = r((max - min) / 15),  code = (x - b) / s to the nearest integer (ties to even), cut to 0..15
  * where r rounds to nearest even, from fp32; a group whose range rounds to 0 (bf16: to a subnormal number) has s = 0 and code 0.
  * A group without a finite range (it holds an infinity or a NaN, or max - min is beyond fp32, or its step or base rounds to
- * infinity) reads as NaN.  Records may be written by others too, with steps of either sign.
+ * infinity) reads as NaN.  Records may be written by others too, with steps of either sign for which code s + b is finite
+ * for every code.
  * Page p begins at byte p * page_stride, with one record per KV head, of w4a16_kv4_record_bytes bytes each:
  *     key codes [page_size][head_dim / 8] words, value codes the same, key (s, b) pairs
  *     [page_size][head_dim / group_size], value pairs the same
@@ -548,7 +549,8 @@ size_t w4a16_kv4_attention_workspace_size(int batch, int n_heads, int n_kv_heads
  * are fp32, no key or value is rounded to 16 bits.  q and out are fp16, or bf16 with W4A16_FLAG_BF16, as are the
  * cache's steps and bases.  As w4a16_paged_attention, but for the cache (above) and these points: queries go in as fp16
  * scaled by a power of two per head, exact down to 2^-38 of the head's largest (in bf16, queries beyond 2^112 are too
- * large); p s goes into the value product to 2^-22 of itself, or to 2^-38 of the largest step of the values seen.  A group
+ * large); p s goes into the value product to 2^-22 of itself, or to 2^-38 of the largest step of the values seen.  Sums of p
+ * times a value are divided by the sum of p at the end, and have to stay within fp32 until then.  A group
  * that reads as NaN makes NaN of what it touches.  page_size at most W4A16_KV4_MAX_PAGE. */
 int w4a16_kv4_attention(const void *q, int ldq, const void *cache, long long page_stride, void *out,
                         int ldo, float *lse, const int32_t *block_table, int ld_table,

@@ -52,3 +52,21 @@ def test_values_that_nearly_cancel(w4, dtype, heads, kv, dim, group_size):  # no
     case.run(ws)
     check(case)
     assert w4.w4a16_status(ws) == 0
+
+
+@pytest.mark.parametrize("sigma", [2.0 ** 112, 2.0 ** 117, 2.0 ** 119, 2.0 ** -112])
+@pytest.mark.parametrize("dim,group_size", [(64, -1), (128, 64), (256, -1)])
+def test_values_of_the_types_whole_range(w4, dim, group_size, sigma):  # noqa: F811
+    """Values in bf16 up to 2^122: steps up to 2^119."""
+    import torch
+    case = Case(w4, 32, "bf16", [1, 3, 17, 33], 4, 2, dim, 16, group_size)
+    every = torch.cat(case.slots)
+    g = torch.Generator(device="cuda").manual_seed(33)
+    k, v = (torch.randn((every.numel(), 2, dim), generator=g, device="cuda", dtype=torch.float64).clamp(-4, 4)
+            for _ in range(2))
+    w4.w4a16_kv4_append(None, k.bfloat16(), (v * sigma).bfloat16(), None, None, 0.0, None, case.cache, None, None, every, None,
+                        every.numel(), 0, 2, dim, 0, (), 0, 16, case.n_pages, group_size, case.flags)
+    ws = case.workspace()
+    case.run(ws)
+    check(case)
+    assert w4.w4a16_status(ws) == 0

@@ -637,7 +637,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
             }
         __syncthreads();
         float *acc = reinterpret_cast<float *>(smem); // [warp][head][D]
-        const float f_even = ref * (16777216.f / KV4_UP), f_odd = ref * (1048576.f / KV4_UP);
+        constexpr float EVEN = 16777216.f / KV4_UP, ODD = 1048576.f / KV4_UP; // (times ref: beyond fp32 where steps are large)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -647,8 +647,8 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
 #pragma unroll
                 for (int n = 0; n < TILES; n += 2) { // values 2 n % 8 .. + 3 of block n / 4
                     const float a = of(base[nt][n / 4 / PER]);
-                    const float4 v = make_float4(fmaf(of(o[nt][n][0]), f_even, a), fmaf(of(o[nt][n][1]), f_odd, a),
-                                                 fmaf(of(o[nt][n + 1][0]), f_even, a), fmaf(of(o[nt][n + 1][1]), f_odd, a));
+                    const float4 v = make_float4(fmaf(of(o[nt][n][0]) * EVEN, ref, a), fmaf(of(o[nt][n][1]) * ODD, ref, a),
+                                                 fmaf(of(o[nt][n + 1][0]) * EVEN, ref, a), fmaf(of(o[nt][n + 1][1]) * ODD, ref, a));
                     *reinterpret_cast<float4 *>(mine + 64 * (n / 4) + 2 * (n % 4)) = v;
                 }
                 if (g == 0) {
