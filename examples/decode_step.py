@@ -209,7 +209,9 @@ class TokenStep:
         self.tokens = torch.randint(0, vocab, (batch,), generator=g, device=DEV, dtype=torch.int32)
 
     def step(self, uniform):
-        x = self.layer.step(self.embedding.index_select(0, self.tokens))
+        # A row that got no token (-1: no logit above -inf, or a setting out of range) goes on with token 0: an index
+        # below 0 would end the process.
+        x = self.layer.step(self.embedding.index_select(0, self.tokens.clamp(min=0)))
         self.tokens.copy_(self.sampler(x, uniform))
         return self.tokens
 
@@ -254,7 +256,7 @@ def main(argv=None):
         bits |= int(chain.sampler.status.item())
     print(f"{args.steps} steps of {args.batch} sequences: {start.elapsed_time(end) / args.steps * 1e3:.1f} us a step, "
           f"lengths now {layer.lens.tolist()}, device status {bits}, " +
-          (f"tokens {state.tolist()}" if args.kv4 else f"|x| {float(state.float().abs().mean()):.3f}"))
+          (f"tokens {state.tolist()}, rows without a token {int((state < 0).sum())}" if args.kv4 else f"|x| {float(state.float().abs().mean()):.3f}"))
 
 
 if __name__ == "__main__":
