@@ -167,6 +167,14 @@ __device__ __forceinline__ constexpr uint32_t lowest_key() // of -inf
     return BF ? 0x007Fu : 0x03FFu;
 }
 
+// Eight keys of -inf: what lies past a slice.
+template <bool BF>
+__device__ __forceinline__ uint4 no_keys()
+{
+    constexpr uint32_t TWO = lowest_key<BF>() * 0x10001u;
+    return make_uint4(TWO, TWO, TWO, TWO);
+}
+
 // P of logits, in units of 2^-43.
 template <bool BF>
 struct Share {
@@ -253,15 +261,16 @@ __device__ __forceinline__ uint32_t pick(const uint32_t (&w)[4], int e)
 }
 
 // Whether some lane's eight keys are all at least `least`, or more than SAMPLE_SPARSE of them; if not, `which` of them are.
+// All lanes of a warp take part.
 __device__ __forceinline__ bool dense(const uint4 &k, uint32_t least, uint32_t &which)
 {
     const uint32_t m = __vminu2(__vminu2(k.x, k.y), __vminu2(k.z, k.w));
     which = 0;
-    if (__any_sync(__activemask(), min(m & 0xFFFFu, m >> 16) >= least))
+    if (__any_sync(0xffffffffu, min(m & 0xFFFFu, m >> 16) >= least))
         return true;
     const uint32_t w[4] = {k.x, k.y, k.z, k.w};
     which = at_least(w, least);
-    return __any_sync(__activemask(), __popc(which) > SAMPLE_SPARSE);
+    return __any_sync(0xffffffffu, __popc(which) > SAMPLE_SPARSE);
 }
 
 // The largest of eight keys.
@@ -379,8 +388,9 @@ struct Sampler {
         const int copy = threadIdx.x % SAMPLE_COPIES;
         constexpr uint32_t least = lowest_key<BF>() + 1;
         clear(sums);
-        for (int v = threadIdx.x; v < vectors; v += SAMPLE_THREADS) {
-            const uint4 k4 = keys[v];
+        for (int first = threadIdx.x & ~31; first < vectors; first += SAMPLE_THREADS) { // (the same turns in all lanes)
+            const int v = first + (threadIdx.x & 31);
+            const uint4 k4 = v < vectors ? keys[v] : no_keys<BF>();
             const uint32_t w[4] = {k4.x, k4.y, k4.z, k4.w};
             uint32_t which;
             if (!dense(k4, least, which)) { // most are masked: the others one by one
@@ -800,9 +810,7 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
     uint32_t at_it = 0;
     for (int st = from; st < to; ++st) {
         const int v = st * 32 + lane;
-        if (v >= vectors)
-            break;
-        const uint4 k4 = keys[v];
+        const uint4 k4 = v < vectors ? keys[v] : no_keys<BF>();
         const uint32_t w[4] = {k4.x, k4.y, k4.z, k4.w};
         uint32_t which;
         if (threshold)
