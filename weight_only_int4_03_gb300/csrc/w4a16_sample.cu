@@ -198,7 +198,8 @@ struct Share {
     __device__ __forceinline__ void operator()(uint32_t keys, unsigned long long &first, unsigned long long &second) const
     {
         const float2 l = numbers_of<BF>(keys), t = both(top);
-        const float2 d = sub(t, l), rest = sub(sub(t, d), l); // d + rest is the difference
+        // d + rest is the difference, exactly, whichever of the two is the larger one in size.
+        const float2 d = sub(t, l), minus = sub(d, t), rest = sub(sub(t, sub(d, minus)), add(l, minus));
         const float2 y = mul(d, both(c_hi));
         const float2 y_lo = add(fma(d, both(c_hi), make_float2(-y.x, -y.y)), fma(d, both(c_lo), mul(rest, both(c_hi))));
         const float2 kk = fma(y, both((float)SAMPLE_TABLE), both(SAMPLE_ROUND)), k = add(kk, both(-SAMPLE_ROUND));
