@@ -570,7 +570,7 @@ int w4a16_kv4_attention(const void *q, int ldq, const void *cache, long long pag
  *                alignment are read in 16-byte loads); a NaN counts as -inf, and -inf is never chosen
  *   uniform      device fp32 [batch], in [0, 1)
  *   temperature  device fp32 [batch] or NULL (1): 0 .. 2^100; 0 takes the largest logit (the lowest index
- *                where some are equal) whatever the other settings
+ *                where some are equal) whatever the other settings; others below 2^-126 count as 2^-126
  *   top_k        device int32 [batch] or NULL: 0 and below: no limit
  *   top_p, min_p device fp32 [batch] or NULL (1, 0): top_p of 1 and above and min_p of 0 and below: no limit; min_p
  *                above 1 counts as 1

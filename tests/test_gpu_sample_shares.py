@@ -36,6 +36,22 @@ def test_logits_far_below_a_largest_near_zero(w4, dtype, top_k):  # noqa: F811
     assert int((got[:n] != 0).sum()) == 0 and int((got[n:] != 1).sum()) == 0, (int((got[:n] != 0).sum()), int((got[n:] != 1).sum()))
 
 
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_the_smallest_temperatures(w4, dtype):  # noqa: F811
+    """Temperatures below 2^-126 count as 2^-126, at which only bf16's subnormal numbers are near one another."""
+    import torch
+    heat = [2.0 ** -126, 2.0 ** -125, 2.0 ** -149, 1e-40, 2.0 ** -120]
+    case = Case(2, dtype, 60, 300, temperature=heat, top_k=[0, 40], top_p=[1.0, 0.8, 0.9])
+    bits = torch.randint(0, 100, (60, 300), generator=torch.Generator(device="cuda").manual_seed(3), device="cuda")
+    case.logits[:] = bits.short().view(case.logits.dtype)  # subnormal numbers
+    case.logits[::7, 5] = 1.0
+    case.run(w4)
+    torch.cuda.synchronize()
+    case.settings["temperature"].clamp_(min=2.0 ** -126)
+    case.check()
+    assert int(case.status.item()) == 0
+
+
 @pytest.mark.parametrize("vocab", [8 * 33, 8 * 31 + 3, 4096 + 8 * 5, 8 * 512 * 3 + 8 * 40 + 1, 50001, 131063])
 @pytest.mark.parametrize("masked", [0.5, 0.9, 0.997])
 def test_masked_rows_that_end_inside_a_warp(w4, vocab, masked):  # noqa: F811

@@ -44,7 +44,8 @@ constexpr int SAMPLE_FEW = 128;        // top_k up to which the tokens in questi
 constexpr int SAMPLE_LIST = 1024;      // of these, at most
 constexpr float SAMPLE_ROUND = 12582912.f; // rounds what is added to it to integers (ties to even), in its lowest bits
 constexpr uint32_t SAMPLE_ROUND_BITS = 0x4B400000u;
-constexpr float SAMPLE_HOTTEST = 0x1p100f; // temperature, at most
+constexpr float SAMPLE_HOTTEST = 0x1p100f;  // temperature, at most
+constexpr float SAMPLE_COLDEST = 0x1p-126f; // what temperatures below count as (log2(e) / T is then still in fp32)
 
 // 2^31 2^(-j/256).
 __device__ const uint32_t SAMPLE_EXP[SAMPLE_TABLE] = {
@@ -662,12 +663,11 @@ __global__ void __launch_bounds__(SAMPLE_THREADS, 2) sample_kernel(const SampleP
     constexpr uint32_t ZERO = 0x8000u; // the key of 0
     Sampler<BF> f{s, keys, vectors, cluster, {}, 0};
     f.share.top = infinite ? 0.f : numbers_of<BF>(best).x;
-    // log2(e) = LOG + LOG_LO over T.  (The smallest temperatures' inverse is cut to what fp32 holds: every other logit's P
-    // is 0 by far.)
+    // log2(e) = LOG + LOG_LO over T.
     constexpr float LOG = 1.44269502162933349609375f, LOG_LO = 1.92596299112661747e-8f;
-    const float t = greedy ? 1.f : temperature, c = LOG / t;
-    f.share.c_hi = fminf(c, 1e38f);
-    f.share.c_lo = c < 1e38f ? (fmaf(-c, t, LOG) + LOG_LO) / t : 0.f;
+    const float t = greedy ? 1.f : fmaxf(temperature, SAMPLE_COLDEST), c = LOG / t;
+    f.share.c_hi = c;
+    f.share.c_lo = (fmaf(-c, t, LOG) + LOG_LO) / t;
     f.share.exp = s.exp;
     const unsigned long long part = fraction(min_p);
     const unsigned long long least =
