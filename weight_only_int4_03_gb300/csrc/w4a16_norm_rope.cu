@@ -732,8 +732,12 @@ __global__ void __launch_bounds__(32 * NORM_WARPS) norm_rope_any_kernel(const No
         } else {
             long long pg;
             int in_page;
-            if (!page_of(p, p.slots[token], pg, in_page))
+            if (!page_of(p, p.slots[token], pg, in_page)) {
+                if (kind == KIND_K) // its positions are looked at all the same
+                    for (int i = lane; i < p.rot / 2; i += 32)
+                        checked_position(p, p.positions[(long long)axis_of(p, i) * p.ld_pos + token]);
                 continue;
+            }
             dst = (kind == KIND_K ? p.k_cache : p.v_cache) + pg * p.page_stride + in_page * p.token_stride +
                   h * p.head_stride;
         }
