@@ -6,6 +6,40 @@ from test_gpu_norm_rope import Case, w4  # noqa: F401  (a fixture)
 pytestmark = pytest.mark.gpu
 
 
+FORMS = [
+    dict(tokens=50, heads=8, kv=2, dim=128, rot=128, sections=[64]),
+    dict(tokens=1500, heads=8, kv=2, dim=128, rot=128, sections=[64]),                    # a prompt
+    dict(tokens=1500, heads=8, kv=2, dim=128, rot=128, sections=[64], adjacent=True),
+    dict(tokens=40, heads=4, kv=1, dim=64, rot=32, sections=[16], adjacent=True),
+    dict(tokens=1100, heads=4, kv=2, dim=256, rot=128, sections=[13, 30, 21]),             # cuts inside eight pairs
+    dict(tokens=1100, heads=4, kv=2, dim=128, rot=128, sections=[13, 30, 21], adjacent=True),
+    dict(tokens=60, heads=3, kv=2, dim=100, rot=36, sections=[11, 7]),                     # without 16-byte copies
+    dict(tokens=60, heads=3, kv=2, dim=100, rot=36, sections=[11, 7], adjacent=True),
+    dict(tokens=900, heads=5, kv=3, dim=128, rot=128, sections=[64], pad=1),
+    dict(tokens=30, heads=5, kv=3, dim=128, rot=64, sections=[32], shift=1, skip=(4,)),
+]
+
+
+@pytest.mark.parametrize("kw", FORMS, ids=lambda c: f"t{c['tokens']}d{c['dim']}r{c['rot']}s{len(c['sections'])}"
+                         f"{'a' if c.get('adjacent') else ''}{'u' if c.get('pad') or c.get('shift') else ''}")
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_without_weights_the_bits_of_the_rotary_append(w4, dtype, kw):  # noqa: F811
+    import torch
+    case = Case(8, dtype, page=16, q_norm=False, k_norm=False, **kw)
+    case.run(w4)
+    q, k, v = torch.full_like(case.q_out, 7.0), torch.full_like(case.k_cache, 5.0), torch.full_like(case.v_cache, 5.0)
+    ld, h, kv, d = case.qkv.shape[1], case.heads, case.kv, case.dim
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    w4.w4a16_rope_append(case.qkv, case.qkv[:, h * d:], case.qkv[:, (h + kv) * d:], q, k, v, case.table, case.positions,
+                         case.slots, status, case.tokens, h, kv, d, case.rot, case.sections, case.max_pos, 16, case.n_pages,
+                         case.flags(w4), ldq=ld, ldk=ld, ldv=ld, ldqo=q.shape[1])
+    torch.cuda.synchronize()
+    assert torch.equal(v, case.v_cache)
+    assert torch.equal(q, case.q_out), int((q != case.q_out).sum())
+    assert torch.equal(k, case.k_cache), int((k != case.k_cache).sum())
+    assert int(case.status.item()) == 0 and int(status.item()) == 0
+
+
 @pytest.mark.parametrize("pad", [0, 1], ids=["wide", "any"])
 @pytest.mark.parametrize("heads", [0, 2])
 @pytest.mark.parametrize("slot", [-1, "past"])

@@ -99,7 +99,8 @@ __device__ __forceinline__ const uint16_t *head_src(const NormParams &p, int kin
     return base + (long long)token * ld + (long long)h * p.dim;
 }
 
-// The rotation, in the same roundings wherever it is used.
+// The rotation of the any-size kernel, in the roundings of w4a16_rope_append's any-size kernel (the 16-byte paths round
+// the other product of the second value).
 __device__ __forceinline__ float turned_first(float a, float b, float c, float s)
 {
     return fmaf(a, c, -(b * s));
@@ -107,7 +108,7 @@ __device__ __forceinline__ float turned_first(float a, float b, float c, float s
 
 __device__ __forceinline__ float turned_second(float a, float b, float c, float s)
 {
-    return fmaf(b, c, a * s);
+    return fmaf(a, s, b * c);
 }
 
 // The smaller and the larger of two values, NaN where one is.
