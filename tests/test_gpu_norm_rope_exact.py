@@ -17,6 +17,9 @@ FORMS = [
     dict(tokens=60, heads=3, kv=2, dim=100, rot=36, sections=[11, 7], adjacent=True),
     dict(tokens=900, heads=5, kv=3, dim=128, rot=128, sections=[64], pad=1),
     dict(tokens=30, heads=5, kv=3, dim=128, rot=64, sections=[32], shift=1, skip=(4,)),
+    dict(tokens=300, heads=3, kv=1, dim=576, rot=576, sections=[288]),                     # heads wider than 512
+    dict(tokens=300, heads=3, kv=1, dim=1024, rot=64, sections=[5, 27], adjacent=True),
+    dict(tokens=300, heads=3, kv=1, dim=576, rot=64, sections=[32], pad=1),
 ]
 
 

@@ -49,6 +49,7 @@ struct NormParams {
     int tokens, heads, kv, dim, rot, axes, max_pos, page;
     int cut[NORM_MAX_AXES]; // pair i belongs to the first axis a with i < cut[a]
     int adjacent, cuts; // cuts: some section ends inside eight pairs
+    int copies16; // everything can be copied 16 bytes at a time
 };
 
 enum { KIND_Q = 0, KIND_K = 1, KIND_V = 2 };
@@ -99,16 +100,17 @@ __device__ __forceinline__ const uint16_t *head_src(const NormParams &p, int kin
     return base + (long long)token * ld + (long long)h * p.dim;
 }
 
-// The rotation of the any-size kernel, in the roundings of w4a16_rope_append's any-size kernel (the 16-byte paths round
-// the other product of the second value).
+// The rotation of the any-size kernel.  It serves sizes without 16-byte copies, and heads that are too wide for the 16-byte
+// kernel here but not for w4a16_rope_append's; the two kernels of that round different products of a pair's second value,
+// and so does this one.
 __device__ __forceinline__ float turned_first(float a, float b, float c, float s)
 {
     return fmaf(a, c, -(b * s));
 }
 
-__device__ __forceinline__ float turned_second(float a, float b, float c, float s)
+__device__ __forceinline__ float turned_second(float a, float b, float c, float s, bool copies16)
 {
-    return fmaf(a, s, b * c);
+    return copies16 ? fmaf(b, c, a * s) : fmaf(a, s, b * c);
 }
 
 // The smaller and the larger of two values, NaN where one is.
@@ -774,7 +776,7 @@ __global__ void __launch_bounds__(32 * NORM_WARPS) norm_rope_any_kernel(const No
                         continue;
                     const float c = p.table[(long long)pos * p.rot + i], s = p.table[(long long)pos * p.rot + half + i];
                     const float z = turned_first(x, y, c, s);
-                    y = turned_second(x, y, c, s);
+                    y = turned_second(x, y, c, s, p.copies16);
                     x = z;
                 }
                 ra = from_float<BF>(x);
@@ -850,7 +852,7 @@ int check_buffers(const NormParams &p)
 bool wide(const NormParams &p)
 {
     const long long any = (p.heads ? (long long)(p.ldq | p.ldqo) : 0) | (p.kv ? p.ldk | p.ldv : 0);
-    return p.dim % 16 == 0 && p.rot % 16 == 0 && p.dim <= 512 && any % 8 == 0 && aligned(p.q, 16) && aligned(p.k, 16) &&
+    return p.dim % 16 == 0 && p.rot % 16 == 0 && any % 8 == 0 && aligned(p.q, 16) && aligned(p.k, 16) &&
            aligned(p.v, 16) && aligned(p.q_out, 16) && aligned(p.q_norm, 16) && aligned(p.k_norm, 16) &&
            aligned(p.table, 16);
 }
@@ -975,7 +977,8 @@ extern "C" int w4a16_norm_rope_append(const void *q, int ldq, const void *k, int
     set_cuts(p, sections);
     const bool bf = (flags & W4A16_FLAG_BF16) != 0;
     const long long strides = n_kv_heads ? kv_page_stride | kv_token_stride | kv_head_stride : 0;
-    if (wide(p) && strides % 8 == 0 && aligned(p.k_cache, 16) && aligned(p.v_cache, 16))
+    p.copies16 = wide(p) && strides % 8 == 0 && aligned(p.k_cache, 16) && aligned(p.v_cache, 16);
+    if (p.copies16 && head_dim <= 512)
         return head_dim <= 64    ? launch_type<0, 4>(bf, p, stream)
                : head_dim <= 128 ? launch_type<0, 8>(bf, p, stream)
                : head_dim <= 256 ? launch_type<0, 16>(bf, p, stream)
