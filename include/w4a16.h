@@ -523,7 +523,8 @@ int w4a16_norm_rope_append(const void *q, int ldq, const void *k, int ldk, const
 /* Bytes of one head's record in a page, a multiple of 16; 0 for sizes that the cache does not take. */
 size_t w4a16_kv4_record_bytes(int page_size, int head_dim, int group_size);
 
-/* w4a16_norm_rope_append into a cache held in 4 bits: keys are coded from the fp32 results of norm and rotation.
+/* w4a16_norm_rope_append into a cache held in 4 bits.  Keys are coded from norm and rotation in two fp32 parts: steps and
+ * bases are those of exact arithmetic, and so are codes but for about three in 10^8, next to a border.
  * As w4a16_norm_rope_append, but for:
  *   cache        device, 16-byte aligned; page_stride in bytes, a multiple of 16, at least n_kv_heads records
  *   k_out, v_out device 16-bit, token t's heads at t * ldko (ldvo), or NULL: what the cache now stands for, rounded

@@ -5,7 +5,7 @@
 //     y = x rsqrt(mean x^2 + eps) w,
 // then pair i < rot_dim / 2 is turned by its position's angle, (y1, y2) -> (y1 c - y2 s, y2 c + y1 s), as
 // w4a16_rope_append does.  All in fp32; q, and k and v of the 16-bit cache, are rounded once.  In the
-// 4-bit cache a group of values is coded from the fp32 results:
+// 4-bit cache a group of values is coded, keys from norm and rotation in two fp32 parts:
 //     b = r(min),  s = r((max - min) / 15),  code = (x - b) / s to the nearest integer, ties to even, in 0..15
 // (r: to the cache's 16-bit type), which stands for code s + b.
 //
@@ -17,8 +17,9 @@
 // axes into 4 bits (groups of 64, with k_out and v_out): 52 us, 4.1 TB/s; one token 3.2 us of latencies.
 //
 // Codes are those of exact arithmetic: a value next to the border of two codes, or a base or step next to the border of
-// two 16-bit numbers, would fall on either side in fp32 (measured: two keys in 10^6).  So keys that are to be coded are
-// computed in two fp32 parts throughout, from the sum of squares to the remainder of the division (one key in 10^7).
+// two 16-bit numbers, would fall on either side in fp32 (measured: four codes in 10^7, and a base or step in 10^4 groups).
+// So keys that are to be coded are computed in two fp32 parts throughout, from the sum of squares to the remainder of the
+// division, whose last roundings leave 2^-25 of a step: three codes in 10^8, and no base or step (of 10^7 groups).
 #include <type_traits>
 
 #include "w4a16_kv4.cuh"
