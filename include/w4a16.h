@@ -549,10 +549,11 @@ size_t w4a16_kv4_attention_workspace_size(int batch, int n_heads, int n_kv_heads
 /* w4a16_paged_attention over a cache held in 4 bits, whose values code s + b are used as they are: products and sums
  * are fp32, no key or value is rounded to 16 bits.  q and out are fp16, or bf16 with W4A16_FLAG_BF16, as are the
  * cache's steps and bases.  As w4a16_paged_attention, but for the cache (above) and these points: queries go in as fp16
- * scaled by a power of two per head, exact down to 2^-38 of the head's largest (in bf16, queries beyond 2^112 are too
- * large); p s goes into the value product to 2^-22 of itself, or to 2^-38 of the largest step of the values seen.  Sums of p
- * times a value are divided by the sum of p at the end, and have to stay within fp32 until then.  A group
- * that reads as NaN makes NaN of what it touches.  page_size at most W4A16_KV4_MAX_PAGE. */
+ * scaled by a power of two per head, off by at most 2^-34 of the head's largest, or 2^-121 (fp16 is exact above 2^-23 of
+ * the largest, bf16 above 2^-26; in bf16, queries beyond 2^112 are too large); p s goes into the value product to 2^-22
+ * of itself, or to 2^-38 of the largest step of the values seen.  Sums of p times a value are divided by the sum of p at
+ * the end, and have to stay within fp32 until then.  A group that reads as NaN makes NaN of what it touches.  page_size
+ * at most W4A16_KV4_MAX_PAGE. */
 int w4a16_kv4_attention(const void *q, int ldq, const void *cache, long long page_stride, void *out,
                         int ldo, float *lse, const int32_t *block_table, int ld_table,
                         const int32_t *seq_lens, void *workspace, size_t workspace_bytes, int batch,

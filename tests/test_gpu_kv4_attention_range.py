@@ -70,3 +70,18 @@ def test_values_of_the_types_whole_range(w4, dim, group_size, sigma):  # noqa: F
     case.run(ws)
     check(case)
     assert w4.w4a16_status(ws) == 0
+
+
+@pytest.mark.parametrize("dtype,low", [("fp16", -14), ("bf16", -40)])
+def test_queries_of_a_wide_range(w4, dtype, low):  # noqa: F811
+    """Sizes from 2^low to 1 inside a head (and heads of different sizes), the largest at even and at odd places."""
+    import torch
+    case = Case(w4, 34, dtype, [5, 200], 16, 2, 128, 16, 64, sigma=64.0)
+    g = torch.Generator(device="cuda").manual_seed(35)
+    size = torch.exp2(low * torch.rand((2, 16, 128), generator=g, device="cuda"))
+    size[:, ::2, ::2] *= 2.0 ** -10
+    size[:, 1::2, 1::2] *= 2.0 ** -10
+    case.q.copy_((torch.randn((2, 16, 128), generator=g, device="cuda") * size).to(case.q.dtype).view(2, -1))
+    ws = case.workspace()
+    case.run(ws)
+    check(case)

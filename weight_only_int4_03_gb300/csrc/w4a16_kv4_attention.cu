@@ -12,8 +12,8 @@
 //   - A code is the fp16 number q 2^-24 (or q 2^-20, four bits higher) as soon as the others are masked
 //     off, so that a pair costs one instruction and a shift for every second.  Values q 2^-20 meet queries a
 //     sixteenth as large, and outputs of their own factor.  That holds for fp16 alone, so queries are
-//     scaled to fp16 by a power of two per head (their values are exact down to 2^-38 of the largest), whatever
-//     the cache's type.
+//     scaled to fp16 by a power of two per head (the largest to 2^13 or more, half of them to a sixteenth of that: off by at
+//     most 2^-34 of the largest), whatever the cache's type.
 //   - Positions are the rows of the score product (S^T = K Q^T) and value dims those of the value product
 //     (O^T = V^T P^T), so that eight heads fill an m16n8k16.  P^T is the scores' fragment transposed by
 //     movmatrix.  p s goes in as fp16, times a power of two that keeps it below 2^15, and the 16-bit remainder: 2^-22 of
