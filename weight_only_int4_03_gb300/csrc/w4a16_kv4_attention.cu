@@ -30,7 +30,9 @@
 // 16-bit cache's bytes would take 327 us at the copy rate); one of 131071 with 40 / 8 heads and groups of 64 44 us, 3.4
 // TB/s, of which about 10 us pass before the first rows and in the join; fp16, 24 sequences of 5 to 9000 with a window of
 // 2048, 12 / 12 heads of 64: 14.2 us, of which most is the start and the join; one of 41 positions: 5.6 us of latencies.
-// Per 16 positions of 128 values: 8 score MMAs, 16 value MMAs and two for the start of each group, 88 conversions of codes.
+// Per 16 positions of 128 values: 8 score MMAs, 16 value MMAs and two for the start of each group, 88 conversions of codes;
+// with eight warps per SM, which is what the registers allow, the issue slots are 49 % busy, the ALU 48 %, the MMA pipe 41 %.
+// Heads of 256 spill (up to 100 bytes) and take eight heads at a time: a KV head of 16 is read twice.
 // The work is split as in the 16-bit cache's attention (w4a16_split.cuh).
 #include <type_traits>
 
@@ -69,7 +71,7 @@ struct Kv4Geom {
     static constexpr int SUB = 2 * KEYS + 2 * PARAMS;
     // Sub-steps of 16 positions that a warp takes at once: what a step costs by itself (pages, the vote, adding up the
     // outputs) is shared by them, and more of them are in one another's shadow, as far as the registers go (one group: the 48
-    // sequences take 123 us with four, 129 with two; groups of 64, which spill with four: the long one 46 and 44).
+    // sequences take 123 us with four, 129 with two; groups of 64, which spill with four: 152 and 143).
     static constexpr int SUBS = D == 128 && NT == 1 && G == 1 ? 4 : 2;
     static constexpr int STEP = 16 * SUBS;
     static constexpr int UNIT = SPLIT_WARPS * STEP;    // positions per work unit: a step of each warp

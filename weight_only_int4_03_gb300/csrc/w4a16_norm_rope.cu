@@ -13,8 +13,8 @@
 // values (eight pairs) each, which meet in shuffles for the sum of squares and for the groups' smallest and largest
 // values; a warp works on 32 / that many heads of one kind, with the next ones' values on their way, and a block on a
 // token.  Arithmetic goes two values to an instruction, as instructions are what the 4-bit kernel is bound by.
-// 6007 tokens of 32 / 8 heads of 128, bf16, 16-bit cache: 29.6 us, 5.1 TB/s of reads and writes; 8191 tokens with three
-// axes into 4 bits (groups of 64, with k_out and v_out): 52 us, 4.1 TB/s; one token 3.2 us of latencies.
+// 6007 tokens of 32 / 8 heads of 128, bf16, 16-bit cache: 29.5 us, 5.1 TB/s of reads and writes; 8191 tokens with three
+// axes into 4 bits (groups of 64, with k_out and v_out): 52 us, 4.1 TB/s (that kernel spills 104 bytes at its 96 registers); one token 3.2 us of latencies.
 //
 // Codes are those of exact arithmetic: a value next to the border of two codes, or a base or step next to the border of
 // two 16-bit numbers, would fall on either side in fp32 (measured: four codes in 10^7, and a base or step in 10^4 groups).
@@ -618,7 +618,7 @@ __device__ __forceinline__ void coded_head(const NormParams &p, const TokenOf &t
 }
 
 // 16-byte path: a block per token, of a warp where there are many (what belongs to a token is then looked up once for
-// all of its heads: 6007 tokens of 32 / 8 heads of 128 take 29.2 us, 31.3 with two warps a block and 36.1 with four), of as
+// all of its heads: 6007 tokens of 32 / 8 heads of 128 take 29.5 us, 2 more with two warps a block and 7 with four), of as
 // many as it has items where all of these run at once (FEW).  Thread j of a head's LANES: chunk j < rot / 16 of q and k is eight pairs, any
 // other 16 values in a row; threads past dim / 16, and past a kind's heads, only take part in the shuffles.  A warp
 // takes items of 32 / LANES heads of one kind, q_items of q, then kv_items of k, then as many of v.  GROUPS: groups of

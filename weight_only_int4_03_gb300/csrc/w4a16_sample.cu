@@ -18,10 +18,11 @@
 // Where neither top-k nor top-p nor min-p limits a row there is no histogram.  Last, each warp sums its own range of
 // indices, and the warp whose range holds u walks it; below the threshold no P is computed.
 //
-// What bounds it: for few rows the chain of cluster barriers, for many the instructions per logit (about thirty for a P).
-// Measured (device): one row of 32000 7.5 us; 48 x 131071 with all kinds of limits 41 (a row with top-p alone takes
-// about 22 by itself: a P and the histogram's atomics for each logit); 32 x 256000 without top-k or top-p 31; 256 x 100003
-// nine tenths masked 83, 7 us of which the reading would take.  64-bit atomics in the histogram instead of three of 32
+// What bounds it: for few rows the chain of cluster barriers, for many the instructions: 62 per logit where nothing limits a
+// row (about thirty of them for its P, the rest for keys, votes and sums), 47 per logit where nine tenths are masked.
+// Measured (device): one row of 32000 7.5 us; 48 x 131071 with all kinds of limits 42 (a row with top-p alone takes
+// about 22 by itself: a P and the histogram's atomics for each logit); 32 x 256000 without limits 31.5; 256 x 100003
+// nine tenths masked 84, 7 us of which the reading would take.  64-bit atomics in the histogram instead of three of 32
 // bits: 96 for the second; 256 or 1024 threads: slower.
 #include <cooperative_groups.h>
 
@@ -972,7 +973,7 @@ extern "C" int w4a16_sample(const void *logits, int ld, const float *uniform, co
     if (err != cudaSuccess)
         return status_of(STAGE_RESOURCE, err);
     // Blocks of a row: up to three an SM in all, of which two run at once (rows differ in work: 48 mixed rows of 131071
-    // take 43.6 us with eight blocks, 48.3 with the six that run in one go, 58 with four); no slices below 4096 logits (one
+    // took, one after the other, 43.6 us with eight blocks, 48.3 with the six that run in one go, 58 with four); no slices below 4096 logits (one
     // row of 32000 takes 7.5 us with 4096, 8.1 with 8192), nor above 32768 where eight blocks allow, so that two blocks fit
     // an SM's shared memory (256 masked rows of 100003: 85 us with four blocks, 109 with seven, 115 with two).
     const long long at_once = 3LL * num_sms / batch, useful = (vocab + 4095) / 4096, needed = (vocab + 32767) / 32768;
