@@ -85,3 +85,35 @@ def test_queries_of_a_wide_range(w4, dtype, low):  # noqa: F811
     ws = case.workspace()
     case.run(ws)
     check(case)
+
+
+@pytest.mark.parametrize("dim,group_size", [(128, -1), (128, 64), (64, -1), (256, 128)])
+def test_long_sums_lean_to_neither_side(w4, dim, group_size):  # noqa: F811
+    """The mean error of the outputs over a long sequence, at even and at odd places (whose codes go in at other sizes).
+
+    Weights within 2^5 of one another in any 32 positions: products of codes (4 bits from 2^-22) and first parts of p s (11 bits) are multiples of
+    2^-32 2^-5 = 2^-37 of the largest, which 24 bits from 2^-14 of it hold, so their sums are exact, and the remainders' are cut
+    2^-11 below.  What is left are roundings to nearest, of fp32 and of the outputs: the latter, spread evenly over half a
+    unit each, have a mean square of (2^-11 out)^2 / 3 at most, and their mean over N outputs a standard deviation of
+    2^-11 rms(out) / sqrt(3 N).  Five of these are allowed.
+    """
+    import torch
+    case = Case(w4, 36, "fp16", [131071], 32, 8, dim, 64, group_size, q_sigma=0.3)
+    ws = case.workspace()
+    case.run(ws)
+    torch.cuda.synchronize()
+    codes, params = (x.flatten(1, 2) for x in kv4.read(case.cache, 64, 8, dim, group_size, "fp16"))
+    at, off, ref = case.slots[0], [], []
+    for c in range(8):
+        k, v = (kv4.values(codes[s][at, c], params[s][at, c]) for s in range(2))
+        q = case.q[0].view(8, 4, dim)[c].double()
+        p = torch.softmax(q @ k.t() * case.scale, -1)
+        ref.append(p @ v)
+        off.append(case.out[0].view(8, 4, dim)[c].double() - ref[-1])
+        near = p[:, :131040].unflatten(-1, (-1, 32))
+        assert float((near.amax(-1) / near.amin(-1)).max()) < 2.0 ** 5
+    off, ref = torch.cat(off), torch.cat(ref)
+    for place in range(2):
+        x = off[:, place::2]
+        limit = 5 * 2.0 ** -11 * float(ref.pow(2).mean().sqrt()) / (3 * x.numel()) ** 0.5
+        assert abs(float(x.mean())) <= limit, (place, float(x.mean()) / limit)

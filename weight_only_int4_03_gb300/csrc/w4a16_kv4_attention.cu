@@ -10,29 +10,33 @@
 // Bound by memory in principle, by instructions in fact: a position of a KV head of 128 is 136 bytes,
 // which at the copy rate leaves an SM 6 cycles for it.  What the design does about it:
 //   - A code is the fp16 number q 2^-24 (or q 2^-20, four bits higher) as soon as the others are masked
-//     off, so that a pair costs one instruction and a shift for every second.  Values q 2^-20 meet queries a
+//     off, so that a pair of keys costs one instruction and a shift for every second.  Values q 2^-20 meet queries a
 //     sixteenth as large, and outputs of their own factor.  That holds for fp16 alone, so queries are
 //     scaled to fp16 by a power of two per head (the largest to 2^13 or more, half of them to a sixteenth of that: off by at
 //     most 2^-34 of the largest), whatever the cache's type.
+//   - Values are taken two bits higher, q 2^-22 and q 2^-18, which costs a shift more: the tensor core aligns products by
+//     their operands' exponents, a subnormal operand's being that of 2^-14, and cuts off what lies below the sum's 24 bits
+//     or so from there.  For the same reason p s and its remainder have sums of their own, which only add exact products.
+//     (With codes at 2^-24 and one chain for both, 36 % of the fp16 outputs over 131071 positions were not the formula's
+//     rounded, all off in one direction; 1.5 % now.  That took 123 us instead of 129 for the 48 sequences below.)
 //   - Positions are the rows of the score product (S^T = K Q^T) and value dims those of the value product
 //     (O^T = V^T P^T), so that eight heads fill an m16n8k16.  P^T is the scores' fragment transposed by
 //     movmatrix.  p s goes in as fp16, times a power of two that keeps it below 2^15, and the 16-bit remainder: 2^-22 of
 //     itself down to 2^-16 of the largest step's, and 2^-38 of that below.  (Without the remainder, in bf16, the two long
 //     cases below took 38 and 106 us; 2^-11 shows where outputs nearly cancel.)
-//   - The maximum is lazy: it moves only when a score passes it by a factor of 4, and a step of 32 or 64 positions
+//   - The maximum is lazy: it moves only when a score passes it by a factor of 4, and a step of 32 positions
 //     asks for that by one vote; sums of p and of p a are kept per lane until the end.
 //   - A value product starts from -8 sum p s (an MMA against constants makes it) and is added to the outputs in
 //     fp32 every step: the MMA cuts sums off, which over many positions of one sign would show.
 //   - The words of a row lie in the order of the lanes, so that a lane's share of a row is one load; keys are
 //     copied to places that only the copying lane reads.  Where pages hold multiples of 16 positions, a page is
 //     looked up once for 16 of them, and masks are applied only in steps that have something to mask.
-// bf16, 128 wide: 48 sequences of 2048 to 32768 positions, 64 / 8 heads, 123 us, 4.8 TB/s of codes and parameters (the
-// 16-bit cache's bytes would take 327 us at the copy rate); one of 131071 with 40 / 8 heads and groups of 64 44 us, 3.4
+// bf16, 128 wide: 48 sequences of 2048 to 32768 positions, 64 / 8 heads, 129 us, 4.6 TB/s of codes and parameters (the
+// 16-bit cache's bytes would take 327 us at the copy rate); one of 131071 with 40 / 8 heads and groups of 64 45.4 us, 3.3
 // TB/s, of which about 10 us pass before the first rows and in the join; fp16, 24 sequences of 5 to 9000 with a window of
-// 2048, 12 / 12 heads of 64: 14.2 us, of which most is the start and the join; one of 41 positions: 5.6 us of latencies.
-// Per 16 positions of 128 values: 8 score MMAs, 16 value MMAs and two for the start of each group, 88 conversions of codes;
-// with eight warps per SM, which is what the registers allow, the issue slots are 49 % busy, the ALU 48 %, the MMA pipe 41 %.
-// Heads of 256 spill (up to 100 bytes) and take eight heads at a time: a KV head of 16 is read twice.
+// 2048, 12 / 12 heads of 64: 14.3 us, of which most is the start and the join; one of 41 positions: 4.4 us of latencies.
+// Per 16 positions of 128 values: 8 score MMAs, 16 value MMAs and two for the start of each group, 96 conversions of codes.
+// Heads of 256 spill (up to 110 bytes) and take eight heads at a time: a KV head of 16 is read twice.
 // The work is split as in the 16-bit cache's attention (w4a16_split.cuh).
 #include <type_traits>
 
@@ -70,13 +74,13 @@ struct Kv4Geom {
     static constexpr int PARAMS = 16 * 4 * G;          // a sub-step's steps and bases of one side
     static constexpr int SUB = 2 * KEYS + 2 * PARAMS;
     // Sub-steps of 16 positions that a warp takes at once: what a step costs by itself (pages, the vote, adding up the
-    // outputs) is shared by them, and more of them are in one another's shadow, as far as the registers go (one group: the 48
-    // sequences take 123 us with four, 129 with two; groups of 64, which spill with four: 152 and 143).
-    static constexpr int SUBS = D == 128 && NT == 1 && G == 1 ? 4 : 2;
+    // outputs) is shared by them.  Four at once, for 128 wide heads of one group, gain nothing in long rows (128.9 and 129.1
+    // us for the 48 sequences) and lose in short ones (41 positions: 5.5 and 4.4 us); groups of 64 spill with four.
+    static constexpr int SUBS = 2;
     static constexpr int STEP = 16 * SUBS;
     static constexpr int UNIT = SPLIT_WARPS * STEP;    // positions per work unit: a step of each warp
     static constexpr int STAGE = SUBS * SUB;
-    static constexpr int STAGES = D == 256 || SUBS == 4 ? 2 : 3; // (shared memory for two blocks at least)
+    static constexpr int STAGES = D == 256 ? 2 : 3; // (shared memory for two blocks at least)
     static constexpr int CTAS = D * NT > 64 ? 2 : 3;   // blocks per SM
     static_assert(CTAS <= SPLIT_MAX_CTAS, "a counter per block");
     static constexpr int ROW_COST = 4;                 // of a row by itself, in units
@@ -565,8 +569,9 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
                 }
 #pragma unroll
             for (int q = 0; q < G; ++q) {
-                uint32_t hi[SUBS][NT][2], lo[SUBS][NT][2]; // p s in two parts
-                float start[NT][4]; // -8 sum p s, as the codes' rows are scaled
+                // p s in two parts, and -8 sum p s of each, as the codes' rows are scaled.
+                uint32_t ps[2][SUBS][NT][2];
+                float start[2][NT][4];
 #pragma unroll
                 for (int u = 0; u < SUBS; ++u)
 #pragma unroll
@@ -574,17 +579,18 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
                             const float2 a = mul(x[u][nt][r], both(vs[u][r][q] * up));
-                            const uint32_t h = pack2<false>(a.x, a.y);
-                            hi[u][nt][r] = transpose8x8(h);
-                            const float2 rest = sub(a, unpack2<false>(h));
-                            lo[u][nt][r] = transpose8x8(pack2<false>(rest.x, rest.y));
+                            const uint32_t first = pack2<false>(a.x, a.y);
+                            const float2 rest = sub(a, unpack2<false>(first));
+                            ps[0][u][nt][r] = transpose8x8(first);
+                            ps[1][u][nt][r] = transpose8x8(pack2<false>(rest.x, rest.y));
                         }
-                        constexpr uint32_t E = 0x80088008u, S = 0x80808080u; // -8 2^-24 and -8 2^-20, twice
-                        if (u == 0)
-                            mma16816_zero<false>(start[nt], E, S, E, S, hi[u][nt][0], hi[u][nt][1]);
-                        else
-                            mma16816<false>(start[nt], E, S, E, S, hi[u][nt][0], hi[u][nt][1]);
-                        mma16816<false>(start[nt], E, S, E, S, lo[u][nt][0], lo[u][nt][1]);
+                        constexpr uint32_t E = 0x80208020u, S = 0x82008200u; // -8 2^-22 and -8 2^-18, twice
+#pragma unroll
+                        for (int part = 0; part < 2; ++part)
+                            if (u == 0)
+                                mma16816_zero<false>(start[part][nt], E, S, E, S, ps[part][u][nt][0], ps[part][u][nt][1]);
+                            else
+                                mma16816<false>(start[part][nt], E, S, E, S, ps[part][u][nt][0], ps[part][u][nt][1]);
                     }
 #pragma unroll
                 for (int k = 0; k < PER; ++k) {
@@ -599,22 +605,27 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
                         }
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            const uint32_t ml = 0x000f000fu, mh = 0x00f000f0u;
+                            const uint32_t ml = 0x003c003cu, mh = 0x03c003c0u;
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
-                                float d[4];
+                                float d[2][4]; // of either part
 #pragma unroll
                                 for (int u = 0; u < SUBS; ++u) {
-                                    const uint32_t a = w01[u] >> (8 * j), e = w23[u] >> (8 * j);
-                                    if (u == 0)
-                                        mma16816_from(d, a & ml, a & mh, e & ml, e & mh, hi[u][nt][0], hi[u][nt][1], start[nt]);
-                                    else
-                                        mma16816<false>(d, a & ml, a & mh, e & ml, e & mh, hi[u][nt][0], hi[u][nt][1]);
-                                    mma16816<false>(d, a & ml, a & mh, e & ml, e & mh, lo[u][nt][0], lo[u][nt][1]);
+                                    const uint32_t a = j ? w01[u] >> 6 : w01[u] << 2, e = j ? w23[u] >> 6 : w23[u] << 2;
+#pragma unroll
+                                    for (int part = 0; part < 2; ++part) {
+                                        const uint32_t(&w)[2] = ps[part][u][nt];
+                                        if (u == 0)
+                                            mma16816_from(d[part], a & ml, a & mh, e & ml, e & mh, w[0], w[1], start[part][nt]);
+                                        else
+                                            mma16816<false>(d[part], a & ml, a & mh, e & ml, e & mh, w[0], w[1]);
+                                    }
                                 }
                                 float2(&acc)[2] = o[nt][4 * blk + 2 * half + j];
-                                acc[0] = add(acc[0], make_float2(d[0], d[1]));
-                                acc[1] = add(acc[1], make_float2(d[2], d[3]));
+#pragma unroll
+                                for (int r = 0; r < 2; ++r)
+                                    acc[r] = add(acc[r], add(make_float2(d[0][2 * r], d[0][2 * r + 1]),
+                                                             make_float2(d[1][2 * r], d[1][2 * r + 1])));
                             }
                         }
                     }
@@ -639,7 +650,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, Kv4Geom<D, G, NT>::CTAS) kv4_at
             }
         __syncthreads();
         float *acc = reinterpret_cast<float *>(smem); // [warp][head][D]
-        constexpr float EVEN = 16777216.f / KV4_UP, ODD = 1048576.f / KV4_UP; // (times ref: beyond fp32 where steps are large)
+        constexpr float EVEN = 4194304.f / KV4_UP, ODD = 262144.f / KV4_UP; // (times ref: beyond fp32 where steps are large)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
