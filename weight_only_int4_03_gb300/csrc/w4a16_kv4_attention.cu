@@ -32,11 +32,12 @@
 //     copied to places that only the copying lane reads.  Where pages hold multiples of 16 positions, a page is
 //     looked up once for 16 of them, and masks are applied only in steps that have something to mask.
 // bf16, 128 wide: 48 sequences of 2048 to 32768 positions, 64 / 8 heads, 129 us, 4.6 TB/s of codes and parameters (the
-// 16-bit cache's bytes would take 327 us at the copy rate); one of 131071 with 40 / 8 heads and groups of 64 45.4 us, 3.3
+// 16-bit cache's bytes would take 327 us at the copy rate); one of 131071 with 40 / 8 heads and groups of 64 45.5 us, 3.3
 // TB/s, of which about 10 us pass before the first rows and in the join; fp16, 24 sequences of 5 to 9000 with a window of
 // 2048, 12 / 12 heads of 64: 14.3 us, of which most is the start and the join; one of 41 positions: 4.4 us of latencies.
 // Per 16 positions of 128 values: 8 score MMAs, 16 value MMAs and two for the start of each group, 96 conversions of codes.
-// Heads of 256 spill (up to 110 bytes) and take eight heads at a time: a KV head of 16 is read twice.
+// Eight warps per SM are what the registers allow: issue slots 52 % busy, ALU 48 %, MMA pipe 38 % in the 48 sequences.
+// Heads of 256 spill (up to 140 bytes) and take eight heads at a time: a KV head of 16 is read twice.
 // The work is split as in the 16-bit cache's attention (w4a16_split.cuh).
 #include <type_traits>
 
@@ -74,7 +75,7 @@ struct Kv4Geom {
     static constexpr int PARAMS = 16 * 4 * G;          // a sub-step's steps and bases of one side
     static constexpr int SUB = 2 * KEYS + 2 * PARAMS;
     // Sub-steps of 16 positions that a warp takes at once: what a step costs by itself (pages, the vote, adding up the
-    // outputs) is shared by them.  Four at once, for 128 wide heads of one group, gain nothing in long rows (128.9 and 129.1
+    // outputs) is shared by them.  Four at once, for 128 wide heads of one group, gain nothing in long rows (128.9 and 129.5
     // us for the 48 sequences) and lose in short ones (41 positions: 5.5 and 4.4 us); groups of 64 spill with four.
     static constexpr int SUBS = 2;
     static constexpr int STEP = 16 * SUBS;
